@@ -145,7 +145,8 @@ def _scale_of(amax, fmt):
         m, e = torch.frexp(amax)
         s = torch.ldexp(torch.ones_like(amax), torch.where(m <= 0.875, e - 9, e - 8).to(torch.int32))
     else:  # amax / 127, rounded up to 8 significant bits
-        bits = (amax / 127.0).contiguous().view(torch.int32)
+        # (a tensor divisor: by a number, torch multiplies by its rounded reciprocal)
+        bits = (amax / torch.full_like(amax, 127.0)).contiguous().view(torch.int32)
         s = torch.bitwise_and(bits + 0xFFFF, -0x10000).view(torch.float32)
     return torch.where(amax > 0, s, torch.zeros_like(s))
 
@@ -547,8 +548,8 @@ def _exact_append(st, case):
                     s0 = float(scales[phys, h]) if lo else 0.0
                     s1 = max(s0, _scale64(top, fmt))
                     if s1 > s0 and lo:
-                        codes[phys, h, :lo] = _round64(codes[phys, h, :lo] * s0 / s1, fmt)
-                    codes[phys, h, lo:hi] = _round64(x[h] / s1, fmt) if s1 else 0.0
+                        codes[phys, h, :lo] = _round64(codes[phys, h, :lo] * s0 / x.new_tensor(s1), fmt)
+                    codes[phys, h, lo:hi] = _round64(x[h] / x.new_tensor(s1), fmt) if s1 else 0.0
                     scales[phys, h] = s1
                 at += hi - lo
         # codes in 8 whole bits have no rounding to be compared with
