@@ -493,6 +493,192 @@ int pa_merge_partials(void* out, const float* max_logits, const float* exp_sums,
                       const int32_t* seq_lens, int num_seqs, int num_heads, int head_dim, int max_seq_len,
                       int partition_size, int num_sources, int partitions_per_source, pa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The cache in 8 bits, and eviction by accumulated attention weight.
+ *
+ * pa_kv_cache describes a paged cache of either kind.  Its formats:
+ *   PA_KV_F16   the fp16 cache of the calls above; no scales
+ *   PA_KV_E4M3  8-bit floats (4 exponent, 3 mantissa bits)
+ *   PA_KV_INT8  8-bit integers in [-127, 127]
+ * An 8-bit cache holds codes [num_blocks][num_kv_heads][block_size][head_dim],
+ * one byte each, and one fp32 scale per (block, kv head) for K and one for V,
+ * [num_blocks][num_kv_heads]; a value is code * scale.  Scales must be finite
+ * and not negative.  Those pa_kv_append makes are S(a) for a block's largest
+ * finite magnitude a, with few significant bits, so that 32-bit arithmetic
+ * decides every rounding exactly:
+ *   E4M3  the smallest power of two s with 448 s >= a
+ *   INT8  the smallest s of 8 significant bits with 127 s >= a
+ *   S(0) = 0.
+ * Slots past a sequence's end may hold anything, NaN codes included.
+ *
+ * The four calls take argument structs, allocate no device memory, are
+ * asynchronous on `stream` and can be captured into a graph (a captured call
+ * keeps its workspace: calls that may overlap need one each).  Pointers are
+ * device pointers; the caches and half tensors 16-byte aligned, the rest
+ * 4-byte, workspaces 256-byte.  Supported shapes, errors and the status word
+ * are those of pa_decode; a sequence whose lengths are out of range (status
+ * PA_DEV_BAD_SEQ_LEN) is skipped. */
+enum {
+    PA_KV_F16 = 0,
+    PA_KV_E4M3 = 1,
+    PA_KV_INT8 = 2
+};
+
+typedef struct {
+    void* k_cache;   /* [num_blocks][num_kv_heads][block_size][head_dim], fp16 or 8-bit codes */
+    void* v_cache;
+    float* k_scales; /* [num_blocks][num_kv_heads]; NULL with PA_KV_F16 */
+    float* v_scales;
+    int64_t num_blocks;
+    int num_kv_heads;
+    int head_dim;
+    int block_size;
+    int format;      /* PA_KV_* */
+} pa_kv_cache;
+
+/* Write new tokens' K and V into the cache.  Sequence b holds context_lens[b]
+ * tokens and gets rows query_start_loc[b] .. query_start_loc[b+1]-1 of k_new
+ * and v_new (fp16 [num_tokens][num_kv_heads][head_dim]) at positions
+ * context_lens[b] onwards, through its row of block_tables, which must cover
+ * them.  Rows from query_start_loc[num_seqs] on are not read, and blocks that
+ * get no token are not touched.  With PA_KV_F16 rows are copied.  In 8 bits,
+ * per (block, kv head) with a = the largest finite magnitude of the tokens
+ * that join it: the scale becomes s = max(scale, S(a)), or S(a) for a block
+ * that held none of the sequence's tokens; when it grew, the sequence's
+ * earlier codes c in the block become the format's nearest to c * scale / s
+ * (ties to even; with powers of two only E4M3's subnormals round).  New codes
+ * are the nearest to x / s; infinities saturate to the largest code, NaN
+ * stays NaN in E4M3 and becomes 0 in INT8.  Calling it again with the same
+ * arguments leaves the same cache.
+ * max_query_len is a host-side bound on the new tokens of a sequence.  A
+ * block may get tokens of one sequence only (copy a shared block first; two
+ * sequences writing to one leave an unspecified mix of both). */
+typedef struct {
+    pa_kv_cache cache;
+    const void* k_new;
+    const void* v_new;
+    const int32_t* block_tables;    /* [num_seqs][max_blocks_per_seq] */
+    const int32_t* context_lens;    /* [num_seqs] */
+    const int32_t* query_start_loc; /* [num_seqs + 1], as for pa_prefix */
+    int num_seqs;
+    int num_tokens;                 /* rows of k_new and v_new */
+    int max_blocks_per_seq;
+    int max_query_len;
+} pa_kv_append_args;
+
+int pa_kv_append(const pa_kv_append_args* args, pa_stream_t stream);
+
+/* Decode over a cache of either kind: pa_decode's result with K and V the
+ * values the cache stands for.  With weights_out it also adds up what each
+ * token was attended to, the measure that pa_kv_evict goes by: for t <
+ * seq_lens[b]
+ *     weights_out[b][kvh][t] = weights_in[b][kvh][t] + sum_h p[b][h][t],
+ * h over the query heads of kv head kvh and p the softmax probabilities; 0 in
+ * place of weights_in where that is NULL.  Both are fp32
+ * [num_seqs][num_kv_heads][weights_stride] with weights_stride >=
+ * max_seq_len; they may be the same array and otherwise must not overlap.
+ * Entries from seq_lens[b] on are neither read nor written.
+ * Of the options partition_size, wait_limit, PA_FLAG_FORCE_TIMEOUT and mode
+ * AUTO, SINGLE and SPLIT apply.  The workspace needs no initialisation and
+ * holds pa_kv_decode_workspace_size bytes (same sizes, format, partition
+ * size and device; partition_size 0 for the library's own plan), 0 where
+ * sizes are out of range. */
+typedef struct {
+    void* out;
+    const void* q;
+    pa_kv_cache cache;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const float* weights_in;  /* NULL: zeros */
+    float* weights_out;       /* NULL: no weights */
+    int64_t weights_stride;
+    int num_seqs;
+    int max_blocks_per_seq;
+    int max_seq_len;
+    int num_heads;
+    float scale;
+} pa_kv_decode_args;
+
+size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                                   int format, int partition_size, int weights);
+int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void* workspace,
+                 size_t workspace_bytes, pa_stream_t stream);
+
+/* Chunked prefill whose context lies in a cache of either kind; the chunk's
+ * own K and V are the fp16 rows of k_new and v_new, as for pa_prefix.  Each
+ * context block is expanded once into an fp16 copy in the workspace, which
+ * the prefill kernel then reads for all of its query tiles: the copy's
+ * traffic is small next to the products, and expanding in every query tile
+ * would repeat it up to max_query_len times.  Context values are rounded to
+ * fp16 (exact for E4M3 within fp16's range; magnitudes above 65504 become
+ * 65504).  With PA_KV_F16 no copy is made and this is pa_prefix_ex. */
+typedef struct {
+    void* out;
+    const void* q;
+    const void* k_new;
+    const void* v_new;
+    pa_kv_cache cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start_loc;
+    int num_seqs;
+    int num_tokens;
+    int max_blocks_per_seq;
+    int max_context_len;
+    int max_query_len;
+    int num_heads;
+    float scale;
+} pa_kv_prefix_args;
+
+size_t pa_kv_prefix_workspace_size(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format);
+int pa_kv_prefix(const pa_kv_prefix_args* args, const pa_decode_opts* opts, void* workspace,
+                 size_t workspace_bytes, pa_stream_t stream);
+
+/* Keep the tokens that were attended to most and move them to other blocks.
+ * Of the L = seq_lens[b] tokens of sequence b every kv head keeps k =
+ * min(keep_lens[b], L) of its own choice: the last r = min(recent, k), the
+ * first s = min(sinks, k - r), and of the tokens between those the k - r - s
+ * with the largest weights[b][kvh][t] (equal ones: the lowest position first;
+ * NaN ranks as -infinity).  The kept tokens stay in the order of their
+ * positions: the i-th goes to slot i % block_size of block
+ * dst_block_tables[b][i / block_size] of `dst`.  What the call writes:
+ *   dst's k_cache, v_cache  the kept rows.  In 8 bits a destination block's
+ *                           scale is the largest of its tokens' scales, and
+ *                           codes are rounded to it again as in pa_kv_append
+ *   kept       int32 [num_seqs][num_kv_heads][max_keep_len]: positions, k of
+ *              them in ascending order
+ *   new_lens   int32 [num_seqs]: k
+ *   dst_weights fp32 [num_seqs][num_kv_heads][dst_weights_stride], may be
+ *              NULL: the kept tokens' weights, for the accumulation to go on
+ * Nothing else is written (not the rest of a last block, nor entries from k
+ * on).  Keys keep the positions that were encoded into them.  `dst` may be
+ * the source's pool or another one of the same format, kv heads and
+ * head_dim; its blocks of dst_block_tables must differ from each other and
+ * from every block read, and dst_weights must not overlap weights. */
+typedef struct {
+    pa_kv_cache src;
+    pa_kv_cache dst;
+    const int32_t* block_tables;     /* [num_seqs][max_blocks_per_seq] */
+    const int32_t* dst_block_tables; /* [num_seqs][dst_max_blocks_per_seq] */
+    const int32_t* seq_lens;
+    const int32_t* keep_lens;        /* [num_seqs], each in [0, max_keep_len] */
+    const float* weights;            /* [num_seqs][num_kv_heads][weights_stride] */
+    float* dst_weights;
+    int32_t* kept;
+    int32_t* new_lens;
+    int64_t weights_stride;          /* >= max_seq_len */
+    int64_t dst_weights_stride;      /* >= max_keep_len when dst_weights is given */
+    int num_seqs;
+    int max_blocks_per_seq;
+    int dst_max_blocks_per_seq;      /* * block_size >= max_keep_len */
+    int max_seq_len;
+    int max_keep_len;
+    int sinks;
+    int recent;
+} pa_kv_evict_args;
+
+int pa_kv_evict(const pa_kv_evict_args* args, pa_stream_t stream);
+
 /* Library version, major*10000 + minor*100 + patch.  No counterpart on the pages. */
 int pa_version(void);
 

@@ -46,6 +46,10 @@ PA_FLAG_DETERMINISTIC = 8
 PA_FLAG_UNIFORM_LENGTHS = 16
 PA_FLAG_PREFIX_GRID = 32
 
+PA_KV_F16 = 0
+PA_KV_E4M3 = 1
+PA_KV_INT8 = 2
+
 
 class pa_decode_args(ctypes.Structure):
     _fields_ = [
@@ -95,6 +99,54 @@ class pa_prefix_split_opts(ctypes.Structure):
     _fields_ = [("parts", ctypes.c_int), ("units", ctypes.c_int)]
 
 
+class pa_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("block_size", ctypes.c_int), ("format", ctypes.c_int),
+    ]
+
+
+class pa_kv_append_args(ctypes.Structure):
+    _fields_ = [
+        ("cache", pa_kv_cache), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p), ("query_start_loc", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int), ("num_tokens", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int),
+        ("max_query_len", ctypes.c_int),
+    ]
+
+
+class pa_kv_decode_args(ctypes.Structure):
+    _fields_ = [
+        ("out", ctypes.c_void_p), ("q", ctypes.c_void_p), ("cache", pa_kv_cache), ("block_tables", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("weights_in", ctypes.c_void_p), ("weights_out", ctypes.c_void_p),
+        ("weights_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int),
+        ("max_seq_len", ctypes.c_int), ("num_heads", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class pa_kv_prefix_args(ctypes.Structure):
+    _fields_ = [
+        ("out", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+        ("cache", pa_kv_cache), ("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+        ("query_start_loc", ctypes.c_void_p), ("num_seqs", ctypes.c_int), ("num_tokens", ctypes.c_int),
+        ("max_blocks_per_seq", ctypes.c_int), ("max_context_len", ctypes.c_int), ("max_query_len", ctypes.c_int),
+        ("num_heads", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class pa_kv_evict_args(ctypes.Structure):
+    _fields_ = [
+        ("src", pa_kv_cache), ("dst", pa_kv_cache), ("block_tables", ctypes.c_void_p),
+        ("dst_block_tables", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("keep_lens", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("dst_weights", ctypes.c_void_p), ("kept", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p), ("weights_stride", ctypes.c_int64), ("dst_weights_stride", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int), ("dst_max_blocks_per_seq", ctypes.c_int),
+        ("max_seq_len", ctypes.c_int), ("max_keep_len", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("recent", ctypes.c_int),
+    ]
+
+
 class PaDecodeError(RuntimeError):
     def __init__(self, code: int, what: str = ""):
         self.code = code
@@ -142,6 +194,20 @@ def _load() -> ctypes.CDLL:
     lib.pa_merge_partials.argtypes = [vp, vp, vp, vp, vp] + [i32] * 7 + [vp]
     lib.pa_decode_noalloc.restype = i32
     lib.pa_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, i32, i32, f32, vp]
+    lib.pa_kv_append.restype = i32
+    lib.pa_kv_append.argtypes = [ctypes.POINTER(pa_kv_append_args), vp]
+    lib.pa_kv_decode_workspace_size.restype = ctypes.c_size_t
+    lib.pa_kv_decode_workspace_size.argtypes = [i32] * 8
+    lib.pa_kv_decode.restype = i32
+    lib.pa_kv_decode.argtypes = [ctypes.POINTER(pa_kv_decode_args), ctypes.POINTER(pa_decode_opts), vp,
+                                 ctypes.c_size_t, vp]
+    lib.pa_kv_prefix_workspace_size.restype = ctypes.c_size_t
+    lib.pa_kv_prefix_workspace_size.argtypes = [i32] * 5
+    lib.pa_kv_prefix.restype = i32
+    lib.pa_kv_prefix.argtypes = [ctypes.POINTER(pa_kv_prefix_args), ctypes.POINTER(pa_decode_opts), vp,
+                                 ctypes.c_size_t, vp]
+    lib.pa_kv_evict.restype = i32
+    lib.pa_kv_evict.argtypes = [ctypes.POINTER(pa_kv_evict_args), vp]
     return lib
 
 
@@ -442,3 +508,242 @@ def pa_merge_partials(out, max_logits, exp_sums, tmp_out, seq_lens, num_heads, h
                                _stream_handle(stream))
     if rc != PA_OK:
         raise PaDecodeError(rc, "pa_merge_partials")
+
+
+# --- the cache in 8 bits, and eviction by accumulated attention weight -------------------------------------------
+
+KV_FORMATS = {torch.float16: PA_KV_F16, torch.float8_e4m3fn: PA_KV_E4M3, torch.int8: PA_KV_INT8}
+
+
+def _need(name, t, dtype, device=None):
+    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _kv_cache(k_cache, v_cache, k_scales, v_scales, device, what="") -> pa_kv_cache:
+    """The cache descriptor of [num_blocks, num_kv_heads, block_size, head_dim] tensors;
+    their dtype (float16, float8_e4m3fn or int8) is the format."""
+    fmt = KV_FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise TypeError(f"{what}k_cache must be float16, float8_e4m3fn or int8, got {k_cache.dtype}")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError(f"{what}k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    _need(what + "k_cache", k_cache, k_cache.dtype, device)
+    _need(what + "v_cache", v_cache, k_cache.dtype, device)
+    shape = k_cache.shape
+    if fmt == PA_KV_F16:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError(f"{what}scales come with an 8-bit cache only")
+    else:
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is None:
+                raise ValueError(f"{what}{name} is needed with an 8-bit cache")
+            _need(what + name, t, torch.float32, device)
+            if t.shape != shape[:2]:
+                raise ValueError(f"{what}{name} must be [num_blocks, num_kv_heads]")
+    return pa_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), shape[0], shape[1],
+                       shape[3], shape[2], fmt)
+
+
+def _shape(name, t, *sizes):
+    if tuple(t.shape) != sizes:
+        raise ValueError(f"{name} must be {list(sizes)}, got {list(t.shape)}")
+
+
+def _lengths(device, num_seqs, **tensors):
+    for name, t in tensors.items():
+        _need(name, t, torch.int32, device)
+        _shape(name, t, num_seqs)
+
+
+def _tables(name, t, num_seqs, device):
+    _need(name, t, torch.int32, device)
+    if t.dim() != 2 or t.shape[0] != num_seqs:
+        raise ValueError(f"{name} must be [{num_seqs}, max_blocks_per_seq], got {list(t.shape)}")
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace, or one that the allocator hands out on the call's stream (so that neither
+    its earlier nor its later users can overlap the call)."""
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if nbytes == 0:
+        return None, 0, None
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws.data_ptr(), nbytes, ws
+
+
+class _on:
+    """The tensors' device as the current one, and the stream (None: that device's current stream)."""
+    __slots__ = ("dev", "prev", "stream")
+
+    def __init__(self, device, stream):
+        self.dev, self.prev, self.stream = device.index, -1, stream
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev:
+            self.prev = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        return _stream_handle(self.stream)
+
+    def __exit__(self, *exc):
+        if self.prev >= 0:
+            torch.cuda.set_device(self.prev)
+
+
+def _raise(rc, what):
+    if rc != PA_OK:
+        raise PaDecodeError(rc, what)
+
+
+def pa_kv_append(k_cache, v_cache, k_scales, v_scales, k_new, v_new, block_tables, context_lens, query_start_loc,
+                 stream=None, *, max_query_len: int) -> None:
+    """Write new tokens' K and V into the paged cache, in place (see include/pa_decode.h).
+
+    k_cache / v_cache: [num_blocks, num_kv_heads, 16, head_dim] float16, float8_e4m3fn or int8;
+    k_scales / v_scales: float32 [num_blocks, num_kv_heads] (None with float16); k_new / v_new:
+    float16 [num_tokens, num_kv_heads, head_dim]."""
+    dev = k_cache.device
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    B = context_lens.shape[0]
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _need(name, t, torch.float16, dev)
+        _shape(name, t, k_new.shape[0], cache.num_kv_heads, cache.head_dim)
+    _tables("block_tables", block_tables, B, dev)
+    _lengths(dev, B, context_lens=context_lens)
+    _lengths(dev, B + 1, query_start_loc=query_start_loc)
+    args = pa_kv_append_args(cache, k_new.data_ptr(), v_new.data_ptr(), block_tables.data_ptr(),
+                             context_lens.data_ptr(), query_start_loc.data_ptr(), B, k_new.shape[0],
+                             block_tables.shape[1], int(max_query_len))
+    with _on(dev, stream) as s:
+        _raise(lib.pa_kv_append(ctypes.byref(args), s), "pa_kv_append")
+
+
+def pa_kv_decode_workspace_size(num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim, dtype,
+                                partition_size: int = 0, weights: bool = False) -> int:
+    """Bytes of pa_kv_decode's workspace on the current device, for a cache of `dtype`."""
+    return lib.pa_kv_decode_workspace_size(int(num_seqs), int(max_seq_len), int(num_heads), int(num_kv_heads),
+                                           int(head_dim), KV_FORMATS[dtype], int(partition_size), int(bool(weights)))
+
+
+def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, stream=None, *,
+                 max_seq_len: int, weights_in: Optional[torch.Tensor] = None,
+                 weights_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 mode="auto", partition_size: int = 0, flags: int = 0, wait_limit: int = 0) -> None:
+    """Decode over a float16, float8_e4m3fn or int8 cache (see include/pa_decode.h).
+
+    out / q: float16 [num_seqs, num_heads, head_dim].  With weights_out (float32
+    [num_seqs, num_kv_heads, >= max_seq_len]) the tokens' attention weights, summed over a kv head's
+    query heads, are added to weights_in (None: zeros; may be weights_out itself).  `workspace`: a
+    tensor of pa_kv_decode_workspace_size bytes (None: one from the allocator)."""
+    dev = q.device
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [num_seqs, num_heads, head_dim]")
+    B, H = q.shape[0], q.shape[1]
+    _need("q", q, torch.float16, dev)
+    _need("out", out, torch.float16, dev)
+    _shape("out", out, B, H, cache.head_dim)
+    _tables("block_tables", block_tables, B, dev)
+    _lengths(dev, B, seq_lens=seq_lens)
+    stride = 0
+    if weights_out is not None:
+        _need("weights_out", weights_out, torch.float32, dev)
+        if weights_out.dim() != 3:
+            raise ValueError("weights_out must be [num_seqs, num_kv_heads, >= max_seq_len]")
+        stride = weights_out.shape[2]
+        _shape("weights_out", weights_out, B, cache.num_kv_heads, stride)
+        if weights_in is not None:
+            _need("weights_in", weights_in, torch.float32, dev)
+            _shape("weights_in", weights_in, B, cache.num_kv_heads, stride)
+    elif weights_in is not None:
+        raise ValueError("weights_in needs weights_out")
+    args = pa_kv_decode_args(out.data_ptr(), q.data_ptr(), cache, block_tables.data_ptr(), seq_lens.data_ptr(),
+                             _ptr(weights_in), _ptr(weights_out), stride, B, block_tables.shape[1], int(max_seq_len),
+                             H, float(scale))
+    opts = make_opts(mode=mode, partition_size=partition_size, flags=flags, wait_limit=wait_limit)
+    with _on(dev, stream) as s:
+        need = 0
+        if workspace is None:
+            need = lib.pa_kv_decode_workspace_size(B, int(max_seq_len), H, cache.num_kv_heads, cache.head_dim,
+                                                   cache.format, int(partition_size), int(weights_out is not None))
+        ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
+        _raise(lib.pa_kv_decode(ctypes.byref(args), ctypes.byref(opts), ptr, nbytes, s), "pa_kv_decode")
+
+
+def pa_kv_prefix_workspace_size(num_seqs, max_context_len, num_kv_heads, head_dim, dtype) -> int:
+    """Bytes of pa_kv_prefix's workspace, for a cache of `dtype`."""
+    return lib.pa_kv_prefix_workspace_size(int(num_seqs), int(max_context_len), int(num_kv_heads), int(head_dim),
+                                           KV_FORMATS[dtype])
+
+
+def pa_kv_prefix(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                 query_start_loc, scale, stream=None, *, max_context_len: int, max_query_len: int,
+                 workspace: Optional[torch.Tensor] = None, flags: int = 0, wait_limit: int = 0) -> None:
+    """Chunked prefill whose context lies in a float16, float8_e4m3fn or int8 cache (see
+    include/pa_decode.h); shapes as for pa_prefix.  `workspace`: a tensor of
+    pa_kv_prefix_workspace_size bytes (None: one from the allocator)."""
+    dev = q.device
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [num_tokens, num_heads, head_dim]")
+    T, H, B = q.shape[0], q.shape[1], context_lens.shape[0]
+    for name, t, heads in (("q", q, H), ("out", out, H), ("k_new", k_new, cache.num_kv_heads),
+                           ("v_new", v_new, cache.num_kv_heads)):
+        _need(name, t, torch.float16, dev)
+        _shape(name, t, T, heads, cache.head_dim)
+    _tables("block_tables", block_tables, B, dev)
+    _lengths(dev, B, context_lens=context_lens)
+    _lengths(dev, B + 1, query_start_loc=query_start_loc)
+    args = pa_kv_prefix_args(out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cache,
+                             block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(), B, T,
+                             block_tables.shape[1], int(max_context_len), int(max_query_len), H, float(scale))
+    opts = make_opts(flags=flags, wait_limit=wait_limit)
+    with _on(dev, stream) as s:
+        need = 0 if workspace is not None else lib.pa_kv_prefix_workspace_size(
+            B, int(max_context_len), cache.num_kv_heads, cache.head_dim, cache.format)
+        ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
+        _raise(lib.pa_kv_prefix(ctypes.byref(args), ctypes.byref(opts), ptr, nbytes, s), "pa_kv_prefix")
+
+
+def pa_kv_evict(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, dst_k_cache, dst_v_cache,
+                dst_k_scales, dst_v_scales, dst_block_tables, keep_lens, weights, kept, new_lens,
+                dst_weights: Optional[torch.Tensor] = None, stream=None, *, max_seq_len: int, max_keep_len: int,
+                sinks: int = 0, recent: int = 0) -> None:
+    """Keep each kv head's most attended tokens and move them to other blocks (see
+    include/pa_decode.h).  The destination may be the same pool; its blocks must not be among the
+    source's.  weights: float32 [num_seqs, num_kv_heads, >= max_seq_len]; kept: int32 [num_seqs,
+    num_kv_heads, max_keep_len]; new_lens: int32 [num_seqs]; dst_weights: float32 [num_seqs,
+    num_kv_heads, >= max_keep_len] or None."""
+    dev = k_cache.device
+    src = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    dst = _kv_cache(dst_k_cache, dst_v_cache, dst_k_scales, dst_v_scales, dev, "dst_")
+    B, hkv = seq_lens.shape[0], src.num_kv_heads
+    _lengths(dev, B, seq_lens=seq_lens, keep_lens=keep_lens, new_lens=new_lens)
+    _tables("block_tables", block_tables, B, dev)
+    _tables("dst_block_tables", dst_block_tables, B, dev)
+    _need("weights", weights, torch.float32, dev)
+    _need("kept", kept, torch.int32, dev)
+    _shape("kept", kept, B, hkv, int(max_keep_len))
+    for name, t in (("weights", weights), ("dst_weights", dst_weights)):
+        if t is not None:
+            _need(name, t, torch.float32, dev)
+            if t.dim() != 3 or tuple(t.shape[:2]) != (B, hkv):
+                raise ValueError(f"{name} must be [{B}, {hkv}, tokens]")
+    args = pa_kv_evict_args(src, dst, block_tables.data_ptr(), dst_block_tables.data_ptr(), seq_lens.data_ptr(),
+                            keep_lens.data_ptr(), weights.data_ptr(), _ptr(dst_weights), kept.data_ptr(),
+                            new_lens.data_ptr(), weights.shape[2], dst_weights.shape[2] if dst_weights is not None else 0,
+                            B, block_tables.shape[1], dst_block_tables.shape[1], int(max_seq_len), int(max_keep_len),
+                            int(sinks), int(recent))
+    with _on(dev, stream) as s:
+        _raise(lib.pa_kv_evict(ctypes.byref(args), s), "pa_kv_evict")

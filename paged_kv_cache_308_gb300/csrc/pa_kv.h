@@ -1,0 +1,119 @@
+// Internal interface between the C-ABI layer of the 8-bit cache and eviction
+// calls (pa_kv_api.cpp) and their kernels (pa_kv_decode.cu, pa_kv_cache.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "pa_decode.h"
+#include "pa_internal.h"
+
+namespace pa {
+
+// Defined in pa_api.cpp for the other C-ABI sources.
+int sm_count(int* num_sms);                               // of the current device; a PA_* code
+int reduce_width(int head_dim, long long pairs, int num_sms);  // head_dim slice of a reduce CTA
+int check_prefix(const pa_prefix_args* args, const pa_decode_opts* opts);  // a PA_* code
+// A cache of `elem_bytes`-byte elements viewed as (box column, row, column
+// chunk); one box brings the 16 rows of a (block, kv head).  Rows of 128
+// bytes or more come in 128-byte chunks with the 128-byte swizzle, 64-byte
+// rows in one chunk with the 64-byte swizzle.
+int make_block_map(CUtensorMap* map, const void* base, long long num_blocks, int num_kv_heads, int head_dim,
+                   int elem_bytes);
+
+struct KvDecodeParams {
+    __half* out;
+    const __half* q;
+    const float* k_scales;  // null for fp16
+    const float* v_scales;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    float* max_logits;  // [B][H][max_partitions]: reference exponents of the partials, log2 domain
+    float* exp_sums;    // [B][H][max_partitions]
+    float* tmp_out;     // [B][H][max_partitions][D], normalised
+    float* scores;      // [B][H][score_stride], log2 domain; null without weights
+    long long score_stride;
+    long long num_blocks;
+    int num_heads, num_kv_heads, group;
+    int max_blocks_per_seq, max_seq_len;
+    int partition_size, max_partitions;
+    float scale_log2;
+    unsigned wait_limit;
+    int force_timeout;
+    unsigned int* status;
+};
+
+struct KvWeightsParams {
+    const float* scores;
+    const float* max_logits;
+    const float* exp_sums;
+    const float* weights_in;  // null: zeros
+    float* weights_out;
+    const int32_t* seq_lens;
+    long long score_stride, weights_stride;
+    int num_heads, num_kv_heads, group;
+    int max_blocks_per_seq, max_seq_len;
+    int partition_size, max_partitions;
+};
+
+// Warps of a decode CTA, and the copies of one block (K and V) each keeps in flight.
+constexpr int kKvWarps = 4;
+int kv_decode_stages(int format, int head_dim);
+int kv_decode_smem_bytes(int format, int head_dim);
+cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, const CUtensorMap& tk,
+                             const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
+constexpr int kKvWeightsTokens = 1024;  // tokens of a CTA of the weights kernel
+cudaError_t launch_kv_weights(const KvWeightsParams& prm, dim3 grid, cudaStream_t stream);
+
+struct KvAppendParams {
+    void* cache[2];        // K, V
+    float* scales[2];
+    const __half* fresh[2];
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start_loc;
+    long long num_blocks;
+    int num_kv_heads, max_blocks_per_seq, num_tokens, max_query_len;
+    unsigned int* status;
+};
+cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, dim3 grid, cudaStream_t stream);
+
+struct KvExpandParams {
+    const uint8_t* cache[2];
+    const float* scales[2];
+    __half* expanded[2];   // [num_seqs * blocks_per_seq][Hkv][16][D]
+    int32_t* tables;       // [num_seqs][blocks_per_seq]: their numbers
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    long long num_blocks;
+    int num_kv_heads, max_blocks_per_seq, blocks_per_seq, max_context_len;
+    unsigned int* status;
+};
+cudaError_t launch_kv_expand(int format, int head_dim, const KvExpandParams& prm, dim3 grid, cudaStream_t stream);
+
+struct KvEvictParams {
+    const void* src[2];
+    const float* src_scales[2];
+    void* dst[2];
+    float* dst_scales[2];
+    const int32_t* block_tables;
+    const int32_t* dst_block_tables;
+    const int32_t* seq_lens;
+    const int32_t* keep_lens;
+    const float* weights;
+    float* dst_weights;
+    int32_t* kept;
+    int32_t* new_lens;
+    long long src_blocks, dst_blocks, weights_stride, dst_weights_stride;
+    int num_kv_heads, max_blocks_per_seq, dst_max_blocks_per_seq;
+    int max_seq_len, max_keep_len, sinks, recent;
+    unsigned int* status;
+};
+constexpr int kEvictThreads = 1024;
+cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream);
+cudaError_t launch_kv_evict_move(int format, int head_dim, const KvEvictParams& prm, dim3 grid, cudaStream_t stream);
+
+}  // namespace pa

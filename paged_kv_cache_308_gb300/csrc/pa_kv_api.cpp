@@ -1,0 +1,453 @@
+// C-ABI layer of the calls over a cache in 8 bits and of eviction (see
+// include/pa_decode.h): argument checks, decode plan, workspace layout and
+// launches.  Shares the device status word, the reduce kernel and the prefill
+// kernels with pa_api.cpp.
+#include "pa_decode.h"
+
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "pa_internal.h"
+#include "pa_kv.h"
+#include "pa_prefix.h"
+
+namespace {
+
+constexpr size_t kWsAlign = 256;
+constexpr int kDefaultPartition = 512;
+constexpr long long kSmemPerSm = 228 * 1024;
+// SM count assumed by the workspace size when no device answers (above any GPU's)
+constexpr int kMaxSmsBound = 1024;
+
+size_t up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int blocks_of(long long tokens) { return static_cast<int>((tokens + pa::kBlockSize - 1) / pa::kBlockSize); }
+
+int check_shape(const pa_kv_cache& c) {
+    if (c.num_kv_heads <= 0 || c.head_dim <= 0 || c.block_size <= 0 || c.num_blocks < 0) return PA_ERR_INVALID_ARG;
+    if (c.format != PA_KV_F16 && c.format != PA_KV_E4M3 && c.format != PA_KV_INT8) return PA_ERR_INVALID_ARG;
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return PA_ERR_UNSUPPORTED;
+    if (c.block_size != pa::kBlockSize) return PA_ERR_UNSUPPORTED;
+    if (c.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a grid dimension
+    // TMA row coordinates are 32-bit
+    if (c.num_blocks >= (1ll << 31) || c.num_blocks * c.num_kv_heads * c.block_size >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+int check_pointers(const pa_kv_cache& c) {
+    if (!c.k_cache || !c.v_cache || !aligned(c.k_cache, 16) || !aligned(c.v_cache, 16)) return PA_ERR_INVALID_ARG;
+    if (c.format != PA_KV_F16 &&
+        (!c.k_scales || !c.v_scales || !aligned(c.k_scales, 4) || !aligned(c.v_scales, 4)))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+bool bad_ptr(const void* p, uintptr_t a) { return !p || !aligned(p, a); }
+
+// ---- decode
+
+struct DecodePlan {
+    int partition_size, parts;
+};
+
+// Partitions of the decode grid.  One sequence: one wave of the CTAs the SMs
+// hold at once.  A batch: 512 tokens, halved when the grid would leave SMs
+// without a CTA; a sequence of one partition needs no reduce.
+DecodePlan plan_decode(int num_seqs, int max_seq_len, int num_kv_heads, int head_dim, int format, int num_sms,
+                       int partition_size, int mode) {
+    const int whole = std::max(1, blocks_of(max_seq_len)) * pa::kBlockSize;
+    int part = partition_size;
+    if (mode == PA_MODE_SINGLE) part = whole;
+    if (part <= 0) {
+        const long long per_sm = std::max(1ll, kSmemPerSm / (pa::kv_decode_smem_bytes(format, head_dim) + 1024));
+        const long long per_seq = per_sm * num_sms / std::max(1ll, (long long)num_seqs * num_kv_heads);
+        if (num_seqs == 1 && per_seq >= 2) {
+            part = std::max(blocks_of((max_seq_len + per_seq - 1) / per_seq), pa::kKvWarps) * pa::kBlockSize;
+        } else {
+            part = kDefaultPartition;
+            const long long ctas = (long long)((max_seq_len + part - 1) / part) * num_kv_heads * num_seqs;
+            if (ctas < num_sms) part /= 2;
+        }
+    }
+    part = std::min(part, whole);
+    return {part, std::max(1, (max_seq_len + part - 1) / part)};
+}
+
+struct DecodeSpace {
+    size_t sums, acc, scores, bytes;  // offsets of exp_sums, tmp_out, scores; max_logits is at 0
+    long long score_stride;
+};
+
+DecodeSpace decode_space(const DecodePlan& p, int num_seqs, int num_heads, int head_dim, int max_seq_len, bool weights) {
+    DecodeSpace s;
+    const size_t rows = (size_t)num_seqs * num_heads * p.parts;
+    const bool partials = p.parts > 1 || weights;
+    s.sums = partials ? up(rows * 4) : 0;
+    s.acc = 2 * s.sums;
+    s.scores = s.acc + (p.parts > 1 ? up(rows * head_dim * 4) : 0);
+    s.score_stride = (long long)blocks_of(max_seq_len) * pa::kBlockSize;
+    s.bytes = s.scores + (weights ? up((size_t)num_seqs * num_heads * s.score_stride * 4) : 0);
+    return s;
+}
+
+int check_decode(const pa_kv_decode_args* a, const pa_decode_opts* o) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_seqs > 65535) return PA_ERR_INVALID_ARG;
+    int rc = check_shape(a->cache);
+    if (rc == PA_ERR_INVALID_ARG) return rc;
+    if (a->num_heads <= 0 || a->num_heads % a->cache.num_kv_heads) return PA_ERR_INVALID_ARG;
+    if (!isfinite(a->scale)) return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len < 0 || a->max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+    if (o && (o->mode < PA_MODE_AUTO || o->mode > PA_MODE_SPLIT)) return PA_ERR_INVALID_ARG;
+    if (o && (o->partition_size < 0 || o->partition_size % pa::kBlockSize)) return PA_ERR_INVALID_ARG;
+    if (o && (o->warps || o->stages)) return PA_ERR_UNSUPPORTED;
+    if (rc) return rc;
+    if (a->num_heads / a->cache.num_kv_heads > pa::kMaxGroup) return PA_ERR_UNSUPPORTED;
+    if ((long long)a->max_seq_len > (long long)a->max_blocks_per_seq * pa::kBlockSize) return PA_ERR_INVALID_ARG;
+    if (a->weights_out && a->weights_stride < a->max_seq_len) return PA_ERR_INVALID_ARG;
+    if (a->weights_in && !a->weights_out) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs == 0) return PA_OK;
+    if (bad_ptr(a->out, 16) || bad_ptr(a->q, 16) || bad_ptr(a->block_tables, 4) || bad_ptr(a->seq_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(a->weights_in, 4) || !aligned(a->weights_out, 4)) return PA_ERR_INVALID_ARG;
+    if ((rc = check_pointers(a->cache))) return rc;
+    if (a->cache.num_blocks == 0 && a->max_seq_len > 0) return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    int rc = check_decode(a, o);
+    if (rc) return rc;
+    if (a->num_seqs == 0) return PA_OK;
+    const pa_kv_cache& c = a->cache;
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;  // the launch reports the missing device
+    const DecodePlan plan = plan_decode(a->num_seqs, a->max_seq_len, c.num_kv_heads, c.head_dim, c.format, num_sms,
+                                        o ? o->partition_size : 0, o ? o->mode : PA_MODE_AUTO);
+    const bool weights = a->weights_out != nullptr;
+    const DecodeSpace sp = decode_space(plan, a->num_seqs, a->num_heads, c.head_dim, a->max_seq_len, weights);
+    if (sp.bytes > 0 && (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign))) return PA_ERR_WORKSPACE;
+
+    const int elem = c.format == PA_KV_F16 ? 2 : 1;
+    CUtensorMap tk, tv;
+    if ((rc = pa::make_block_map(&tk, c.k_cache, c.num_blocks, c.num_kv_heads, c.head_dim, elem)) ||
+        (rc = pa::make_block_map(&tv, c.v_cache, c.num_blocks, c.num_kv_heads, c.head_dim, elem)))
+        return rc;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const bool split = plan.parts > 1;
+    pa::KvDecodeParams p{};
+    p.out = static_cast<__half*>(a->out);
+    p.q = static_cast<const __half*>(a->q);
+    p.k_scales = c.k_scales;
+    p.v_scales = c.v_scales;
+    p.block_tables = a->block_tables;
+    p.seq_lens = a->seq_lens;
+    p.max_logits = split || weights ? reinterpret_cast<float*>(w) : nullptr;
+    p.exp_sums = split || weights ? reinterpret_cast<float*>(w + sp.sums) : nullptr;
+    p.tmp_out = split ? reinterpret_cast<float*>(w + sp.acc) : nullptr;
+    p.scores = weights ? reinterpret_cast<float*>(w + sp.scores) : nullptr;
+    p.score_stride = sp.score_stride;
+    p.num_blocks = c.num_blocks;
+    p.num_heads = a->num_heads;
+    p.num_kv_heads = c.num_kv_heads;
+    p.group = a->num_heads / c.num_kv_heads;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    p.max_seq_len = a->max_seq_len;
+    p.partition_size = plan.partition_size;
+    p.max_partitions = plan.parts;
+    p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
+    p.wait_limit = (o && o->wait_limit) ? o->wait_limit : pa::kDefaultWaitLimit;
+    p.force_timeout = (o && (o->flags & PA_FLAG_FORCE_TIMEOUT)) ? 1 : 0;
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    if (pa::launch_kv_decode(c.format, c.head_dim, p, tk, tv, dim3(plan.parts, c.num_kv_heads, a->num_seqs), stream) !=
+        cudaSuccess)
+        return PA_ERR_CUDA;
+    if (split) {
+        pa::ReduceParams r{};
+        r.out = p.out;
+        r.max_logits = p.max_logits;
+        r.exp_sums = p.exp_sums;
+        r.tmp_out = p.tmp_out;
+        r.seq_lens = a->seq_lens;
+        r.num_heads = a->num_heads;
+        r.max_blocks_per_seq = a->max_blocks_per_seq;
+        r.max_seq_len = a->max_seq_len;
+        r.partition_size = plan.partition_size;
+        r.max_partitions = plan.parts;
+        r.group = p.group;
+        const int width = pa::reduce_width(c.head_dim, (long long)a->num_seqs * a->num_heads, num_sms);
+        if (pa::launch_reduce(c.head_dim, width, r, dim3(a->num_heads, a->num_seqs, c.head_dim / width), stream) !=
+            cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    if (weights && a->max_seq_len > 0) {
+        pa::KvWeightsParams k{};
+        k.scores = p.scores;
+        k.max_logits = p.max_logits;
+        k.exp_sums = p.exp_sums;
+        k.weights_in = a->weights_in;
+        k.weights_out = a->weights_out;
+        k.seq_lens = a->seq_lens;
+        k.score_stride = sp.score_stride;
+        k.weights_stride = a->weights_stride;
+        k.num_heads = a->num_heads;
+        k.num_kv_heads = c.num_kv_heads;
+        k.group = p.group;
+        k.max_blocks_per_seq = a->max_blocks_per_seq;
+        k.max_seq_len = a->max_seq_len;
+        k.partition_size = plan.partition_size;
+        k.max_partitions = plan.parts;
+        const int chunks = (a->max_seq_len + pa::kKvWeightsTokens - 1) / pa::kKvWeightsTokens;
+        if (pa::launch_kv_weights(k, dim3(chunks, c.num_kv_heads, a->num_seqs), stream) != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    return PA_OK;
+}
+
+// ---- append
+
+int check_append(const pa_kv_append_args* a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (a->max_blocks_per_seq < 0 || a->max_query_len < 0) return PA_ERR_INVALID_ARG;
+    int rc = check_shape(a->cache);
+    if (rc) return rc;
+    // the largest position must be an int
+    if ((long long)a->max_blocks_per_seq * pa::kBlockSize >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    if (a->num_tokens > 0 && a->max_query_len == 0) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
+    if (bad_ptr(a->k_new, 16) || bad_ptr(a->v_new, 16) || bad_ptr(a->block_tables, 4) ||
+        bad_ptr(a->context_lens, 4) || bad_ptr(a->query_start_loc, 4))
+        return PA_ERR_INVALID_ARG;
+    return check_pointers(a->cache);
+}
+
+// ---- prefill
+
+size_t prefix_copy_bytes(int num_seqs, int blocks_per_seq, int num_kv_heads, int head_dim) {
+    return up((size_t)num_seqs * blocks_per_seq * num_kv_heads * pa::kBlockSize * head_dim * 2);
+}
+
+size_t prefix_space(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format) {
+    if (format == PA_KV_F16 || max_context_len == 0) return 0;
+    const int n = blocks_of(max_context_len);
+    return 2 * prefix_copy_bytes(num_seqs, n, num_kv_heads, head_dim) + up((size_t)num_seqs * n * 4);
+}
+
+int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    const pa_kv_cache& c = a->cache;
+    int rc = check_shape(c);
+    if (rc) return rc;
+    pa_prefix_args p;
+    p.out = a->out;
+    p.q = a->q;
+    p.k_new = a->k_new;
+    p.v_new = a->v_new;
+    p.k_cache = c.k_cache;
+    p.v_cache = c.v_cache;
+    p.block_tables = a->block_tables;
+    p.context_lens = a->context_lens;
+    p.query_start_loc = a->query_start_loc;
+    p.num_seqs = a->num_seqs;
+    p.num_tokens = a->num_tokens;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    p.max_context_len = a->max_context_len;
+    p.max_query_len = a->max_query_len;
+    p.num_blocks = c.num_blocks;
+    p.num_heads = a->num_heads;
+    p.num_kv_heads = c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.block_size = c.block_size;
+    p.scale = a->scale;
+    if ((rc = pa::check_prefix(&p, o))) return rc;  // as the caller gave it
+    if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
+    if ((rc = check_pointers(c))) return rc;
+    if (c.format == PA_KV_F16) return pa_prefix_ex(&p, o, reinterpret_cast<pa_stream_t>(stream));
+
+    const int n = blocks_of(a->max_context_len);
+    const size_t need = prefix_space(a->num_seqs, a->max_context_len, c.num_kv_heads, c.head_dim, c.format);
+    // the copy replaces the cache; it has room for every sequence's longest context
+    p.num_blocks = (int64_t)a->num_seqs * n;
+    p.max_blocks_per_seq = n;
+    if (n > 0) {
+        if (p.num_blocks * c.num_kv_heads * pa::kBlockSize >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+        if (!ws || ws_bytes < need || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
+        const size_t copy = prefix_copy_bytes(a->num_seqs, n, c.num_kv_heads, c.head_dim);
+        uint8_t* w = static_cast<uint8_t*>(ws);
+        pa::KvExpandParams e{};
+        e.cache[0] = static_cast<const uint8_t*>(c.k_cache);
+        e.cache[1] = static_cast<const uint8_t*>(c.v_cache);
+        e.scales[0] = c.k_scales;
+        e.scales[1] = c.v_scales;
+        e.expanded[0] = reinterpret_cast<__half*>(w);
+        e.expanded[1] = reinterpret_cast<__half*>(w + copy);
+        e.tables = reinterpret_cast<int32_t*>(w + 2 * copy);
+        e.block_tables = a->block_tables;
+        e.context_lens = a->context_lens;
+        e.num_blocks = c.num_blocks;
+        e.num_kv_heads = c.num_kv_heads;
+        e.max_blocks_per_seq = a->max_blocks_per_seq;
+        e.blocks_per_seq = n;
+        e.max_context_len = a->max_context_len;
+        e.status = pa::device_status_ptr();
+        if (!e.status) return PA_ERR_CUDA;
+        p.k_cache = e.expanded[0];
+        p.v_cache = e.expanded[1];
+        p.block_tables = e.tables;
+        if (pa::launch_kv_expand(c.format, c.head_dim, e, dim3(n, c.num_kv_heads, a->num_seqs), stream) !=
+            cudaSuccess)
+            return PA_ERR_CUDA;
+    }
+    return pa_prefix_ex(&p, o, reinterpret_cast<pa_stream_t>(stream));
+}
+
+// ---- eviction
+
+int check_evict(const pa_kv_evict_args* a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_seqs > 65535) return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len < 0 || a->max_keep_len < 0 || a->sinks < 0 || a->recent < 0) return PA_ERR_INVALID_ARG;
+    if (a->max_blocks_per_seq < 0 || a->dst_max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+    int rc = check_shape(a->src);
+    if (rc || (rc = check_shape(a->dst))) return rc;
+    if (a->src.format != a->dst.format || a->src.num_kv_heads != a->dst.num_kv_heads ||
+        a->src.head_dim != a->dst.head_dim)
+        return PA_ERR_INVALID_ARG;
+    if ((long long)a->max_seq_len > (long long)a->max_blocks_per_seq * pa::kBlockSize ||
+        (long long)a->max_keep_len > (long long)a->dst_max_blocks_per_seq * pa::kBlockSize)
+        return PA_ERR_INVALID_ARG;
+    if (a->weights_stride < a->max_seq_len || (a->dst_weights && a->dst_weights_stride < a->max_keep_len))
+        return PA_ERR_INVALID_ARG;
+    if (a->num_seqs == 0) return PA_OK;
+    if (bad_ptr(a->seq_lens, 4) || bad_ptr(a->keep_lens, 4) || bad_ptr(a->new_lens, 4)) return PA_ERR_INVALID_ARG;
+    if (!aligned(a->weights, 4) || !aligned(a->dst_weights, 4) || !aligned(a->kept, 4)) return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len > 0 && !a->weights) return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len > 0 && a->max_keep_len > 0) {
+        if (!a->kept || bad_ptr(a->block_tables, 4) || bad_ptr(a->dst_block_tables, 4)) return PA_ERR_INVALID_ARG;
+        if ((rc = check_pointers(a->src)) || (rc = check_pointers(a->dst))) return rc;
+        if (a->src.num_blocks == 0 || a->dst.num_blocks == 0) return PA_ERR_INVALID_ARG;
+    }
+    // in place would read rows that are already overwritten
+    if (a->weights && a->weights == a->dst_weights) return PA_ERR_INVALID_ARG;
+    if (a->block_tables && a->block_tables == a->dst_block_tables &&
+        (a->src.k_cache == a->dst.k_cache || a->src.v_cache == a->dst.v_cache))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+// Blocks that share a (sequence, kv head) in the selection.
+int evict_cluster(int max_seq_len) { return max_seq_len <= 8192 ? 1 : max_seq_len <= 32768 ? 4 : 8; }
+
+}  // namespace
+
+extern "C" {
+
+int pa_kv_append(const pa_kv_append_args* a, pa_stream_t stream) {
+    int rc = check_append(a);
+    if (rc) return rc;
+    if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
+    const pa_kv_cache& c = a->cache;
+    pa::KvAppendParams p{};
+    p.cache[0] = c.k_cache;
+    p.cache[1] = c.v_cache;
+    p.scales[0] = c.k_scales;
+    p.scales[1] = c.v_scales;
+    p.fresh[0] = static_cast<const __half*>(a->k_new);
+    p.fresh[1] = static_cast<const __half*>(a->v_new);
+    p.block_tables = a->block_tables;
+    p.context_lens = a->context_lens;
+    p.query_start_loc = a->query_start_loc;
+    p.num_blocks = c.num_blocks;
+    p.num_kv_heads = c.num_kv_heads;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    p.num_tokens = a->num_tokens;
+    p.max_query_len = std::min(a->max_query_len, a->num_tokens);
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    // a run of n tokens touches at most ceil((n - 1) / 16) + 1 blocks
+    const int tiles = blocks_of(p.max_query_len - 1) + 1;
+    return pa::launch_kv_append(c.format, c.head_dim, p, dim3(tiles, c.num_kv_heads, a->num_seqs),
+                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
+                                   int format, int partition_size, int weights) {
+    if (num_seqs <= 0 || max_seq_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || partition_size < 0 ||
+        partition_size % pa::kBlockSize || pa::kv_decode_smem_bytes(format, head_dim) < 0)
+        return 0;
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK || num_sms <= 0) num_sms = kMaxSmsBound;
+    const DecodePlan plan =
+        plan_decode(num_seqs, max_seq_len, num_kv_heads, head_dim, format, num_sms, partition_size, PA_MODE_AUTO);
+    return decode_space(plan, num_seqs, num_heads, head_dim, max_seq_len, weights != 0).bytes;
+}
+
+int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void* workspace, size_t workspace_bytes,
+                 pa_stream_t stream) {
+    return run_decode(args, opts, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pa_kv_prefix_workspace_size(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format) {
+    if (num_seqs <= 0 || max_context_len <= 0 || num_kv_heads <= 0 || pa::kv_decode_smem_bytes(format, head_dim) < 0)
+        return 0;
+    return prefix_space(num_seqs, max_context_len, num_kv_heads, head_dim, format);
+}
+
+int pa_kv_prefix(const pa_kv_prefix_args* args, const pa_decode_opts* opts, void* workspace, size_t workspace_bytes,
+                 pa_stream_t stream) {
+    return run_prefix(args, opts, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pa_kv_evict(const pa_kv_evict_args* a, pa_stream_t stream_) {
+    int rc = check_evict(a);
+    if (rc) return rc;
+    if (a->num_seqs == 0) return PA_OK;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    pa::KvEvictParams p{};
+    p.src[0] = a->src.k_cache;
+    p.src[1] = a->src.v_cache;
+    p.src_scales[0] = a->src.k_scales;
+    p.src_scales[1] = a->src.v_scales;
+    p.dst[0] = a->dst.k_cache;
+    p.dst[1] = a->dst.v_cache;
+    p.dst_scales[0] = a->dst.k_scales;
+    p.dst_scales[1] = a->dst.v_scales;
+    p.block_tables = a->block_tables;
+    p.dst_block_tables = a->dst_block_tables;
+    p.seq_lens = a->seq_lens;
+    p.keep_lens = a->keep_lens;
+    p.weights = a->weights;
+    p.dst_weights = a->dst_weights;
+    p.kept = a->kept;
+    p.new_lens = a->new_lens;
+    p.src_blocks = a->src.num_blocks;
+    p.dst_blocks = a->dst.num_blocks;
+    p.weights_stride = a->weights_stride;
+    p.dst_weights_stride = a->dst_weights_stride;
+    p.num_kv_heads = a->src.num_kv_heads;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    p.dst_max_blocks_per_seq = a->dst_max_blocks_per_seq;
+    p.max_seq_len = a->max_seq_len;
+    p.max_keep_len = a->max_keep_len;
+    p.sinks = a->sinks;
+    p.recent = a->recent;
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    if (pa::launch_kv_evict_select(p, a->num_seqs, evict_cluster(a->max_seq_len), stream) != cudaSuccess)
+        return PA_ERR_CUDA;
+    const int blocks = blocks_of(std::min(a->max_keep_len, a->max_seq_len));
+    if (blocks > 0 && pa::launch_kv_evict_move(a->src.format, a->src.head_dim, p,
+                                               dim3(blocks, p.num_kv_heads, a->num_seqs), stream) != cudaSuccess)
+        return PA_ERR_CUDA;
+    return PA_OK;
+}
+
+}  // extern "C"
