@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional
 
 import torch
@@ -195,19 +196,17 @@ def _load() -> ctypes.CDLL:
     lib.pa_decode_noalloc.restype = i32
     lib.pa_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, i32, i32, f32, vp]
     lib.pa_kv_append.restype = i32
-    lib.pa_kv_append.argtypes = [ctypes.POINTER(pa_kv_append_args), vp]
+    lib.pa_kv_append.argtypes = [vp, vp]  # pa_kv_append_args
     lib.pa_kv_decode_workspace_size.restype = ctypes.c_size_t
     lib.pa_kv_decode_workspace_size.argtypes = [i32] * 8
     lib.pa_kv_decode.restype = i32
-    lib.pa_kv_decode.argtypes = [ctypes.POINTER(pa_kv_decode_args), ctypes.POINTER(pa_decode_opts), vp,
-                                 ctypes.c_size_t, vp]
+    lib.pa_kv_decode.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]  # pa_kv_decode_args, pa_decode_opts
     lib.pa_kv_prefix_workspace_size.restype = ctypes.c_size_t
     lib.pa_kv_prefix_workspace_size.argtypes = [i32] * 5
     lib.pa_kv_prefix.restype = i32
-    lib.pa_kv_prefix.argtypes = [ctypes.POINTER(pa_kv_prefix_args), ctypes.POINTER(pa_decode_opts), vp,
-                                 ctypes.c_size_t, vp]
+    lib.pa_kv_prefix.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]  # pa_kv_prefix_args, pa_decode_opts
     lib.pa_kv_evict.restype = i32
-    lib.pa_kv_evict.argtypes = [ctypes.POINTER(pa_kv_evict_args), vp]
+    lib.pa_kv_evict.argtypes = [vp, vp]  # pa_kv_evict_args
     return lib
 
 
@@ -511,68 +510,101 @@ def pa_merge_partials(out, max_logits, exp_sums, tmp_out, seq_lens, num_heads, h
 
 
 # --- the cache in 8 bits, and eviction by accumulated attention weight -------------------------------------------
+#
+# A short call's time is the host's, so these wrappers check each tensor with
+# plain attribute reads and pack the argument struct in one go.
 
 KV_FORMATS = {torch.float16: PA_KV_F16, torch.float8_e4m3fn: PA_KV_E4M3, torch.int8: PA_KV_INT8}
 
 
-def _need(name, t, dtype, device=None):
-    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _packer(cls):
+    """struct.Struct packing the (flattened) fields of a ctypes structure in native layout."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i", ctypes.c_float: "f"}
+
+    def flat(c):
+        return "".join(flat(t) if issubclass(t, ctypes.Structure) else codes[t] for _, t in c._fields_)
+
+    s = struct.Struct("@" + flat(cls))
+    # (a nested struct ends on its own alignment, as in C; only padding at the very end may be missing)
+    assert 0 <= ctypes.sizeof(cls) - s.size < 8, cls
+    return s
 
 
-def _kv_cache(k_cache, v_cache, k_scales, v_scales, device, what="") -> pa_kv_cache:
-    """The cache descriptor of [num_blocks, num_kv_heads, block_size, head_dim] tensors;
-    their dtype (float16, float8_e4m3fn or int8) is the format."""
-    fmt = KV_FORMATS.get(k_cache.dtype)
+_APPEND, _DECODE, _PREFIX, _EVICT = (_packer(c) for c in (pa_kv_append_args, pa_kv_decode_args, pa_kv_prefix_args,
+                                                          pa_kv_evict_args))
+
+
+def _bad(name, t, dtype, shape, dev):
+    """Say what is wrong with a tensor that failed its check."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _kv_cache(k_cache, v_cache, k_scales, v_scales, dev, what=""):
+    """The fields of the descriptor of [num_blocks, num_kv_heads, block_size, head_dim] caches; their
+    dtype (float16, float8_e4m3fn or int8) is the format."""
+    dtype = k_cache.dtype
+    fmt = KV_FORMATS.get(dtype)
     if fmt is None:
-        raise TypeError(f"{what}k_cache must be float16, float8_e4m3fn or int8, got {k_cache.dtype}")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError(f"{what}k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    _need(what + "k_cache", k_cache, k_cache.dtype, device)
-    _need(what + "v_cache", v_cache, k_cache.dtype, device)
+        raise TypeError(f"{what}k_cache must be float16, float8_e4m3fn or int8, got {dtype}")
     shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"{what}k_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    if dev < 0 or k_cache.get_device() != dev or not k_cache.is_contiguous():
+        _bad(what + "k_cache", k_cache, dtype, shape, dev)
+    if v_cache.dtype != dtype or v_cache.get_device() != dev or v_cache.shape != shape or not v_cache.is_contiguous():
+        _bad(what + "v_cache", v_cache, dtype, shape, dev)
+    nb, hkv, bs, d = shape
     if fmt == PA_KV_F16:
         if k_scales is not None or v_scales is not None:
             raise ValueError(f"{what}scales come with an 8-bit cache only")
-    else:
-        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if t is None:
-                raise ValueError(f"{what}{name} is needed with an 8-bit cache")
-            _need(what + name, t, torch.float32, device)
-            if t.shape != shape[:2]:
-                raise ValueError(f"{what}{name} must be [num_blocks, num_kv_heads]")
-    return pa_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), shape[0], shape[1],
-                       shape[3], shape[2], fmt)
+        return k_cache.data_ptr(), v_cache.data_ptr(), 0, 0, nb, hkv, d, bs, fmt
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t is None:
+            raise ValueError(f"{what}{name} is needed with an 8-bit cache")
+        if t.dtype != torch.float32 or t.get_device() != dev or t.shape != (nb, hkv) or not t.is_contiguous():
+            _bad(what + name, t, torch.float32, (nb, hkv), dev)
+    return k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), nb, hkv, d, bs, fmt
 
 
-def _shape(name, t, *sizes):
-    if tuple(t.shape) != sizes:
-        raise ValueError(f"{name} must be {list(sizes)}, got {list(t.shape)}")
+def _tensor(name, t, dtype, shape, dev):
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _bad(name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _lengths(device, num_seqs, **tensors):
-    for name, t in tensors.items():
-        _need(name, t, torch.int32, device)
-        _shape(name, t, num_seqs)
+def _table(name, t, num_seqs, dev):
+    """(pointer, columns) of a block table."""
+    shape = t.shape
+    if t.dtype != torch.int32 or t.get_device() != dev or len(shape) != 2 or shape[0] != num_seqs or not t.is_contiguous():
+        _bad(name, t, torch.int32, (num_seqs, "max_blocks_per_seq"), dev)
+    return t.data_ptr(), shape[1]
 
 
-def _tables(name, t, num_seqs, device):
-    _need(name, t, torch.int32, device)
-    if t.dim() != 2 or t.shape[0] != num_seqs:
-        raise ValueError(f"{name} must be [{num_seqs}, max_blocks_per_seq], got {list(t.shape)}")
+def _weights(name, t, num_seqs, heads, dev):
+    """(pointer, tokens of a row) of a weights array."""
+    shape = t.shape
+    if (t.dtype != torch.float32 or t.get_device() != dev or len(shape) != 3 or shape[0] != num_seqs
+            or shape[1] != heads or not t.is_contiguous()):
+        _bad(name, t, torch.float32, (num_seqs, heads, "tokens"), dev)
+    return t.data_ptr(), shape[2]
 
 
-def _workspace(workspace, nbytes, device, stream):
-    """The caller's workspace, or one that the allocator hands out on the call's stream (so that neither
-    its earlier nor its later users can overlap the call)."""
+def _workspace(workspace, nbytes, dev, stream):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one that the allocator hands out on the
+    call's stream (so that neither its earlier nor its later users can overlap the call)."""
     if workspace is not None:
-        if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
+    device = torch.device("cuda", dev)
     if stream is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     else:
@@ -583,25 +615,16 @@ def _workspace(workspace, nbytes, device, stream):
     return ws.data_ptr(), nbytes, ws
 
 
-class _on:
-    """The tensors' device as the current one, and the stream (None: that device's current stream)."""
-    __slots__ = ("dev", "prev", "stream")
-
-    def __init__(self, device, stream):
-        self.dev, self.prev, self.stream = device.index, -1, stream
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev:
-            self.prev = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-        return _stream_handle(self.stream)
-
-    def __exit__(self, *exc):
-        if self.prev >= 0:
-            torch.cuda.set_device(self.prev)
-
-
-def _raise(rc, what):
+def _call(what, dev, stream, fn, *args):
+    """Call fn(*args, stream) with the tensors' device current; None is that device's current stream."""
+    prev = torch.cuda.current_device()
+    if prev != dev:
+        torch.cuda.set_device(dev)
+    try:
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream_handle(stream))
+    finally:
+        if prev != dev:
+            torch.cuda.set_device(prev)
     if rc != PA_OK:
         raise PaDecodeError(rc, what)
 
@@ -613,20 +636,17 @@ def pa_kv_append(k_cache, v_cache, k_scales, v_scales, k_new, v_new, block_table
     k_cache / v_cache: [num_blocks, num_kv_heads, 16, head_dim] float16, float8_e4m3fn or int8;
     k_scales / v_scales: float32 [num_blocks, num_kv_heads] (None with float16); k_new / v_new:
     float16 [num_tokens, num_kv_heads, head_dim]."""
-    dev = k_cache.device
+    dev = k_cache.get_device()
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
-    B = context_lens.shape[0]
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _need(name, t, torch.float16, dev)
-        _shape(name, t, k_new.shape[0], cache.num_kv_heads, cache.head_dim)
-    _tables("block_tables", block_tables, B, dev)
-    _lengths(dev, B, context_lens=context_lens)
-    _lengths(dev, B + 1, query_start_loc=query_start_loc)
-    args = pa_kv_append_args(cache, k_new.data_ptr(), v_new.data_ptr(), block_tables.data_ptr(),
-                             context_lens.data_ptr(), query_start_loc.data_ptr(), B, k_new.shape[0],
-                             block_tables.shape[1], int(max_query_len))
-    with _on(dev, stream) as s:
-        _raise(lib.pa_kv_append(ctypes.byref(args), s), "pa_kv_append")
+    B, T = context_lens.shape[0], k_new.shape[0]
+    new = (T, cache[5], cache[6])
+    table, cols = _table("block_tables", block_tables, B, dev)
+    args = _APPEND.pack(*cache, _tensor("k_new", k_new, torch.float16, new, dev),
+                        _tensor("v_new", v_new, torch.float16, new, dev), table,
+                        _tensor("context_lens", context_lens, torch.int32, (B,), dev),
+                        _tensor("query_start_loc", query_start_loc, torch.int32, (B + 1,), dev), B, T, cols,
+                        int(max_query_len))
+    _call("pa_kv_append", dev, stream, lib.pa_kv_append, args)
 
 
 def pa_kv_decode_workspace_size(num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim, dtype,
@@ -646,39 +666,36 @@ def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq
     [num_seqs, num_kv_heads, >= max_seq_len]) the tokens' attention weights, summed over a kv head's
     query heads, are added to weights_in (None: zeros; may be weights_out itself).  `workspace`: a
     tensor of pa_kv_decode_workspace_size bytes (None: one from the allocator)."""
-    dev = q.device
+    dev = q.get_device()
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError("q must be [num_seqs, num_heads, head_dim]")
     B, H = q.shape[0], q.shape[1]
-    _need("q", q, torch.float16, dev)
-    _need("out", out, torch.float16, dev)
-    _shape("out", out, B, H, cache.head_dim)
-    _tables("block_tables", block_tables, B, dev)
-    _lengths(dev, B, seq_lens=seq_lens)
-    stride = 0
+    hkv, dim = cache[5], cache[6]
+    shape = (B, H, dim)
+    qp, op = _tensor("q", q, torch.float16, shape, dev), _tensor("out", out, torch.float16, shape, dev)
+    table, cols = _table("block_tables", block_tables, B, dev)
+    win = wout = stride = 0
     if weights_out is not None:
-        _need("weights_out", weights_out, torch.float32, dev)
-        if weights_out.dim() != 3:
-            raise ValueError("weights_out must be [num_seqs, num_kv_heads, >= max_seq_len]")
-        stride = weights_out.shape[2]
-        _shape("weights_out", weights_out, B, cache.num_kv_heads, stride)
+        wout, stride = _weights("weights_out", weights_out, B, hkv, dev)
         if weights_in is not None:
-            _need("weights_in", weights_in, torch.float32, dev)
-            _shape("weights_in", weights_in, B, cache.num_kv_heads, stride)
+            win = _tensor("weights_in", weights_in, torch.float32, (B, hkv, stride), dev)
     elif weights_in is not None:
         raise ValueError("weights_in needs weights_out")
-    args = pa_kv_decode_args(out.data_ptr(), q.data_ptr(), cache, block_tables.data_ptr(), seq_lens.data_ptr(),
-                             _ptr(weights_in), _ptr(weights_out), stride, B, block_tables.shape[1], int(max_seq_len),
-                             H, float(scale))
-    opts = make_opts(mode=mode, partition_size=partition_size, flags=flags, wait_limit=wait_limit)
-    with _on(dev, stream) as s:
+    max_seq_len = int(max_seq_len)
+    args = _DECODE.pack(op, qp, *cache, table, _tensor("seq_lens", seq_lens, torch.int32, (B,), dev), win, wout, stride,
+                        B, cols, max_seq_len, H, scale)
+    opts = None
+    if partition_size or flags or wait_limit or mode != "auto":
+        opts = ctypes.byref(make_opts(mode=mode, partition_size=partition_size, flags=flags, wait_limit=wait_limit))
+
+    def run(stream_handle):
         need = 0
         if workspace is None:
-            need = lib.pa_kv_decode_workspace_size(B, int(max_seq_len), H, cache.num_kv_heads, cache.head_dim,
-                                                   cache.format, int(partition_size), int(weights_out is not None))
+            need = lib.pa_kv_decode_workspace_size(B, max_seq_len, H, hkv, dim, cache[8], int(partition_size),
+                                                   int(wout != 0))
         ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
-        _raise(lib.pa_kv_decode(ctypes.byref(args), ctypes.byref(opts), ptr, nbytes, s), "pa_kv_decode")
+        return lib.pa_kv_decode(args, opts, ptr, nbytes, stream_handle)
+
+    _call("pa_kv_decode", dev, stream, run)
 
 
 def pa_kv_prefix_workspace_size(num_seqs, max_context_len, num_kv_heads, head_dim, dtype) -> int:
@@ -693,27 +710,22 @@ def pa_kv_prefix(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, blo
     """Chunked prefill whose context lies in a float16, float8_e4m3fn or int8 cache (see
     include/pa_decode.h); shapes as for pa_prefix.  `workspace`: a tensor of
     pa_kv_prefix_workspace_size bytes (None: one from the allocator)."""
-    dev = q.device
+    dev = q.get_device()
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError("q must be [num_tokens, num_heads, head_dim]")
     T, H, B = q.shape[0], q.shape[1], context_lens.shape[0]
-    for name, t, heads in (("q", q, H), ("out", out, H), ("k_new", k_new, cache.num_kv_heads),
-                           ("v_new", v_new, cache.num_kv_heads)):
-        _need(name, t, torch.float16, dev)
-        _shape(name, t, T, heads, cache.head_dim)
-    _tables("block_tables", block_tables, B, dev)
-    _lengths(dev, B, context_lens=context_lens)
-    _lengths(dev, B + 1, query_start_loc=query_start_loc)
-    args = pa_kv_prefix_args(out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cache,
-                             block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(), B, T,
-                             block_tables.shape[1], int(max_context_len), int(max_query_len), H, float(scale))
-    opts = make_opts(flags=flags, wait_limit=wait_limit)
-    with _on(dev, stream) as s:
-        need = 0 if workspace is not None else lib.pa_kv_prefix_workspace_size(
-            B, int(max_context_len), cache.num_kv_heads, cache.head_dim, cache.format)
-        ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
-        _raise(lib.pa_kv_prefix(ctypes.byref(args), ctypes.byref(opts), ptr, nbytes, s), "pa_kv_prefix")
+    hkv, dim = cache[5], cache[6]
+    shape, new = (T, H, dim), (T, hkv, dim)
+    table, cols = _table("block_tables", block_tables, B, dev)
+    args = _PREFIX.pack(_tensor("out", out, torch.float16, shape, dev), _tensor("q", q, torch.float16, shape, dev),
+                        _tensor("k_new", k_new, torch.float16, new, dev),
+                        _tensor("v_new", v_new, torch.float16, new, dev), *cache, table,
+                        _tensor("context_lens", context_lens, torch.int32, (B,), dev),
+                        _tensor("query_start_loc", query_start_loc, torch.int32, (B + 1,), dev), B, T, cols,
+                        int(max_context_len), int(max_query_len), H, scale)
+    opts = ctypes.byref(make_opts(flags=flags, wait_limit=wait_limit)) if flags or wait_limit else None
+    need = 0 if workspace is not None else lib.pa_kv_prefix_workspace_size(B, int(max_context_len), hkv, dim, cache[8])
+    ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
+    _call("pa_kv_prefix", dev, stream, lib.pa_kv_prefix, args, opts, ptr, nbytes)
 
 
 def pa_kv_evict(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, dst_k_cache, dst_v_cache,
@@ -725,25 +737,17 @@ def pa_kv_evict(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, ds
     source's.  weights: float32 [num_seqs, num_kv_heads, >= max_seq_len]; kept: int32 [num_seqs,
     num_kv_heads, max_keep_len]; new_lens: int32 [num_seqs]; dst_weights: float32 [num_seqs,
     num_kv_heads, >= max_keep_len] or None."""
-    dev = k_cache.device
+    dev = k_cache.get_device()
     src = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
     dst = _kv_cache(dst_k_cache, dst_v_cache, dst_k_scales, dst_v_scales, dev, "dst_")
-    B, hkv = seq_lens.shape[0], src.num_kv_heads
-    _lengths(dev, B, seq_lens=seq_lens, keep_lens=keep_lens, new_lens=new_lens)
-    _tables("block_tables", block_tables, B, dev)
-    _tables("dst_block_tables", dst_block_tables, B, dev)
-    _need("weights", weights, torch.float32, dev)
-    _need("kept", kept, torch.int32, dev)
-    _shape("kept", kept, B, hkv, int(max_keep_len))
-    for name, t in (("weights", weights), ("dst_weights", dst_weights)):
-        if t is not None:
-            _need(name, t, torch.float32, dev)
-            if t.dim() != 3 or tuple(t.shape[:2]) != (B, hkv):
-                raise ValueError(f"{name} must be [{B}, {hkv}, tokens]")
-    args = pa_kv_evict_args(src, dst, block_tables.data_ptr(), dst_block_tables.data_ptr(), seq_lens.data_ptr(),
-                            keep_lens.data_ptr(), weights.data_ptr(), _ptr(dst_weights), kept.data_ptr(),
-                            new_lens.data_ptr(), weights.shape[2], dst_weights.shape[2] if dst_weights is not None else 0,
-                            B, block_tables.shape[1], dst_block_tables.shape[1], int(max_seq_len), int(max_keep_len),
-                            int(sinks), int(recent))
-    with _on(dev, stream) as s:
-        _raise(lib.pa_kv_evict(ctypes.byref(args), s), "pa_kv_evict")
+    B, hkv, max_keep_len = seq_lens.shape[0], src[5], int(max_keep_len)
+    table, cols = _table("block_tables", block_tables, B, dev)
+    dst_table, dst_cols = _table("dst_block_tables", dst_block_tables, B, dev)
+    w, stride = _weights("weights", weights, B, hkv, dev)
+    dst_w, dst_stride = (0, 0) if dst_weights is None else _weights("dst_weights", dst_weights, B, hkv, dev)
+    args = _EVICT.pack(*src, *dst, table, dst_table, _tensor("seq_lens", seq_lens, torch.int32, (B,), dev),
+                       _tensor("keep_lens", keep_lens, torch.int32, (B,), dev), w, dst_w,
+                       _tensor("kept", kept, torch.int32, (B, hkv, max_keep_len), dev),
+                       _tensor("new_lens", new_lens, torch.int32, (B,), dev), stride, dst_stride, B, cols, dst_cols,
+                       int(max_seq_len), max_keep_len, int(sinks), int(recent))
+    _call("pa_kv_evict", dev, stream, lib.pa_kv_evict, args)
