@@ -1034,8 +1034,6 @@ namespace pa {
 
 int sm_count(int* num_sms) { return query_sm_count(num_sms); }
 
-int reduce_width(int head_dim, long long pairs, int num_sms) { return reduce_slice(head_dim, pairs, num_sms); }
-
 int check_prefix(const pa_prefix_args* a, const pa_decode_opts* o) { return validate_prefix(a, o); }
 
 int make_block_map(CUtensorMap* map, const void* base, long long num_blocks, int num_kv_heads, int head_dim,

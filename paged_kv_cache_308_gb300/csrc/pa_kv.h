@@ -15,7 +15,6 @@ namespace pa {
 
 // Defined in pa_api.cpp for the other C-ABI sources.
 int sm_count(int* num_sms);                               // of the current device; a PA_* code
-int reduce_width(int head_dim, long long pairs, int num_sms);  // head_dim slice of a reduce CTA
 int check_prefix(const pa_prefix_args* args, const pa_decode_opts* opts);  // a PA_* code
 // A cache of `elem_bytes`-byte elements viewed as (box column, row, column
 // chunk); one box brings the 16 rows of a (block, kv head).  Rows of 128
@@ -31,42 +30,45 @@ struct KvDecodeParams {
     const float* v_scales;
     const int32_t* block_tables;
     const int32_t* seq_lens;
-    float* max_logits;  // [B][H][max_partitions]: reference exponents of the partials, log2 domain
-    float* exp_sums;    // [B][H][max_partitions]
-    float* tmp_out;     // [B][H][max_partitions][D], normalised
-    float* scores;      // [B][H][score_stride], log2 domain; null without weights
+    // Partials, `slots` per kv head (slot: see pa_kv_decode.cu):
+    float2* sums;  // [Hkv][slots][group]: reference exponent (log2 domain) and sum relative to it
+    float* acc;    // [Hkv][slots][group][D], normalised
+    int* seq_parts;  // flat: [B] of (first slot, number of partials), of sequences with tokens
+    float* scores;   // [B][H][score_stride], log2 domain; null without weights
     long long score_stride;
-    long long num_blocks;
-    int num_heads, num_kv_heads, group;
+    long long num_blocks, slots;
+    int num_seqs, num_heads, num_kv_heads, group;
     int max_blocks_per_seq, max_seq_len;
-    int partition_size, max_partitions;
+    int flat, ctas_per_head;                // flat form
+    int partition_size, max_partitions;     // grid form
     float scale_log2;
     unsigned wait_limit;
     int force_timeout;
     unsigned int* status;
 };
 
-struct KvWeightsParams {
+struct KvMergeParams {
+    __half* out;
+    const float2* sums;
+    const float* acc;
+    const int* seq_parts;
     const float* scores;
-    const float* max_logits;
-    const float* exp_sums;
     const float* weights_in;  // null: zeros
     float* weights_out;
     const int32_t* seq_lens;
-    long long score_stride, weights_stride;
-    int num_heads, num_kv_heads, group;
-    int max_blocks_per_seq, max_seq_len;
-    int partition_size, max_partitions;
+    long long score_stride, weights_stride, slots;
+    int num_heads, num_kv_heads, group, max_seq_len;
+    int slices;  // blocks of a (sequence, kv head) that merge; the rest add weights
+    int flat, partition_size, max_partitions;
+    unsigned int* status;
 };
 
-// Warps of a decode CTA, and the copies of one block (K and V) each keeps in flight.
-constexpr int kKvWarps = 4;
-int kv_decode_stages(int format, int head_dim);
-int kv_decode_smem_bytes(int format, int head_dim);
+constexpr int kKvWarps = 4;                        // of a decode CTA
+int kv_decode_ctas(int format, int head_dim);      // decode CTAs an SM holds at once; -1: not compiled
 cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, const CUtensorMap& tk,
                              const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
-constexpr int kKvWeightsTokens = 1024;  // tokens of a CTA of the weights kernel
-cudaError_t launch_kv_weights(const KvWeightsParams& prm, dim3 grid, cudaStream_t stream);
+constexpr int kKvWeightsTokens = 1024;  // tokens of a CTA that adds weights
+cudaError_t launch_kv_merge(int head_dim, const KvMergeParams& prm, dim3 grid, cudaStream_t stream);
 
 struct KvAppendParams {
     void* cache[2];        // K, V

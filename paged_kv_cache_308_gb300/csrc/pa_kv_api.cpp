@@ -17,8 +17,6 @@
 namespace {
 
 constexpr size_t kWsAlign = 256;
-constexpr int kDefaultPartition = 512;
-constexpr long long kSmemPerSm = 228 * 1024;
 // SM count assumed by the workspace size when no device answers (above any GPU's)
 constexpr int kMaxSmsBound = 1024;
 
@@ -51,46 +49,66 @@ bool bad_ptr(const void* p, uintptr_t a) { return !p || !aligned(p, a); }
 // ---- decode
 
 struct DecodePlan {
-    int partition_size, parts;
+    bool flat;
+    int ctas_per_head;          // flat
+    int partition_size, parts;  // grid
+    long long slots;            // partials of a kv head
 };
 
-// Partitions of the decode grid.  One sequence: one wave of the CTAs the SMs
-// hold at once.  A batch: 512 tokens, halved when the grid would leave SMs
-// without a CTA; a sequence of one partition needs no reduce.
+// Sequences of up to this many tokens take one CTA each and no merge; one
+// sequence takes a wave of equal partitions (whose block ids can be read before
+// its length is known), a batch equal shares of its blocks for the CTAs the
+// SMs hold at once.
+constexpr int kSingleMaxLen = 128;
+
 DecodePlan plan_decode(int num_seqs, int max_seq_len, int num_kv_heads, int head_dim, int format, int num_sms,
                        int partition_size, int mode) {
+    DecodePlan p{};
     const int whole = std::max(1, blocks_of(max_seq_len)) * pa::kBlockSize;
-    int part = partition_size;
-    if (mode == PA_MODE_SINGLE) part = whole;
-    if (part <= 0) {
-        const long long per_sm = std::max(1ll, kSmemPerSm / (pa::kv_decode_smem_bytes(format, head_dim) + 1024));
-        const long long per_seq = per_sm * num_sms / std::max(1ll, (long long)num_seqs * num_kv_heads);
-        if (num_seqs == 1 && per_seq >= 2) {
-            part = std::max(blocks_of((max_seq_len + per_seq - 1) / per_seq), pa::kKvWarps) * pa::kBlockSize;
-        } else {
-            part = kDefaultPartition;
-            const long long ctas = (long long)((max_seq_len + part - 1) / part) * num_kv_heads * num_seqs;
-            if (ctas < num_sms) part /= 2;
-        }
+    if (mode == PA_MODE_SINGLE || (partition_size <= 0 && mode == PA_MODE_AUTO && max_seq_len <= kSingleMaxLen))
+        partition_size = whole;
+    const long long slots = std::max(1ll, (long long)pa::kv_decode_ctas(format, head_dim) * num_sms / num_kv_heads);
+    if (partition_size <= 0 && num_seqs == 1)  // (one block per warp at least)
+        partition_size =
+            std::max(blocks_of((max_seq_len + slots - 1) / slots), pa::kKvWarps) * pa::kBlockSize;
+    if (partition_size > 0) {
+        p.partition_size = std::min(partition_size, whole);
+        p.parts = std::max(1, (max_seq_len + p.partition_size - 1) / p.partition_size);
+        p.slots = (long long)num_seqs * p.parts;
+        return p;
     }
-    part = std::min(part, whole);
-    return {part, std::max(1, (max_seq_len + part - 1) / part)};
+    p.flat = true;
+    p.ctas_per_head = static_cast<int>(slots);
+    p.slots = (long long)p.ctas_per_head + num_seqs;
+    return p;
 }
 
 struct DecodeSpace {
-    size_t sums, acc, scores, bytes;  // offsets of exp_sums, tmp_out, scores; max_logits is at 0
+    size_t parts, acc, scores, bytes;  // offsets of seq_parts, acc and scores; the sums are at 0
     long long score_stride;
 };
 
-DecodeSpace decode_space(const DecodePlan& p, int num_seqs, int num_heads, int head_dim, int max_seq_len, bool weights) {
+DecodeSpace decode_space(const DecodePlan& p, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                         int max_seq_len, bool weights) {
     DecodeSpace s;
-    const size_t rows = (size_t)num_seqs * num_heads * p.parts;
-    const bool partials = p.parts > 1 || weights;
-    s.sums = partials ? up(rows * 4) : 0;
-    s.acc = 2 * s.sums;
-    s.scores = s.acc + (p.parts > 1 ? up(rows * head_dim * 4) : 0);
+    const size_t rows = (size_t)p.slots * num_heads;  // slots of a kv head x kv heads x group
+    const bool split = p.flat || p.parts > 1;
+    s.parts = split || weights ? up(rows * 8) : 0;
+    s.acc = s.parts + (p.flat ? up((size_t)num_seqs * 8) : 0);
+    s.scores = s.acc + (split ? up(rows * head_dim * 4) : 0);
     s.score_stride = (long long)blocks_of(max_seq_len) * pa::kBlockSize;
     s.bytes = s.scores + (weights ? up((size_t)num_seqs * num_heads * s.score_stride * 4) : 0);
+    return s;
+}
+
+// Blocks that merge one (sequence, kv head): about two per SM over the batch,
+// a power of two that leaves each at least 8 and at most 256 columns of four.
+int merge_slices(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_sms) {
+    const int cols = num_heads / num_kv_heads * (head_dim / 4);
+    int s = 1;
+    while (cols / s > 256) s *= 2;
+    while ((long long)num_seqs * num_kv_heads * s < 2ll * num_sms && head_dim / 4 % (2 * s) == 0 && cols / (2 * s) >= 8)
+        s *= 2;
     return s;
 }
 
@@ -110,6 +128,8 @@ int check_decode(const pa_kv_decode_args* a, const pa_decode_opts* o) {
     if ((long long)a->max_seq_len > (long long)a->max_blocks_per_seq * pa::kBlockSize) return PA_ERR_INVALID_ARG;
     if (a->weights_out && a->weights_stride < a->max_seq_len) return PA_ERR_INVALID_ARG;
     if (a->weights_in && !a->weights_out) return PA_ERR_INVALID_ARG;
+    // the batch's blocks are numbered in 32 bits
+    if ((long long)a->num_seqs * blocks_of(a->max_seq_len) >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     if (a->num_seqs == 0) return PA_OK;
     if (bad_ptr(a->out, 16) || bad_ptr(a->q, 16) || bad_ptr(a->block_tables, 4) || bad_ptr(a->seq_lens, 4))
         return PA_ERR_INVALID_ARG;
@@ -129,8 +149,10 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     const DecodePlan plan = plan_decode(a->num_seqs, a->max_seq_len, c.num_kv_heads, c.head_dim, c.format, num_sms,
                                         o ? o->partition_size : 0, o ? o->mode : PA_MODE_AUTO);
     const bool weights = a->weights_out != nullptr;
-    const DecodeSpace sp = decode_space(plan, a->num_seqs, a->num_heads, c.head_dim, a->max_seq_len, weights);
+    const DecodeSpace sp =
+        decode_space(plan, a->num_seqs, a->num_heads, c.num_kv_heads, c.head_dim, a->max_seq_len, weights);
     if (sp.bytes > 0 && (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign))) return PA_ERR_WORKSPACE;
+    const bool split = plan.flat || plan.parts > 1;
 
     const int elem = c.format == PA_KV_F16 ? 2 : 1;
     CUtensorMap tk, tv;
@@ -138,7 +160,6 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
         (rc = pa::make_block_map(&tv, c.v_cache, c.num_blocks, c.num_kv_heads, c.head_dim, elem)))
         return rc;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    const bool split = plan.parts > 1;
     pa::KvDecodeParams p{};
     p.out = static_cast<__half*>(a->out);
     p.q = static_cast<const __half*>(a->q);
@@ -146,17 +167,21 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     p.v_scales = c.v_scales;
     p.block_tables = a->block_tables;
     p.seq_lens = a->seq_lens;
-    p.max_logits = split || weights ? reinterpret_cast<float*>(w) : nullptr;
-    p.exp_sums = split || weights ? reinterpret_cast<float*>(w + sp.sums) : nullptr;
-    p.tmp_out = split ? reinterpret_cast<float*>(w + sp.acc) : nullptr;
+    p.sums = split || weights ? reinterpret_cast<float2*>(w) : nullptr;
+    p.seq_parts = plan.flat ? reinterpret_cast<int*>(w + sp.parts) : nullptr;
+    p.acc = split ? reinterpret_cast<float*>(w + sp.acc) : nullptr;
     p.scores = weights ? reinterpret_cast<float*>(w + sp.scores) : nullptr;
     p.score_stride = sp.score_stride;
     p.num_blocks = c.num_blocks;
+    p.slots = plan.slots;
+    p.num_seqs = a->num_seqs;
     p.num_heads = a->num_heads;
     p.num_kv_heads = c.num_kv_heads;
     p.group = a->num_heads / c.num_kv_heads;
     p.max_blocks_per_seq = a->max_blocks_per_seq;
     p.max_seq_len = a->max_seq_len;
+    p.flat = plan.flat;
+    p.ctas_per_head = plan.ctas_per_head;
     p.partition_size = plan.partition_size;
     p.max_partitions = plan.parts;
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
@@ -164,49 +189,37 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     p.force_timeout = (o && (o->flags & PA_FLAG_FORCE_TIMEOUT)) ? 1 : 0;
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
-    if (pa::launch_kv_decode(c.format, c.head_dim, p, tk, tv, dim3(plan.parts, c.num_kv_heads, a->num_seqs), stream) !=
-        cudaSuccess)
-        return PA_ERR_CUDA;
-    if (split) {
-        pa::ReduceParams r{};
-        r.out = p.out;
-        r.max_logits = p.max_logits;
-        r.exp_sums = p.exp_sums;
-        r.tmp_out = p.tmp_out;
-        r.seq_lens = a->seq_lens;
-        r.num_heads = a->num_heads;
-        r.max_blocks_per_seq = a->max_blocks_per_seq;
-        r.max_seq_len = a->max_seq_len;
-        r.partition_size = plan.partition_size;
-        r.max_partitions = plan.parts;
-        r.group = p.group;
-        const int width = pa::reduce_width(c.head_dim, (long long)a->num_seqs * a->num_heads, num_sms);
-        if (pa::launch_reduce(c.head_dim, width, r, dim3(a->num_heads, a->num_seqs, c.head_dim / width), stream) !=
-            cudaSuccess)
-            return PA_ERR_CUDA;
-    }
-    if (weights && a->max_seq_len > 0) {
-        pa::KvWeightsParams k{};
-        k.scores = p.scores;
-        k.max_logits = p.max_logits;
-        k.exp_sums = p.exp_sums;
-        k.weights_in = a->weights_in;
-        k.weights_out = a->weights_out;
-        k.seq_lens = a->seq_lens;
-        k.score_stride = sp.score_stride;
-        k.weights_stride = a->weights_stride;
-        k.num_heads = a->num_heads;
-        k.num_kv_heads = c.num_kv_heads;
-        k.group = p.group;
-        k.max_blocks_per_seq = a->max_blocks_per_seq;
-        k.max_seq_len = a->max_seq_len;
-        k.partition_size = plan.partition_size;
-        k.max_partitions = plan.parts;
-        const int chunks = (a->max_seq_len + pa::kKvWeightsTokens - 1) / pa::kKvWeightsTokens;
-        if (pa::launch_kv_weights(k, dim3(chunks, c.num_kv_heads, a->num_seqs), stream) != cudaSuccess)
-            return PA_ERR_CUDA;
-    }
-    return PA_OK;
+    const dim3 grid = plan.flat ? dim3(plan.ctas_per_head * c.num_kv_heads)
+                                : dim3(plan.parts, c.num_kv_heads, a->num_seqs);
+    if (pa::launch_kv_decode(c.format, c.head_dim, p, tk, tv, grid, stream) != cudaSuccess) return PA_ERR_CUDA;
+    if (!split && !weights) return PA_OK;
+    pa::KvMergeParams m{};
+    m.out = p.out;
+    m.sums = p.sums;
+    m.acc = p.acc;
+    m.seq_parts = p.seq_parts;
+    m.scores = p.scores;
+    m.weights_in = a->weights_in;
+    m.weights_out = a->weights_out;
+    m.seq_lens = a->seq_lens;
+    m.score_stride = sp.score_stride;
+    m.weights_stride = a->weights_stride;
+    m.slots = plan.slots;
+    m.num_heads = a->num_heads;
+    m.num_kv_heads = c.num_kv_heads;
+    m.group = p.group;
+    m.max_seq_len = a->max_seq_len;
+    m.slices = split ? merge_slices(a->num_seqs, a->num_heads, c.num_kv_heads, c.head_dim, num_sms) : 0;
+    m.flat = plan.flat;
+    m.partition_size = plan.partition_size;
+    m.max_partitions = plan.parts;
+    m.status = p.status;
+    const int chunks = weights ? (a->max_seq_len + pa::kKvWeightsTokens - 1) / pa::kKvWeightsTokens : 0;
+    if (m.slices + chunks == 0) return PA_OK;
+    return pa::launch_kv_merge(c.head_dim, m, dim3(m.slices + chunks, c.num_kv_heads, a->num_seqs), stream) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 // ---- append
@@ -381,13 +394,13 @@ int pa_kv_append(const pa_kv_append_args* a, pa_stream_t stream) {
 size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
                                    int format, int partition_size, int weights) {
     if (num_seqs <= 0 || max_seq_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || partition_size < 0 ||
-        partition_size % pa::kBlockSize || pa::kv_decode_smem_bytes(format, head_dim) < 0)
+        partition_size % pa::kBlockSize || pa::kv_decode_ctas(format, head_dim) < 0)
         return 0;
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK || num_sms <= 0) num_sms = kMaxSmsBound;
     const DecodePlan plan =
         plan_decode(num_seqs, max_seq_len, num_kv_heads, head_dim, format, num_sms, partition_size, PA_MODE_AUTO);
-    return decode_space(plan, num_seqs, num_heads, head_dim, max_seq_len, weights != 0).bytes;
+    return decode_space(plan, num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len, weights != 0).bytes;
 }
 
 int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void* workspace, size_t workspace_bytes,
@@ -396,7 +409,7 @@ int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void
 }
 
 size_t pa_kv_prefix_workspace_size(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format) {
-    if (num_seqs <= 0 || max_context_len <= 0 || num_kv_heads <= 0 || pa::kv_decode_smem_bytes(format, head_dim) < 0)
+    if (num_seqs <= 0 || max_context_len <= 0 || num_kv_heads <= 0 || pa::kv_decode_ctas(format, head_dim) < 0)
         return 0;
     return prefix_space(num_seqs, max_context_len, num_kv_heads, head_dim, format);
 }

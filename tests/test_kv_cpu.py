@@ -89,7 +89,7 @@ def test_decode_options_and_workspace_are_checked():
     n = pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.float8_e4m3fn, 64)
     up = lambda x: -(-x // 256) * 256
     rows = 2 * 24 * 13
-    assert n == 2 * up(rows * 4) + rows * 256 * 4
+    assert n == up(rows * 8) + rows * 256 * 4
     assert call("pa_kv_decode", decode_args(), o, FAKE, n - 1) == pb.PA_ERR_WORKSPACE
     assert call("pa_kv_decode", decode_args(), o, None, n) == pb.PA_ERR_WORKSPACE
     assert call("pa_kv_decode", decode_args(), o, FAKE + 16, n) == pb.PA_ERR_WORKSPACE
