@@ -81,7 +81,8 @@ struct KvAppendParams {
     int num_kv_heads, max_blocks_per_seq, num_tokens, max_query_len;
     unsigned int* status;
 };
-cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, dim3 grid, cudaStream_t stream);
+cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, int tiles, int num_seqs,
+                             cudaStream_t stream);
 
 struct KvExpandParams {
     const uint8_t* cache[2];
@@ -112,9 +113,11 @@ struct KvEvictParams {
     long long src_blocks, dst_blocks, weights_stride, dst_weights_stride;
     int num_kv_heads, max_blocks_per_seq, dst_max_blocks_per_seq;
     int max_seq_len, max_keep_len, sinks, recent;
+    int key_words;  // keys a block of the selection holds in shared memory
     unsigned int* status;
 };
 constexpr int kEvictThreads = 1024;
+constexpr int kEvictKeyWords = 48 * 1024;  // at most: 192 KB
 cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream);
 cudaError_t launch_kv_evict_move(int format, int head_dim, const KvEvictParams& prm, dim3 grid, cudaStream_t stream);
 

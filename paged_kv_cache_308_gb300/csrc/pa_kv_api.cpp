@@ -29,7 +29,7 @@ int check_shape(const pa_kv_cache& c) {
     if (c.format != PA_KV_F16 && c.format != PA_KV_E4M3 && c.format != PA_KV_INT8) return PA_ERR_INVALID_ARG;
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return PA_ERR_UNSUPPORTED;
     if (c.block_size != pa::kBlockSize) return PA_ERR_UNSUPPORTED;
-    if (c.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a grid dimension
+    if (c.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a grid dimension (and x 8 another's)
     // TMA row coordinates are 32-bit
     if (c.num_blocks >= (1ll << 31) || c.num_blocks * c.num_kv_heads * c.block_size >= (1ll << 31))
         return PA_ERR_UNSUPPORTED;
@@ -354,8 +354,16 @@ int check_evict(const pa_kv_evict_args* a) {
     return PA_OK;
 }
 
-// Blocks that share a (sequence, kv head) in the selection.
-int evict_cluster(int max_seq_len) { return max_seq_len <= 8192 ? 1 : max_seq_len <= 32768 ? 4 : 8; }
+// Blocks that share a (sequence, kv head) in the selection: while the SMs hold
+// the whole grid and each block gets 1024 tokens or more, up to the 8 of a
+// portable cluster.
+int evict_cluster(int max_seq_len, long long pairs, int num_sms) {
+    int c = 1;
+    while (c < 8 && pairs * 2 * c <= num_sms && max_seq_len >= 2048 * c) c *= 2;
+    // more than one block can hold in shared memory is shared out whatever the grid
+    while (c < 8 && max_seq_len > (long long)pa::kEvictKeyWords * c) c *= 2;
+    return c;
+}
 
 }  // namespace
 
@@ -385,7 +393,7 @@ int pa_kv_append(const pa_kv_append_args* a, pa_stream_t stream) {
     if (!p.status) return PA_ERR_CUDA;
     // a run of n tokens touches at most ceil((n - 1) / 16) + 1 blocks
     const int tiles = blocks_of(p.max_query_len - 1) + 1;
-    return pa::launch_kv_append(c.format, c.head_dim, p, dim3(tiles, c.num_kv_heads, a->num_seqs),
+    return pa::launch_kv_append(c.format, c.head_dim, p, tiles, a->num_seqs,
                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
@@ -454,8 +462,11 @@ int pa_kv_evict(const pa_kv_evict_args* a, pa_stream_t stream_) {
     p.recent = a->recent;
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
-    if (pa::launch_kv_evict_select(p, a->num_seqs, evict_cluster(a->max_seq_len), stream) != cudaSuccess)
-        return PA_ERR_CUDA;
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;
+    const int cluster = evict_cluster(a->max_seq_len, (long long)a->num_seqs * p.num_kv_heads, num_sms);
+    p.key_words = std::min(pa::kEvictKeyWords, (a->max_seq_len + cluster - 1) / cluster);
+    if (pa::launch_kv_evict_select(p, a->num_seqs, cluster, stream) != cudaSuccess) return PA_ERR_CUDA;
     const int blocks = blocks_of(std::min(a->max_keep_len, a->max_seq_len));
     if (blocks > 0 && pa::launch_kv_evict_move(a->src.format, a->src.head_dim, p,
                                                dim3(blocks, p.num_kv_heads, a->num_seqs), stream) != cudaSuccess)

@@ -35,17 +35,21 @@ __device__ __forceinline__ float block_scale(float amax) {
     }
 }
 
-// x in units of s.  Scales of E4M3 blocks are powers of two unless a caller
-// wrote others: then multiplying by 1 / s is the same as dividing.
+__device__ __forceinline__ bool power_of_two(float s) {
+    return (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-100f && s <= 0x1p100f;
+}
+
+// A scale to divide by.  E4M3 scales are powers of two unless a caller wrote
+// others: then multiplying by 1 / s is the same as dividing.  For INT8 the
+// product with 1 / s finds the nearest integer wherever it is not next to a
+// tie (see codes8).
 struct Unit {
     float s, inv;
     bool pow2;
-    __device__ explicit Unit(float scale) : s(scale) {
-        const uint32_t bits = __float_as_uint(scale);
-        pow2 = (bits & 0x7fffffu) == 0 && scale >= 0x1p-100f && scale <= 0x1p100f;
-        inv = pow2 ? __uint_as_float((254u << 23) - bits) : 0.f;
+    __device__ explicit Unit(float scale) : s(scale), pow2(power_of_two(scale)) {
+        inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(scale)) : scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
     }
-    __device__ __forceinline__ float of(float x) const {
+    __device__ __forceinline__ float of(float x) const {  // x / s; x itself for s = 0
         if (pow2) return x * inv;
         return s > 0.f ? __fdiv_rn(x, s) : x;
     }
@@ -61,22 +65,104 @@ __device__ __forceinline__ uint32_t code_of(float t) {
     }
 }
 
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Codes of eight values in the unit u.
+// INT8: with t = x / s rounded twice (1 / s and the product, off by less than
+// 127 * 2^-22 < 2^-14 in all), adding and taking away 1.5 * 2^23 rounds t to
+// the nearest integer q, and the sum's low byte is q's code.  |t - q| below
+// 1/2 - 2^-12 proves that x / s rounds to q too.  Anything else (a tie or
+// next to one, a code out of range, infinities, NaN, s = 0) takes the division.
 template <int F>
-__device__ __forceinline__ float value_of(uint32_t code) {
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Unit& u) {
+    uint32_t w[2];
     if constexpr (F == PA_KV_E4M3) {
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
+        if (u.pow2) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[j] = e4m3x2(x[4 * j] * u.inv, x[4 * j + 1] * u.inv) |
+                       e4m3x2(x[4 * j + 2] * u.inv, x[4 * j + 3] * u.inv) << 16;
+            return make_uint2(w[0], w[1]);
+        }
     } else {
-        return static_cast<float>(static_cast<int8_t>(code));
+        constexpr float kMagic = 12582912.f;
+        uint32_t r[8];
+        float off = 0.f, top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float t = x[j] * u.inv;
+            const float v = t + kMagic;
+            r[j] = __float_as_uint(v);
+            off = fmaxf(off, fabsf(t - (v - kMagic)));
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(t)));  // NaN stays visible
+        }
+        if (off < 0.5f - 0x1p-12f && top < 127.4f && u.s > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[j] = __byte_perm(__byte_perm(r[4 * j], r[4 * j + 1], 0x0040),
+                                   __byte_perm(r[4 * j + 2], r[4 * j + 3], 0x0040), 0x5410);
+            return make_uint2(w[0], w[1]);
+        }
+    }
+    w[0] = w[1] = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j >> 2] |= code_of<F>(u.of(x[j])) << (8 * (j & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+// Eight codes as numbers.
+template <int F>
+__device__ __forceinline__ void values8(uint2 w, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t v = j < 4 ? w.x : w.y;
+        if constexpr (F == PA_KV_E4M3) {
+            if (j & 1) continue;
+            const __half2_raw h =
+                __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> (8 * (j & 2))), __NV_E4M3);
+            const float2 f = __half22float2(__half2(h));
+            x[j] = f.x;
+            x[j + 1] = f.y;
+        } else {  // the byte plus 128 under the exponent of 2^23
+            const uint32_t b = __byte_perm(v ^ 0x80808080u, 0x4b000000u, 0x7540 + (j & 3));
+            x[j] = __uint_as_float(b) - (8388608.f + 128.f);
+        }
     }
 }
 
-// Four codes of `w` from scale s0 to the unit u.
+// Eight codes from scale s0 to the unit u.
 template <int F>
-__device__ __forceinline__ uint32_t recode(uint32_t w, float s0, const Unit& u) {
-    uint32_t r = 0;
+__device__ __forceinline__ uint2 recode8(uint2 w, float s0, const Unit& u) {
+    if constexpr (F == PA_KV_E4M3) {
+        const float ratio = s0 * u.inv;
+        if (u.pow2 && power_of_two(s0) && ratio <= 1.f) {
+            // halves do: a code times a power of two is exact in them unless it is
+            // far below the smallest code, where both round to zero
+            const __half2 k = __float2half2_rn(ratio);
+            uint32_t r[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r |= code_of<F>(u.of(value_of<F>((w >> (8 * i)) & 0xffu) * s0)) << (8 * i);
-    return r;
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t v = j ? w.y : w.x;
+                uint32_t two[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 h = __half2(
+                        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v >> (16 * i)), __NV_E4M3));
+                    two[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(h, k)), __NV_SATFINITE,
+                                                        __NV_E4M3);
+                }
+                r[j] = two[0] | two[1] << 16;
+            }
+            return make_uint2(r[0], r[1]);
+        }
+    }
+    float x[8];
+    values8<F>(w, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= s0;
+    return codes8<F>(x, u);
 }
 
 // K's or V's of a pair of arguments, without indexing the parameter memory.
@@ -85,40 +171,44 @@ __device__ __forceinline__ T of_kv(const T (&two)[2], int kv) {
     return kv ? two[1] : two[0];
 }
 
-// One warp per (block, kv head, K or V): the new rows of the block in
-// registers (D / 16 loads of 16 bytes a lane, all in flight together), their
+// One warp per (block, kv head, K or V), up to kAppendHeads kv heads a CTA
+// (their rows of a token are neighbours in memory): the new rows of the block
+// in registers (D / 16 loads of 16 bytes a lane, all in flight together), their
 // largest magnitude, the scale, then the codes.  Only a block whose scale
 // grows has its older rows read and rounded again.
+constexpr int kAppendHeads = 4;
+
 template <int F, int D>
-__global__ void __launch_bounds__(64) kv_append_kernel(const KvAppendParams prm) {
+__global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAppendParams prm) {
     constexpr int kLanes = D / 8;            // lanes of a row: 8 halves each
     constexpr int kRows = 32 / kLanes;       // rows of a pass
     constexpr int kPasses = kBlockSize / kRows;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int kv = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kv = warp & 1, kvh = blockIdx.y * kAppendHeads + (warp >> 1), b = blockIdx.z;
     const int ctx = __ldg(prm.context_lens + b);
     const int q0 = __ldg(prm.query_start_loc + b), q1 = __ldg(prm.query_start_loc + b + 1);
     const long long end = (long long)ctx + q1 - q0;
     if (ctx < 0 || q0 < 0 || q1 < q0 || q1 > prm.num_tokens || q1 - q0 > prm.max_query_len ||
         end > (long long)prm.max_blocks_per_seq * kBlockSize) {
-        if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return;
     }
     const int blk = ctx / kBlockSize + (int)blockIdx.x;
     const long long p0 = (long long)blk * kBlockSize;  // position of the block's slot 0
-    if (q1 == q0 || p0 >= end) return;
+    if (q1 == q0 || p0 >= end || kvh >= prm.num_kv_heads) return;
     const int lo = p0 < ctx ? (int)(ctx - p0) : 0;  // the block's new slots: [lo, hi)
     const int hi = end - p0 < kBlockSize ? (int)(end - p0) : kBlockSize;
     const int phys = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + blk);
     if (phys < 0 || (long long)phys >= prm.num_blocks) {
-        if (kvh == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
+        if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
         return;
     }
     const size_t bh = (size_t)phys * prm.num_kv_heads + kvh;
     const int sub = lane / kLanes, col = lane % kLanes;
-    const __half* src = of_kv(prm.fresh, kv) + ((size_t)(q0 + (p0 - ctx)) * prm.num_kv_heads + kvh) * D + 8 * col;
+    const __half* src =
+        of_kv(prm.fresh, kv) + ((long long)(q0 + (p0 - ctx)) * prm.num_kv_heads + kvh) * D + 8 * col;
     const size_t step = (size_t)prm.num_kv_heads * D;
 
     uint4 x[kPasses];
@@ -137,19 +227,27 @@ __global__ void __launch_bounds__(64) kv_append_kernel(const KvAppendParams prm)
     } else {
         float* scale = of_kv(prm.scales, kv) + bh;
         const float s0 = lo > 0 ? *scale : 0.f;
-        float amax = 0.f;
+        // the largest magnitude of the finite ones: bits of |x|, two halves at a time
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const __half* h = reinterpret_cast<const __half*>(&x[i]);
+        for (int i = 0; i < kPasses; ++i)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                         __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+        uint32_t amax = max(top & 0xffffu, top >> 16);
+        if (__any_sync(kFull, amax >= 0x7c00u)) {
+            amax = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float a = fabsf(__half2float(h[j]));
-                if (a <= 65504.f) amax = fmaxf(amax, a);  // finite ones only
+            for (int i = 0; i < kPasses; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t v = (w[j >> 1] >> (16 * (j & 1))) & 0x7fffu;
+                    amax = v < 0x7c00u ? max(amax, v) : amax;
+                }
             }
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, off));
-        const float s1 = fmaxf(s0, block_scale<F>(amax));
+        amax = __reduce_max_sync(kFull, amax);
+        const float s1 = fmaxf(s0, block_scale<F>(__half2float(__ushort_as_half(static_cast<unsigned short>(amax)))));
         const Unit u(s1);
         uint8_t* dst = static_cast<uint8_t*>(of_kv(prm.cache, kv)) + bh * kBlockSize * D + 8 * col;
         if (s1 > s0 && lo > 0) {
@@ -157,10 +255,8 @@ __global__ void __launch_bounds__(64) kv_append_kernel(const KvAppendParams prm)
             for (int i = 0; i < kPasses; ++i) {
                 const int r = i * kRows + sub;
                 if (r < lo) {
-                    uint2 w = *reinterpret_cast<const uint2*>(dst + r * D);
-                    w.x = recode<F>(w.x, s0, u);
-                    w.y = recode<F>(w.y, s0, u);
-                    *reinterpret_cast<uint2*>(dst + r * D) = w;
+                    uint2* w = reinterpret_cast<uint2*>(dst + r * D);
+                    *w = recode8<F>(*w, s0, u);
                 }
             }
         }
@@ -168,11 +264,15 @@ __global__ void __launch_bounds__(64) kv_append_kernel(const KvAppendParams prm)
         for (int i = 0; i < kPasses; ++i) {
             const int r = i * kRows + sub;
             if (r >= lo && r < hi) {
-                const __half* h = reinterpret_cast<const __half*>(&x[i]);
-                uint32_t w[2] = {0u, 0u};
+                const __half2* h = reinterpret_cast<const __half2*>(&x[i]);
+                float f[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j >> 2] |= code_of<F>(u.of(__half2float(h[j]))) << (8 * (j & 3));
-                *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(w[0], w[1]);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 two = __half22float2(h[j]);
+                    f[2 * j] = two.x;
+                    f[2 * j + 1] = two.y;
+                }
+                *reinterpret_cast<uint2*>(dst + r * D) = codes8<F>(f, u);
             }
         }
         __syncwarp();  // every lane has read the old scale
@@ -208,19 +308,20 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
     uint4* dst = reinterpret_cast<uint4*>(of_kv(prm.expanded, kv) + ((size_t)to * prm.num_kv_heads + kvh) * kBlockSize * D);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        __half2 h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t two = w[j >> 1] >> (16 * (j & 1));
-            const float a = value_of<F>(two & 0xffu) * s, c = value_of<F>((two >> 8) & 0xffu) * s;
-            // (fminf and fmaxf would turn a NaN code into a number)
-            h[j] = __floats2half2_rn(fabsf(a) > 65504.f ? copysignf(65504.f, a) : a,
-                                     fabsf(c) > 65504.f ? copysignf(65504.f, c) : c);
+        for (int j = 0; j < 2; ++j) {
+            float f[8];
+            values8<F>(j ? make_uint2(x[i].z, x[i].w) : make_uint2(x[i].x, x[i].y), f);
+            __half2 h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // saturated; NaN stays NaN
+                const float a = f[2 * k] * s, c = f[2 * k + 1] * s;
+                h[k] = __hmax2_nan(__hmin2_nan(__floats2half2_rn(a, c), __float2half2_rn(65504.f)),
+                                   __float2half2_rn(-65504.f));
+            }
+            dst[2 * (32 * i + lane) + j] = *reinterpret_cast<const uint4*>(h);
         }
-        const uint4* r = reinterpret_cast<const uint4*>(h);
-        dst[2 * (32 * i + lane)] = r[0];
-        dst[2 * (32 * i + lane) + 1] = r[1];
     }
 }
 
@@ -250,22 +351,50 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 // radix select over the weights' ordered bits: three rounds of a histogram
 // (11, 11 and 10 bits) find the smallest kept key T and how many of the
 // tokens that equal it are kept (the first ones); then a scan over the
-// positions writes the kept ones in order.  A cluster of `CS` blocks shares a
-// (sequence, kv head): each takes a stretch of the positions, the histograms
-// are summed through distributed shared memory, and a block's first output
-// follows from its predecessors' counts.  Integer counts only, so the result
-// does not depend on the order of the atomics.
-constexpr int kBins = 2048;
+// positions gives each kept token its place.  A cluster of blocks shares a
+// (sequence, kv head): each takes a stretch of the positions, whose keys stay
+// in its shared memory (the weights are read once), the histograms are summed
+// through distributed shared memory, and a block's first output follows from
+// its predecessors' counts.  Integer counts only, so the result does not
+// depend on the order of the atomics.  Bound by latency: per round one
+// barrier of the cluster and two of the block.
+constexpr int kHistWords = 2048 + 2048 + 1024;
+
+// Exclusive prefix sums of a pair of counts over the block's threads (in
+// their order), and the block's totals.  One barrier; `part` (2 x 32 words)
+// must not be in use.
+__device__ __forceinline__ uint2 block_scan(uint2 v, unsigned (*part)[32], uint2* total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint2 incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned a = __shfl_up_sync(kFull, incl.x, off), c = __shfl_up_sync(kFull, incl.y, off);
+        if (lane >= off) incl.x += a, incl.y += c;
+    }
+    if (lane == 31) part[0][warp] = incl.x, part[1][warp] = incl.y;
+    __syncthreads();
+    uint2 w = make_uint2(part[0][lane], part[1][lane]);  // 32 warps: every warp scans their totals
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned a = __shfl_up_sync(kFull, w.x, off), c = __shfl_up_sync(kFull, w.y, off);
+        if (lane >= off) w.x += a, w.y += c;
+    }
+    *total = make_uint2(__shfl_sync(kFull, w.x, 31), __shfl_sync(kFull, w.y, 31));
+    const unsigned bx = __shfl_sync(kFull, w.x, (warp + 31) & 31), by = __shfl_sync(kFull, w.y, (warp + 31) & 31);
+    return make_uint2((warp ? bx : 0u) + incl.x - v.x, (warp ? by : 0u) + incl.y - v.y);
+}
 
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const KvEvictParams prm) {
-    __shared__ unsigned hist[kBins];
-    __shared__ unsigned warp_a[32], warp_b[32];
-    __shared__ unsigned found[2];    // bin, tokens above it
-    __shared__ unsigned counts[2];   // this block's kept for sure, and ties
+    extern __shared__ uint32_t keys[];  // prm.key_words of them
+    __shared__ unsigned hist[kHistWords];
+    __shared__ unsigned part[4][2][32];  // one per block scan
+    __shared__ unsigned found[3][2];     // per round: bin, tokens above it
+    __shared__ unsigned counts[2];       // this block's kept for sure, and ties
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int kvh = blockIdx.x / CS, b = blockIdx.y;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < kHistWords; i += kEvictThreads) hist[i] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const KeepPlan plan(prm, b);
@@ -279,144 +408,105 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     const float* w = prm.weights + row * prm.weights_stride;
     int32_t* kept = prm.kept + row * prm.max_keep_len;
     float* dst_w = prm.dst_weights ? prm.dst_weights + row * prm.dst_weights_stride : nullptr;
-
-    // this block's stretch of the tokens between sinks and recent ones
-    const int m0 = plan.sinks, m1 = L - plan.recent, mid = m1 - m0;
-    const int each = (mid + CS - 1) / CS;
-    const int t0 = min(m1, m0 + rank * each), t1 = min(m1, t0 + each);
-    unsigned need = (unsigned)(k - plan.recent - plan.sinks);  // of the mid tokens
-
-    // sinks and recent ones keep their order around the rest
-    for (int i = rank * kEvictThreads + tid; i < plan.sinks; i += CS * kEvictThreads) {
-        kept[i] = i;
-        if (dst_w) dst_w[i] = w[i];
-    }
-    for (int i = rank * kEvictThreads + tid; i < plan.recent; i += CS * kEvictThreads) {
-        const int at = k - plan.recent + i, t = L - plan.recent + i;
+    auto put = [&](int at, int t) {
         kept[at] = t;
         if (dst_w) dst_w[at] = w[t];
-    }
-    if (need == 0) return;  // the same for the whole cluster
+    };
 
-    uint32_t T = 0;       // the keys that are kept for sure are above T
-    unsigned ties = need; // of those equal to T, so many
-    if (need < (unsigned)mid) {
-        uint32_t prefix = 0, mask = 0;
-#pragma unroll 1
-        for (int round = 0; round < 3; ++round) {
-            const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
-            const int bins = round == 2 ? 1024 : 2048;
-            for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
-            __syncthreads();
-            for (int t = t0 + tid; t < t1; t += kEvictThreads) {
-                const uint32_t key = order_key(w[t]);
-                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
-            }
-            cluster.sync();
-            // bins in descending order: thread i sums bins 2 i, 2 i + 1 from the top
-            unsigned v[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int bin = kBins - 1 - (2 * tid + j);
-                v[j] = 0;
-                for (int r = 0; r < CS; ++r) v[j] += cluster.map_shared_rank(hist, r)[bin];
-            }
-            unsigned pair = v[0] + v[1], incl = pair;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const unsigned up = __shfl_up_sync(kFull, incl, off);
-                if (lane >= off) incl += up;
-            }
-            if (lane == 31) warp_a[warp] = incl;
-            __syncthreads();
-            if (warp == 0) {
-                unsigned x = warp_a[lane];
-                const unsigned own = x;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const unsigned up = __shfl_up_sync(kFull, x, off);
-                    if (lane >= off) x += up;
-                }
-                warp_b[lane] = x - own;
-            }
-            __syncthreads();
-            const unsigned above = warp_b[warp] + incl - pair;  // in the bins before this thread's
-            if (above < need && need <= above + pair) {
-                const bool first = need <= above + v[0];
-                found[0] = (unsigned)(kBins - 1 - (2 * tid + (first ? 0 : 1)));
-                found[1] = above + (first ? 0u : v[0]);
-            }
-            cluster.sync();  // also: every block has read the histograms before they are cleared
-            prefix |= found[0] << shift;
-            mask |= (uint32_t)(bins - 1) << shift;
-            need -= found[1];
-            __syncthreads();
-        }
-        T = prefix;
-        ties = need;
+    // sinks and recent ones keep their order around the rest
+    for (int i = rank * kEvictThreads + tid; i < plan.sinks; i += CS * kEvictThreads) put(i, i);
+    for (int i = rank * kEvictThreads + tid; i < plan.recent; i += CS * kEvictThreads)
+        put(k - plan.recent + i, L - plan.recent + i);
+
+    // this block's stretch of the tokens between them
+    const int m0 = plan.sinks, m1 = L - plan.recent, mid = m1 - m0;
+    const int each = (mid + CS - 1) / CS;
+    const int t0 = min(m1, m0 + rank * each), n = min(m1 - t0, each);
+    unsigned need = (unsigned)(k - plan.recent - plan.sinks);  // of the mid tokens
+    if (need == 0) return;                                      // the same for the whole cluster
+    if (need == (unsigned)mid) {                                // all of them: L <= the budget
+        for (int i = tid; i < n; i += kEvictThreads) put(t0 + i, t0 + i);
+        return;
     }
-    // need == mid: T = 0 is below every key but key 0, which no weight has, so all are kept for sure
-    // counts of the stretch, then its start in the output
+    const bool held = n <= prm.key_words;
+    auto key_of = [&](int i) { return held ? keys[i] : order_key(w[t0 + i]); };
+    // Weights are often mostly equal (zero), which would queue a warp's
+    // atomics on one bin: the lanes that share the first lane's bin add once.
+    auto count = [&](unsigned* h, bool in, unsigned bin) {
+        const unsigned act = __ballot_sync(kFull, in);
+        if (act == 0) return;
+        const int lead = __ffs(act) - 1;
+        const unsigned b0 = __shfl_sync(kFull, bin, lead);
+        const unsigned same = __ballot_sync(kFull, in && bin == b0);
+        if (lane == lead)
+            atomicAdd(h + b0, (unsigned)__popc(same));
+        else if (in && bin != b0)
+            atomicAdd(h + bin, 1u);
+    };
+    __syncthreads();  // the histograms are clear
+    uint32_t T = 0, mask = 0;  // the key so far, and its bits
+#pragma unroll
+    for (int round = 0; round < 3; ++round) {
+        unsigned* h = hist + 2048 * round;
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bins = round == 2 ? 1024 : 2048;
+        for (int i0 = 0; i0 < n; i0 += 4 * kEvictThreads) {
+            uint32_t key[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * kEvictThreads + tid;
+                key[j] = i < n ? (round == 0 ? order_key(w[t0 + i]) : key_of(i)) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * kEvictThreads + tid;
+                if (round == 0 && held && i < n) keys[i] = key[j];
+                count(h, i < n && (key[j] & mask) == T, (key[j] >> shift) & (bins - 1));
+            }
+        }
+        cluster.sync();
+        // bins in descending order: thread i has bins 2 i and 2 i + 1 from the top
+        unsigned v[2] = {0u, 0u};
+        if (2 * tid < bins) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                for (int r = 0; r < CS; ++r) v[j] += cluster.map_shared_rank(h, r)[bins - 1 - 2 * tid - j];
+        }
+        uint2 total;
+        const unsigned above = block_scan(make_uint2(v[0] + v[1], 0u), part[round], &total).x;
+        if (above < need && need <= above + v[0] + v[1]) {
+            const bool first = need <= above + v[0];
+            found[round][0] = (unsigned)(bins - 1 - 2 * tid - (first ? 0 : 1));
+            found[round][1] = above + (first ? 0u : v[0]);
+        }
+        __syncthreads();
+        T |= found[round][0] << shift;
+        mask |= (uint32_t)(bins - 1) << shift;
+        need -= found[round][1];
+    }
+    // Kept: the keys above T, and of those equal to it the first `need`.
+    // Each thread counts a run of the stretch (an odd number of words, so that
+    // the threads of a warp read different banks).
+    const int run = ((n + kEvictThreads - 1) / kEvictThreads) | 1;
+    const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
     unsigned sure = 0, tie = 0;
-    for (int t = t0 + tid; t < t1; t += kEvictThreads) {
-        const uint32_t key = order_key(w[t]);
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t key = key_of(i);
         sure += key > T;
         tie += key == T;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        sure += __shfl_xor_sync(kFull, sure, off);
-        tie += __shfl_xor_sync(kFull, tie, off);
-    }
-    if (lane == 0) {
-        warp_a[warp] = sure;
-        warp_b[warp] = tie;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        unsigned a = 0, c = 0;
-        for (int i = 0; i < kEvictThreads / 32; ++i) {
-            a += warp_a[i];
-            c += warp_b[i];
-        }
-        counts[0] = a;
-        counts[1] = c;
-    }
+    uint2 total;
+    uint2 before = block_scan(make_uint2(sure, tie), part[3], &total);
+    if (tid == 0) counts[0] = total.x, counts[1] = total.y;
     cluster.sync();
-    unsigned sure_before = 0, tie_before = 0;
     for (int r = 0; r < rank; ++r) {
-        sure_before += cluster.map_shared_rank(counts, r)[0];
-        tie_before += cluster.map_shared_rank(counts, r)[1];
+        before.x += cluster.map_shared_rank(counts, r)[0];
+        before.y += cluster.map_shared_rank(counts, r)[1];
     }
-    for (int base = t0; base < t1; base += kEvictThreads) {
-        const int t = base + tid;
-        const float wt = t < t1 ? w[t] : 0.f;
-        const uint32_t key = order_key(wt);
-        const bool s = t < t1 && key > T, e = t < t1 && key == T;
-        const unsigned bs = __ballot_sync(kFull, s), be = __ballot_sync(kFull, e);
-        if (lane == 0) {
-            warp_a[warp] = __popc(bs);
-            warp_b[warp] = __popc(be);
-        }
-        __syncthreads();
-        unsigned a = 0, c = 0, ta = 0, tc = 0;
-        for (int i = 0; i < kEvictThreads / 32; ++i) {
-            const unsigned x = warp_a[i], y = warp_b[i];
-            a += i < warp ? x : 0u;
-            c += i < warp ? y : 0u;
-            ta += x;
-            tc += y;
-        }
-        const unsigned below = (1u << lane) - 1u;
-        const unsigned my_sure = sure_before + a + __popc(bs & below), my_tie = tie_before + c + __popc(be & below);
-        if (s || (e && my_tie < ties)) {
-            const unsigned at = plan.sinks + my_sure + min(my_tie, ties);
-            kept[at] = t;
-            if (dst_w) dst_w[at] = wt;
-        }
-        sure_before += ta;
-        tie_before += tc;
-        __syncthreads();
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t key = key_of(i);
+        if (key > T || (key == T && before.y < need)) put(plan.sinks + before.x + min(before.y, need), t0 + i);
+        before.x += key > T;
+        before.y += key == T;
     }
     cluster.sync();  // no block leaves while another may still read its counts
 }
@@ -476,10 +566,9 @@ __global__ void __launch_bounds__(64) kv_evict_move_kernel(const KvEvictParams p
         for (int i = 0; i < kPasses; ++i) {
             const float s = __shfl_sync(kFull, s0, i * kRows + sub);
             if (s != s1) {
-                x[i].x = recode<F>(x[i].x, s, u);
-                x[i].y = recode<F>(x[i].y, s, u);
-                x[i].z = recode<F>(x[i].z, s, u);
-                x[i].w = recode<F>(x[i].w, s, u);
+                const uint2 a = recode8<F>(make_uint2(x[i].x, x[i].y), s, u);
+                const uint2 c = recode8<F>(make_uint2(x[i].z, x[i].w), s, u);
+                x[i] = make_uint4(a.x, a.y, c.x, c.y);
             }
         }
     }
@@ -492,10 +581,12 @@ __global__ void __launch_bounds__(64) kv_evict_move_kernel(const KvEvictParams p
 }
 
 template <typename P>
-cudaError_t launch(void (*kern)(P), const P& prm, dim3 grid, int threads, int cluster, cudaStream_t stream) {
+cudaError_t launch(void (*kern)(P), const P& prm, dim3 grid, int threads, int cluster, cudaStream_t stream,
+                   size_t smem = 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
     cfg.attrs = attr;
@@ -511,33 +602,42 @@ cudaError_t launch(void (*kern)(P), const P& prm, dim3 grid, int threads, int cl
 
 }  // namespace
 
-#define PA_FOR_D(F_, K_)                                                                                    \
-    if (format == F_ && head_dim == 64) return launch(K_<F_, 64>, prm, grid, 64, 0, stream);                \
-    if (format == F_ && head_dim == 128) return launch(K_<F_, 128>, prm, grid, 64, 0, stream);              \
-    if (format == F_ && head_dim == 256) return launch(K_<F_, 256>, prm, grid, 64, 0, stream);
+#define PA_FOR_D(F_, K_, THREADS_)                                                                          \
+    if (format == F_ && head_dim == 64) return launch(K_<F_, 64>, prm, grid, THREADS_, 0, stream);          \
+    if (format == F_ && head_dim == 128) return launch(K_<F_, 128>, prm, grid, THREADS_, 0, stream);        \
+    if (format == F_ && head_dim == 256) return launch(K_<F_, 256>, prm, grid, THREADS_, 0, stream);
 
-cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, dim3 grid, cudaStream_t stream) {
-    PA_FOR_D(PA_KV_F16, kv_append_kernel)
-    PA_FOR_D(PA_KV_E4M3, kv_append_kernel)
-    PA_FOR_D(PA_KV_INT8, kv_append_kernel)
+cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, int tiles, int num_seqs,
+                             cudaStream_t stream) {
+    const dim3 grid(tiles, (prm.num_kv_heads + kAppendHeads - 1) / kAppendHeads, num_seqs);
+    const int threads = 64 * (prm.num_kv_heads < kAppendHeads ? prm.num_kv_heads : kAppendHeads);
+    PA_FOR_D(PA_KV_F16, kv_append_kernel, threads)
+    PA_FOR_D(PA_KV_E4M3, kv_append_kernel, threads)
+    PA_FOR_D(PA_KV_INT8, kv_append_kernel, threads)
     return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_kv_expand(int format, int head_dim, const KvExpandParams& prm, dim3 grid, cudaStream_t stream) {
-    PA_FOR_D(PA_KV_E4M3, kv_expand_kernel)
-    PA_FOR_D(PA_KV_INT8, kv_expand_kernel)
+    PA_FOR_D(PA_KV_E4M3, kv_expand_kernel, 64)
+    PA_FOR_D(PA_KV_INT8, kv_expand_kernel, 64)
     return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream) {
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kEvictKeyWords * 4);
+    });
+    if (e != cudaSuccess) return e;
     return launch(kv_evict_select_kernel, prm, dim3(prm.num_kv_heads * cluster, num_seqs), kEvictThreads, cluster,
-                  stream);
+                  stream, prm.key_words * 4);
 }
 
 cudaError_t launch_kv_evict_move(int format, int head_dim, const KvEvictParams& prm, dim3 grid, cudaStream_t stream) {
-    PA_FOR_D(PA_KV_F16, kv_evict_move_kernel)
-    PA_FOR_D(PA_KV_E4M3, kv_evict_move_kernel)
-    PA_FOR_D(PA_KV_INT8, kv_evict_move_kernel)
+    PA_FOR_D(PA_KV_F16, kv_evict_move_kernel, 64)
+    PA_FOR_D(PA_KV_E4M3, kv_evict_move_kernel, 64)
+    PA_FOR_D(PA_KV_INT8, kv_evict_move_kernel, 64)
     return cudaErrorInvalidValue;
 }
 
