@@ -78,11 +78,11 @@ struct KvAppendParams {
     const int32_t* context_lens;
     const int32_t* query_start_loc;
     long long num_blocks;
-    int num_kv_heads, max_blocks_per_seq, num_tokens, max_query_len;
+    int num_kv_heads, max_blocks_per_seq, num_tokens, max_query_len, num_seqs;
+    int packed;  // the grid's tile slots are packed over the sequences (else one grid layer a sequence)
     unsigned int* status;
 };
-cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, int tiles, int num_seqs,
-                             cudaStream_t stream);
+cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, int tiles, cudaStream_t stream);
 
 struct KvExpandParams {
     const uint8_t* cache[2];

@@ -391,9 +391,13 @@ int pa_kv_append(const pa_kv_append_args* a, pa_stream_t stream) {
     p.max_query_len = std::min(a->max_query_len, a->num_tokens);
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
-    // a run of n tokens touches at most ceil((n - 1) / 16) + 1 blocks
-    const int tiles = blocks_of(p.max_query_len - 1) + 1;
-    return pa::launch_kv_append(c.format, c.head_dim, p, tiles, a->num_seqs,
+    // a run of n tokens touches at most ceil((n - 1) / 16) + 1 blocks; packed,
+    // the slots of all sequences end below num_tokens / 16 + 2 num_seqs
+    p.num_seqs = a->num_seqs;
+    const long long each = blocks_of(p.max_query_len - 1) + 1;
+    const long long packed = a->num_tokens / pa::kBlockSize + 2ll * a->num_seqs;
+    p.packed = packed < each * a->num_seqs;
+    return pa::launch_kv_append(c.format, c.head_dim, p, static_cast<int>(p.packed ? packed : each),
                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
@@ -465,7 +469,10 @@ int pa_kv_evict(const pa_kv_evict_args* a, pa_stream_t stream_) {
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;
     const int cluster = evict_cluster(a->max_seq_len, (long long)a->num_seqs * p.num_kv_heads, num_sms);
-    p.key_words = std::min(pa::kEvictKeyWords, (a->max_seq_len + cluster - 1) / cluster);
+    // (each warp's run is a multiple of 128 keys)
+    constexpr int kRound = 4 * pa::kEvictThreads;
+    p.key_words = static_cast<int>(std::min<long long>(
+        pa::kEvictKeyWords, ((a->max_seq_len + cluster - 1ll) / cluster + kRound - 1) / kRound * kRound));
     if (pa::launch_kv_evict_select(p, a->num_seqs, cluster, stream) != cudaSuccess) return PA_ERR_CUDA;
     const int blocks = blocks_of(std::min(a->max_keep_len, a->max_seq_len));
     if (blocks > 0 && pa::launch_kv_evict_move(a->src.format, a->src.head_dim, p,

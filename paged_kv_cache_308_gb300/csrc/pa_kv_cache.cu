@@ -39,14 +39,14 @@ __device__ __forceinline__ bool power_of_two(float s) {
     return (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-100f && s <= 0x1p100f;
 }
 
-// A scale to divide by.  E4M3 scales are powers of two unless a caller wrote
-// others: then multiplying by 1 / s is the same as dividing.  For INT8 the
-// product with 1 / s finds the nearest integer wherever it is not next to a
-// tie (see codes8).
+// A scale to divide by: E4M3 scales are powers of two and INT8 scales have 8
+// significant bits unless a caller wrote others.
 struct Unit {
     float s, inv;
     bool pow2;
+    bool short8;  // positive, at most 8 significant bits
     __device__ explicit Unit(float scale) : s(scale), pow2(power_of_two(scale)) {
+        short8 = (__float_as_uint(scale) & 0xffffu) == 0 && scale >= 0x1p-60f && scale <= 0x1p60f;
         inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(scale)) : scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
     }
     __device__ __forceinline__ float of(float x) const {  // x / s; x itself for s = 0
@@ -70,12 +70,16 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 }
 
 // Codes of eight values in the unit u.
-// INT8: with t = x / s rounded twice (1 / s and the product, off by less than
-// 127 * 2^-22 < 2^-14 in all), adding and taking away 1.5 * 2^23 rounds t to
-// the nearest integer q, and the sum's low byte is q's code.  |t - q| below
-// 1/2 - 2^-12 proves that x / s rounds to q too.  Anything else (a tie or
-// next to one, a code out of range, infinities, NaN, s = 0) takes the division.
-template <int F>
+// INT8, for a scale of 8 significant bits and |x| <= 127 s of at most 15 (a
+// half, or a code times such a scale), without a division: t = x / s with one
+// residual step, t + (x - t s) / s, is within 2^-23 t of the quotient and equal
+// to it where that is a number of 24 bits.  The quotient is N / M with N <
+// 2^15, so it is either a tie exactly, and then t is that tie, or at least
+// 1 / (2 M) > 2^-16 t away from one: rounding t rounds the quotient.  Adding
+// 1.5 * 2^23 does that (ties to even), and the sum's low byte is the code.
+// Plain: what that needs is known; else a scale of more bits, infinities and
+// NaN take the division.
+template <int F, bool Plain>
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Unit& u) {
     uint32_t w[2];
     if constexpr (F == PA_KV_E4M3) {
@@ -86,25 +90,19 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Unit& u) {
                        e4m3x2(x[4 * j + 2] * u.inv, x[4 * j + 3] * u.inv) << 16;
             return make_uint2(w[0], w[1]);
         }
-    } else {
-        constexpr float kMagic = 12582912.f;
+    } else if constexpr (Plain) {
         uint32_t r[8];
-        float off = 0.f, top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float t = x[j] * u.inv;
-            const float v = t + kMagic;
-            r[j] = __float_as_uint(v);
-            off = fmaxf(off, fabsf(t - (v - kMagic)));
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(t)));  // NaN stays visible
+            float t = x[j] * u.inv;
+            t = fmaf(fmaf(-t, u.s, x[j]), u.inv, t);
+            r[j] = __float_as_uint(t + 12582912.f);
         }
-        if (off < 0.5f - 0x1p-12f && top < 127.4f && u.s > 0.f) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                w[j] = __byte_perm(__byte_perm(r[4 * j], r[4 * j + 1], 0x0040),
-                                   __byte_perm(r[4 * j + 2], r[4 * j + 3], 0x0040), 0x5410);
-            return make_uint2(w[0], w[1]);
-        }
+        for (int j = 0; j < 2; ++j)
+            w[j] = __byte_perm(__byte_perm(r[4 * j], r[4 * j + 1], 0x0040),
+                               __byte_perm(r[4 * j + 2], r[4 * j + 3], 0x0040), 0x5410);
+        return make_uint2(w[0], w[1]);
     }
     w[0] = w[1] = 0u;
 #pragma unroll
@@ -162,7 +160,22 @@ __device__ __forceinline__ uint2 recode8(uint2 w, float s0, const Unit& u) {
     values8<F>(w, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= s0;
-    return codes8<F>(x, u);
+    // (a code of -128, which only a caller writes, may not fit)
+    const bool low = F == PA_KV_INT8 && (__vcmpeq4(w.x, 0x80808080u) | __vcmpeq4(w.y, 0x80808080u));
+    const bool plain = u.short8 && (__float_as_uint(s0) & 0xffffu) == 0 && s0 >= 0.f && s0 <= u.s && !low;
+    return plain ? codes8<F, true>(x, u) : codes8<F, false>(x, u);
+}
+
+// 16 read-only bytes, loaded before any store that follows in the source (left
+// to itself the compiler takes one load and one store at a time where that
+// saves registers, and a warp then has one load in flight).
+__device__ __forceinline__ uint4 load_ahead(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
 }
 
 // K's or V's of a pair of arguments, without indexing the parameter memory.
@@ -186,26 +199,53 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kv = warp & 1, kvh = blockIdx.y * kAppendHeads + (warp >> 1), b = blockIdx.z;
-    const int ctx = __ldg(prm.context_lens + b);
-    const int q0 = __ldg(prm.query_start_loc + b), q1 = __ldg(prm.query_start_loc + b + 1);
+    const int kv = warp & 1, kvh = blockIdx.y * kAppendHeads + (warp >> 1);
+    int b, tile, ctx, q0, q1;
+    if (prm.packed) {
+        // Tile slots of sequence b from floor(q0 / 16) + 2 b on: n tokens touch at
+        // most floor(n / 16) + 2 blocks, and floor(q1 / 16) - floor(q0 / 16) >=
+        // floor(n / 16).  The last b whose slots begin at or before this one, by
+        // 32 probes at a time; the last round's probes hold its lengths too.
+        int lo = 0, hi = prm.num_seqs, step, at, loc;  // the answer is in [lo, hi)
+        unsigned m;
+        do {
+            step = (hi - lo + 31) / 32;
+            at = min(lo + lane * step, prm.num_seqs);
+            loc = __ldg(prm.query_start_loc + at);
+            ctx = step == 1 ? __ldg(prm.context_lens + min(at, prm.num_seqs - 1)) : 0;
+            const bool before = at < hi && max(loc, 0) / kBlockSize + 2ll * at <= (long long)blockIdx.x;
+            m = __ballot_sync(kFull, before) | 1u;  // (a bad table may begin anywhere)
+            lo += (31 - __clz(m)) * step;
+            hi = min(hi, lo + step);
+        } while (step > 1);
+        const int probe = 31 - __clz(m);
+        b = lo;
+        ctx = __shfl_sync(kFull, ctx, probe);
+        q0 = __shfl_sync(kFull, loc, probe);
+        q1 = __shfl_sync(kFull, loc, (probe + 1) & 31);
+        if (probe == 31) q1 = __ldg(prm.query_start_loc + b + 1);
+        const long long t = (long long)blockIdx.x - max(q0, 0) / kBlockSize - 2ll * b;
+        if (t < 0) return;
+        tile = (int)t;
+    } else {
+        b = blockIdx.z;
+        tile = blockIdx.x;
+        ctx = __ldg(prm.context_lens + b);
+        q0 = __ldg(prm.query_start_loc + b);
+        q1 = __ldg(prm.query_start_loc + b + 1);
+    }
     const long long end = (long long)ctx + q1 - q0;
     if (ctx < 0 || q0 < 0 || q1 < q0 || q1 > prm.num_tokens || q1 - q0 > prm.max_query_len ||
         end > (long long)prm.max_blocks_per_seq * kBlockSize) {
-        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
+        if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return;
     }
-    const int blk = ctx / kBlockSize + (int)blockIdx.x;
+    const int blk = ctx / kBlockSize + tile;
     const long long p0 = (long long)blk * kBlockSize;  // position of the block's slot 0
     if (q1 == q0 || p0 >= end || kvh >= prm.num_kv_heads) return;
     const int lo = p0 < ctx ? (int)(ctx - p0) : 0;  // the block's new slots: [lo, hi)
     const int hi = end - p0 < kBlockSize ? (int)(end - p0) : kBlockSize;
     const int phys = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + blk);
-    if (phys < 0 || (long long)phys >= prm.num_blocks) {
-        if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
-        return;
-    }
-    const size_t bh = (size_t)phys * prm.num_kv_heads + kvh;
     const int sub = lane / kLanes, col = lane % kLanes;
     const __half* src =
         of_kv(prm.fresh, kv) + ((long long)(q0 + (p0 - ctx)) * prm.num_kv_heads + kvh) * D + 8 * col;
@@ -215,8 +255,14 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int r = i * kRows + sub;
-        x[i] = (r >= lo && r < hi) ? __ldg(reinterpret_cast<const uint4*>(src + r * step)) : make_uint4(0u, 0u, 0u, 0u);
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= lo && r < hi) x[i] = load_ahead(src + r * step);
     }
+    if (phys < 0 || (long long)phys >= prm.num_blocks) {
+        if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
+        return;
+    }
+    const size_t bh = (size_t)phys * prm.num_kv_heads + kvh;
     if constexpr (F == PA_KV_F16) {
         __half* dst = static_cast<__half*>(of_kv(prm.cache, kv)) + bh * kBlockSize * D + 8 * col;
 #pragma unroll
@@ -234,7 +280,8 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
             top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
                                          __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
         uint32_t amax = max(top & 0xffffu, top >> 16);
-        if (__any_sync(kFull, amax >= 0x7c00u)) {
+        const bool special = __any_sync(kFull, amax >= 0x7c00u);
+        if (special) {
             amax = 0;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
@@ -249,6 +296,7 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
         amax = __reduce_max_sync(kFull, amax);
         const float s1 = fmaxf(s0, block_scale<F>(__half2float(__ushort_as_half(static_cast<unsigned short>(amax)))));
         const Unit u(s1);
+        const bool plain = u.short8 && !special;
         uint8_t* dst = static_cast<uint8_t*>(of_kv(prm.cache, kv)) + bh * kBlockSize * D + 8 * col;
         if (s1 > s0 && lo > 0) {
 #pragma unroll
@@ -272,7 +320,7 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
                     f[2 * j] = two.x;
                     f[2 * j + 1] = two.y;
                 }
-                *reinterpret_cast<uint2*>(dst + r * D) = codes8<F>(f, u);
+                *reinterpret_cast<uint2*>(dst + r * D) = plain ? codes8<F, true>(f, u) : codes8<F, false>(f, u);
             }
         }
         __syncwarp();  // every lane has read the old scale
@@ -303,7 +351,7 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
     const uint4* src = reinterpret_cast<const uint4*>(of_kv(prm.cache, kv) + bh * kBlockSize * D) + lane;
     uint4 x[kPasses];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) x[i] = __ldg(src + 32 * i);
+    for (int i = 0; i < kPasses; ++i) x[i] = load_ahead(src + 32 * i);
     const float s = __ldg(of_kv(prm.scales, kv) + bh);
     uint4* dst = reinterpret_cast<uint4*>(of_kv(prm.expanded, kv) + ((size_t)to * prm.num_kv_heads + kvh) * kBlockSize * D);
 #pragma unroll
@@ -347,6 +395,12 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// The weight of a key; NaN and the zeros, which share keys, are read again.
+__device__ __forceinline__ float weight_of(uint32_t key, const float* w) {
+    const uint32_t bits = (key & 0x80000000u) ? key & 0x7fffffffu : ~key;
+    return bits == 0u || bits == 0xff800000u ? *w : __uint_as_float(bits);
+}
+
 // The k - r - s heaviest tokens between the first s and the last r, by a
 // radix select over the weights' ordered bits: three rounds of a histogram
 // (11, 11 and 10 bits) find the smallest kept key T and how many of the
@@ -385,8 +439,8 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, unsigned (*part)[32], uint2
 }
 
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const KvEvictParams prm) {
-    extern __shared__ uint32_t keys[];  // prm.key_words of them
-    __shared__ unsigned hist[kHistWords];
+    extern __shared__ __align__(16) uint32_t keys[];  // prm.key_words of them
+    __shared__ __align__(8) unsigned hist[kHistWords];
     __shared__ unsigned part[4][2][32];  // one per block scan
     __shared__ unsigned found[3][2];     // per round: bin, tokens above it
     __shared__ unsigned counts[2];       // this block's kept for sure, and ties
@@ -428,48 +482,62 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         for (int i = tid; i < n; i += kEvictThreads) put(t0 + i, t0 + i);
         return;
     }
-    const bool held = n <= prm.key_words;
-    auto key_of = [&](int i) { return held ? keys[i] : order_key(w[t0 + i]); };
-    // Weights are often mostly equal (zero), which would queue a warp's
-    // atomics on one bin: the lanes that share the first lane's bin add once.
-    auto count = [&](unsigned* h, bool in, unsigned bin) {
-        const unsigned act = __ballot_sync(kFull, in);
-        if (act == 0) return;
-        const int lead = __ffs(act) - 1;
-        const unsigned b0 = __shfl_sync(kFull, bin, lead);
-        const unsigned same = __ballot_sync(kFull, in && bin == b0);
-        if (lane == lead)
-            atomicAdd(h + b0, (unsigned)__popc(same));
-        else if (in && bin != b0)
-            atomicAdd(h + bin, 1u);
+    // Each warp takes a run of the stretch, a lane four neighbours at a time;
+    // keys past the stretch are 0, below every weight's.
+    const int warp = tid >> 5;
+    const int run = (n + 4 * kEvictThreads - 1) / (4 * kEvictThreads) * 128;
+    const int i0 = warp * run + 4 * lane, i1 = min(n, (warp + 1) * run);
+    const bool held = 32 * run <= prm.key_words;
+    auto fresh_keys = [&](int i) {
+        const float* p = w + t0 + i;
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = i + j < n ? p[j] : 0.f;
+        return make_uint4(i < n ? order_key(v[0]) : 0u, i + 1 < n ? order_key(v[1]) : 0u,
+                          i + 2 < n ? order_key(v[2]) : 0u, i + 3 < n ? order_key(v[3]) : 0u);
     };
+    auto keys_of = [&](int i) { return held ? *reinterpret_cast<const uint4*>(keys + i) : fresh_keys(i); };
     __syncthreads();  // the histograms are clear
     uint32_t T = 0, mask = 0;  // the key so far, and its bits
 #pragma unroll
     for (int round = 0; round < 3; ++round) {
         unsigned* h = hist + 2048 * round;
         const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bins = round == 2 ? 1024 : 2048;
-        for (int i0 = 0; i0 < n; i0 += 4 * kEvictThreads) {
-            uint32_t key[4];
+        if (round == 0) {
+            // Weights that underflowed to zero can be most of them: counted apart,
+            // lest every atomic of a warp queue on their bin.
+            unsigned zeros = 0;
+#pragma unroll 2
+            for (int i = i0; i < (warp + 1) * run; i += 128) {  // to the run's end: keys past n become 0
+                const uint4 q = fresh_keys(i);
+                if (held) *reinterpret_cast<uint4*>(keys + i) = q;
+                const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + j * kEvictThreads + tid;
-                key[j] = i < n ? (round == 0 ? order_key(w[t0 + i]) : key_of(i)) : 0u;
+                for (int j = 0; j < 4; ++j) {
+                    zeros += k4[j] == 0x80000000u;
+                    if (k4[j] != 0u && k4[j] != 0x80000000u) atomicAdd(h + (k4[j] >> 21), 1u);
+                }
             }
+            zeros = __reduce_add_sync(kFull, zeros);
+            if (lane == 0 && zeros) atomicAdd(h + (0x80000000u >> 21), zeros);
+        } else {
+            for (int i = i0; i < i1; i += 128) {
+                const uint4 q = keys_of(i);
+                const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + j * kEvictThreads + tid;
-                if (round == 0 && held && i < n) keys[i] = key[j];
-                count(h, i < n && (key[j] & mask) == T, (key[j] >> shift) & (bins - 1));
+                for (int j = 0; j < 4; ++j)
+                    if ((k4[j] & mask) == T) atomicAdd(h + ((k4[j] >> shift) & (bins - 1)), 1u);
             }
         }
         cluster.sync();
         // bins in descending order: thread i has bins 2 i and 2 i + 1 from the top
         unsigned v[2] = {0u, 0u};
         if (2 * tid < bins) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                for (int r = 0; r < CS; ++r) v[j] += cluster.map_shared_rank(h, r)[bins - 1 - 2 * tid - j];
+            for (int r = 0; r < CS; ++r) {
+                const uint2 two = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(h, r) + bins - 2 - 2 * tid);
+                v[0] += two.y;
+                v[1] += two.x;
+            }
         }
         uint2 total;
         const unsigned above = block_scan(make_uint2(v[0] + v[1], 0u), part[round], &total).x;
@@ -483,30 +551,57 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         mask |= (uint32_t)(bins - 1) << shift;
         need -= found[round][1];
     }
-    // Kept: the keys above T, and of those equal to it the first `need`.
-    // Each thread counts a run of the stretch (an odd number of words, so that
-    // the threads of a warp read different banks).
-    const int run = ((n + kEvictThreads - 1) / kEvictThreads) | 1;
-    const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
+    // Kept: the keys above T, and of those equal to it the first `need`.  Counts
+    // of both in one word while they are a warp's 128 keys.
+    auto marks = [&](const uint4& q, unsigned (&k)[4]) {
+        const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = (k4[j] > T ? 1u : 0u) + (k4[j] == T ? 0x10000u : 0u);
+        return k[0] + k[1] + k[2] + k[3];
+    };
     unsigned sure = 0, tie = 0;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t key = key_of(i);
-        sure += key > T;
-        tie += key == T;
+    for (int i = i0; i < i1; i += 128) {
+        unsigned k[4];
+        const unsigned c = marks(keys_of(i), k);
+        sure += c & 0xffffu;
+        tie += c >> 16;
     }
     uint2 total;
     uint2 before = block_scan(make_uint2(sure, tie), part[3], &total);
+    before = make_uint2(__shfl_sync(kFull, before.x, 0), __shfl_sync(kFull, before.y, 0));  // the warp's first
     if (tid == 0) counts[0] = total.x, counts[1] = total.y;
     cluster.sync();
     for (int r = 0; r < rank; ++r) {
         before.x += cluster.map_shared_rank(counts, r)[0];
         before.y += cluster.map_shared_rank(counts, r)[1];
     }
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t key = key_of(i);
-        if (key > T || (key == T && before.y < need)) put(plan.sinks + before.x + min(before.y, need), t0 + i);
-        before.x += key > T;
-        before.y += key == T;
+    for (int i = i0; i - 4 * lane < i1; i += 128) {  // (the whole warp, for the shuffles)
+        const uint4 q = i < i1 ? keys_of(i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+        unsigned k[4];
+        const unsigned mine = marks(q, k);
+        unsigned incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const unsigned up = __shfl_up_sync(kFull, incl, off);
+            if (lane >= off) incl += up;
+        }
+        const unsigned all = __shfl_sync(kFull, incl, 31);
+        unsigned a = before.x + ((incl - mine) & 0xffffu), c = before.y + ((incl - mine) >> 16);
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (k[j] == 1u || (k[j] && c < need)) {
+                    const int at = plan.sinks + (int)(a + min(c, need));
+                    kept[at] = t0 + i + j;
+                    if (dst_w) dst_w[at] = weight_of(k4[j], w + t0 + i + j);
+                }
+                a += k[j] & 0xffffu;
+                c += k[j] >> 16;
+            }
+        }
+        before.x += all & 0xffffu;
+        before.y += all >> 16;
     }
     cluster.sync();  // no block leaves while another may still read its counts
 }
@@ -553,7 +648,8 @@ __global__ void __launch_bounds__(64) kv_evict_move_kernel(const KvEvictParams p
         const int r = i * kRows + sub;
         const int f = __shfl_sync(kFull, from, r), s = __shfl_sync(kFull, slot, r);
         const size_t at = (((size_t)max(f, 0) * prm.num_kv_heads + kvh) * kBlockSize + s) * D * kElem + 16 * col;
-        x[i] = f >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + at)) : make_uint4(0u, 0u, 0u, 0u);
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (f >= 0) x[i] = load_ahead(src + at);
     }
     if constexpr (F != PA_KV_F16) {
         float s0 = from >= 0 ? __ldg(of_kv(prm.src_scales, kv) + (size_t)from * prm.num_kv_heads + kvh) : 0.f;
@@ -607,9 +703,8 @@ cudaError_t launch(void (*kern)(P), const P& prm, dim3 grid, int threads, int cl
     if (format == F_ && head_dim == 128) return launch(K_<F_, 128>, prm, grid, THREADS_, 0, stream);        \
     if (format == F_ && head_dim == 256) return launch(K_<F_, 256>, prm, grid, THREADS_, 0, stream);
 
-cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, int tiles, int num_seqs,
-                             cudaStream_t stream) {
-    const dim3 grid(tiles, (prm.num_kv_heads + kAppendHeads - 1) / kAppendHeads, num_seqs);
+cudaError_t launch_kv_append(int format, int head_dim, const KvAppendParams& prm, int tiles, cudaStream_t stream) {
+    const dim3 grid(tiles, (prm.num_kv_heads + kAppendHeads - 1) / kAppendHeads, prm.packed ? 1 : prm.num_seqs);
     const int threads = 64 * (prm.num_kv_heads < kAppendHeads ? prm.num_kv_heads : kAppendHeads);
     PA_FOR_D(PA_KV_F16, kv_append_kernel, threads)
     PA_FOR_D(PA_KV_E4M3, kv_append_kernel, threads)

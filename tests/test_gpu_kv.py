@@ -368,3 +368,28 @@ def test_evict_long(n, keep):
     w = torch.rand(2, 2, n, generator=g, device=DEV) ** 8
     w = torch.where(w < 0.01, torch.zeros_like(w), w)
     check_evict(c, w, [keep, 20], 4, 64 if keep > 64 else 1, evict(c, w, [keep, 20], 4, 64 if keep > 64 else 1))
+
+
+def test_evict_more_tokens_than_the_blocks_can_hold():
+    # beyond the shared memory of a whole cluster the weights are read again in every round
+    n = 400003
+    c = K.Case([n], 1, 1, 64, "f16", seed=29, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(30)
+    w = torch.rand(1, 1, n, generator=g, device=DEV) ** 3
+    w = torch.where(w < 0.2, torch.zeros_like(w), w)
+    check_evict(c, w, [150001], 4, 100, evict(c, w, [150001], 4, 100))
+
+
+@pytest.mark.parametrize("fmt", ["f16", "int8"])
+@pytest.mark.parametrize("B", [31, 32, 33, 70, 1100])
+def test_append_finds_its_sequence_in_large_batches(fmt, B):
+    g = torch.Generator().manual_seed(B)
+    ctx = torch.randint(0, 40, (B,), generator=g).tolist()
+    new = torch.randint(0, 20, (B,), generator=g).tolist()
+    new[0], new[-1], new[B // 2] = 0, 50, 90
+    c = K.Case(ctx, 5, 5, 64, fmt, seed=31, device=DEV, room=[a + b for a, b in zip(ctx, new)])
+    _, k_new, v_new, loc = _chunks(c, new, 32)
+    ref = K.append_reference(c, new, k_new, v_new)
+    append(c, new, k_new, v_new, loc)
+    assert status() == 0
+    same_cache(c, ref)
