@@ -33,7 +33,7 @@ struct KvDecodeParams {
     // Partials, `slots` per kv head (slot: see pa_kv_decode.cu):
     float2* sums;  // [Hkv][slots][group]: reference exponent (log2 domain) and sum relative to it
     float* acc;    // [Hkv][slots][group][D], normalised
-    int* seq_parts;  // flat: [B] of (first slot, number of partials), of sequences with tokens
+    int* seq_parts;  // flat: [B][8], where the partials of the sequences with tokens are
     float* scores;   // [B][H][score_stride], log2 domain; null without weights
     long long score_stride;
     long long num_blocks, slots;

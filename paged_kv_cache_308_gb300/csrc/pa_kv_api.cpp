@@ -79,7 +79,7 @@ DecodePlan plan_decode(int num_seqs, int max_seq_len, int num_kv_heads, int head
     }
     p.flat = true;
     p.ctas_per_head = static_cast<int>(slots);
-    p.slots = (long long)p.ctas_per_head + num_seqs;
+    p.slots = (1ll + pa::kKvWarps) * p.ctas_per_head + num_seqs;  // CTAs, warps + sequences
     return p;
 }
 
@@ -94,7 +94,7 @@ DecodeSpace decode_space(const DecodePlan& p, int num_seqs, int num_heads, int n
     const size_t rows = (size_t)p.slots * num_heads;  // slots of a kv head x kv heads x group
     const bool split = p.flat || p.parts > 1;
     s.parts = split || weights ? up(rows * 8) : 0;
-    s.acc = s.parts + (p.flat ? up((size_t)num_seqs * 8) : 0);
+    s.acc = s.parts + (p.flat ? up((size_t)num_seqs * 32) : 0);
     s.scores = s.acc + (split ? up(rows * head_dim * 4) : 0);
     s.score_stride = (long long)blocks_of(max_seq_len) * pa::kBlockSize;
     s.bytes = s.scores + (weights ? up((size_t)num_seqs * num_heads * s.score_stride * 4) : 0);
@@ -128,8 +128,8 @@ int check_decode(const pa_kv_decode_args* a, const pa_decode_opts* o) {
     if ((long long)a->max_seq_len > (long long)a->max_blocks_per_seq * pa::kBlockSize) return PA_ERR_INVALID_ARG;
     if (a->weights_out && a->weights_stride < a->max_seq_len) return PA_ERR_INVALID_ARG;
     if (a->weights_in && !a->weights_out) return PA_ERR_INVALID_ARG;
-    // the batch's blocks are numbered in 32 bits
-    if ((long long)a->num_seqs * blocks_of(a->max_seq_len) >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    // the batch's blocks are numbered in 32 bits (with a few more a sequence)
+    if ((long long)a->num_seqs * (blocks_of(a->max_seq_len) + 8ll) >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     if (a->num_seqs == 0) return PA_OK;
     if (bad_ptr(a->out, 16) || bad_ptr(a->q, 16) || bad_ptr(a->block_tables, 4) || bad_ptr(a->seq_lens, 4))
         return PA_ERR_INVALID_ARG;

@@ -8,14 +8,18 @@
 //     s[t, h] = c ks sum_d k8[t, d] q[h, d]             ks, vs: the block's scales
 //     m'      = max(m, max_t s),  p = 2^(s - m' + kShift)
 //     l       = l 2^(m - m') + sum_t p
-//     o[d, h] = o 2^(m - m') + vs sum_t v8[t, d] p16[t, h]
+//     o[d, h] = o 2^(m - m') + sum_t v8[t, d] p16[t, h],  p16 = half(p vs / vr)
 // The scales stay outside the products, so K and V enter the tensor cores as
-// exact halves (a code is at most 448) and a block's scale costs one multiply
-// per score and one FMA per output instead of one per element.
+// exact halves (a code is at most 448).  ks costs one multiply per score.  vs
+// multiplies the probabilities, relative to vr, the largest block scale so
+// far, which o is kept in units of (when it grows, o is rescaled along with
+// the change of m): one multiply per probability instead of one per output.
+// A block whose vs is below 2^-20 vr, where p16 could lose bits, adds vs / vr
+// times its product to o instead.
 // p is rounded to fp16 for the product (relative 2^-11; the shift keeps
-// probabilities down to 2^-28 of the maximum normal and 2^-38 above zero);
-// l adds the unrounded p, in 32 bits as m and o are, so that the weights of
-// the accumulation are exact to 32-bit rounding.
+// products of probability and scale ratio down to 2^-28 normal and 2^-38 above
+// zero); l adds the unrounded p, in 32 bits as m and o are, so that the
+// weights of the accumulation are exact to 32-bit rounding.
 //
 // From 8 bits to MMA fragments: a 32-bit register of ldmatrix holds four
 // consecutive d of one token (K), or two d of two neighbouring tokens (V,
@@ -28,17 +32,20 @@
 // with the sign bit flipped, placed under the exponent of 1024, minus 1152).
 //
 // How the work is dealt out.  Flat form: a grid of the CTAs the SMs hold at
-// once, C per kv head.  The blocks of the batch's sequences form one list of
-// T; CTA c takes blocks [f(c), f(c+1)), f(c) = floor(c T / C'), so every CTA
-// reads the same amount whatever the lengths, and no CTA is launched for a
-// partition that its sequence does not have.  A share that crosses sequences
-// is processed sequence by sequence; each gives one partial (or, if it holds
-// the whole sequence, the output).  Partial slots are c + b, b the sequence:
-// along the list either c or b grows from one segment to the next, so slots
-// never collide and C + B of them suffice.  Every CTA derives its share from
-// seq_lens itself; the host never reads them.  Grid form (a partition size
-// was given, or every sequence fits one CTA): one CTA per (partition, kv
-// head, sequence).
+// once, C per kv head.  The blocks of the batch's sequences form one list, in
+// which each sequence counts kLead units more than it has blocks (what it costs
+// to begin one); CTA c takes the c-th of equal runs of units.  So the CTAs end
+// together whatever the lengths, none is launched for a partition that its
+// sequence does not have, and the host never reads the lengths: every warp
+// finds its run from seq_lens itself.  A run within one sequence is dealt
+// round-robin to the CTA's warps, which merge their states into one partial
+// (slot c).  A run that crosses sequences is cut into one run per warp; the
+// warps then work alone, sequence by sequence, the copies running on from one
+// into the next, and each segment leaves a partial (slot C + warp + b, for the
+// b-th sequence: from one segment to the next either the warp's number or b
+// grows, so slots never collide) or, if it is the whole sequence, the output.
+// Grid form (one sequence, a partition size was given, or every sequence fits
+// one CTA): one CTA per (partition, kv head, sequence).
 //
 // kv_merge_kernel: the log-sum-exp merge of the partials, and in further CTAs
 // of the same launch weights_out = weights_in + sum_h 2^(s - lse) from the
@@ -56,7 +63,66 @@ namespace pa {
 namespace {
 
 constexpr float kShift = 14.f;
-constexpr int kMinBlocks = kKvWarps;  // blocks of a share at least, while there are enough
+constexpr int kLead = 2;  // units a sequence counts beyond its blocks
+
+// The flat form's runs: `ctas` of them over `units` units, q each and one more
+// for the first r, at least kMinUnits long while there are as many units.
+struct FlatRuns {
+    static constexpr int kMinUnits = 2 * kKvWarps;
+    int most, ctas, q, r;
+    __device__ FlatRuns(int units, int most_) : most(most_) {
+        ctas = min(most, units / kMinUnits);
+        if (ctas == 0) ctas = units > 0 ? 1 : 0;
+        q = ctas ? units / ctas : 0;
+        r = units - q * ctas;
+    }
+    __device__ int begin(int c) const { return c * q + min(c, r); }
+    __device__ int of(int u) const { return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q; }
+    // a warp's part of a run that crosses sequences
+    static __device__ int warp_begin(int u0, int u1, int w) {
+        return u0 + (int)((long long)(u1 - u0) * w / kKvWarps);
+    }
+    __device__ int warp_of(int c, int u) const {
+        const int u0 = begin(c), u1 = begin(c + 1);
+        int w = 0;
+        while (w + 1 < kKvWarps && warp_begin(u0, u1, w + 1) <= u) ++w;
+        return w;
+    }
+};
+
+// The partial slots of a sequence with n blocks whose units begin at `first`:
+// three stretches (some empty), in the order of its tokens -- warps of a first
+// CTA that it shares with the sequence before, CTAs of its own, warps of a
+// last one.
+struct SeqParts {
+    int first[3], count[3];
+    __device__ SeqParts(const FlatRuns& runs, int at, int n, int b) {
+        const int ua = at + kLead, uz = ua + n - 1;  // units of its first and last block
+        int ca = runs.of(ua), cz = runs.of(uz);
+        auto whole = [&](int c) { return runs.begin(c) >= at && runs.begin(c + 1) <= uz + 1; };
+        auto slot = [&](int c, int w) { return runs.most + c * kKvWarps + w + b; };
+        first[0] = first[1] = first[2] = count[0] = count[1] = count[2] = 0;
+        if (ca == cz && !whole(ca)) {
+            const int wa = runs.warp_of(ca, ua);
+            first[0] = slot(ca, wa);
+            count[0] = runs.warp_of(ca, uz) - wa + 1;
+            return;
+        }
+        if (!whole(ca)) {
+            const int wa = runs.warp_of(ca, ua);
+            first[0] = slot(ca, wa);
+            count[0] = kKvWarps - wa;
+            ++ca;
+        }
+        if (!whole(cz)) {
+            first[2] = slot(cz, 0);
+            count[2] = runs.warp_of(cz, uz) + 1;
+            --cz;
+        }
+        first[1] = ca;
+        count[1] = cz - ca + 1;
+    }
+};
 
 template <int F, int D, int NS>
 struct KvShape {
@@ -86,38 +152,43 @@ __device__ __forceinline__ uint32_t unit_at(int row, int unit) {
         return static_cast<uint32_t>((unit >> 3) * (kBlockSize * 128)) + swz(row, unit & 7);
 }
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-    return r;
-}
-
-// Two halves from bytes `sel` (a byte-permute selector of two bytes) of w.
+// Halves of the four bytes of w: bytes 0 and 1, bytes 2 and 3.  INT8 bytes come
+// with the sign bit flipped (v + 128).
 template <int F>
-__device__ __forceinline__ uint32_t halves_lo(uint32_t w) {  // bytes 0, 1
+__device__ __forceinline__ void to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (F == PA_KV_E4M3) {
-        return cvt_e4m3x2(w);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     } else {
-        const uint32_t u = __byte_perm(w, 0x64646464u, 0x4140);
         const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-        return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&u), k));
+        const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+        lo = half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&a), k));
+        hi = half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&b), k));
     }
 }
 
 template <int F>
-__device__ __forceinline__ uint32_t halves_hi(uint32_t w) {  // bytes 2, 3
-    if constexpr (F == PA_KV_E4M3) {
-        return cvt_e4m3x2(w >> 16);
-    } else {
-        const uint32_t u = __byte_perm(w, 0x64646464u, 0x4342);
-        const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&u), k));
-    }
-}
-
-template <int F>
-__device__ __forceinline__ uint32_t unsign(uint32_t w) {  // int8: bytes v + 128
+__device__ __forceinline__ uint32_t unsign(uint32_t w) {
     return F == PA_KV_INT8 ? w ^ 0x80808080u : w;
+}
+
+// D = A . B (no accumulator read).
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 2^x by the hardware's approximation (relative error about 2^-22; results
+// below 2^-126 are 0, which no sum here would notice).
+__device__ __forceinline__ float pow2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // (d of o[mt][0..1], d of o[mt][2..3]) of a lane with row group g.
@@ -138,6 +209,179 @@ constexpr int ctas_of() {
     return F == PA_KV_F16 ? (D == 256 ? 1 : D == 128 ? 2 : 3) : (D == 256 ? 2 : D == 128 ? 3 : 5);
 }
 
+// A warp's online softmax over the heads of a kv head: lane (g, c) of an MMA
+// fragment holds heads 2c and 2c + 1.
+template <int D>
+struct WarpState {
+    float o[D / 16][4];
+    float m0, m1;  // running maximum
+    float l0, l1;  // this lane's share of the exp sums
+    float vr, rvr; // V unit of o, and its reciprocal (0: no block yet)
+    __device__ void clear() {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+        vr = rvr = 0.f;
+    }
+};
+
+// One 16-token block.  `kst`, `vst`: its staged K and V, `vgen` V as a generic
+// pointer.  `ks`: softmax scale (log2) times K's block scale.  `score0`: where
+// the scores of head 2c from the block's first token on go (null: nowhere),
+// head 2c + 1's `score_stride` further if `two`.
+template <int F, int D>
+__device__ __forceinline__ void block_update(WarpState<D>& st, const uint32_t (&qb)[D / 16][2], uint32_t kst,
+                                             uint32_t vst, uint8_t* vgen, int nvalid, float ks, float vs,
+                                             float* score0, long long score_stride, bool two) {
+    constexpr int kRow = D * (F == PA_KV_F16 ? 2 : 1);
+    const int lane = threadIdx.x & 31;
+    const int g = lane >> 2;
+    const int mi = lane >> 3, r8 = lane & 7;
+
+    // S^T = K . Q^T, in several accumulators for shorter chains
+    constexpr int kAcc = D == 256 ? 4 : 2;
+    float sa[kAcc][4];
+    const int rq = r8 + ((mi & 1) << 3);
+    if constexpr (F == PA_KV_F16) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4];
+            ldsm_x4(a, kst + unit_at<F, D>(rq, 2 * k + (mi >> 1)));
+            if (k < kAcc)
+                mma_16816_first(sa[k], a, qb[k][0], qb[k][1]);
+            else
+                mma_16816(sa[k % kAcc], a, qb[k][0], qb[k][1]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {  // 16-byte units 2k and 2k + 1
+            uint32_t w[4], a[4], e[4];
+            ldsm_x4(w, kst + unit_at<F, D>(rq, 2 * k + (mi >> 1)));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = unsign<F>(w[x]);
+            to_halves<F>(w[0], a[0], a[2]);
+            to_halves<F>(w[1], a[1], a[3]);
+            to_halves<F>(w[2], e[0], e[2]);
+            to_halves<F>(w[3], e[1], e[3]);
+            if (2 * k < kAcc) {
+                mma_16816_first(sa[2 * k], a, qb[2 * k][0], qb[2 * k][1]);
+                mma_16816_first(sa[2 * k + 1], e, qb[2 * k + 1][0], qb[2 * k + 1][1]);
+            } else {
+                mma_16816(sa[2 * k % kAcc], a, qb[2 * k][0], qb[2 * k][1]);
+                mma_16816(sa[(2 * k + 1) % kAcc], e, qb[2 * k + 1][0], qb[2 * k + 1][1]);
+            }
+        }
+    }
+    float s[4];  // tokens g (0, 1) and g + 8 (2, 3) of heads 2c, 2c + 1
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        float v = sa[0][x] + sa[1][x];
+        if constexpr (kAcc == 4) v += sa[2][x] + sa[3][x];
+        s[x] = v * ks;
+    }
+    if (score0) {
+        if (g < nvalid) {
+            score0[g] = s[0];
+            if (two) score0[score_stride + g] = s[1];
+        }
+        if (g + 8 < nvalid) {
+            score0[g + 8] = s[2];
+            if (two) score0[score_stride + g + 8] = s[3];
+        }
+    }
+    if (g >= nvalid) s[0] = s[1] = -INFINITY;  // tokens past the end are excluded
+    if (g + 8 >= nvalid) s[2] = s[3] = -INFINITY;
+
+    float bm0 = fmaxf(s[0], s[2]), bm1 = fmaxf(s[1], s[3]);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+        bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, off));
+        bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, off));
+    }
+    const float mn0 = fmaxf(st.m0, bm0), mn1 = fmaxf(st.m1, bm1);
+    float al0 = pow2_of(st.m0 - mn0), al1 = pow2_of(st.m1 - mn1);
+    st.m0 = mn0;
+    st.m1 = mn1;
+    const float e0 = mn0 - kShift, e1 = mn1 - kShift;
+    float p0 = pow2_of(s[0] - e0), p1 = pow2_of(s[1] - e1), p2 = pow2_of(s[2] - e0), p3 = pow2_of(s[3] - e1);
+    st.l0 = st.l0 * al0 + (p0 + p2);
+    st.l1 = st.l1 * al1 + (p1 + p3);
+    bool small = false;  // V's scale is far below the unit
+    float ratio = 1.f;
+    if constexpr (F != PA_KV_F16) {
+        if (vs > st.vr && vs >= 0x1p-100f) {  // (448 times less than that is zero in the output)
+            const float down = st.vr * (1.f / vs);  // 0 for the first block
+            al0 *= down;
+            al1 *= down;
+            st.vr = vs;
+            st.rvr = 1.f / vs;
+        }
+        ratio = vs * st.rvr;
+        small = ratio < 0x1p-20f;
+        if (!small) p0 *= ratio, p1 *= ratio, p2 *= ratio, p3 *= ratio;
+    }
+    if (__any_sync(kFull, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            st.o[mt][0] *= al0;
+            st.o[mt][1] *= al1;
+            st.o[mt][2] *= al0;
+            st.o[mt][3] *= al1;
+        }
+    }
+    const uint32_t pb0 = movmatrix_trans(half2_bits(__floats2half2_rn(p0, p1)));  // tokens 0..7
+    const uint32_t pb1 = movmatrix_trans(half2_bits(__floats2half2_rn(p2, p3)));  // tokens 8..15
+
+    if (nvalid < kBlockSize) {
+        // 0 * NaN would poison P.V: clear the V rows past the end
+        constexpr int kUnits = kRow / 16;
+        for (int u = lane; u < (kBlockSize - nvalid) * kUnits; u += 32)
+            *reinterpret_cast<uint4*>(vgen + unit_at<F, D>(nvalid + u / kUnits, u % kUnits)) =
+                make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    }
+
+    // O^T += V^T . P^T
+    if constexpr (F == PA_KV_F16) {
+        const int rv = r8 + ((mi >> 1) << 3);
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            uint32_t a[4];
+            ldsm_x4_trans(a, vst + unit_at<F, D>(rv, 2 * mt + (mi & 1)));
+            mma_16816(st.o[mt], a, pb0, pb1);
+        }
+    } else {
+        auto product = [&](auto add) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t w[4];
+                ldsm_x4_trans(w, vst + unit_at<F, D>(rq, 2 * k + (mi >> 1)));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = unsign<F>(__byte_perm(w[x], 0u, 0x3120));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t a[4];
+                    to_halves<F>(w[2 * y], a[0], a[1]);
+                    to_halves<F>(w[2 * y + 1], a[2], a[3]);
+                    add(st.o[2 * k + y], a);
+                }
+            }
+        };
+        if (!small) {
+            product([&](float(&o)[4], const uint32_t(&a)[4]) { mma_16816(o, a, pb0, pb1); });
+        } else {
+            product([&](float(&o)[4], const uint32_t(&a)[4]) {
+                float x[4];
+                mma_16816_first(x, a, pb0, pb1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = fmaf(ratio, x[i], o[i]);
+            });
+        }
+    }
+}
+
 template <int F, int D, int NS>
 __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     kv_partition_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -150,7 +394,6 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     float* sm_m = reinterpret_cast<float*>(bars + NW * NS);
     float* sm_l = sm_m + NW * kMaxGroup;
     int* sm_abort = reinterpret_cast<int*>(sm_l + NW * kMaxGroup);
-    __shared__ int sm_sum[NW], sm_start[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t stage0 = smem_addr(smem) + warp * NS * S::kStage;
     const uint32_t bar0 = smem_addr(bars) + warp * NS * 8;
@@ -170,70 +413,78 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
 
     const int G = prm.group, H = prm.num_heads;
     const int g = lane >> 2, c = lane & 3;
-    const int mi = lane >> 3, r8 = lane & 7;
     auto length = [&](int b) {  // tokens of sequence b: 0 if out of range
         const int L = __ldg(prm.seq_lens + b);
         return L > 0 && L <= prm.max_seq_len ? L : 0;
     };
+    auto blocks = [&](int b) { return (length(b) + kBlockSize - 1) / kBlockSize; };
 
-    // The share [x, x1) of the list of blocks, from block `first` (list index)
-    // of sequence b on; the list's T blocks are dealt to `ctas` CTAs, q each and
-    // one more to the first r.
-    int kvh, b, cta, x, x1, first, q = 0, r = 0;
+    // The warp's first segment: `cnt` blocks of sequence b from block j0 on,
+    // `stride` apart.  whole: the CTA's warps share the segment and merge.
+    int kvh, b, j0, cnt, stride, cta, nseq;
+    int units = 0, end = 0, first = 0;  // flat, by warp: the run's end and sequence b's first unit
+    bool whole = true;
     int ids_early = -1;  // grid form: ids read before the length is known
     if (prm.flat) {
         kvh = blockIdx.x % prm.num_kv_heads;
         cta = blockIdx.x / prm.num_kv_heads;
-        // thread i sums the blocks of sequences [i per, (i + 1) per)
-        const int per = (prm.num_seqs + NW * 32 - 1) / (NW * 32);
-        const int i0 = threadIdx.x * per, i1 = min(prm.num_seqs, i0 + per);
+        // lane i has sequences [i per, (i + 1) per)
+        const int per = (prm.num_seqs + 31) / 32;
+        const int i0 = min(prm.num_seqs, lane * per), i1 = min(prm.num_seqs, i0 + per);
         int mine = 0;
-        for (int i = i0; i < i1; ++i) mine += (length(i) + kBlockSize - 1) / kBlockSize;
+        for (int i = i0; i < i1; ++i) {
+            const int n = blocks(i);
+            mine += n ? n + kLead : 0;
+        }
         int incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int up = __shfl_up_sync(kFull, incl, off);
             if (lane >= off) incl += up;
         }
-        if (lane == 31) sm_sum[warp] = incl;
-        __syncthreads();
-        int T = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w < warp) incl += sm_sum[w];
-            T += sm_sum[w];
-        }
-        const int ctas = min(prm.ctas_per_head, max(1, T / kMinBlocks));
-        if (cta >= ctas || T == 0) return;
-        q = T / ctas;
-        r = T - q * ctas;
-        x = cta * q + min(cta, r);
-        x1 = x + q + (cta < r ? 1 : 0);
-        if (x >= incl - mine && x < incl) {  // the thread whose sequences hold block x
-            int at = incl - mine, i = i0;
-            for (;; ++i) {
-                const int n = (length(i) + kBlockSize - 1) / kBlockSize;
-                if (x < at + n) break;
-                at += n;
+        units = __shfl_sync(kFull, incl, 31);
+        const FlatRuns runs(units, prm.ctas_per_head);
+        if (cta >= runs.ctas) return;
+        // the sequence that unit u belongs to, and its first unit
+        auto locate = [&](int u, int& seq, int& at) {
+            const int owner = __ffs(__ballot_sync(kFull, u >= incl - mine && u < incl)) - 1;
+            seq = __shfl_sync(kFull, i0, owner);
+            at = __shfl_sync(kFull, incl - mine, owner);
+            for (;; ++seq) {
+                const int n = blocks(seq);
+                const int size = n ? n + kLead : 0;
+                if (u < at + size) return n;
+                at += size;
             }
-            sm_start[0] = i;
-            sm_start[1] = at;
+        };
+        const int u0 = runs.begin(cta), u1 = runs.begin(cta + 1);
+        nseq = locate(u0, b, first);
+        whole = u1 <= first + kLead + nseq;
+        if (whole) {
+            const int lo = max(0, u0 - first - kLead), hi = u1 - first - kLead;  // blocks of the run
+            j0 = lo + warp;
+            stride = NW;
+            cnt = hi - lo > warp ? (hi - lo - warp + NW - 1) / NW : 0;
+        } else {
+            const int v0 = FlatRuns::warp_begin(u0, u1, warp);
+            end = FlatRuns::warp_begin(u0, u1, warp + 1);
+            if (v0 >= first + kLead + nseq) nseq = locate(v0, b, first);
+            j0 = max(0, v0 - first - kLead);
+            stride = 1;
+            cnt = max(0, min(nseq, end - first - kLead) - j0);
         }
-        __syncthreads();
-        b = sm_start[0];
-        first = sm_start[1];
     } else {
         kvh = blockIdx.y;
         b = blockIdx.z;
         cta = blockIdx.x;
-        const int each = prm.partition_size / kBlockSize;
-        first = 0;
-        x = cta * each;
-        const int j = warp + lane * NW;  // bounded by the table's row
-        if (j < each && x + j < prm.max_blocks_per_seq)
-            ids_early = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + x + j);
-        const int n = (length(b) + kBlockSize - 1) / kBlockSize;
-        if (n == 0 && cta == 0) {  // (there may be no merge to do this)
+        stride = NW;
+        const int each = prm.partition_size / kBlockSize, lo = cta * each;
+        j0 = lo + warp;
+        // bounded by the table's row
+        if (lane * NW + warp < each && j0 + lane * NW < prm.max_blocks_per_seq)
+            ids_early = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + j0 + lane * NW);
+        nseq = blocks(b);
+        if (nseq == 0 && cta == 0) {  // (there may be no merge to do this)
             if (__ldg(prm.seq_lens + b) != 0) {
                 if (kvh == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
             } else {
@@ -241,37 +492,19 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
                     prm.out[((size_t)b * H + kvh * G) * D + i] = __float2half_rn(0.f);
             }
         }
-        x1 = min(n, x + each);
-        if (x >= x1) return;
+        const int n = min(nseq - lo, each);
+        if (n <= 0) return;
+        cnt = n > warp ? (n - warp + NW - 1) / NW : 0;
     }
 
-    // score rows, Q and the state are per sequence; the copy ring runs through
-    int done = 0;  // blocks this warp has consumed in earlier segments
-    for (;;) {
-    const int L = length(b);
-    const int nseq = (L + kBlockSize - 1) / kBlockSize;
-    const int blk0 = x - first;
-    const int nblk = min(x1, first + nseq) - x;
-    const bool direct = blk0 == 0 && nblk == nseq;
-    const size_t slot = prm.flat ? (size_t)(cta + b) : (size_t)b * prm.max_partitions + cta;
-    if (prm.flat && blk0 == 0 && kvh == 0 && threadIdx.x == 0) {
-        const int z = first + nseq - 1;  // the sequence's last block, and the CTA that has it
-        const int last = z < r * (q + 1) ? z / (q + 1) : r + (z - r * (q + 1)) / q;
-        prm.seq_parts[2 * b] = cta + b;
-        prm.seq_parts[2 * b + 1] = last - cta + 1;
-    }
-    const int32_t* bt = prm.block_tables + (size_t)b * prm.max_blocks_per_seq + blk0;
-    const int nmine = warp < nblk ? (nblk - warp + NW - 1) / NW : 0;
-
-    // Ids and scales of this warp's iterations, 32 at a time: lane k of batch
-    // n holds iteration 32 n + k, block warp + it * NW of the segment.  The
-    // copies run up to NS iterations ahead, so at most one batch: ids, ks_i and
-    // vs_i belong to the batch of the latest copy, ks_c and vs_c to that of the
-    // block at hand.
+    // Ids and scales of the segment's iterations, 32 at a time: lane k of batch
+    // n holds iteration 32 n + k.  The copies run up to NS iterations ahead, so
+    // at most one batch: ids, ks_i and vs_i belong to the batch of the latest
+    // copy, ks_c and vs_c to that of the block at hand.
     int ids = -1;
     float ks_i = 1.f, vs_i = 1.f, ks_c = 1.f, vs_c = 1.f;
-    auto load_ids = [&](int j, int early) {
-        ids = j < nblk ? (early >= 0 ? early : __ldg(bt + j)) : -1;
+    auto load_ids = [&](int seq, int j, bool in, int early) {
+        ids = !in ? -1 : early >= 0 ? early : __ldg(prm.block_tables + (size_t)seq * prm.max_blocks_per_seq + j);
         if constexpr (F != PA_KV_F16) {
             const bool ok = ids >= 0 && (long long)ids < prm.num_blocks;
             const size_t at = ok ? (size_t)ids * prm.num_kv_heads + kvh : 0;
@@ -279,16 +512,11 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
             vs_i = ok ? __ldg(prm.v_scales + at) : 0.f;
         }
     };
-    load_ids(warp + lane * NW, ids_early);
-    int batch = 0;
     uint32_t valid_bits = 0;  // stage s holds a block with a legal id
-    auto issue = [&](int it) {
-        if ((it >> 5) != batch) {
-            batch = it >> 5;
-            load_ids(warp + ((it & ~31) + lane) * NW, -1);
-        }
-        const int phys = __shfl_sync(kFull, ids, it & 31);
-        const int s = (done + it) % NS;
+    // Copy the block of the batch's lane k into the stage of the warp's n-th block.
+    auto copy = [&](int n, int k) {
+        const int phys = __shfl_sync(kFull, ids, k);
+        const int s = n % NS;
         const uint32_t bar = bar0 + 8 * s;
         const bool ok = phys >= 0 && (long long)phys < prm.num_blocks;
         valid_bits = ok ? (valid_bits | (1u << s)) : (valid_bits & ~(1u << s));
@@ -305,182 +533,153 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
             }
         }
     };
-    for (int it = 0; it < NS && it < nmine; ++it) issue(it);
 
-    // Q as the B operand, its k index in K's order: for fp16 the lane holds
-    // dims 16 i + 2c (+1) and + 8, in 8 bits dims 16 i' + 4c .. + 3, i' = the
-    // i-th 16-byte unit of the row.
+    int done = 0;    // blocks this warp has consumed in earlier segments
+    int issued = 0;  // copies of this segment that are on their way
+    load_ids(b, j0 + lane * stride, lane < cnt, ids_early);
+    for (; issued < NS && issued < cnt; ++issued) copy(issued, issued);
+
     uint32_t qb[D / 16][2];
-    {
-        const uint32_t* qrow =
-            reinterpret_cast<const uint32_t*>(prm.q + ((size_t)b * H + kvh * G + (g < G ? g : 0)) * D);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const int lo = F == PA_KV_F16 ? 8 * i + c : 8 * i + 2 * c;
-            const int hi = F == PA_KV_F16 ? lo + 4 : lo + 1;
-            qb[i][0] = g < G ? __ldg(qrow + lo) : 0u;
-            qb[i][1] = g < G ? __ldg(qrow + hi) : 0u;
-        }
-    }
-
-    float o[S::kTilesM][4];
-#pragma unroll
-    for (int i = 0; i < S::kTilesM; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY;  // running maximum of heads 2c, 2c + 1
-    float l0 = 0.f, l1 = 0.f;              // this lane's share of the exp sums
-    // score rows of heads 2c and 2c + 1
-    float* score0 = nullptr;
-    if (prm.scores && 2 * c < G) score0 = prm.scores + ((size_t)b * H + kvh * G + 2 * c) * prm.score_stride;
-
+    WarpState<D> st;
     bool timed_out = false;
-    int i = 0;
-    for (; i < nmine; ++i) {
-        const int s = (done + i) % NS;
-        if (prm.force_timeout || !mbar_wait(bar0 + 8 * s, ((done + i) / NS) & 1, prm.wait_limit)) {
-            timed_out = true;
-            break;
+    for (;;) {
+        const int L = length(b);
+        if (prm.flat && j0 == 0 && kvh == 0 && lane == 0 && cnt > 0) {
+            // where the merge finds the sequence's partials
+            const FlatRuns runs(units, prm.ctas_per_head);
+            const SeqParts parts(runs, first, nseq, b);
+            int4* to = reinterpret_cast<int4*>(prm.seq_parts) + 2 * (size_t)b;
+            to[0] = make_int4(parts.first[0], parts.count[0], parts.first[1], parts.count[1]);
+            to[1] = make_int4(parts.first[2], parts.count[2], 0, 0);
         }
-        if ((i & 31) == 0) ks_c = ks_i, vs_c = vs_i;  // copy i, and none of the next batch, has been issued
-        if ((valid_bits >> s) & 1u) {
-            const int tok0 = (blk0 + warp + i * NW) * kBlockSize;
-            const int nvalid = min(kBlockSize, L - tok0);
-            const uint32_t kst = stage0 + s * S::kStage, vst = kst + S::kTile;
-            const float ks = F == PA_KV_F16 ? prm.scale_log2 : prm.scale_log2 * __shfl_sync(kFull, ks_c, i & 31);
-            const float vs = F == PA_KV_F16 ? 1.f : __shfl_sync(kFull, vs_c, i & 31);
+        // Q as the B operand, its k index in K's order: for fp16 the lane holds
+        // dims 16 i + 2c (+1) and + 8, in 8 bits dims 16 i + 4c .. + 3
+        {
+            const uint32_t* qrow =
+                reinterpret_cast<const uint32_t*>(prm.q + ((size_t)b * H + kvh * G + (g < G ? g : 0)) * D);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const int lo = F == PA_KV_F16 ? 8 * i + c : 8 * i + 2 * c;
+                const int hi = F == PA_KV_F16 ? lo + 4 : lo + 1;
+                qb[i][0] = g < G ? __ldg(qrow + lo) : 0u;
+                qb[i][1] = g < G ? __ldg(qrow + hi) : 0u;
+            }
+        }
+        st.clear();
+        float* scores = nullptr;  // of head 2c
+        if (prm.scores && 2 * c < G) scores = prm.scores + ((size_t)b * H + kvh * G + 2 * c) * prm.score_stride;
+        const bool two = 2 * c + 1 < G;
 
-            // S^T = K . Q^T
-            float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (F == PA_KV_F16) {
-                const int rq = r8 + ((mi & 1) << 3);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t a[4];
-                    ldsm_x4(a, kst + unit_at<F, D>(rq, 2 * k + (mi >> 1)));
-                    if (k & 1)
-                        mma_16816(sb, a, qb[k][0], qb[k][1]);
-                    else
-                        mma_16816(sa, a, qb[k][0], qb[k][1]);
-                }
-            } else {
-                const int rq = r8 + ((mi & 1) << 3);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) {  // two 16-byte units: units 2k and 2k + 1
-                    uint32_t w[4];
-                    ldsm_x4(w, kst + unit_at<F, D>(rq, 2 * k + (mi >> 1)));
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = unsign<F>(w[x]);
-                    const uint32_t a[4] = {halves_lo<F>(w[0]), halves_lo<F>(w[1]), halves_hi<F>(w[0]),
-                                           halves_hi<F>(w[1])};
-                    mma_16816(sa, a, qb[2 * k][0], qb[2 * k][1]);
-                    const uint32_t e[4] = {halves_lo<F>(w[2]), halves_lo<F>(w[3]), halves_hi<F>(w[2]),
-                                           halves_hi<F>(w[3])};
-                    mma_16816(sb, e, qb[2 * k + 1][0], qb[2 * k + 1][1]);
-                }
-            }
-            // lane holds tokens g (s0, s1) and g + 8 (s2, s3) of heads 2c, 2c + 1
-            float s0 = (sa[0] + sb[0]) * ks, s1 = (sa[1] + sb[1]) * ks;
-            float s2 = (sa[2] + sb[2]) * ks, s3 = (sa[3] + sb[3]) * ks;
-            if (score0) {
-                float* r0 = score0 + tok0 + g;
-                float* r1 = r0 + prm.score_stride;
-                const bool two = 2 * c + 1 < G;
-                if (g < nvalid) {
-                    r0[0] = s0;
-                    if (two) r1[0] = s1;
-                }
-                if (g + 8 < nvalid) {
-                    r0[8] = s2;
-                    if (two) r1[8] = s3;
-                }
-            }
-            if (g >= nvalid) s0 = s1 = -INFINITY;  // tokens past the end are excluded
-            if (g + 8 >= nvalid) s2 = s3 = -INFINITY;
+        // a warp's next segment (runs of their own): the next sequence with tokens
+        int b_next = b, n_next = 0, first_next = first, cnt_next = 0;
+        if (!whole && first + kLead + nseq < end) {
+            first_next = first + kLead + nseq;
+            do n_next = blocks(++b_next);
+            while (n_next == 0);  // the run goes on, so there is one
+            cnt_next = max(0, min(n_next, end - first_next - kLead));
+        }
+        int issued_next = 0;
 
-            float bm0 = fmaxf(s0, s2), bm1 = fmaxf(s1, s3);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, off));
-                bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, off));
+        for (int i = 0; i < cnt; ++i) {
+            const int n = done + i, s = n % NS;
+            if (prm.force_timeout || !mbar_wait(bar0 + 8 * s, (n / NS) & 1, prm.wait_limit)) {
+                // wait for this warp's copies still in flight before it may leave
+                for (int k = n; k < done + issued + issued_next; ++k)
+                    mbar_wait(bar0 + 8 * (k % NS), (k / NS) & 1, kDefaultWaitLimit);
+                timed_out = true;
+                break;
             }
-            const float mn0 = fmaxf(m0, bm0), mn1 = fmaxf(m1, bm1);
-            const float al0 = exp2f(m0 - mn0), al1 = exp2f(m1 - mn1);
-            m0 = mn0;
-            m1 = mn1;
-            const float e0 = mn0 - kShift, e1 = mn1 - kShift;
-            const float p0 = exp2f(s0 - e0), p1 = exp2f(s1 - e1), p2 = exp2f(s2 - e0), p3 = exp2f(s3 - e1);
-            l0 = l0 * al0 + (p0 + p2);
-            l1 = l1 * al1 + (p1 + p3);
-            if (__any_sync(kFull, al0 != 1.f || al1 != 1.f)) {
-#pragma unroll
-                for (int mt = 0; mt < S::kTilesM; ++mt) {
-                    o[mt][0] *= al0;
-                    o[mt][1] *= al1;
-                    o[mt][2] *= al0;
-                    o[mt][3] *= al1;
+            // copy i has been issued, and none of the next batch or sequence
+            if ((i & 31) == 0) ks_c = ks_i, vs_c = vs_i;
+            if ((valid_bits >> s) & 1u) {
+                const int tok0 = (j0 + i * stride) * kBlockSize;
+                const uint32_t kst = stage0 + s * S::kStage;
+                const float ks = F == PA_KV_F16 ? prm.scale_log2 : prm.scale_log2 * __shfl_sync(kFull, ks_c, i & 31);
+                const float vs = F == PA_KV_F16 ? 1.f : __shfl_sync(kFull, vs_c, i & 31);
+                block_update<F, D>(st, qb, kst, kst + S::kTile, smem + (kst + S::kTile - smem_addr(smem)),
+                                   min(kBlockSize, L - tok0), ks, vs, scores ? scores + tok0 : nullptr,
+                                   prm.score_stride, two);
+            }
+            __syncwarp();
+            if (issued < cnt) {
+                if ((issued & 31) == 0) {
+                    const int it = issued + lane;
+                    load_ids(b, j0 + it * stride, it < cnt, -1);
                 }
+                copy(done + issued, issued & 31);
+                ++issued;
+            } else if (issued_next < cnt_next && (i >> 5) == ((cnt - 1) >> 5)) {
+                // (the last batch's scales have been taken over)
+                if (issued_next == 0) load_ids(b_next, lane, lane < cnt_next, -1);
+                copy(done + cnt + issued_next, issued_next);
+                ++issued_next;
             }
-            const uint32_t pb0 = movmatrix_trans(half2_bits(__floats2half2_rn(p0, p1)));  // tokens 0..7
-            const uint32_t pb1 = movmatrix_trans(half2_bits(__floats2half2_rn(p2, p3)));  // tokens 8..15
+        }
+        if (timed_out) {
+            if (lane == 0) {
+                atomicOr(prm.status, PA_DEV_TIMEOUT);
+                atomicExch(sm_abort, 1);
+            }
+            if (!whole) return;
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            st.l0 += __shfl_xor_sync(kFull, st.l0, off);
+            st.l1 += __shfl_xor_sync(kFull, st.l1, off);
+        }
+        if (F == PA_KV_F16) st.vr = 1.f;
+        if (whole) break;
 
-            if (nvalid < kBlockSize) {
-                // 0 * NaN would poison P.V: clear the V rows past the end
-                constexpr int kUnits = S::kRow / 16;
-                for (int u = lane; u < (kBlockSize - nvalid) * kUnits; u += 32) {
-                    const uint32_t at = unit_at<F, D>(nvalid + u / kUnits, u % kUnits);
-                    *reinterpret_cast<uint4*>(smem + (vst - smem_addr(smem)) + at) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-            }
-
-            // O^T += V^T . P^T
-            if constexpr (F == PA_KV_F16) {
-                const int rv = r8 + ((mi >> 1) << 3);
+        // the segment's partial, or the output, straight from the fragments
+        if (cnt > 0) {
+            const bool direct = j0 == 0 && cnt == nseq;
+            const float f0 = st.vr / st.l0, f1 = st.vr / st.l1;
+            const size_t head0 = (size_t)b * H + kvh * G + 2 * c;
+            const size_t slot = (size_t)(prm.ctas_per_head + cta * NW + warp + b);
+            const size_t pi = ((size_t)kvh * prm.slots + slot) * G + 2 * c;
+            const bool one = 2 * c < G;
 #pragma unroll
-                for (int mt = 0; mt < S::kTilesM; ++mt) {
-                    uint32_t a[4];
-                    ldsm_x4_trans(a, vst + unit_at<F, D>(rv, 2 * mt + (mi & 1)));
-                    mma_16816(o[mt], a, pb0, pb1);
-                }
-            } else {
-                const int rv = r8 + ((mi & 1) << 3);
+            for (int mt = 0; mt < D / 16; ++mt) {
+                const float v[4] = {st.o[mt][0] * f0, st.o[mt][1] * f1, st.o[mt][2] * f0, st.o[mt][3] * f1};
+                const int d0 = out_dim<F>(mt, g, 0), d1 = out_dim<F>(mt, g, 1);
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    uint32_t w[4];
-                    ldsm_x4_trans(w, vst + unit_at<F, D>(rv, 2 * k + (mi >> 1)));
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = unsign<F>(__byte_perm(w[x], 0u, 0x3120));
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t a[4] = {halves_lo<F>(w[2 * y]), halves_hi<F>(w[2 * y]),
-                                               halves_lo<F>(w[2 * y + 1]), halves_hi<F>(w[2 * y + 1])};
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_16816(t, a, pb0, pb1);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) o[2 * k + y][x] = fmaf(vs, t[x], o[2 * k + y][x]);
+                for (int h = 0; h < 2; ++h) {
+                    if (!(h ? two : one)) continue;
+                    if (direct) {
+                        __half* o = prm.out + (head0 + h) * D;
+                        if (F == PA_KV_F16) {
+                            o[d0] = __float2half_rn(v[h]);
+                            o[d1] = __float2half_rn(v[2 + h]);
+                        } else {
+                            *reinterpret_cast<__half2*>(o + d0) = __floats2half2_rn(v[h], v[2 + h]);
+                        }
+                    } else {
+                        float* o = prm.acc + (pi + h) * D;
+                        if (F == PA_KV_F16) {
+                            o[d0] = v[h];
+                            o[d1] = v[2 + h];
+                        } else {
+                            *reinterpret_cast<float2*>(o + d0) = make_float2(v[h], v[2 + h]);
+                        }
                     }
                 }
             }
+            // the sum is relative to 2^(m - kShift)
+            if (g == 0 && one) prm.sums[pi] = make_float2(st.m0 - kShift, st.l0);
+            if (g == 0 && two) prm.sums[pi + 1] = make_float2(st.m1 - kShift, st.l1);
         }
-        __syncwarp();
-        if (i + NS < nmine) issue(i + NS);
+        if (n_next == 0) return;
+        done += cnt;
+        b = b_next;
+        nseq = n_next;
+        first = first_next;
+        j0 = 0;
+        cnt = cnt_next;
+        issued = issued_next;
+        if (issued == 0) load_ids(b, lane, lane < cnt, -1);
+        for (; issued < NS && issued < cnt; ++issued) copy(done + issued, issued);
     }
 
-    if (timed_out) {
-        // wait for this warp's copies still in flight before the CTA may exit
-        const int issued = min(nmine, i + NS);
-        for (int k = done + i; k < done + issued; ++k)
-            mbar_wait(bar0 + 8 * (k % NS), (k / NS) & 1, kDefaultWaitLimit);
-        if (lane == 0) {
-            atomicOr(prm.status, PA_DEV_TIMEOUT);
-            atomicExch(sm_abort, 1);
-        }
-    }
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-        l0 += __shfl_xor_sync(kFull, l0, off);
-        l1 += __shfl_xor_sync(kFull, l1, off);
-    }
     __syncthreads();  // all stages consumed; the area is reused below
     if (*sm_abort) return;
 
@@ -493,67 +692,58 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
 #pragma unroll
         for (int mt = 0; mt < S::kTilesM; ++mt) {
             const int d0 = out_dim<F>(mt, g, 0), d1 = out_dim<F>(mt, g, 1);
-            rw[(2 * c) * S::kRedStride + d0] = o[mt][0];
-            rw[(2 * c + 1) * S::kRedStride + d0] = o[mt][1];
-            rw[(2 * c) * S::kRedStride + d1] = o[mt][2];
-            rw[(2 * c + 1) * S::kRedStride + d1] = o[mt][3];
+            rw[(2 * c) * S::kRedStride + d0] = st.o[mt][0] * st.vr;
+            rw[(2 * c + 1) * S::kRedStride + d0] = st.o[mt][1] * st.vr;
+            rw[(2 * c) * S::kRedStride + d1] = st.o[mt][2] * st.vr;
+            rw[(2 * c + 1) * S::kRedStride + d1] = st.o[mt][3] * st.vr;
         }
         if (g == 0) {
-            sm_m[warp * kMaxGroup + 2 * c] = m0;
-            sm_m[warp * kMaxGroup + 2 * c + 1] = m1;
-            sm_l[warp * kMaxGroup + 2 * c] = l0;
-            sm_l[warp * kMaxGroup + 2 * c + 1] = l1;
+            sm_m[warp * kMaxGroup + 2 * c] = st.m0;
+            sm_m[warp * kMaxGroup + 2 * c + 1] = st.m1;
+            sm_l[warp * kMaxGroup + 2 * c] = st.l0;
+            sm_l[warp * kMaxGroup + 2 * c + 1] = st.l1;
         }
     }
     __syncthreads();
     constexpr int kSlice = D / NW;
     const int h = lane >> 2, qd = lane & 3;
-    if (h < G) {
-        float Mh = sm_m[h];
+    if (h >= G) return;
+    float Mh = sm_m[h];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) Mh = fmaxf(Mh, sm_m[w * kMaxGroup + h]);
-        float f[NW], Lh = 0.f;
+    for (int w = 1; w < NW; ++w) Mh = fmaxf(Mh, sm_m[w * kMaxGroup + h]);
+    float f[NW], Lh = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {  // a warp without blocks has m = -inf and counts for nothing
-            const float mw = sm_m[w * kMaxGroup + h];
-            f[w] = mw == -INFINITY ? 0.f : exp2f(mw - Mh);
-            Lh += f[w] * sm_l[w * kMaxGroup + h];
-        }
-        const float inv = 1.f / Lh;
-        const size_t head = (size_t)b * H + kvh * G + h;
-        const size_t pi = ((size_t)kvh * prm.slots + slot) * G + h;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) f[w] *= inv;
-#pragma unroll
-        for (int k = 0; k < kSlice / 8; ++k) {
-            const int d = warp * kSlice + 8 * k + 2 * qd;
-            float v0 = 0.f, v1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float* rw = red + (w * kMaxGroup + h) * S::kRedStride + d;
-                v0 += f[w] * rw[0];
-                v1 += f[w] * rw[1];
-            }
-            if (direct)
-                *reinterpret_cast<__half2*>(prm.out + head * D + d) = __floats2half2_rn(v0, v1);
-            else
-                *reinterpret_cast<float2*>(prm.acc + pi * D + d) = make_float2(v0, v1);
-        }
-        // the sum is relative to 2^(M - kShift): log2 of the whole is its reference plus log2 l
-        if (warp == 0 && qd == 0 && prm.sums) prm.sums[pi] = make_float2(Mh - kShift, Lh);
+    for (int w = 0; w < NW; ++w) {  // a warp without blocks has m = -inf and counts for nothing
+        const float mw = sm_m[w * kMaxGroup + h];
+        f[w] = mw == -INFINITY ? 0.f : exp2f(mw - Mh);
+        Lh += f[w] * sm_l[w * kMaxGroup + h];
     }
-    // on to the next sequence of the share
-    x += nblk;
-    if (x >= x1) return;
-    first += nseq;
-    do ++b;
-    while (length(b) == 0);  // x < x1 <= T: there is one
-    done += nmine;
-    ids_early = -1;
-    // the next copies overwrite what the merge wrote and read through the generic proxy
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
+    const float inv = 1.f / Lh;
+    const size_t head = (size_t)b * H + kvh * G + h;
+    const size_t slot = prm.flat ? (size_t)cta : (size_t)b * prm.max_partitions + cta;
+    const size_t pi = ((size_t)kvh * prm.slots + slot) * G + h;
+    // the CTA has the whole sequence: its run begins in or before block 0 and ends with the last
+    const bool direct = j0 == warp && (prm.flat ? FlatRuns(units, prm.ctas_per_head).begin(cta + 1) == first + kLead + nseq
+                                                : prm.partition_size / kBlockSize >= nseq);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) f[w] *= inv;
+#pragma unroll
+    for (int k = 0; k < kSlice / 8; ++k) {
+        const int d = warp * kSlice + 8 * k + 2 * qd;
+        float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float* rw = red + (w * kMaxGroup + h) * S::kRedStride + d;
+            v0 += f[w] * rw[0];
+            v1 += f[w] * rw[1];
+        }
+        if (direct)
+            *reinterpret_cast<__half2*>(prm.out + head * D + d) = __floats2half2_rn(v0, v1);
+        else
+            *reinterpret_cast<float2*>(prm.acc + pi * D + d) = make_float2(v0, v1);
     }
+    // the sum is relative to 2^(M - kShift): log2 of the whole is its reference plus log2 l
+    if (warp == 0 && qd == 0 && prm.sums) prm.sums[pi] = make_float2(Mh - kShift, Lh);
 }
 
 // Blocks x < slices of a (sequence, kv head): slice x of the merge of its
@@ -571,24 +761,34 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
     const int kvh = blockIdx.y, b = blockIdx.z, G = prm.group;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int L = __ldg(prm.seq_lens + b);
-    long long slot0;
-    int n;
+    // Partial p of the sequence is slot at(p).  seq_parts is not written for an
+    // empty sequence (and then not used) nor after a timeout: the clamps keep the
+    // reads inside the workspace.
+    int n, n0 = 0, n1 = 0;
+    long long s0 = 0, s1 = 0, s2 = 0;
     if (prm.flat) {
-        // not written for an empty sequence (and then not used) nor after a
-        // timeout: the clamps keep the reads inside the workspace
-        slot0 = min(max((long long)prm.seq_parts[2 * b], 0ll), prm.slots - 1);
-        n = (int)min(max((long long)prm.seq_parts[2 * b + 1], 1ll), prm.slots - slot0);
+        const int4* parts = reinterpret_cast<const int4*>(prm.seq_parts) + 2 * (size_t)b;
+        const int4 u = parts[0], v = parts[1];
+        const long long most = prm.slots;
+        auto clamp = [&](long long x, long long lo, long long hi) { return min(max(x, lo), hi); };
+        n0 = (int)clamp(u.y, 0, kKvWarps);
+        n1 = (int)clamp(u.w, 0, most);
+        n = n0 + n1 + (int)clamp(v.y, 0, kKvWarps);
+        s0 = clamp(u.x, 0, most - n0);
+        s1 = clamp(u.z, 0, most - n1) - n0;
+        s2 = clamp(v.x, 0, most - (n - n0 - n1)) - n0 - n1;
     } else {
-        slot0 = (long long)b * prm.max_partitions;
         n = (L + prm.partition_size - 1) / prm.partition_size;
+        n0 = n;
+        s0 = (long long)b * prm.max_partitions;
     }
+    const size_t head_slots = (size_t)(kvh * prm.slots);
+    auto at = [&](int p) { return head_slots + (size_t)(p + (p < n0 ? s0 : p < n0 + n1 ? s1 : s2)); };
     const bool merge = (int)blockIdx.x < prm.slices;
     if (L < 0 || L > prm.max_seq_len) {
         if (blockIdx.x == 0 && kvh == 0 && tid == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return;
     }
-    const size_t p0 = (size_t)(kvh * prm.slots + slot0);
-    const float2* sums = prm.sums + p0 * G;
     if (merge) {
         // float4 column `col` of the G D outputs, by `groups` groups of threads
         // that take every groups-th partial
@@ -605,11 +805,12 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
         float m = -INFINITY, l = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         if (grp < groups) {
-            const float4* acc = reinterpret_cast<const float4*>(prm.acc + p0 * G * D) + col;
+            const float4* acc = reinterpret_cast<const float4*>(prm.acc) + col;
 #pragma unroll 4
             for (int p = grp; p < n; p += groups) {
-                const float2 ml = sums[(size_t)p * G + h];
-                const float4 t = acc[(size_t)p * G * (D / 4)];
+                const size_t row = at(p) * G;
+                const float2 ml = prm.sums[row + h];
+                const float4 t = acc[row * (D / 4)];
                 const float mn = fmaxf(m, ml.x);
                 const float alpha = exp2f(m - mn), beta = ml.y * exp2f(ml.x - mn);
                 l = l * alpha + beta;
@@ -662,7 +863,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
     if (warp < G) {  // 8 warps, at most 8 heads
         float m = -INFINITY, l = 0.f;
         for (int p = lane; p < n; p += 32) {
-            const float2 ml = sums[(size_t)p * G + warp];
+            const float2 ml = prm.sums[at(p) * G + warp];
             const float mn = fmaxf(m, ml.x);
             l = l * exp2f(m - mn) + ml.y * exp2f(ml.x - mn);
             m = mn;

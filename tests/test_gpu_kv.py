@@ -393,3 +393,48 @@ def test_append_finds_its_sequence_in_large_batches(fmt, B):
     append(c, new, k_new, v_new, loc)
     assert status() == 0
     same_cache(c, ref)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,top,long,hkv,dim", [(200, 60, 0, 2, 64), (33, 300, 2500, 3, 128), (64, 40, 5000, 1, 256), (700, 20, 0, 1, 64),
+                                                (5, 900, 0, 16, 64)])
+def test_decode_ragged_batches(fmt, B, top, long, hkv, dim):
+    # runs of blocks that cross many sequences, empty ones among them, one long sequence in the middle
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    lens[0] = lens[-1] = 0
+    if long:
+        lens[B // 2] = long
+    c = K.Case(lens, 3 * hkv, hkv, dim, fmt, seed=33, device=DEV)
+    ref, bound, w, wb = K.decode_reference(c)
+    out, got = decode(c, weights=True)
+    check(out, ref, bound)
+    for b, n in enumerate(c.lens):
+        check(got[b, :, :n], w[b, :, :n], wb[b, :, :n] + 1e-30)
+        assert bool((got[b, :, n:] == -7).all())
+    assert torch.equal(decode(c), out) and torch.equal(decode(c), out)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_decode_value_scales_far_apart(fmt):
+    # the block with the weight has values 2^-30 of its neighbours', whose keys are far below
+    c = K.Case([64, 100, 33], 4, 1, 128, fmt, seed=34, device=DEV, spread=0.0)
+    for b in range(3):
+        for j in range(-(-c.lens[b] // BS)):
+            c.vs[int(c.tables[b, j])] *= 2.0 ** (-30 if j == b else 0)
+            if j != b:
+                c.ks[int(c.tables[b, j])] = 0.0  # scores 0
+    # scores of the small blocks: about 60 above the rest
+    for b in range(3):
+        blk = int(c.tables[b, b])
+        c.k[blk] = torch.tensor(1.0).to(c.k.dtype).to(DEV)
+        c.ks[blk] = 30.0
+    c.q.fill_(0.18)
+    ref, bound, w, wb = K.decode_reference(c)
+    out, got = decode(c, weights=True)
+    check(out.double() * 2 ** 12, ref * 2 ** 12, bound * 2 ** 12)
+    for b, n in enumerate(c.lens):
+        check(got[b, :, :n], w[b, :, :n], wb[b, :, :n] + 1e-30)
+    tiny = K.Case([40], 4, 1, 64, fmt, seed=35, device=DEV)
+    tiny.vs[tiny.tables[0].long()] = 1e-42  # a subnormal scale: zero in fp16
+    assert bool((decode(tiny) == 0).all())
