@@ -578,9 +578,9 @@ int pa_kv_append(const pa_kv_append_args* args, pa_stream_t stream);
  * [num_seqs][num_kv_heads][weights_stride] with weights_stride >=
  * max_seq_len; they may be the same array and otherwise must not overlap.
  * Entries from seq_lens[b] on are neither read nor written.
- * Of the options partition_size, wait_limit, PA_FLAG_FORCE_TIMEOUT and mode
- * AUTO, SINGLE and SPLIT apply.  The workspace needs no initialisation and
- * holds pa_kv_decode_workspace_size bytes (same sizes, format, partition
+ * Of the options partition_size and mode AUTO, SINGLE and SPLIT apply (no wait
+ * of this call can run out).  The workspace needs no initialisation and holds
+ * pa_kv_decode_workspace_size bytes (same sizes, format, partition
  * size and device; partition_size 0 for the library's own plan), 0 where
  * sizes are out of range. */
 typedef struct {

@@ -659,7 +659,7 @@ def pa_kv_decode_workspace_size(num_seqs, max_seq_len, num_heads, num_kv_heads, 
 def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, stream=None, *,
                  max_seq_len: int, weights_in: Optional[torch.Tensor] = None,
                  weights_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                 mode="auto", partition_size: int = 0, flags: int = 0, wait_limit: int = 0) -> None:
+                 mode="auto", partition_size: int = 0) -> None:
     """Decode over a float16, float8_e4m3fn or int8 cache (see include/pa_decode.h).
 
     out / q: float16 [num_seqs, num_heads, head_dim].  With weights_out (float32
@@ -684,8 +684,8 @@ def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq
     args = _DECODE.pack(op, qp, *cache, table, _tensor("seq_lens", seq_lens, torch.int32, (B,), dev), win, wout, stride,
                         B, cols, max_seq_len, H, scale)
     opts = None
-    if partition_size or flags or wait_limit or mode != "auto":
-        opts = ctypes.byref(make_opts(mode=mode, partition_size=partition_size, flags=flags, wait_limit=wait_limit))
+    if partition_size or mode != "auto":
+        opts = ctypes.byref(make_opts(mode=mode, partition_size=partition_size))
 
     def run(stream_handle):
         need = 0

@@ -1036,23 +1036,6 @@ int sm_count(int* num_sms) { return query_sm_count(num_sms); }
 
 int check_prefix(const pa_prefix_args* a, const pa_decode_opts* o) { return validate_prefix(a, o); }
 
-int make_block_map(CUtensorMap* map, const void* base, long long num_blocks, int num_kv_heads, int head_dim,
-                   int elem_bytes) {
-    if (elem_bytes == 2) return make_cache_block_map(map, base, num_blocks, num_kv_heads, head_dim);
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return PA_ERR_CUDA;
-    const cuuint64_t rows = static_cast<cuuint64_t>(num_blocks) * num_kv_heads * kBlockSize;
-    const cuuint32_t cols = head_dim < 128 ? head_dim : 128;
-    cuuint64_t dims[3] = {cols, rows > 0 ? rows : 1, static_cast<cuuint64_t>(head_dim) / cols};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim), cols};
-    cuuint32_t box[3] = {cols, static_cast<cuuint32_t>(kBlockSize), static_cast<cuuint32_t>(head_dim) / cols};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
-}
-
 }  // namespace pa
 
 extern "C" {

@@ -2,7 +2,6 @@
 // calls (pa_kv_api.cpp) and their kernels (pa_kv_decode.cu, pa_kv_cache.cu).
 #pragma once
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -16,16 +15,12 @@ namespace pa {
 // Defined in pa_api.cpp for the other C-ABI sources.
 int sm_count(int* num_sms);                               // of the current device; a PA_* code
 int check_prefix(const pa_prefix_args* args, const pa_decode_opts* opts);  // a PA_* code
-// A cache of `elem_bytes`-byte elements viewed as (box column, row, column
-// chunk); one box brings the 16 rows of a (block, kv head).  Rows of 128
-// bytes or more come in 128-byte chunks with the 128-byte swizzle, 64-byte
-// rows in one chunk with the 64-byte swizzle.
-int make_block_map(CUtensorMap* map, const void* base, long long num_blocks, int num_kv_heads, int head_dim,
-                   int elem_bytes);
 
 struct KvDecodeParams {
     __half* out;
     const __half* q;
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
     const float* k_scales;  // null for fp16
     const float* v_scales;
     const int32_t* block_tables;
@@ -42,8 +37,6 @@ struct KvDecodeParams {
     int flat, ctas_per_head;                // flat form
     int partition_size, max_partitions;     // grid form
     float scale_log2;
-    unsigned wait_limit;
-    int force_timeout;
     unsigned int* status;
 };
 
@@ -65,8 +58,7 @@ struct KvMergeParams {
 
 constexpr int kKvWarps = 4;                        // of a decode CTA
 int kv_decode_ctas(int format, int head_dim);      // decode CTAs an SM holds at once; -1: not compiled
-cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, const CUtensorMap& tk,
-                             const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
+cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, dim3 grid, cudaStream_t stream);
 constexpr int kKvWeightsTokens = 1024;  // tokens of a CTA that adds weights
 cudaError_t launch_kv_merge(int head_dim, const KvMergeParams& prm, dim3 grid, cudaStream_t stream);
 

@@ -154,15 +154,12 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     if (sp.bytes > 0 && (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign))) return PA_ERR_WORKSPACE;
     const bool split = plan.flat || plan.parts > 1;
 
-    const int elem = c.format == PA_KV_F16 ? 2 : 1;
-    CUtensorMap tk, tv;
-    if ((rc = pa::make_block_map(&tk, c.k_cache, c.num_blocks, c.num_kv_heads, c.head_dim, elem)) ||
-        (rc = pa::make_block_map(&tv, c.v_cache, c.num_blocks, c.num_kv_heads, c.head_dim, elem)))
-        return rc;
     uint8_t* w = static_cast<uint8_t*>(ws);
     pa::KvDecodeParams p{};
     p.out = static_cast<__half*>(a->out);
     p.q = static_cast<const __half*>(a->q);
+    p.k_cache = static_cast<const uint8_t*>(c.k_cache);
+    p.v_cache = static_cast<const uint8_t*>(c.v_cache);
     p.k_scales = c.k_scales;
     p.v_scales = c.v_scales;
     p.block_tables = a->block_tables;
@@ -185,13 +182,11 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     p.partition_size = plan.partition_size;
     p.max_partitions = plan.parts;
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
-    p.wait_limit = (o && o->wait_limit) ? o->wait_limit : pa::kDefaultWaitLimit;
-    p.force_timeout = (o && (o->flags & PA_FLAG_FORCE_TIMEOUT)) ? 1 : 0;
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
     const dim3 grid = plan.flat ? dim3(plan.ctas_per_head * c.num_kv_heads)
                                 : dim3(plan.parts, c.num_kv_heads, a->num_seqs);
-    if (pa::launch_kv_decode(c.format, c.head_dim, p, tk, tv, grid, stream) != cudaSuccess) return PA_ERR_CUDA;
+    if (pa::launch_kv_decode(c.format, c.head_dim, p, grid, stream) != cudaSuccess) return PA_ERR_CUDA;
     if (!split && !weights) return PA_OK;
     pa::KvMergeParams m{};
     m.out = p.out;

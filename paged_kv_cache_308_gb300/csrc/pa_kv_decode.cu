@@ -127,9 +127,7 @@ struct SeqParts {
 template <int F, int D, int NS>
 struct KvShape {
     static constexpr int kNW = kKvWarps;
-    static constexpr int kElem = F == PA_KV_F16 ? 2 : 1;
-    static constexpr int kRow = D * kElem;                       // bytes of a token's row
-    static constexpr int kChunk = kRow < 128 ? kRow : 128;       // bytes of a row in one swizzled box
+    static constexpr int kRow = D * (F == PA_KV_F16 ? 2 : 1);    // bytes of a token's row
     static constexpr int kTile = kBlockSize * kRow;              // K (or V) of a block
     static constexpr int kStage = 2 * kTile;
     static constexpr int kStageArea = kNW * NS * kStage;
@@ -137,19 +135,46 @@ struct KvShape {
     static constexpr int kRedStride = D + 4;
     static constexpr int kRedBytes = kNW * kMaxGroup * kRedStride * 4;
     static constexpr int kArea = kStageArea > kRedBytes ? kStageArea : kRedBytes;
-    // barriers, (m, l) of the warps, abort flag
-    static constexpr int kCtrl = kNW * NS * 8 + 2 * kNW * kMaxGroup * 4 + 16;
-    static constexpr int kSmem = 1024 + kArea + kCtrl;
+    static constexpr int kSmem = kArea + 2 * kNW * kMaxGroup * 4;  // + (m, l) of the warps
     static_assert(kSmem <= 227 * 1024, "shared memory budget of one CTA");
 };
 
-// Byte offset of 16-byte unit `unit` of row `row` in a staged tile.
+// Byte offset of 16-byte unit `unit` of row `row` in a staged tile: 128-byte
+// columns, the units of a row exchanged by the row's number modulo 8 (64-byte
+// rows: modulo 4, every other row), so that the eight rows of an ldmatrix
+// matrix lie in different banks.
 template <int F, int D>
 __device__ __forceinline__ uint32_t unit_at(int row, int unit) {
-    if constexpr (F != PA_KV_F16 && D == 64)  // 64-byte rows, 64-byte swizzle
+    if constexpr (F != PA_KV_F16 && D == 64)
         return static_cast<uint32_t>(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
     else
         return static_cast<uint32_t>((unit >> 3) * (kBlockSize * 128)) + swz(row, unit & 7);
+}
+
+// Start copying a tile (contiguous in memory) to `stage`, 16 bytes a lane and
+// instruction.  Pass i begins kRows i rows on; as kRows is a power of two, row
+// & 7 is (kRows i & 7) ^ (the row in the pass), so the swizzle of a pass is the
+// first one's, exclusive-or a constant.
+template <int F, int D>
+__device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t* src) {
+    constexpr int kRow = D * (F == PA_KV_F16 ? 2 : 1);
+    constexpr int kRows = 512 / kRow;  // rows of a pass (1 to 8)
+    const int lane = threadIdx.x & 31;
+    const uint32_t first = stage + unit_at<F, D>(lane * 16 / kRow, lane * 16 % kRow / 16);
+    src += lane * 16;
+#pragma unroll
+    for (int i = 0; i < kBlockSize / kRows; ++i) {
+        constexpr bool kPlain = F != PA_KV_F16 && D == 64;  // 8 rows a pass: nothing changes
+        const uint32_t at = kPlain ? first + i * 512 : (first ^ ((kRows * i & 7) << 4)) + kRows * i * 128;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src + 512 * i) : "memory");
+    }
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the latest N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Halves of the four bytes of w: bytes 0 and 1, bytes 2 and 3.  INT8 bytes come
@@ -339,7 +364,6 @@ __device__ __forceinline__ void block_update(WarpState<D>& st, const uint32_t (&
         for (int u = lane; u < (kBlockSize - nvalid) * kUnits; u += 32)
             *reinterpret_cast<uint4*>(vgen + unit_at<F, D>(nvalid + u / kUnits, u % kUnits)) =
                 make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
     }
 
@@ -382,32 +406,29 @@ __device__ __forceinline__ void block_update(WarpState<D>& st, const uint32_t (&
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <int F, int D, int NS>
 __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
-    kv_partition_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                        const KvDecodeParams prm) {
+    kv_partition_kernel(const KvDecodeParams prm) {
     using S = KvShape<F, D, NS>;
     constexpr int NW = S::kNW;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kArea);
-    float* sm_m = reinterpret_cast<float*>(bars + NW * NS);
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* sm_m = reinterpret_cast<float*>(smem + S::kArea);
     float* sm_l = sm_m + NW * kMaxGroup;
-    int* sm_abort = reinterpret_cast<int*>(sm_l + NW * kMaxGroup);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t stage0 = smem_addr(smem) + warp * NS * S::kStage;
-    const uint32_t bar0 = smem_addr(bars) + warp * NS * 8;
+    uint8_t* const my_stages = smem + warp * NS * S::kStage;
+    const uint32_t stage0 = smem_addr(my_stages);
 
-    if (threadIdx.x == 0) {
-        *sm_abort = 0;
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    // While the preceding kernel ends: the lengths and the block tables on
+    // their way to L2 (a hint; they are read after the wait).
+    {
+        const size_t cta = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+        const size_t line = (cta * blockDim.x + threadIdx.x) * 128;
+        const size_t lens = (size_t)prm.num_seqs * 4, tables = lens * prm.max_blocks_per_seq;
+        if (line < tables) prefetch_l2(reinterpret_cast<const char*>(prm.block_tables) + line);
+        if (line < lens) prefetch_l2(reinterpret_cast<const char*>(prm.seq_lens) + line);
     }
-    if (lane == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -513,35 +534,34 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         }
     };
     uint32_t valid_bits = 0;  // stage s holds a block with a legal id
-    // Copy the block of the batch's lane k into the stage of the warp's n-th block.
+    // Start copying the block of the batch's lane k into the stage of the
+    // warp's n-th block.  Every block's copies are one group, and after the
+    // first NS of a segment one group (it may be empty) follows each block
+    // consumed, so the block at hand is in all but the latest NS - 1.
     auto copy = [&](int n, int k) {
         const int phys = __shfl_sync(kFull, ids, k);
         const int s = n % NS;
-        const uint32_t bar = bar0 + 8 * s;
         const bool ok = phys >= 0 && (long long)phys < prm.num_blocks;
         valid_bits = ok ? (valid_bits | (1u << s)) : (valid_bits & ~(1u << s));
-        if (lane == 0) {
-            if (ok) {
-                mbar_arrive_expect_tx(bar, S::kStage);
-                const int row = (phys * prm.num_kv_heads + kvh) * kBlockSize;
-                const uint32_t kdst = stage0 + s * S::kStage;
-                tma_load_3d(kdst, &tmap_k, 0, row, 0, bar);
-                tma_load_3d(kdst + S::kTile, &tmap_v, 0, row, 0, bar);
-            } else {
-                atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
-                mbar_arrive(bar);  // complete the phase so the wait below stays in step
-            }
+        if (ok) {
+            const size_t at = ((size_t)phys * prm.num_kv_heads + kvh) * S::kTile;
+            copy_tile<F, D>(stage0 + s * S::kStage, prm.k_cache + at);
+            copy_tile<F, D>(stage0 + s * S::kStage + S::kTile, prm.v_cache + at);
+        } else if (lane == 0) {
+            atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
         }
     };
 
     int done = 0;    // blocks this warp has consumed in earlier segments
-    int issued = 0;  // copies of this segment that are on their way
+    int issued = 0;  // blocks of this segment that are on their way
     load_ids(b, j0 + lane * stride, lane < cnt, ids_early);
-    for (; issued < NS && issued < cnt; ++issued) copy(issued, issued);
+    for (int k = 0; k < NS; ++k) {
+        if (k < cnt) copy(k, k), ++issued;
+        copies_commit();
+    }
 
     uint32_t qb[D / 16][2];
     WarpState<D> st;
-    bool timed_out = false;
     for (;;) {
         const int L = length(b);
         if (prm.flat && j0 == 0 && kvh == 0 && lane == 0 && cnt > 0) {
@@ -581,14 +601,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         int issued_next = 0;
 
         for (int i = 0; i < cnt; ++i) {
-            const int n = done + i, s = n % NS;
-            if (prm.force_timeout || !mbar_wait(bar0 + 8 * s, (n / NS) & 1, prm.wait_limit)) {
-                // wait for this warp's copies still in flight before it may leave
-                for (int k = n; k < done + issued + issued_next; ++k)
-                    mbar_wait(bar0 + 8 * (k % NS), (k / NS) & 1, kDefaultWaitLimit);
-                timed_out = true;
-                break;
-            }
+            const int s = (done + i) % NS;
+            copies_wait<NS - 1>();
+            __syncwarp();
             // copy i has been issued, and none of the next batch or sequence
             if ((i & 31) == 0) ks_c = ks_i, vs_c = vs_i;
             if ((valid_bits >> s) & 1u) {
@@ -596,7 +611,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
                 const uint32_t kst = stage0 + s * S::kStage;
                 const float ks = F == PA_KV_F16 ? prm.scale_log2 : prm.scale_log2 * __shfl_sync(kFull, ks_c, i & 31);
                 const float vs = F == PA_KV_F16 ? 1.f : __shfl_sync(kFull, vs_c, i & 31);
-                block_update<F, D>(st, qb, kst, kst + S::kTile, smem + (kst + S::kTile - smem_addr(smem)),
+                block_update<F, D>(st, qb, kst, kst + S::kTile, my_stages + s * S::kStage + S::kTile,
                                    min(kBlockSize, L - tok0), ks, vs, scores ? scores + tok0 : nullptr,
                                    prm.score_stride, two);
             }
@@ -614,13 +629,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
                 copy(done + cnt + issued_next, issued_next);
                 ++issued_next;
             }
-        }
-        if (timed_out) {
-            if (lane == 0) {
-                atomicOr(prm.status, PA_DEV_TIMEOUT);
-                atomicExch(sm_abort, 1);
-            }
-            if (!whole) return;
+            copies_commit();
         }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
@@ -677,11 +686,13 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         cnt = cnt_next;
         issued = issued_next;
         if (issued == 0) load_ids(b, lane, lane < cnt, -1);
-        for (; issued < NS && issued < cnt; ++issued) copy(done + issued, issued);
+        for (int k = issued_next; k < NS; ++k) {
+            if (k < cnt) copy(done + k, k), ++issued;
+            copies_commit();
+        }
     }
 
     __syncthreads();  // all stages consumed; the area is reused below
-    if (*sm_abort) return;
 
     // Merge the warps' states: every warp leaves (m, l, O) in shared memory,
     // then warp w merges dims [w D/NW, (w+1) D/NW) of every head, the sums in
@@ -762,8 +773,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int L = __ldg(prm.seq_lens + b);
     // Partial p of the sequence is slot at(p).  seq_parts is not written for an
-    // empty sequence (and then not used) nor after a timeout: the clamps keep the
-    // reads inside the workspace.
+    // empty sequence (and then not used).
     int n, n0 = 0, n1 = 0;
     long long s0 = 0, s1 = 0, s2 = 0;
     if (prm.flat) {
@@ -891,15 +901,16 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
 }
 
 template <int F, int D>
-cudaError_t launch_fd(const KvDecodeParams& prm, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
-                      cudaStream_t stream) {
+cudaError_t launch_fd(const KvDecodeParams& prm, dim3 grid, cudaStream_t stream) {
     constexpr int NS = stages_of<F, D>();
     using S = KvShape<F, D, NS>;
     static_assert(ctas_of<F, D>() * (S::kSmem + 1024 + 64) <= 228 * 1024, "shared memory of an SM");
     static std::atomic<unsigned long long> done{0};
     auto kern = kv_partition_kernel<F, D, NS>;
-    cudaError_t e = once_per_device(
-        done, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem); });
+    cudaError_t e = once_per_device(done, [&] {
+        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -909,7 +920,7 @@ cudaError_t launch_fd(const KvDecodeParams& prm, const CUtensorMap& tk, const CU
     cudaLaunchAttribute attr = pdl_attribute();
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tk, tv, prm);
+    return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
 }  // namespace
@@ -926,13 +937,24 @@ int kv_decode_ctas(int format, int head_dim) {
     return -1;
 }
 
-cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, const CUtensorMap& tk,
-                             const CUtensorMap& tv, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, dim3 grid, cudaStream_t stream) {
 #define PA_CASE(F_, D_) \
-    if (format == F_ && head_dim == D_) return launch_fd<F_, D_>(prm, tk, tv, grid, stream);
+    if (format == F_ && head_dim == D_) return launch_fd<F_, D_>(prm, grid, stream);
     PA_KV_FOR_FD(PA_CASE)
 #undef PA_CASE
     return cudaErrorInvalidValue;
+}
+
+// The merge asks for the decode kernel's division of an SM's memory although
+// it needs little shared memory itself: while an SM is divided otherwise, fewer
+// of the next decode's CTAs fit on it, and the rest would run as a second wave.
+template <int D>
+cudaError_t launch_merge_d(const cudaLaunchConfig_t& cfg, const KvMergeParams& prm) {
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kv_merge_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    });
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, prm);
 }
 
 cudaError_t launch_kv_merge(int head_dim, const KvMergeParams& prm, dim3 grid, cudaStream_t stream) {
@@ -944,9 +966,9 @@ cudaError_t launch_kv_merge(int head_dim, const KvMergeParams& prm, dim3 grid, c
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     switch (head_dim) {
-        case 64: return cudaLaunchKernelEx(&cfg, kv_merge_kernel<64>, prm);
-        case 128: return cudaLaunchKernelEx(&cfg, kv_merge_kernel<128>, prm);
-        case 256: return cudaLaunchKernelEx(&cfg, kv_merge_kernel<256>, prm);
+        case 64: return launch_merge_d<64>(cfg, prm);
+        case 128: return launch_merge_d<128>(cfg, prm);
+        case 256: return launch_merge_d<256>(cfg, prm);
         default: return cudaErrorInvalidValue;
     }
 }
