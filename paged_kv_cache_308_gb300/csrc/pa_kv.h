@@ -51,7 +51,7 @@ struct KvMergeParams {
     const int32_t* seq_lens;
     long long score_stride, weights_stride, slots;
     int num_heads, num_kv_heads, group, max_seq_len;
-    int slices;  // blocks of a (sequence, kv head) that merge; the rest add weights
+    int slices, cols;  // blocks of a (sequence, kv head) that merge, and their columns; the rest add weights
     int flat, partition_size, max_partitions;
     unsigned int* status;
 };

@@ -55,18 +55,32 @@ struct DecodePlan {
     long long slots;            // partials of a kv head
 };
 
-// Sequences of up to this many tokens take one CTA each and no merge; one
-// sequence takes a wave of equal partitions (whose block ids can be read before
-// its length is known), a batch equal shares of its blocks for the CTAs the
-// SMs hold at once.
-constexpr int kSingleMaxLen = 128;
+// Which form (us per call on GB300, e4m3, flat shares against one CTA per
+// sequence and kv head):
+// * up to kSingleMaxLen tokens one CTA each, with no merge: 2 x 512 tokens of 8
+//   x 128: 8.0 against 7.1, 8 x 256 8.5 / 4.7, 32 x 512 15.5 / 11.9, 128 x 512
+//   34.0 / 30.7, 512 x 256 63.5 / 59.3; 4 x 256 likewise (2 x 512: 8.7 / 8.8);
+// * up to kSingleManyMaxLen where the pairs nearly fill the SMs: 32 x 1024 of 8
+//   x 128 19.5 / 19.0, of 4 x 256 20.6 / 17.4; 128 x U[1, 1024] 34.3 / 33.4; with
+//   few pairs the flat form wins there (8 x 1024: 11.3 / 13.0);
+// * one sequence: a wave of equal partitions, whose block ids can be read before
+//   its length is known;
+// * other batches: equal shares for the CTAs the SMs hold at once (against the
+//   best of partitions of 256 to 8192 tokens: 64 log-uniform up to 8192 26.0 /
+//   33.2, 8 x U[1, 8192] 18.1 / 18.7, 64 x U[1, 4096] 60.9 / 60.9, 16 x 16384 93.8 /
+//   91.3, 64 x 2048 52.7 / 53.9).
+// A caller's partition size gives the grid of partitions.
+constexpr int kSingleOneMaxLen = 128, kSingleMaxLen = 512, kSingleManyMaxLen = 1024;
 
 DecodePlan plan_decode(int num_seqs, int max_seq_len, int num_kv_heads, int head_dim, int format, int num_sms,
                        int partition_size, int mode) {
     DecodePlan p{};
     const int whole = std::max(1, blocks_of(max_seq_len)) * pa::kBlockSize;
-    if (mode == PA_MODE_SINGLE || (partition_size <= 0 && mode == PA_MODE_AUTO && max_seq_len <= kSingleMaxLen))
+    const bool many = (long long)num_seqs * num_kv_heads * 4 >= num_sms * 3ll;
+    if (mode == PA_MODE_SINGLE || (partition_size <= 0 && mode == PA_MODE_AUTO && num_seqs > 1 &&
+                                   max_seq_len <= (many ? kSingleManyMaxLen : kSingleMaxLen)))
         partition_size = whole;
+    if (partition_size <= 0 && mode == PA_MODE_AUTO && max_seq_len <= kSingleOneMaxLen) partition_size = whole;
     const long long slots = std::max(1ll, (long long)pa::kv_decode_ctas(format, head_dim) * num_sms / num_kv_heads);
     if (partition_size <= 0 && num_seqs == 1)  // (one block per warp at least)
         partition_size =
@@ -101,15 +115,13 @@ DecodeSpace decode_space(const DecodePlan& p, int num_seqs, int num_heads, int n
     return s;
 }
 
-// Blocks that merge one (sequence, kv head): about two per SM over the batch,
-// a power of two that leaves each at least 8 and at most 256 columns of four.
-int merge_slices(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_sms) {
-    const int cols = num_heads / num_kv_heads * (head_dim / 4);
-    int s = 1;
-    while (cols / s > 256) s *= 2;
-    while ((long long)num_seqs * num_kv_heads * s < 2ll * num_sms && head_dim / 4 % (2 * s) == 0 && cols / (2 * s) >= 8)
-        s *= 2;
-    return s;
+// Columns of four of a merging block: a power of two, so many that the batch
+// gives about two blocks per SM.
+int merge_cols(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_sms) {
+    const int total = num_heads / num_kv_heads * (head_dim / 4);
+    int cols = 256;
+    while (cols > 8 && (long long)num_seqs * num_kv_heads * ((total + cols - 1) / cols) < 2ll * num_sms) cols /= 2;
+    return cols;
 }
 
 int check_decode(const pa_kv_decode_args* a, const pa_decode_opts* o) {
@@ -204,7 +216,8 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     m.num_kv_heads = c.num_kv_heads;
     m.group = p.group;
     m.max_seq_len = a->max_seq_len;
-    m.slices = split ? merge_slices(a->num_seqs, a->num_heads, c.num_kv_heads, c.head_dim, num_sms) : 0;
+    m.cols = merge_cols(a->num_seqs, a->num_heads, c.num_kv_heads, c.head_dim, num_sms);
+    m.slices = split ? (p.group * c.head_dim / 4 + m.cols - 1) / m.cols : 0;
     m.flat = plan.flat;
     m.partition_size = plan.partition_size;
     m.max_partitions = plan.parts;

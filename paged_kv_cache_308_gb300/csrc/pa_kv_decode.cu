@@ -63,7 +63,7 @@ namespace pa {
 namespace {
 
 constexpr float kShift = 14.f;
-constexpr int kLead = 2;  // units a sequence counts beyond its blocks
+constexpr int kLead = 6;  // units a sequence counts beyond its blocks
 
 // The flat form's runs: `ctas` of them over `units` units, q each and one more
 // for the first r, at least kMinUnits long while there are as many units.
@@ -234,6 +234,17 @@ constexpr int ctas_of() {
     return F == PA_KV_F16 ? (D == 256 ? 1 : D == 128 ? 2 : 3) : (D == 256 ? 2 : D == 128 ? 3 : 5);
 }
 
+// Scores are read again by the next kernel: K and V passing through L2 should
+// not push them out.
+__device__ __forceinline__ uint64_t keep_in_l2() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void store_kept(float* p, float v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(p), "f"(v), "l"(policy) : "memory");
+}
+
 // A warp's online softmax over the heads of a kv head: lane (g, c) of an MMA
 // fragment holds heads 2c and 2c + 1.
 template <int D>
@@ -306,13 +317,14 @@ __device__ __forceinline__ void block_update(WarpState<D>& st, const uint32_t (&
         s[x] = v * ks;
     }
     if (score0) {
+        const uint64_t keep = keep_in_l2();
         if (g < nvalid) {
-            score0[g] = s[0];
-            if (two) score0[score_stride + g] = s[1];
+            store_kept(score0 + g, s[0], keep);
+            if (two) store_kept(score0 + score_stride + g, s[1], keep);
         }
         if (g + 8 < nvalid) {
-            score0[g + 8] = s[2];
-            if (two) score0[score_stride + g + 8] = s[3];
+            store_kept(score0 + g + 8, s[2], keep);
+            if (two) store_kept(score0 + score_stride + g + 8, s[3], keep);
         }
     }
     if (g >= nvalid) s[0] = s[1] = -INFINITY;  // tokens past the end are excluded
@@ -757,13 +769,32 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     if (warp == 0 && qd == 0 && prm.sums) prm.sums[pi] = make_float2(Mh - kShift, Lh);
 }
 
-// Blocks x < slices of a (sequence, kv head): slice x of the merge of its
-// partials; the rest: kWeightsTokens tokens of the weights each.
+// Blocks x < slices of a (sequence, kv head): `cols` float4 columns of the
+// merge of its partials each; the rest: kKvWeightsTokens tokens of the weights
+// each.  Both are chains of a few loads; each link loads all it can at once.
 constexpr int kMergeThreads = 256;
 constexpr int kPerThread = kKvWeightsTokens / kMergeThreads;
 
+// Exponent reference, sum and weighted columns of some partials; empty: m = -inf.
+struct MergeState {
+    float m = -INFINITY, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    // with a partial's normalised columns t (beta: its weight) or another state's (beta: 2^(m - m'))
+    __device__ __forceinline__ void add(float mo, float lo, const float4& t, float scale) {
+        const float mn = fmaxf(m, mo);
+        const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn), f = mo == -INFINITY ? 0.f : exp2f(mo - mn);
+        const float beta = f * scale;
+        l = l * alpha + lo * f;
+        a.x = a.x * alpha + beta * t.x;
+        a.y = a.y * alpha + beta * t.y;
+        a.z = a.z * alpha + beta * t.z;
+        a.w = a.w * alpha + beta * t.w;
+        m = mn;
+    }
+};
+
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergeParams prm) {
+__global__ void __launch_bounds__(kMergeThreads, 4) kv_merge_kernel(const KvMergeParams prm) {
     __shared__ float4 red[kMergeThreads];
     __shared__ float2 red_ml[kMergeThreads];
     __shared__ float lse[kMaxGroup];
@@ -792,66 +823,62 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
         n0 = n;
         s0 = (long long)b * prm.max_partitions;
     }
-    const size_t head_slots = (size_t)(kvh * prm.slots);
-    auto at = [&](int p) { return head_slots + (size_t)(p + (p < n0 ? s0 : p < n0 + n1 ? s1 : s2)); };
     const bool merge = (int)blockIdx.x < prm.slices;
     if (L < 0 || L > prm.max_seq_len) {
         if (blockIdx.x == 0 && kvh == 0 && tid == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return;
     }
+    const size_t head_slots = (size_t)(kvh * prm.slots);
+    auto at = [&](int p) { return head_slots + (size_t)(p + (p < n0 ? s0 : p < n0 + n1 ? s1 : s2)); };
+    constexpr int kAtOnce = 3;  // partials of a thread in flight
     if (merge) {
-        // float4 column `col` of the G D outputs, by `groups` groups of threads
-        // that take every groups-th partial
-        const int cols = G * (D / 4) / prm.slices;
-        const int groups = kMergeThreads / cols;
-        const int col = blockIdx.x * cols + tid % cols, grp = tid / cols;
+        // column `col` of the G D / 4, by `groups` groups of threads that take
+        // every groups-th partial; cols is a power of two
+        const int cols = prm.cols, groups = kMergeThreads / cols;
+        const int col = blockIdx.x * cols + (tid & (cols - 1)), grp = tid / cols;
+        const bool in = col < G * (D / 4);
         __half* out = prm.out + ((size_t)b * prm.num_heads + (size_t)kvh * G) * D;
         if (L == 0) {  // no tokens: zero
-            if (grp == 0) *reinterpret_cast<uint2*>(out + 4 * col) = make_uint2(0u, 0u);
+            if (grp == 0 && in) *reinterpret_cast<uint2*>(out + 4 * col) = make_uint2(0u, 0u);
             return;
         }
         if (n <= 1) return;  // written by the partition kernel
-        const int h = col / (D / 4);
-        float m = -INFINITY, l = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (grp < groups) {
-            const float4* acc = reinterpret_cast<const float4*>(prm.acc) + col;
-#pragma unroll 4
-            for (int p = grp; p < n; p += groups) {
-                const size_t row = at(p) * G;
-                const float2 ml = prm.sums[row + h];
-                const float4 t = acc[row * (D / 4)];
-                const float mn = fmaxf(m, ml.x);
-                const float alpha = exp2f(m - mn), beta = ml.y * exp2f(ml.x - mn);
-                l = l * alpha + beta;
-                a.x = a.x * alpha + beta * t.x;
-                a.y = a.y * alpha + beta * t.y;
-                a.z = a.z * alpha + beta * t.z;
-                a.w = a.w * alpha + beta * t.w;
-                m = mn;
+        const int h = in ? col / (D / 4) : 0;
+        MergeState st;
+        const float4* acc = reinterpret_cast<const float4*>(prm.acc) + (in ? col : 0);
+        for (int p = grp; p < n; p += kAtOnce * groups) {
+            float2 ml[kAtOnce];
+            float4 t[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int q = p + k * groups;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                t[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q < n) {
+                    const size_t row = at(q) * G;
+                    ml[k] = prm.sums[row + h];
+                    t[k] = acc[row * (D / 4)];
+                }
             }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) st.add(ml[k].x, ml[k].y, t[k], ml[k].y);
         }
-        red[tid] = a;
-        red_ml[tid] = make_float2(m, l);
+        // the groups of a warp, then the warps
+        for (int off = cols; off < 32; off <<= 1) {
+            const float mo = __shfl_xor_sync(kFull, st.m, off), lo = __shfl_xor_sync(kFull, st.l, off);
+            const float4 t = make_float4(__shfl_xor_sync(kFull, st.a.x, off), __shfl_xor_sync(kFull, st.a.y, off),
+                                         __shfl_xor_sync(kFull, st.a.z, off), __shfl_xor_sync(kFull, st.a.w, off));
+            st.add(mo, lo, t, 1.f);
+        }
+        red[tid] = st.a;
+        red_ml[tid] = make_float2(st.m, st.l);
         __syncthreads();
-        if (grp == 0) {
-            float M = m;
-            for (int q = 1; q < groups; ++q) M = fmaxf(M, red_ml[q * cols + tid].x);
-            float w = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int q = 0; q < groups; ++q) {
-                const float2 ml = red_ml[q * cols + tid];
-                const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);  // a group without partials
-                const float4 t = red[q * cols + tid];
-                w += f * ml.y;
-                o.x += f * t.x;
-                o.y += f * t.y;
-                o.z += f * t.z;
-                o.w += f * t.w;
-            }
-            const float inv = 1.f / w;
-            const __half2 v[2] = {__floats2half2_rn(o.x * inv, o.y * inv), __floats2half2_rn(o.z * inv, o.w * inv)};
+        if (grp == 0 && in) {
+            const int step = max(cols, 32);  // the first group of every warp (or every group)
+            for (int q = tid + step; q < kMergeThreads; q += step) st.add(red_ml[q].x, red_ml[q].y, red[q], 1.f);
+            const float inv = 1.f / st.l;
+            const __half2 v[2] = {__floats2half2_rn(st.a.x * inv, st.a.y * inv),
+                                  __floats2half2_rn(st.a.z * inv, st.a.w * inv)};
             *reinterpret_cast<uint2*>(out + 4 * col) = *reinterpret_cast<const uint2*>(v);
         }
         return;
@@ -871,21 +898,20 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const KvMergePa
             s[k][h] = h < G && t < L ? prm.scores[(head0 + h) * prm.score_stride + t] : -INFINITY;
     }
     if (warp < G) {  // 8 warps, at most 8 heads
-        float m = -INFINITY, l = 0.f;
-        for (int p = lane; p < n; p += 32) {
-            const float2 ml = prm.sums[at(p) * G + warp];
-            const float mn = fmaxf(m, ml.x);
-            l = l * exp2f(m - mn) + ml.y * exp2f(ml.x - mn);
-            m = mn;
+        MergeState st;
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = lane; p < n; p += 32 * kAtOnce) {
+            float2 ml[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                ml[k] = p + 32 * k < n ? prm.sums[at(p + 32 * k) * G + warp] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) st.add(ml[k].x, ml[k].y, none, 0.f);
         }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const float mo = __shfl_xor_sync(kFull, m, off), lo = __shfl_xor_sync(kFull, l, off);
-            const float mn = fmaxf(m, mo);
-            l = (m == -INFINITY ? 0.f : l * exp2f(m - mn)) + (mo == -INFINITY ? 0.f : lo * exp2f(mo - mn));
-            m = mn;
-        }
-        if (lane == 0) lse[warp] = m + log2f(l);
+        for (int off = 16; off > 0; off >>= 1)
+            st.add(__shfl_xor_sync(kFull, st.m, off), __shfl_xor_sync(kFull, st.l, off), none, 0.f);
+        if (lane == 0) lse[warp] = st.m + log2f(st.l);
     }
     __syncthreads();
 #pragma unroll
