@@ -227,7 +227,7 @@ __device__ __forceinline__ int out_dim(int mt, int g, int hi) {
 // thread) and 228 KB of shared memory.
 template <int F, int D>
 constexpr int stages_of() {
-    return F == PA_KV_F16 ? (D == 256 ? 2 : D == 128 ? 3 : 4) : (D == 256 ? 3 : 4);
+    return F == PA_KV_F16 ? (D == 64 ? 4 : 3) : (D == 256 ? 3 : 4);
 }
 template <int F, int D>
 constexpr int ctas_of() {
@@ -793,7 +793,8 @@ struct MergeState {
     }
 };
 
-template <int D>
+// GW: a bound on the heads of a kv head, for the weights' registers.
+template <int D, int GW>
 __global__ void __launch_bounds__(kMergeThreads, 4) kv_merge_kernel(const KvMergeParams prm) {
     __shared__ float4 red[kMergeThreads];
     __shared__ float2 red_ml[kMergeThreads];
@@ -886,16 +887,16 @@ __global__ void __launch_bounds__(kMergeThreads, 4) kv_merge_kernel(const KvMerg
     const int t0 = ((int)blockIdx.x - prm.slices) * kKvWeightsTokens + tid;
     if (t0 - tid >= L) return;
     // the tokens' scores and old weights are on their way while the sums are added up
-    const size_t head0 = (size_t)b * prm.num_heads + (size_t)kvh * G;
-    const size_t row = ((size_t)b * prm.num_kv_heads + kvh) * prm.weights_stride;
-    float s[kPerThread][kMaxGroup], w[kPerThread];
+    const float* sc = prm.scores + ((size_t)b * prm.num_heads + (size_t)kvh * G) * prm.score_stride + t0;
+    const size_t row = ((size_t)b * prm.num_kv_heads + kvh) * prm.weights_stride + t0;
+    float s[kPerThread][GW], w[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-        const int t = t0 + k * kMergeThreads;
-        w[k] = t < L && prm.weights_in ? prm.weights_in[row + t] : 0.f;
+        const bool in = t0 + k * kMergeThreads < L;
+        w[k] = in && prm.weights_in ? prm.weights_in[row + k * kMergeThreads] : 0.f;
+        const float* from = sc + k * kMergeThreads;
 #pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h)
-            s[k][h] = h < G && t < L ? prm.scores[(head0 + h) * prm.score_stride + t] : -INFINITY;
+        for (int h = 0; h < GW; ++h, from += prm.score_stride) s[k][h] = h < G && in ? *from : -INFINITY;
     }
     if (warp < G) {  // 8 warps, at most 8 heads
         MergeState st;
@@ -914,15 +915,15 @@ __global__ void __launch_bounds__(kMergeThreads, 4) kv_merge_kernel(const KvMerg
         if (lane == 0) lse[warp] = st.m + log2f(st.l);
     }
     __syncthreads();
+    float by[GW];
+#pragma unroll
+    for (int h = 0; h < GW; ++h) by[h] = h < G ? lse[h] : 0.f;  // (absent heads: 2^-inf = 0)
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-        const int t = t0 + k * kMergeThreads;
-        if (t >= L) break;
         float sum = 0.f;
 #pragma unroll
-        for (int h = 0; h < kMaxGroup; ++h)
-            if (h < G) sum += exp2f(s[k][h] - lse[h]);
-        prm.weights_out[row + t] = w[k] + sum;
+        for (int h = 0; h < GW; ++h) sum += pow2_of(s[k][h] - by[h]);
+        if (t0 + k * kMergeThreads < L) prm.weights_out[row + k * kMergeThreads] = w[k] + sum;
     }
 }
 
@@ -974,13 +975,21 @@ cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm
 // The merge asks for the decode kernel's division of an SM's memory although
 // it needs little shared memory itself: while an SM is divided otherwise, fewer
 // of the next decode's CTAs fit on it, and the rest would run as a second wave.
-template <int D>
-cudaError_t launch_merge_d(const cudaLaunchConfig_t& cfg, const KvMergeParams& prm) {
+template <int D, int GW>
+cudaError_t launch_merge_dg(const cudaLaunchConfig_t& cfg, const KvMergeParams& prm) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = once_per_device(done, [&] {
-        return cudaFuncSetAttribute(kv_merge_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        return cudaFuncSetAttribute(kv_merge_kernel<D, GW>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     });
-    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, prm);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, GW>, prm);
+}
+
+template <int D>
+cudaError_t launch_merge_d(const cudaLaunchConfig_t& cfg, const KvMergeParams& prm) {
+    if (prm.group == 1) return launch_merge_dg<D, 1>(cfg, prm);
+    if (prm.group == 2) return launch_merge_dg<D, 2>(cfg, prm);
+    if (prm.group <= 4) return launch_merge_dg<D, 4>(cfg, prm);
+    return launch_merge_dg<D, 8>(cfg, prm);
 }
 
 cudaError_t launch_kv_merge(int head_dim, const KvMergeParams& prm, dim3 grid, cudaStream_t stream) {
