@@ -617,13 +617,16 @@ def _workspace(workspace, nbytes, dev, stream):
 
 def _call(what, dev, stream, fn, *args):
     """Call fn(*args, stream) with the tensors' device current; None is that device's current stream."""
-    prev = torch.cuda.current_device()
-    if prev != dev:
+    # (what torch.cuda.current_device and current_stream read, without building objects)
+    prev = torch._C._cuda_getDevice()
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    if prev == dev:
+        rc = fn(*args, handle)
+    else:
         torch.cuda.set_device(dev)
-    try:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream_handle(stream))
-    finally:
-        if prev != dev:
+        try:
+            rc = fn(*args, handle)
+        finally:
             torch.cuda.set_device(prev)
     if rc != PA_OK:
         raise PaDecodeError(rc, what)
@@ -687,15 +690,14 @@ def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq
     if partition_size or mode != "auto":
         opts = ctypes.byref(make_opts(mode=mode, partition_size=partition_size))
 
-    def run(stream_handle):
-        need = 0
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):  # (the plan goes by the device's SMs)
             need = lib.pa_kv_decode_workspace_size(B, max_seq_len, H, hkv, dim, cache[8], int(partition_size),
                                                    int(wout != 0))
-        ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
-        return lib.pa_kv_decode(args, opts, ptr, nbytes, stream_handle)
-
-    _call("pa_kv_decode", dev, stream, run)
+        ptr, nbytes, _hold = _workspace(None, need, dev, stream)
+    else:
+        ptr, nbytes, _hold = _workspace(workspace, 0, dev, stream)
+    _call("pa_kv_decode", dev, stream, lib.pa_kv_decode, args, opts, ptr, nbytes)
 
 
 def pa_kv_prefix_workspace_size(num_seqs, max_context_len, num_kv_heads, head_dim, dtype) -> int:

@@ -349,27 +349,38 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
     }
     const size_t bh = (size_t)phys * prm.num_kv_heads + kvh;
     const uint4* src = reinterpret_cast<const uint4*>(of_kv(prm.cache, kv) + bh * kBlockSize * D) + lane;
-    uint4 x[kPasses];
+    // through shared memory, each lane its own pieces: every load in flight
+    // without a register (held in registers, the compiler took one or two at a
+    // time: 43 us for 4 x 8192 tokens of 4 x 256)
+    __shared__ uint4 held[2][kPasses][32];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) x[i] = load_ahead(src + 32 * i);
+    for (int i = 0; i < kPasses; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(&held[kv][i][lane])), "l"(src + 32 * i)
+                     : "memory");
     const float s = __ldg(of_kv(prm.scales, kv) + bh);
-    uint4* dst = reinterpret_cast<uint4*>(of_kv(prm.expanded, kv) + ((size_t)to * prm.num_kv_heads + kvh) * kBlockSize * D);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    uint8_t* dst = reinterpret_cast<uint8_t*>(of_kv(prm.expanded, kv) +
+                                              ((size_t)to * prm.num_kv_heads + kvh) * kBlockSize * D);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
+        const uint4 x = held[kv][i][lane];
+        uint32_t h[8];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float f[8];
-            values8<F>(j ? make_uint2(x[i].z, x[i].w) : make_uint2(x[i].x, x[i].y), f);
-            __half2 h[4];
+            values8<F>(j ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y), f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 // saturated; NaN stays NaN
                 const float a = f[2 * k] * s, c = f[2 * k + 1] * s;
-                h[k] = __hmax2_nan(__hmin2_nan(__floats2half2_rn(a, c), __float2half2_rn(65504.f)),
-                                   __float2half2_rn(-65504.f));
+                h[4 * j + k] = half2_bits(__hmax2_nan(
+                    __hmin2_nan(__floats2half2_rn(a, c), __float2half2_rn(65504.f)), __float2half2_rn(-65504.f)));
             }
-            dst[2 * (32 * i + lane) + j] = *reinterpret_cast<const uint4*>(h);
         }
+        // a lane's 32 bytes in one store: as two of 16 each would write half a sector
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 32 * (32 * i + lane)),
+                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                     : "memory");
     }
 }
 
@@ -468,17 +479,20 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     };
 
     // sinks and recent ones keep their order around the rest
-    for (int i = rank * kEvictThreads + tid; i < plan.sinks; i += CS * kEvictThreads) put(i, i);
-    for (int i = rank * kEvictThreads + tid; i < plan.recent; i += CS * kEvictThreads)
-        put(k - plan.recent + i, L - plan.recent + i);
+    auto put_protected = [&]() {
+        for (int i = rank * kEvictThreads + tid; i < plan.sinks; i += CS * kEvictThreads) put(i, i);
+        for (int i = rank * kEvictThreads + tid; i < plan.recent; i += CS * kEvictThreads)
+            put(k - plan.recent + i, L - plan.recent + i);
+    };
 
     // this block's stretch of the tokens between them
     const int m0 = plan.sinks, m1 = L - plan.recent, mid = m1 - m0;
     const int each = (mid + CS - 1) / CS;
     const int t0 = min(m1, m0 + rank * each), n = min(m1 - t0, each);
     unsigned need = (unsigned)(k - plan.recent - plan.sinks);  // of the mid tokens
-    if (need == 0) return;                                      // the same for the whole cluster
-    if (need == (unsigned)mid) {                                // all of them: L <= the budget
+    if (need == 0 || need == (unsigned)mid) put_protected();
+    if (need == 0) return;        // the same for the whole cluster
+    if (need == (unsigned)mid) {  // all of them: L <= the budget
         for (int i = tid; i < n; i += kEvictThreads) put(t0 + i, t0 + i);
         return;
     }
@@ -529,7 +543,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
                     if ((k4[j] & mask) == T) atomicAdd(h + ((k4[j] >> shift) & (bins - 1)), 1u);
             }
         }
-        cluster.sync();
+        cluster.barrier_arrive();
+        if (round == 0) put_protected();  // while the others arrive
+        cluster.barrier_wait();
         // bins in descending order: thread i has bins 2 i and 2 i + 1 from the top
         unsigned v[2] = {0u, 0u};
         if (2 * tid < bins) {
