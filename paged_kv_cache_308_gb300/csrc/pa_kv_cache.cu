@@ -634,14 +634,17 @@ __global__ void __launch_bounds__(64) kv_evict_move_kernel(const KvEvictParams p
     asm volatile("griddepcontrol.launch_dependents;");
     const int kv = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blk = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    const size_t row = (size_t)b * prm.num_kv_heads + kvh;
+    // what the lengths allow is known later: these loads stay inside the arrays
+    const int i = blk * kBlockSize + (lane & (kBlockSize - 1));
+    const int t = i < prm.max_keep_len ? prm.kept[row * prm.max_keep_len + i] : 0;
+    const int to = __ldg(prm.dst_block_tables + (size_t)b * prm.dst_max_blocks_per_seq + blk);
     const KeepPlan plan(prm, b);
     if (plan.bad || blk * kBlockSize >= plan.k) return;
     const int n = min(kBlockSize, plan.k - blk * kBlockSize);
-    const size_t row = (size_t)b * prm.num_kv_heads + kvh;
     // lane r < 16: where the block's r-th row comes from
     int from = -1, slot = 0;
     if (lane < n) {
-        const int t = prm.kept[row * prm.max_keep_len + blk * kBlockSize + lane];
         slot = t % kBlockSize;
         from = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + t / kBlockSize);
         if (from < 0 || (long long)from >= prm.src_blocks) {
@@ -649,7 +652,6 @@ __global__ void __launch_bounds__(64) kv_evict_move_kernel(const KvEvictParams p
             from = -1;
         }
     }
-    const int to = __ldg(prm.dst_block_tables + (size_t)b * prm.dst_max_blocks_per_seq + blk);
     if (to < 0 || (long long)to >= prm.dst_blocks) {
         if (lane == 0) atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
         return;
