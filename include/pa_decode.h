@@ -580,9 +580,9 @@ int pa_kv_append(const pa_kv_append_args* args, pa_stream_t stream);
  * Entries from seq_lens[b] on are neither read nor written.
  * Of the options partition_size and mode AUTO, SINGLE and SPLIT apply (no wait
  * of this call can run out).  The workspace needs no initialisation and holds
- * pa_kv_decode_workspace_size bytes (same sizes, format, partition
- * size and device; partition_size 0 for the library's own plan), 0 where
- * sizes are out of range. */
+ * pa_kv_decode_workspace_size bytes (for the same sizes, format, mode and
+ * partition size, 0 for the library's own, with this device current), which
+ * is 0 where sizes are out of range. */
 typedef struct {
     void* out;
     const void* q;
@@ -600,7 +600,7 @@ typedef struct {
 } pa_kv_decode_args;
 
 size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
-                                   int format, int partition_size, int weights);
+                                   int format, int mode, int partition_size, int weights);
 int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void* workspace,
                  size_t workspace_bytes, pa_stream_t stream);
 

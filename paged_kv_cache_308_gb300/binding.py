@@ -198,7 +198,7 @@ def _load() -> ctypes.CDLL:
     lib.pa_kv_append.restype = i32
     lib.pa_kv_append.argtypes = [vp, vp]  # pa_kv_append_args
     lib.pa_kv_decode_workspace_size.restype = ctypes.c_size_t
-    lib.pa_kv_decode_workspace_size.argtypes = [i32] * 8
+    lib.pa_kv_decode_workspace_size.argtypes = [i32] * 9
     lib.pa_kv_decode.restype = i32
     lib.pa_kv_decode.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]  # pa_kv_decode_args, pa_decode_opts
     lib.pa_kv_prefix_workspace_size.restype = ctypes.c_size_t
@@ -653,10 +653,11 @@ def pa_kv_append(k_cache, v_cache, k_scales, v_scales, k_new, v_new, block_table
 
 
 def pa_kv_decode_workspace_size(num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim, dtype,
-                                partition_size: int = 0, weights: bool = False) -> int:
+                                mode="auto", partition_size: int = 0, weights: bool = False) -> int:
     """Bytes of pa_kv_decode's workspace on the current device, for a cache of `dtype`."""
     return lib.pa_kv_decode_workspace_size(int(num_seqs), int(max_seq_len), int(num_heads), int(num_kv_heads),
-                                           int(head_dim), KV_FORMATS[dtype], int(partition_size), int(bool(weights)))
+                                           int(head_dim), KV_FORMATS[dtype], MODES[mode], int(partition_size),
+                                           int(bool(weights)))
 
 
 def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, stream=None, *,
@@ -692,8 +693,8 @@ def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq
 
     if workspace is None:
         with torch.cuda.device(dev):  # (the plan goes by the device's SMs)
-            need = lib.pa_kv_decode_workspace_size(B, max_seq_len, H, hkv, dim, cache[8], int(partition_size),
-                                                   int(wout != 0))
+            need = lib.pa_kv_decode_workspace_size(B, max_seq_len, H, hkv, dim, cache[8], MODES[mode],
+                                                   int(partition_size), int(wout != 0))
         ptr, nbytes, _hold = _workspace(None, need, dev, stream)
     else:
         ptr, nbytes, _hold = _workspace(workspace, 0, dev, stream)

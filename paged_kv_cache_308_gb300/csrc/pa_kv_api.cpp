@@ -160,7 +160,7 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;  // the launch reports the missing device
     const DecodePlan plan = plan_decode(a->num_seqs, a->max_seq_len, c.num_kv_heads, c.head_dim, c.format, num_sms,
                                         o ? o->partition_size : 0, o ? o->mode : PA_MODE_AUTO);
-    const bool weights = a->weights_out != nullptr;
+    const bool weights = a->weights_out && a->max_seq_len > 0;
     const DecodeSpace sp =
         decode_space(plan, a->num_seqs, a->num_heads, c.num_kv_heads, c.head_dim, a->max_seq_len, weights);
     if (sp.bytes > 0 && (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign))) return PA_ERR_WORKSPACE;
@@ -413,14 +413,15 @@ int pa_kv_append(const pa_kv_append_args* a, pa_stream_t stream) {
 }
 
 size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_dim,
-                                   int format, int partition_size, int weights) {
+                                   int format, int mode, int partition_size, int weights) {
     if (num_seqs <= 0 || max_seq_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || partition_size < 0 ||
-        partition_size % pa::kBlockSize || pa::kv_decode_ctas(format, head_dim) < 0)
+        partition_size % pa::kBlockSize || mode < PA_MODE_AUTO || mode > PA_MODE_SPLIT ||
+        num_heads % num_kv_heads || pa::kv_decode_ctas(format, head_dim) < 0)
         return 0;
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK || num_sms <= 0) num_sms = kMaxSmsBound;
     const DecodePlan plan =
-        plan_decode(num_seqs, max_seq_len, num_kv_heads, head_dim, format, num_sms, partition_size, PA_MODE_AUTO);
+        plan_decode(num_seqs, max_seq_len, num_kv_heads, head_dim, format, num_sms, partition_size, mode);
     return decode_space(plan, num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len, weights != 0).bytes;
 }
 

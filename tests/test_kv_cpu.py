@@ -86,7 +86,7 @@ def test_decode_options_and_workspace_are_checked():
                     (dict(warps=4, stages=2), pb.PA_ERR_UNSUPPORTED)):
         assert call("pa_kv_decode", decode_args(), pb.make_opts(**o), **big) == code, o
     o = pb.make_opts(partition_size=64)
-    n = pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.float8_e4m3fn, 64)
+    n = pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.float8_e4m3fn, partition_size=64)
     up = lambda x: -(-x // 256) * 256
     rows = 2 * 24 * 13
     assert n == up(rows * 8) + rows * 256 * 4
@@ -94,10 +94,26 @@ def test_decode_options_and_workspace_are_checked():
     assert call("pa_kv_decode", decode_args(), o, None, n) == pb.PA_ERR_WORKSPACE
     assert call("pa_kv_decode", decode_args(), o, FAKE + 16, n) == pb.PA_ERR_WORKSPACE
     # the weights add the scores of 50 whole blocks
-    assert pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.float8_e4m3fn, 64, True) == n + 2 * 24 * 800 * 4
+    assert pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.float8_e4m3fn, partition_size=64, weights=True) == n + 2 * 24 * 800 * 4
     for bad in ((0, 800, 24, 4, 256), (2, 0, 24, 4, 256), (2, 800, 0, 4, 256), (2, 800, 24, 0, 256), (2, 800, 24, 4, 96)):
         assert pb.pa_kv_decode_workspace_size(*bad, torch.int8) == 0
-    assert pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.int8, 24) == 0
+    assert pb.pa_kv_decode_workspace_size(2, 800, 24, 4, 256, torch.int8, partition_size=24) == 0
+
+
+def test_decode_workspace_follows_the_plan():
+    size = lambda B, L, **kw: pb.pa_kv_decode_workspace_size(B, L, 24, 4, 256, torch.int8, **kw)
+    # one CTA per (sequence, kv head): nothing to merge; the weights still need the sums and the scores
+    up = lambda x: -(-x // 256) * 256
+    assert size(8, 512) == 0 and size(1, 128) == 0 and size(8, 4000, mode="single") == 0
+    assert size(8, 512, weights=True) == up(8 * 24 * 8) + 8 * 24 * 512 * 4
+    assert size(8, 512, mode="split") > 0 and size(1, 129) > 0 and size(8, 513) > 0
+    # equal shares: per kv head a slot for every CTA, every warp and every sequence
+    one, two = size(8, 100000), size(9, 100000)
+    assert 0 < two - one < 24 * 256 * 4 + 24 * 8 + 1024
+    assert size(8, 100000) == size(8, 5000)  # whatever the lengths
+    # the weights add fp32 scores of whole blocks
+    assert size(8, 5000, weights=True) == one + 8 * 24 * 5008 * 4
+    assert size(2, 0) == 0
 
 
 @pytest.mark.parametrize("kw,code", [
