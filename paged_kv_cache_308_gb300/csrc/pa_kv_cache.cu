@@ -423,8 +423,9 @@ __device__ __forceinline__ float weight_of(uint32_t key, const float* w) {
 // through distributed shared memory, and a block's first output follows from
 // its predecessors' counts.  Integer counts only, so the result does not
 // depend on the order of the atomics.  Bound by latency: per round one
-// barrier of the cluster and two of the block.
+// barrier of the cluster and three of the block.
 constexpr int kHistWords = 2048 + 2048 + 1024;
+constexpr int kMaxCluster = 8;  // blocks of a cluster
 
 // Exclusive prefix sums of a pair of counts over the block's threads (in
 // their order), and the block's totals.  One barrier; `part` (2 x 32 words)
@@ -450,12 +451,15 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, unsigned (*part)[32], uint2
     return make_uint2((warp ? bx : 0u) + incl.x - v.x, (warp ? by : 0u) + incl.y - v.y);
 }
 
-__global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const KvEvictParams prm) {
+// (one block per SM: left at 32 registers two share one, and 8 sequences of up to
+// 8192 tokens take 27.4 us with the move instead of 24.3)
+__global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const KvEvictParams prm) {
     extern __shared__ __align__(16) uint32_t keys[];  // prm.key_words of them
     __shared__ __align__(8) unsigned hist[kHistWords];
-    __shared__ unsigned part[4][2][32];  // one per block scan
-    __shared__ unsigned found[3][2];     // per round: bin, tokens above it
-    __shared__ unsigned counts[2];       // this block's kept for sure, and ties
+    __shared__ __align__(8) unsigned coarse[3][64];
+    __shared__ unsigned part[2][32];
+    __shared__ unsigned found[3][2];  // per round: bin, tokens to take from it on
+    __shared__ __align__(8) unsigned counts[2];  // this block's kept for sure, and ties
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int kvh = blockIdx.x / CS, b = blockIdx.y;
@@ -544,81 +548,97 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
                     if ((k4[j] & mask) == T) atomicAdd(h + ((k4[j] >> shift) & (bins - 1)), 1u);
             }
         }
+        // Sums over the cluster of 64 groups of bins find the group, then of the
+        // group's bins the bin: reading all bins of all blocks was bound by the
+        // network between the SMs (2.4 us a round with 8 blocks).
+        __syncthreads();
+        const int per = bins / 64;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const unsigned sum = __reduce_add_sync(kFull, lane < per ? h[(2 * warp + j) * per + lane] : 0u);
+            if (lane == 0) coarse[round][2 * warp + j] = sum;
+        }
         cluster.barrier_arrive();
         if (round == 0) put_protected();  // while the others arrive
         cluster.barrier_wait();
-        // bins in descending order: thread i has bins 2 i and 2 i + 1 from the top
-        unsigned v[2] = {0u, 0u};
-        if (2 * tid < bins) {
-            for (int r = 0; r < CS; ++r) {
-                const uint2 two = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(h, r) + bins - 2 - 2 * tid);
-                v[0] += two.y;
-                v[1] += two.x;
-            }
-        }
-        uint2 total;
-        const unsigned above = block_scan(make_uint2(v[0] + v[1], 0u), part[round], &total).x;
-        if (above < need && need <= above + v[0] + v[1]) {
-            const bool first = need <= above + v[0];
-            found[round][0] = (unsigned)(bins - 1 - 2 * tid - (first ? 0 : 1));
-            found[round][1] = above + (first ? 0u : v[0]);
+        if (warp == 0) {
+            // in descending order: lane i has groups 63 - 2 i and 62 - 2 i, then bin per - 1 - i
+            auto pick = [&](unsigned a, unsigned c, unsigned& above) {  // the lane whose counts reach `need`
+                unsigned incl = a + c;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const unsigned up = __shfl_up_sync(kFull, incl, off);
+                    if (lane >= off) incl += up;
+                }
+                above = incl - a - c;
+                return __ffs(__ballot_sync(kFull, above < need && need <= incl)) - 1;
+            };
+            unsigned a = 0, c = 0, above;
+            uint2 two[kMaxCluster];  // all reads on their way at once
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                two[r] = r < CS ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(coarse[round], r) + 62 - 2 * lane)
+                                : make_uint2(0u, 0u);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) a += two[r].y, c += two[r].x;
+            int who = pick(a, c, above);
+            const bool second = need > above + a;
+            const int group = 63 - 2 * who - (int)__shfl_sync(kFull, (unsigned)second, who);
+            need -= __shfl_sync(kFull, above + (second ? a : 0u), who);  // less the groups above
+            a = 0;
+            unsigned one[kMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                one[r] = r < CS && lane < per ? cluster.map_shared_rank(h, r)[group * per + per - 1 - lane] : 0u;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) a += one[r];
+            who = pick(a, 0u, above);
+            need -= __shfl_sync(kFull, above, who);
+            if (lane == 0) found[round][0] = (unsigned)(group * per + per - 1 - who), found[round][1] = need;
         }
         __syncthreads();
         T |= found[round][0] << shift;
         mask |= (uint32_t)(bins - 1) << shift;
-        need -= found[round][1];
+        need = found[round][1];
     }
-    // Kept: the keys above T, and of those equal to it the first `need`.  Counts
-    // of both in one word while they are a warp's 128 keys.
-    auto marks = [&](const uint4& q, unsigned (&k)[4]) {
-        const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = (k4[j] > T ? 1u : 0u) + (k4[j] == T ? 0x10000u : 0u);
-        return k[0] + k[1] + k[2] + k[3];
-    };
+    // Kept: the keys above T, and of those equal to it the first `need`.
     unsigned sure = 0, tie = 0;
     for (int i = i0; i < i1; i += 128) {
-        unsigned k[4];
-        const unsigned c = marks(keys_of(i), k);
-        sure += c & 0xffffu;
-        tie += c >> 16;
+        const uint4 q = keys_of(i);
+        const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sure += k4[j] > T;
+            tie += k4[j] == T;
+        }
     }
     uint2 total;
-    uint2 before = block_scan(make_uint2(sure, tie), part[3], &total);
+    uint2 before = block_scan(make_uint2(sure, tie), part, &total);
     before = make_uint2(__shfl_sync(kFull, before.x, 0), __shfl_sync(kFull, before.y, 0));  // the warp's first
     if (tid == 0) counts[0] = total.x, counts[1] = total.y;
     cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        before.x += cluster.map_shared_rank(counts, r)[0];
-        before.y += cluster.map_shared_rank(counts, r)[1];
-    }
-    for (int i = i0; i - 4 * lane < i1; i += 128) {  // (the whole warp, for the shuffles)
-        const uint4 q = i < i1 ? keys_of(i) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
-        unsigned k[4];
-        const unsigned mine = marks(q, k);
-        unsigned incl = mine;
+    uint2 others[kMaxCluster];
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const unsigned up = __shfl_up_sync(kFull, incl, off);
-            if (lane >= off) incl += up;
-        }
-        const unsigned all = __shfl_sync(kFull, incl, 31);
-        unsigned a = before.x + ((incl - mine) & 0xffffu), c = before.y + ((incl - mine) >> 16);
-        if (mine) {
+    for (int r = 0; r < kMaxCluster; ++r)
+        others[r] = r < rank ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(counts, r)) : make_uint2(0u, 0u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (k[j] == 1u || (k[j] && c < need)) {
-                    const int at = plan.sinks + (int)(a + min(c, need));
-                    kept[at] = t0 + i + j;
-                    if (dst_w) dst_w[at] = weight_of(k4[j], w + t0 + i + j);
-                }
-                a += k[j] & 0xffffu;
-                c += k[j] >> 16;
-            }
+    for (int r = 0; r < kMaxCluster; ++r) before.x += others[r].x, before.y += others[r].y;
+    // the warp's run again, a key a lane
+    const unsigned below = (1u << lane) - 1u;
+    const float* from = w + t0;
+    kept += plan.sinks;
+    if (dst_w) dst_w += plan.sinks;
+    for (int i = warp * run + lane; i - lane < i1; i += 32) {
+        const uint32_t key = i >= n ? 0u : held ? keys[i] : order_key(from[i]);
+        const unsigned bs = __ballot_sync(kFull, key > T), be = __ballot_sync(kFull, key == T);
+        const unsigned my_tie = before.y + __popc(be & below);
+        if (key > T || (key == T && my_tie < need)) {
+            const unsigned at = before.x + __popc(bs & below) + min(my_tie, need);
+            kept[at] = t0 + i;
+            if (dst_w) dst_w[at] = weight_of(key, from + i);
         }
-        before.x += all & 0xffffu;
-        before.y += all >> 16;
+        before.x += __popc(bs);
+        before.y += __popc(be);
     }
     cluster.sync();  // no block leaves while another may still read its counts
 }
