@@ -66,9 +66,10 @@ struct DecodePlan {
 // * one sequence: a wave of equal partitions, whose block ids can be read before
 //   its length is known;
 // * other batches: equal shares for the CTAs the SMs hold at once (against the
-//   best of partitions of 256 to 8192 tokens: 64 log-uniform up to 8192 26.0 /
-//   33.2, 8 x U[1, 8192] 18.1 / 18.7, 64 x U[1, 4096] 60.9 / 60.9, 16 x 16384 93.8 /
-//   91.3, 64 x 2048 52.7 / 53.9).
+//   best of partitions of 256 to 8192 tokens, 8 x 128: 64 log-uniform up to 8192
+//   26.5 / 33.5, 16 x U[1, 8192] 27.4 / 30.7, 64 x U[1, 4096] 59.6 / 61.1, 16 x 16384
+//   86.9 / 94.4, 64 x 2048 51.5 / 55.8; 4 x 256: 8 x U[1, 8192] 17.2 / 18.0, 16 x U[1,
+//   8192] 28.7 / 27.5, 64 x 2048 51.9 / 45.0, which only equal lengths give).
 // A caller's partition size gives the grid of partitions.
 constexpr int kSingleOneMaxLen = 128, kSingleMaxLen = 512, kSingleManyMaxLen = 1024;
 

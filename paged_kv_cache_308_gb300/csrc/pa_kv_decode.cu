@@ -222,12 +222,17 @@ __device__ __forceinline__ int out_dim(int mt, int g, int hi) {
     return F == PA_KV_F16 ? 16 * mt + g + 8 * hi : 16 * mt + 2 * g + hi;
 }
 
-// Stages per warp, and the CTAs an SM holds: 96 to 192 KB of copies in flight
-// per SM, within its registers (an accumulator of 4 D / 16 and D / 8 of Q a
-// thread) and 228 KB of shared memory.
+// Stages per warp, and the CTAs an SM holds, within its registers (D / 4 of O and
+// D / 8 of Q a thread) and 228 KB of shared memory.  More copies in flight than
+// the latency asks for only queue in memory and let the SMs drift apart: 3
+// instead of 2 stages at head_dim 256 in 8 bits (192 against 128 KB per SM)
+// took 132.0 instead of 126.1 us for 400,000 tokens of 4 kv heads, 3 and 4
+// instead of 2 at 128 (144, 192 / 96 KB) 133.1 and 138.5 instead of 128.4.  At
+// 64, whose blocks are small next to a block's latency, 3 were slower than 4
+// (152.0 / 149.9), and 16-bit tiles want 192 KB.
 template <int F, int D>
 constexpr int stages_of() {
-    return F == PA_KV_F16 ? (D == 64 ? 4 : 3) : (D == 256 ? 3 : 4);
+    return F == PA_KV_F16 ? (D == 64 ? 4 : 3) : (D == 64 ? 4 : 2);
 }
 template <int F, int D>
 constexpr int ctas_of() {
