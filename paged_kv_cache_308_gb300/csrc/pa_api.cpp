@@ -895,7 +895,8 @@ int ensure_prefix_sched(cudaStream_t stream, unsigned int** out) {
 // split_call: pa_prefix_split (the key split of `split`, or the plan's,
 // into workspace `ws`); otherwise pa_prefix / pa_prefix_ex.
 int run_prefix(const pa_prefix_args* a, const pa_decode_opts* o, cudaStream_t stream, bool split_call = false,
-               const pa_prefix_split_opts* split = nullptr, void* ws = nullptr, size_t ws_bytes = 0) {
+               const pa_prefix_split_opts* split = nullptr, void* ws = nullptr, size_t ws_bytes = 0,
+               const float2* factors = nullptr) {
     int rc = validate_prefix(a, o);
     if (rc) return rc;
     if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
@@ -950,6 +951,7 @@ int run_prefix(const pa_prefix_args* a, const pa_decode_opts* o, cudaStream_t st
     prm.status = pa::device_status_ptr();
     if (!prm.status) return PA_ERR_CUDA;
     prm.trace = g_trace;
+    prm.factors = factors;
     const int tile_tokens = (warp_mma ? 64 : 128) / prm.group;
     dim3 grid((a->max_query_len + tile_tokens - 1) / tile_tokens, a->num_kv_heads, a->num_seqs);
     prm.tiles_per_seq = static_cast<int>(grid.x);
@@ -1035,6 +1037,10 @@ namespace pa {
 int sm_count(int* num_sms) { return query_sm_count(num_sms); }
 
 int check_prefix(const pa_prefix_args* a, const pa_decode_opts* o) { return validate_prefix(a, o); }
+
+int prefix_with_factors(const pa_prefix_args* a, const pa_decode_opts* o, const float2* factors, cudaStream_t stream) {
+    return run_prefix(a, o, stream, false, nullptr, nullptr, 0, factors);
+}
 
 }  // namespace pa
 

@@ -15,6 +15,10 @@ namespace pa {
 // Defined in pa_api.cpp for the other C-ABI sources.
 int sm_count(int* num_sms);                               // of the current device; a PA_* code
 int check_prefix(const pa_prefix_args* args, const pa_decode_opts* opts);  // a PA_* code
+// pa_prefix_ex whose caches hold the context without its factors, float2 [num_seqs]
+// [max_blocks_per_seq][num_kv_heads] of (K, V) (see PrefixParams::factors).
+int prefix_with_factors(const pa_prefix_args* args, const pa_decode_opts* opts, const float2* factors,
+                        cudaStream_t stream);
 
 struct KvDecodeParams {
     __half* out;
@@ -81,6 +85,7 @@ struct KvExpandParams {
     const float* scales[2];
     __half* expanded[2];   // [num_seqs * blocks_per_seq][Hkv][16][D]
     int32_t* tables;       // [num_seqs][blocks_per_seq]: their numbers
+    float* factors;        // [num_seqs * blocks_per_seq][Hkv][K, V], or null
     const int32_t* block_tables;
     const int32_t* context_lens;
     long long num_blocks;

@@ -258,7 +258,8 @@ size_t prefix_copy_bytes(int num_seqs, int blocks_per_seq, int num_kv_heads, int
 size_t prefix_space(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format) {
     if (format == PA_KV_F16 || max_context_len == 0) return 0;
     const int n = blocks_of(max_context_len);
-    return 2 * prefix_copy_bytes(num_seqs, n, num_kv_heads, head_dim) + up((size_t)num_seqs * n * 4);
+    return 2 * prefix_copy_bytes(num_seqs, n, num_kv_heads, head_dim) + up((size_t)num_seqs * n * 4) +
+           (format == PA_KV_INT8 ? up((size_t)num_seqs * n * num_kv_heads * 8) : 0);
 }
 
 int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, size_t ws_bytes, cudaStream_t stream) {
@@ -297,6 +298,7 @@ int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, si
     // the copy replaces the cache; it has room for every sequence's longest context
     p.num_blocks = (int64_t)a->num_seqs * n;
     p.max_blocks_per_seq = n;
+    float* factors = nullptr;
     if (n > 0) {
         if (p.num_blocks * c.num_kv_heads * pa::kBlockSize >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
         if (!ws || ws_bytes < need || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
@@ -310,6 +312,12 @@ int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, si
         e.expanded[0] = reinterpret_cast<__half*>(w);
         e.expanded[1] = reinterpret_cast<__half*>(w + copy);
         e.tables = reinterpret_cast<int32_t*>(w + 2 * copy);
+        // INT8 scales have more bits than a product with a code leaves room for in
+        // fp16: their significands go to the kernel apart (the warp-level kernel
+        // cannot take them; there the values are rounded)
+        if (c.format == PA_KV_INT8 && !(o && (o->flags & PA_FLAG_PREFIX_WARP_MMA)))
+            factors = reinterpret_cast<float*>(w + 2 * copy + up((size_t)a->num_seqs * n * 4));
+        e.factors = factors;
         e.block_tables = a->block_tables;
         e.context_lens = a->context_lens;
         e.num_blocks = c.num_blocks;
@@ -326,7 +334,7 @@ int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, si
             cudaSuccess)
             return PA_ERR_CUDA;
     }
-    return pa_prefix_ex(&p, o, reinterpret_cast<pa_stream_t>(stream));
+    return pa::prefix_with_factors(&p, o, reinterpret_cast<const float2*>(factors), stream);
 }
 
 // ---- eviction

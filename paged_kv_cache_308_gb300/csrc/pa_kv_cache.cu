@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
 }
 
 // An 8-bit context block to halves (values above fp16's range become its
-// largest), and the copy's block table.  One warp per (block, kv head, K or V).
+// largest), and the copy's block table; with factors only the power of two of
+// the block's scale goes into the halves.  One warp per (block, kv head, K or V).
 template <int F, int D>
 __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm) {
     constexpr int kPasses = kBlockSize * D / (32 * 16);  // 16 codes a lane
@@ -358,7 +359,18 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
     for (int i = 0; i < kPasses; ++i)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(&held[kv][i][lane])), "l"(src + 32 * i)
                      : "memory");
-    const float s = __ldg(of_kv(prm.scales, kv) + bh);
+    float s = __ldg(of_kv(prm.scales, kv) + bh);
+    if (prm.factors) {
+        // s = f 2^e, 1 <= f < 2: the copy holds code 2^e, exact in fp16, and f goes
+        // into the factors
+        const uint32_t bits = __float_as_uint(s);
+        float f = 1.f;
+        if (s >= 0x1p-126f && s <= 0x1p126f) {
+            f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+            s = __uint_as_float(bits & 0x7f800000u);
+        }
+        if (lane == 0) prm.factors[2 * ((size_t)to * prm.num_kv_heads + kvh) + kv] = f;
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
     uint8_t* dst = reinterpret_cast<uint8_t*>(of_kv(prm.expanded, kv) +
                                               ((size_t)to * prm.num_kv_heads + kvh) * kBlockSize * D);

@@ -37,6 +37,10 @@ struct PrefixParams {
     // counts the CTAs that finished, and the last one re-arms both to zero.
     unsigned int* sched = nullptr;
     int total_units = 0;
+    // tcgen05 kernel: (K, V) factors of the context blocks, [B][max_blocks_per_seq]
+    // [Hkv], positive: the keys and values are factor times what the caches hold
+    // (null: the caches' own).
+    const float2* factors = nullptr;
     // Diagnostic builds (-DPA_TRACE) only: the tcgen05 kernel records
     // SM clock stamps of its pipeline events, kPrefixTraceIters x 16 per CTA
     // (the last of the kPrefixTraceIters records holds the CTA's phases in

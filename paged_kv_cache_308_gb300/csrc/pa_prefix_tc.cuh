@@ -342,7 +342,9 @@ __device__ __forceinline__ TcUnit tc_unit(const PrefixParams& prm, int c, bool r
     return u;
 }
 
-template <int D, bool Persist>
+// Scaled: the context's keys and values come with a factor per block (see
+// PrefixParams::factors), applied to the scores and the probabilities.
+template <int D, bool Persist, bool Scaled>
 __global__ void __maxnreg__(kTcMaxRegs)
     pa_prefix_tc_kernel(const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc,
                         const __grid_constant__ CUtensorMap tmap_kn, const __grid_constant__ CUtensorMap tmap_vn,
@@ -817,8 +819,27 @@ __global__ void __maxnreg__(kTcMaxRegs)
             const int my_tok = cur.t0 + ti;  // chunk token index of the row
             const int n = cur.n, jb = cur.jb, nctx = cur.nctx, C = cur.C;
             float m = -INFINITY, l = 0.f;  // reference max (scaled, log2 domain) and exp sum
+            // Scaled: lane i < 4 holds the factors of block i of a tile, read a
+            // tile ahead; chunk blocks (and none) have 1
+            float2 fac = make_float2(1.f, 1.f);
+            const float2* facs = nullptr;
+            if constexpr (Scaled) facs = prm.factors + (size_t)cur.b * prm.max_blocks_per_seq * prm.num_kv_heads + cur.kvh;
+            auto load_factors = [&](int j) {
+                const int blk = 4 * (jb + j) + lane;
+                fac = make_float2(1.f, 1.f);
+                if (lane < 4 && blk < nctx) fac = __ldg(facs + (size_t)blk * prm.num_kv_heads);
+            };
+            if constexpr (Scaled) load_factors(0);
             for (int j = 0; j < n; ++j) {
                 const int x = g + j;
+                float slk[4], fv[4];  // of the tile's blocks: scale and K's factor; V's
+#pragma unroll
+                for (int qb = 0; qb < 4; ++qb) {
+                    slk[qb] = Scaled ? sl2 * __shfl_sync(kFull, fac.x, qb) : sl2;
+                    fv[qb] = Scaled ? __shfl_sync(kFull, fac.y, qb) : 1.f;
+                }
+                if constexpr (Scaled)
+                    if (j + 1 < n) load_factors(j + 1);
                 const uint32_t sb = tS + (uint32_t)(x & 1) * kTcKeys + lane_off;  // this row of score buffer x % 2
                 if (!(ok = tc_warp_wait(bar(kTcBarSDone + (x & 1)), (x >> 1) & 1, limit, sm_abort))) break;
                 tc_fence_after();
@@ -851,10 +872,10 @@ __global__ void __maxnreg__(kTcMaxRegs)
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {  // on scaled scores: the scale may be negative
-                    mx0 = fmaxf(mx0, __uint_as_float(sv[0][c]) * sl2);
-                    mx1 = fmaxf(mx1, __uint_as_float(sv[0][c + 1]) * sl2);
-                    mx2 = fmaxf(mx2, __uint_as_float(sv[1][c]) * sl2);
-                    mx3 = fmaxf(mx3, __uint_as_float(sv[1][c + 1]) * sl2);
+                    mx0 = fmaxf(mx0, __uint_as_float(sv[0][c]) * slk[c >> 4]);
+                    mx1 = fmaxf(mx1, __uint_as_float(sv[0][c + 1]) * slk[c >> 4]);
+                    mx2 = fmaxf(mx2, __uint_as_float(sv[1][c]) * slk[2 + (c >> 4)]);
+                    mx3 = fmaxf(mx3, __uint_as_float(sv[1][c + 1]) * slk[2 + (c >> 4)]);
                 }
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                 // The reference max m only moves when the tile max exceeds it by
@@ -870,11 +891,13 @@ __global__ void __maxnreg__(kTcMaxRegs)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const int h2 = c >> 4, cc = (c & 15) * 2;
-                    const float p0 = tc_ex2(fmaf(__uint_as_float(sv[h2][cc]), sl2, -base));
-                    const float p1 = tc_ex2(fmaf(__uint_as_float(sv[h2][cc + 1]), sl2, -base));
+                    const int qb = 2 * h2 + (cc >> 4);  // the keys' block in the tile
+                    const float p0 = tc_ex2(fmaf(__uint_as_float(sv[h2][cc]), slk[qb], -base));
+                    const float p1 = tc_ex2(fmaf(__uint_as_float(sv[h2][cc + 1]), slk[qb], -base));
                     rs0 += p0;
                     rs1 += p1;
-                    pk[c] = half2_bits(__floats2half2_rn(p0, p1));
+                    pk[c] = Scaled ? half2_bits(__floats2half2_rn(p0 * fv[qb], p1 * fv[qb]))
+                                   : half2_bits(__floats2half2_rn(p0, p1));
                 }
                 l = l * alpha + (rs0 + rs1);
                 // P(x) over S(x), which is in registers now: the S MMA of this
@@ -1099,15 +1122,16 @@ int prefix_tc_ctas_per_sm(int head_dim) {
 }
 
 namespace {
-template <int D>
+template <int D, bool Scaled>
 cudaError_t launch_prefix_tc_t(const PrefixParams& prm, const CUtensorMap* maps, dim3 grid, cudaStream_t stream) {
     const int smem = PrefixTcShape<D>::kSmemBytes;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = once_per_device(done, [&] {
-        cudaError_t r = cudaFuncSetAttribute(pa_prefix_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+        cudaError_t r = cudaFuncSetAttribute(pa_prefix_tc_kernel<D, false, Scaled>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(pa_prefix_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            r = cudaFuncSetAttribute(pa_prefix_tc_kernel<D, true, Scaled>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     smem);
         return r;
     });
     if (e != cudaSuccess) return e;
@@ -1119,8 +1143,9 @@ cudaError_t launch_prefix_tc_t(const PrefixParams& prm, const CUtensorMap* maps,
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = prm.sched ? cudaLaunchKernelEx(&cfg, pa_prefix_tc_kernel<D, true>, maps[0], maps[1], maps[2], maps[3], prm)
-                  : cudaLaunchKernelEx(&cfg, pa_prefix_tc_kernel<D, false>, maps[0], maps[1], maps[2], maps[3], prm);
+    e = prm.sched
+            ? cudaLaunchKernelEx(&cfg, pa_prefix_tc_kernel<D, true, Scaled>, maps[0], maps[1], maps[2], maps[3], prm)
+            : cudaLaunchKernelEx(&cfg, pa_prefix_tc_kernel<D, false, Scaled>, maps[0], maps[1], maps[2], maps[3], prm);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -1129,9 +1154,15 @@ cudaError_t launch_prefix_tc_t(const PrefixParams& prm, const CUtensorMap* maps,
 cudaError_t launch_prefix_tc(int head_dim, const PrefixParams& prm, const CUtensorMap* maps, dim3 grid,
                              cudaStream_t stream) {
     switch (head_dim) {
-        case 64: return launch_prefix_tc_t<64>(prm, maps, grid, stream);
-        case 128: return launch_prefix_tc_t<128>(prm, maps, grid, stream);
-        case 256: return launch_prefix_tc_t<256>(prm, maps, grid, stream);
+        case 64:
+            return prm.factors ? launch_prefix_tc_t<64, true>(prm, maps, grid, stream)
+                               : launch_prefix_tc_t<64, false>(prm, maps, grid, stream);
+        case 128:
+            return prm.factors ? launch_prefix_tc_t<128, true>(prm, maps, grid, stream)
+                               : launch_prefix_tc_t<128, false>(prm, maps, grid, stream);
+        case 256:
+            return prm.factors ? launch_prefix_tc_t<256, true>(prm, maps, grid, stream)
+                               : launch_prefix_tc_t<256, false>(prm, maps, grid, stream);
         default: return cudaErrorInvalidValue;
     }
 }

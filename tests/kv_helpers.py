@@ -167,10 +167,10 @@ def decode_reference(c: Case):
     return out, bound, w, wb
 
 
-def prefix_reference(c: Case, new_lens, q, k_new, v_new):
-    """out and its bound for chunks behind c's contexts.  Beyond decode_reference: context values rounded to fp16 (int8:
-    2^-11 of K in the scores and of V in the sum), probabilities under 2^-24 of the row's largest may be lost or
-    rounded by 2^-25, and the sum may run over the rounded ones (2^-11 more)."""
+def prefix_reference(c: Case, new_lens, q, k_new, v_new, rounded=False):
+    """out and its bound for chunks behind c's contexts.  Beyond decode_reference: probabilities under 2^-24 of the
+    row's largest may be lost or rounded by 2^-25, and the sum may run over the rounded ones (2^-11 more).  `rounded`:
+    context values are rounded to fp16 (2^-11 of K in the scores and of V in the sum)."""
     g = c.heads // c.hkv
     out = torch.zeros(q.shape, dtype=torch.float64, device=c.device)
     bound = torch.zeros_like(out)
@@ -186,7 +186,7 @@ def prefix_reference(c: Case, new_lens, q, k_new, v_new):
             v = torch.cat([vc[h], v_new[at:at + m, h].double()])
             for j in range(h * g, (h + 1) * g):
                 o, p, a, size = attend(q[at:at + m, j].double(), k, v, c.scale, mask)
-                r = 2.0 ** -11 if c.fmt == "int8" else 0.0
+                r = 2.0 ** -11 if rounded else 0.0
                 e = math.expm1(2 * (score_error(c.dim, size) + r * size)) + 2.0 ** -18
                 out[at:at + m, j] = o
                 bound[at:at + m, j] = (2.0 ** -11 * o.abs() + (2 * 2.0 ** -11 * 1.01 + r + e) * a

@@ -243,6 +243,41 @@ def test_prefix(fmt, heads, hkv, dim):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("form", ["persistent", "grid", "warp"])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_prefix_kernels_and_scales(fmt, form, dim):
+    # every kernel form; block scales e^8 apart, some of them 0, for INT8 of 24 significant bits
+    ctx, new = [200, 7, 1000], [70, 150, 3]
+    c = K.Case(ctx, 6, 2, dim, fmt, seed=84, device=DEV, spread=4.0)
+    if fmt == "int8":
+        c.ks *= 1.2345678
+        c.vs *= 0.8765432
+    for s in (c.ks, c.vs):
+        s[int(c.tables[2, 5])] = 0.0
+    q, k_new, v_new, loc = _chunks(c, new, 85)
+    flags = {"persistent": 0, "grid": pb().PA_FLAG_PREFIX_GRID, "warp": pb().PA_FLAG_PREFIX_WARP_MMA}[form]
+    ref, bound = K.prefix_reference(c, new, q, k_new, v_new, rounded=form == "warp" and fmt == "int8")
+    out = torch.full_like(q, math.nan)
+    pb().pa_kv_prefix(out, q, k_new, v_new, *c.cache(), c.tables, c.seq_lens, loc, c.scale, max_context_len=1000,
+                      max_query_len=150, flags=flags)
+    assert status() == 0
+    check(out, ref, bound)
+
+
+def test_prefix_negative_scale_and_special_blocks():
+    # a negative softmax scale; NaN codes past the context's end in a block with a factor
+    c = K.Case([37, 90], 4, 2, 128, "int8", seed=86, device=DEV, spread=2.0)
+    c.scale = -c.scale
+    q, k_new, v_new, loc = _chunks(c, [40, 20], 87)
+    ref, bound = K.prefix_reference(c, [40, 20], q, k_new, v_new)
+    out = torch.full_like(q, math.nan)
+    pb().pa_kv_prefix(out, q, k_new, v_new, *c.cache(), c.tables, c.seq_lens, loc, c.scale, max_context_len=90,
+                      max_query_len=40)
+    assert status() == 0
+    check(out, ref, bound)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_prefix_without_context(fmt):
     c = K.Case([0, 0], 4, 2, 64, fmt, seed=19, device=DEV)
     q, k_new, v_new, loc = _chunks(c, [20, 3], 20)

@@ -135,11 +135,13 @@ def test_prefix_refusals(kw, code):
 
 def test_prefix_workspace():
     n = pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.int8)
-    assert n == 2 * (2 * 50 * 4 * 16 * 256 * 2) + 512
+    # K and V in fp16, the copy's table, the factors of INT8's scales
+    assert n == 2 * (2 * 50 * 4 * 16 * 256 * 2) + 512 + 2 * 50 * 4 * 8 + 128
+    assert pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.float8_e4m3fn) == 2 * (2 * 50 * 4 * 16 * 256 * 2) + 512
     assert pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.float16) == 0
     assert pb.pa_kv_prefix_workspace_size(2, 0, 4, 256, torch.int8) == 0
     for ws, size in ((FAKE, n - 1), (None, n), (FAKE + 16, n)):
-        assert call("pa_kv_prefix", prefix_args(), None, ws, size) == pb.PA_ERR_WORKSPACE
+        assert call("pa_kv_prefix", prefix_args(cache(fmt=pb.PA_KV_INT8)), None, ws, size) == pb.PA_ERR_WORKSPACE
     # an fp16 copy whose rows would not fit 32 bits
     big = prefix_args(cache(nb=20000), B=30000, T=30000, mbps=20000, max_ctx=320000)
     assert call("pa_kv_prefix", big, None, FAKE, 1 << 62) == pb.PA_ERR_UNSUPPORTED
