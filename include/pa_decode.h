@@ -511,8 +511,8 @@ int pa_merge_partials(void* out, const float* max_logits, const float* exp_sums,
  *   S(0) = 0.
  * Slots past a sequence's end may hold anything, NaN codes included.
  *
- * The four calls take argument structs, allocate no device memory, are
- * asynchronous on `stream` and can be captured into a graph (a captured call
+ * The four calls take argument structs, allocate no device memory (but the
+ * prefill's counter, see pa_prefix), are asynchronous on `stream` and can be captured into a graph (a captured call
  * keeps its workspace: calls that may overlap need one each).  Pointers are
  * device pointers; the caches and half tensors 16-byte aligned, the rest
  * 4-byte, workspaces 256-byte.  Supported shapes, errors and the status word
@@ -547,7 +547,8 @@ typedef struct {
  * that held none of the sequence's tokens; when it grew, the sequence's
  * earlier codes c in the block become the format's nearest to c * scale / s
  * (ties to even; with powers of two only E4M3's subnormals round).  New codes
- * are the nearest to x / s; infinities saturate to the largest code, NaN
+ * are the nearest to x / s (rounded to 32 bits first where a caller has written
+ * a scale of more significant bits); infinities saturate to the largest code, NaN
  * stays NaN in E4M3 and becomes 0 in INT8.  Calling it again with the same
  * arguments leaves the same cache.
  * max_query_len is a host-side bound on the new tokens of a sequence.  A

@@ -202,7 +202,18 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kv = warp & 1, kvh = blockIdx.y * kAppendHeads + (warp >> 1);
     int b, tile, ctx, q0, q1;
+    // bad tables or lengths of a sequence
+    auto bad = [&](int c, int s, int e) {
+        return c < 0 || s < 0 || e < s || e > prm.num_tokens || e - s > prm.max_query_len ||
+               (long long)c + e - s > (long long)prm.max_blocks_per_seq * kBlockSize;
+    };
     if (prm.packed) {
+        if (blockIdx.x == 0 && blockIdx.y == 0) {
+            // (a table out of order may hide a sequence from the search below)
+            for (int i = threadIdx.x; i < prm.num_seqs; i += blockDim.x)
+                if (bad(__ldg(prm.context_lens + i), __ldg(prm.query_start_loc + i), __ldg(prm.query_start_loc + i + 1)))
+                    atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
+        }
         // Tile slots of sequence b from floor(q0 / 16) + 2 b on: n tokens touch at
         // most floor(n / 16) + 2 blocks, and floor(q1 / 16) - floor(q0 / 16) >=
         // floor(n / 16).  The last b whose slots begin at or before this one, by
@@ -235,12 +246,11 @@ __global__ void __launch_bounds__(64 * kAppendHeads) kv_append_kernel(const KvAp
         q0 = __ldg(prm.query_start_loc + b);
         q1 = __ldg(prm.query_start_loc + b + 1);
     }
-    const long long end = (long long)ctx + q1 - q0;
-    if (ctx < 0 || q0 < 0 || q1 < q0 || q1 > prm.num_tokens || q1 - q0 > prm.max_query_len ||
-        end > (long long)prm.max_blocks_per_seq * kBlockSize) {
+    if (bad(ctx, q0, q1)) {
         if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return;
     }
+    const long long end = (long long)ctx + q1 - q0;
     const int blk = ctx / kBlockSize + tile;
     const long long p0 = (long long)blk * kBlockSize;  // position of the block's slot 0
     if (q1 == q0 || p0 >= end || kvh >= prm.num_kv_heads) return;

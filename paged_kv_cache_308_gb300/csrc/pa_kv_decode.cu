@@ -342,10 +342,12 @@ __device__ __forceinline__ void block_update(WarpState<D>& st, const uint32_t (&
         bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, off));
     }
     const float mn0 = fmaxf(st.m0, bm0), mn1 = fmaxf(st.m1, bm1);
-    float al0 = pow2_of(st.m0 - mn0), al1 = pow2_of(st.m1 - mn1);
+    // (scores of -infinity alone leave m there: 0 then stands in as the reference)
+    const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
+    float al0 = pow2_of(st.m0 - r0), al1 = pow2_of(st.m1 - r1);
     st.m0 = mn0;
     st.m1 = mn1;
-    const float e0 = mn0 - kShift, e1 = mn1 - kShift;
+    const float e0 = r0 - kShift, e1 = r1 - kShift;
     float p0 = pow2_of(s[0] - e0), p1 = pow2_of(s[1] - e1), p2 = pow2_of(s[2] - e0), p3 = pow2_of(s[3] - e1);
     st.l0 = st.l0 * al0 + (p0 + p2);
     st.l1 = st.l1 * al1 + (p1 + p3);
@@ -659,7 +661,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         // the segment's partial, or the output, straight from the fragments
         if (cnt > 0) {
             const bool direct = j0 == 0 && cnt == nseq;
-            const float f0 = st.vr / st.l0, f1 = st.vr / st.l1;
+            // (a partial without weight is 0, a whole sequence without any NaN)
+            const float f0 = st.l0 == 0.f && !direct ? 0.f : st.vr / st.l0;
+            const float f1 = st.l1 == 0.f && !direct ? 0.f : st.vr / st.l1;
             const size_t head0 = (size_t)b * H + kvh * G + 2 * c;
             const size_t slot = (size_t)(prm.ctas_per_head + cta * NW + warp + b);
             const size_t pi = ((size_t)kvh * prm.slots + slot) * G + 2 * c;
@@ -746,13 +750,13 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         f[w] = mw == -INFINITY ? 0.f : exp2f(mw - Mh);
         Lh += f[w] * sm_l[w * kMaxGroup + h];
     }
-    const float inv = 1.f / Lh;
     const size_t head = (size_t)b * H + kvh * G + h;
     const size_t slot = prm.flat ? (size_t)cta : (size_t)b * prm.max_partitions + cta;
     const size_t pi = ((size_t)kvh * prm.slots + slot) * G + h;
     // the CTA has the whole sequence: its run begins in or before block 0 and ends with the last
     const bool direct = j0 == warp && (prm.flat ? FlatRuns(units, prm.ctas_per_head).begin(cta + 1) == first + kLead + nseq
                                                 : prm.partition_size / kBlockSize >= nseq);
+    const float inv = Lh == 0.f && !direct ? 0.f : 1.f / Lh;
 #pragma unroll
     for (int w = 0; w < NW; ++w) f[w] *= inv;
 #pragma unroll

@@ -473,3 +473,52 @@ def test_decode_value_scales_far_apart(fmt):
     tiny = K.Case([40], 4, 1, 64, fmt, seed=35, device=DEV)
     tiny.vs[tiny.tables[0].long()] = 1e-42  # a subnormal scale: zero in fp16
     assert bool((decode(tiny) == 0).all())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_to_blocks_with_a_callers_scales(fmt):
+    # scales of 24 significant bits, and a code of -128: quotients are rounded to 32 bits first
+    c = K.Case([5, 9], 2, 2, 64, fmt, seed=88, device=DEV, room=[16, 16])
+    c.ks *= 1.2345678
+    c.vs *= 0.000123456
+    if fmt == "int8":
+        c.k[int(c.tables[0, 0]), 0, 1, ::3] = -128
+    _, k_new, v_new, loc = _chunks(c, [4, 7], 89)
+    k_new *= 0.1
+    old = [(c.k.clone(), c.ks.clone()), (c.v.clone(), c.vs.clone())]
+    append(c, [4, 7], k_new, v_new, loc)
+    assert status() == 0
+    for (codes, scales), got, got_s, new in zip(old, (c.k, c.v), (c.ks, c.vs), (k_new, v_new)):
+        for b, (n, m) in enumerate(zip(c.lens, (4, 7))):
+            blk = int(c.tables[b, 0])
+            x = new[int(loc[b]):int(loc[b]) + m].float().transpose(0, 1)
+            for h in range(2):
+                s0 = scales[blk, h]
+                s1 = torch.maximum(s0, s0.new_tensor(K.scale_of(float(x[h].abs().max()), fmt)))
+                assert float(got_s[blk, h]) == float(s1)
+                want = K.round_code((x[h] / s1).double(), fmt)
+                same(got[blk, h, n:n + m], want, "new")
+                was = codes[blk, h, :n].float()
+                want = K.round_code(((was * s0) / s1).double(), fmt) if float(s1) > float(s0) else was.double()
+                same(got[blk, h, :n], want, "old")
+
+
+@pytest.mark.parametrize("mode", ["auto", "single", "split"])
+def test_decode_blocks_of_minus_infinity(mode):
+    # scores of -infinity fill whole blocks, partitions and one head's whole sequence: they weigh nothing; a sequence
+    # without any other score has none to normalise (NaN), as a softmax of -infinity alone
+    c = K.Case([1100, 40, 700, 20], 4, 2, 64, "f16", seed=90, device=DEV)
+    c.q[:, :, 0] = 1.0
+    for b, upto in ((0, 600), (1, 16), (2, 0), (3, 20)):
+        for t in range(upto):
+            c.k[int(c.tables[b, t // BS]), :, t % BS, 0] = -math.inf
+    ref, bound, w, wb = K.decode_reference(c)
+    out = torch.full_like(c.q, 7.0)
+    got = torch.full((4, 2, 1100), -7.0, device=DEV)
+    pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=1100, weights_out=got, mode=mode)
+    assert status() == 0
+    for b in range(3):  # (the bound of a dot product with infinities is none: a plain tolerance for fp16 outputs)
+        err = (out[b].double() - ref[b]).abs()
+        assert bool((err <= 2.0 ** -10 * (1 + ref[b].abs())).all())
+        assert bool(((got[b, :, :c.lens[b]].double() - w[b, :, :c.lens[b]]).abs() <= 1e-5 * (1 + w[b, :, :c.lens[b]])).all())
+    assert bool(out[3].isnan().all()) and bool(ref[3].isnan().all())

@@ -347,6 +347,25 @@ def test_append_reports_bad_tables_and_lengths(fmt):
                     assert torch.equal(raw(got)[ids], raw(was)[ids]), change
 
 
+@pytest.mark.parametrize("change", ["order", "negative", "end", "ctx"])
+def test_append_reports_bad_lengths_in_a_large_batch(change):
+    # a batch whose tile slots are packed: the report does not hang on which sequences the search meets
+    lens = [3] * 100
+    c = K.Case(lens, 2, 2, 64, "int8", seed=91, device=DEV, room=[40] * 100)
+    new = [1] * 99 + [30]
+    _, k_new, v_new, loc = _chunks(c, new, 92)
+    if change == "order":
+        loc[50] = 5
+    if change == "negative":
+        loc[50] = -2 ** 31
+    if change == "end":
+        loc[100] = 2 ** 31 - 1
+    if change == "ctx":
+        c.seq_lens[7] = 2 ** 31 - 1
+    append(c, new, k_new, v_new, loc)
+    assert _flags(status()) == (False, True)
+
+
 def test_evict_reports_bad_tables_and_lengths():
     c = K.Case([100, 200, 50], 2, 2, 64, "int8", seed=74, device=DEV)
     g = torch.Generator(device=DEV).manual_seed(75)
