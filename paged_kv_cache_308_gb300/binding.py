@@ -512,7 +512,13 @@ def pa_merge_partials(out, max_logits, exp_sums, tmp_out, seq_lens, num_heads, h
 # --- the cache in 8 bits, and eviction by accumulated attention weight -------------------------------------------
 #
 # A short call's time is the host's, so these wrappers check each tensor with
-# plain attribute reads and pack the argument struct in one go.
+# plain attribute reads (a dtype is one object, compared as such), pack the
+# argument struct in one go, and read the current device and stream without
+# building torch's objects for them.
+
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+_device = getattr(torch._C, "_cuda_getDevice", None)  # (absent from builds of torch without CUDA)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 KV_FORMATS = {torch.float16: PA_KV_F16, torch.float8_e4m3fn: PA_KV_E4M3, torch.int8: PA_KV_INT8}
 
@@ -557,23 +563,23 @@ def _kv_cache(k_cache, v_cache, k_scales, v_scales, dev, what=""):
         raise ValueError(f"{what}k_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
     if dev < 0 or k_cache.get_device() != dev or not k_cache.is_contiguous():
         _bad(what + "k_cache", k_cache, dtype, shape, dev)
-    if v_cache.dtype != dtype or v_cache.get_device() != dev or v_cache.shape != shape or not v_cache.is_contiguous():
+    if (v_cache.dtype is not dtype or v_cache.get_device() != dev or v_cache.shape != shape
+            or not v_cache.is_contiguous()):
         _bad(what + "v_cache", v_cache, dtype, shape, dev)
     nb, hkv, bs, d = shape
     if fmt == PA_KV_F16:
         if k_scales is not None or v_scales is not None:
             raise ValueError(f"{what}scales come with an 8-bit cache only")
         return k_cache.data_ptr(), v_cache.data_ptr(), 0, 0, nb, hkv, d, bs, fmt
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t is None:
-            raise ValueError(f"{what}{name} is needed with an 8-bit cache")
-        if t.dtype != torch.float32 or t.get_device() != dev or t.shape != (nb, hkv) or not t.is_contiguous():
-            _bad(what + name, t, torch.float32, (nb, hkv), dev)
-    return k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), nb, hkv, d, bs, fmt
+    if k_scales is None or v_scales is None:
+        raise ValueError(f"{what}k_scales and v_scales are needed with an 8-bit cache")
+    per_block = (nb, hkv)
+    return (k_cache.data_ptr(), v_cache.data_ptr(), _tensor(what + "k_scales", k_scales, _F32, per_block, dev),
+            _tensor(what + "v_scales", v_scales, _F32, per_block, dev), nb, hkv, d, bs, fmt)
 
 
 def _tensor(name, t, dtype, shape, dev):
-    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         _bad(name, t, dtype, shape, dev)
     return t.data_ptr()
 
@@ -581,7 +587,7 @@ def _tensor(name, t, dtype, shape, dev):
 def _table(name, t, num_seqs, dev):
     """(pointer, columns) of a block table."""
     shape = t.shape
-    if t.dtype != torch.int32 or t.get_device() != dev or len(shape) != 2 or shape[0] != num_seqs or not t.is_contiguous():
+    if t.dtype is not _I32 or t.get_device() != dev or len(shape) != 2 or shape[0] != num_seqs or not t.is_contiguous():
         _bad(name, t, torch.int32, (num_seqs, "max_blocks_per_seq"), dev)
     return t.data_ptr(), shape[1]
 
@@ -589,7 +595,7 @@ def _table(name, t, num_seqs, dev):
 def _weights(name, t, num_seqs, heads, dev):
     """(pointer, tokens of a row) of a weights array."""
     shape = t.shape
-    if (t.dtype != torch.float32 or t.get_device() != dev or len(shape) != 3 or shape[0] != num_seqs
+    if (t.dtype is not _F32 or t.get_device() != dev or len(shape) != 3 or shape[0] != num_seqs
             or shape[1] != heads or not t.is_contiguous()):
         _bad(name, t, torch.float32, (num_seqs, heads, "tokens"), dev)
     return t.data_ptr(), shape[2]
@@ -617,9 +623,8 @@ def _workspace(workspace, nbytes, dev, stream):
 
 def _call(what, dev, stream, fn, *args):
     """Call fn(*args, stream) with the tensors' device current; None is that device's current stream."""
-    # (what torch.cuda.current_device and current_stream read, without building objects)
-    prev = torch._C._cuda_getDevice()
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    prev = _device()
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
     if prev == dev:
         rc = fn(*args, handle)
     else:
@@ -644,10 +649,10 @@ def pa_kv_append(k_cache, v_cache, k_scales, v_scales, k_new, v_new, block_table
     B, T = context_lens.shape[0], k_new.shape[0]
     new = (T, cache[5], cache[6])
     table, cols = _table("block_tables", block_tables, B, dev)
-    args = _APPEND.pack(*cache, _tensor("k_new", k_new, torch.float16, new, dev),
-                        _tensor("v_new", v_new, torch.float16, new, dev), table,
-                        _tensor("context_lens", context_lens, torch.int32, (B,), dev),
-                        _tensor("query_start_loc", query_start_loc, torch.int32, (B + 1,), dev), B, T, cols,
+    args = _APPEND.pack(*cache, _tensor("k_new", k_new, _F16, new, dev),
+                        _tensor("v_new", v_new, _F16, new, dev), table,
+                        _tensor("context_lens", context_lens, _I32, (B,), dev),
+                        _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev), B, T, cols,
                         int(max_query_len))
     _call("pa_kv_append", dev, stream, lib.pa_kv_append, args)
 
@@ -675,17 +680,17 @@ def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq
     B, H = q.shape[0], q.shape[1]
     hkv, dim = cache[5], cache[6]
     shape = (B, H, dim)
-    qp, op = _tensor("q", q, torch.float16, shape, dev), _tensor("out", out, torch.float16, shape, dev)
+    qp, op = _tensor("q", q, _F16, shape, dev), _tensor("out", out, _F16, shape, dev)
     table, cols = _table("block_tables", block_tables, B, dev)
     win = wout = stride = 0
     if weights_out is not None:
         wout, stride = _weights("weights_out", weights_out, B, hkv, dev)
         if weights_in is not None:
-            win = _tensor("weights_in", weights_in, torch.float32, (B, hkv, stride), dev)
+            win = _tensor("weights_in", weights_in, _F32, (B, hkv, stride), dev)
     elif weights_in is not None:
         raise ValueError("weights_in needs weights_out")
     max_seq_len = int(max_seq_len)
-    args = _DECODE.pack(op, qp, *cache, table, _tensor("seq_lens", seq_lens, torch.int32, (B,), dev), win, wout, stride,
+    args = _DECODE.pack(op, qp, *cache, table, _tensor("seq_lens", seq_lens, _I32, (B,), dev), win, wout, stride,
                         B, cols, max_seq_len, H, scale)
     opts = None
     if partition_size or mode != "auto":
@@ -719,11 +724,11 @@ def pa_kv_prefix(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, blo
     hkv, dim = cache[5], cache[6]
     shape, new = (T, H, dim), (T, hkv, dim)
     table, cols = _table("block_tables", block_tables, B, dev)
-    args = _PREFIX.pack(_tensor("out", out, torch.float16, shape, dev), _tensor("q", q, torch.float16, shape, dev),
-                        _tensor("k_new", k_new, torch.float16, new, dev),
-                        _tensor("v_new", v_new, torch.float16, new, dev), *cache, table,
-                        _tensor("context_lens", context_lens, torch.int32, (B,), dev),
-                        _tensor("query_start_loc", query_start_loc, torch.int32, (B + 1,), dev), B, T, cols,
+    args = _PREFIX.pack(_tensor("out", out, _F16, shape, dev), _tensor("q", q, _F16, shape, dev),
+                        _tensor("k_new", k_new, _F16, new, dev),
+                        _tensor("v_new", v_new, _F16, new, dev), *cache, table,
+                        _tensor("context_lens", context_lens, _I32, (B,), dev),
+                        _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev), B, T, cols,
                         int(max_context_len), int(max_query_len), H, scale)
     opts = ctypes.byref(make_opts(flags=flags, wait_limit=wait_limit)) if flags or wait_limit else None
     need = 0 if workspace is not None else lib.pa_kv_prefix_workspace_size(B, int(max_context_len), hkv, dim, cache[8])
@@ -748,9 +753,9 @@ def pa_kv_evict(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, ds
     dst_table, dst_cols = _table("dst_block_tables", dst_block_tables, B, dev)
     w, stride = _weights("weights", weights, B, hkv, dev)
     dst_w, dst_stride = (0, 0) if dst_weights is None else _weights("dst_weights", dst_weights, B, hkv, dev)
-    args = _EVICT.pack(*src, *dst, table, dst_table, _tensor("seq_lens", seq_lens, torch.int32, (B,), dev),
-                       _tensor("keep_lens", keep_lens, torch.int32, (B,), dev), w, dst_w,
-                       _tensor("kept", kept, torch.int32, (B, hkv, max_keep_len), dev),
-                       _tensor("new_lens", new_lens, torch.int32, (B,), dev), stride, dst_stride, B, cols, dst_cols,
+    args = _EVICT.pack(*src, *dst, table, dst_table, _tensor("seq_lens", seq_lens, _I32, (B,), dev),
+                       _tensor("keep_lens", keep_lens, _I32, (B,), dev), w, dst_w,
+                       _tensor("kept", kept, _I32, (B, hkv, max_keep_len), dev),
+                       _tensor("new_lens", new_lens, _I32, (B,), dev), stride, dst_stride, B, cols, dst_cols,
                        int(max_seq_len), max_keep_len, int(sinks), int(recent))
     _call("pa_kv_evict", dev, stream, lib.pa_kv_evict, args)
