@@ -512,12 +512,14 @@ int pa_merge_partials(void* out, const float* max_logits, const float* exp_sums,
  * Slots past a sequence's end may hold anything, NaN codes included.
  *
  * The four calls take argument structs, allocate no device memory (but the
- * prefill's counter, see pa_prefix), are asynchronous on `stream` and can be captured into a graph (a captured call
- * keeps its workspace: calls that may overlap need one each).  Pointers are
- * device pointers; the caches and half tensors 16-byte aligned, the rest
+ * prefill's counter, see pa_prefix), are asynchronous on `stream` and can be
+ * captured into a graph (a captured call keeps its workspace: calls that may
+ * overlap need one each).  Pointers are device pointers; the caches and half tensors 16-byte aligned, the rest
  * 4-byte, workspaces 256-byte.  Supported shapes, errors and the status word
- * are those of pa_decode; a sequence whose lengths are out of range (status
- * PA_DEV_BAD_SEQ_LEN) is skipped. */
+ * are those of pa_decode; lengths, new tokens and partition sizes go up to 2^30
+ * (PA_ERR_UNSUPPORTED beyond).  A sequence whose lengths are out of range
+ * (status PA_DEV_BAD_SEQ_LEN) is skipped; where query_start_loc is out of order,
+ * pa_kv_append may skip others with it. */
 enum {
     PA_KV_F16 = 0,
     PA_KV_E4M3 = 1,

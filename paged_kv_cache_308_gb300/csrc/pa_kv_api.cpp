@@ -19,6 +19,9 @@ namespace {
 constexpr size_t kWsAlign = 256;
 // SM count assumed by the workspace size when no device answers (above any GPU's)
 constexpr int kMaxSmsBound = 1024;
+// Tokens of a sequence at most: positions and counts of them, rounded up to any
+// kernel's step, stay ints.
+constexpr int kMaxTokens = 1 << 30;
 
 size_t up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -141,6 +144,7 @@ int check_decode(const pa_kv_decode_args* a, const pa_decode_opts* o) {
     if ((long long)a->max_seq_len > (long long)a->max_blocks_per_seq * pa::kBlockSize) return PA_ERR_INVALID_ARG;
     if (a->weights_out && a->weights_stride < a->max_seq_len) return PA_ERR_INVALID_ARG;
     if (a->weights_in && !a->weights_out) return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len > kMaxTokens || (o && o->partition_size > kMaxTokens)) return PA_ERR_UNSUPPORTED;
     // the batch's blocks are numbered in 32 bits (with a few more a sequence)
     if ((long long)a->num_seqs * (blocks_of(a->max_seq_len) + 8ll) >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     if (a->num_seqs == 0) return PA_OK;
@@ -241,6 +245,7 @@ int check_append(const pa_kv_append_args* a) {
     if (rc) return rc;
     // the largest position must be an int
     if ((long long)a->max_blocks_per_seq * pa::kBlockSize >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    if (a->num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
     if (a->num_tokens > 0 && a->max_query_len == 0) return PA_ERR_INVALID_ARG;
     if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
     if (bad_ptr(a->k_new, 16) || bad_ptr(a->v_new, 16) || bad_ptr(a->block_tables, 4) ||
@@ -354,6 +359,7 @@ int check_evict(const pa_kv_evict_args* a) {
         return PA_ERR_INVALID_ARG;
     if (a->weights_stride < a->max_seq_len || (a->dst_weights && a->dst_weights_stride < a->max_keep_len))
         return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len > kMaxTokens || a->max_keep_len > kMaxTokens) return PA_ERR_UNSUPPORTED;
     if (a->num_seqs == 0) return PA_OK;
     if (bad_ptr(a->seq_lens, 4) || bad_ptr(a->keep_lens, 4) || bad_ptr(a->new_lens, 4)) return PA_ERR_INVALID_ARG;
     if (!aligned(a->weights, 4) || !aligned(a->dst_weights, 4) || !aligned(a->kept, 4)) return PA_ERR_INVALID_ARG;
@@ -425,7 +431,7 @@ size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads,
                                    int format, int mode, int partition_size, int weights) {
     if (num_seqs <= 0 || max_seq_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || partition_size < 0 ||
         partition_size % pa::kBlockSize || mode < PA_MODE_AUTO || mode > PA_MODE_SPLIT ||
-        num_heads % num_kv_heads || pa::kv_decode_ctas(format, head_dim) < 0)
+        max_seq_len > kMaxTokens || partition_size > kMaxTokens || num_heads % num_kv_heads || pa::kv_decode_ctas(format, head_dim) < 0)
         return 0;
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK || num_sms <= 0) num_sms = kMaxSmsBound;

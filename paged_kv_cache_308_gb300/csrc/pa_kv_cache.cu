@@ -350,13 +350,19 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
     const int kv = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blk = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int to = b * prm.blocks_per_seq + blk;
-    if (kvh == 0 && threadIdx.x == 0) prm.tables[to] = to;
+    const bool first = kvh == 0 && threadIdx.x == 0;
+    if (first) prm.tables[to] = to;
     const int ctx = __ldg(prm.context_lens + b);
     // a context out of range is reported and skipped by the prefill kernel
     if (ctx < 0 || ctx > prm.max_context_len || blk * kBlockSize >= ctx) return;
     const int phys = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + blk);
     if (phys < 0 || (long long)phys >= prm.num_blocks) {
-        if (kvh == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
+        // the prefill kernel treats it like a bad block of its own
+        if (first) {
+            prm.tables[to] = -1;
+            atomicOr(prm.status, PA_DEV_BAD_BLOCK_ID);
+        }
+        if (prm.factors && lane == 0) prm.factors[2 * ((size_t)to * prm.num_kv_heads + kvh) + kv] = 1.f;
         return;
     }
     const size_t bh = (size_t)phys * prm.num_kv_heads + kvh;

@@ -633,6 +633,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
                 block_update<F, D>(st, qb, kst, kst + S::kTile, my_stages + s * S::kStage + S::kTile,
                                    min(kBlockSize, L - tok0), ks, vs, scores ? scores + tok0 : nullptr,
                                    prm.score_stride, two);
+            } else if (scores) {  // a block that is not there gets no weight
+                const int tok0 = (j0 + i * stride) * kBlockSize;
+                for (int t = g; t < min(kBlockSize, L - tok0); t += 8) {
+                    scores[tok0 + t] = -INFINITY;
+                    if (two) scores[prm.score_stride + tok0 + t] = -INFINITY;
+                }
             }
             __syncwarp();
             if (issued < cnt) {

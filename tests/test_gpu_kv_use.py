@@ -278,6 +278,40 @@ def test_decode_reports_bad_block_ids(fmt, bad):
         check(out[1:], ref[1:], bound[1:])
 
 
+@pytest.mark.parametrize("fmt", ["f16", "e4m3"])
+def test_tokens_of_a_bad_block_get_no_weight(fmt):
+    c = K.Case([700, 40, 90], 4, 2, 64, fmt, seed=74, device=DEV)
+    c.tables[0, 7] = -1
+    before = torch.rand(3, 2, 700, device=DEV)
+    out = torch.empty_like(c.q)
+    for kw in ({}, dict(mode="single"), dict(partition_size=64)):
+        ws = torch.full((1 << 22,), 0.5, device=DEV)  # what an earlier call may have left as scores
+        got = before.clone()
+        pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=700, weights_in=got,
+                          weights_out=got, workspace=ws, **kw)
+        assert _flags(status()) == (True, False)
+        assert torch.equal(got[0, :, 112:128], before[0, :, 112:128])
+        # the others' still add up to one a query head (2^-12 for p's sum of 684 terms, half an ulp of the sums)
+        rest = (got - before)[0].double().sum(dim=1)
+        assert bool(((rest - 2).abs() < 1e-3).all())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_prefix_with_a_bad_block_does_not_read_an_old_workspace(fmt):
+    c = K.Case([128, 64], 4, 2, 64, fmt, seed=75, device=DEV)
+    q, k_new, v_new, loc = _chunks(c, [20, 9], 76)
+    c.tables[0, 3] = 10 ** 6
+    outs = []
+    for fill in (0x00, 0x7f):
+        ws = torch.full((1 << 22,), fill, dtype=torch.uint8, device=DEV)
+        out = torch.empty_like(q)
+        pb().pa_kv_prefix(out, q, k_new, v_new, *c.cache(), c.tables, c.seq_lens, loc, c.scale, max_context_len=128,
+                          max_query_len=20, workspace=ws)
+        assert _flags(status()) == (True, False)
+        outs.append(out.clone())
+    assert torch.equal(outs[0], outs[1]) and bool(torch.isfinite(outs[0]).all())
+
+
 @pytest.mark.parametrize("bad", [-1, 701, 2 ** 31 - 1, -2 ** 31])
 def test_decode_reports_bad_lengths(bad):
     c = K.Case([700, 40, 90], 4, 2, 64, "e4m3", seed=71, device=DEV)

@@ -159,6 +159,27 @@ def test_evict_refusals(kw, code):
     assert call("pa_kv_evict", evict_args(**kw)) == code
 
 
+def test_lengths_past_2_to_the_30_are_refused():
+    top = 1 << 30
+    wide = dict(mbps=1 << 27, stride=1 << 31)
+    for n in (top + 1, 2 ** 31 - 1):
+        assert call("pa_kv_decode", decode_args(B=1, max_len=n, **wide), None, FAKE, 1 << 62) == pb.PA_ERR_UNSUPPORTED
+        assert call("pa_kv_evict", evict_args(mbps=1 << 27, max_len=n, ws=1 << 31)) == pb.PA_ERR_UNSUPPORTED
+        assert call("pa_kv_evict", evict_args(dmbps=1 << 27, max_keep=n, dws=1 << 31)) == pb.PA_ERR_UNSUPPORTED
+        assert call("pa_kv_append", append_args(T=n, max_q=n)) == pb.PA_ERR_UNSUPPORTED
+        assert pb.pa_kv_decode_workspace_size(1, n, 24, 4, 256, torch.int8) == 0
+    big = (2 ** 31 - 16)
+    assert call("pa_kv_decode", decode_args(), pb.make_opts(partition_size=big), FAKE, 1 << 62) == pb.PA_ERR_UNSUPPORTED
+    assert pb.pa_kv_decode_workspace_size(1, 100, 24, 4, 256, torch.int8, partition_size=big) == 0
+    # and the largest one is accepted up to its workspace: 24 heads, partitions of 2^30 and of 2^20 tokens
+    for part, slots in ((top, 1), (1 << 20, 1 << 10)):
+        o = pb.make_opts(partition_size=part)
+        n = pb.pa_kv_decode_workspace_size(1, top, 24, 4, 256, torch.int8, partition_size=part)
+        assert n == (slots * 24 * (8 + 256 * 4) if slots > 1 else 0)
+        if n:
+            assert call("pa_kv_decode", decode_args(B=1, max_len=top, **wide), o, FAKE, n - 1) == pb.PA_ERR_WORKSPACE
+
+
 def test_null_arguments_and_empty_calls():
     for fn in ("pa_kv_append", "pa_kv_evict"):
         assert getattr(pb.lib, fn)(None, None) == pb.PA_ERR_INVALID_ARG
