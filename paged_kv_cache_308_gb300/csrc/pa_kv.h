@@ -35,11 +35,15 @@ struct KvDecodeParams {
     int* seq_parts;  // flat: [B][8], where the partials of the sequences with tokens are
     float* scores;   // [B][H][score_stride], log2 domain; null without weights
     long long score_stride;
+    const float* weights_in;  // cluster form: null: zeros
+    float* weights_out;       // cluster form: null: none
+    long long weights_stride;
     long long num_blocks, slots;
     int num_seqs, num_heads, num_kv_heads, group;
     int max_blocks_per_seq, max_seq_len;
     int flat, ctas_per_head;                // flat form
     int partition_size, max_partitions;     // grid form
+    int cluster;                            // cluster form: CTAs of a cluster (1: no cluster); else 0
     float scale_log2;
     unsigned int* status;
 };
@@ -61,6 +65,7 @@ struct KvMergeParams {
 };
 
 constexpr int kKvWarps = 4;                        // of a decode CTA
+constexpr int kKvMaxCluster = 8;                   // decode CTAs of a cluster (portable)
 int kv_decode_ctas(int format, int head_dim);      // decode CTAs an SM holds at once; -1: not compiled
 cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, dim3 grid, cudaStream_t stream);
 constexpr int kKvWeightsTokens = 1024;  // tokens of a CTA that adds weights

@@ -55,17 +55,23 @@ struct DecodePlan {
     bool flat;
     int ctas_per_head;          // flat
     int partition_size, parts;  // grid
+    int cluster;                // CTAs of a cluster that has a (sequence, kv head) to itself, else 0; 1: a CTA that
+                                // adds its weights itself
     long long slots;            // partials of a kv head
 };
 
-// Which form (us per call on GB300, e4m3, flat shares against one CTA per
-// sequence and kv head):
-// * up to kSingleMaxLen tokens one CTA each, with no merge: 2 x 512 tokens of 8
-//   x 128: 8.0 against 7.1, 8 x 256 8.5 / 4.7, 32 x 512 15.5 / 11.9, 128 x 512
-//   34.0 / 30.7, 512 x 256 63.5 / 59.3; 4 x 256 likewise (2 x 512: 8.7 / 8.8);
-// * up to kSingleManyMaxLen where the pairs nearly fill the SMs: 32 x 1024 of 8
-//   x 128 19.5 / 19.0, of 4 x 256 20.6 / 17.4; 128 x U[1, 1024] 34.3 / 33.4; with
-//   few pairs the flat form wins there (8 x 1024: 11.3 / 13.0);
+// Which form (us per call on GB300, replayed from a graph):
+// * up to kSingleMaxLen tokens one CTA per (sequence, kv head), with no merge: 8
+//   x 128 tokens of 4 x 256 in e4m3 4.9 against 5.8 in clusters, 16 x 512 of 8 x
+//   128 7.7 / 8.1, 128 x 512 30.7 / 34.0 in equal shares;
+// * a cluster per pair, which merges over distributed shared memory in the same
+//   launch, while it has room and few rounds (see cluster_ctas): 8 x 512 of 4 x
+//   256 6.7 against 9.6 with one CTA, 8 x 2048 10.9 / 14.1 in equal shares, 4 x
+//   U[1, 2048] of 8 x 128 6.6 / 9.1; with the weights 2 x 512 of 4 x 256 7.4 /
+//   12.8, 2 x 2048 10.0 / 11.2;
+// * one CTA per pair up to kSingleManyMaxLen where the pairs nearly fill the SMs:
+//   32 x 1024 of 8 x 128 19.0 against 19.5 in equal shares, of 4 x 256 17.4 /
+//   20.6; 128 x U[1, 1024] 33.4 / 34.3;
 // * one sequence: a wave of equal partitions, whose block ids can be read before
 //   its length is known;
 // * other batches: equal shares for the CTAs the SMs hold at once (against the
@@ -76,22 +82,60 @@ struct DecodePlan {
 // A caller's partition size gives the grid of partitions.
 constexpr int kSingleOneMaxLen = 128, kSingleMaxLen = 512, kSingleManyMaxLen = 1024;
 
+// CTAs of the clusters that take a pair each, or 0 for another form.  The most
+// that leave every warp a block, up to the portable 8, that the SMs hold at
+// once: clusters fill 85 % of the places, those of 8 with one CTA per SM half
+// of them (4 x 1024 of 4 x 256 in fp16, 128 CTAs of 8 on 152 SMs: 12.3 us against
+// 8.4 in clusters of 4).  Two CTAs only beat one above 512 tokens (16 of 8 x 128:
+// 512 tokens 8.1 / 7.7, 1024 12.5 / 13.7).  A pair's time grows with its blocks
+// per warp, as others' do not: up to 8 rounds (4 x 4096 of 4 x 256 13.6 against
+// 14.2 in equal shares; at 16, 8 x 4096 of 8 x 128 19.3 / 19.2 and with uniform
+// lengths 12.6 / 11.4), with the weights, which need them again, 4 (8 rounds:
+// 2 x 4096 of 4 x 256 13.2 / 12.0).  One sequence, whose partitions have more CTAs,
+// without weights only and up to 4: 2048 tokens take 7.9 against 7.7, but the
+// launch less saves the host 2.
+int cluster_ctas(int num_seqs, int max_seq_len, int num_kv_heads, int ctas, int num_sms, bool weights) {
+    const int blocks = blocks_of(max_seq_len);
+    if (blocks * pa::kBlockSize <= kSingleOneMaxLen) return 0;
+    const long long pairs = (long long)num_seqs * num_kv_heads, room = (long long)ctas * num_sms;
+    int c = pa::kKvMaxCluster;
+    while (c >= 2 && (blocks <= pa::kKvWarps * (c / 2) || pairs * c * 20 > room * (c == 8 && ctas == 1 ? 10 : 17)))
+        c /= 2;
+    if (c < 2 || (c == 2 && blocks * pa::kBlockSize <= kSingleMaxLen)) return 0;
+    const int rounds = (blocks + pa::kKvWarps * c - 1) / (pa::kKvWarps * c);
+    const int most = num_seqs == 1 ? (weights ? 0 : 4) : (weights ? 4 : 8);
+    return rounds <= most ? c : 0;
+}
+
 DecodePlan plan_decode(int num_seqs, int max_seq_len, int num_kv_heads, int head_dim, int format, int num_sms,
-                       int partition_size, int mode) {
+                       int partition_size, int mode, bool weights) {
     DecodePlan p{};
     const int whole = std::max(1, blocks_of(max_seq_len)) * pa::kBlockSize;
+    const int ctas = pa::kv_decode_ctas(format, head_dim);
+    if (mode == PA_MODE_AUTO && partition_size <= 0 &&
+        (p.cluster = cluster_ctas(num_seqs, max_seq_len, num_kv_heads, ctas, num_sms, weights))) {
+        p.partition_size = whole;
+        p.parts = 1;
+        return p;
+    }
     const bool many = (long long)num_seqs * num_kv_heads * 4 >= num_sms * 3ll;
     if (mode == PA_MODE_SINGLE || (partition_size <= 0 && mode == PA_MODE_AUTO && num_seqs > 1 &&
                                    max_seq_len <= (many ? kSingleManyMaxLen : kSingleMaxLen)))
         partition_size = whole;
     if (partition_size <= 0 && mode == PA_MODE_AUTO && max_seq_len <= kSingleOneMaxLen) partition_size = whole;
-    const long long slots = std::max(1ll, (long long)pa::kv_decode_ctas(format, head_dim) * num_sms / num_kv_heads);
+    const long long slots = std::max(1ll, (long long)ctas * num_sms / num_kv_heads);
     if (partition_size <= 0 && num_seqs == 1)  // (one block per warp at least)
         partition_size =
             std::max(blocks_of((max_seq_len + slots - 1) / slots), pa::kKvWarps) * pa::kBlockSize;
     if (partition_size > 0) {
         p.partition_size = std::min(partition_size, whole);
         p.parts = std::max(1, (max_seq_len + p.partition_size - 1) / p.partition_size);
+        // A CTA with a whole sequence adds its weights itself while that is short and
+        // the grid at most one and a half times what the SMs hold (with and without a
+        // launch of their own: 8 x 128 of 4 x 256 in e4m3 7.6 / 6.2 us, 32 x 512 of 8 x
+        // 128 15.0 / 14.5; 32 x 1024 23.6 / 25.2, 256 x 300 47.5 / 50.9).
+        const long long pairs = (long long)num_seqs * num_kv_heads;
+        if (p.parts == 1 && weights && max_seq_len <= kSingleMaxLen && pairs * 2 <= 3ll * ctas * num_sms) p.cluster = 1;
         p.slots = (long long)num_seqs * p.parts;
         return p;
     }
@@ -111,7 +155,7 @@ DecodeSpace decode_space(const DecodePlan& p, int num_seqs, int num_heads, int n
     DecodeSpace s;
     const size_t rows = (size_t)p.slots * num_heads;  // slots of a kv head x kv heads x group
     const bool split = p.flat || p.parts > 1;
-    s.parts = split || weights ? up(rows * 8) : 0;
+    s.parts = split || (weights && !p.cluster) ? up(rows * 8) : 0;
     s.acc = s.parts + (p.flat ? up((size_t)num_seqs * 32) : 0);
     s.scores = s.acc + (split ? up(rows * head_dim * 4) : 0);
     s.score_stride = (long long)blocks_of(max_seq_len) * pa::kBlockSize;
@@ -163,9 +207,9 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     const pa_kv_cache& c = a->cache;
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;  // the launch reports the missing device
-    const DecodePlan plan = plan_decode(a->num_seqs, a->max_seq_len, c.num_kv_heads, c.head_dim, c.format, num_sms,
-                                        o ? o->partition_size : 0, o ? o->mode : PA_MODE_AUTO);
     const bool weights = a->weights_out && a->max_seq_len > 0;
+    const DecodePlan plan = plan_decode(a->num_seqs, a->max_seq_len, c.num_kv_heads, c.head_dim, c.format, num_sms,
+                                        o ? o->partition_size : 0, o ? o->mode : PA_MODE_AUTO, weights);
     const DecodeSpace sp =
         decode_space(plan, a->num_seqs, a->num_heads, c.num_kv_heads, c.head_dim, a->max_seq_len, weights);
     if (sp.bytes > 0 && (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign))) return PA_ERR_WORKSPACE;
@@ -181,11 +225,14 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     p.v_scales = c.v_scales;
     p.block_tables = a->block_tables;
     p.seq_lens = a->seq_lens;
-    p.sums = split || weights ? reinterpret_cast<float2*>(w) : nullptr;
+    p.sums = split || (weights && !plan.cluster) ? reinterpret_cast<float2*>(w) : nullptr;
     p.seq_parts = plan.flat ? reinterpret_cast<int*>(w + sp.parts) : nullptr;
     p.acc = split ? reinterpret_cast<float*>(w + sp.acc) : nullptr;
     p.scores = weights ? reinterpret_cast<float*>(w + sp.scores) : nullptr;
     p.score_stride = sp.score_stride;
+    p.weights_in = a->weights_in;
+    p.weights_out = weights && plan.cluster ? a->weights_out : nullptr;
+    p.weights_stride = a->weights_stride;
     p.num_blocks = c.num_blocks;
     p.slots = plan.slots;
     p.num_seqs = a->num_seqs;
@@ -198,13 +245,14 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     p.ctas_per_head = plan.ctas_per_head;
     p.partition_size = plan.partition_size;
     p.max_partitions = plan.parts;
+    p.cluster = plan.cluster;
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
     const dim3 grid = plan.flat ? dim3(plan.ctas_per_head * c.num_kv_heads)
-                                : dim3(plan.parts, c.num_kv_heads, a->num_seqs);
+                                : dim3(plan.cluster ? plan.cluster : plan.parts, c.num_kv_heads, a->num_seqs);
     if (pa::launch_kv_decode(c.format, c.head_dim, p, grid, stream) != cudaSuccess) return PA_ERR_CUDA;
-    if (!split && !weights) return PA_OK;
+    if (plan.cluster || (!split && !weights)) return PA_OK;
     pa::KvMergeParams m{};
     m.out = p.out;
     m.sums = p.sums;
@@ -436,7 +484,8 @@ size_t pa_kv_decode_workspace_size(int num_seqs, int max_seq_len, int num_heads,
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK || num_sms <= 0) num_sms = kMaxSmsBound;
     const DecodePlan plan =
-        plan_decode(num_seqs, max_seq_len, num_kv_heads, head_dim, format, num_sms, partition_size, mode);
+        plan_decode(num_seqs, max_seq_len, num_kv_heads, head_dim, format, num_sms, partition_size, mode,
+                    weights != 0);
     return decode_space(plan, num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len, weights != 0).bytes;
 }
 

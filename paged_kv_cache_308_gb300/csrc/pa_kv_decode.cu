@@ -1,8 +1,8 @@
 // Decode attention over a cache in 8 bits (or fp16), and the accumulation of
 // its attention weights.
 //
-// kv_partition_kernel<F, D, NS>: one CTA per (partition, kv head, sequence),
-// the decomposition of pa_partition_kernel, over cache format F.  The math
+// kv_partition_kernel<F, D, NS, Cluster>: the decomposition of pa_partition_kernel
+// (partitions of a sequence, by kv head) over cache format F.  The math
 // per 16-token block, for the <= 8 query heads of a kv head (log2 domain,
 // c = scale * log2 e):
 //     s[t, h] = c ks sum_d k8[t, d] q[h, d]             ks, vs: the block's scales
@@ -46,6 +46,10 @@
 // grows, so slots never collide) or, if it is the whole sequence, the output.
 // Grid form (one sequence, a partition size was given, or every sequence fits
 // one CTA): one CTA per (partition, kv head, sequence).
+// Cluster form (few and short sequences): a cluster of CTAs per (kv head,
+// sequence), whose warps take the blocks in turns.  It merges over distributed
+// shared memory and adds the weights itself: no second launch, which costs
+// about 3 us on the device and 2 on the host.
 //
 // kv_merge_kernel: the log-sum-exp merge of the partials, and in further CTAs
 // of the same launch weights_out = weights_in + sum_h 2^(s - lse) from the
@@ -53,6 +57,7 @@
 // and read again, instead of K's D bytes a second time.
 #include "pa_kv.h"
 
+#include <cooperative_groups.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -61,6 +66,8 @@
 
 namespace pa {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr float kShift = 14.f;
 constexpr int kLead = 6;  // units a sequence counts beyond its blocks
@@ -427,12 +434,15 @@ __device__ __forceinline__ void block_update(WarpState<D>& st, const uint32_t (&
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <int F, int D, int NS>
+// Cluster: the cluster form (of its own, so that the others keep their code: in
+// one kernel 64 x 128 tokens of 8 x 128 took 8.2 instead of 7.4 us).
+template <int F, int D, int NS, bool Cluster>
 __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     kv_partition_kernel(const KvDecodeParams prm) {
     using S = KvShape<F, D, NS>;
     constexpr int NW = S::kNW;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 part_ml[kMaxGroup];  // cluster form: the CTA's (reference, sum) by head
     float* sm_m = reinterpret_cast<float*>(smem + S::kArea);
     float* sm_l = sm_m + NW * kMaxGroup;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -464,8 +474,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     int kvh, b, j0, cnt, stride, cta, nseq;
     int units = 0, end = 0, first = 0;  // flat, by warp: the run's end and sequence b's first unit
     bool whole = true;
+    bool joint = false;  // the CTAs of the cluster merge
     int ids_early = -1;  // grid form: ids read before the length is known
-    if (prm.flat) {
+    if (!Cluster && prm.flat) {
         kvh = blockIdx.x % prm.num_kv_heads;
         cta = blockIdx.x / prm.num_kv_heads;
         // lane i has sequences [i per, (i + 1) per)
@@ -517,12 +528,13 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         kvh = blockIdx.y;
         b = blockIdx.z;
         cta = blockIdx.x;
-        stride = NW;
-        const int each = prm.partition_size / kBlockSize, lo = cta * each;
+        // a partition's blocks are its own; the CTAs of a cluster take turns
+        stride = Cluster ? NW * prm.cluster : NW;
+        const int each = prm.partition_size / kBlockSize, lo = cta * (Cluster ? NW : each);
         j0 = lo + warp;
         // bounded by the table's row
-        if (lane * NW + warp < each && j0 + lane * NW < prm.max_blocks_per_seq)
-            ids_early = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + j0 + lane * NW);
+        if ((Cluster || lane * NW + warp < each) && j0 + lane * stride < prm.max_blocks_per_seq)
+            ids_early = __ldg(prm.block_tables + (size_t)b * prm.max_blocks_per_seq + j0 + lane * stride);
         nseq = blocks(b);
         if (nseq == 0 && cta == 0) {  // (there may be no merge to do this)
             if (__ldg(prm.seq_lens + b) != 0) {
@@ -532,9 +544,11 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
                     prm.out[((size_t)b * H + kvh * G) * D + i] = __float2half_rn(0.f);
             }
         }
-        const int n = min(nseq - lo, each);
-        if (n <= 0) return;
-        cnt = n > warp ? (n - warp + NW - 1) / NW : 0;
+        if (nseq == 0) return;
+        joint = Cluster && prm.cluster > 1 && nseq > NW;  // else the first CTA has it all
+        const int n = Cluster ? nseq - lo : min(nseq - lo, each);
+        if (n <= 0 && !joint) return;
+        cnt = n > warp ? (n - warp + stride - 1) / stride : 0;
     }
 
     // Ids and scales of the segment's iterations, 32 at a time: lane k of batch
@@ -583,7 +597,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     WarpState<D> st;
     for (;;) {
         const int L = length(b);
-        if (prm.flat && j0 == 0 && kvh == 0 && lane == 0 && cnt > 0) {
+        if (!Cluster && prm.flat && j0 == 0 && kvh == 0 && lane == 0 && cnt > 0) {
             // where the merge finds the sequence's partials
             const FlatRuns runs(units, prm.ctas_per_head);
             const SeqParts parts(runs, first, nseq, b);
@@ -611,7 +625,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
 
         // a warp's next segment (runs of their own): the next sequence with tokens
         int b_next = b, n_next = 0, first_next = first, cnt_next = 0;
-        if (!whole && first + kLead + nseq < end) {
+        if (!Cluster && !whole && first + kLead + nseq < end) {
             first_next = first + kLead + nseq;
             do n_next = blocks(++b_next);
             while (n_next == 0);  // the run goes on, so there is one
@@ -662,7 +676,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
             st.l1 += __shfl_xor_sync(kFull, st.l1, off);
         }
         if (F == PA_KV_F16) st.vr = 1.f;
-        if (whole) break;
+        if (Cluster || whole) break;
 
         // the segment's partial, or the output, straight from the fragments
         if (cnt > 0) {
@@ -745,7 +759,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
     __syncthreads();
     constexpr int kSlice = D / NW;
     const int h = lane >> 2, qd = lane & 3;
-    if (h >= G) return;
+    if (!Cluster && h >= G) return;
     float Mh = sm_m[h];
 #pragma unroll
     for (int w = 1; w < NW; ++w) Mh = fmaxf(Mh, sm_m[w * kMaxGroup + h]);
@@ -757,11 +771,12 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
         Lh += f[w] * sm_l[w * kMaxGroup + h];
     }
     const size_t head = (size_t)b * H + kvh * G + h;
-    const size_t slot = prm.flat ? (size_t)cta : (size_t)b * prm.max_partitions + cta;
+    const size_t slot = !Cluster && prm.flat ? (size_t)cta : (size_t)b * prm.max_partitions + cta;
     const size_t pi = ((size_t)kvh * prm.slots + slot) * G + h;
     // the CTA has the whole sequence: its run begins in or before block 0 and ends with the last
-    const bool direct = j0 == warp && (prm.flat ? FlatRuns(units, prm.ctas_per_head).begin(cta + 1) == first + kLead + nseq
-                                                : prm.partition_size / kBlockSize >= nseq);
+    const bool direct = !joint && j0 == warp &&
+                        (!Cluster && prm.flat ? FlatRuns(units, prm.ctas_per_head).begin(cta + 1) == first + kLead + nseq
+                                  : Cluster || prm.partition_size / kBlockSize >= nseq);
     const float inv = Lh == 0.f && !direct ? 0.f : 1.f / Lh;
 #pragma unroll
     for (int w = 0; w < NW; ++w) f[w] *= inv;
@@ -775,13 +790,102 @@ __global__ void __launch_bounds__(kKvWarps * 32, ctas_of<F, D>())
             v0 += f[w] * rw[0];
             v1 += f[w] * rw[1];
         }
-        if (direct)
+        if (joint)  // over the first warp's, which only this lane reads
+            *reinterpret_cast<float2*>(red + h * S::kRedStride + d) = make_float2(v0, v1);
+        else if (direct && h < G)
             *reinterpret_cast<__half2*>(prm.out + head * D + d) = __floats2half2_rn(v0, v1);
-        else
+        else if (!Cluster)
             *reinterpret_cast<float2*>(prm.acc + pi * D + d) = make_float2(v0, v1);
     }
     // the sum is relative to 2^(M - kShift): log2 of the whole is its reference plus log2 l
-    if (warp == 0 && qd == 0 && prm.sums) prm.sums[pi] = make_float2(Mh - kShift, Lh);
+    if constexpr (!Cluster) {
+        if (warp == 0 && qd == 0 && prm.sums) prm.sums[pi] = make_float2(Mh - kShift, Lh);
+        return;
+    }
+    if (warp == 0 && qd == 0) part_ml[h] = make_float2(Mh, Lh);
+    if (joint) {
+        // The cluster's CTAs merge over distributed shared memory, each a share of
+        // the G D / 4 columns of four, all reads of a column on their way at once.
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const int CS = prm.cluster;
+        auto weights_of = [&](int head_, float (&w)[kKvMaxCluster]) {  // 2^(M_r - M) l_r of the CTAs; their sum's log2
+            float2 ml[kKvMaxCluster];
+            float M = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int r = 0; r < kKvMaxCluster; ++r)
+                ml[r] = r < CS ? *cluster.map_shared_rank(part_ml + head_, r) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int r = 0; r < kKvMaxCluster; ++r) M = fmaxf(M, ml[r].x);
+#pragma unroll
+            for (int r = 0; r < kKvMaxCluster; ++r) {
+                w[r] = ml[r].x == -INFINITY ? 0.f : exp2f(ml[r].x - M) * ml[r].y;
+                l += w[r];
+            }
+            return make_float2(M, l);
+        };
+        const int share = (G * (D / 4) + CS - 1) / CS;
+        const int end_col = min(G * (D / 4), (cta + 1) * share);
+        for (int col = cta * share + (int)threadIdx.x; col < end_col; col += NW * 32) {
+            const int hh = col / (D / 4), d = col % (D / 4) * 4;
+            float4 v[kKvMaxCluster];
+            float w[kKvMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kKvMaxCluster; ++r)
+                v[r] = r < CS ? *reinterpret_cast<const float4*>(cluster.map_shared_rank(red + hh * S::kRedStride + d, r))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float inv_l = 1.f / weights_of(hh, w).y;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kKvMaxCluster; ++r) {
+                a.x += w[r] * v[r].x;
+                a.y += w[r] * v[r].y;
+                a.z += w[r] * v[r].z;
+                a.w += w[r] * v[r].w;
+            }
+            const __half2 o2[2] = {__floats2half2_rn(a.x * inv_l, a.y * inv_l),
+                                   __floats2half2_rn(a.z * inv_l, a.w * inv_l)};
+            *reinterpret_cast<uint2*>(prm.out + ((size_t)b * H + kvh * G + hh) * D + d) =
+                *reinterpret_cast<const uint2*>(o2);
+        }
+        if (prm.weights_out && threadIdx.x < G) {
+            float w[kKvMaxCluster];
+            const float2 ml = weights_of(threadIdx.x, w);
+            sm_m[threadIdx.x] = ml.x - kShift + log2f(ml.y);
+        }
+        cluster.sync();  // no CTA leaves while another may still read from it
+    } else {
+        __syncthreads();
+        if (threadIdx.x < G) sm_m[threadIdx.x] = part_ml[threadIdx.x].x - kShift + log2f(part_ml[threadIdx.x].y);
+        __syncthreads();
+    }
+    if (!prm.weights_out) return;
+    // the weights of the warp's own tokens, from the scores that it left
+    const size_t row = ((size_t)b * prm.num_kv_heads + kvh) * prm.weights_stride;
+    const float* sc = prm.scores + ((size_t)b * H + kvh * G) * prm.score_stride;
+    const int L = length(b);
+    constexpr int kAtOnce = 2;  // pairs of blocks whose loads are in flight together
+    for (int i = lane >> 4; i < cnt; i += 2 * kAtOnce) {
+        float s[kAtOnce][kMaxGroup], w[kAtOnce];
+        int tok[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int t = (j0 + (i + 2 * k) * stride) * kBlockSize + (lane & 15);
+            const bool in = i + 2 * k < cnt && t < L;
+            tok[k] = in ? t : -1;
+            w[k] = in && prm.weights_in ? prm.weights_in[row + t] : 0.f;
+#pragma unroll
+            for (int x = 0; x < kMaxGroup; ++x) s[k][x] = in && x < G ? sc[x * prm.score_stride + t] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < kMaxGroup; ++x)
+                if (x < G) sum += pow2_of(s[k][x] - sm_m[x]);
+            if (tok[k] >= 0) prm.weights_out[row + tok[k]] = w[k] + sum;
+        }
+    }
 }
 
 // Blocks x < slices of a (sequence, kv head): `cols` float4 columns of the
@@ -942,13 +1046,13 @@ __global__ void __launch_bounds__(kMergeThreads, 4) kv_merge_kernel(const KvMerg
     }
 }
 
-template <int F, int D>
+template <int F, int D, bool Cluster>
 cudaError_t launch_fd(const KvDecodeParams& prm, dim3 grid, cudaStream_t stream) {
     constexpr int NS = stages_of<F, D>();
     using S = KvShape<F, D, NS>;
     static_assert(ctas_of<F, D>() * (S::kSmem + 1024 + 64) <= 228 * 1024, "shared memory of an SM");
     static std::atomic<unsigned long long> done{0};
-    auto kern = kv_partition_kernel<F, D, NS>;
+    auto kern = kv_partition_kernel<F, D, NS, Cluster>;
     cudaError_t e = once_per_device(done, [&] {
         cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         return r != cudaSuccess ? r : cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -959,9 +1063,15 @@ cudaError_t launch_fd(const KvDecodeParams& prm, dim3 grid, cudaStream_t stream)
     cfg.blockDim = dim3(kKvWarps * 32);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr = pdl_attribute();
-    cfg.attrs = &attr;
+    cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (prm.cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = prm.cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
@@ -981,7 +1091,8 @@ int kv_decode_ctas(int format, int head_dim) {
 
 cudaError_t launch_kv_decode(int format, int head_dim, const KvDecodeParams& prm, dim3 grid, cudaStream_t stream) {
 #define PA_CASE(F_, D_) \
-    if (format == F_ && head_dim == D_) return launch_fd<F_, D_>(prm, grid, stream);
+    if (format == F_ && head_dim == D_) \
+        return prm.cluster ? launch_fd<F_, D_, true>(prm, grid, stream) : launch_fd<F_, D_, false>(prm, grid, stream);
     PA_KV_FOR_FD(PA_CASE)
 #undef PA_CASE
     return cudaErrorInvalidValue;

@@ -52,8 +52,9 @@ def test_decode_lengths(fmt, heads, hkv, dim):
     for b, n in enumerate(c.lens):
         check(got[b, :, :n], w[b, :, :n], wb[b, :, :n] + 1e-30, "weights")
         assert bool((got[b, :, n:] == -7).all())  # nothing is written past the end
-    # without weights the output has the same bits
-    assert torch.equal(decode(c), out)
+    # in the same form the output has the same bits without the weights
+    for mode in ("single", "split"):
+        assert torch.equal(decode(c, mode=mode), decode(c, weights=True, mode=mode)[0])
 
 
 @pytest.mark.parametrize("fmt", ["f16", "e4m3", "int8"])
@@ -448,6 +449,31 @@ def test_decode_ragged_batches(fmt, B, top, long, hkv, dim):
         check(got[b, :, :n], w[b, :, :n], wb[b, :, :n] + 1e-30)
         assert bool((got[b, :, n:] == -7).all())
     assert torch.equal(decode(c), out) and torch.equal(decode(c), out)
+
+
+@pytest.mark.parametrize("mode", ["auto", "split"])
+@pytest.mark.parametrize("fmt", ["f16", "e4m3", "int8"])
+@pytest.mark.parametrize("heads,hkv,dim,B", [(6, 1, 256, 1), (24, 4, 256, 3), (32, 8, 128, 8), (8, 8, 64, 20), (7, 1, 128, 70),
+                                             (3, 3, 64, 2)])
+def test_decode_forms(mode, fmt, heads, hkv, dim, B):
+    # few and short sequences in clusters of 2, 4 and 8 CTAs (auto) and in equal shares: lengths that leave CTAs and warps
+    # without blocks, one block past a round, none
+    lens = ([1000, 0, 1, 64, 65, 513, 130, 16] + [(37 * i) % 600 for i in range(B)])[:B]
+    c = K.Case(lens, heads, hkv, dim, fmt, seed=34, device=DEV, extra_cols=2)
+    ref, bound, w, wb = K.decode_reference(c)
+    start = torch.rand(B, hkv, c.max_len, device=DEV)
+    for again in range(2):
+        out, got = decode(c, weights=True, w_in=start, mode=mode)
+        check(out, ref, bound)
+        for b, n in enumerate(c.lens):
+            # (adding the old weight rounds the sum once more, by 2^-24 of at most 1 + the heads)
+            check(got[b, :, :n], w[b, :, :n] + start[b, :, :n].double(), wb[b, :, :n] + (1 + heads / hkv) * 2.0 ** -24)
+            assert bool((got[b, :, n:] == -7).all())
+        plain = decode(c, mode=mode)  # (with and without the weights the form may differ)
+        check(plain, ref, bound)
+        if again:
+            assert torch.equal(plain, first[0]) and torch.equal(out, first[1]) and torch.equal(got, first[2])
+        first = plain, out, got
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])

@@ -272,7 +272,7 @@ def test_decode_reports_bad_block_ids(fmt, bad):
     ref, bound, _, _ = K.decode_reference(c)
     c.tables[0, 7] = bad
     out = torch.full_like(c.q, math.nan)
-    for kw in ({}, dict(mode="single"), dict(partition_size=64)):
+    for kw in ({}, dict(mode="single"), dict(mode="split"), dict(partition_size=64)):
         pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=700, **kw)
         assert _flags(status()) == (True, False)
         check(out[1:], ref[1:], bound[1:])
@@ -284,7 +284,7 @@ def test_tokens_of_a_bad_block_get_no_weight(fmt):
     c.tables[0, 7] = -1
     before = torch.rand(3, 2, 700, device=DEV)
     out = torch.empty_like(c.q)
-    for kw in ({}, dict(mode="single"), dict(partition_size=64)):
+    for kw in ({}, dict(mode="single"), dict(mode="split"), dict(partition_size=64)):
         ws = torch.full((1 << 22,), 0.5, device=DEV)  # what an earlier call may have left as scores
         got = before.clone()
         pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=700, weights_in=got,
@@ -317,7 +317,7 @@ def test_decode_reports_bad_lengths(bad):
     c = K.Case([700, 40, 90], 4, 2, 64, "e4m3", seed=71, device=DEV)
     ref, bound, w, wb = K.decode_reference(c)
     c.seq_lens[1] = bad
-    for kw in ({}, dict(mode="single"), dict(partition_size=64)):
+    for kw in ({}, dict(mode="single"), dict(mode="split"), dict(partition_size=64)):
         out = torch.full_like(c.q, math.nan)
         got = torch.full((3, 2, 700), -7.0, device=DEV)
         pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=700, weights_out=got, **kw)

@@ -102,11 +102,17 @@ def test_decode_options_and_workspace_are_checked():
 
 def test_decode_workspace_follows_the_plan():
     size = lambda B, L, **kw: pb.pa_kv_decode_workspace_size(B, L, 24, 4, 256, torch.int8, **kw)
-    # one CTA per (sequence, kv head): nothing to merge; the weights still need the sums and the scores
+    # one CTA or one cluster per (sequence, kv head): nothing to merge; the weights still need the scores, and the sums
+    # where another launch adds them
     up = lambda x: -(-x // 256) * 256
-    assert size(8, 512) == 0 and size(1, 128) == 0 and size(8, 4000, mode="single") == 0
-    assert size(8, 512, weights=True) == up(8 * 24 * 8) + 8 * 24 * 512 * 4
-    assert size(8, 512, mode="split") > 0 and size(1, 129) > 0 and size(8, 513) > 0
+    assert size(1, 128) == 0 and size(8, 128) == 0 and size(8, 4000, mode="single") == 0
+    assert size(8, 128, weights=True) == 8 * 24 * 128 * 4
+    assert size(8, 4000, mode="single", weights=True) == up(8 * 24 * 8) + 8 * 24 * 4000 * 4
+    assert size(1, 2048) == 0 and size(8, 512) == 0 and size(2, 4096) == 0
+    assert size(8, 512, weights=True) == 8 * 24 * 512 * 4 and size(2, 2048, weights=True) == 2 * 24 * 2048 * 4
+    # longer ones, and one sequence with the weights: partials
+    assert size(1, 2049) > 0 and size(2, 4097) > 0 and size(8, 512, mode="split") > 0
+    assert size(1, 512, weights=True) > 24 * 512 * 4 and size(2, 2049, weights=True) > 2 * 24 * 2064 * 4
     # equal shares: per kv head a slot for every CTA, every warp and every sequence
     one, two = size(8, 100000), size(9, 100000)
     assert 0 < two - one < 24 * 256 * 4 + 24 * 8 + 1024
