@@ -481,15 +481,21 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, unsigned (*part)[32], uint2
 
 // (one block per SM: left at 32 registers two share one, and 8 sequences of up to
 // 8192 tokens take 27.4 us with the move instead of 24.3)
+// One: no cluster, a block has a (sequence, kv head) to itself.
+template <bool One>
 __global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const KvEvictParams prm) {
     extern __shared__ __align__(16) uint32_t keys[];  // prm.key_words of them
     __shared__ __align__(8) unsigned hist[kHistWords];
     __shared__ __align__(8) unsigned coarse[3][64];
     __shared__ unsigned part[2][32];
-    __shared__ unsigned found[3][2];  // per round: bin, tokens to take from it on
+    __shared__ unsigned found[3][3];  // per round: bin, tokens to take from it on, tokens in it
     __shared__ __align__(8) unsigned counts[2];  // this block's kept for sure, and ties
     cg::cluster_group cluster = cg::this_cluster();
-    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int CS = One ? 1 : (int)cluster.num_blocks(), rank = One ? 0 : (int)cluster.block_rank();
+    auto of_block = [&](unsigned* p, int r) {  // a shared array of block r of the cluster
+        if constexpr (One) return p;
+        else return cluster.map_shared_rank(p, r);
+    };
     const int kvh = blockIdx.x / CS, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31;
     for (int i = tid; i < kHistWords; i += kEvictThreads) hist[i] = 0;
@@ -586,9 +592,14 @@ __global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const
             const unsigned sum = __reduce_add_sync(kFull, lane < per ? h[(2 * warp + j) * per + lane] : 0u);
             if (lane == 0) coarse[round][2 * warp + j] = sum;
         }
-        cluster.barrier_arrive();
-        if (round == 0) put_protected();  // while the others arrive
-        cluster.barrier_wait();
+        if constexpr (One) {
+            if (round == 0) put_protected();
+            __syncthreads();
+        } else {
+            cluster.barrier_arrive();
+            if (round == 0) put_protected();  // while the others arrive
+            cluster.barrier_wait();
+        }
         if (warp == 0) {
             // in descending order: lane i has groups 63 - 2 i and 62 - 2 i, then bin per - 1 - i
             auto pick = [&](unsigned a, unsigned c, unsigned& above) {  // the lane whose counts reach `need`
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const
             uint2 two[kMaxCluster];  // all reads on their way at once
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r)
-                two[r] = r < CS ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(coarse[round], r) + 62 - 2 * lane)
+                two[r] = r < CS ? *reinterpret_cast<const uint2*>(of_block(coarse[round], r) + 62 - 2 * lane)
                                 : make_uint2(0u, 0u);
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r) a += two[r].y, c += two[r].x;
@@ -617,17 +628,24 @@ __global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const
             unsigned one[kMaxCluster];
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r)
-                one[r] = r < CS && lane < per ? cluster.map_shared_rank(h, r)[group * per + per - 1 - lane] : 0u;
+                one[r] = r < CS && lane < per ? of_block(h, r)[group * per + per - 1 - lane] : 0u;
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r) a += one[r];
             who = pick(a, 0u, above);
             need -= __shfl_sync(kFull, above, who);
-            if (lane == 0) found[round][0] = (unsigned)(group * per + per - 1 - who), found[round][1] = need;
+            a = __shfl_sync(kFull, a, who);
+            if (lane == 0)
+                found[round][0] = (unsigned)(group * per + per - 1 - who), found[round][1] = need, found[round][2] = a;
         }
         __syncthreads();
         T |= found[round][0] << shift;
         mask |= (uint32_t)(bins - 1) << shift;
         need = found[round][1];
+        if (need == found[round][2]) {  // the bin is kept whole, whatever its keys' other bits
+            T -= 1;                     // (no weight's key is below 2^22)
+            need = 0;
+            break;
+        }
     }
     // Kept: the keys above T, and of those equal to it the first `need`.
     unsigned sure = 0, tie = 0;
@@ -644,13 +662,15 @@ __global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const
     uint2 before = block_scan(make_uint2(sure, tie), part, &total);
     before = make_uint2(__shfl_sync(kFull, before.x, 0), __shfl_sync(kFull, before.y, 0));  // the warp's first
     if (tid == 0) counts[0] = total.x, counts[1] = total.y;
-    cluster.sync();
-    uint2 others[kMaxCluster];
+    if constexpr (!One) {
+        cluster.sync();
+        uint2 others[kMaxCluster];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-        others[r] = r < rank ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(counts, r)) : make_uint2(0u, 0u);
+        for (int r = 0; r < kMaxCluster; ++r)
+            others[r] = r < rank ? *reinterpret_cast<const uint2*>(of_block(counts, r)) : make_uint2(0u, 0u);
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) before.x += others[r].x, before.y += others[r].y;
+        for (int r = 0; r < kMaxCluster; ++r) before.x += others[r].x, before.y += others[r].y;
+    }
     // the warp's run again, a key a lane
     const unsigned below = (1u << lane) - 1u;
     const float* from = w + t0;
@@ -668,7 +688,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const
         before.x += __popc(bs);
         before.y += __popc(be);
     }
-    cluster.sync();  // no block leaves while another may still read its counts
+    if constexpr (!One) cluster.sync();  // no block leaves while another may still read its counts
 }
 
 // The kept rows to their new blocks.  One warp per (destination block, kv
@@ -785,15 +805,21 @@ cudaError_t launch_kv_expand(int format, int head_dim, const KvExpandParams& prm
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream) {
+template <bool One>
+static cudaError_t launch_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(kv_evict_select_kernel<One>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kEvictKeyWords * 4);
     });
     if (e != cudaSuccess) return e;
-    return launch(kv_evict_select_kernel, prm, dim3(prm.num_kv_heads * cluster, num_seqs), kEvictThreads, cluster,
-                  stream, prm.key_words * 4);
+    return launch(kv_evict_select_kernel<One>, prm, dim3(prm.num_kv_heads * cluster, num_seqs), kEvictThreads,
+                  One ? 0 : cluster, stream, prm.key_words * 4);
+}
+
+cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream) {
+    return cluster == 1 ? launch_select<true>(prm, num_seqs, cluster, stream)
+                        : launch_select<false>(prm, num_seqs, cluster, stream);
 }
 
 cudaError_t launch_kv_evict_move(int format, int head_dim, const KvEvictParams& prm, dim3 grid, cudaStream_t stream) {
