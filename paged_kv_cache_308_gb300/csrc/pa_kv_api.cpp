@@ -425,13 +425,15 @@ int check_evict(const pa_kv_evict_args* a) {
     return PA_OK;
 }
 
-// Blocks that share a (sequence, kv head) in the selection: while the SMs hold
-// the whole grid and each block gets 1024 tokens or more, up to the 8 of a
-// portable cluster (16 measured slower: 102400 tokens of 4 kv heads, with the
-// move, 34.9 -> 41.7 us).
+// Blocks that share a (sequence, kv head) in the selection.  A cluster costs about
+// 3 us more than a block alone and pays for itself above 12,000 tokens (us with
+// the move, 1, 2, 4 and 8 blocks: 8 heads of one sequence of 8192 tokens 10.1,
+// 12.3, 11.8, 12.1, of 16384 13.4, 13.9, 12.5, 12.2, of 32768 20.8, 18.1, 15.2,
+// 13.8), a pair of blocks above 24,000, as long as the SMs hold the whole grid,
+// of clusters of 8 half of it (16 pairs of 16384: 20.3 in clusters of 8, 13.5 of 4).
 int evict_cluster(int max_seq_len, long long pairs, int num_sms) {
-    int c = 1;
-    while (c < 8 && pairs * 2 * c <= num_sms && max_seq_len >= 2048 * c) c *= 2;
+    int c = max_seq_len <= 12 * 1024 ? 1 : pairs * 16 <= num_sms ? 8 : pairs * 4 <= num_sms ? 4 : 1;
+    if (c == 1 && max_seq_len > 24 * 1024 && pairs * 2 <= num_sms) c = 2;
     // more than one block can hold in shared memory is shared out whatever the grid
     while (c < 8 && max_seq_len > (long long)pa::kEvictKeyWords * c) c *= 2;
     return c;

@@ -445,13 +445,13 @@ __device__ __forceinline__ float weight_of(uint32_t key, const float* w) {
 // radix select over the weights' ordered bits: three rounds of a histogram
 // (11, 11 and 10 bits) find the smallest kept key T and how many of the
 // tokens that equal it are kept (the first ones); then a scan over the
-// positions gives each kept token its place.  A cluster of blocks shares a
-// (sequence, kv head): each takes a stretch of the positions, whose keys stay
-// in its shared memory (the weights are read once), the histograms are summed
-// through distributed shared memory, and a block's first output follows from
-// its predecessors' counts.  Integer counts only, so the result does not
-// depend on the order of the atomics.  Bound by latency: per round one
-// barrier of the cluster and three of the block.
+// positions gives each kept token its place.  The rounds end where a bin is kept
+// whole.  A (sequence, kv head) has a block to itself, or a cluster of them: each
+// takes a stretch of the positions, whose keys stay in its shared memory (the
+// weights are read once), the histograms are summed through distributed shared
+// memory, and a block's first output follows from its predecessors' counts.  Integer counts only, so the result does not
+// depend on the order of the atomics.  Bound by latency: per round three
+// barriers of the block, or two and one of the cluster.
 constexpr int kHistWords = 2048 + 2048 + 1024;
 constexpr int kMaxCluster = 8;  // blocks of a cluster
 
@@ -479,11 +479,12 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, unsigned (*part)[32], uint2
     return make_uint2((warp ? bx : 0u) + incl.x - v.x, (warp ? by : 0u) + incl.y - v.y);
 }
 
-// (one block per SM: left at 32 registers two share one, and 8 sequences of up to
-// 8192 tokens take 27.4 us with the move instead of 24.3)
-// One: no cluster, a block has a (sequence, kv head) to itself.
+// One: no cluster, a block has a (sequence, kv head) to itself; two share an SM,
+// in 32 registers (768 pairs of up to 1024 tokens: 32.0 instead of 40.0 us with
+// the move; 32 pairs of up to 8192 21.2 instead of 21.0), a cluster's do not (27.4
+// instead of 24.3).
 template <bool One>
-__global__ void __launch_bounds__(kEvictThreads, 1) kv_evict_select_kernel(const KvEvictParams prm) {
+__global__ void __launch_bounds__(kEvictThreads, One ? 2 : 1) kv_evict_select_kernel(const KvEvictParams prm) {
     extern __shared__ __align__(16) uint32_t keys[];  // prm.key_words of them
     __shared__ __align__(8) unsigned hist[kHistWords];
     __shared__ __align__(8) unsigned coarse[3][64];

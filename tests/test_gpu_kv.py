@@ -396,14 +396,16 @@ def test_evict_orders_weights(kind):
         check_evict(c, w, keep, 2, 3, evict(c, w, keep, 2, 3))
 
 
-@pytest.mark.parametrize("n,keep", [(9000, 1000), (20000, 19999), (40000, 5), (40001, 20000)])
-def test_evict_long(n, keep):
-    # lengths that several blocks of a cluster share
-    c = K.Case([n, 50], 2, 2, 64, "e4m3", seed=27, device=DEV)
+@pytest.mark.parametrize("B,n,keep", [(2, 9000, 1000), (2, 20000, 19999), (2, 40000, 5), (2, 40001, 20000), (8, 14001, 3000),
+                                      (20, 26003, 2000), (90, 13000, 50)])
+def test_evict_long(B, n, keep):
+    # lengths that one block has to itself, and that 2, 4 and 8 blocks of a cluster share
+    c = K.Case([n] + [50] * (B - 1), 2, 2, 64, "e4m3", seed=27, device=DEV)
     g = torch.Generator(device=DEV).manual_seed(28)
-    w = torch.rand(2, 2, n, generator=g, device=DEV) ** 8
+    w = torch.rand(B, 2, n, generator=g, device=DEV) ** 8
     w = torch.where(w < 0.01, torch.zeros_like(w), w)
-    check_evict(c, w, [keep, 20], 4, 64 if keep > 64 else 1, evict(c, w, [keep, 20], 4, 64 if keep > 64 else 1))
+    want, recent = [keep] + [20] * (B - 1), 64 if keep > 64 else 1
+    check_evict(c, w, want, 4, recent, evict(c, w, want, 4, recent))
 
 
 def test_evict_more_tokens_than_the_blocks_can_hold():
