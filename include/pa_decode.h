@@ -612,12 +612,16 @@ int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void
  * context block is expanded once into an fp16 copy in the workspace, which
  * the prefill kernel then reads for all of its query tiles: the copy's
  * traffic is small next to the products, and expanding in every query tile
- * would repeat it up to max_query_len times.  The copy holds codes times the
+ * would repeat it up to max_query_len times.  Where few query tiles have long
+ * contexts, their keys are walked in several ranges and merged, as
+ * pa_prefix_split does.  The copy holds codes times the
  * power of two of their block's scale, for INT8; the rest of the scale
  * multiplies the scores and probabilities.  E4M3 values (of any scale), and
  * INT8 ones under PA_FLAG_PREFIX_WARP_MMA, are rounded to
  * fp16 (exact for scales that are powers of two; magnitudes above 65504 become
- * 65504).  With PA_KV_F16 no copy is made and this is pa_prefix_ex. */
+ * 65504).  The workspace needs no initialisation and holds
+ * pa_kv_prefix_workspace_size bytes (for the same sizes and format, with this
+ * device current).  With PA_KV_F16 no copy is made and this is pa_prefix_ex. */
 typedef struct {
     void* out;
     const void* q;

@@ -707,7 +707,7 @@ def pa_kv_decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq
 
 
 def pa_kv_prefix_workspace_size(num_seqs, max_context_len, num_kv_heads, head_dim, dtype) -> int:
-    """Bytes of pa_kv_prefix's workspace, for a cache of `dtype`."""
+    """Bytes of pa_kv_prefix's workspace on the current device, for a cache of `dtype`."""
     return lib.pa_kv_prefix_workspace_size(int(num_seqs), int(max_context_len), int(num_kv_heads), int(head_dim),
                                            KV_FORMATS[dtype])
 
@@ -731,7 +731,10 @@ def pa_kv_prefix(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, blo
                         _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev), B, T, cols,
                         int(max_context_len), int(max_query_len), H, scale)
     opts = ctypes.byref(make_opts(flags=flags, wait_limit=wait_limit)) if flags or wait_limit else None
-    need = 0 if workspace is not None else lib.pa_kv_prefix_workspace_size(B, int(max_context_len), hkv, dim, cache[8])
+    need = 0
+    if workspace is None:
+        with torch.cuda.device(dev):  # (the splits go by the device's SMs)
+            need = lib.pa_kv_prefix_workspace_size(B, int(max_context_len), hkv, dim, cache[8])
     ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
     _call("pa_kv_prefix", dev, stream, lib.pa_kv_prefix, args, opts, ptr, nbytes)
 

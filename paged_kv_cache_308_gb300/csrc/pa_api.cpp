@@ -1038,8 +1038,9 @@ int sm_count(int* num_sms) { return query_sm_count(num_sms); }
 
 int check_prefix(const pa_prefix_args* a, const pa_decode_opts* o) { return validate_prefix(a, o); }
 
-int prefix_with_factors(const pa_prefix_args* a, const pa_decode_opts* o, const float2* factors, cudaStream_t stream) {
-    return run_prefix(a, o, stream, false, nullptr, nullptr, 0, factors);
+int prefix_with_factors(const pa_prefix_args* a, const pa_decode_opts* o, const float2* factors,
+                        const pa_prefix_split_opts* split, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    return run_prefix(a, o, stream, split != nullptr, split, ws, ws_bytes, factors);
 }
 
 }  // namespace pa

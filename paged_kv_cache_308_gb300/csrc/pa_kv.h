@@ -16,9 +16,10 @@ namespace pa {
 int sm_count(int* num_sms);                               // of the current device; a PA_* code
 int check_prefix(const pa_prefix_args* args, const pa_decode_opts* opts);  // a PA_* code
 // pa_prefix_ex whose caches hold the context without its factors, float2 [num_seqs]
-// [max_blocks_per_seq][num_kv_heads] of (K, V) (see PrefixParams::factors).
+// [max_blocks_per_seq][num_kv_heads] of (K, V) (see PrefixParams::factors; null:
+// with them); split (null: none) as for pa_prefix_split, its states in `ws`.
 int prefix_with_factors(const pa_prefix_args* args, const pa_decode_opts* opts, const float2* factors,
-                        cudaStream_t stream);
+                        const pa_prefix_split_opts* split, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 struct KvDecodeParams {
     __half* out;

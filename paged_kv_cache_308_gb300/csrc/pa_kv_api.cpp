@@ -17,7 +17,7 @@
 namespace {
 
 constexpr size_t kWsAlign = 256;
-// SM count assumed by the workspace size when no device answers (above any GPU's)
+// SM count assumed when no device answers (above any GPU's; a call then fails later)
 constexpr int kMaxSmsBound = 1024;
 // Tokens of a sequence at most: positions and counts of them, rounded up to any
 // kernel's step, stay ints.
@@ -206,7 +206,7 @@ int run_decode(const pa_kv_decode_args* a, const pa_decode_opts* o, void* ws, si
     if (a->num_seqs == 0) return PA_OK;
     const pa_kv_cache& c = a->cache;
     int num_sms = 0;
-    if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;  // the launch reports the missing device
+    if (pa::sm_count(&num_sms) != PA_OK) num_sms = kMaxSmsBound;  // (as for the size)
     const bool weights = a->weights_out && a->max_seq_len > 0;
     const DecodePlan plan = plan_decode(a->num_seqs, a->max_seq_len, c.num_kv_heads, c.head_dim, c.format, num_sms,
                                         o ? o->partition_size : 0, o ? o->mode : PA_MODE_AUTO, weights);
@@ -308,11 +308,39 @@ size_t prefix_copy_bytes(int num_seqs, int blocks_per_seq, int num_kv_heads, int
     return up((size_t)num_seqs * blocks_per_seq * num_kv_heads * pa::kBlockSize * head_dim * 2);
 }
 
-size_t prefix_space(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format) {
-    if (format == PA_KV_F16 || max_context_len == 0) return 0;
+// The copy's K and V, its table, INT8's factors; then the states of split query
+// tiles, one tile per SM at most (see plan_prefix).
+struct PrefixSpace {
+    size_t copy, factors, states, bytes;  // bytes of K's copy; offsets; all
+};
+
+constexpr int kPrefixSplitMinContext = 512;
+
+PrefixSpace prefix_space(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format, int num_sms) {
+    PrefixSpace s{};
+    if (format == PA_KV_F16 || max_context_len == 0) return s;
     const int n = blocks_of(max_context_len);
-    return 2 * prefix_copy_bytes(num_seqs, n, num_kv_heads, head_dim) + up((size_t)num_seqs * n * 4) +
-           (format == PA_KV_INT8 ? up((size_t)num_seqs * n * num_kv_heads * 8) : 0);
+    s.copy = prefix_copy_bytes(num_seqs, n, num_kv_heads, head_dim);
+    s.factors = 2 * s.copy + up((size_t)num_seqs * n * 4);
+    s.states = s.factors + (format == PA_KV_INT8 ? up((size_t)num_seqs * n * num_kv_heads * 8) : 0);
+    s.bytes = s.states;
+    if (max_context_len >= kPrefixSplitMinContext && 2ll * num_seqs * num_kv_heads <= num_sms)
+        s.bytes += up((size_t)num_sms * pa::kPrefixTileRows * head_dim * 4) + up((size_t)num_sms * pa::kPrefixTileRows * 8);
+    return s;
+}
+
+// Key ranges that each of `tiles` query tiles has its keys cut into (0: none): one
+// (query tile, range) per SM at most, four key tiles a range or more, and only
+// where the longest tile's walk gets ten key tiles shorter, which pays for the
+// merge of the ranges' states (chunks of 37 tokens, whole / split: 8 x 128 after
+// 8000 tokens in int8 117.7 / 36.2 us, after 1000 22.8 / 17.5, four such chunks
+// after 8000 137.9 / 94.5, after 1000, two ranges each, 26.5 / 27.5; 4 x 256
+// after 500 in e4m3 19.3 / 21.9).
+int plan_prefix(const pa_prefix_args* a, int num_sms, long long tiles) {
+    if (a->max_context_len < kPrefixSplitMinContext || tiles * 2 > num_sms) return 0;
+    const int keys = (blocks_of(a->max_context_len) + blocks_of(a->max_query_len) + 3) / 4;  // key tiles of 64
+    const int parts = static_cast<int>(std::min<long long>(num_sms / tiles, std::min(64, keys / 4)));
+    return parts >= 2 && (long long)keys * (parts - 1) >= 10ll * parts ? parts : 0;
 }
 
 int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, size_t ws_bytes, cudaStream_t stream) {
@@ -347,15 +375,18 @@ int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, si
     if (c.format == PA_KV_F16) return pa_prefix_ex(&p, o, reinterpret_cast<pa_stream_t>(stream));
 
     const int n = blocks_of(a->max_context_len);
-    const size_t need = prefix_space(a->num_seqs, a->max_context_len, c.num_kv_heads, c.head_dim, c.format);
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK) num_sms = kMaxSmsBound;  // (as for the size)
+    const PrefixSpace sp =
+        prefix_space(a->num_seqs, a->max_context_len, c.num_kv_heads, c.head_dim, c.format, num_sms);
+    const bool warp_mma = o && (o->flags & PA_FLAG_PREFIX_WARP_MMA);
     // the copy replaces the cache; it has room for every sequence's longest context
     p.num_blocks = (int64_t)a->num_seqs * n;
     p.max_blocks_per_seq = n;
     float* factors = nullptr;
     if (n > 0) {
         if (p.num_blocks * c.num_kv_heads * pa::kBlockSize >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-        if (!ws || ws_bytes < need || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
-        const size_t copy = prefix_copy_bytes(a->num_seqs, n, c.num_kv_heads, c.head_dim);
+        if (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
         uint8_t* w = static_cast<uint8_t*>(ws);
         pa::KvExpandParams e{};
         e.cache[0] = static_cast<const uint8_t*>(c.k_cache);
@@ -363,13 +394,12 @@ int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, si
         e.scales[0] = c.k_scales;
         e.scales[1] = c.v_scales;
         e.expanded[0] = reinterpret_cast<__half*>(w);
-        e.expanded[1] = reinterpret_cast<__half*>(w + copy);
-        e.tables = reinterpret_cast<int32_t*>(w + 2 * copy);
+        e.expanded[1] = reinterpret_cast<__half*>(w + sp.copy);
+        e.tables = reinterpret_cast<int32_t*>(w + 2 * sp.copy);
         // INT8 scales have more bits than a product with a code leaves room for in
         // fp16: their significands go to the kernel apart (the warp-level kernel
         // cannot take them; there the values are rounded)
-        if (c.format == PA_KV_INT8 && !(o && (o->flags & PA_FLAG_PREFIX_WARP_MMA)))
-            factors = reinterpret_cast<float*>(w + 2 * copy + up((size_t)a->num_seqs * n * 4));
+        if (c.format == PA_KV_INT8 && !warp_mma) factors = reinterpret_cast<float*>(w + sp.factors);
         e.factors = factors;
         e.block_tables = a->block_tables;
         e.context_lens = a->context_lens;
@@ -387,7 +417,20 @@ int run_prefix(const pa_kv_prefix_args* a, const pa_decode_opts* o, void* ws, si
             cudaSuccess)
             return PA_ERR_CUDA;
     }
-    return pa::prefix_with_factors(&p, o, reinterpret_cast<const float2*>(factors), stream);
+    // Few query tiles: one CTA each, without the counter they would be claimed
+    // from (that form takes 1.5 to 2 us less there), and their keys in several
+    // ranges where that fills the SMs.
+    pa_decode_opts opts = {};
+    if (o) opts = *o;
+    const int tile_tokens = pa::kPrefixTileRows / (a->num_heads / c.num_kv_heads);
+    const long long tiles =
+        (long long)((a->max_query_len + tile_tokens - 1) / tile_tokens) * c.num_kv_heads * a->num_seqs;
+    if (tiles <= num_sms && !warp_mma) opts.flags |= PA_FLAG_PREFIX_GRID;
+    pa_prefix_split_opts split = {};
+    if (!warp_mma && n > 0) split.parts = plan_prefix(&p, num_sms, tiles);
+    split.units = static_cast<int>(split.parts ? tiles : 0);
+    return pa::prefix_with_factors(&p, &opts, reinterpret_cast<const float2*>(factors), split.parts ? &split : nullptr,
+                                   static_cast<uint8_t*>(ws) + sp.states, sp.bytes - sp.states, stream);
 }
 
 // ---- eviction
@@ -499,7 +542,9 @@ int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void
 size_t pa_kv_prefix_workspace_size(int num_seqs, int max_context_len, int num_kv_heads, int head_dim, int format) {
     if (num_seqs <= 0 || max_context_len <= 0 || num_kv_heads <= 0 || pa::kv_decode_ctas(format, head_dim) < 0)
         return 0;
-    return prefix_space(num_seqs, max_context_len, num_kv_heads, head_dim, format);
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK || num_sms <= 0) num_sms = kMaxSmsBound;
+    return prefix_space(num_seqs, max_context_len, num_kv_heads, head_dim, format, num_sms).bytes;
 }
 
 int pa_kv_prefix(const pa_kv_prefix_args* args, const pa_decode_opts* opts, void* workspace, size_t workspace_bytes,

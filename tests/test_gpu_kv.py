@@ -453,6 +453,28 @@ def test_decode_ragged_batches(fmt, B, top, long, hkv, dim):
     assert torch.equal(decode(c), out) and torch.equal(decode(c), out)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("heads,hkv,dim,ctx,new", [(24, 4, 256, [1500], [3]), (32, 8, 128, [2100, 0, 64, 700], [37, 5, 1, 0]),
+                                                   (8, 1, 64, [4003, 100, 1, 1000, 513], [1, 150, 17, 40, 64]),
+                                                   (3, 3, 256, [1023, 1024], [1, 130])])
+def test_prefix_in_key_ranges(fmt, heads, hkv, dim, ctx, new):
+    # few query tiles after long contexts; sequences shorter than a range, without context, without a chunk
+    c = K.Case(ctx, heads, hkv, dim, fmt, seed=35, device=DEV)
+    q, k_new, v_new, loc = _chunks(c, new, 36)
+    ref, bound = K.prefix_reference(c, new, q, k_new, v_new)
+    first = None
+    for fill in (0x00, 0xff):  # whatever the workspace holds
+        ws = torch.full((pb().pa_kv_prefix_workspace_size(len(ctx), max(ctx), hkv, dim, DTYPES[fmt]),), fill,
+                        dtype=torch.uint8, device=DEV)
+        out = torch.full_like(q, math.nan)
+        pb().pa_kv_prefix(out, q, k_new, v_new, *c.cache(), c.tables, c.seq_lens, loc, c.scale, max_context_len=max(ctx),
+                          max_query_len=max(new), workspace=ws)
+        assert status() == 0
+        check(out, ref, bound)
+        assert first is None or torch.equal(first, out)
+        first = out
+
+
 @pytest.mark.parametrize("mode", ["auto", "split"])
 @pytest.mark.parametrize("fmt", ["f16", "e4m3", "int8"])
 @pytest.mark.parametrize("heads,hkv,dim,B", [(6, 1, 256, 1), (24, 4, 256, 3), (32, 8, 128, 8), (8, 8, 64, 20), (7, 1, 128, 70),

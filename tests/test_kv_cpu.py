@@ -142,8 +142,15 @@ def test_prefix_refusals(kw, code):
 def test_prefix_workspace():
     n = pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.int8)
     # K and V in fp16, the copy's table, the factors of INT8's scales
-    assert n == 2 * (2 * 50 * 4 * 16 * 256 * 2) + 512 + 2 * 50 * 4 * 8 + 128
-    assert pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.float8_e4m3fn) == 2 * (2 * 50 * 4 * 16 * 256 * 2) + 512
+    copy = lambda L: 2 * (2 * -(-L // 16) * 4 * 16 * 256 * 2)
+    assert pb.pa_kv_prefix_workspace_size(2, 496, 4, 256, torch.float8_e4m3fn) == copy(496) + 256
+    assert pb.pa_kv_prefix_workspace_size(2, 496, 4, 256, torch.int8) == copy(496) + 256 + 2 * 31 * 4 * 8 + 64
+    # from 512 tokens on the states of split query tiles: 128 rows of 256 numbers and two for each SM
+    states = n - copy(800) - 512 - 2 * 50 * 4 * 8 - 128
+    assert states > 0 and states % (128 * 258 * 4) == 0
+    assert pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.float8_e4m3fn) == copy(800) + 512 + states
+    # (none where the batch has more heads than half the SMs)
+    assert pb.pa_kv_prefix_workspace_size(200, 800, 4, 256, torch.float8_e4m3fn) == 100 * copy(800) + 40192
     assert pb.pa_kv_prefix_workspace_size(2, 800, 4, 256, torch.float16) == 0
     assert pb.pa_kv_prefix_workspace_size(2, 0, 4, 256, torch.int8) == 0
     for ws, size in ((FAKE, n - 1), (None, n), (FAKE + 16, n)):
