@@ -91,7 +91,7 @@ constexpr int kSingleOneMaxLen = 128, kSingleMaxLen = 512, kSingleManyMaxLen = 1
 // per warp, as others' do not: up to 8 rounds (4 x 4096 of 4 x 256 13.6 against
 // 14.2 in equal shares; at 16, 8 x 4096 of 8 x 128 19.3 / 19.2 and with uniform
 // lengths 12.6 / 11.4), with the weights, which need them again, 4 (8 rounds:
-// 2 x 4096 of 4 x 256 13.2 / 12.0).  One sequence, whose partitions have more CTAs,
+// 2 x 4096 of 4 x 256 14.1 / 12.0).  One sequence, whose partitions have more CTAs,
 // without weights only and up to 4: 2048 tokens take 7.9 against 7.7, but the
 // launch less saves the host 2.
 int cluster_ctas(int num_seqs, int max_seq_len, int num_kv_heads, int ctas, int num_sms, bool weights) {
