@@ -946,6 +946,11 @@ int run_prefix(const pa_prefix_args* a, const pa_decode_opts* o, cudaStream_t st
     prm.max_query_len = a->max_query_len;
     prm.num_tokens = a->num_tokens;
     prm.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
+    // The tcgen05 kernel masks a key by an infinite raw score, which times a
+    // scale of 0 would be NaN.  With the smallest normal number in its place
+    // the score stays infinite, and those of halves (below 256 * 65504^2 = 2^40)
+    // become differences below 2^-85: equal weights, as 0 gives.
+    if (!warp_mma && prm.scale_log2 == 0.f) prm.scale_log2 = 0x1p-126f;
     prm.wait_limit = (o && o->wait_limit) ? o->wait_limit : pa::kDefaultWaitLimit;
     prm.force_timeout = (o && (o->flags & PA_FLAG_FORCE_TIMEOUT)) ? 1 : 0;
     prm.status = pa::device_status_ptr();
