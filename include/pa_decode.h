@@ -664,7 +664,9 @@ int pa_kv_prefix(const pa_kv_prefix_args* args, const pa_decode_opts* opts, void
  * on).  Keys keep the positions that were encoded into them.  `dst` may be
  * the source's pool or another one of the same format, kv heads and
  * head_dim; its blocks of dst_block_tables must differ from each other and
- * from every block read, and dst_weights must not overlap weights. */
+ * from every block read.  new_lens may be seq_lens or keep_lens itself (it is
+ * then written by a third launch, about 1 us); kept, new_lens and dst_weights
+ * must not overlap each other, nor any array that the call reads otherwise. */
 typedef struct {
     pa_kv_cache src;
     pa_kv_cache dst;
@@ -675,7 +677,7 @@ typedef struct {
     const float* weights;            /* [num_seqs][num_kv_heads][weights_stride] */
     float* dst_weights;
     int32_t* kept;
-    int32_t* new_lens;
+    int32_t* new_lens;               /* may be seq_lens or keep_lens */
     int64_t weights_stride;          /* >= max_seq_len */
     int64_t dst_weights_stride;      /* >= max_keep_len when dst_weights is given */
     int num_seqs;

@@ -746,8 +746,8 @@ def pa_kv_evict(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, ds
     """Keep each kv head's most attended tokens and move them to other blocks (see
     include/pa_decode.h).  The destination may be the same pool; its blocks must not be among the
     source's.  weights: float32 [num_seqs, num_kv_heads, >= max_seq_len]; kept: int32 [num_seqs,
-    num_kv_heads, max_keep_len]; new_lens: int32 [num_seqs]; dst_weights: float32 [num_seqs,
-    num_kv_heads, >= max_keep_len] or None."""
+    num_kv_heads, max_keep_len]; new_lens: int32 [num_seqs] (may be seq_lens or keep_lens);
+    dst_weights: float32 [num_seqs, num_kv_heads, >= max_keep_len] or None."""
     dev = k_cache.get_device()
     src = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
     dst = _kv_cache(dst_k_cache, dst_v_cache, dst_k_scales, dst_v_scales, dev, "dst_")

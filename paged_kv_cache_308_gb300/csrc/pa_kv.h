@@ -112,7 +112,7 @@ struct KvEvictParams {
     const float* weights;
     float* dst_weights;
     int32_t* kept;
-    int32_t* new_lens;
+    int32_t* new_lens;  // null: launch_kv_evict_lens writes it
     long long src_blocks, dst_blocks, weights_stride, dst_weights_stride;
     int num_kv_heads, max_blocks_per_seq, dst_max_blocks_per_seq;
     int max_seq_len, max_keep_len, sinks, recent;
@@ -122,6 +122,12 @@ struct KvEvictParams {
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictKeyWords = 48 * 1024;  // at most: 192 KB
 cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream);
+struct KvEvictLensParams {
+    KvEvictParams evict;
+    int32_t* new_lens;  // may be evict.seq_lens or evict.keep_lens
+    int num_seqs;
+};
+cudaError_t launch_kv_evict_lens(const KvEvictLensParams& prm, cudaStream_t stream);  // after the move
 cudaError_t launch_kv_evict_move(int format, int head_dim, const KvEvictParams& prm, dim3 grid, cudaStream_t stream);
 
 }  // namespace pa

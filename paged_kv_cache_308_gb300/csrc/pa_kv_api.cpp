@@ -47,6 +47,12 @@ int check_pointers(const pa_kv_cache& c) {
     return PA_OK;
 }
 
+// Whether n and m words of four bytes share memory.
+bool overlap(const void* p, long long n, const void* q, long long m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return p && q && n > 0 && m > 0 && (x < y ? y - x < 4ull * n : x - y < 4ull * m);
+}
+
 bool bad_ptr(const void* p, uintptr_t a) { return !p || !aligned(p, a); }
 
 // ---- decode
@@ -460,6 +466,9 @@ int check_evict(const pa_kv_evict_args* a) {
         if ((rc = check_pointers(a->src)) || (rc = check_pointers(a->dst))) return rc;
         if (a->src.num_blocks == 0 || a->dst.num_blocks == 0) return PA_ERR_INVALID_ARG;
     }
+    // new_lens takes seq_lens' or keep_lens' place element by element, or has memory of its own
+    for (const int32_t* lens : {a->seq_lens, a->keep_lens})
+        if (lens != a->new_lens && overlap(a->new_lens, a->num_seqs, lens, a->num_seqs)) return PA_ERR_INVALID_ARG;
     // in place would read rows that are already overwritten
     if (a->weights && a->weights == a->dst_weights) return PA_ERR_INVALID_ARG;
     if (a->block_tables && a->block_tables == a->dst_block_tables &&
@@ -573,7 +582,8 @@ int pa_kv_evict(const pa_kv_evict_args* a, pa_stream_t stream_) {
     p.weights = a->weights;
     p.dst_weights = a->dst_weights;
     p.kept = a->kept;
-    p.new_lens = a->new_lens;
+    const bool in_place = a->new_lens == a->seq_lens || a->new_lens == a->keep_lens;
+    p.new_lens = in_place ? nullptr : a->new_lens;
     p.src_blocks = a->src.num_blocks;
     p.dst_blocks = a->dst.num_blocks;
     p.weights_stride = a->weights_stride;
@@ -587,9 +597,15 @@ int pa_kv_evict(const pa_kv_evict_args* a, pa_stream_t stream_) {
     p.recent = a->recent;
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
+    // lengths that change while blocks read them would part the blocks of a cluster
+    const long long pairs = (long long)a->num_seqs * p.num_kv_heads;
+    for (const int32_t* lens : {a->seq_lens, a->keep_lens})
+        if (overlap(a->kept, pairs * a->max_keep_len, lens, a->num_seqs) ||
+            overlap(a->dst_weights, pairs * a->dst_weights_stride, lens, a->num_seqs))
+            return PA_ERR_INVALID_ARG;
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK) num_sms = 1;
-    const int cluster = evict_cluster(a->max_seq_len, (long long)a->num_seqs * p.num_kv_heads, num_sms);
+    const int cluster = evict_cluster(a->max_seq_len, pairs, num_sms);
     // (each warp's run is a multiple of 128 keys)
     constexpr int kRound = 4 * pa::kEvictThreads;
     p.key_words = static_cast<int>(std::min<long long>(
@@ -599,6 +615,7 @@ int pa_kv_evict(const pa_kv_evict_args* a, pa_stream_t stream_) {
     if (blocks > 0 && pa::launch_kv_evict_move(a->src.format, a->src.head_dim, p,
                                                dim3(blocks, p.num_kv_heads, a->num_seqs), stream) != cudaSuccess)
         return PA_ERR_CUDA;
+    if (in_place && pa::launch_kv_evict_lens({p, a->new_lens, a->num_seqs}, stream) != cudaSuccess) return PA_ERR_CUDA;
     return PA_OK;
 }
 

@@ -1,7 +1,8 @@
 // Writing, expanding and thinning out the paged cache: kv_append_kernel,
 // kv_expand_kernel (8-bit context blocks to an fp16 copy, for the prefill
-// kernel), kv_evict_select_kernel and kv_evict_move_kernel.  All of them are
-// bound by memory: each moves its rows once, 16 bytes a lane.
+// kernel), kv_evict_select_kernel, kv_evict_move_kernel and
+// kv_evict_lens_kernel.  Those that move rows are bound by memory: each moves
+// its rows once, 16 bytes a lane.
 #include "pa_kv.h"
 
 #include <cooperative_groups.h>
@@ -417,9 +418,9 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
 struct KeepPlan {
     int L, k, sinks, recent;
     bool bad;
-    __device__ KeepPlan(const KvEvictParams& prm, int b) {
-        L = __ldg(prm.seq_lens + b);
-        const int want = __ldg(prm.keep_lens + b);
+    __device__ KeepPlan(const KvEvictParams& prm, int b)
+        : KeepPlan(prm, __ldg(prm.seq_lens + b), __ldg(prm.keep_lens + b)) {}
+    __device__ KeepPlan(const KvEvictParams& prm, int len, int want) : L(len) {
         bad = L < 0 || L > prm.max_seq_len || L > (long long)prm.max_blocks_per_seq * kBlockSize || want < 0 ||
               want > prm.max_keep_len;
         k = min(want, L);
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kEvictThreads, One ? 2 : 1) kv_evict_select_ke
         return;
     }
     const int L = plan.L, k = plan.k;
-    if (blockIdx.x == 0 && tid == 0) prm.new_lens[b] = k;
+    if (prm.new_lens && blockIdx.x == 0 && tid == 0) prm.new_lens[b] = k;
     const size_t row = (size_t)b * prm.num_kv_heads + kvh;
     const float* w = prm.weights + row * prm.weights_stride;
     int32_t* kept = prm.kept + row * prm.max_keep_len;
@@ -764,6 +765,18 @@ __global__ void __launch_bounds__(64) kv_evict_move_kernel(const KvEvictParams p
     }
 }
 
+// new_lens in place of seq_lens or keep_lens: the selection's and the move's
+// blocks read those, so it is written when all of them have ended (3 sequences of
+// 300 tokens 7.2 instead of 6.2 us on the device).
+__global__ void __launch_bounds__(256) kv_evict_lens_kernel(const KvEvictLensParams prm) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b >= prm.num_seqs) return;
+    const KeepPlan plan(prm.evict, prm.evict.seq_lens[b], prm.evict.keep_lens[b]);
+    if (!plan.bad) prm.new_lens[b] = plan.k;
+}
+
 template <typename P>
 cudaError_t launch(void (*kern)(P), const P& prm, dim3 grid, int threads, int cluster, cudaStream_t stream,
                    size_t smem = 0) {
@@ -821,6 +834,10 @@ static cudaError_t launch_select(const KvEvictParams& prm, int num_seqs, int clu
 cudaError_t launch_kv_evict_select(const KvEvictParams& prm, int num_seqs, int cluster, cudaStream_t stream) {
     return cluster == 1 ? launch_select<true>(prm, num_seqs, cluster, stream)
                         : launch_select<false>(prm, num_seqs, cluster, stream);
+}
+
+cudaError_t launch_kv_evict_lens(const KvEvictLensParams& prm, cudaStream_t stream) {
+    return launch(kv_evict_lens_kernel, prm, dim3((prm.num_seqs + 255) / 256), 256, 0, stream);
 }
 
 cudaError_t launch_kv_evict_move(int format, int head_dim, const KvEvictParams& prm, dim3 grid, cudaStream_t stream) {

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import kv_helpers as K
-from test_gpu_kv import DEV, _chunks, check, pb, status
+from test_gpu_kv import DEV, _chunks, check, check_evict, evict, pb, status
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,70 @@ def test_prefix_with_a_softmax_scale_of_zero(form, fmt, scale):
     else:
         out = prefix(c, q, k_new, v_new, loc, new, flags)
     check(out, ref, bound)
+
+
+@pytest.mark.parametrize("place", ["seq_lens", "keep_lens"])
+@pytest.mark.parametrize("hkv,lens", [(2, [20000, 50]), (8, [(37 * i) % 700 for i in range(60)]), (1, [30, 0, 5]),
+                                      (2, [26003] + [100] * 19)])
+def test_evict_writes_the_new_lengths_in_place_of_the_old(hkv, lens, place):
+    # in clusters, in more blocks than the SMs hold at once, with sequences below their budget: the same as into an
+    # array of their own, for the later blocks too, which find the lengths where they were
+    c = K.Case(lens, hkv, hkv, 64, "int8", seed=97, device=DEV)
+    w = torch.rand(len(lens), hkv, c.max_len, generator=torch.Generator(device=DEV).manual_seed(98), device=DEV)
+    keep = [(29 * i + 11) % 60 for i in range(len(lens))]
+    d = evict(c, w, keep, 2, 3)
+    check_evict(c, w, keep, 2, 3, d)
+    for replayed in (False, True):
+        seq, want = c.seq_lens.clone(), torch.tensor(keep, dtype=torch.int32, device=DEV)
+        new = seq if place == "seq_lens" else want
+        got = {n: torch.full_like(t, -5) if n in ("kept", "w") else torch.full(t.shape, 9.0, device=DEV).to(t.dtype)
+               for n, t in d.items() if n not in ("tables", "lens")}
+        call = lambda: pb().pa_kv_evict(*c.cache(), c.tables, seq, got["k"], got["v"], got["ks"], got["vs"], d["tables"], want,
+                                        w, got["kept"], new, got["w"], max_seq_len=c.max_len, max_keep_len=max(keep), sinks=2,
+                                        recent=3)
+        if replayed:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+                call()
+            g.replay()
+        else:
+            call()
+        assert status() == 0
+        check_evict(c, w, keep, 2, 3, {**got, "lens": new, "tables": d["tables"]})
+        other, was = (want, keep) if new is seq else (seq, c.lens)
+        assert other.tolist() == list(was)
+
+
+def test_evict_in_place_leaves_a_bad_length():
+    c = K.Case([100, 200], 2, 2, 64, "f16", seed=99, device=DEV)
+    w = torch.rand(2, 2, 200, device=DEV)
+    seq = torch.tensor([100, 201], dtype=torch.int32, device=DEV)
+    dst = torch.arange(2, dtype=torch.int32, device=DEV).view(2, 1)
+    pool = [torch.zeros(2, 2, 16, 64, dtype=torch.float16, device=DEV) for _ in range(2)]
+    pb().pa_kv_evict(c.k, c.v, None, None, c.tables, seq, *pool, None, None, dst,
+                     torch.tensor([9, 9], dtype=torch.int32, device=DEV), w,
+                     torch.zeros(2, 2, 16, dtype=torch.int32, device=DEV), seq, max_seq_len=200, max_keep_len=16)
+    assert status() == pb().PA_DEV_BAD_SEQ_LEN and seq.tolist() == [9, 201]
+
+
+def test_evict_refuses_outputs_over_the_lengths():
+    c = K.Case([100, 90], 1, 1, 64, "f16", seed=100, device=DEV)
+    w = torch.rand(2, 1, 100, device=DEV)
+    room = torch.zeros(64, dtype=torch.int32, device=DEV)
+    seq, keep, new = room[:2], torch.tensor([9, 9], dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    seq.copy_(c.seq_lens)
+    dst = torch.arange(2, dtype=torch.int32, device=DEV).view(2, 1)
+    pool = [torch.zeros(2, 1, 16, 64, dtype=torch.float16, device=DEV) for _ in range(2)]
+    call = lambda kept, dst_w: pb().pa_kv_evict(c.k, c.v, None, None, c.tables, seq, *pool, None, None, dst, keep, w, kept, new,
+                                                dst_w, max_seq_len=100, max_keep_len=16)
+    kept = torch.zeros(2, 1, 16, dtype=torch.int32, device=DEV)
+    for bad in ((room[:32].view(2, 1, 16), None), (room[1:33].view(2, 1, 16), None),
+                (kept, room[:32].view(torch.float32).view(2, 1, 16))):
+        with pytest.raises(pb().PaDecodeError):
+            call(*bad)
+    torch.cuda.synchronize()
+    assert seq.tolist() == [100, 90] and new.tolist() == [0, 0]
+    call(room[2:34].view(2, 1, 16), None)  # right behind them
+    assert status() == 0 and new.tolist() == [9, 9] and seq.tolist() == [100, 90]
