@@ -125,7 +125,8 @@ DecodePlan plan_decode(int num_seqs, int max_seq_len, int num_kv_heads, int head
         return p;
     }
     const bool many = (long long)num_seqs * num_kv_heads * 4 >= num_sms * 3ll;
-    if (mode == PA_MODE_SINGLE || (partition_size <= 0 && mode == PA_MODE_AUTO && num_seqs > 1 &&
+    // (a batch of empty sequences has nothing to share out, and needs no workspace)
+    if (max_seq_len == 0 || mode == PA_MODE_SINGLE || (partition_size <= 0 && mode == PA_MODE_AUTO && num_seqs > 1 &&
                                    max_seq_len <= (many ? kSingleManyMaxLen : kSingleMaxLen)))
         partition_size = whole;
     if (partition_size <= 0 && mode == PA_MODE_AUTO && max_seq_len <= kSingleOneMaxLen) partition_size = whole;

@@ -117,3 +117,20 @@ def test_evict_refuses_outputs_over_the_lengths():
     assert seq.tolist() == [100, 90] and new.tolist() == [0, 0]
     call(room[2:34].view(2, 1, 16), None)  # right behind them
     assert status() == 0 and new.tolist() == [9, 9] and seq.tolist() == [100, 90]
+
+
+@pytest.mark.parametrize("opt", [dict(), dict(mode="single"), dict(mode="split"), dict(partition_size=64)])
+@pytest.mark.parametrize("fmt", ["f16", "e4m3"])
+@pytest.mark.parametrize("B", [1, 2, 70])
+def test_decode_of_empty_sequences_in_every_form(B, fmt, opt):
+    c = K.Case([0] * B, 4, 2, 64, fmt, seed=101, device=DEV)
+    w = torch.full((B, 2, 4), -7.0, device=DEV)
+    for weights in (None, w):
+        out = torch.full_like(c.q, math.nan)
+        pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=0, weights_out=weights, **opt)
+        assert status() == 0 and bool((out == 0).all()) and bool((w == -7).all())
+    # a length that the bound of 0 does not allow is reported
+    c.seq_lens[B - 1] = 3
+    out = torch.full_like(c.q, math.nan)
+    pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=0, **opt)
+    assert status() == pb().PA_DEV_BAD_SEQ_LEN and bool((out[:B - 1] == 0).all()) and bool(out[B - 1].isnan().all())
