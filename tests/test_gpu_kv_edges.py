@@ -52,6 +52,34 @@ def test_prefix_with_a_softmax_scale_of_zero(form, fmt, scale):
     check(out, ref, bound)
 
 
+@pytest.mark.parametrize("fmt", ["f16", "e4m3", "int8"])
+@pytest.mark.parametrize("heads,hkv,dim", [(12, 4, 64), (16, 4, 128), (24, 4, 256), (7, 7, 64)])
+def test_prefix_with_more_query_tiles_than_the_device_has_sms(fmt, heads, hkv, dim):
+    # the form whose CTAs claim tile after tile: ragged contexts and chunks, some empty, unlike block scales (for INT8 of
+    # 24 significant bits), so that a factor of the tile, sequence or head before would show; the same bits as a CTA a tile
+    g = torch.Generator().manual_seed(dim + hkv)
+    B = 24
+    ctx = [0, 511, 16, 17, 1] + torch.randint(0, 500, (B - 5,), generator=g).tolist()
+    new = [33, 1, 0, 200, 16] + torch.randint(0, 130, (B - 5,), generator=g).tolist()
+    ctx[9] = new[11] = 0
+    c = K.Case(ctx, heads, hkv, dim, fmt, seed=95, device=DEV, spread=4.0, extra_cols=1)
+    if fmt == "int8":
+        c.ks *= 1.2345678
+        c.vs *= 0.8765432
+    if fmt != "f16":
+        for s in (c.ks, c.vs):
+            s[int(c.tables[3, 1])] = 0.0
+    q, k_new, v_new, loc = _chunks(c, new, 96)
+    assert prefix_tiles(c, new) > 2 * sms()
+    ref, bound = K.prefix_reference(c, new, q, k_new, v_new)
+    size = pb().pa_kv_prefix_workspace_size(B, c.max_len, hkv, dim, K.DTYPES[fmt])
+    for fill in (0x00, 0xff):  # (and again: the claims begin at the first tile)
+        ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV) if size else None
+        out = prefix(c, q, k_new, v_new, loc, new, workspace=ws)
+        check(out, ref, bound)
+        assert torch.equal(out, prefix(c, q, k_new, v_new, loc, new, pb().PA_FLAG_PREFIX_GRID))
+
+
 @pytest.mark.parametrize("place", ["seq_lens", "keep_lens"])
 @pytest.mark.parametrize("hkv,lens", [(2, [20000, 50]), (8, [(37 * i) % 700 for i in range(60)]), (1, [30, 0, 5]),
                                       (2, [26003] + [100] * 19)])
