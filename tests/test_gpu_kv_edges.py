@@ -162,3 +162,86 @@ def test_decode_of_empty_sequences_in_every_form(B, fmt, opt):
     out = torch.full_like(c.q, math.nan)
     pb().pa_kv_decode(out, c.q, *c.cache(), c.tables, c.seq_lens, c.scale, max_seq_len=0, **opt)
     assert status() == pb().PA_DEV_BAD_SEQ_LEN and bool((out[:B - 1] == 0).all()) and bool(out[B - 1].isnan().all())
+
+
+def _raw_append(k, v, ks, vs, new_k, new_v, ctx):
+    """Append new_k and new_v ([blocks, heads, tokens, dim]) to blocks that hold ctx tokens each, a sequence a block."""
+    B, hkv, n, dim = new_k.shape
+    rows = lambda x: x.transpose(1, 2).reshape(B * n, hkv, dim).contiguous()
+    ints = lambda x: torch.as_tensor(x, dtype=torch.int32, device=DEV)
+    pb().pa_kv_append(k, v, ks, vs, rows(new_k), rows(new_v), torch.arange(B, dtype=torch.int32, device=DEV).view(B, 1),
+                      ints([ctx] * B), torch.arange(0, B * n + 1, n, dtype=torch.int32, device=DEV), max_query_len=n)
+    assert status() == 0
+
+
+def test_int8_codes_of_every_half_in_every_scale():
+    # A code is the integer nearest to x / s, ties to even; s has 8 significant bits.  Its exponent only shifts the
+    # quotients, so 128 scales and all halves are every case.  In 64 bits x / s (11 bits over 8) is a tie exactly or further
+    # from one than its rounding, so the reference's round is the quotient's.
+    halves = torch.arange(0, 0x7c00, dtype=torch.int16, device=DEV).view(torch.float16)
+    x = torch.cat([halves, -halves])                       # 63488
+    per = 15 * 256                                         # new tokens of a block of 16, the first being there already
+    n = -(-x.numel() // per)
+    x = torch.nn.functional.pad(x, (0, n * per - x.numel())).view(1, n, 15, 256)
+    s = torch.arange(128, 256, device=DEV).float() * 2
+    hkv = 8
+    x = torch.where(x.float().abs() > 127 * s[:, None, None, None], torch.zeros_like(x), x)  # so that no scale grows
+    new = x.reshape(128 * n // hkv, hkv, 15, 256)
+    scales = s[:, None].expand(128, n).reshape(-1, hkv).contiguous()
+    k = torch.zeros(new.shape[0], hkv, 16, 256, dtype=torch.int8, device=DEV)
+    v, ks, vs = k.clone(), scales.clone(), scales.clone()
+    _raw_append(k, v, ks, vs, new, -new, 1)
+    want = torch.round(new.double() / scales.double()[:, :, None, None]).clamp(-127, 127).to(torch.int8)
+    assert torch.equal(ks, scales) and torch.equal(vs, scales)
+    assert torch.equal(k[:, :, 1:], want) and torch.equal(v[:, :, 1:], -want)
+    assert bool((k[:, :, 0] == 0).all())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_every_code_from_every_scale_to_every_larger_one(fmt):
+    # A block whose scale grows from s0 to s1 has its codes c rounded again to c s0 / s1.  INT8: all pairs of 8-bit
+    # significands, s1 up to 2^9 of s0 (there every code is 0); E4M3: all powers of two that an append can make.  c s0 and
+    # s1 are exact in 64 bits, and their quotient (15 bits over 8) is a tie exactly or further from one than its rounding.
+    # (torch's pow on the GPU is not exact at powers of two)
+    powers = lambda lo, hi: torch.tensor([2.0 ** i for i in range(lo, hi + 1)], dtype=torch.float64, device=DEV)
+    if fmt == "int8":
+        codes = torch.arange(-127, 128, device=DEV).float()
+        s1, s0, e = torch.meshgrid(torch.arange(128, 256, device=DEV).double(), torch.arange(128, 256, device=DEV).double(),
+                                   powers(-9, 0), indexing="ij")
+        s0 = s0 * e
+        s0, s1 = s0[s0 < s1], s1[s0 < s1]
+        top = 127 * s1
+    else:
+        codes = torch.tensor(K.E4M3_VALUES + [-c for c in K.E4M3_VALUES], device=DEV)
+        s1, s0 = torch.meshgrid(powers(-32, 8), powers(-32, 8), indexing="ij")
+        s0, s1 = s0[s0 < s1], s1[s0 < s1]
+        top = (448 * s1).clamp(max=65504)
+    # the largest half whose scale is s1: one that does not exceed `top`
+    a = top.half()
+    a = torch.where(a.double() > top, (a.view(torch.int16) - 1).view(torch.float16), a)
+    assert bool((a.double() <= top).all()) and bool(a.isfinite().all())
+    hkv, dim = 4, 64
+    pad = -s0.numel() % (2 * hkv)
+    s0, s1, a = (torch.cat([t, t[:1].expand(pad)]) for t in (s0, s1, a))
+    old = torch.nn.functional.pad(codes, (0, 256 - codes.numel())).view(4, dim)  # four tokens
+    dt = K.DTYPES[fmt]
+
+    def side(s0, s1, a):
+        cache = torch.zeros(s0.shape[0], hkv, 16, dim, device=DEV)
+        cache[:, :, :4] = old
+        new = torch.zeros(s0.shape[0], hkv, 1, dim, dtype=torch.float16, device=DEV)
+        new[:, :, 0, 5] = a
+        return cache.to(dt), s0.float(), new
+
+    half = s0.numel() // 2
+    parts = [[t[i * half:(i + 1) * half].view(-1, hkv).contiguous() for t in (s0, s1, a)] for i in range(2)]
+    (k, ks, new_k), (v, vs, new_v) = side(*parts[0]), side(*parts[1])
+    _raw_append(k, v, ks, vs, new_k, new_v, 4)
+    for got, scales, (p0, p1, top) in ((k, ks, parts[0]), (v, vs, parts[1])):
+        assert torch.equal(scales.double(), p1)
+        for at in range(0, got.shape[0], 4096):
+            r = slice(at, at + 4096)
+            want = K.round_code(old.double() * (p0[r] / p1[r])[:, :, None, None] if fmt == "e4m3" else
+                                old.double() * p0[r][:, :, None, None] / p1[r][:, :, None, None], fmt)
+            assert torch.equal(got[r, :, :4].float().double(), want)
+            assert torch.equal(got[r, :, 4, 5].float().double(), K.round_code(top[r].double() / p1[r], fmt))
