@@ -48,6 +48,13 @@ __device__ __forceinline__ uint32_t q_swz(int r, int u) {
     return static_cast<uint32_t>(r * (D * 2) + ((u ^ (r & 7)) << 4));
 }
 
+// Offsets of a sequence's rows in the chunk tensors that are out of order or
+// out of range.  Compared before anything is subtracted: the difference of
+// such offsets may wrap around to a small length.
+__device__ __forceinline__ bool bad_rows(const PrefixParams& prm, int q0, int q1) {
+    return q0 < 0 || q1 < q0 || q1 > prm.num_tokens || q1 - q0 > prm.max_query_len;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrefixWarps * 32, 1)
     pa_prefix_kernel(const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc,
@@ -73,12 +80,11 @@ __global__ void __launch_bounds__(kPrefixWarps * 32, 1)
 
     const int C = __ldg(prm.context_lens + b);
     const int q0 = __ldg(prm.query_start_loc + b), q1 = __ldg(prm.query_start_loc + b + 1);
-    const int qlen = q1 - q0;
-    if (C < 0 || C > prm.max_context_len || C > prm.max_blocks_per_seq * kBlockSize || qlen < 0 ||
-        qlen > prm.max_query_len || q0 < 0 || q1 > prm.num_tokens) {
+    if (C < 0 || C > prm.max_context_len || C > prm.max_blocks_per_seq * kBlockSize || bad_rows(prm, q0, q1)) {
         if (tile == 0 && kvh == 0 && threadIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return;
     }
+    const int qlen = q1 - q0;
     const int t0 = tile * tile_tokens;  // first chunk token of this tile
     if (t0 >= qlen) return;
     const int tlast = min(qlen, t0 + tile_tokens) - 1;

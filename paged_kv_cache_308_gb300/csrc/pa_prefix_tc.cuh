@@ -312,17 +312,19 @@ __device__ __forceinline__ TcUnit tc_unit(const PrefixParams& prm, int c, bool r
     u.b = w / (prm.tiles_per_seq * prm.num_kv_heads);
     u.C = __ldg(prm.context_lens + u.b);
     u.q0 = __ldg(prm.query_start_loc + u.b);
-    u.qlen = __ldg(prm.query_start_loc + u.b + 1) - u.q0;
+    const int q1 = __ldg(prm.query_start_loc + u.b + 1);
+    u.qlen = 0;
     u.t0 = u.tile * (kTcRows / prm.group);
     u.nctx = 0;
     u.jb = 0;
     u.n = 0;
     u.run = false;
-    if (u.C < 0 || u.C > prm.max_context_len || u.C > prm.max_blocks_per_seq * kBlockSize || u.qlen < 0 ||
-        u.qlen > prm.max_query_len || u.q0 < 0 || u.q0 + u.qlen > prm.num_tokens) {
+    if (u.C < 0 || u.C > prm.max_context_len || u.C > prm.max_blocks_per_seq * kBlockSize ||
+        bad_rows(prm, u.q0, q1)) {
         if (report && u.tile == 0 && u.kvh == 0) atomicOr(prm.status, PA_DEV_BAD_SEQ_LEN);
         return u;
     }
+    u.qlen = q1 - u.q0;
     if (u.t0 >= u.qlen) return u;
     const int tlast = min(u.qlen, u.t0 + kTcRows / prm.group) - 1;
     u.nctx = (u.C + kBlockSize - 1) / kBlockSize;         // context blocks
@@ -1060,10 +1062,8 @@ __global__ void __launch_bounds__(256) pa_prefix_merge_kernel(const PrefixParams
     // is left here too
     const int C = __ldg(prm.context_lens + b);
     const int q0 = __ldg(prm.query_start_loc + b), q1 = __ldg(prm.query_start_loc + b + 1);
+    if (C < 0 || C > prm.max_context_len || C > prm.max_blocks_per_seq * kBlockSize || bad_rows(prm, q0, q1)) return;
     const int qlen = q1 - q0;
-    if (C < 0 || C > prm.max_context_len || C > prm.max_blocks_per_seq * kBlockSize || qlen < 0 ||
-        qlen > prm.max_query_len || q0 < 0 || q1 > prm.num_tokens)
-        return;
     const int row = blockIdx.y * kRowsPerCta + (int)threadIdx.x / kCols, col = (int)threadIdx.x % kCols;
     const int ti = row / G, tok = tile * tile_tokens + ti;
     if (ti >= tile_tokens || tok >= qlen) return;

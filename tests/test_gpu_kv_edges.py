@@ -80,6 +80,27 @@ def test_prefix_with_more_query_tiles_than_the_device_has_sms(fmt, heads, hkv, d
         assert torch.equal(out, prefix(c, q, k_new, v_new, loc, new, pb().PA_FLAG_PREFIX_GRID))
 
 
+@pytest.mark.parametrize("fmt", ["f16", "int8"])
+@pytest.mark.parametrize("form", ["grid", "ranges", "persistent", "warp"])
+def test_prefix_reports_offsets_whose_difference_wraps_around(form, fmt):
+    # 2^31 - 3 and -2^31 + 2 are five apart in 32 bits: no sequence of five tokens, and no row there to read or write
+    few = form != "persistent"
+    ctx, new = ([1500, 700] if form == "ranges" else [20, 90], [5, 5]) if few else ([20] * 12, [70] + [5] * 11)
+    c = K.Case(ctx, 16, 2 if few else 8, 64, fmt, seed=102, device=DEV)
+    q, k_new, v_new, loc = _chunks(c, new, 103)
+    assert (prefix_tiles(c, new) > sms()) == (form == "persistent")
+    ref, bound = K.prefix_reference(c, new, q, k_new, v_new, rounded=form == "warp" and fmt == "int8")
+    loc[1], loc[2] = 2 ** 31 - 3, -2 ** 31 + 2
+    flags = pb().PA_FLAG_PREFIX_GRID if form == "grid" else pb().PA_FLAG_PREFIX_WARP_MMA if form == "warp" else 0
+    out = torch.full_like(q, 7.0)
+    pb().pa_kv_prefix(out, q, k_new, v_new, *c.cache(), c.tables, c.seq_lens, loc, c.scale, max_context_len=c.max_len,
+                      max_query_len=max(new), flags=flags)
+    assert status() == pb().PA_DEV_BAD_SEQ_LEN
+    at = sum(new[:3])  # the sequences behind them have their rows
+    assert bool((out[:at] == 7).all())
+    check(out[at:], ref[at:], bound[at:])
+
+
 @pytest.mark.parametrize("place", ["seq_lens", "keep_lens"])
 @pytest.mark.parametrize("hkv,lens", [(2, [20000, 50]), (8, [(37 * i) % 700 for i in range(60)]), (1, [30, 0, 5]),
                                       (2, [26003] + [100] * 19)])
