@@ -614,14 +614,22 @@ int pa_kv_decode(const pa_kv_decode_args* args, const pa_decode_opts* opts, void
  * traffic is small next to the products, and expanding in every query tile
  * would repeat it up to max_query_len times.  Where few query tiles have long
  * contexts, their keys are walked in several ranges and merged, as
- * pa_prefix_split does.  The copy holds codes times the
- * power of two of their block's scale, for INT8; the rest of the scale
- * multiplies the scores and probabilities.  E4M3 values (of any scale), and
- * INT8 ones under PA_FLAG_PREFIX_WARP_MMA, are rounded to
- * fp16 (exact for scales that are powers of two; magnitudes above 65504 become
- * 65504).  The workspace needs no initialisation and holds
- * pa_kv_prefix_workspace_size bytes (for the same sizes and format, with this
- * device current).  With PA_KV_F16 no copy is made and this is pa_prefix_ex. */
+ * pa_prefix_split does.  The copy holds E4M3 values as they are and INT8 codes
+ * times the power of two of their block's scale, whose significand then
+ * multiplies the scores and probabilities; under PA_FLAG_PREFIX_WARP_MMA it
+ * holds INT8 values as they are too.  What it holds is rounded to fp16.  That
+ * is exact for E4M3 scales that are powers of two from 2^-15 to 2^7 (those
+ * pa_kv_append makes for magnitudes from 0.007 to 57344), and for INT8 scales
+ * in [2^-24, 2^10) (magnitudes from 8e-6 on) but under that flag.  With
+ * smaller scales it rounds to fp16's subnormal steps of 2^-24, with other
+ * E4M3 scales by up to 2^-11 of a value, and magnitudes above 65504 become
+ * 65504.
+ * The workspace needs no initialisation and holds pa_kv_prefix_workspace_size
+ * bytes (for the same sizes and format, with this device current).  That goes
+ * by the bounds, not by the lengths: 4 head_dim num_kv_heads bytes for each of
+ * num_seqs times max_context_len tokens (rounded up to blocks), twice what
+ * full contexts take in the cache.  With PA_KV_F16 no copy is made and this
+ * is pa_prefix_ex. */
 typedef struct {
     void* out;
     const void* q;

@@ -479,8 +479,8 @@ int check_evict(const pa_kv_evict_args* a) {
 }
 
 // Blocks that share a (sequence, kv head) in the selection.  A cluster costs about
-// 3 us more than a block alone and pays for itself above 12,000 tokens (us with
-// the move, 1, 2, 4 and 8 blocks: 8 heads of one sequence of 8192 tokens 10.1,
+// 3 us more than a block alone and pays for itself above 12,000 tokens (device us
+// with the move, 1, 2, 4 and 8 blocks: 8 heads of one sequence of 8192 tokens 10.1,
 // 12.3, 11.8, 12.1, of 16384 13.4, 13.9, 12.5, 12.2, of 32768 20.8, 18.1, 15.2,
 // 13.8), a pair of blocks above 24,000, as long as the SMs hold the whole grid,
 // of clusters of 8 half of it (16 pairs of 16384: 20.3 in clusters of 8, 13.5 of 4).

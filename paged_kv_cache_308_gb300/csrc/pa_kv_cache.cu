@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(64) kv_expand_kernel(const KvExpandParams prm)
                      : "memory");
     float s = __ldg(of_kv(prm.scales, kv) + bh);
     if (prm.factors) {
-        // s = f 2^e, 1 <= f < 2: the copy holds code 2^e, exact in fp16, and f goes
-        // into the factors
+        // s = f 2^e, 1 <= f < 2: the copy holds code 2^e, exact in fp16 for e from
+        // -24 to 9, and f goes into the factors
         const uint32_t bits = __float_as_uint(s);
         float f = 1.f;
         if (s >= 0x1p-126f && s <= 0x1p126f) {
@@ -481,8 +481,8 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, unsigned (*part)[32], uint2
 }
 
 // One: no cluster, a block has a (sequence, kv head) to itself; two share an SM,
-// in 32 registers (768 pairs of up to 1024 tokens: 32.0 instead of 40.0 us with
-// the move; 32 pairs of up to 8192 21.2 instead of 21.0), a cluster's do not (27.4
+// in 32 registers (768 pairs of up to 1024 tokens: 32.0 instead of 40.0 device us
+// with the move; 32 pairs of up to 8192 21.2 instead of 21.0), a cluster's do not (27.4
 // instead of 24.3).
 template <bool One>
 __global__ void __launch_bounds__(kEvictThreads, One ? 2 : 1) kv_evict_select_kernel(const KvEvictParams prm) {

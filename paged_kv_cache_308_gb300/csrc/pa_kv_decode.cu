@@ -18,8 +18,9 @@
 // times its product to o instead.
 // p is rounded to fp16 for the product (relative 2^-11; the shift keeps
 // products of probability and scale ratio down to 2^-28 normal and 2^-38 above
-// zero); l adds the unrounded p, in 32 bits as m and o are, so that the
-// weights of the accumulation are exact to 32-bit rounding.
+// zero); l adds the unrounded p, in 32 bits as m and o are.  So the weights of
+// the accumulation have the error of a score (a dot product in 32 bits) and of
+// the exponential (2^-22), and none of the rounding to fp16.
 //
 // From 8 bits to MMA fragments: a 32-bit register of ldmatrix holds four
 // consecutive d of one token (K), or two d of two neighbouring tokens (V,

@@ -80,6 +80,37 @@ def test_prefix_with_more_query_tiles_than_the_device_has_sms(fmt, heads, hkv, d
         assert torch.equal(out, prefix(c, q, k_new, v_new, loc, new, pb().PA_FLAG_PREFIX_GRID))
 
 
+@pytest.mark.parametrize("fmt,exponent,exact", [("e4m3", -15, True), ("e4m3", 7, True), ("e4m3", -22, False), ("e4m3", 8, False),
+                                                ("int8", -24, True), ("int8", 8, True), ("int8", -28, False)])
+def test_prefix_over_the_smallest_and_largest_scales(fmt, exponent, exact):
+    # the fp16 copy of the context: exact for the scales that the header names, its rounding outside of them
+    s = 2.0 ** exponent
+    ctx, new = [200, 33, 700], [40, 5, 3]
+    c = K.Case(ctx, 6, 2, 64, fmt, seed=104, device=DEV, spread=0.0)
+    factor = 1.0 if fmt == "e4m3" else 1.2109375  # (8 significant bits)
+    c.ks.fill_(s * factor), c.vs.fill_(s * factor)
+    for x in (c.k, c.v):  # every code, the smallest ones too
+        codes = (torch.tensor([a * b for a in K.E4M3_VALUES for b in (1, -1)]) if fmt == "e4m3" else
+                 torch.arange(-127, 128).float()).to(DEV)
+        pick = torch.randint(0, codes.numel(), x.shape, generator=torch.Generator(device=DEV).manual_seed(105), device=DEV)
+        live = x.float().isfinite() if fmt == "e4m3" else x != -128
+        x.copy_(torch.where(live, codes[pick].to(x.dtype).float(), x.float()).to(x.dtype))
+    size = 100 * s
+    c.scale = 1 / (8 * size)
+    q, k_new, v_new, loc = _chunks(c, new, 106)
+    k_new, v_new = ((x.double() * size).clamp(-65504, 65504).half() for x in (k_new, v_new))
+    copy = K.Case(ctx, 6, 2, 64, "f16", seed=104, device=DEV)
+    copy.scale, copy.tables = c.scale, c.tables
+    copy.k, copy.v = ((x.float() * s).clamp(-65504, 65504).half() for x in (c.k, c.v))
+    copy.ks, copy.vs = (torch.full_like(x, factor) for x in (c.ks, c.vs))
+    for b in range(3):
+        for a, h in zip(c.tokens(b), copy.tokens(b)):
+            assert torch.equal(a, h) == exact
+    ref, bound = K.prefix_reference(copy, new, q, k_new, v_new)
+    for flags in (0, pb().PA_FLAG_PREFIX_GRID):
+        check(prefix(c, q, k_new, v_new, loc, new, flags), ref, bound)
+
+
 @pytest.mark.parametrize("fmt", ["f16", "int8"])
 @pytest.mark.parametrize("form", ["grid", "ranges", "persistent", "warp"])
 def test_prefix_reports_offsets_whose_difference_wraps_around(form, fmt):
