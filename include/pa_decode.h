@@ -76,7 +76,9 @@ enum {
 enum {
     PA_DEV_BAD_BLOCK_ID = 1,  /* a block id read from block_tables was outside [0, num_blocks) */
     PA_DEV_BAD_SEQ_LEN = 2,   /* seq_lens[b] < 0, > max_seq_len or > max_blocks_per_seq*block_size */
-    PA_DEV_TIMEOUT = 4        /* a shared-memory copy wait gave up (bounded wait, see opts.wait_limit) */
+    PA_DEV_TIMEOUT = 4,       /* a shared-memory copy wait gave up (bounded wait, see opts.wait_limit) */
+    PA_DEV_NO_BLOCKS = 8,     /* pa_kv_alloc: too few free blocks, or free_count out of range */
+    PA_DEV_BAD_DECAY = 16     /* pa_linear_*: a log decay that is positive or NaN */
 };
 
 /* Execution modes. */
@@ -698,6 +700,182 @@ typedef struct {
 } pa_kv_evict_args;
 
 int pa_kv_evict(const pa_kv_evict_args* args, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A serving step around the cache: blocks handed out on the device, and the
+ * rotary embedding with the write into the cache.  No counterpart on the pages.
+ * Both calls allocate no device memory, are asynchronous on `stream` and can be
+ * captured into a graph; pointers are device pointers, half tensors and the
+ * rotation table 16-byte aligned, the rest 4-byte.
+ *
+ * pa_kv_alloc builds block tables and slot maps from request lengths, with the
+ * free blocks on a stack in device memory: free_blocks[0 .. free_count[0]-1] of
+ * free_blocks [num_blocks].  Sequence b holds the blocks of held_lens[b] tokens
+ * (the first ceil(held_lens[b] / block_size) entries of its row of
+ * block_tables), of which the first context_lens[b] <= held_lens[b] tokens stay,
+ * and gets query_lens[b] new ones: a decode step has one new token and held =
+ * context; a sequence that ended holds some, keeps 0 and gets 0; one that starts
+ * holds 0; one that takes back tokens written ahead keeps fewer than it holds.
+ * Afterwards it holds the blocks of context + query tokens:
+ *   entries of its row that it no longer needs go onto the stack, in the order
+ *   of the sequences and in a row from the first (the row keeps them);
+ *   entries that it needs more come from the top of the stack, in the same order,
+ *   after everything has been given back.
+ * It writes
+ *   block_tables      the new entries of the rows
+ *   free_blocks       the blocks given back
+ *   new_free_count    [1] (may be free_count)
+ *   query_start_loc   [num_seqs + 1], as for pa_prefix
+ *   seq_lens          [num_seqs]: context + query
+ *   slot_map          [num_tokens]: block * block_size + place in the block, for
+ *                     each new token in the order of query_start_loc
+ *   positions         [num_tokens]: its position in its sequence
+ * with -1 in both for rows from query_start_loc[num_seqs] on (padding).
+ * When blocks run out (PA_DEV_NO_BLOCKS) the sequences up to the last one that
+ * can be served are: from there on one that needs blocks gets none, seq_lens is
+ * its context length and its slots are -1; those that need none are served.  A
+ * sequence whose lengths are out of range (PA_DEV_BAD_SEQ_LEN: negative, context
+ * above held, more blocks than a row has) keeps its row, with seq_lens 0, slots
+ * -1 and positions unspecified; runs that end past num_tokens are cut there (PA_DEV_BAD_SEQ_LEN).  Where
+ * free_count is outside [0, num_blocks], or more blocks come back than there
+ * are, no block moves (PA_DEV_NO_BLOCKS).  Each block belongs in one row only.
+ * The outputs must not overlap each other or the inputs, but for new_free_count.
+ * num_blocks * block_size < 2^31; lengths and num_tokens up to 2^30. */
+typedef struct {
+    int32_t* block_tables;       /* [num_seqs][max_blocks_per_seq], in place */
+    int32_t* free_blocks;        /* [num_blocks], in place */
+    const int32_t* free_count;
+    int32_t* new_free_count;     /* may be free_count */
+    const int32_t* held_lens;    /* NULL: context_lens */
+    const int32_t* context_lens;
+    const int32_t* query_lens;
+    int32_t* query_start_loc;
+    int32_t* seq_lens;
+    int32_t* slot_map;
+    int32_t* positions;
+    int64_t num_blocks;
+    int num_seqs;                /* 0..65535 */
+    int num_tokens;
+    int max_blocks_per_seq;
+    int block_size;
+} pa_kv_alloc_args;
+
+int pa_kv_alloc(const pa_kv_alloc_args* args, pa_stream_t stream);
+
+/* Rotate new tokens' Q and K by their positions and put K and V into the slots
+ * of a slot map.  With r = rotary_dim (even, at most head_dim), p = positions[t],
+ * c and s the halves of row p of cos_sin (fp32 [max_positions][r]: r / 2 cosines,
+ * then r / 2 sines), for i < r / 2 and (a, b) the dims (i, i + r / 2), or (2 i,
+ * 2 i + 1) with `pairs`:
+ *     y[a] = x[a] c[i] - x[b] s[i],   y[b] = x[b] c[i] + x[a] s[i],
+ * in 32 bits, rounded once to fp16; dims from r on are copied.  q_out and k_out
+ * (fp16 [num_tokens][heads][head_dim]) get the rotated rows; they may be q and k
+ * themselves, and k_out may be NULL.  The rotated K and V go to slot_map[t] =
+ * block * block_size + place of the cache (PA_KV_F16; for an 8-bit cache, whose
+ * blocks have scales, put without a cache and call pa_kv_append with k_out).
+ * A negative slot is not written.  A negative position is a row of padding:
+ * nothing of it is read or written.  Without a cache (k_cache and v_cache NULL)
+ * v and slot_map are not used.  Slots beyond the pool set PA_DEV_BAD_BLOCK_ID
+ * and positions from max_positions on PA_DEV_BAD_SEQ_LEN; the first are not
+ * written, the second treated as padding.  Two tokens with one slot leave an
+ * unspecified mix of both.  q, k and v may have other distances between tokens
+ * than num_heads * head_dim elements (a row of a joint projection): q_stride,
+ * k_stride and v_stride, multiples of 8, 0 for contiguous tokens (in place only
+ * for these). */
+typedef struct {
+    pa_kv_cache cache;           /* PA_KV_F16; scales not used */
+    void* q_out;
+    void* k_out;                 /* may be NULL */
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* slot_map;     /* [num_tokens] */
+    const int32_t* positions;    /* [num_tokens] */
+    const float* cos_sin;        /* [max_positions][rotary_dim] */
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    int num_tokens;
+    int num_heads;
+    int rotary_dim;              /* 0: no rotation */
+    int max_positions;
+    int pairs;                   /* 0: halves, 1: neighbouring pairs */
+} pa_kv_put_args;
+
+int pa_kv_put(const pa_kv_put_args* args, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each kv head, for layers that keep a state
+ * in place of a cache.  No counterpart on the pages.
+ * The state of a (sequence, kv head) is S, fp32 [head_dim (of K)][head_dim (of V)].
+ * With g = log_decay[kv head] <= 0 (natural log; -infinity forgets at once),
+ * each token t of the sequence takes it from S_(t-1) to
+ *     S_t = exp(g) S_(t-1) + k_t v_t^T,   out[t, h, :] = scale * q[t, h, :] S_t,
+ * h over the query heads of the kv head (h / (num_heads / num_kv_heads) as for
+ * pa_decode); there is no softmax.  States lie in a pool, that of sequence b in
+ * slot slots[b]; a negative slot is no sequence (a row of padding: nothing of it
+ * is read or written), one beyond the pool is skipped with PA_DEV_BAD_BLOCK_ID.  A
+ * slot may be in a batch once (twice leaves an unspecified mix).
+ * q and out fp16 [tokens][num_heads][head_dim], k and v [tokens][num_kv_heads]
+ * [head_dim]; head_dim in {64, 128, 256}, a ratio of 1..8.  Device pointers;
+ * half tensors and states 16-byte aligned, the rest 4-byte, workspaces 256-byte.
+ * The calls allocate nothing, are asynchronous and can be captured into a graph
+ * (calls that may overlap need a workspace each).  A decay that is positive or
+ * NaN sets PA_DEV_BAD_DECAY; its head's outputs and states are then unspecified.
+ * A NaN or infinity in a token's v reaches this token's outputs and later
+ * ones of its sequence and kv head, in its own column of v only; no other. */
+typedef struct {
+    float* states;               /* [num_slots][num_kv_heads][head_dim][head_dim], in place */
+    int64_t num_slots;           /* below 2^31 */
+    int num_kv_heads;
+    int head_dim;
+} pa_linear_state;
+
+/* One new token for each sequence, row b of q, k and v. */
+typedef struct {
+    void* out;
+    const void* q;
+    const void* k;
+    const void* v;
+    pa_linear_state state;
+    const float* log_decay;      /* [num_kv_heads] */
+    const int32_t* slots;        /* [num_seqs] */
+    int num_seqs;                /* 0..65535 */
+    int num_heads;
+    float scale;
+} pa_linear_decode_args;
+
+int pa_linear_decode(const pa_linear_decode_args* args, pa_stream_t stream);
+
+/* Packed chunks of new tokens: rows query_start_loc[b] .. query_start_loc[b+1]-1
+ * belong to sequence b, which goes on from its state, or from zeros where
+ * context_lens[b] is 0 (the slot then need not hold anything), and leaves its
+ * state after its last token.  A sequence without new tokens is left as it is;
+ * rows from query_start_loc[num_seqs] on are neither read nor written.
+ * max_query_len is a host-side bound on a sequence's new tokens.  Lengths out of
+ * range set PA_DEV_BAD_SEQ_LEN and skip the sequence.  The workspace needs no
+ * initialisation and holds pa_linear_prefix_workspace_size bytes for the same
+ * sizes. */
+typedef struct {
+    void* out;
+    const void* q;
+    const void* k;
+    const void* v;
+    pa_linear_state state;
+    const float* log_decay;
+    const int32_t* slots;
+    const int32_t* context_lens;    /* [num_seqs] */
+    const int32_t* query_start_loc; /* [num_seqs + 1], as for pa_prefix */
+    int num_seqs;
+    int num_tokens;                 /* rows of q, k and v */
+    int max_query_len;
+    int num_heads;
+    float scale;
+} pa_linear_prefix_args;
+
+size_t pa_linear_prefix_workspace_size(int num_seqs, int num_tokens, int max_query_len, int num_heads,
+                                       int num_kv_heads, int head_dim);
+int pa_linear_prefix(const pa_linear_prefix_args* args, void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /* Library version, major*10000 + minor*100 + patch.  No counterpart on the pages. */
 int pa_version(void);

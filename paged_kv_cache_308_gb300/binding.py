@@ -30,6 +30,8 @@ PA_ERR_WORKSPACE = -5
 PA_DEV_BAD_BLOCK_ID = 1
 PA_DEV_BAD_SEQ_LEN = 2
 PA_DEV_TIMEOUT = 4
+PA_DEV_NO_BLOCKS = 8
+PA_DEV_BAD_DECAY = 16
 
 PA_MODE_AUTO = 0
 PA_MODE_SINGLE = 1
@@ -148,6 +150,52 @@ class pa_kv_evict_args(ctypes.Structure):
     ]
 
 
+class pa_kv_alloc_args(ctypes.Structure):
+    _fields_ = [
+        ("block_tables", ctypes.c_void_p), ("free_blocks", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+        ("new_free_count", ctypes.c_void_p), ("held_lens", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+        ("query_lens", ctypes.c_void_p), ("query_start_loc", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("slot_map", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int), ("num_tokens", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int),
+        ("block_size", ctypes.c_int),
+    ]
+
+
+class pa_kv_put_args(ctypes.Structure):
+    _fields_ = [
+        ("cache", pa_kv_cache), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("slot_map", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("cos_sin", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("num_tokens", ctypes.c_int), ("num_heads", ctypes.c_int),
+        ("rotary_dim", ctypes.c_int), ("max_positions", ctypes.c_int), ("pairs", ctypes.c_int),
+    ]
+
+
+class pa_linear_state(ctypes.Structure):
+    _fields_ = [
+        ("states", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+    ]
+
+
+class pa_linear_decode_args(ctypes.Structure):
+    _fields_ = [
+        ("out", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("state", pa_linear_state), ("log_decay", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int), ("num_heads", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class pa_linear_prefix_args(ctypes.Structure):
+    _fields_ = [
+        ("out", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("state", pa_linear_state), ("log_decay", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("context_lens", ctypes.c_void_p), ("query_start_loc", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+        ("num_tokens", ctypes.c_int), ("max_query_len", ctypes.c_int), ("num_heads", ctypes.c_int),
+        ("scale", ctypes.c_float),
+    ]
+
+
 class PaDecodeError(RuntimeError):
     def __init__(self, code: int, what: str = ""):
         self.code = code
@@ -207,6 +255,16 @@ def _load() -> ctypes.CDLL:
     lib.pa_kv_prefix.argtypes = [vp, vp, vp, ctypes.c_size_t, vp]  # pa_kv_prefix_args, pa_decode_opts
     lib.pa_kv_evict.restype = i32
     lib.pa_kv_evict.argtypes = [vp, vp]  # pa_kv_evict_args
+    lib.pa_kv_alloc.restype = i32
+    lib.pa_kv_alloc.argtypes = [vp, vp]  # pa_kv_alloc_args
+    lib.pa_kv_put.restype = i32
+    lib.pa_kv_put.argtypes = [vp, vp]  # pa_kv_put_args
+    lib.pa_linear_decode.restype = i32
+    lib.pa_linear_decode.argtypes = [vp, vp]  # pa_linear_decode_args
+    lib.pa_linear_prefix_workspace_size.restype = ctypes.c_size_t
+    lib.pa_linear_prefix_workspace_size.argtypes = [i32] * 6
+    lib.pa_linear_prefix.restype = i32
+    lib.pa_linear_prefix.argtypes = [vp, vp, ctypes.c_size_t, vp]  # pa_linear_prefix_args
     return lib
 
 
@@ -762,3 +820,139 @@ def pa_kv_evict(k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, ds
                        _tensor("new_lens", new_lens, _I32, (B,), dev), stride, dst_stride, B, cols, dst_cols,
                        int(max_seq_len), max_keep_len, int(sinks), int(recent))
     _call("pa_kv_evict", dev, stream, lib.pa_kv_evict, args)
+
+
+# --- a serving step around the cache; linear attention ---------------------------------------------------------------
+
+_ALLOC, _PUT, _LDECODE, _LPREFIX = (_packer(c) for c in (pa_kv_alloc_args, pa_kv_put_args, pa_linear_decode_args,
+                                                         pa_linear_prefix_args))
+
+
+def pa_kv_alloc(block_tables, free_blocks, free_count, context_lens, query_lens, query_start_loc, seq_lens, slot_map,
+                positions, stream=None, *, held_lens: Optional[torch.Tensor] = None,
+                new_free_count: Optional[torch.Tensor] = None, block_size: int = 16) -> None:
+    """Hand out and take back cache blocks, and build slot map and positions (see include/pa_decode.h).
+
+    All int32: block_tables [num_seqs, max_blocks_per_seq] and free_blocks [num_blocks] in place;
+    free_count / new_free_count [1] (None: in place); held_lens (None: context_lens), context_lens,
+    query_lens and the output seq_lens [num_seqs]; the outputs query_start_loc [num_seqs + 1], slot_map
+    and positions [num_tokens] (-1 behind the last token)."""
+    dev = block_tables.get_device()
+    B, T, nb = context_lens.shape[0], slot_map.shape[0], free_blocks.shape[0]
+    table, cols = _table("block_tables", block_tables, B, dev)
+    count = _tensor("free_count", free_count, _I32, (1,), dev)
+    per_seq = (B,)
+    args = _ALLOC.pack(table, _tensor("free_blocks", free_blocks, _I32, (nb,), dev), count,
+                       count if new_free_count is None else _tensor("new_free_count", new_free_count, _I32, (1,), dev),
+                       0 if held_lens is None else _tensor("held_lens", held_lens, _I32, per_seq, dev),
+                       _tensor("context_lens", context_lens, _I32, per_seq, dev),
+                       _tensor("query_lens", query_lens, _I32, per_seq, dev),
+                       _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev),
+                       _tensor("seq_lens", seq_lens, _I32, per_seq, dev), _tensor("slot_map", slot_map, _I32, (T,), dev),
+                       _tensor("positions", positions, _I32, (T,), dev), nb, B, T, cols, int(block_size))
+    _call("pa_kv_alloc", dev, stream, lib.pa_kv_alloc, args)
+
+
+def _rows(name, t, shape, dev):
+    """(pointer, elements between rows) of float16 rows that are contiguous in themselves."""
+    if t.dtype is not _F16 or t.get_device() != dev or t.shape != shape or (
+            t.numel() and (t.stride(2) != 1 or t.stride(1) != shape[2])):
+        _bad(name, t, torch.float16, shape, dev)
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+
+
+def pa_kv_put(q_out, k_out, q, k, v, k_cache, v_cache, slot_map, positions, cos_sin, stream=None, *,
+              pairs: bool = False) -> None:
+    """Rotate q and k by position and put k and v into the slots of a float16 cache (see
+    include/pa_decode.h).
+
+    q / q_out: float16 [num_tokens, num_heads, head_dim]; k / k_out / v: [num_tokens, num_kv_heads,
+    head_dim] (inputs may be parts of a joint projection's rows); q_out and k_out may be q and k,
+    k_out may be None.  cos_sin: float32 [max_positions, rotary_dim], cosines then sines.  k_cache and
+    v_cache None: rotation only; v and slot_map are then not used and may be None."""
+    dev = q.get_device()
+    T, H, dim = q.shape
+    hkv = k.shape[1]
+    q_shape, k_shape = (T, H, dim), (T, hkv, dim)
+    qp, qs = _rows("q", q, q_shape, dev)
+    kp, ks = _rows("k", k, k_shape, dev)
+    vp = vs = slots = 0
+    if k_cache is None and v_cache is None:
+        cache = (0, 0, 0, 0, 0, hkv, dim, 16, PA_KV_F16)
+    else:
+        if k_cache is None or v_cache is None:
+            raise ValueError("k_cache and v_cache come together")
+        if k_cache.dtype is not _F16:
+            raise TypeError(f"k_cache must be {_F16}, got {k_cache.dtype} (for an 8-bit cache: pa_kv_append)")
+        cache = _kv_cache(k_cache, v_cache, None, None, dev)
+        if cache[5] != hkv or cache[6] != dim:
+            raise ValueError(f"k_cache must have {hkv} kv heads of {dim}, got {list(k_cache.shape)}")
+        vp, vs = _rows("v", v, k_shape, dev)
+        slots = _tensor("slot_map", slot_map, _I32, (T,), dev)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_positions, rotary_dim]")
+    args = _PUT.pack(*cache, _tensor("q_out", q_out, _F16, q_shape, dev),
+                     0 if k_out is None else _tensor("k_out", k_out, _F16, k_shape, dev), qp, kp, vp, slots,
+                     _tensor("positions", positions, _I32, (T,), dev),
+                     _tensor("cos_sin", cos_sin, _F32, cos_sin.shape, dev), qs, ks, vs, T, H, cos_sin.shape[1],
+                     cos_sin.shape[0], int(bool(pairs)))
+    _call("pa_kv_put", dev, stream, lib.pa_kv_put, args)
+
+
+def _linear_state(states, dev):
+    shape = states.shape
+    if (states.dtype is not _F32 or states.get_device() != dev or len(shape) != 4 or shape[2] != shape[3]
+            or not states.is_contiguous()):
+        _bad("states", states, torch.float32, ("num_slots", "num_kv_heads", "head_dim", "head_dim"), dev)
+    return states.data_ptr(), shape[0], shape[1], shape[3]
+
+
+def pa_linear_decode(out, q, k, v, states, slots, log_decay, scale, stream=None) -> None:
+    """One new token a sequence of linear attention with a decay a kv head (see include/pa_decode.h).
+
+    q / out: float16 [num_seqs, num_heads, head_dim]; k / v: [num_seqs, num_kv_heads, head_dim];
+    states: float32 [num_slots, num_kv_heads, head_dim, head_dim], in place; slots: int32 [num_seqs]
+    (negative: none); log_decay: float32 [num_kv_heads], <= 0."""
+    dev = q.get_device()
+    state = _linear_state(states, dev)
+    B, H = q.shape[0], q.shape[1]
+    hkv, dim = state[2], state[3]
+    shape, new = (B, H, dim), (B, hkv, dim)
+    args = _LDECODE.pack(_tensor("out", out, _F16, shape, dev), _tensor("q", q, _F16, shape, dev),
+                         _tensor("k", k, _F16, new, dev), _tensor("v", v, _F16, new, dev), *state,
+                         _tensor("log_decay", log_decay, _F32, (hkv,), dev), _tensor("slots", slots, _I32, (B,), dev),
+                         B, H, scale)
+    _call("pa_linear_decode", dev, stream, lib.pa_linear_decode, args)
+
+
+def pa_linear_prefix_workspace_size(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads, head_dim) -> int:
+    """Bytes of pa_linear_prefix's workspace on the current device."""
+    return lib.pa_linear_prefix_workspace_size(int(num_seqs), int(num_tokens), int(max_query_len), int(num_heads),
+                                               int(num_kv_heads), int(head_dim))
+
+
+def pa_linear_prefix(out, q, k, v, states, slots, log_decay, context_lens, query_start_loc, scale, stream=None, *,
+                     max_query_len: int, workspace: Optional[torch.Tensor] = None) -> None:
+    """Packed chunks of new tokens of linear attention with a decay a kv head (see include/pa_decode.h).
+
+    q / out: float16 [num_tokens, num_heads, head_dim]; k / v: [num_tokens, num_kv_heads, head_dim];
+    states, slots and log_decay as for pa_linear_decode; context_lens: int32 [num_seqs], 0 where the
+    sequence has no state yet; query_start_loc: int32 [num_seqs + 1].  `workspace`: a tensor of
+    pa_linear_prefix_workspace_size bytes (None: one from the allocator)."""
+    dev = q.get_device()
+    state = _linear_state(states, dev)
+    T, H, B = q.shape[0], q.shape[1], context_lens.shape[0]
+    hkv, dim = state[2], state[3]
+    shape, new = (T, H, dim), (T, hkv, dim)
+    max_query_len = int(max_query_len)
+    args = _LPREFIX.pack(_tensor("out", out, _F16, shape, dev), _tensor("q", q, _F16, shape, dev),
+                         _tensor("k", k, _F16, new, dev), _tensor("v", v, _F16, new, dev), *state,
+                         _tensor("log_decay", log_decay, _F32, (hkv,), dev), _tensor("slots", slots, _I32, (B,), dev),
+                         _tensor("context_lens", context_lens, _I32, (B,), dev),
+                         _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev), B, T, max_query_len, H, scale)
+    need = 0
+    if workspace is None:
+        with torch.cuda.device(dev):  # (the blocks go by the device's SMs)
+            need = lib.pa_linear_prefix_workspace_size(B, T, max_query_len, H, hkv, dim)
+    ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
+    _call("pa_linear_prefix", dev, stream, lib.pa_linear_prefix, args, ptr, nbytes)

@@ -1,0 +1,67 @@
+// Internal interface between the C-ABI layer of block allocation, rotary put and
+// linear attention (pa_step_api.cpp) and their kernels (pa_step.cu, pa_linear.cu).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_internal.h"
+
+namespace pa {
+
+struct KvAllocParams {
+    int32_t* tables;
+    int32_t* free_blocks;
+    const int32_t* count;
+    int32_t* new_count;
+    const int32_t* held;
+    const int32_t* context;
+    const int32_t* query;
+    int32_t* loc;
+    int32_t* lens;
+    int32_t* slots;
+    int32_t* positions;
+    int num_blocks, num_seqs, num_tokens, cols;
+    unsigned int* status;
+};
+constexpr int kAllocThreads = 512;
+constexpr int kAllocMaxCluster = 8;
+cudaError_t launch_kv_alloc(const KvAllocParams& prm, int cluster, cudaStream_t stream);
+
+struct KvPutParams {
+    __half* cache[2];  // null: no cache
+    __half* q_out;
+    __half* k_out;  // may be null
+    const __half* q;
+    const __half* k;
+    const __half* v;
+    const int32_t* slots;
+    const int32_t* positions;
+    const float* cos_sin;
+    long long q_stride, k_stride, v_stride;
+    int num_blocks, num_tokens, num_heads, num_kv_heads, rot, max_positions, pairs;
+    int rows_per_warp;  // heads (of Q, K and V together) that a warp takes
+    unsigned int* status;
+};
+constexpr int kPutThreads = 128;
+cudaError_t launch_kv_put(int head_dim, const KvPutParams& prm, dim3 grid, cudaStream_t stream);
+
+struct LinearParams {
+    __half* out;
+    const __half* q;
+    const __half* k;
+    const __half* v;
+    float* states;
+    const float* log_decay;
+    const int32_t* slots;
+    const int32_t* context_lens;     // null: every sequence has a state
+    const int32_t* query_start_loc;  // null: row b is sequence b's one token
+    int num_slots, num_seqs, num_tokens, max_query_len;
+    int num_heads, num_kv_heads, group;
+    float scale;
+    unsigned int* status;
+};
+cudaError_t launch_linear_recurrent(int head_dim, const LinearParams& prm, cudaStream_t stream);
+
+}  // namespace pa

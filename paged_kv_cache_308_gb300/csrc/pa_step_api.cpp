@@ -1,0 +1,252 @@
+// C-ABI layer of block allocation, rotary put and linear attention (see
+// include/pa_decode.h): argument checks, workspace layout and launches.
+#include "pa_decode.h"
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pa_kv.h"
+#include "pa_step.h"
+
+namespace {
+
+constexpr int kMaxTokens = 1 << 30;  // lengths, rounded up to any kernel's step, stay ints
+constexpr size_t kWsAlign = 256;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool bad_ptr(const void* p, uintptr_t a) { return !p || !aligned(p, a); }
+
+// An array of words of four bytes that a call reads or writes.
+struct Words {
+    const void* p;
+    long long n;
+};
+bool overlap(const Words& a, const Words& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.n > 0 && b.n > 0 && (x < y ? y - x < 4ull * a.n : x - y < 4ull * b.n);
+}
+
+int check_alloc(const pa_kv_alloc_args* a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->num_tokens < 0 || a->max_blocks_per_seq < 0 || a->num_blocks < 0 ||
+        a->block_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (a->block_size != pa::kBlockSize || a->num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
+    if (a->num_blocks >= (1ll << 31) / pa::kBlockSize) return PA_ERR_UNSUPPORTED;  // slots are ints
+    if (bad_ptr(a->free_count, 4) || bad_ptr(a->new_free_count, 4) || bad_ptr(a->query_start_loc, 4))
+        return PA_ERR_INVALID_ARG;
+    if (a->num_seqs > 0 && (bad_ptr(a->context_lens, 4) || bad_ptr(a->query_lens, 4) || bad_ptr(a->seq_lens, 4) ||
+                            !aligned(a->held_lens, 4)))
+        return PA_ERR_INVALID_ARG;
+    if (a->num_seqs > 0 && a->max_blocks_per_seq > 0 && bad_ptr(a->block_tables, 4)) return PA_ERR_INVALID_ARG;
+    if (a->num_blocks > 0 && bad_ptr(a->free_blocks, 4)) return PA_ERR_INVALID_ARG;
+    if (a->num_tokens > 0 && (bad_ptr(a->slot_map, 4) || bad_ptr(a->positions, 4))) return PA_ERR_INVALID_ARG;
+    const long long B = a->num_seqs;
+    const Words out[] = {{a->block_tables, B * a->max_blocks_per_seq},
+                         {a->free_blocks, a->num_blocks},
+                         {a->new_free_count, 1},
+                         {a->query_start_loc, B + 1},
+                         {a->seq_lens, B},
+                         {a->slot_map, a->num_tokens},
+                         {a->positions, a->num_tokens}};
+    const Words in[] = {{a->free_count, 1}, {a->held_lens, B}, {a->context_lens, B}, {a->query_lens, B}};
+    for (const Words& o : out) {
+        for (const Words& x : out)
+            if (&x != &o && overlap(o, x)) return PA_ERR_INVALID_ARG;
+        for (const Words& x : in)  // (the new count may take the old one's place)
+            if (!(o.p == a->new_free_count && x.p == o.p && x.p == a->free_count) && overlap(o, x))
+                return PA_ERR_INVALID_ARG;
+    }
+    return PA_OK;
+}
+
+int check_put(const pa_kv_put_args* a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    const pa_kv_cache& c = a->cache;
+    if (c.num_kv_heads <= 0 || c.head_dim <= 0 || c.block_size <= 0 || c.num_blocks < 0 || a->num_tokens < 0 ||
+        a->num_heads <= 0 || a->rotary_dim < 0 || a->rotary_dim > c.head_dim || a->rotary_dim % 2 ||
+        a->max_positions < 0 || (a->pairs != 0 && a->pairs != 1))
+        return PA_ERR_INVALID_ARG;
+    if (c.format != PA_KV_F16 && c.format != PA_KV_E4M3 && c.format != PA_KV_INT8) return PA_ERR_INVALID_ARG;
+    const long long row[3] = {(long long)a->num_heads * c.head_dim, (long long)c.num_kv_heads * c.head_dim,
+                              (long long)c.num_kv_heads * c.head_dim};
+    const long long stride[3] = {a->q_stride, a->k_stride, a->v_stride};
+    for (int i = 0; i < 3; ++i)
+        if (stride[i] < 0 || stride[i] % 8 || (stride[i] && stride[i] < row[i])) return PA_ERR_INVALID_ARG;
+    if (c.format != PA_KV_F16 || c.block_size != pa::kBlockSize ||
+        (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256))
+        return PA_ERR_UNSUPPORTED;
+    // slots are ints; heads a grid dimension
+    if (c.num_blocks >= (1ll << 31) / pa::kBlockSize || a->num_heads > 65535 || c.num_kv_heads > 16384 || a->num_tokens > kMaxTokens)
+        return PA_ERR_UNSUPPORTED;
+    if (a->num_tokens == 0) return PA_OK;
+    if (bad_ptr(a->q, 16) || bad_ptr(a->k, 16) || bad_ptr(a->q_out, 16) || !aligned(a->k_out, 16) ||
+        bad_ptr(a->positions, 4) || (a->rotary_dim > 0 && bad_ptr(a->cos_sin, 16)))
+        return PA_ERR_INVALID_ARG;
+    if (!c.k_cache != !c.v_cache) return PA_ERR_INVALID_ARG;
+    if (c.k_cache && (!aligned(c.k_cache, 16) || !aligned(c.v_cache, 16) || bad_ptr(a->v, 16) || bad_ptr(a->slot_map, 4)))
+        return PA_ERR_INVALID_ARG;
+    // rows of another pitch than the outputs' cannot be rotated in place
+    if ((a->q_out == a->q && stride[0] && stride[0] != row[0]) || (a->k_out == a->k && stride[1] && stride[1] != row[1]))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+int check_linear(const pa_linear_state& s, int num_heads, float scale) {
+    if (s.num_kv_heads <= 0 || s.head_dim <= 0 || s.num_slots < 0 || num_heads <= 0 || num_heads % s.num_kv_heads ||
+        !isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if (s.head_dim != 64 && s.head_dim != 128 && s.head_dim != 256) return PA_ERR_UNSUPPORTED;
+    if (num_heads / s.num_kv_heads > pa::kMaxGroup || s.num_kv_heads > 65535 || s.num_slots >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+bool bad_linear_pointers(const void* out, const void* q, const void* k, const void* v, const pa_linear_state& s,
+                         const void* log_decay, const void* slots) {
+    return bad_ptr(out, 16) || bad_ptr(q, 16) || bad_ptr(k, 16) || bad_ptr(v, 16) || bad_ptr(s.states, 16) ||
+           bad_ptr(log_decay, 4) || bad_ptr(slots, 4);
+}
+
+int check_linear_prefix(const pa_linear_prefix_args* a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->num_tokens < 0 || a->max_query_len < 0) return PA_ERR_INVALID_ARG;
+    int rc = check_linear(a->state, a->num_heads, a->scale);
+    if (rc) return rc;
+    if (a->num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
+    if (a->num_tokens > 0 && a->max_query_len == 0) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
+    if (bad_linear_pointers(a->out, a->q, a->k, a->v, a->state, a->log_decay, a->slots) || bad_ptr(a->context_lens, 4) ||
+        bad_ptr(a->query_start_loc, 4))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_kv_alloc(const pa_kv_alloc_args* a, pa_stream_t stream) {
+    int rc = check_alloc(a);
+    if (rc) return rc;
+    pa::KvAllocParams p{};
+    p.tables = a->block_tables;
+    p.free_blocks = a->free_blocks;
+    p.count = a->free_count;
+    p.new_count = a->new_free_count;
+    p.held = a->held_lens ? a->held_lens : a->context_lens;
+    p.context = a->context_lens;
+    p.query = a->query_lens;
+    p.loc = a->query_start_loc;
+    p.lens = a->seq_lens;
+    p.slots = a->slot_map;
+    p.positions = a->positions;
+    p.num_blocks = static_cast<int>(a->num_blocks);
+    p.num_seqs = a->num_seqs;
+    p.num_tokens = a->num_tokens;
+    p.cols = a->max_blocks_per_seq;
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    return pa::launch_kv_alloc(p, pa::kAllocMaxCluster, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_kv_put(const pa_kv_put_args* a, pa_stream_t stream) {
+    int rc = check_put(a);
+    if (rc) return rc;
+    if (a->num_tokens == 0) return PA_OK;
+    const pa_kv_cache& c = a->cache;
+    pa::KvPutParams p{};
+    p.cache[0] = static_cast<__half*>(c.k_cache);
+    p.cache[1] = static_cast<__half*>(c.v_cache);
+    p.q_out = static_cast<__half*>(a->q_out);
+    p.k_out = static_cast<__half*>(a->k_out);
+    p.q = static_cast<const __half*>(a->q);
+    p.k = static_cast<const __half*>(a->k);
+    p.v = static_cast<const __half*>(a->v);
+    p.slots = a->slot_map;
+    p.positions = a->positions;
+    p.cos_sin = a->cos_sin;
+    p.q_stride = a->q_stride ? a->q_stride : (long long)a->num_heads * c.head_dim;
+    p.k_stride = a->k_stride ? a->k_stride : (long long)c.num_kv_heads * c.head_dim;
+    p.v_stride = a->v_stride ? a->v_stride : (long long)c.num_kv_heads * c.head_dim;
+    p.num_blocks = static_cast<int>(c.num_blocks);
+    p.num_tokens = a->num_tokens;
+    p.num_heads = a->num_heads;
+    p.num_kv_heads = c.num_kv_heads;
+    p.rot = a->rotary_dim;
+    p.max_positions = a->max_positions;
+    p.pairs = a->pairs;
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    const int rows = a->num_heads + 2 * c.num_kv_heads, warps = pa::kPutThreads / 32;
+    p.rows_per_warp = std::max(8, (rows + 65534) / 65535);
+    const dim3 grid((a->num_tokens + warps - 1) / warps, (rows + p.rows_per_warp - 1) / p.rows_per_warp);
+    return pa::launch_kv_put(c.head_dim, p, grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                         : PA_ERR_CUDA;
+}
+
+int pa_linear_decode(const pa_linear_decode_args* a, pa_stream_t stream) {
+    if (!a || a->num_seqs < 0 || a->num_seqs > 65535) return PA_ERR_INVALID_ARG;
+    int rc = check_linear(a->state, a->num_heads, a->scale);
+    if (rc || a->num_seqs == 0) return rc;
+    if (bad_linear_pointers(a->out, a->q, a->k, a->v, a->state, a->log_decay, a->slots)) return PA_ERR_INVALID_ARG;
+    pa::LinearParams p{};
+    p.out = static_cast<__half*>(a->out);
+    p.q = static_cast<const __half*>(a->q);
+    p.k = static_cast<const __half*>(a->k);
+    p.v = static_cast<const __half*>(a->v);
+    p.states = a->state.states;
+    p.log_decay = a->log_decay;
+    p.slots = a->slots;
+    p.num_slots = static_cast<int>(a->state.num_slots);
+    p.num_seqs = p.num_tokens = a->num_seqs;
+    p.max_query_len = 1;
+    p.num_heads = a->num_heads;
+    p.num_kv_heads = a->state.num_kv_heads;
+    p.group = a->num_heads / a->state.num_kv_heads;
+    p.scale = a->scale;
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    return pa::launch_linear_recurrent(a->state.head_dim, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_linear_prefix_workspace_size(int num_seqs, int num_tokens, int max_query_len, int num_heads,
+                                       int num_kv_heads, int head_dim) {
+    return 0;
+}
+
+int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, pa_stream_t stream) {
+    int rc = check_linear_prefix(a);
+    if (rc || a->num_seqs == 0 || a->num_tokens == 0) return rc;
+    pa::LinearParams p{};
+    p.out = static_cast<__half*>(a->out);
+    p.q = static_cast<const __half*>(a->q);
+    p.k = static_cast<const __half*>(a->k);
+    p.v = static_cast<const __half*>(a->v);
+    p.states = a->state.states;
+    p.log_decay = a->log_decay;
+    p.slots = a->slots;
+    p.context_lens = a->context_lens;
+    p.query_start_loc = a->query_start_loc;
+    p.num_slots = static_cast<int>(a->state.num_slots);
+    p.num_seqs = a->num_seqs;
+    p.num_tokens = a->num_tokens;
+    p.max_query_len = a->max_query_len;
+    p.num_heads = a->num_heads;
+    p.num_kv_heads = a->state.num_kv_heads;
+    p.group = a->num_heads / a->state.num_kv_heads;
+    p.scale = a->scale;
+    p.status = pa::device_status_ptr();
+    if (!p.status) return PA_ERR_CUDA;
+    return pa::launch_linear_recurrent(a->state.head_dim, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+}  // extern "C"
