@@ -853,9 +853,11 @@ int pa_linear_decode(const pa_linear_decode_args* args, pa_stream_t stream);
  * state after its last token.  A sequence without new tokens is left as it is;
  * rows from query_start_loc[num_seqs] on are neither read nor written.
  * max_query_len is a host-side bound on a sequence's new tokens.  Lengths out of
- * range set PA_DEV_BAD_SEQ_LEN and skip the sequence.  The workspace needs no
- * initialisation and holds pa_linear_prefix_workspace_size bytes for the same
- * sizes. */
+ * range set PA_DEV_BAD_SEQ_LEN and skip the sequence; where query_start_loc is out
+ * of order, outputs and states of the whole batch are unspecified.  The workspace
+ * needs no initialisation and holds pa_linear_prefix_workspace_size bytes for the
+ * same sizes: 0 up to 8 tokens a sequence, else about 6 head_dim^2 num_kv_heads
+ * bytes for each of num_seqs + num_tokens / 256 blocks of tokens. */
 typedef struct {
     void* out;
     const void* q;

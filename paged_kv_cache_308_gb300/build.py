@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa_decode.so")
 SOURCES = ["pa_kernels.cu", "pa_persistent.cu", "pa_prefix.cu", "pa_api.cpp", "pa_noalloc.cu", "pa_kv_decode.cu",
-           "pa_kv_cache.cu", "pa_kv_api.cpp", "pa_step.cu", "pa_linear.cu", "pa_step_api.cpp"]
+           "pa_kv_cache.cu", "pa_kv_api.cpp", "pa_step.cu", "pa_linear.cu", "pa_linear_prefix.cu", "pa_step_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

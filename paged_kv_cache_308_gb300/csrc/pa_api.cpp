@@ -21,6 +21,7 @@
 #include "pa_internal.h"
 #include "pa_kv.h"
 #include "pa_prefix.h"
+#include "pa_step.h"
 
 namespace {
 
@@ -739,17 +740,7 @@ int make_cache_block_map(CUtensorMap* map, const void* base, long long num_block
 // The same for the chunk's packed [token][kv head][head_dim] tensor: dims
 // (64 halves, kv head, token, chunk); tokens past the tensor read as zeros.
 int make_new_kv_block_map(CUtensorMap* map, const void* base, int num_tokens, int num_kv_heads, int head_dim) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return PA_ERR_CUDA;
-    cuuint64_t dims[4] = {64, (cuuint64_t)num_kv_heads, (cuuint64_t)(num_tokens > 0 ? num_tokens : 1),
-                          (cuuint64_t)(head_dim / 64)};
-    cuuint64_t strides[3] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_kv_heads * head_dim * 2, 128};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)pa::kBlockSize, (cuuint32_t)(head_dim / 64)};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+    return pa::make_rows_map(map, base, num_tokens, num_kv_heads, head_dim, pa::kBlockSize, head_dim);
 }
 
 int validate_prefix(const pa_prefix_args* a, const pa_decode_opts* o) {
@@ -1040,6 +1031,19 @@ int ensure_workspace(size_t need, void** out) {
 namespace pa {
 
 int sm_count(int* num_sms) { return query_sm_count(num_sms); }
+
+int make_rows_map(CUtensorMap* map, const void* base, long long tokens, int heads, int head_dim, int rows, int cols) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PA_ERR_CUDA;
+    cuuint64_t dims[4] = {64, (cuuint64_t)heads, (cuuint64_t)(tokens > 0 ? tokens : 1), (cuuint64_t)(head_dim / 64)};
+    cuuint64_t strides[3] = {(cuuint64_t)head_dim * 2, (cuuint64_t)heads * head_dim * 2, 128};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, (cuuint32_t)(cols / 64)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
 
 int check_prefix(const pa_prefix_args* a, const pa_decode_opts* o) { return validate_prefix(a, o); }
 

@@ -7,6 +7,7 @@
 
 #include "pa_decode.h"
 #include "pa_device.cuh"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 

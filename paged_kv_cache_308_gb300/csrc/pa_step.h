@@ -64,4 +64,33 @@ struct LinearParams {
 };
 cudaError_t launch_linear_recurrent(int head_dim, const LinearParams& prm, cudaStream_t stream);
 
+// The chunked form: a sequence's new tokens in blocks of kLinearBlock; block n of
+// sequence b is number query_start_loc[b] / kLinearBlock + b + n, so that the
+// blocks of packed sequences are numbered without gaps wider than one.
+constexpr int kLinearBlock = 256;
+constexpr int kLinearTile = 128;  // rows of an output tile; columns and rows of a state tile
+struct LinearChunkParams {
+    LinearParams lin;
+    float* adds;           // [blocks][Hkv][D][D]: what a block's tokens add to the state
+    __half* starts;        // [blocks][Hkv][D][D]: the state before a block, times 2^-exponent
+    int* exponents;        // [blocks][Hkv]
+    float* add_max;        // [blocks][Hkv][tiles]: largest finite magnitude in adds
+    float* state_max;      // [B][Hkv]: of the state before the first block
+    int* first_bad;        // [blocks][Hkv][D]: first token of a block with a NaN or infinity in that column of v
+    int blocks;            // numbers of blocks, those of no block among them
+    int wait_limit;
+};
+// k and v: [token][kv head][D] in boxes of (rows, columns); q: 128 rows of all columns;
+// starts: 64 rows of a tile's columns.
+struct LinearMaps {
+    CUtensorMap k_block, q, k, v, starts;
+};
+cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
+cudaError_t launch_linear_scan(int head_dim, const LinearChunkParams& prm, cudaStream_t stream);
+cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
+
+// Tensor map of packed rows [tokens][heads][head_dim] of halves: a box is `rows` tokens of one head by `cols`
+// columns, laid out [64-column chunk][rows][128 B] with the 128-byte swizzle; coordinates (0, head, token, chunk).
+int make_rows_map(CUtensorMap* map, const void* base, long long tokens, int heads, int head_dim, int rows, int cols);
+
 }  // namespace pa

@@ -124,6 +124,30 @@ int check_linear_prefix(const pa_linear_prefix_args* a) {
     return PA_OK;
 }
 
+// Up to so many new tokens a sequence go token by token.
+constexpr int kLinearFewTokens = 8;
+
+// The chunked form's workspace: bytes, offsets (the blocks' sums are at 0).
+struct LinearSpace {
+    long long blocks;
+    size_t starts, exponents, add_max, state_max, first_bad, bytes;
+};
+
+LinearSpace linear_space(int num_seqs, int num_tokens, int num_kv_heads, int head_dim) {
+    auto up = [](size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; };
+    LinearSpace s;
+    s.blocks = num_tokens / pa::kLinearBlock + (long long)num_seqs;
+    const size_t heads = (size_t)s.blocks * num_kv_heads, square = (size_t)head_dim * head_dim;
+    const int tiles = std::max(1, head_dim / pa::kLinearTile);
+    s.starts = up(heads * square * 4);
+    s.exponents = s.starts + up(heads * square * 2);
+    s.add_max = s.exponents + up(heads * 4);
+    s.state_max = s.add_max + up(heads * tiles * tiles * 4);
+    s.first_bad = s.state_max + up((size_t)num_seqs * num_kv_heads * 4);
+    s.bytes = s.first_bad + up(heads * head_dim * 4);
+    return s;
+}
+
 }  // namespace
 
 extern "C" {
@@ -218,13 +242,20 @@ int pa_linear_decode(const pa_linear_decode_args* a, pa_stream_t stream) {
 
 size_t pa_linear_prefix_workspace_size(int num_seqs, int num_tokens, int max_query_len, int num_heads,
                                        int num_kv_heads, int head_dim) {
-    return 0;
+    if (num_seqs <= 0 || num_seqs > 65535 || num_tokens <= 0 || num_tokens > kMaxTokens || max_query_len <= 0 ||
+        num_heads <= 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_query_len <= kLinearFewTokens)
+        return 0;
+    return linear_space(num_seqs, num_tokens, num_kv_heads, head_dim).bytes;
 }
 
-int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, pa_stream_t stream) {
+int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, pa_stream_t stream_) {
     int rc = check_linear_prefix(a);
     if (rc || a->num_seqs == 0 || a->num_tokens == 0) return rc;
-    pa::LinearParams p{};
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const int D = a->state.head_dim, K = a->state.num_kv_heads;
+    pa::LinearChunkParams c{};
+    pa::LinearParams& p = c.lin;
     p.out = static_cast<__half*>(a->out);
     p.q = static_cast<const __half*>(a->q);
     p.k = static_cast<const __half*>(a->k);
@@ -239,14 +270,40 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     p.num_tokens = a->num_tokens;
     p.max_query_len = a->max_query_len;
     p.num_heads = a->num_heads;
-    p.num_kv_heads = a->state.num_kv_heads;
-    p.group = a->num_heads / a->state.num_kv_heads;
+    p.num_kv_heads = K;
+    p.group = a->num_heads / K;
     p.scale = a->scale;
+    const bool few = a->max_query_len <= kLinearFewTokens;
+    const LinearSpace sp = linear_space(a->num_seqs, a->num_tokens, K, D);
+    if (!few) {
+        // rows of the tensor maps and CTAs of a grid are 32-bit
+        if (sp.blocks * K * D >= (1ll << 31) || sp.blocks * 2 * a->num_heads * 2 >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+        if (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
+    }
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
-    return pa::launch_linear_recurrent(a->state.head_dim, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    if (few) return pa::launch_linear_recurrent(D, p, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    c.adds = reinterpret_cast<float*>(w);
+    c.starts = reinterpret_cast<__half*>(w + sp.starts);
+    c.exponents = reinterpret_cast<int*>(w + sp.exponents);
+    c.add_max = reinterpret_cast<float*>(w + sp.add_max);
+    c.state_max = reinterpret_cast<float*>(w + sp.state_max);
+    c.first_bad = reinterpret_cast<int*>(w + sp.first_bad);
+    c.blocks = static_cast<int>(sp.blocks);
+    c.wait_limit = pa::kDefaultWaitLimit;
+    const int tile = std::min(D, pa::kLinearTile);
+    pa::LinearMaps maps;
+    if ((rc = pa::make_rows_map(&maps.k_block, a->k, a->num_tokens, K, D, pa::kLinearBlock, tile)) ||
+        (rc = pa::make_rows_map(&maps.q, a->q, a->num_tokens, a->num_heads, D, 128, D)) ||
+        (rc = pa::make_rows_map(&maps.k, a->k, a->num_tokens, K, D, 64, tile)) ||
+        (rc = pa::make_rows_map(&maps.v, a->v, a->num_tokens, K, D, 64, tile)) ||
+        (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, 64, tile)))
+        return rc;
+    if (pa::launch_linear_adds(D, c, maps, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
+        pa::launch_linear_out(D, c, maps, stream) != cudaSuccess)
+        return PA_ERR_CUDA;
+    return PA_OK;
 }
 
 }  // extern "C"
