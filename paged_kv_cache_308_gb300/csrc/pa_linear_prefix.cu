@@ -54,15 +54,20 @@ __device__ __forceinline__ bool seq_of(const LinearParams& p, int b, Seq& s, uns
     return status == 0 && s.count > 0;
 }
 
-// The block of a number: sequence, its place in it, its tokens.
+// The block of a number: sequence, its place in it, its tokens.  By a whole warp: 32
+// sequences at a time, so that a batch of up to 32 takes one round of loads.
 struct Block {
     int b, n, first, count, context;
 };
 __device__ __forceinline__ bool block_of(const LinearParams& p, int number, Block& k) {
-    int lo = 0, hi = p.num_seqs;  // the last sequence whose numbers start at or before it
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        (__ldg(p.query_start_loc + mid) / kLinearBlock + mid <= number ? lo : hi) = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, left = p.num_seqs;  // the last sequence whose numbers start at or before it is one of these
+    while (left > 1) {
+        const int step = (left + 31) / 32, at = lo + lane * step;
+        const bool before = lane == 0 || (at < lo + left && __ldg(p.query_start_loc + at) / kLinearBlock + at <= number);
+        const int skip = (31 - __clz(__ballot_sync(kFull, before))) * step;
+        lo += skip;
+        left = min(step, left - skip);
     }
     Seq s;
     unsigned status;
@@ -82,40 +87,46 @@ template <int D>
 struct AddShape {
     static constexpr int kTile = D < kLinearTile ? D : kLinearTile;
     static constexpr int kTiles = D / kTile;
-    static constexpr int kKBytes = kLinearBlock * kTile * 2;
+    static constexpr int kGroup = 64;                     // tokens of a stage
+    static constexpr int kHalf = kGroup * kTile * 2;      // bytes of a stage's k, and of its v
+    static constexpr int kSlots = 3;
+    static constexpr int kRing = kSlots * 2 * kHalf;
     // two CTAs an SM, whose TMEM allocations then always fit
-    static constexpr int kSmem = (kKBytes > 78 * 1024 ? kKBytes : 78 * 1024) + 2048 + 1024;
-    static constexpr int kTmem = 256;  // the sum, and 128 tokens of v in two halves
+    static constexpr int kSmem = (kRing > 78 * 1024 ? kRing : 78 * 1024) + 2048 + 1024;
+    static constexpr int kTmem = 256;  // the sum, and 64 tokens of v in two halves, twice
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
+constexpr int kAddThreads = 6 * 32;
 
-// A CTA has a tile of (128 columns of k) x (128 columns of v) of a block's sum.
-// Lane (thread) c of the accumulator is a column of v: the thread reads that column of
-// the block's tokens, 64 contiguous bytes a warp and token, scales it and writes it to
-// tensor memory as the MMA's A operand (two halves, 128 tokens at a time); k is the B
-// operand as TMA brings it, token by token.  CTAs past the blocks find the largest
-// entries of the sequences' first states.
+// A CTA has a tile of (128 columns of k) x (128 columns of v) of a block's sum, and
+// takes the block's tokens 64 at a time, the last ones first.  Warp 5 brings them; lane
+// (thread) c of warps 0-3 is a column of v, whose tokens it scales and writes to tensor
+// memory as the MMA's A operand (two halves); warp 4 multiplies by k, the B operand, as TMA
+// laid it out.  The column's power of two is set by the first tokens that are not 0 (the
+// decay makes earlier ones smaller) with room above, and moves, with the column's sum so far,
+// where later ones would not fit.  CTAs past the blocks find the largest entries of the
+// sequences' first states.
 template <int D>
-__global__ void __launch_bounds__(128, 2)
-    linear_adds_kernel(const __grid_constant__ CUtensorMap tmap_k, const LinearChunkParams c) {
+__global__ void __launch_bounds__(kAddThreads, 2)
+    linear_adds_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {
     using S = AddShape<D>;
     const LinearParams& p = c.lin;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* ks = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    float* w = reinterpret_cast<float*>(ks + S::kKBytes);
+    uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    float* w = reinterpret_cast<float*>(ring + S::kRing);
     uint64_t* bars = reinterpret_cast<uint64_t*>(w + kLinearBlock);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 8);
     volatile int* failed = reinterpret_cast<volatile int*>(tslot + 1);
-    float* red = reinterpret_cast<float*>(tslot + 2);
+    int* bad_sm = reinterpret_cast<int*>(tslot + 2);
+    float* red = reinterpret_cast<float*>(tslot + 3);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, kvh = blockIdx.y, number = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    auto block_max = [&](float m) {
+    auto warp_max = [&](float m) {
 #pragma unroll
         for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-        if (lane == 0) red[warp] = m;
-        __syncthreads();
-        return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        return m;
     };
     auto finite_max = [](float m, float x) {
         const float a = fabsf(x);
@@ -130,169 +141,212 @@ __global__ void __launch_bounds__(128, 2)
         if (s.context > 0) {
             const float4* st = reinterpret_cast<const float4*>(p.states + ((size_t)s.slot * p.num_kv_heads + kvh) * D * D);
 #pragma unroll 8
-            for (int i = t; i < D * D / 4; i += 128) {
+            for (int i = t; i < D * D / 4; i += kAddThreads) {
                 const float4 x = st[i];
                 m = finite_max(finite_max(finite_max(finite_max(m, x.x), x.y), x.z), x.w);
             }
         }
-        m = block_max(m);
-        if (t == 0) c.state_max[(size_t)b * p.num_kv_heads + kvh] = m;
+        m = warp_max(m);
+        if (lane == 0) red[warp] = m;
+        __syncthreads();
+        if (t == 0) {
+            for (int i = 1; i < kAddThreads / 32; ++i) m = fmaxf(m, red[i]);
+            c.state_max[(size_t)b * p.num_kv_heads + kvh] = m;
+        }
         return;
     }
     Block k;
     if (!block_of(p, number, k)) return;
     const int k_tile = blockIdx.z / S::kTiles, v_tile = blockIdx.z % S::kTiles;
-    const uint32_t bar_k = smem_addr(bars), bar_mma = bar_k + 8;
+    const int groups = (k.count + S::kGroup - 1) / S::kGroup;
+    const uint32_t bar_full = smem_addr(bars), bar_v = bar_full + 8 * S::kSlots, bar_mma = bar_v + 16;
     if (t == 0) {
         *failed = 0;
-        mbar_init(bar_k, 1);
-        mbar_init(bar_mma, 1);
+        *bad_sm = 0;
+        for (int i = 0; i < S::kSlots; ++i) mbar_init(bar_full + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_v + 8 * i, 4);    // the operand of a group in buffer i is written
+            mbar_init(bar_mma + 8 * i, 1);  // and has been read
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        mbar_arrive_expect_tx(bar_k, S::kKBytes);
-        tc_tma_load_4d(smem_addr(ks), &tmap_k, 0, kvh, k.first, k_tile * (S::kTile / 64), bar_k);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)), "r"(S::kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // 64 tokens of the thread's column, in pairs; none past the block.  Read twice, for the column's
-    // largest and for the operand: 256 tokens at once would not fit in registers.
-    const bool mine = t < S::kTile;
-    const size_t row = (size_t)p.num_kv_heads * D;
-    const unsigned short* col = reinterpret_cast<const unsigned short*>(p.v) + (size_t)k.first * row + (size_t)kvh * D +
-                                v_tile * S::kTile + t;
-    auto read = [&](int first, uint32_t(&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int at = first + 2 * i;
-            const unsigned a = mine && at < k.count ? __ldg(col + at * row) : 0;
-            const unsigned b = mine && at + 1 < k.count ? __ldg(col + (at + 1) * row) : 0;
-            v[i] = a | b << 16;
-        }
-    };
     const float g = fmaxf(__ldg(p.log_decay + kvh), -1e4f);  // (whose exp is 0, and 1 for no tokens)
-    for (int i = t; i < kLinearBlock; i += 128) w[i] = i < k.count ? expf(g * (float)(k.count - 1 - i)) : 0.f;
+    for (int i = t; i < kLinearBlock; i += kAddThreads) w[i] = i < k.count ? expf(g * (float)(k.count - 1 - i)) : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot, lanes = (uint32_t)(warp * 32) << 16;
-    const uint32_t t_sum = tmem, t_v = tmem + 128;
+    const uint32_t tmem = *tslot, t_sum = tmem, t_v = tmem + 128;
+    const unsigned limit = c.wait_limit;
+    // group x holds the tokens from 64 * (groups - 1 - x) of the block on
+    auto tokens_at = [&](int x) { return (groups - 1 - x) * S::kGroup; };
+    auto fail = [&] {
+        *failed = 1;
+        atomicOr(p.status, PA_DEV_TIMEOUT);
+    };
 
-    auto halves = [](uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); };
-    float m = 0.f;
-    int first = kLinearBlock;  // token with a NaN or infinity
-#pragma unroll 1
-    for (int at = 0; at < k.count; at += 64) {
-        uint32_t v[32];
-        read(at, v);
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float2 x = halves(v[i]);
-            const float2 wi = *reinterpret_cast<const float2*>(w + at + 2 * i);
-            bad |= !(fabsf(x.x) <= 65504.f) || !(fabsf(x.y) <= 65504.f);
-            m = finite_max(finite_max(m, x.x * wi.x), x.y * wi.y);
-        }
-        if (bad && first == kLinearBlock) {
-#pragma unroll
-            for (int i = 31; i >= 0; --i) {
-                if ((v[i] & 0x7c000000u) == 0x7c000000u) first = at + 2 * i + 1;
-                if ((v[i] & 0x7c00u) == 0x7c00u) first = at + 2 * i;
+    if (warp == 5) {
+        if (lane == 0) {
+            bool ok = true;
+            int x = 0;
+            for (; x < groups; ++x) {
+                const int s = x % S::kSlots;
+                if (x >= S::kSlots &&
+                    !(ok = tc_wait(bar_mma + 8 * ((x - S::kSlots) & 1), ((x - S::kSlots) >> 1) & 1, limit, failed)))
+                    break;
+                mbar_arrive_expect_tx(bar_full + 8 * s, 2 * S::kHalf);
+                const uint32_t dst = smem_addr(ring + s * 2 * S::kHalf);
+                tc_tma_load_4d(dst, &maps.k, 0, kvh, k.first + tokens_at(x), k_tile * (S::kTile / 64), bar_full + 8 * s);
+                tc_tma_load_4d(dst + S::kHalf, &maps.v, 0, kvh, k.first + tokens_at(x), v_tile * (S::kTile / 64), bar_full + 8 * s);
             }
+            if (!ok) fail();
+            // every copy lands before the CTA's memory is given back
+            for (int i = max(0, x - S::kSlots); i < x; ++i)
+                mbar_wait(bar_full + 8 * (i % S::kSlots), (i / S::kSlots) & 1, kDefaultWaitLimit);
         }
-    }
-    const int up = m > 0.f ? min(13 - exponent_of(m), 100) : 0;
-    const float raise = pow2(up), lower = pow2(-up);
-    if (k_tile == 0 && mine)
-        c.first_bad[((size_t)number * p.num_kv_heads + kvh) * D + v_tile * S::kTile + t] = first;
-
-    constexpr uint32_t id = tc_idesc(128, S::kTile, 1);
-    const uint64_t kdesc = tc_desc(smem_addr(ks), kLinearBlock * 128, 1024);
-    const int steps = (k.count + 15) / 16;
-    bool ok = true;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        if (half * 128 < k.count) {
-            if (half == 1) {  // the operand's memory is read until the first half's MMAs end
-                ok = tc_warp_wait(bar_mma, 0, c.wait_limit, failed);
+        __syncwarp();
+    } else if (warp == 4) {
+        if (lane == 0) {
+            constexpr uint32_t id = tc_idesc(128, S::kTile, 1);
+            bool ok = true;
+            int x = 0;
+            for (; x < groups; ++x) {
+                // (the rows wait for the group's copies before they write the operand)
+                if (!(ok = tc_wait(bar_v + 8 * (x & 1), (x >> 1) & 1, limit, failed))) break;
+                tc_fence_after();
+                const uint64_t kd = tc_desc(smem_addr(ring + (x % S::kSlots) * 2 * S::kHalf), S::kGroup * 128, 1024);
+                const int steps = (min(k.count - tokens_at(x), S::kGroup) + 15) / 16;
+                for (int part = 1; part >= 0; --part)  // the small halves first
+                    for (int s = 0; s < steps; ++s)
+                        tc_mma_ts(t_sum, t_v + (x & 1) * 64 + part * 32 + s * 8, kd + (uint64_t)((s * 2048) >> 4), id,
+                                  x > 0 || part == 0 || s > 0);
+                tc_commit(bar_mma + 8 * (x & 1));
+            }
+            if (!ok) fail();
+            // every MMA is done before the CTA's memory is given back
+            if (x > 0) mbar_wait(bar_mma + 8 * ((x - 1) & 1), ((x - 1) >> 1) & 1, kDefaultWaitLimit);
+        }
+        __syncwarp();
+    } else {
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const bool mine = t < S::kTile;
+        const int chunk = t >> 6, unit = (t & 63) >> 3, in_unit = t & 7;  // of the column in a row's 64-column chunk
+        // (the 128-byte swizzle: 16-byte units exchanged by the row's number)
+        auto column = [&](const uint8_t* tile, int i) {
+            return __half2float(*reinterpret_cast<const __half*>(tile + i * 128 + ((unit ^ (i & 7)) << 4) + in_unit * 2));
+        };
+        int up = 0, first = kLinearBlock;
+        bool set = false, ok = true;
+        for (int x = 0; x < groups; ++x) {
+            const int at = tokens_at(x), count = min(k.count - at, S::kGroup);
+            uint8_t* ks = ring + (x % S::kSlots) * 2 * S::kHalf;
+            const uint8_t* vs = ks + S::kHalf + chunk * (S::kGroup * 128);
+            if (!(ok = tc_warp_wait(bar_full + 8 * (x % S::kSlots), (x / S::kSlots) & 1, limit, failed))) break;
+            // rows of other sequences behind the block's last token: nothing of them, whatever they hold
+            const int tail = (count + 15) / 16 * 16 - count;
+            for (int i = t; i < tail * (S::kTile / 8); i += 128) {
+                const int r = count + i / (S::kTile / 8), u = i % (S::kTile / 8);
+                *reinterpret_cast<uint4*>(ks + (u >> 3) * (S::kGroup * 128) + r * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (tail) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            float a[64];
+            float m = 0.f;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                const float v = mine && i < count ? column(vs, i) : 0.f;
+                bad |= !(fabsf(v) <= 65504.f);
+                a[i] = v * w[at + i];
+                m = fmaxf(m, fabsf(a[i]));
+            }
+            if (bad) {  // the power of two is that of the others
+                m = 0.f;
+#pragma unroll
+                for (int i = 63; i >= 0; --i) {
+                    const bool there = mine && i < count;
+                    if (there && !(fabsf(column(vs, i)) <= 65504.f))
+                        first = at + i;
+                    else
+                        m = fmaxf(m, fabsf(a[i]));
+                }
+            }
+            const int e = exponent_of(m);
+            const bool move = m > 0.f && (!set || e + up > 14);
+            const int was = up;
+            if (move) up = min(8 - e, 100);
+            if (x >= 2) {  // the operand's buffer has been read
+                if (!(ok = tc_warp_wait(bar_mma + 8 * (x & 1), ((x - 2) >> 1) & 1, limit, failed))) break;
                 tc_fence_after();
             }
+            if (x > 0 && __any_sync(kFull, move && set)) {
+                if (!(ok = tc_warp_wait(bar_mma + 8 * ((x - 1) & 1), ((x - 1) >> 1) & 1, limit, failed))) break;
+                tc_fence_after();
+                const float f = move && set ? pow2(up - was) : 1.f;
 #pragma unroll 1
-            for (int part = 0; part < 2; ++part) {
-                const int at = half * 128 + part * 64;
-                uint32_t v[32], hi[32], lo[32];
-                read(at, v);
+                for (int c0 = 0; c0 < S::kTile; c0 += 32) {
+                    uint32_t o[32];
+                    tc_ld32(t_sum + lanes + c0, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float2 x = halves(v[i]);
-                    const float2 wi = *reinterpret_cast<const float2*>(w + at + 2 * i);
-                    const float a = x.x * wi.x * raise, b = x.y * wi.y * raise;
-                    const __half2 h = __floats2half2_rn(a, b);
-                    const float2 back = __half22float2(h);
-                    hi[i] = half2_bits(h);
-                    lo[i] = half2_bits(__floats2half2_rn(a - back.x, b - back.y));
+                    for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                    tc_st32(t_sum + lanes + c0, o);
                 }
-                tc_st32x2(t_v + lanes + part * 32, hi, t_v + lanes + 64 + part * 32, lo);
             }
-            if (half == 0) {
-                ok = tc_warp_wait(bar_k, 0, c.wait_limit, failed);
-                // rows of other sequences behind the block's last token: their v is 0 here, but
-                // 0 * NaN is not
-                const int tail = steps * 16 - k.count;
-                for (int i = t; i < tail * (S::kTile / 8); i += 128) {
-                    const int r = k.count + i / (S::kTile / 8), u = i % (S::kTile / 8);
-                    *reinterpret_cast<uint4*>(ks + (u >> 3) * (kLinearBlock * 128) + r * 128 + (u & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                if (tail) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            set |= move;
+            const float raise = pow2(up);
+            uint32_t hi[32], lo[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float y0 = a[2 * i] * raise, y1 = a[2 * i + 1] * raise;
+                const __half2 h = __floats2half2_rn(y0, y1);
+                const float2 back = __half22float2(h);
+                hi[i] = half2_bits(h);
+                lo[i] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
             }
-            if (!ok) *failed = 1;
+            tc_st32x2(t_v + lanes + (x & 1) * 64, hi, t_v + lanes + (x & 1) * 64 + 32, lo);
             tc_fence_before();
-            __syncthreads();
-            if (t == 0 && !*failed) {
-                tc_fence_after();
-                const int s0 = half * 8, s1 = min(steps, s0 + 8);
-                for (int x = 1; x >= 0; --x)  // the small halves first
-                    for (int s = s0; s < s1; ++s)
-                        tc_mma_ts(t_sum, t_v + x * 64 + (s - s0) * 8, kdesc + (uint64_t)((s * 2048) >> 4), id,
-                                  half > 0 || x == 0 || s > s0);
-                tc_commit(bar_mma);
-            }
             __syncwarp();
+            if (lane == 0) mbar_arrive(bar_v + 8 * (x & 1));
         }
-    }
-    if (!*failed) {
-        ok = tc_warp_wait(bar_mma, k.count > 128 ? 1 : 0, c.wait_limit, failed);
-        if (!ok) *failed = 1;
-    }
-    __syncthreads();
-    if (*failed) {
-        if (t == 0) atomicOr(p.status, PA_DEV_TIMEOUT);
-        // what is in flight lands before the CTA's memory is given back
-        mbar_wait(bar_k, 0, kDefaultWaitLimit);
-        mbar_wait(bar_mma, k.count > 128 ? 1 : 0, kDefaultWaitLimit);
-    }
-    tc_fence_after();
-    m = 0.f;
-    float* dst = c.adds + (((size_t)number * p.num_kv_heads + kvh) * D + k_tile * S::kTile) * D + v_tile * S::kTile + t;
+        if (k_tile == 0 && mine) {
+            c.first_bad[((size_t)number * p.num_kv_heads + kvh) * D + v_tile * S::kTile + t] = first;
+            if (first < kLinearBlock) *bad_sm = 1;
+        }
+        if (ok) ok = tc_warp_wait(bar_mma + 8 * ((groups - 1) & 1), ((groups - 1) >> 1) & 1, limit, failed);
+        float m = 0.f;
+        if (ok) {
+            tc_fence_after();
+            const float lower = pow2(-up);
+            float* dst = c.adds + (((size_t)number * p.num_kv_heads + kvh) * D + k_tile * S::kTile) * D + v_tile * S::kTile + t;
+#pragma unroll 1
+            for (int c0 = 0; c0 < S::kTile; c0 += 32) {
+                uint32_t o[32];
+                tc_ld32(t_sum + lanes + c0, o);
+                if (mine) {
 #pragma unroll
-    for (int c0 = 0; c0 < S::kTile; c0 += 32) {
-        uint32_t x[32];
-        tc_ld32(t_sum + lanes + c0, x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float y = __uint_as_float(x[i]) * lower;
-            if (mine) {
-                m = finite_max(m, y);
-                dst[(size_t)(c0 + i) * D] = y;
+                    for (int i = 0; i < 32; ++i) {
+                        const float y = __uint_as_float(o[i]) * lower;
+                        m = finite_max(m, y);
+                        dst[(size_t)(c0 + i) * D] = y;
+                    }
+                }
             }
+        } else if (lane == 0) {
+            fail();
         }
+        m = warp_max(m);
+        if (lane == 0) red[warp] = m;
     }
-    m = block_max(m);
-    if (t == 0) c.add_max[((size_t)number * p.num_kv_heads + kvh) * (S::kTiles * S::kTiles) + blockIdx.z] = m;
     tc_fence_before();
     __syncthreads();
+    if (t == 0) {
+        const size_t index = (size_t)number * p.num_kv_heads + kvh;
+        c.add_max[index * (S::kTiles * S::kTiles) + blockIdx.z] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        if (k_tile == 0) c.any_bad[index * S::kTiles + v_tile] = *bad_sm;
+    }
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem));
 }
 
@@ -331,10 +385,23 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
     const size_t index = (size_t)(s.first / kLinearBlock + b) * p.num_kv_heads + kvh;  // of the first block
     const float4* add = reinterpret_cast<const float4*>(c.adds + index * D * D + at);
     const size_t step = (size_t)p.num_kv_heads * D * D;
-    float4 next = __ldcs(add);
-    for (int n = 0; n < blocks; ++n) {
-        const float4 a = next;
-        if (n + 1 < blocks) next = __ldcs(add + (n + 1) * step / 4);
+    // four blocks ahead: what a round of the loop waits for has long been asked for
+    constexpr int kAhead = 4;
+    float4 next[kAhead];
+    float most_next[kAhead];
+    auto fetch = [&](int n, float4& a, float& most) {
+        if (n >= blocks) return;
+        a = __ldcs(add + n * step / 4);
+        most = 0.f;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) most = fmaxf(most, __ldg(c.add_max + (index + (size_t)n * p.num_kv_heads) * kTiles + j));
+    };
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) fetch(n, next[n], most_next[n]);
+    auto one = [&](int n, float4& slot, float& most_slot) {
+        const float4 a = slot;
+        const float most = most_slot;
+        fetch(n + kAhead, slot, most_slot);
         const size_t i = index + (size_t)n * p.num_kv_heads;
         if (n > 0 || s.context > 0) {
             const int e = bound > 0.f ? max(min(exponent_of(bound) - 13, 100), -100) : 0;
@@ -350,10 +417,12 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
         const float whole = y > -0.5f ? 1.f : 0.f, rest = y > -0.5f ? expm1f(y) : expf(y);
         auto chain = [&](float v, float plus) { return fmaf(v, rest, v * whole) + plus; };
         x = make_float4(chain(x.x, a.x), chain(x.y, a.y), chain(x.z, a.z), chain(x.w, a.w));
-        float most = 0.f;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) most = fmaxf(most, __ldg(c.add_max + i * kTiles + j));
         bound = (bound * (whole + rest) + most) * 1.0001f;
+    };
+    for (int n = 0; n < blocks; n += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (n + j < blocks) one(n + j, next[j], most_next[j]);
     }
     *state = x;
 }
@@ -362,30 +431,87 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
 
 template <int D>
 struct OutShape {
-    static constexpr int kCols = D < 128 ? D : 128;      // of v and out, of a CTA
+    static constexpr int kCols = D < 128 ? D : 128;      // of v and out, of a unit
     static constexpr int kSplits = D / kCols;
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = 64 * kCols * 2;   // 64 tokens or state rows by kCols columns
     static constexpr int kSlots = D == 256 ? 3 : D == 128 ? 5 : 8;
-    static constexpr int kBars = 9 + 2 * kSlots;
-    static constexpr int kCtrl = kCols * 4 + kBars * 8 + 16 + 256;  // first_bad, barriers, TMEM address and flag, d^(63-j)
+    static constexpr int kBars = 16 + 2 * kSlots;
+    static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64;  // barriers, TMEM address and flag, two units
     static constexpr int kSmem = kQBytes + kSlots * kStageBytes + kCtrl;
     static constexpr int kTmem = 256;                    // kCols of the outputs, two buffers of 64 scores
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 constexpr int kOutRowWarps = 4, kOutThreads = (kOutRowWarps + 2) * 32;
 
-enum : int { kBarQ = 0, kBarInter, kBarScores, kBarP = kBarScores + 2, kBarPV = kBarP + 2, kBarDrain = kBarPV + 2, kBarFull };
+// 128 tokens (a half of a block) of one query head and 128 columns of v.
+struct OutUnit {
+    int first, count;  // of the block; count 0: no more units
+    int index;         // of the block and kv head
+    int half, kvh, head, split;
+    int tiles;         // of 64 keys, up to the half's last token
+    int inter;         // whether there is a state before the block
+    int dirty;         // whether a column of v has a NaN or infinity
+    int exponent;      // of that state
+    float l2;          // log2 of the decay
+};
 
-// A CTA has 128 tokens (a half of a block) of one query head and 128 columns of v.
-// Its 128 rows are the lanes of the accumulator.  Warp 5 brings Q, then in stages of
-// 64 rows the K tiles of 64 keys, the state's rows and the V tiles, in the order in
-// which warp 4 feeds them to the tensor cores: scores of the first key tile; Q S_n;
-// then for each key tile P V and the scores of the tile after the next, in the
-// score buffer that P V has left.  Warps 0-3 own a row a thread, turn its scores into
-// P, in fp16 over the scores, and keep the accumulator in the row's power of two.  Key
-// tiles go from the row's own backwards, where scores only shrink by the decay, so that
-// the first one nearly always sets that power.
+// mbarriers of a CTA
+enum : int {
+    kBarQ = 0,                 // Q has landed
+    kBarQFree,                 // and its MMAs are done
+    kBarInter,                 // the accumulator holds Q S
+    kBarRead,                  // the rows have read the accumulator
+    kBarScores,                // a score buffer holds its scores, 2
+    kBarP = kBarScores + 2,    // P over them, 2
+    kBarPV = kBarP + 2,        // P V is done, 2
+    kBarUnit = kBarPV + 2,     // a unit's slot is written, 2
+    kBarUnitFree = kBarUnit + 2,  // and read by the MMAs' warp and the rows', 2
+    kBarDrain = kBarUnitFree + 2,
+    kBarFull = 16
+};
+
+// A row's 32 outputs go out as whole 64-byte pieces of rows: four
+// lanes exchange their rows' four pieces, so that a store of the warp touches 8 rows and
+// not 32.
+__device__ __forceinline__ void store_rows(__half* out, size_t row_stride, int rows_left, const uint32_t (&y)[16]) {
+    const int lane = threadIdx.x & 31;
+    uint4 piece[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) piece[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    auto exchange = [&](uint4& a, uint4& b, int bit) {  // b of the lower lane with a of the upper
+        const bool upper = lane & bit;
+        const uint4 send = upper ? a : b;
+        uint4 got;
+        got.x = __shfl_xor_sync(kFull, send.x, bit);
+        got.y = __shfl_xor_sync(kFull, send.y, bit);
+        got.z = __shfl_xor_sync(kFull, send.z, bit);
+        got.w = __shfl_xor_sync(kFull, send.w, bit);
+        if (upper)
+            a = got;
+        else
+            b = got;
+    };
+    exchange(piece[0], piece[1], 1);
+    exchange(piece[2], piece[3], 1);
+    exchange(piece[0], piece[2], 2);
+    exchange(piece[1], piece[3], 2);
+    __half* at = out + (size_t)(lane & ~3) * row_stride + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((lane & ~3) + i < rows_left) *reinterpret_cast<uint4*>(at + i * row_stride) = piece[i];
+}
+
+// A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
+// (two and four key tiles) neighbours in that order.  A unit's 128 rows are the
+// lanes of the accumulator.  Warp 5 finds the units and brings Q, then in stages of 64 rows the
+// K tiles of 64 keys, the state's rows and the V tiles, in the order in which warp 4
+// feeds them to the tensor cores: scores of the first key tile; Q S_n; then for each
+// key tile P V and the scores of the tile after the next, in the score buffer that P V has
+// left.  Both run ahead into the next unit while warps 0-3, a row a thread, turn
+// scores into P, in fp16 over the scores, keep the accumulator in the row's power of
+// two, and write the outputs.  Key tiles go from the row's own backwards, where scores only
+// shrink by the decay, so that the first one nearly always sets that power.
 template <int D>
 __global__ void __launch_bounds__(kOutThreads, 2)
     linear_out_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {
@@ -394,39 +520,28 @@ __global__ void __launch_bounds__(kOutThreads, 2)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* qs = smem;
     uint8_t* ring = qs + S::kQBytes;
-    float* falling = reinterpret_cast<float*>(ring + S::kSlots * S::kStageBytes);  // d^(63 - j)
-    int* first_bad = reinterpret_cast<int*>(falling + 64);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(first_bad + S::kCols);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kSlots * S::kStageBytes);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + S::kBars);
     volatile int* failed = reinterpret_cast<volatile int*>(tslot + 1);
+    OutUnit* units = reinterpret_cast<OutUnit*>(tslot + 4);
+    static_assert(sizeof(OutUnit) <= 64, "unit slots");
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int G = p.group, H = p.num_heads, K = p.num_kv_heads;
-    unsigned x = blockIdx.x;
-    const int split = x % S::kSplits;
-    x /= S::kSplits;
-    const int head = x % G;
-    x /= G;
-    const int r = x % 2;  // which half of the block
-    x /= 2;
-    const int kvh = x % K, number = x / K;
-    Block k;
-    if (!block_of(p, number, k) || r * 128 >= k.count) return;
-    if (smem_addr(smem) & 1023u) {  // (the layouts need it; no launch has been seen to break it)
+    if (smem_addr(smem) & 1023u) {  // (the layouts need it; dynamic shared memory starts there)
         if (t == 0) atomicOr(p.status, PA_DEV_TIMEOUT);
         return;
     }
-    const size_t index = (size_t)number * K + kvh;
-    const bool inter = k.n > 0 || k.context > 0;
-    const int tiles = (min(k.count, r * 128 + 128) - 1) / 64 + 1;  // key tiles
-    const float l2 = fmaxf(__ldg(p.log_decay + kvh) * kLog2e, -1e6f);
     const uint32_t bar0 = smem_addr(bars);
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     constexpr int kBarEmpty = kBarFull + S::kSlots;
     if (t == 0) {
         *failed = 0;
-        for (int i = 0; i < S::kBars; ++i) mbar_init(bar(i), i == kBarP || i == kBarP + 1 ? kOutRowWarps : 1);
+        for (int i = 0; i < S::kBars; ++i)
+            mbar_init(bar(i), i == kBarP || i == kBarP + 1 || i == kBarRead       ? kOutRowWarps
+                              : i == kBarUnitFree || i == kBarUnitFree + 1 ? kOutRowWarps + 1
+                                                                           : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -434,55 +549,104 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    int bad = 0;
-    if (t < S::kCols) {
-        first_bad[t] = __ldg(c.first_bad + index * D + split * S::kCols + t);
-        bad = first_bad[t] < kLinearBlock;
-    }
-    if (t < 64) falling[t] = exp2f(l2 * (float)(63 - t));
     tc_fence_before();
-    const bool dirty = __syncthreads_or(bad);  // a column of v with a NaN or infinity
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot, t_out = tmem, t_s = tmem + S::kCols;
     const unsigned limit = c.wait_limit;
     constexpr int kKStages = D / S::kCols;  // stages of a key tile
-    const int inter_stages = inter ? D / 64 : 0;
-    // stage of V tile j: behind the first two K tiles, the state and the V and K tiles before it
-    auto v_stage = [&](int j) { return kKStages * min(tiles, 2) + inter_stages + j + kKStages * min(j, max(tiles - 2, 0)); };
+    auto fail = [&] {
+        *failed = 1;
+        atomicOr(p.status, PA_DEV_TIMEOUT);
+    };
+    // ring stage of V tile j, counted from the unit's first: behind the first two K tiles, the
+    // state and the V and K tiles before it
+    auto v_stage = [&](const OutUnit& u, int j) {
+        return kKStages * min(u.tiles, 2) + (u.inter ? D / 64 : 0) + j + kKStages * min(j, max(u.tiles - 2, 0));
+    };
 
     if (warp == kOutRowWarps + 1) {
+        int n = 0;  // stages
+        bool ok = true;
+        const unsigned total = (unsigned)c.blocks * K * G * S::kSplits * 2;
+        int done = 0, q_tiles = 0;  // units; Q tiles
+        Block k;
+        int number_of_k = -1;
+        bool valid = false;
+        for (unsigned x = blockIdx.x;; x += gridDim.x) {
+            OutUnit u;
+            u.count = 0;
+            if (x < total) {
+                unsigned y = x;
+                u.half = y % 2;
+                y /= 2;
+                u.split = y % S::kSplits;
+                y /= S::kSplits;
+                const int h = y % G;
+                y /= G;
+                u.kvh = y % K;
+                u.head = u.kvh * G + h;
+                const int number = y / K;
+                if (number != number_of_k) {
+                    valid = block_of(p, number, k);
+                    number_of_k = number;
+                }
+                if (!valid || u.half * 128 >= k.count) continue;
+                u.first = k.first;
+                u.count = k.count;
+                u.index = number * K + u.kvh;
+                u.tiles = (min(k.count, u.half * 128 + 128) - 1) / 64 + 1;
+                u.inter = k.n > 0 || k.context > 0;
+                u.dirty = __ldg(c.any_bad + (size_t)u.index * S::kSplits + u.split);
+                u.exponent = u.inter ? __ldg(c.exponents + u.index) : 0;
+                u.l2 = fmaxf(__ldg(p.log_decay + u.kvh) * kLog2e, -1e6f);
+            }
+            if (lane == 0) {
+                const int s = done & 1;
+                if (done >= 2) ok = ok && tc_wait(bar(kBarUnitFree + s), ((done - 2) >> 1) & 1, limit, failed);
+                if (ok) {
+                    units[s] = u;
+                    mbar_arrive(bar(kBarUnit + s));
+                }
+                if (ok && u.count > 0) {
+                    auto stage = [&](const CUtensorMap* map, int y, int z, int ch) {
+                        if (!ok) return;
+                        if (n >= S::kSlots &&
+                            !(ok = tc_wait(bar(kBarEmpty + n % S::kSlots), (n / S::kSlots - 1) & 1, limit, failed)))
+                            return;
+                        const uint32_t full = bar(kBarFull + n % S::kSlots);
+                        mbar_arrive_expect_tx(full, S::kStageBytes);
+                        tc_tma_load_4d(smem_addr(ring + (n % S::kSlots) * S::kStageBytes), map, 0, y, z, ch, full);
+                        ++n;
+                    };
+                    auto key = [&](int j) { return u.first + (u.tiles - 1 - j) * 64; };
+                    auto k_tile = [&](int j) {
+                        for (int ch = 0; ch < kKStages; ++ch) stage(&maps.k, u.kvh, key(j), ch * (S::kCols / 64));
+                    };
+                    if (done >= 1) ok = tc_wait(bar(kBarQFree), (done - 1) & 1, limit, failed);
+                    if (ok) {
+                        mbar_arrive_expect_tx(bar(kBarQ), S::kQBytes);
+                        tc_tma_load_4d(smem_addr(qs), &maps.q, 0, u.head, u.first + u.half * 128, 0, bar(kBarQ));
+                        ++q_tiles;
+                    }
+                    k_tile(0);
+                    if (u.inter)
+                        for (int d = 0; d < D / 64; ++d) stage(&maps.starts, 0, u.index * D + d * 64, u.split * (S::kCols / 64));
+                    if (u.tiles > 1) k_tile(1);
+                    for (int j = 0; j < u.tiles; ++j) {
+                        stage(&maps.v, u.kvh, key(j), u.split * (S::kCols / 64));
+                        if (j + 2 < u.tiles) k_tile(j + 2);
+                    }
+                }
+                if (!ok) fail();
+            }
+            ok = __shfl_sync(kFull, ok, 0);
+            if (!ok || u.count == 0) break;
+            ++done;
+        }
         if (lane == 0) {
-            int n = 0;
-            bool ok = true;
-            auto stage = [&](const CUtensorMap* map, int y, int z, int ch) {
-                if (!ok) return;
-                if (n >= S::kSlots && !(ok = tc_wait(bar(kBarEmpty + n % S::kSlots), (n / S::kSlots - 1) & 1, limit, failed)))
-                    return;
-                const uint32_t full = bar(kBarFull + n % S::kSlots);
-                mbar_arrive_expect_tx(full, S::kStageBytes);
-                tc_tma_load_4d(smem_addr(ring + (n % S::kSlots) * S::kStageBytes), map, 0, y, z, ch, full);
-                ++n;
-            };
-            auto key = [&](int j) { return k.first + (tiles - 1 - j) * 64; };
-            auto k_tile = [&](int j) {
-                for (int ch = 0; ch < kKStages; ++ch) stage(&maps.k, kvh, key(j), ch * (S::kCols / 64));
-            };
-            mbar_arrive_expect_tx(bar(kBarQ), S::kQBytes);
-            tc_tma_load_4d(smem_addr(qs), &maps.q, 0, kvh * G + head, k.first + r * 128, 0, bar(kBarQ));
-            k_tile(0);
-            for (int d = 0; d < inter_stages; ++d)
-                stage(&maps.starts, 0, (int)(index * D) + d * 64, split * (S::kCols / 64));
-            if (tiles > 1) k_tile(1);
-            for (int j = 0; j < tiles; ++j) {
-                stage(&maps.v, kvh, key(j), split * (S::kCols / 64));
-                if (j + 2 < tiles) k_tile(j + 2);
-            }
-            if (!ok) {
-                *failed = 1;
-                atomicOr(p.status, PA_DEV_TIMEOUT);
-            }
             // every copy lands before the CTA's memory is given back
-            mbar_wait(bar(kBarQ), 0, kDefaultWaitLimit);
+            if (q_tiles > 0) mbar_wait(bar(kBarQ), (q_tiles - 1) & 1, kDefaultWaitLimit);
             for (int i = max(0, n - S::kSlots); i < n; ++i)
                 mbar_wait(bar(kBarFull + i % S::kSlots), (i / S::kSlots) & 1, kDefaultWaitLimit);
         }
@@ -492,190 +656,226 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             constexpr uint32_t id_s = tc_idesc(128, 64, 0), id_o = tc_idesc(128, S::kCols, 1);
             const uint64_t qdesc = tc_desc(smem_addr(qs), 16, 1024);
             const uint64_t kdesc = tc_desc(smem_addr(ring), 16, 1024), vdesc = tc_desc(smem_addr(ring), 64 * 128, 1024);
-            int n = 0;
-            bool ok = tc_wait(bar(kBarQ), 0, limit, failed);
-            auto landed = [&] { return ok = ok && tc_wait(bar(kBarFull + n % S::kSlots), (n / S::kSlots) & 1, limit, failed); };
-            auto scores = [&](int j) {
+            int n = 0, g = 0, inters = 0;  // stages, key tiles of earlier units
+            bool ok = true;
+            auto wait = [&](int b, int parity) { return ok = ok && tc_wait(bar(b), parity & 1, limit, failed); };
+            auto landed = [&] { return wait(kBarFull + n % S::kSlots, n / S::kSlots); };
+            auto stage_at = [&] { return (uint64_t)((n % S::kSlots) * (S::kStageBytes >> 4)); };
+            auto scores = [&](int x) {
+                // over the P that P V has read
+                if (x >= 2 && !wait(kBarPV + (x & 1), (x - 2) >> 1)) return;
                 for (int ch = 0; ch < kKStages; ++ch) {
                     if (!landed()) return;
                     tc_fence_after();
-                    const uint64_t at = (uint64_t)((n % S::kSlots) * (S::kStageBytes >> 4));
 #pragma unroll
                     for (int i = 0; i < S::kCols / 16; ++i)
-                        tc_mma_ss(t_s + (j & 1) * 64,
+                        tc_mma_ss(t_s + (x & 1) * 64,
                                   qdesc + (uint64_t)(((ch * (S::kCols / 64) + (i >> 2)) * (128 * 128) + (i & 3) * 32) >> 4),
-                                  kdesc + at + (uint64_t)(((i >> 2) * (64 * 128) + (i & 3) * 32) >> 4), id_s, ch > 0 || i > 0);
+                                  kdesc + stage_at() + (uint64_t)(((i >> 2) * (64 * 128) + (i & 3) * 32) >> 4), id_s,
+                                  ch > 0 || i > 0);
                     tc_commit(bar(kBarEmpty + n % S::kSlots));
                     ++n;
                 }
-                tc_commit(bar(kBarScores + (j & 1)));
+                tc_commit(bar(kBarScores + (x & 1)));
             };
-            scores(0);
-            for (int d = 0; d < inter_stages && landed(); ++d) {
-                tc_fence_after();
-                const uint64_t at = (uint64_t)((n % S::kSlots) * (S::kStageBytes >> 4));
+            for (int done = 0;; ++done) {
+                const int s = done & 1;
+                if (!wait(kBarUnit + s, done >> 1)) break;
+                const int count = units[s].count, tiles = units[s].tiles;
+                const bool inter = units[s].inter;
+                mbar_arrive(bar(kBarUnitFree + s));
+                if (count == 0) break;
+                if (!wait(kBarQ, done)) break;
+                scores(g);
+                if (inter) {
+                    // the accumulator's last outputs have been read
+                    if (done >= 1 && !wait(kBarRead, done - 1)) break;
+                    for (int d = 0; d < D / 64 && landed(); ++d) {
+                        tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc_mma_ss(t_out, qdesc + (uint64_t)((d * (128 * 128) + i * 32) >> 4), vdesc + at + (uint64_t)((i * 2048) >> 4),
-                              id_o, d > 0 || i > 0);
-                tc_commit(bar(kBarEmpty + n % S::kSlots));
-                ++n;
-            }
-            if (inter) tc_commit(bar(kBarInter));
-            if (tiles > 1) scores(1);
-            for (int j = 0; j < tiles && ok; ++j) {
-                ok = tc_wait(bar(kBarP + (j & 1)), (j >> 1) & 1, limit, failed);
-                if (!landed()) break;
-                tc_fence_after();
-                const uint64_t at = (uint64_t)((n % S::kSlots) * (S::kStageBytes >> 4));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc_mma_ts(t_out, t_s + (j & 1) * 64 + i * 8, vdesc + at + (uint64_t)((i * 2048) >> 4), id_o,
-                              inter || j > 0 || i > 0);
-                tc_commit(bar(kBarEmpty + n % S::kSlots));
-                tc_commit(bar(kBarPV + (j & 1)));
-                ++n;
-                if (j + 2 < tiles) {  // over the P that this P V reads
-                    ok = tc_wait(bar(kBarPV + (j & 1)), (j >> 1) & 1, limit, failed);
-                    if (ok) scores(j + 2);
+                        for (int i = 0; i < 4; ++i)
+                            tc_mma_ss(t_out, qdesc + (uint64_t)((d * (128 * 128) + i * 32) >> 4),
+                                      vdesc + stage_at() + (uint64_t)((i * 2048) >> 4), id_o, d > 0 || i > 0);
+                        tc_commit(bar(kBarEmpty + n % S::kSlots));
+                        ++n;
+                    }
+                    if (!ok) break;
+                    tc_commit(bar(kBarInter));
+                    ++inters;
                 }
+                if (tiles > 1) scores(g + 1);
+                if (tiles <= 2) tc_commit(bar(kBarQFree));
+                for (int j = 0; j < tiles; ++j) {
+                    const int x = g + j;
+                    // (rows that have written P have read the last outputs too)
+                    if (!wait(kBarP + (x & 1), x >> 1) || !landed()) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc_mma_ts(t_out, t_s + (x & 1) * 64 + i * 8, vdesc + stage_at() + (uint64_t)((i * 2048) >> 4), id_o,
+                                  inter || j > 0 || i > 0);
+                    tc_commit(bar(kBarEmpty + n % S::kSlots));
+                    tc_commit(bar(kBarPV + (x & 1)));
+                    ++n;
+                    if (j + 2 < tiles) {
+                        scores(x + 2);
+                        if (j + 3 == tiles) tc_commit(bar(kBarQFree));
+                    }
+                }
+                if (!ok) break;
+                g += tiles;
             }
-            if (!ok) {
-                *failed = 1;
-                atomicOr(p.status, PA_DEV_TIMEOUT);
-            }
+            if (!ok) fail();
             tc_commit(bar(kBarDrain));
             mbar_wait(bar(kBarDrain), 0, kDefaultWaitLimit);
         }
         __syncwarp();
     } else {
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const int i = r * 128 + t;  // the row's token in the block
-        const float state_log2 = inter ? (float)__ldg(c.exponents + index) + l2 * (float)(i + 1) : 0.f;
-        // The accumulator holds the outputs times 2^-e.  Where the state's part is far larger than the
-        // scores, e stays so near that this part does not overflow.
-        const int e_least = inter ? (int)fmaxf(-100.f, state_log2 - 60.f) : -100;
-        int e = max(0, e_least);
-        bool set = false, ok = true;
-        auto rescale = [&](float f) {
+        bool ok = true;
+        int g = 0, inters = 0;  // key tiles, and units with a state, of earlier units
+        int stages = 0;         // ring stages of earlier units
+        for (int done = 0;; ++done) {
+            const int s = done & 1;
+            if (!(ok = tc_warp_wait(bar(kBarUnit + s), (done >> 1) & 1, limit, failed))) break;
+            const OutUnit u = units[s];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarUnitFree + s));
+            if (u.count == 0) break;
+            const int i = u.half * 128 + t;  // the row's token in the block
+            const float state_log2 = (float)u.exponent + u.l2 * (float)(i + 1);
+            // The accumulator holds the outputs times 2^-e.  Where the state's part is far larger than
+            // the scores, e stays so near that this part does not overflow.
+            const int e_least = u.inter ? (int)fmaxf(-100.f, state_log2 - 60.f) : -100;
+            int e = max(0, e_least);
+            bool set = false;
+            auto rescale = [&](float f) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < S::kCols; c0 += 32) {
+                    uint32_t o[32];
+                    tc_ld32(t_out + lanes + c0, o);
+#pragma unroll
+                    for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * f);
+                    tc_st32(t_out + lanes + c0, o);
+                }
+            };
+            float within[8];  // decays inside a group of 8 keys
+#pragma unroll
+            for (int v = 0; v < 8; ++v) within[v] = tc_ex2(u.l2 * (float)(7 - v));
+            for (int j = 0; j < u.tiles; ++j) {
+                const int x = g + j;
+                const int k0 = (u.tiles - 1 - j) * 64;  // first key of the tile
+                const uint32_t buf = t_s + (x & 1) * 64 + lanes;
+                if (!(ok = tc_warp_wait(bar(kBarScores + (x & 1)), (x >> 1) & 1, limit, failed))) break;
+                tc_fence_after();
+                uint32_t s0[32], s1[32];
+                tc_ld32x2(buf, s0, buf + 32, s1);
+                float m = 0.f;
+                if (k0 + 63 <= u.half * 128 + warp * 32) {  // every key of the tile is seen by every row of the warp
+                    // d^(i - key), for groups of 8 keys the decay to the last of them and the one within
+#pragma unroll
+                    for (int v = 0; v < 32; v += 8) {
+                        const float to0 = tc_ex2(u.l2 * (float)(i - k0 - v - 7)), to1 = tc_ex2(u.l2 * (float)(i - k0 - v - 39));
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            s0[v + y] = __float_as_uint(__uint_as_float(s0[v + y]) * (to0 * within[y]));
+                            s1[v + y] = __float_as_uint(__uint_as_float(s1[v + y]) * (to1 * within[y]));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 32; ++v) {
+                        const int d0 = i - k0 - v, d1 = d0 - 32;
+                        s0[v] = d0 >= 0 ? __float_as_uint(__uint_as_float(s0[v]) * tc_ex2(u.l2 * (float)d0)) : 0u;
+                        s1[v] = d1 >= 0 ? __float_as_uint(__uint_as_float(s1[v]) * tc_ex2(u.l2 * (float)d1)) : 0u;
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 32; ++v)
+                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(s0[v])), fabsf(__uint_as_float(s1[v]))));
+                // e moves where the row has its first scores that are not 0, and where later ones
+                // would leave fp16 (the first put their largest at 2^10)
+                const int e_new = max(exponent_of(m) - 10, e_least);
+                const bool move = m > 0.f && (!set || e_new > e + 4);
+                const int e_old = e;
+                if (move) {
+                    e = e_new;
+                    set = true;
+                }
+                const float down = pow2(-e);
+                uint32_t pk[32];
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    pk[v] = half2_bits(__floats2half2_rn(__uint_as_float(s0[2 * v]) * down, __uint_as_float(s0[2 * v + 1]) * down));
+                    pk[16 + v] = half2_bits(__floats2half2_rn(__uint_as_float(s1[2 * v]) * down, __uint_as_float(s1[2 * v + 1]) * down));
+                }
+                tc_st32(buf, pk);
+                if (j == 0) {
+                    if (u.inter) {
+                        if (!(ok = tc_warp_wait(bar(kBarInter), inters & 1, limit, failed))) break;
+                        tc_fence_after();
+                        rescale(exp2f(state_log2 - (float)e));
+                    }
+                } else if (__any_sync(kFull, move && e != e_old)) {
+                    if (!(ok = tc_warp_wait(bar(kBarPV + ((x - 1) & 1)), ((x - 1) >> 1) & 1, limit, failed))) break;
+                    tc_fence_after();
+                    rescale(exp2f((float)(e_old - e)));
+                }
+                if (u.dirty || k0 + 64 > u.count) {
+                    // V rows behind the block's last token belong to other sequences, and a NaN or
+                    // infinity must not meet the zeros of tokens before it: both become 0 (the latter's column
+                    // is set from its token on in the end)
+                    const int n = stages + v_stage(u, j);
+                    if (!(ok = tc_warp_wait(bar(kBarFull + n % S::kSlots), (n / S::kSlots) & 1, limit, failed))) break;
+                    uint8_t* vt = ring + (n % S::kSlots) * S::kStageBytes;
+                    for (int v = t; v < S::kStageBytes / 16; v += 128) {
+                        const int row = (v >> 3) & 63;
+                        uint4* at = reinterpret_cast<uint4*>(vt + (size_t)v * 16);
+                        uint4 y = *at;
+                        auto clean = [](uint32_t h) {
+                            if ((h & 0x7c00u) == 0x7c00u) h &= 0xffff0000u;
+                            if ((h & 0x7c000000u) == 0x7c000000u) h &= 0xffffu;
+                            return h;
+                        };
+                        y = k0 + row < u.count ? make_uint4(clean(y.x), clean(y.y), clean(y.z), clean(y.w)) : make_uint4(0u, 0u, 0u, 0u);
+                        *at = y;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarP + (x & 1)));
+            }
+            if (!ok) break;
+            const int last = g + u.tiles - 1;
+            if (!(ok = tc_warp_wait(bar(kBarPV + (last & 1)), (last >> 1) & 1, limit, failed))) break;
+            tc_fence_after();
+            const float f = p.scale * pow2(e);
+            const int row0 = u.half * 128 + warp * 32;  // of the warp
+            __half* out = p.out + ((size_t)(u.first + row0) * H + u.head) * D + u.split * S::kCols;
 #pragma unroll 1
             for (int c0 = 0; c0 < S::kCols; c0 += 32) {
-                uint32_t o[32];
+                uint32_t o[32], y[16];
                 tc_ld32(t_out + lanes + c0, o);
+                if (u.dirty) {
+                    const int* bad = c.first_bad + (size_t)u.index * D + u.split * S::kCols + c0;
 #pragma unroll
-                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-                tc_st32(t_out + lanes + c0, o);
-            }
-        };
-        for (int j = 0; j < tiles; ++j) {
-            const int k0 = (tiles - 1 - j) * 64;  // first key of the tile
-            const uint32_t buf = t_s + (j & 1) * 64 + lanes;
-            if (!(ok = tc_warp_wait(bar(kBarScores + (j & 1)), (j >> 1) & 1, limit, failed))) break;
-            tc_fence_after();
-            uint32_t s0[32], s1[32];
-            tc_ld32x2(buf, s0, buf + 32, s1);
-            float m = 0.f;
-            if (k0 + 63 <= r * 128 + warp * 32) {  // every key of the tile is seen by every row of the warp
-                const float base = tc_ex2(l2 * (float)(i - k0 - 63));
-#pragma unroll
-                for (int u = 0; u < 32; ++u) {
-                    s0[u] = __float_as_uint(__uint_as_float(s0[u]) * (base * falling[u]));
-                    s1[u] = __float_as_uint(__uint_as_float(s1[u]) * (base * falling[32 + u]));
+                    for (int v = 0; v < 32; ++v)
+                        if (i >= __ldg(bad + v)) o[v] = 0x7fffffffu;
                 }
-            } else {
 #pragma unroll
-                for (int u = 0; u < 32; ++u) {
-                    const int d0 = i - k0 - u, d1 = d0 - 32;
-                    s0[u] = d0 >= 0 ? __float_as_uint(__uint_as_float(s0[u]) * tc_ex2(l2 * (float)d0)) : 0u;
-                    s1[u] = d1 >= 0 ? __float_as_uint(__uint_as_float(s1[u]) * tc_ex2(l2 * (float)d1)) : 0u;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 32; ++u)
-                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(s0[u])), fabsf(__uint_as_float(s1[u]))));
-            // e moves where the row has its first scores that are not 0, and where later ones
-            // would leave fp16 (the first put their largest at 2^10)
-            const int e_new = max(exponent_of(m) - 10, e_least);
-            const bool move = m > 0.f && (!set || e_new > e + 4);
-            const int e_old = e;
-            if (move) {
-                e = e_new;
-                set = true;
-            }
-            if (j == 0) {
-                if (inter) {
-                    if (!(ok = tc_warp_wait(bar(kBarInter), 0, limit, failed))) break;
-                    tc_fence_after();
-                    rescale(exp2f(state_log2 - (float)e));
-                }
-            } else if (__any_sync(kFull, move && e != e_old)) {
-                if (!(ok = tc_warp_wait(bar(kBarPV + ((j - 1) & 1)), ((j - 1) >> 1) & 1, limit, failed))) break;
-                tc_fence_after();
-                rescale(exp2f((float)(e_old - e)));
-            }
-            const float down = pow2(-e);
-            uint32_t pk[32];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                pk[u] = half2_bits(__floats2half2_rn(__uint_as_float(s0[2 * u]) * down, __uint_as_float(s0[2 * u + 1]) * down));
-                pk[16 + u] = half2_bits(__floats2half2_rn(__uint_as_float(s1[2 * u]) * down, __uint_as_float(s1[2 * u + 1]) * down));
-            }
-            tc_st32(buf, pk);
-            if (dirty || k0 + 64 > k.count) {
-                // V rows behind the block's last token belong to other sequences, and a NaN or infinity
-                // must not meet the zeros of tokens before it: both become 0 (the latter's column is
-                // set from its token on in the end)
-                const int n = v_stage(j);
-                if (!(ok = tc_warp_wait(bar(kBarFull + n % S::kSlots), (n / S::kSlots) & 1, limit, failed))) break;
-                uint8_t* vt = ring + (n % S::kSlots) * S::kStageBytes;
-                for (int u = t; u < S::kStageBytes / 16; u += 128) {
-                    const int row = (u >> 3) & 63;
-                    uint4* at = reinterpret_cast<uint4*>(vt + (size_t)u * 16);
-                    uint4 y = *at;
-                    auto clean = [](uint32_t h) {
-                        if ((h & 0x7c00u) == 0x7c00u) h &= 0xffff0000u;
-                        if ((h & 0x7c000000u) == 0x7c000000u) h &= 0xffffu;
-                        return h;
-                    };
-                    y = k0 + row < k.count ? make_uint4(clean(y.x), clean(y.y), clean(y.z), clean(y.w)) : make_uint4(0u, 0u, 0u, 0u);
-                    *at = y;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                for (int v = 0; v < 16; ++v)
+                    y[v] = half2_bits(__floats2half2_rn(__uint_as_float(o[2 * v]) * f, __uint_as_float(o[2 * v + 1]) * f));
+                store_rows(out + c0, (size_t)H * D, u.count - row0, y);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarP + (j & 1)));
+            if (lane == 0) mbar_arrive(bar(kBarRead));
+            g += u.tiles;
+            inters += u.inter;
+            stages += v_stage(u, u.tiles - 1) + 1;
         }
-        if (ok) ok = tc_warp_wait(bar(kBarPV + ((tiles - 1) & 1)), ((tiles - 1) >> 1) & 1, limit, failed);
-        if (ok) {
-            tc_fence_after();
-            const float f = p.scale * pow2(e);
-            __half* out = p.out + ((size_t)(k.first + i) * H + kvh * G + head) * D + split * S::kCols;
-#pragma unroll 1
-            for (int c0 = 0; c0 < S::kCols; c0 += 32) {
-                uint32_t o[32];
-                tc_ld32(t_out + lanes + c0, o);
-                if (i < k.count) {
-                    if (dirty) {
-#pragma unroll
-                        for (int u = 0; u < 32; ++u)
-                            if (i >= first_bad[c0 + u]) o[u] = 0x7fffffffu;
-                    }
-#pragma unroll
-                    for (int u = 0; u < 32; u += 8) {
-                        uint4 y;
-                        uint32_t* yp = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            yp[q] = half2_bits(__floats2half2_rn(__uint_as_float(o[u + 2 * q]) * f, __uint_as_float(o[u + 2 * q + 1]) * f));
-                        *reinterpret_cast<uint4*>(out + c0 + u) = y;
-                    }
-                }
-            }
-        } else if (lane == 0) {
-            *failed = 1;
-            atomicOr(p.status, PA_DEV_TIMEOUT);
-        }
+        if (!ok && lane == 0) fail();
     }
     tc_fence_before();
     __syncthreads();  // no copy or MMA is in flight
@@ -703,20 +903,22 @@ cudaError_t adds(const LinearChunkParams& prm, const LinearMaps& maps, cudaStrea
         return cudaFuncSetAttribute(linear_adds_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    return launch(linear_adds_kernel<D>, dim3(prm.blocks + prm.lin.num_seqs, prm.lin.num_kv_heads, S::kTiles * S::kTiles), 128,
-                  S::kSmem, stream, maps.k_block, prm);
+    return launch(linear_adds_kernel<D>, dim3(prm.blocks + prm.lin.num_seqs, prm.lin.num_kv_heads, S::kTiles * S::kTiles),
+                  kAddThreads, S::kSmem, stream, maps, prm);
 }
 
 template <int D>
-cudaError_t out(const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream) {
+cudaError_t out(const LinearChunkParams& prm, const LinearMaps& maps, int num_sms, cudaStream_t stream) {
     using S = OutShape<D>;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(linear_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    return launch(linear_out_kernel<D>, dim3((unsigned)prm.blocks * 2 * prm.lin.num_heads * S::kSplits), kOutThreads, S::kSmem,
-                  stream, maps, prm);
+    // An odd number of CTAs, so that each takes first and second halves of blocks in turn.
+    const long long units = (long long)prm.blocks * 2 * prm.lin.num_heads * S::kSplits;
+    const long long room = 2ll * num_sms - 1;
+    return launch(linear_out_kernel<D>, dim3((unsigned)(units < room ? units : room)), kOutThreads, S::kSmem, stream, maps, prm);
 }
 
 }  // namespace
@@ -740,11 +942,12 @@ cudaError_t launch_linear_scan(int head_dim, const LinearChunkParams& prm, cudaS
     }
 }
 
-cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream) {
+cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, int num_sms,
+                              cudaStream_t stream) {
     switch (head_dim) {
-        case 64: return out<64>(prm, maps, stream);
-        case 128: return out<128>(prm, maps, stream);
-        case 256: return out<256>(prm, maps, stream);
+        case 64: return out<64>(prm, maps, num_sms, stream);
+        case 128: return out<128>(prm, maps, num_sms, stream);
+        case 256: return out<256>(prm, maps, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

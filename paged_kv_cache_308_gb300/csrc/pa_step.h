@@ -77,17 +77,18 @@ struct LinearChunkParams {
     float* add_max;        // [blocks][Hkv][tiles]: largest finite magnitude in adds
     float* state_max;      // [B][Hkv]: of the state before the first block
     int* first_bad;        // [blocks][Hkv][D]: first token of a block with a NaN or infinity in that column of v
+    int* any_bad;          // [blocks][Hkv][D / tile]: whether a tile's columns have one
     int blocks;            // numbers of blocks, those of no block among them
     int wait_limit;
 };
-// k and v: [token][kv head][D] in boxes of (rows, columns); q: 128 rows of all columns;
-// starts: 64 rows of a tile's columns.
+// 64 rows of a tile's columns of k, v and starts; 128 rows of q.
 struct LinearMaps {
-    CUtensorMap k_block, q, k, v, starts;
+    CUtensorMap q, k, v, starts;
 };
 cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
 cudaError_t launch_linear_scan(int head_dim, const LinearChunkParams& prm, cudaStream_t stream);
-cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
+cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, int num_sms,
+                              cudaStream_t stream);
 
 // Tensor map of packed rows [tokens][heads][head_dim] of halves: a box is `rows` tokens of one head by `cols`
 // columns, laid out [64-column chunk][rows][128 B] with the 128-byte swizzle; coordinates (0, head, token, chunk).

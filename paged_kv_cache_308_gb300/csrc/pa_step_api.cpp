@@ -130,7 +130,7 @@ constexpr int kLinearFewTokens = 8;
 // The chunked form's workspace: bytes, offsets (the blocks' sums are at 0).
 struct LinearSpace {
     long long blocks;
-    size_t starts, exponents, add_max, state_max, first_bad, bytes;
+    size_t starts, exponents, add_max, state_max, first_bad, any_bad, bytes;
 };
 
 LinearSpace linear_space(int num_seqs, int num_tokens, int num_kv_heads, int head_dim) {
@@ -144,7 +144,8 @@ LinearSpace linear_space(int num_seqs, int num_tokens, int num_kv_heads, int hea
     s.add_max = s.exponents + up(heads * 4);
     s.state_max = s.add_max + up(heads * tiles * tiles * 4);
     s.first_bad = s.state_max + up((size_t)num_seqs * num_kv_heads * 4);
-    s.bytes = s.first_bad + up(heads * head_dim * 4);
+    s.any_bad = s.first_bad + up(heads * head_dim * 4);
+    s.bytes = s.any_bad + up(heads * tiles * 4);
     return s;
 }
 
@@ -290,18 +291,20 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     c.add_max = reinterpret_cast<float*>(w + sp.add_max);
     c.state_max = reinterpret_cast<float*>(w + sp.state_max);
     c.first_bad = reinterpret_cast<int*>(w + sp.first_bad);
+    c.any_bad = reinterpret_cast<int*>(w + sp.any_bad);
     c.blocks = static_cast<int>(sp.blocks);
     c.wait_limit = pa::kDefaultWaitLimit;
     const int tile = std::min(D, pa::kLinearTile);
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK) return PA_ERR_CUDA;
     pa::LinearMaps maps;
-    if ((rc = pa::make_rows_map(&maps.k_block, a->k, a->num_tokens, K, D, pa::kLinearBlock, tile)) ||
-        (rc = pa::make_rows_map(&maps.q, a->q, a->num_tokens, a->num_heads, D, 128, D)) ||
+    if ((rc = pa::make_rows_map(&maps.q, a->q, a->num_tokens, a->num_heads, D, 128, D)) ||
         (rc = pa::make_rows_map(&maps.k, a->k, a->num_tokens, K, D, 64, tile)) ||
         (rc = pa::make_rows_map(&maps.v, a->v, a->num_tokens, K, D, 64, tile)) ||
         (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, 64, tile)))
         return rc;
     if (pa::launch_linear_adds(D, c, maps, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
-        pa::launch_linear_out(D, c, maps, stream) != cudaSuccess)
+        pa::launch_linear_out(D, c, maps, num_sms, stream) != cudaSuccess)
         return PA_ERR_CUDA;
     return PA_OK;
 }
