@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
         fetch(n + kAhead, slot, most_slot);
         const size_t i = index + (size_t)n * p.num_kv_heads;
         if (n > 0 || s.context > 0) {
-            const int e = bound > 0.f ? max(min(exponent_of(bound) - 13, 100), -100) : 0;
+            const int e = bound > 0.f ? max(min(exponent_of(bound) - 8, 100), -100) : 0;
             const float down = pow2(-e);
             uint2 h;
             h.x = half2_bits(__floats2half2_rn(x.x * down, x.y * down));
@@ -437,12 +437,13 @@ struct OutShape {
     static constexpr int kStageBytes = 64 * kCols * 2;   // 64 tokens or state rows by kCols columns
     static constexpr int kSlots = D == 256 ? 3 : D == 128 ? 5 : 8;
     static constexpr int kBars = 16 + 2 * kSlots;
-    static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64;  // barriers, TMEM address and flag, two units
+    // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by halves
+    static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * 2 * 128;
     static constexpr int kSmem = kQBytes + kSlots * kStageBytes + kCtrl;
     static constexpr int kTmem = 256;                    // kCols of the outputs, two buffers of 64 scores
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
-constexpr int kOutRowWarps = 4, kOutThreads = (kOutRowWarps + 2) * 32;
+constexpr int kOutRowWarps = 8, kOutThreads = (kOutRowWarps + 2) * 32;
 
 // 128 tokens (a half of a block) of one query head and 128 columns of v.
 struct OutUnit {
@@ -468,6 +469,7 @@ enum : int {
     kBarUnit = kBarPV + 2,     // a unit's slot is written, 2
     kBarUnitFree = kBarUnit + 2,  // and read by the MMAs' warp and the rows', 2
     kBarDrain = kBarUnitFree + 2,
+    kBarV,                        // a V tile that the rows clean has landed
     kBarFull = 16
 };
 
@@ -504,11 +506,11 @@ __device__ __forceinline__ void store_rows(__half* out, size_t row_stride, int r
 
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
 // (two and four key tiles) neighbours in that order.  A unit's 128 rows are the
-// lanes of the accumulator.  Warp 5 finds the units and brings Q, then in stages of 64 rows the
-// K tiles of 64 keys, the state's rows and the V tiles, in the order in which warp 4
-// feeds them to the tensor cores: scores of the first key tile; Q S_n; then for each
+// lanes of the accumulator.  The last warp finds the units and brings Q, then in stages of 64 rows the
+// K tiles of 64 keys, the state's rows and the V tiles, in the order in which the one
+// before it feeds them to the tensor cores: scores of the first key tile; Q S_n; then for each
 // key tile P V and the scores of the tile after the next, in the score buffer that P V has
-// left.  Both run ahead into the next unit while warps 0-3, a row a thread, turn
+// left.  Both run ahead into the next unit while warps 0-7, two threads a row, turn
 // scores into P, in fp16 over the scores, keep the accumulator in the row's power of
 // two, and write the outputs.  Key tiles go from the row's own backwards, where scores only
 // shrink by the decay, so that the first one nearly always sets that power.
@@ -525,6 +527,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
     volatile int* failed = reinterpret_cast<volatile int*>(tslot + 1);
     OutUnit* units = reinterpret_cast<OutUnit*>(tslot + 4);
     static_assert(sizeof(OutUnit) <= 64, "unit slots");
+    uint8_t* largest = reinterpret_cast<uint8_t*>(tslot + 4 + 2 * 16);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -559,6 +562,8 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         *failed = 1;
         atomicOr(p.status, PA_DEV_TIMEOUT);
     };
+    // whether the rows change V tile j before it is multiplied (see there)
+    auto cleaned = [](bool dirty, int count, int tiles, int j) { return dirty || (tiles - j) * 64 > count; };
     // ring stage of V tile j, counted from the unit's first: behind the first two K tiles, the
     // state and the V and K tiles before it
     auto v_stage = [&](const OutUnit& u, int j) {
@@ -682,7 +687,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                 const int s = done & 1;
                 if (!wait(kBarUnit + s, done >> 1)) break;
                 const int count = units[s].count, tiles = units[s].tiles;
-                const bool inter = units[s].inter;
+                const bool inter = units[s].inter, dirty = units[s].dirty;
                 mbar_arrive(bar(kBarUnitFree + s));
                 if (count == 0) break;
                 if (!wait(kBarQ, done)) break;
@@ -708,7 +713,15 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                 for (int j = 0; j < tiles; ++j) {
                     const int x = g + j;
                     // (rows that have written P have read the last outputs too)
+                    // (the rows cannot tell a ring slot's phases apart: they may be two behind)
+                    if (cleaned(dirty, count, tiles, j)) {
+                        if (!landed()) break;
+                        mbar_arrive(bar(kBarV));
+                    }
                     if (!wait(kBarP + (x & 1), x >> 1) || !landed()) break;
+                    // Q S, whose operand comes from shared memory, is done before P V, whose comes from
+                    // tensor memory, adds to it: nothing orders the two kinds in the tensor cores
+                    if (j == 0 && inter && !wait(kBarInter, inters - 1)) break;
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -731,10 +744,16 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         }
         __syncwarp();
     } else {
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // Warps w and w + 4 have the same 32 rows (tensor memory gives a warp those of its number
+        // modulo 4), each half of the keys of a tile and half of the outputs' columns.
+        const int quarter = warp & 3, side = warp >> 2;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        constexpr int kMine = S::kCols / 2;  // columns of the outputs
+        const uint32_t acc = t_out + lanes + side * kMine;
         bool ok = true;
         int g = 0, inters = 0;  // key tiles, and units with a state, of earlier units
         int stages = 0;         // ring stages of earlier units
+        int cleans = 0;         // V tiles cleaned
         for (int done = 0;; ++done) {
             const int s = done & 1;
             if (!(ok = tc_warp_wait(bar(kBarUnit + s), (done >> 1) & 1, limit, failed))) break;
@@ -742,21 +761,23 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarUnitFree + s));
             if (u.count == 0) break;
-            const int i = u.half * 128 + t;  // the row's token in the block
-            const float state_log2 = (float)u.exponent + u.l2 * (float)(i + 1);
-            // The accumulator holds the outputs times 2^-e.  Where the state's part is far larger than
-            // the scores, e stays so near that this part does not overflow.
-            const int e_least = u.inter ? (int)fmaxf(-100.f, state_log2 - 60.f) : -100;
-            int e = max(0, e_least);
+            const int row0 = u.half * 128 + quarter * 32, i = row0 + lane;  // the warp's first token in the block; the row's
+            // The accumulator holds the outputs times 2^-level.  It starts out with Q S, whose row is so
+            // many times the state's part as `state` says; where that number is moderate the scores
+            // simply go by it, and the accumulator is not touched.
+            const float state = u.inter ? (float)u.exponent + u.l2 * (float)(i + 1) : 0.f;
+            float level = fminf(fmaxf(state, -40.f), 60.f);
+            const float least = u.inter ? state - 60.f : -200.f;  // below which the state's part could overflow
+            float pending = u.inter ? state - level : 0.f;        // by how much the accumulator is behind
             bool set = false;
             auto rescale = [&](float f) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < S::kCols; c0 += 32) {
+                for (int c0 = 0; c0 < kMine; c0 += 32) {
                     uint32_t o[32];
-                    tc_ld32(t_out + lanes + c0, o);
+                    tc_ld32(acc + c0, o);
 #pragma unroll
                     for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * f);
-                    tc_st32(t_out + lanes + c0, o);
+                    tc_st32(acc + c0, o);
                 }
             };
             float within[8];  // decays inside a group of 8 keys
@@ -765,70 +786,80 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             for (int j = 0; j < u.tiles; ++j) {
                 const int x = g + j;
                 const int k0 = (u.tiles - 1 - j) * 64;  // first key of the tile
+                const int kc = k0 + side * 32;          // and of the warp's half
                 const uint32_t buf = t_s + (x & 1) * 64 + lanes;
                 if (!(ok = tc_warp_wait(bar(kBarScores + (x & 1)), (x >> 1) & 1, limit, failed))) break;
                 tc_fence_after();
-                uint32_t s0[32], s1[32];
-                tc_ld32x2(buf, s0, buf + 32, s1);
+                uint32_t sc[32];
                 float m = 0.f;
-                if (k0 + 63 <= u.half * 128 + warp * 32) {  // every key of the tile is seen by every row of the warp
-                    // d^(i - key), for groups of 8 keys the decay to the last of them and the one within
+                if (kc > row0) {  // keys behind all of the rows
 #pragma unroll
-                    for (int v = 0; v < 32; v += 8) {
-                        const float to0 = tc_ex2(u.l2 * (float)(i - k0 - v - 7)), to1 = tc_ex2(u.l2 * (float)(i - k0 - v - 39));
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            s0[v + y] = __float_as_uint(__uint_as_float(s0[v + y]) * (to0 * within[y]));
-                            s1[v + y] = __float_as_uint(__uint_as_float(s1[v + y]) * (to1 * within[y]));
-                        }
-                    }
+                    for (int v = 0; v < 32; ++v) sc[v] = 0u;
                 } else {
+                    tc_ld32(buf + side * 32, sc);
+                    if (kc < row0) {
+                        // d^(i - key) 2^-level: for groups of 8 keys up to the last of them, and the one within
 #pragma unroll
-                    for (int v = 0; v < 32; ++v) {
-                        const int d0 = i - k0 - v, d1 = d0 - 32;
-                        s0[v] = d0 >= 0 ? __float_as_uint(__uint_as_float(s0[v]) * tc_ex2(u.l2 * (float)d0)) : 0u;
-                        s1[v] = d1 >= 0 ? __float_as_uint(__uint_as_float(s1[v]) * tc_ex2(u.l2 * (float)d1)) : 0u;
+                        for (int v = 0; v < 32; v += 8) {
+                            const float to = tc_ex2(fmaf(u.l2, (float)(i - kc - v - 7), -level));
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) sc[v + y] = __float_as_uint(__uint_as_float(sc[v + y]) * (to * within[y]));
+                        }
+                    } else {  // the diagonal
+#pragma unroll
+                        for (int v = 0; v < 32; ++v)
+                            sc[v] = lane >= v ? __float_as_uint(__uint_as_float(sc[v]) * tc_ex2(fmaf(u.l2, (float)(lane - v), -level))) : 0u;
                     }
-                }
 #pragma unroll
-                for (int v = 0; v < 32; ++v)
-                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(s0[v])), fabsf(__uint_as_float(s1[v]))));
-                // e moves where the row has its first scores that are not 0, and where later ones
-                // would leave fp16 (the first put their largest at 2^10)
-                const int e_new = max(exponent_of(m) - 10, e_least);
-                const bool move = m > 0.f && (!set || e_new > e + 4);
-                const int e_old = e;
-                if (move) {
-                    e = e_new;
-                    set = true;
+                    for (int v = 0; v < 32; v += 2)
+                        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(sc[v])), fabsf(__uint_as_float(sc[v + 1]))));
                 }
-                const float down = pow2(-e);
-                uint32_t pk[32];
+                // the exponent of the row's largest, of both halves (what is not a normal number counts as 0)
+                uint8_t* mine = largest + (x & 1) * 256 + quarter * 32 + lane;
+                int e = exponent_of(m);
+                mine[side * 128] = (uint8_t)(e + 127);
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                e = max(e, (int)mine[(side ^ 1) * 128] - 127);
+                // The level moves where the row's first scores that are not 0 are not of a middling size, and
+                // where later ones would leave fp16.
+                const bool move = e > -127 && (e >= 15 || (!set && e < -4));
+                set |= e > -127;
+                if (__any_sync(kFull, move)) {
+                    const float by = move ? fmaxf((float)(e - 8), least - level) : 0.f;
+                    const float f = exp2f(-by);
+                    level += by;
+                    pending -= by;
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    pk[v] = half2_bits(__floats2half2_rn(__uint_as_float(s0[2 * v]) * down, __uint_as_float(s0[2 * v + 1]) * down));
-                    pk[16 + v] = half2_bits(__floats2half2_rn(__uint_as_float(s1[2 * v]) * down, __uint_as_float(s1[2 * v + 1]) * down));
+                    for (int v = 0; v < 32; ++v) sc[v] = __float_as_uint(__uint_as_float(sc[v]) * f);
                 }
-                tc_st32(buf, pk);
-                if (j == 0) {
-                    if (u.inter) {
-                        if (!(ok = tc_warp_wait(bar(kBarInter), inters & 1, limit, failed))) break;
+                uint32_t pk[16];
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    pk[v] = half2_bits(__floats2half2_rn(__uint_as_float(sc[2 * v]), __uint_as_float(sc[2 * v + 1])));
+                tc_st16(buf + side * 16, pk);
+                if (__any_sync(kFull, pending != 0.f)) {
+                    // (the accumulator holds nothing before a first tile without a state)
+                    if (j == 0 && u.inter) {
+                        ok = tc_warp_wait(bar(kBarInter), inters & 1, limit, failed);
+                    } else if (j > 0) {
+                        ok = tc_warp_wait(bar(kBarPV + ((x - 1) & 1)), ((x - 1) >> 1) & 1, limit, failed);
+                    }
+                    if (!ok) break;
+                    if (j > 0 || u.inter) {
                         tc_fence_after();
-                        rescale(exp2f(state_log2 - (float)e));
+                        rescale(exp2f(pending));
                     }
-                } else if (__any_sync(kFull, move && e != e_old)) {
-                    if (!(ok = tc_warp_wait(bar(kBarPV + ((x - 1) & 1)), ((x - 1) >> 1) & 1, limit, failed))) break;
-                    tc_fence_after();
-                    rescale(exp2f((float)(e_old - e)));
+                    pending = 0.f;
                 }
-                if (u.dirty || k0 + 64 > u.count) {
+                if (cleaned(u.dirty, u.count, u.tiles, j)) {
                     // V rows behind the block's last token belong to other sequences, and a NaN or
                     // infinity must not meet the zeros of tokens before it: both become 0 (the latter's column
                     // is set from its token on in the end)
                     const int n = stages + v_stage(u, j);
-                    if (!(ok = tc_warp_wait(bar(kBarFull + n % S::kSlots), (n / S::kSlots) & 1, limit, failed))) break;
+                    if (!(ok = tc_warp_wait(bar(kBarV), cleans & 1, limit, failed))) break;
+                    ++cleans;
                     uint8_t* vt = ring + (n % S::kSlots) * S::kStageBytes;
-                    for (int v = t; v < S::kStageBytes / 16; v += 128) {
+                    for (int v = t; v < S::kStageBytes / 16; v += kOutRowWarps * 32) {
                         const int row = (v >> 3) & 63;
                         uint4* at = reinterpret_cast<uint4*>(vt + (size_t)v * 16);
                         uint4 y = *at;
@@ -850,15 +881,14 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             const int last = g + u.tiles - 1;
             if (!(ok = tc_warp_wait(bar(kBarPV + (last & 1)), (last >> 1) & 1, limit, failed))) break;
             tc_fence_after();
-            const float f = p.scale * pow2(e);
-            const int row0 = u.half * 128 + warp * 32;  // of the warp
-            __half* out = p.out + ((size_t)(u.first + row0) * H + u.head) * D + u.split * S::kCols;
+            const float f = p.scale * exp2f(level);
+            __half* out = p.out + ((size_t)(u.first + row0) * H + u.head) * D + u.split * S::kCols + side * kMine;
 #pragma unroll 1
-            for (int c0 = 0; c0 < S::kCols; c0 += 32) {
+            for (int c0 = 0; c0 < kMine; c0 += 32) {
                 uint32_t o[32], y[16];
-                tc_ld32(t_out + lanes + c0, o);
+                tc_ld32(acc + c0, o);
                 if (u.dirty) {
-                    const int* bad = c.first_bad + (size_t)u.index * D + u.split * S::kCols + c0;
+                    const int* bad = c.first_bad + (size_t)u.index * D + u.split * S::kCols + side * kMine + c0;
 #pragma unroll
                     for (int v = 0; v < 32; ++v)
                         if (i >= __ldg(bad + v)) o[v] = 0x7fffffffu;
