@@ -473,35 +473,31 @@ enum : int {
     kBarFull = 16
 };
 
-// A row's 32 outputs go out as whole 64-byte pieces of rows: four
-// lanes exchange their rows' four pieces, so that a store of the warp touches 8 rows and
-// not 32.
-__device__ __forceinline__ void store_rows(__half* out, size_t row_stride, int rows_left, const uint32_t (&y)[16]) {
-    const int lane = threadIdx.x & 31;
-    uint4 piece[4];
+// Products of two numbers at a time (one instruction), and the larger magnitude of three.
+__device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\t"
+        "mov.b64 {%0, %1}, p;\n\t}"
+        : "+r"(a), "+r"(b)
+        : "f"(x), "f"(y));
+}
+__device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return m;
+}
+
+// 32 outputs of a row: 32 bytes (a whole sector) a store where they are aligned so.
+__device__ __forceinline__ void store32(__half* to, const uint32_t (&y)[16], bool wide) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) piece[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    auto exchange = [&](uint4& a, uint4& b, int bit) {  // b of the lower lane with a of the upper
-        const bool upper = lane & bit;
-        const uint4 send = upper ? a : b;
-        uint4 got;
-        got.x = __shfl_xor_sync(kFull, send.x, bit);
-        got.y = __shfl_xor_sync(kFull, send.y, bit);
-        got.z = __shfl_xor_sync(kFull, send.z, bit);
-        got.w = __shfl_xor_sync(kFull, send.w, bit);
-        if (upper)
-            a = got;
-        else
-            b = got;
-    };
-    exchange(piece[0], piece[1], 1);
-    exchange(piece[2], piece[3], 1);
-    exchange(piece[0], piece[2], 2);
-    exchange(piece[1], piece[3], 2);
-    __half* at = out + (size_t)(lane & ~3) * row_stride + (lane & 3) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if ((lane & ~3) + i < rows_left) *reinterpret_cast<uint4*>(at + i * row_stride) = piece[i];
+    for (int v = 0; v < 16; v += 8) {
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * v), "r"(y[v]), "r"(y[v + 1]),
+                         "r"(y[v + 2]), "r"(y[v + 3]), "r"(y[v + 4]), "r"(y[v + 5]), "r"(y[v + 6]), "r"(y[v + 7])
+                         : "memory");
+        } else {
+            *reinterpret_cast<uint4*>(to + 2 * v) = make_uint4(y[v], y[v + 1], y[v + 2], y[v + 3]);
+            *reinterpret_cast<uint4*>(to + 2 * v + 8) = make_uint4(y[v + 4], y[v + 5], y[v + 6], y[v + 7]);
+        }
+    }
 }
 
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
@@ -776,7 +772,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     uint32_t o[32];
                     tc_ld32(acc + c0, o);
 #pragma unroll
-                    for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * f);
+                    for (int v = 0; v < 32; v += 2) mul2(o[v], o[v + 1], f, f);
                     tc_st32(acc + c0, o);
                 }
             };
@@ -803,7 +799,11 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                         for (int v = 0; v < 32; v += 8) {
                             const float to = tc_ex2(fmaf(u.l2, (float)(i - kc - v - 7), -level));
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) sc[v + y] = __float_as_uint(__uint_as_float(sc[v + y]) * (to * within[y]));
+                            for (int y = 0; y < 8; y += 2) {
+                                uint32_t d0 = __float_as_uint(within[y]), d1 = __float_as_uint(within[y + 1]);
+                                mul2(d0, d1, to, to);
+                                mul2(sc[v + y], sc[v + y + 1], __uint_as_float(d0), __uint_as_float(d1));
+                            }
                         }
                     } else {  // the diagonal
 #pragma unroll
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     }
 #pragma unroll
                     for (int v = 0; v < 32; v += 2)
-                        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(sc[v])), fabsf(__uint_as_float(sc[v + 1]))));
+                        m = max3(m, sc[v], sc[v + 1]);
                 }
                 // the exponent of the row's largest, of both halves (what is not a normal number counts as 0)
                 uint8_t* mine = largest + (x & 1) * 256 + quarter * 32 + lane;
@@ -882,7 +882,8 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             if (!(ok = tc_warp_wait(bar(kBarPV + (last & 1)), (last >> 1) & 1, limit, failed))) break;
             tc_fence_after();
             const float f = p.scale * exp2f(level);
-            __half* out = p.out + ((size_t)(u.first + row0) * H + u.head) * D + u.split * S::kCols + side * kMine;
+            __half* out = p.out + ((size_t)(u.first + i) * H + u.head) * D + u.split * S::kCols + side * kMine;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
             for (int c0 = 0; c0 < kMine; c0 += 32) {
                 uint32_t o[32], y[16];
@@ -894,9 +895,11 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                         if (i >= __ldg(bad + v)) o[v] = 0x7fffffffu;
                 }
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    y[v] = half2_bits(__floats2half2_rn(__uint_as_float(o[2 * v]) * f, __uint_as_float(o[2 * v + 1]) * f));
-                store_rows(out + c0, (size_t)H * D, u.count - row0, y);
+                for (int v = 0; v < 16; ++v) {
+                    mul2(o[2 * v], o[2 * v + 1], f, f);
+                    y[v] = half2_bits(__floats2half2_rn(__uint_as_float(o[2 * v]), __uint_as_float(o[2 * v + 1])));
+                }
+                if (i < u.count) store32(out + c0, y, wide);
             }
             tc_fence_before();
             __syncwarp();
