@@ -156,7 +156,10 @@ __global__ void __launch_bounds__(kAddThreads, 2)
         return;
     }
     Block k;
-    if (!block_of(p, number, k)) return;
+    const bool real = block_of(p, number, k);
+    if (t == 0 && kvh == 0 && blockIdx.z == 0)
+        c.block_info[number] = real ? make_int4(k.first, k.count, k.n > 0 || k.context > 0, 0) : make_int4(0, 0, 0, 0);
+    if (!real) return;
     const int k_tile = blockIdx.z / S::kTiles, v_tile = blockIdx.z % S::kTiles;
     const int groups = (k.count + S::kGroup - 1) / S::kGroup;
     const uint32_t bar_full = smem_addr(bars), bar_v = bar_full + 8 * S::kSlots, bar_mma = bar_v + 16;
@@ -571,13 +574,12 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         bool ok = true;
         const unsigned total = (unsigned)c.blocks * K * G * S::kSplits * 2;
         int done = 0, q_tiles = 0;  // units; Q tiles
-        Block k;
-        int number_of_k = -1;
-        bool valid = false;
-        for (unsigned x = blockIdx.x;; x += gridDim.x) {
+        // The next unit of the CTA, from number x on; what it takes from memory is asked for at once, and a unit
+        // ahead of when it is needed.
+        auto unit_at = [&](unsigned& x) {
             OutUnit u;
             u.count = 0;
-            if (x < total) {
+            for (; x < total; x += gridDim.x) {
                 unsigned y = x;
                 u.half = y % 2;
                 y /= 2;
@@ -587,20 +589,27 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                 y /= G;
                 u.kvh = y % K;
                 u.head = u.kvh * G + h;
-                const int number = y / K;
-                if (number != number_of_k) {
-                    valid = block_of(p, number, k);
-                    number_of_k = number;
-                }
-                if (!valid || u.half * 128 >= k.count) continue;
-                u.first = k.first;
-                u.count = k.count;
-                u.index = number * K + u.kvh;
-                u.tiles = (min(k.count, u.half * 128 + 128) - 1) / 64 + 1;
-                u.inter = k.n > 0 || k.context > 0;
-                u.dirty = __ldg(c.any_bad + (size_t)u.index * S::kSplits + u.split);
-                u.exponent = u.inter ? __ldg(c.exponents + u.index) : 0;
+                u.index = (int)y;  // (number * K + kvh)
+                const int4 info = __ldg(c.block_info + y / K);
+                u.dirty = __ldg(c.any_bad + (size_t)y * S::kSplits + u.split);
+                u.exponent = __ldg(c.exponents + y);
                 u.l2 = fmaxf(__ldg(p.log_decay + u.kvh) * kLog2e, -1e6f);
+                u.first = info.x;
+                u.inter = info.z;
+                if (u.half * 128 >= info.y) continue;
+                u.count = info.y;
+                u.tiles = (min(u.count, u.half * 128 + 128) - 1) / 64 + 1;
+                break;
+            }
+            return u;
+        };
+        unsigned x = blockIdx.x;
+        OutUnit coming = unit_at(x);
+        for (;;) {
+            const OutUnit u = coming;
+            if (u.count > 0) {
+                x += gridDim.x;
+                coming = unit_at(x);
             }
             if (lane == 0) {
                 const int s = done & 1;

@@ -78,6 +78,7 @@ struct LinearChunkParams {
     float* state_max;      // [B][Hkv]: of the state before the first block
     int* first_bad;        // [blocks][Hkv][D]: first token of a block with a NaN or infinity in that column of v
     int* any_bad;          // [blocks][Hkv][D / tile]: whether a tile's columns have one
+    int4* block_info;      // [blocks]: first token, tokens (0: no such block), whether there is a state before it
     int blocks;            // numbers of blocks, those of no block among them
     int wait_limit;
 };

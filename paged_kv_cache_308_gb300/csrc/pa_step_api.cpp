@@ -130,7 +130,7 @@ constexpr int kLinearFewTokens = 8;
 // The chunked form's workspace: bytes, offsets (the blocks' sums are at 0).
 struct LinearSpace {
     long long blocks;
-    size_t starts, exponents, add_max, state_max, first_bad, any_bad, bytes;
+    size_t starts, exponents, add_max, state_max, first_bad, any_bad, block_info, bytes;
 };
 
 LinearSpace linear_space(int num_seqs, int num_tokens, int num_kv_heads, int head_dim) {
@@ -145,7 +145,8 @@ LinearSpace linear_space(int num_seqs, int num_tokens, int num_kv_heads, int hea
     s.state_max = s.add_max + up(heads * tiles * tiles * 4);
     s.first_bad = s.state_max + up((size_t)num_seqs * num_kv_heads * 4);
     s.any_bad = s.first_bad + up(heads * head_dim * 4);
-    s.bytes = s.any_bad + up(heads * tiles * 4);
+    s.block_info = s.any_bad + up(heads * tiles * 4);
+    s.bytes = s.block_info + up((size_t)s.blocks * 16);
     return s;
 }
 
@@ -292,6 +293,7 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     c.state_max = reinterpret_cast<float*>(w + sp.state_max);
     c.first_bad = reinterpret_cast<int*>(w + sp.first_bad);
     c.any_bad = reinterpret_cast<int*>(w + sp.any_bad);
+    c.block_info = reinterpret_cast<int4*>(w + sp.block_info);
     c.blocks = static_cast<int>(sp.blocks);
     c.wait_limit = pa::kDefaultWaitLimit;
     const int tile = std::min(D, pa::kLinearTile);
