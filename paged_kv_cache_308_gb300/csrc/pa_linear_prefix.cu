@@ -439,11 +439,11 @@ struct OutShape {
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = 64 * kCols * 2;   // 64 tokens or state rows by kCols columns
     static constexpr int kSlots = D == 256 ? 3 : D == 128 ? 5 : 8;
-    static constexpr int kBars = 16 + 2 * kSlots;
+    static constexpr int kBars = 13 + 2 * kSlots;
     // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by halves
     static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * 2 * 128;
     static constexpr int kSmem = kQBytes + kSlots * kStageBytes + kCtrl;
-    static constexpr int kTmem = 256;                    // kCols of the outputs, two buffers of 64 scores
+    static constexpr int kTmem = 256;                    // kCols of the outputs, 128 scores
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 constexpr int kOutRowWarps = 8, kOutThreads = (kOutRowWarps + 2) * 32;
@@ -466,14 +466,14 @@ enum : int {
     kBarQFree,                 // and its MMAs are done
     kBarInter,                 // the accumulator holds Q S
     kBarRead,                  // the rows have read the accumulator
-    kBarScores,                // a score buffer holds its scores, 2
-    kBarP = kBarScores + 2,    // P over them, 2
-    kBarPV = kBarP + 2,        // P V is done, 2
-    kBarUnit = kBarPV + 2,     // a unit's slot is written, 2
+    kBarScores,                // a step's scores are there
+    kBarP,                     // P over them
+    kBarPV,                    // P V is done
+    kBarUnit,                  // a unit's slot is written, 2
     kBarUnitFree = kBarUnit + 2,  // and read by the MMAs' warp and the rows', 2
     kBarDrain = kBarUnitFree + 2,
-    kBarV,                        // a V tile that the rows clean has landed
-    kBarFull = 16
+    kBarV,                        // V tiles that the rows clean have landed
+    kBarFull
 };
 
 // Products of two numbers at a time (one instruction), and the larger magnitude of three.
@@ -504,15 +504,15 @@ __device__ __forceinline__ void store32(__half* to, const uint32_t (&y)[16], boo
 }
 
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
-// (two and four key tiles) neighbours in that order.  A unit's 128 rows are the
+// (one and two steps of 128 keys) neighbours in that order.  A unit's 128 rows are the
 // lanes of the accumulator.  The last warp finds the units and brings Q, then in stages of 64 rows the
-// K tiles of 64 keys, the state's rows and the V tiles, in the order in which the one
-// before it feeds them to the tensor cores: scores of the first key tile; Q S_n; then for each
-// key tile P V and the scores of the tile after the next, in the score buffer that P V has
-// left.  Both run ahead into the next unit while warps 0-7, two threads a row, turn
+// K tiles of a step, the state's rows (behind the first step's) and the V tiles, in the order
+// in which the one before it feeds them to the tensor cores: a step's scores; Q S_n; P V.
+// Both run ahead into the next unit while warps 0-7, two threads a row, turn a step's
 // scores into P, in fp16 over the scores, keep the accumulator in the row's power of
-// two, and write the outputs.  Key tiles go from the row's own backwards, where scores only
-// shrink by the decay, so that the first one nearly always sets that power.
+// two, and write the outputs.  Steps go from the row's own keys backwards, where scores only
+// shrink by the decay, so that the first one nearly always sets that power.  Steps of 128 keys
+// rather than 64 halve the hand-overs, which take longer than the products.
 template <int D>
 __global__ void __launch_bounds__(kOutThreads, 2)
     linear_out_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
     if (t == 0) {
         *failed = 0;
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bar(i), i == kBarP || i == kBarP + 1 || i == kBarRead       ? kOutRowWarps
+            mbar_init(bar(i), i == kBarP || i == kBarRead ? kOutRowWarps
                               : i == kBarUnitFree || i == kBarUnitFree + 1 ? kOutRowWarps + 1
                                                                            : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -561,16 +561,19 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         *failed = 1;
         atomicOr(p.status, PA_DEV_TIMEOUT);
     };
-    // whether the rows change V tile j before it is multiplied (see there)
-    auto cleaned = [](bool dirty, int count, int tiles, int j) { return dirty || (tiles - j) * 64 > count; };
-    // ring stage of V tile j, counted from the unit's first: behind the first two K tiles, the
-    // state and the V and K tiles before it
+    // A unit's steps are of 128 keys, the last ones first: half + 1 of them, of two key tiles, but for
+    // the first one's, which may be one.
+    auto step_tiles = [](int half, int tiles, int j) { return j > 0 ? 2 : tiles - 2 * half; };
+    // whether the rows change a step's V tiles before they are multiplied (see there)
+    auto cleaned = [](bool dirty, int count, int tiles, int j) { return dirty || (j == 0 && tiles * 64 > count); };
+    // ring stage of a step's first V tile, counted from the unit's first stage
     auto v_stage = [&](const OutUnit& u, int j) {
-        return kKStages * min(u.tiles, 2) + (u.inter ? D / 64 : 0) + j + kKStages * min(j, max(u.tiles - 2, 0));
+        const int n0 = u.tiles - 2 * u.half;
+        return kKStages * n0 + (u.inter ? D / 64 : 0) + (j > 0 ? n0 + 2 * kKStages : 0);
     };
 
     if (warp == kOutRowWarps + 1) {
-        int n = 0;  // stages
+        int n = 0, slot = 0, turn = 0;  // stages; the next one's slot of the ring and its phase
         bool ok = true;
         const unsigned total = (unsigned)c.blocks * K * G * S::kSplits * 2;
         int done = 0, q_tiles = 0;  // units; Q tiles
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                 x += gridDim.x;
                 coming = unit_at(x);
             }
-            if (lane == 0) {
+            if (tc_elect()) {
                 const int s = done & 1;
                 if (done >= 2) ok = ok && tc_wait(bar(kBarUnitFree + s), ((done - 2) >> 1) & 1, limit, failed);
                 if (ok) {
@@ -621,17 +624,20 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                 if (ok && u.count > 0) {
                     auto stage = [&](const CUtensorMap* map, int y, int z, int ch) {
                         if (!ok) return;
-                        if (n >= S::kSlots &&
-                            !(ok = tc_wait(bar(kBarEmpty + n % S::kSlots), (n / S::kSlots - 1) & 1, limit, failed)))
-                            return;
-                        const uint32_t full = bar(kBarFull + n % S::kSlots);
+                        if (n >= S::kSlots && !(ok = tc_wait(bar(kBarEmpty + slot), turn ^ 1, limit, failed))) return;
+                        const uint32_t full = bar(kBarFull + slot);
                         mbar_arrive_expect_tx(full, S::kStageBytes);
-                        tc_tma_load_4d(smem_addr(ring + (n % S::kSlots) * S::kStageBytes), map, 0, y, z, ch, full);
+                        tc_tma_load_4d(smem_addr(ring) + slot * S::kStageBytes, map, 0, y, z, ch, full);
                         ++n;
+                        if (++slot == S::kSlots) {
+                            slot = 0;
+                            turn ^= 1;
+                        }
                     };
-                    auto key = [&](int j) { return u.first + (u.tiles - 1 - j) * 64; };
-                    auto k_tile = [&](int j) {
-                        for (int ch = 0; ch < kKStages; ++ch) stage(&maps.k, u.kvh, key(j), ch * (S::kCols / 64));
+                    auto k_tiles = [&](int j) {
+                        for (int y = 0; y < step_tiles(u.half, u.tiles, j); ++y)
+                            for (int ch = 0; ch < kKStages; ++ch)
+                                stage(&maps.k, u.kvh, u.first + (u.half - j) * 128 + y * 64, ch * (S::kCols / 64));
                     };
                     if (done >= 1) ok = tc_wait(bar(kBarQFree), (done - 1) & 1, limit, failed);
                     if (ok) {
@@ -639,13 +645,13 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                         tc_tma_load_4d(smem_addr(qs), &maps.q, 0, u.head, u.first + u.half * 128, 0, bar(kBarQ));
                         ++q_tiles;
                     }
-                    k_tile(0);
+                    k_tiles(0);
                     if (u.inter)
                         for (int d = 0; d < D / 64; ++d) stage(&maps.starts, 0, u.index * D + d * 64, u.split * (S::kCols / 64));
-                    if (u.tiles > 1) k_tile(1);
-                    for (int j = 0; j < u.tiles; ++j) {
-                        stage(&maps.v, u.kvh, key(j), u.split * (S::kCols / 64));
-                        if (j + 2 < u.tiles) k_tile(j + 2);
+                    for (int j = 0; j <= u.half; ++j) {
+                        if (j > 0) k_tiles(j);
+                        for (int y = 0; y < step_tiles(u.half, u.tiles, j); ++y)
+                            stage(&maps.v, u.kvh, u.first + (u.half - j) * 128 + y * 64, u.split * (S::kCols / 64));
                     }
                 }
                 if (!ok) fail();
@@ -654,7 +660,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             if (!ok || u.count == 0) break;
             ++done;
         }
-        if (lane == 0) {
+        if (tc_elect()) {
             // every copy lands before the CTA's memory is given back
             if (q_tiles > 0) mbar_wait(bar(kBarQ), (q_tiles - 1) & 1, kDefaultWaitLimit);
             for (int i = max(0, n - S::kSlots); i < n; ++i)
@@ -662,86 +668,95 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         }
         __syncwarp();
     } else if (warp == kOutRowWarps) {
-        if (lane == 0) {
+        if (tc_elect()) {
             constexpr uint32_t id_s = tc_idesc(128, 64, 0), id_o = tc_idesc(128, S::kCols, 1);
             const uint64_t qdesc = tc_desc(smem_addr(qs), 16, 1024);
             const uint64_t kdesc = tc_desc(smem_addr(ring), 16, 1024), vdesc = tc_desc(smem_addr(ring), 64 * 128, 1024);
-            int n = 0, g = 0, inters = 0;  // stages, key tiles of earlier units
+            int slot = 0, turn = 0;   // of the ring: the next stage's slot, and its phase
+            int x = 0, inters = 0;    // steps, units with a state
             bool ok = true;
             auto wait = [&](int b, int parity) { return ok = ok && tc_wait(bar(b), parity & 1, limit, failed); };
-            auto landed = [&] { return wait(kBarFull + n % S::kSlots, n / S::kSlots); };
-            auto stage_at = [&] { return (uint64_t)((n % S::kSlots) * (S::kStageBytes >> 4)); };
-            auto scores = [&](int x) {
-                // over the P that P V has read
-                if (x >= 2 && !wait(kBarPV + (x & 1), (x - 2) >> 1)) return;
-                for (int ch = 0; ch < kKStages; ++ch) {
-                    if (!landed()) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < S::kCols / 16; ++i)
-                        tc_mma_ss(t_s + (x & 1) * 64,
-                                  qdesc + (uint64_t)(((ch * (S::kCols / 64) + (i >> 2)) * (128 * 128) + (i & 3) * 32) >> 4),
-                                  kdesc + stage_at() + (uint64_t)(((i >> 2) * (64 * 128) + (i & 3) * 32) >> 4), id_s,
-                                  ch > 0 || i > 0);
-                    tc_commit(bar(kBarEmpty + n % S::kSlots));
-                    ++n;
+            auto landed = [&] { return wait(kBarFull + slot, turn); };
+            auto stage_at = [&] { return (uint64_t)(slot * (S::kStageBytes >> 4)); };
+            auto release = [&] {
+                tc_commit(bar(kBarEmpty + slot));
+                if (++slot == S::kSlots) {
+                    slot = 0;
+                    turn ^= 1;
                 }
-                tc_commit(bar(kBarScores + (x & 1)));
             };
             for (int done = 0;; ++done) {
                 const int s = done & 1;
                 if (!wait(kBarUnit + s, done >> 1)) break;
-                const int count = units[s].count, tiles = units[s].tiles;
+                const int count = units[s].count, tiles = units[s].tiles, half = units[s].half;
                 const bool inter = units[s].inter, dirty = units[s].dirty;
                 mbar_arrive(bar(kBarUnitFree + s));
                 if (count == 0) break;
                 if (!wait(kBarQ, done)) break;
-                scores(g);
-                if (inter) {
-                    // the accumulator's last outputs have been read
-                    if (done >= 1 && !wait(kBarRead, done - 1)) break;
-                    for (int d = 0; d < D / 64 && landed(); ++d) {
-                        tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j <= half; ++j, ++x) {
+                    const int mine = step_tiles(half, tiles, j);
+                    // scores over the P that P V has read
+                    if (x > 0 && !wait(kBarPV, x - 1)) break;
+#pragma unroll 1
+                    for (int y = 0; y < mine; ++y) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc_mma_ss(t_out, qdesc + (uint64_t)((d * (128 * 128) + i * 32) >> 4),
-                                      vdesc + stage_at() + (uint64_t)((i * 2048) >> 4), id_o, d > 0 || i > 0);
-                        tc_commit(bar(kBarEmpty + n % S::kSlots));
-                        ++n;
+                        for (int ch = 0; ch < kKStages; ++ch) {
+                            if (!landed()) break;
+                            tc_fence_after();
+                            const uint64_t kd = kdesc + stage_at();
+#pragma unroll
+                            for (int i = 0; i < S::kCols / 16; ++i)
+                                tc_mma_ss(t_s + y * 64,
+                                          qdesc + (uint64_t)(((ch * (S::kCols / 64) + (i >> 2)) * (128 * 128) + (i & 3) * 32) >> 4),
+                                          kd + (uint64_t)(((i >> 2) * (64 * 128) + (i & 3) * 32) >> 4), id_s, ch > 0 || i > 0);
+                            release();
+                        }
                     }
                     if (!ok) break;
-                    tc_commit(bar(kBarInter));
-                    ++inters;
-                }
-                if (tiles > 1) scores(g + 1);
-                if (tiles <= 2) tc_commit(bar(kBarQFree));
-                for (int j = 0; j < tiles; ++j) {
-                    const int x = g + j;
-                    // (rows that have written P have read the last outputs too)
+                    tc_commit(bar(kBarScores));
+                    if (j == 0 && inter) {
+                        // the accumulator's last outputs have been read
+                        if (done >= 1 && !wait(kBarRead, done - 1)) break;
+#pragma unroll 1
+                        for (int d = 0; d < D / 64 && landed(); ++d) {
+                            tc_fence_after();
+                            const uint64_t qd = qdesc + (uint64_t)((d * (128 * 128)) >> 4), sd = vdesc + stage_at();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                tc_mma_ss(t_out, qd + (uint64_t)((i * 32) >> 4), sd + (uint64_t)((i * 2048) >> 4), id_o, d > 0 || i > 0);
+                            release();
+                        }
+                        if (!ok) break;
+                        tc_commit(bar(kBarInter));
+                        ++inters;
+                    }
+                    if (j == half) tc_commit(bar(kBarQFree));
                     // (the rows cannot tell a ring slot's phases apart: they may be two behind)
                     if (cleaned(dirty, count, tiles, j)) {
-                        if (!landed()) break;
+                        const bool wraps = slot + mine - 1 >= S::kSlots;  // (the second one's slot)
+                        if (!landed() || !wait(kBarFull + slot + mine - 1 - (wraps ? S::kSlots : 0), turn ^ (int)wraps)) break;
                         mbar_arrive(bar(kBarV));
                     }
-                    if (!wait(kBarP + (x & 1), x >> 1) || !landed()) break;
+                    // (rows that have written P have read the last outputs too)
+                    if (!wait(kBarP, x)) break;
                     // Q S, whose operand comes from shared memory, is done before P V, whose comes from
                     // tensor memory, adds to it: nothing orders the two kinds in the tensor cores
                     if (j == 0 && inter && !wait(kBarInter, inters - 1)) break;
-                    tc_fence_after();
+#pragma unroll 1
+                    for (int y = 0; y < mine && landed(); ++y) {
+                        tc_fence_after();
+                        const uint64_t vd = vdesc + stage_at();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tc_mma_ts(t_out, t_s + (x & 1) * 64 + i * 8, vdesc + stage_at() + (uint64_t)((i * 2048) >> 4), id_o,
-                                  inter || j > 0 || i > 0);
-                    tc_commit(bar(kBarEmpty + n % S::kSlots));
-                    tc_commit(bar(kBarPV + (x & 1)));
-                    ++n;
-                    if (j + 2 < tiles) {
-                        scores(x + 2);
-                        if (j + 3 == tiles) tc_commit(bar(kBarQFree));
+                        for (int i = 0; i < 4; ++i)
+                            tc_mma_ts(t_out, t_s + y * 64 + i * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
+                                      inter || j > 0 || y > 0 || i > 0);
+                        release();
                     }
+                    if (!ok) break;
+                    tc_commit(bar(kBarPV));
                 }
                 if (!ok) break;
-                g += tiles;
             }
             if (!ok) fail();
             tc_commit(bar(kBarDrain));
@@ -756,7 +771,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         constexpr int kMine = S::kCols / 2;  // columns of the outputs
         const uint32_t acc = t_out + lanes + side * kMine;
         bool ok = true;
-        int g = 0, inters = 0;  // key tiles, and units with a state, of earlier units
+        int x = 0, inters = 0;  // steps; units with a state
         int stages = 0;         // ring stages of earlier units
         int cleans = 0;         // V tiles cleaned
         for (int done = 0;; ++done) {
@@ -771,7 +786,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             // many times the state's part as `state` says; where that number is moderate the scores
             // simply go by it, and the accumulator is not touched.
             const float state = u.inter ? (float)u.exponent + u.l2 * (float)(i + 1) : 0.f;
-            float level = fminf(fmaxf(state, -40.f), 60.f);
+            float level = u.inter ? fminf(fmaxf(state, -6.f), 60.f) : 0.f;
             const float least = u.inter ? state - 60.f : -200.f;  // below which the state's part could overflow
             float pending = u.inter ? state - level : 0.f;        // by how much the accumulator is behind
             bool set = false;
@@ -788,70 +803,77 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             float within[8];  // decays inside a group of 8 keys
 #pragma unroll
             for (int v = 0; v < 8; ++v) within[v] = tc_ex2(u.l2 * (float)(7 - v));
-            for (int j = 0; j < u.tiles; ++j) {
-                const int x = g + j;
-                const int k0 = (u.tiles - 1 - j) * 64;  // first key of the tile
-                const int kc = k0 + side * 32;          // and of the warp's half
-                const uint32_t buf = t_s + (x & 1) * 64 + lanes;
-                if (!(ok = tc_warp_wait(bar(kBarScores + (x & 1)), (x >> 1) & 1, limit, failed))) break;
+#pragma unroll 1
+            for (int j = 0; j <= u.half; ++j, ++x) {
+                const int kc = (u.half - j) * 128 + side * 64;  // first key of the warp's half of the step
+                if (!(ok = tc_warp_wait(bar(kBarScores), x & 1, limit, failed))) break;
                 tc_fence_after();
-                uint32_t sc[32];
-                float m = 0.f;
-                if (kc > row0) {  // keys behind all of the rows
+                uint32_t pk[32];
+                // A second time where a row's level has to move: 64 scores a thread kept beside their P would not
+                // fit in its registers.
+#pragma unroll 1
+                for (bool again = false;;) {
+                    float m = 0.f;
 #pragma unroll
-                    for (int v = 0; v < 32; ++v) sc[v] = 0u;
-                } else {
-                    tc_ld32(buf + side * 32, sc);
-                    if (kc < row0) {
-                        // d^(i - key) 2^-level: for groups of 8 keys up to the last of them, and the one within
+                    for (int h = 0; h < 2; ++h) {
+                        const int k0 = kc + h * 32;
+                        uint32_t sc[32];
+                        if (k0 > row0) {  // keys behind all of the rows
 #pragma unroll
-                        for (int v = 0; v < 32; v += 8) {
-                            const float to = tc_ex2(fmaf(u.l2, (float)(i - kc - v - 7), -level));
-#pragma unroll
-                            for (int y = 0; y < 8; y += 2) {
-                                uint32_t d0 = __float_as_uint(within[y]), d1 = __float_as_uint(within[y + 1]);
-                                mul2(d0, d1, to, to);
-                                mul2(sc[v + y], sc[v + y + 1], __uint_as_float(d0), __uint_as_float(d1));
-                            }
+                            for (int v = 0; v < 16; ++v) pk[h * 16 + v] = 0u;
+                            continue;
                         }
-                    } else {  // the diagonal
+                        tc_ld32(t_s + lanes + side * 64 + h * 32, sc);
+                        // times d^(i - key) 2^-level
+                        if (k0 < row0) {
+                            // for groups of 8 keys up to the last of them, and the one within
 #pragma unroll
-                        for (int v = 0; v < 32; ++v)
-                            sc[v] = lane >= v ? __float_as_uint(__uint_as_float(sc[v]) * tc_ex2(fmaf(u.l2, (float)(lane - v), -level))) : 0u;
+                            for (int v = 0; v < 32; v += 8) {
+                                const float to = tc_ex2(fmaf(u.l2, (float)(i - k0 - v - 7), -level));
+#pragma unroll
+                                for (int y = 0; y < 8; y += 2) {
+                                    uint32_t d0 = __float_as_uint(within[y]), d1 = __float_as_uint(within[y + 1]);
+                                    mul2(d0, d1, to, to);
+                                    mul2(sc[v + y], sc[v + y + 1], __uint_as_float(d0), __uint_as_float(d1));
+                                }
+                            }
+                        } else {  // the diagonal
+#pragma unroll
+                            for (int v = 0; v < 32; ++v)
+                                sc[v] = lane >= v ? __float_as_uint(__uint_as_float(sc[v]) *
+                                                                    tc_ex2(fmaf(u.l2, (float)(lane - v), -level)))
+                                                  : 0u;
+                        }
+#pragma unroll
+                        for (int v = 0; v < 32; v += 2) {
+                            m = max3(m, sc[v], sc[v + 1]);
+                            pk[h * 16 + v / 2] = half2_bits(__floats2half2_rn(__uint_as_float(sc[v]), __uint_as_float(sc[v + 1])));
+                        }
                     }
-#pragma unroll
-                    for (int v = 0; v < 32; v += 2)
-                        m = max3(m, sc[v], sc[v + 1]);
-                }
-                // the exponent of the row's largest, of both halves (what is not a normal number counts as 0)
-                uint8_t* mine = largest + (x & 1) * 256 + quarter * 32 + lane;
-                int e = exponent_of(m);
-                mine[side * 128] = (uint8_t)(e + 127);
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                e = max(e, (int)mine[(side ^ 1) * 128] - 127);
-                // The level moves where the row's first scores that are not 0 are not of a middling size, and
-                // where later ones would leave fp16.
-                const bool move = e > -127 && (e >= 15 || (!set && e < -4));
-                set |= e > -127;
-                if (__any_sync(kFull, move)) {
+                    if (again) break;
+                    // the exponent of the row's largest, of both halves (what is not a normal number counts as 0)
+                    uint8_t* mine = largest + (x & 1) * 256 + quarter * 32 + lane;
+                    int e = exponent_of(m);
+                    mine[side * 128] = (uint8_t)(e + 127);
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                    e = max(e, (int)mine[(side ^ 1) * 128] - 127);
+                    // The level moves where the row's first scores that are not 0 are not of a middling size, and
+                    // where later ones would leave fp16.
+                    const bool move = e > -127 && (e >= 15 || (!set && e < -4));
+                    set |= e > -127;
+                    if (!__any_sync(kFull, move)) break;
                     const float by = move ? fmaxf((float)(e - 8), least - level) : 0.f;
-                    const float f = exp2f(-by);
                     level += by;
                     pending -= by;
-#pragma unroll
-                    for (int v = 0; v < 32; ++v) sc[v] = __float_as_uint(__uint_as_float(sc[v]) * f);
+                    again = true;
                 }
-                uint32_t pk[16];
-#pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    pk[v] = half2_bits(__floats2half2_rn(__uint_as_float(sc[2 * v]), __uint_as_float(sc[2 * v + 1])));
-                tc_st16(buf + side * 16, pk);
+                tc_st32(t_s + lanes + side * 64, pk);  // over the thread's own scores
                 if (__any_sync(kFull, pending != 0.f)) {
                     // (the accumulator holds nothing before a first tile without a state)
                     if (j == 0 && u.inter) {
                         ok = tc_warp_wait(bar(kBarInter), inters & 1, limit, failed);
                     } else if (j > 0) {
-                        ok = tc_warp_wait(bar(kBarPV + ((x - 1) & 1)), ((x - 1) >> 1) & 1, limit, failed);
+                        ok = tc_warp_wait(bar(kBarPV), (x - 1) & 1, limit, failed);
                     }
                     if (!ok) break;
                     if (j > 0 || u.inter) {
@@ -864,31 +886,32 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     // V rows behind the block's last token belong to other sequences, and a NaN or
                     // infinity must not meet the zeros of tokens before it: both become 0 (the latter's column
                     // is set from its token on in the end)
-                    const int n = stages + v_stage(u, j);
                     if (!(ok = tc_warp_wait(bar(kBarV), cleans & 1, limit, failed))) break;
                     ++cleans;
-                    uint8_t* vt = ring + (n % S::kSlots) * S::kStageBytes;
-                    for (int v = t; v < S::kStageBytes / 16; v += kOutRowWarps * 32) {
-                        const int row = (v >> 3) & 63;
-                        uint4* at = reinterpret_cast<uint4*>(vt + (size_t)v * 16);
-                        uint4 y = *at;
-                        auto clean = [](uint32_t h) {
-                            if ((h & 0x7c00u) == 0x7c00u) h &= 0xffff0000u;
-                            if ((h & 0x7c000000u) == 0x7c000000u) h &= 0xffffu;
-                            return h;
-                        };
-                        y = k0 + row < u.count ? make_uint4(clean(y.x), clean(y.y), clean(y.z), clean(y.w)) : make_uint4(0u, 0u, 0u, 0u);
-                        *at = y;
+#pragma unroll 1
+                    for (int y = 0; y < step_tiles(u.half, u.tiles, j); ++y) {
+                        uint8_t* vt = ring + ((stages + v_stage(u, j) + y) % S::kSlots) * S::kStageBytes;
+                        const int k0 = (u.half - j) * 128 + y * 64;
+                        for (int v = t; v < S::kStageBytes / 16; v += kOutRowWarps * 32) {
+                            const int row = (v >> 3) & 63;
+                            uint4* at = reinterpret_cast<uint4*>(vt + (size_t)v * 16);
+                            const uint4 z = *at;
+                            auto clean = [](uint32_t h) {
+                                if ((h & 0x7c00u) == 0x7c00u) h &= 0xffff0000u;
+                                if ((h & 0x7c000000u) == 0x7c000000u) h &= 0xffffu;
+                                return h;
+                            };
+                            *at = k0 + row < u.count ? make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w)) : make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarP + (x & 1)));
+                if (lane == 0) mbar_arrive(bar(kBarP));
             }
             if (!ok) break;
-            const int last = g + u.tiles - 1;
-            if (!(ok = tc_warp_wait(bar(kBarPV + (last & 1)), (last >> 1) & 1, limit, failed))) break;
+            if (!(ok = tc_warp_wait(bar(kBarPV), (x - 1) & 1, limit, failed))) break;
             tc_fence_after();
             const float f = p.scale * exp2f(level);
             __half* out = p.out + ((size_t)(u.first + i) * H + u.head) * D + u.split * S::kCols + side * kMine;
@@ -913,9 +936,8 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarRead));
-            g += u.tiles;
             inters += u.inter;
-            stages += v_stage(u, u.tiles - 1) + 1;
+            stages += v_stage(u, u.half) + step_tiles(u.half, u.tiles, u.half);
         }
         if (!ok && lane == 0) fail();
     }

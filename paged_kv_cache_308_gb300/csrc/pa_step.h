@@ -23,10 +23,12 @@ struct KvAllocParams {
     int32_t* slots;
     int32_t* positions;
     int num_blocks, num_seqs, num_tokens, cols;
+    int place;  // the cluster places the tokens too; else a launch of their own
     unsigned int* status;
 };
 constexpr int kAllocThreads = 512;
 constexpr int kAllocMaxCluster = 8;
+constexpr int kAllocAllSeqs = 2048;  // up to so many are kept in each block's shared memory
 cudaError_t launch_kv_alloc(const KvAllocParams& prm, int cluster, cudaStream_t stream);
 
 struct KvPutParams {

@@ -124,6 +124,10 @@ int check_linear_prefix(const pa_linear_prefix_args* a) {
     return PA_OK;
 }
 
+// pa_kv_alloc: up to so many tokens are placed by the cluster that moves the blocks, and up to so many
+// sequences take a cluster of one block.
+constexpr int kAllocPlaceTokens = 4096, kAllocOneSeqs = 128;
+
 // Up to so many new tokens a sequence go token by token.
 constexpr int kLinearFewTokens = 8;
 
@@ -175,7 +179,9 @@ int pa_kv_alloc(const pa_kv_alloc_args* a, pa_stream_t stream) {
     p.cols = a->max_blocks_per_seq;
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
-    return pa::launch_kv_alloc(p, pa::kAllocMaxCluster, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    p.place = a->num_tokens <= kAllocPlaceTokens;
+    const int cluster = a->num_seqs <= kAllocOneSeqs ? 1 : pa::kAllocMaxCluster;
+    return pa::launch_kv_alloc(p, cluster, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
@@ -209,7 +215,11 @@ int pa_kv_put(const pa_kv_put_args* a, pa_stream_t stream) {
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
     const int rows = a->num_heads + 2 * c.num_kv_heads, warps = pa::kPutThreads / 32;
-    p.rows_per_warp = std::max(8, (rows + 65534) / 65535);
+    // all heads of a token to a warp where there are many tokens, at least 8
+    int num_sms = 0;
+    if (pa::sm_count(&num_sms) != PA_OK) return PA_ERR_CUDA;
+    const long long splits = std::max(1ll, std::min((long long)rows / 8, 32ll * num_sms / a->num_tokens));
+    p.rows_per_warp = static_cast<int>(std::max((rows + splits - 1) / splits, (rows + 65534ll) / 65535));
     const dim3 grid((a->num_tokens + warps - 1) / warps, (rows + p.rows_per_warp - 1) / p.rows_per_warp);
     return pa::launch_kv_put(c.head_dim, p, grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                                          : PA_ERR_CUDA;
