@@ -840,25 +840,33 @@ def pa_kv_alloc(block_tables, free_blocks, free_count, context_lens, query_lens,
     dev = block_tables.get_device()
     B, T, nb = context_lens.shape[0], slot_map.shape[0], free_blocks.shape[0]
     table, cols = _table("block_tables", block_tables, B, dev)
-    count = _tensor("free_count", free_count, _I32, (1,), dev)
-    per_seq = (B,)
-    args = _ALLOC.pack(table, _tensor("free_blocks", free_blocks, _I32, (nb,), dev), count,
-                       count if new_free_count is None else _tensor("new_free_count", new_free_count, _I32, (1,), dev),
-                       0 if held_lens is None else _tensor("held_lens", held_lens, _I32, per_seq, dev),
-                       _tensor("context_lens", context_lens, _I32, per_seq, dev),
-                       _tensor("query_lens", query_lens, _I32, per_seq, dev),
-                       _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev),
-                       _tensor("seq_lens", seq_lens, _I32, per_seq, dev), _tensor("slot_map", slot_map, _I32, (T,), dev),
-                       _tensor("positions", positions, _I32, (T,), dev), nb, B, T, cols, int(block_size))
+    count = _ints("free_count", free_count, 1, dev)
+    args = _ALLOC.pack(table, _ints("free_blocks", free_blocks, nb, dev), count,
+                       count if new_free_count is None else _ints("new_free_count", new_free_count, 1, dev),
+                       0 if held_lens is None else _ints("held_lens", held_lens, B, dev),
+                       _ints("context_lens", context_lens, B, dev), _ints("query_lens", query_lens, B, dev),
+                       _ints("query_start_loc", query_start_loc, B + 1, dev), _ints("seq_lens", seq_lens, B, dev),
+                       _ints("slot_map", slot_map, T, dev), _ints("positions", positions, T, dev), nb, B, T, cols,
+                       int(block_size))
     _call("pa_kv_alloc", dev, stream, lib.pa_kv_alloc, args)
 
 
+def _ints(name, t, n, dev):
+    """The pointer of n int32."""
+    if t.dtype is not _I32 or t.get_device() != dev or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+        _bad(name, t, torch.int32, (n,), dev)
+    return t.data_ptr()
+
+
 def _rows(name, t, shape, dev):
-    """(pointer, elements between rows) of float16 rows that are contiguous in themselves."""
-    if t.dtype is not _F16 or t.get_device() != dev or t.shape != shape or (
-            t.numel() and (t.stride(2) != 1 or t.stride(1) != shape[2])):
+    """(pointer, elements between rows; 0: contiguous) of float16 rows that are contiguous in themselves."""
+    if t.dtype is not _F16 or t.get_device() != dev or t.shape != shape:
         _bad(name, t, torch.float16, shape, dev)
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        _bad(name, t, torch.float16, shape, dev)
+    return t.data_ptr(), t.stride(0)
 
 
 def pa_kv_put(q_out, k_out, q, k, v, k_cache, v_cache, slot_map, positions, cos_sin, stream=None, *,
@@ -888,14 +896,14 @@ def pa_kv_put(q_out, k_out, q, k, v, k_cache, v_cache, slot_map, positions, cos_
         if cache[5] != hkv or cache[6] != dim:
             raise ValueError(f"k_cache must have {hkv} kv heads of {dim}, got {list(k_cache.shape)}")
         vp, vs = _rows("v", v, k_shape, dev)
-        slots = _tensor("slot_map", slot_map, _I32, (T,), dev)
-    if cos_sin.dim() != 2:
+        slots = _ints("slot_map", slot_map, T, dev)
+    top_rot = cos_sin.shape
+    if len(top_rot) != 2:
         raise ValueError("cos_sin must be [max_positions, rotary_dim]")
     args = _PUT.pack(*cache, _tensor("q_out", q_out, _F16, q_shape, dev),
                      0 if k_out is None else _tensor("k_out", k_out, _F16, k_shape, dev), qp, kp, vp, slots,
-                     _tensor("positions", positions, _I32, (T,), dev),
-                     _tensor("cos_sin", cos_sin, _F32, cos_sin.shape, dev), qs, ks, vs, T, H, cos_sin.shape[1],
-                     cos_sin.shape[0], int(bool(pairs)))
+                     _ints("positions", positions, T, dev), _tensor("cos_sin", cos_sin, _F32, top_rot, dev), qs, ks, vs, T, H,
+                     top_rot[1], top_rot[0], int(bool(pairs)))
     _call("pa_kv_put", dev, stream, lib.pa_kv_put, args)
 
 

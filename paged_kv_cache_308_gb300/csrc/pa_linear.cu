@@ -30,17 +30,40 @@ __device__ __forceinline__ Decay decay_of(float g) {
     return {0.f, expf(g)};
 }
 
+// Two 32-bit numbers a register pair, for the instructions that take two at a time.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 parts(Two x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // A block takes kCols columns of a (sequence, kv head)'s state through all of its
-// tokens; each thread holds kPasses rows of four columns.  A token's products with
+// tokens; each thread holds kPasses rows, next to each other, of four columns.  A token's products with
 // q are summed over the block's rows by shuffles and in shared memory.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const LinearParams prm) {
+__global__ void __launch_bounds__(kThreads, G > 4 ? 3 : 4) linear_recurrent_kernel(const LinearParams prm) {
     using S = Slice<D>;
-    __shared__ float ks[D];
-    __shared__ float qs[G][D];
-    __shared__ float red[kThreads / 32][G][S::kCols];
+    __shared__ __align__(16) float ks[D];
+    __shared__ __align__(16) float qs[G][D];
+    __shared__ __align__(16) float red[kThreads / 32][G][S::kCols];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int kvh = blockIdx.y, b = blockIdx.z, c0 = blockIdx.x * S::kCols + (t % S::kLanes) * 4, r0 = t / S::kLanes;
+    const int kvh = blockIdx.y, b = blockIdx.z, c0 = blockIdx.x * S::kCols + (t % S::kLanes) * 4, r0 = t / S::kLanes * S::kPasses;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int slot = __ldg(prm.slots + b);
@@ -66,11 +89,11 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
     if (!(g <= 0.f) && t == 0 && blockIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_DECAY);
     const Decay dec = decay_of(g);
 
-    float4* state = reinterpret_cast<float4*>(prm.states + (((size_t)slot * prm.num_kv_heads + kvh) * D + r0) * D + c0);
-    float4 s[S::kPasses];
+    ulonglong2* state = reinterpret_cast<ulonglong2*>(prm.states + (((size_t)slot * prm.num_kv_heads + kvh) * D + r0) * D + c0);
+    ulonglong2 s[S::kPasses];
 #pragma unroll
-    for (int i = 0; i < S::kPasses; ++i)
-        s[i] = fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcs(state + (size_t)i * S::kRows * D / 4);
+    for (int i = 0; i < S::kPasses; ++i) s[i] = fresh ? make_ulonglong2(0, 0) : __ldcs(state + i * D / 4);
+    const Two whole = two(dec.whole, dec.whole), rest = two(dec.rest, dec.rest);
 
     for (int row = first; row < last; ++row) {
         const __half* k = prm.k + ((size_t)row * prm.num_kv_heads + kvh) * D;
@@ -80,23 +103,37 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
         for (int i = t; i < G * D; i += kThreads) qs[i / D][i % D] = i < prm.group * D ? __half2float(q[i]) : 0.f;
         const float2 v01 = __half22float2(*reinterpret_cast<const __half2*>(&vr.x));
         const float2 v23 = __half22float2(*reinterpret_cast<const __half2*>(&vr.y));
+        const Two va = two(v01.x, v01.y), vb = two(v23.x, v23.y);
         __syncthreads();
-        float4 acc[G];
+        Two sum[G][2];
 #pragma unroll
-        for (int h = 0; h < G; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int h = 0; h < G; ++h) sum[h][0] = sum[h][1] = 0;
 #pragma unroll
-        for (int i = 0; i < S::kPasses; ++i) {
-            const float kk = ks[r0 + i * S::kRows];
-            auto step = [&](float x, float v) { return fmaf(kk, v, fmaf(x, dec.rest, x * dec.whole)); };
-            s[i] = make_float4(step(s[i].x, v01.x), step(s[i].y, v01.y), step(s[i].z, v23.x), step(s[i].w, v23.y));
+        for (int i = 0; i < S::kPasses; i += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(ks + r0 + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float kk = j == 0 ? k4.x : j == 1 ? k4.y : j == 2 ? k4.z : k4.w;
+                ulonglong2& x = s[i + j];
+                x.x = fma2(two(kk, kk), va, fma2(x.x, rest, mul2(x.x, whole)));
+                x.y = fma2(two(kk, kk), vb, fma2(x.y, rest, mul2(x.y, whole)));
+            }
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-                const float qq = qs[h][r0 + i * S::kRows];
-                acc[h].x = fmaf(qq, s[i].x, acc[h].x);
-                acc[h].y = fmaf(qq, s[i].y, acc[h].y);
-                acc[h].z = fmaf(qq, s[i].z, acc[h].z);
-                acc[h].w = fmaf(qq, s[i].w, acc[h].w);
+                const float4 q4 = *reinterpret_cast<const float4*>(&qs[h][r0 + i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float qq = j == 0 ? q4.x : j == 1 ? q4.y : j == 2 ? q4.z : q4.w;
+                    sum[h][0] = fma2(two(qq, qq), s[i + j].x, sum[h][0]);
+                    sum[h][1] = fma2(two(qq, qq), s[i + j].y, sum[h][1]);
+                }
             }
+        }
+        float4 acc[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float2 a = parts(sum[h][0]), b = parts(sum[h][1]);
+            acc[h] = make_float4(a.x, a.y, b.x, b.y);
         }
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -120,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
         }
     }
 #pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) __stcs(state + (size_t)i * S::kRows * D / 4, s[i]);
+    for (int i = 0; i < S::kPasses; ++i) __stcs(state + i * D / 4, s[i]);
 }
 
 template <int D, int G>

@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kAddThreads, 2)
                     break;
                 mbar_arrive_expect_tx(bar_full + 8 * s, 2 * S::kHalf);
                 const uint32_t dst = smem_addr(ring + s * 2 * S::kHalf);
-                tc_tma_load_4d(dst, &maps.k, 0, kvh, k.first + tokens_at(x), k_tile * (S::kTile / 64), bar_full + 8 * s);
-                tc_tma_load_4d(dst + S::kHalf, &maps.v, 0, kvh, k.first + tokens_at(x), v_tile * (S::kTile / 64), bar_full + 8 * s);
+                tc_tma_load_4d(dst, &maps.k_group, 0, kvh, k.first + tokens_at(x), k_tile * (S::kTile / 64), bar_full + 8 * s);
+                tc_tma_load_4d(dst + S::kHalf, &maps.v_group, 0, kvh, k.first + tokens_at(x), v_tile * (S::kTile / 64), bar_full + 8 * s);
             }
             if (!ok) fail();
             // every copy lands before the CTA's memory is given back
@@ -434,26 +434,33 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
 
 template <int D>
 struct OutShape {
-    static constexpr int kCols = D < 128 ? D : 128;      // of v and out, of a unit
-    static constexpr int kSplits = D / kCols;
+    // two CTAs an SM up to head_dim 128; at 256 the accumulator takes half of the tensor memory
+    static constexpr int kCtas = D == 256 ? 1 : 2;
+    static constexpr int kSides = D == 256 ? 4 : 2;       // threads of a row
+    static constexpr int kRowWarps = 4 * kSides;
+    static constexpr int kThreads = (kRowWarps + 2) * 32;
+    static constexpr int kStageRows = D == 256 ? 64 : 128;  // keys or state rows of a ring slot, 16 or 32 KB
+    static constexpr int kStateRows = D < kStageRows ? D : kStageRows;
+    static constexpr int kStepStages = 128 / kStageRows;
     static constexpr int kQBytes = 128 * D * 2;
-    static constexpr int kStageBytes = 64 * kCols * 2;   // 64 tokens or state rows by kCols columns
-    static constexpr int kSlots = D == 256 ? 3 : D == 128 ? 5 : 8;
+    static constexpr int kStageBytes = kStageRows * D * 2;
+    static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 2 : 4;
     static constexpr int kBars = 13 + 2 * kSlots;
-    // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by halves
-    static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * 2 * 128;
-    static constexpr int kSmem = kQBytes + kSlots * kStageBytes + kCtrl;
-    static constexpr int kTmem = 256;                    // kCols of the outputs, 128 scores
-    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+    // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by threads
+    static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * kSides * 128;
+    static constexpr int kSmemNeed = kQBytes + kSlots * kStageBytes + kCtrl;
+    // (so much that no more CTAs fit, and their TMEM allocations always do)
+    static constexpr int kSmem = kSmemNeed > 80 * 1024 ? kSmemNeed : 80 * 1024;
+    static constexpr int kTmem = D == 256 ? 512 : 256;    // D of the outputs, 128 scores
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "CTAs an SM");
+    static_assert(D + 128 <= kTmem && kCtas * kTmem <= 512, "tensor memory of an SM");
 };
-constexpr int kOutRowWarps = 8, kOutThreads = (kOutRowWarps + 2) * 32;
 
-// 128 tokens (a half of a block) of one query head and 128 columns of v.
+// 128 tokens (a half of a block) of one query head.
 struct OutUnit {
     int first, count;  // of the block; count 0: no more units
     int index;         // of the block and kv head
-    int half, kvh, head, split;
-    int tiles;         // of 64 keys, up to the half's last token
+    int half, kvh, head;
     int inter;         // whether there is a state before the block
     int dirty;         // whether a column of v has a NaN or infinity
     int exponent;      // of that state
@@ -505,16 +512,19 @@ __device__ __forceinline__ void store32(__half* to, const uint32_t (&y)[16], boo
 
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
 // (one and two steps of 128 keys) neighbours in that order.  A unit's 128 rows are the
-// lanes of the accumulator.  The last warp finds the units and brings Q, then in stages of 64 rows the
-// K tiles of a step, the state's rows (behind the first step's) and the V tiles, in the order
-// in which the one before it feeds them to the tensor cores: a step's scores; Q S_n; P V.
-// Both run ahead into the next unit while warps 0-7, two threads a row, turn a step's
-// scores into P, in fp16 over the scores, keep the accumulator in the row's power of
-// two, and write the outputs.  Steps go from the row's own keys backwards, where scores only
-// shrink by the decay, so that the first one nearly always sets that power.  Steps of 128 keys
-// rather than 64 halve the hand-overs, which take longer than the products.
+// lanes of the accumulator.  The last warp finds the units and brings Q, then in ring stages a
+// step's keys, the state's rows (behind the first step's keys) and the step's values, in the
+// order in which the warp before it feeds them to the tensor cores: a step's scores; Q S_n;
+// P V.  Both run ahead into the next unit while the row warps, two or four threads a
+// row, turn a step's scores into P, in fp16 over the scores, keep the accumulator in the
+// row's power of two, and write the outputs.  Steps go from the row's own keys backwards,
+// where scores only shrink by the decay, so that the first one nearly always sets that
+// power.  What bounds it is the chain of hand-overs between the roles, each of which takes
+// longer than its products: hence steps of 128 keys (64 were 10 to 20 % slower), whole steps a
+// stage where they fit, and one elected thread for the copies and one for the MMAs (in a branch
+// of `lane == 0` the compiler does not know that it is one).
 template <int D>
-__global__ void __launch_bounds__(kOutThreads, 2)
+__global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
     linear_out_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {
     using S = OutShape<D>;
     const LinearParams& p = c.lin;
@@ -541,8 +551,8 @@ __global__ void __launch_bounds__(kOutThreads, 2)
     if (t == 0) {
         *failed = 0;
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bar(i), i == kBarP || i == kBarRead ? kOutRowWarps
-                              : i == kBarUnitFree || i == kBarUnitFree + 1 ? kOutRowWarps + 1
+            mbar_init(bar(i), i == kBarP || i == kBarRead                      ? S::kRowWarps
+                              : i == kBarUnitFree || i == kBarUnitFree + 1 ? S::kRowWarps + 1
                                                                            : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -554,28 +564,21 @@ __global__ void __launch_bounds__(kOutThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot, t_out = tmem, t_s = tmem + S::kCols;
+    const uint32_t tmem = *tslot, t_out = tmem, t_s = tmem + D;
     const unsigned limit = c.wait_limit;
-    constexpr int kKStages = D / S::kCols;  // stages of a key tile
     auto fail = [&] {
         *failed = 1;
         atomicOr(p.status, PA_DEV_TIMEOUT);
     };
-    // A unit's steps are of 128 keys, the last ones first: half + 1 of them, of two key tiles, but for
-    // the first one's, which may be one.
-    auto step_tiles = [](int half, int tiles, int j) { return j > 0 ? 2 : tiles - 2 * half; };
-    // whether the rows change a step's V tiles before they are multiplied (see there)
-    auto cleaned = [](bool dirty, int count, int tiles, int j) { return dirty || (j == 0 && tiles * 64 > count); };
-    // ring stage of a step's first V tile, counted from the unit's first stage
-    auto v_stage = [&](const OutUnit& u, int j) {
-        const int n0 = u.tiles - 2 * u.half;
-        return kKStages * n0 + (u.inter ? D / 64 : 0) + (j > 0 ? n0 + 2 * kKStages : 0);
-    };
+    // A unit's steps are of 128 keys, the last ones first: half + 1 of them.  Whether the rows change a
+    // step's V before it is multiplied (see there):
+    auto cleaned = [](bool dirty, int count, int half, int j) { return dirty || (j == 0 && count < half * 128 + 128); };
+    constexpr int kStateStages = D / S::kStateRows;
 
-    if (warp == kOutRowWarps + 1) {
+    if (warp == S::kRowWarps + 1) {
         int n = 0, slot = 0, turn = 0;  // stages; the next one's slot of the ring and its phase
         bool ok = true;
-        const unsigned total = (unsigned)c.blocks * K * G * S::kSplits * 2;
+        const unsigned total = (unsigned)c.blocks * K * G * 2;
         int done = 0, q_tiles = 0;  // units; Q tiles
         // The next unit of the CTA, from number x on; what it takes from memory is asked for at once, and a unit
         // ahead of when it is needed.
@@ -586,98 +589,91 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                 unsigned y = x;
                 u.half = y % 2;
                 y /= 2;
-                u.split = y % S::kSplits;
-                y /= S::kSplits;
                 const int h = y % G;
                 y /= G;
                 u.kvh = y % K;
                 u.head = u.kvh * G + h;
                 u.index = (int)y;  // (number * K + kvh)
                 const int4 info = __ldg(c.block_info + y / K);
-                u.dirty = __ldg(c.any_bad + (size_t)y * S::kSplits + u.split);
+                u.dirty = 0;
+#pragma unroll
+                for (int i = 0; i < AddShape<D>::kTiles; ++i) u.dirty |= __ldg(c.any_bad + (size_t)y * AddShape<D>::kTiles + i);
                 u.exponent = __ldg(c.exponents + y);
                 u.l2 = fmaxf(__ldg(p.log_decay + u.kvh) * kLog2e, -1e6f);
                 u.first = info.x;
                 u.inter = info.z;
                 if (u.half * 128 >= info.y) continue;
                 u.count = info.y;
-                u.tiles = (min(u.count, u.half * 128 + 128) - 1) / 64 + 1;
                 break;
             }
             return u;
         };
         unsigned x = blockIdx.x;
         OutUnit coming = unit_at(x);
-        for (;;) {
-            const OutUnit u = coming;
-            if (u.count > 0) {
-                x += gridDim.x;
-                coming = unit_at(x);
-            }
-            if (tc_elect()) {
-                const int s = done & 1;
-                if (done >= 2) ok = ok && tc_wait(bar(kBarUnitFree + s), ((done - 2) >> 1) & 1, limit, failed);
-                if (ok) {
-                    units[s] = u;
-                    mbar_arrive(bar(kBarUnit + s));
-                }
-                if (ok && u.count > 0) {
-                    auto stage = [&](const CUtensorMap* map, int y, int z, int ch) {
-                        if (!ok) return;
-                        if (n >= S::kSlots && !(ok = tc_wait(bar(kBarEmpty + slot), turn ^ 1, limit, failed))) return;
-                        const uint32_t full = bar(kBarFull + slot);
-                        mbar_arrive_expect_tx(full, S::kStageBytes);
-                        tc_tma_load_4d(smem_addr(ring) + slot * S::kStageBytes, map, 0, y, z, ch, full);
-                        ++n;
-                        if (++slot == S::kSlots) {
-                            slot = 0;
-                            turn ^= 1;
-                        }
-                    };
-                    auto k_tiles = [&](int j) {
-                        for (int y = 0; y < step_tiles(u.half, u.tiles, j); ++y)
-                            for (int ch = 0; ch < kKStages; ++ch)
-                                stage(&maps.k, u.kvh, u.first + (u.half - j) * 128 + y * 64, ch * (S::kCols / 64));
-                    };
-                    if (done >= 1) ok = tc_wait(bar(kBarQFree), (done - 1) & 1, limit, failed);
-                    if (ok) {
-                        mbar_arrive_expect_tx(bar(kBarQ), S::kQBytes);
-                        tc_tma_load_4d(smem_addr(qs), &maps.q, 0, u.head, u.first + u.half * 128, 0, bar(kBarQ));
-                        ++q_tiles;
-                    }
-                    k_tiles(0);
-                    if (u.inter)
-                        for (int d = 0; d < D / 64; ++d) stage(&maps.starts, 0, u.index * D + d * 64, u.split * (S::kCols / 64));
-                    for (int j = 0; j <= u.half; ++j) {
-                        if (j > 0) k_tiles(j);
-                        for (int y = 0; y < step_tiles(u.half, u.tiles, j); ++y)
-                            stage(&maps.v, u.kvh, u.first + (u.half - j) * 128 + y * 64, u.split * (S::kCols / 64));
-                    }
-                }
-                if (!ok) fail();
-            }
-            ok = __shfl_sync(kFull, ok, 0);
-            if (!ok || u.count == 0) break;
-            ++done;
-        }
         if (tc_elect()) {
+            for (;;) {
+                const OutUnit u = coming;
+                if (u.count > 0) {
+                    x += gridDim.x;
+                    coming = unit_at(x);
+                }
+                const int s = done & 1;
+                if (done >= 2 && !(ok = tc_wait(bar(kBarUnitFree + s), ((done - 2) >> 1) & 1, limit, failed))) break;
+                units[s] = u;
+                mbar_arrive(bar(kBarUnit + s));
+                if (u.count == 0) break;
+                auto stage = [&](const CUtensorMap* map, int y, int z, int bytes) {
+                    if (!ok || (n >= S::kSlots && !(ok = tc_wait(bar(kBarEmpty + slot), turn ^ 1, limit, failed)))) return;
+                    const uint32_t full = bar(kBarFull + slot);
+                    mbar_arrive_expect_tx(full, bytes);
+                    tc_tma_load_4d(smem_addr(ring) + slot * S::kStageBytes, map, 0, y, z, 0, full);
+                    ++n;
+                    if (++slot == S::kSlots) {
+                        slot = 0;
+                        turn ^= 1;
+                    }
+                };
+                auto step = [&](const CUtensorMap* map, int j) {
+#pragma unroll
+                    for (int y = 0; y < S::kStepStages; ++y)
+                        stage(map, u.kvh, u.first + (u.half - j) * 128 + y * S::kStageRows, S::kStageBytes);
+                };
+                if (done >= 1 && !(ok = tc_wait(bar(kBarQFree), (done - 1) & 1, limit, failed))) break;
+                mbar_arrive_expect_tx(bar(kBarQ), S::kQBytes);
+                tc_tma_load_4d(smem_addr(qs), &maps.q, 0, u.head, u.first + u.half * 128, 0, bar(kBarQ));
+                ++q_tiles;
+#pragma unroll 1
+                for (int j = 0; j <= u.half; ++j) {
+                    step(&maps.k, j);
+                    if (j == 0 && u.inter)
+#pragma unroll
+                        for (int d = 0; d < kStateStages; ++d)
+                            stage(&maps.starts, 0, u.index * D + d * S::kStateRows, S::kStateRows * D * 2);
+                    step(&maps.v, j);
+                }
+                if (!ok) break;
+                ++done;
+            }
+            if (!ok) fail();
             // every copy lands before the CTA's memory is given back
             if (q_tiles > 0) mbar_wait(bar(kBarQ), (q_tiles - 1) & 1, kDefaultWaitLimit);
             for (int i = max(0, n - S::kSlots); i < n; ++i)
                 mbar_wait(bar(kBarFull + i % S::kSlots), (i / S::kSlots) & 1, kDefaultWaitLimit);
         }
         __syncwarp();
-    } else if (warp == kOutRowWarps) {
+    } else if (warp == S::kRowWarps) {
         if (tc_elect()) {
-            constexpr uint32_t id_s = tc_idesc(128, 64, 0), id_o = tc_idesc(128, S::kCols, 1);
-            const uint64_t qdesc = tc_desc(smem_addr(qs), 16, 1024);
-            const uint64_t kdesc = tc_desc(smem_addr(ring), 16, 1024), vdesc = tc_desc(smem_addr(ring), 64 * 128, 1024);
-            int slot = 0, turn = 0;   // of the ring: the next stage's slot, and its phase
-            int x = 0, inters = 0;    // steps, units with a state
+            constexpr uint32_t id_s = tc_idesc(128, S::kStageRows, 0), id_o = tc_idesc(128, D, 1);
+            const uint64_t qdesc = tc_desc(smem_addr(qs), 16, 1024), kdesc = tc_desc(smem_addr(ring), 16, 1024);
+            // columns of V and of the state 64 at a time, one 64-column chunk behind the other
+            const uint64_t vdesc = tc_desc(smem_addr(ring), S::kStageRows * 128, 1024);
+            const uint64_t sdesc = tc_desc(smem_addr(ring), S::kStateRows * 128, 1024);
+            int slot = 0, turn = 0;  // of the ring: the next stage's slot, and its phase
+            int x = 0, inters = 0;   // steps, units with a state
             bool ok = true;
             auto wait = [&](int b, int parity) { return ok = ok && tc_wait(bar(b), parity & 1, limit, failed); };
             auto landed = [&] { return wait(kBarFull + slot, turn); };
-            auto stage_at = [&] { return (uint64_t)(slot * (S::kStageBytes >> 4)); };
+            auto at = [&] { return (uint64_t)(slot * (S::kStageBytes >> 4)); };
             auto release = [&] {
                 tc_commit(bar(kBarEmpty + slot));
                 if (++slot == S::kSlots) {
@@ -688,30 +684,25 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             for (int done = 0;; ++done) {
                 const int s = done & 1;
                 if (!wait(kBarUnit + s, done >> 1)) break;
-                const int count = units[s].count, tiles = units[s].tiles, half = units[s].half;
+                const int count = units[s].count, half = units[s].half;
                 const bool inter = units[s].inter, dirty = units[s].dirty;
                 mbar_arrive(bar(kBarUnitFree + s));
                 if (count == 0) break;
                 if (!wait(kBarQ, done)) break;
 #pragma unroll 1
                 for (int j = 0; j <= half; ++j, ++x) {
-                    const int mine = step_tiles(half, tiles, j);
                     // scores over the P that P V has read
                     if (x > 0 && !wait(kBarPV, x - 1)) break;
-#pragma unroll 1
-                    for (int y = 0; y < mine; ++y) {
 #pragma unroll
-                        for (int ch = 0; ch < kKStages; ++ch) {
-                            if (!landed()) break;
-                            tc_fence_after();
-                            const uint64_t kd = kdesc + stage_at();
+                    for (int y = 0; y < S::kStepStages; ++y) {
+                        if (!landed()) break;
+                        tc_fence_after();
+                        const uint64_t kd = kdesc + at();
 #pragma unroll
-                            for (int i = 0; i < S::kCols / 16; ++i)
-                                tc_mma_ss(t_s + y * 64,
-                                          qdesc + (uint64_t)(((ch * (S::kCols / 64) + (i >> 2)) * (128 * 128) + (i & 3) * 32) >> 4),
-                                          kd + (uint64_t)(((i >> 2) * (64 * 128) + (i & 3) * 32) >> 4), id_s, ch > 0 || i > 0);
-                            release();
-                        }
+                        for (int i = 0; i < D / 16; ++i)
+                            tc_mma_ss(t_s + y * S::kStageRows, qdesc + (uint64_t)(((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4),
+                                      kd + (uint64_t)(((i >> 2) * (S::kStageRows * 128) + (i & 3) * 32) >> 4), id_s, i > 0);
+                        release();
                     }
                     if (!ok) break;
                     tc_commit(bar(kBarScores));
@@ -719,12 +710,14 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                         // the accumulator's last outputs have been read
                         if (done >= 1 && !wait(kBarRead, done - 1)) break;
 #pragma unroll 1
-                        for (int d = 0; d < D / 64 && landed(); ++d) {
+                        for (int d = 0; d < kStateStages && landed(); ++d) {
                             tc_fence_after();
-                            const uint64_t qd = qdesc + (uint64_t)((d * (128 * 128)) >> 4), sd = vdesc + stage_at();
+                            const uint64_t sd = sdesc + at();
+                            const uint64_t qd = qdesc + (uint64_t)((d * (S::kStateRows / 64) * (128 * 128)) >> 4);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                tc_mma_ss(t_out, qd + (uint64_t)((i * 32) >> 4), sd + (uint64_t)((i * 2048) >> 4), id_o, d > 0 || i > 0);
+                            for (int i = 0; i < S::kStateRows / 16; ++i)
+                                tc_mma_ss(t_out, qd + (uint64_t)(((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4),
+                                          sd + (uint64_t)((i * 2048) >> 4), id_o, d > 0 || i > 0);
                             release();
                         }
                         if (!ok) break;
@@ -733,9 +726,12 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     }
                     if (j == half) tc_commit(bar(kBarQFree));
                     // (the rows cannot tell a ring slot's phases apart: they may be two behind)
-                    if (cleaned(dirty, count, tiles, j)) {
-                        const bool wraps = slot + mine - 1 >= S::kSlots;  // (the second one's slot)
-                        if (!landed() || !wait(kBarFull + slot + mine - 1 - (wraps ? S::kSlots : 0), turn ^ (int)wraps)) break;
+                    if (cleaned(dirty, count, half, j)) {
+                        if (!landed()) break;
+                        if (S::kStepStages == 2) {
+                            const bool wraps = slot + 1 == S::kSlots;
+                            if (!wait(kBarFull + (wraps ? 0 : slot + 1), turn ^ (int)wraps)) break;
+                        }
                         mbar_arrive(bar(kBarV));
                     }
                     // (rows that have written P have read the last outputs too)
@@ -743,14 +739,20 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     // Q S, whose operand comes from shared memory, is done before P V, whose comes from
                     // tensor memory, adds to it: nothing orders the two kinds in the tensor cores
                     if (j == 0 && inter && !wait(kBarInter, inters - 1)) break;
-#pragma unroll 1
-                    for (int y = 0; y < mine && landed(); ++y) {
-                        tc_fence_after();
-                        const uint64_t vd = vdesc + stage_at();
+                    const uint32_t add = inter || j > 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc_mma_ts(t_out, t_s + y * 64 + i * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
-                                      inter || j > 0 || y > 0 || i > 0);
+                    for (int y = 0; y < S::kStepStages; ++y) {
+                        if (!landed()) break;
+                        tc_fence_after();
+                        const uint64_t vd = vdesc + at();
+#pragma unroll
+                        for (int i = 0; i < S::kStageRows / 16; ++i) {
+                            // each of a row's threads has its P over its own 128 / kSides scores
+                            constexpr int kPer = 8 / S::kSides;
+                            const int k = y * (S::kStageRows / 16) + i;
+                            tc_mma_ts(t_out, t_s + k / kPer * (128 / S::kSides) + k % kPer * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
+                                      k > 0 ? 1u : add);
+                        }
                         release();
                     }
                     if (!ok) break;
@@ -764,16 +766,16 @@ __global__ void __launch_bounds__(kOutThreads, 2)
         }
         __syncwarp();
     } else {
-        // Warps w and w + 4 have the same 32 rows (tensor memory gives a warp those of its number
-        // modulo 4), each half of the keys of a tile and half of the outputs' columns.
+        // Warps w, w + 4, ... have the same 32 rows (tensor memory gives a warp those of its number
+        // modulo 4), each a share of a step's keys and of the outputs' columns.
         const int quarter = warp & 3, side = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        constexpr int kMine = S::kCols / 2;  // columns of the outputs
-        const uint32_t acc = t_out + lanes + side * kMine;
+        constexpr int kMine = D / S::kSides, kKeys = 128 / S::kSides;
+        const uint32_t acc = t_out + lanes + side * kMine, own = t_s + lanes + side * kKeys;
         bool ok = true;
         int x = 0, inters = 0;  // steps; units with a state
-        int stages = 0;         // ring stages of earlier units
-        int cleans = 0;         // V tiles cleaned
+        int stages = 0;         // ring stages of earlier steps
+        int cleans = 0;         // steps whose V was cleaned
         for (int done = 0;; ++done) {
             const int s = done & 1;
             if (!(ok = tc_warp_wait(bar(kBarUnit + s), (done >> 1) & 1, limit, failed))) break;
@@ -790,32 +792,22 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             const float least = u.inter ? state - 60.f : -200.f;  // below which the state's part could overflow
             float pending = u.inter ? state - level : 0.f;        // by how much the accumulator is behind
             bool set = false;
-            auto rescale = [&](float f) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < kMine; c0 += 32) {
-                    uint32_t o[32];
-                    tc_ld32(acc + c0, o);
-#pragma unroll
-                    for (int v = 0; v < 32; v += 2) mul2(o[v], o[v + 1], f, f);
-                    tc_st32(acc + c0, o);
-                }
-            };
             float within[8];  // decays inside a group of 8 keys
 #pragma unroll
             for (int v = 0; v < 8; ++v) within[v] = tc_ex2(u.l2 * (float)(7 - v));
 #pragma unroll 1
             for (int j = 0; j <= u.half; ++j, ++x) {
-                const int kc = (u.half - j) * 128 + side * 64;  // first key of the warp's half of the step
+                const int kc = (u.half - j) * 128 + side * kKeys;  // first key of the warp's share of the step
                 if (!(ok = tc_warp_wait(bar(kBarScores), x & 1, limit, failed))) break;
                 tc_fence_after();
-                uint32_t pk[32];
+                uint32_t pk[kKeys / 2];
                 // A second time where a row's level has to move: 64 scores a thread kept beside their P would not
                 // fit in its registers.
 #pragma unroll 1
                 for (bool again = false;;) {
                     float m = 0.f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < kKeys / 32; ++h) {
                         const int k0 = kc + h * 32;
                         uint32_t sc[32];
                         if (k0 > row0) {  // keys behind all of the rows
@@ -823,7 +815,7 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                             for (int v = 0; v < 16; ++v) pk[h * 16 + v] = 0u;
                             continue;
                         }
-                        tc_ld32(t_s + lanes + side * 64 + h * 32, sc);
+                        tc_ld32(own + h * 32, sc);
                         // times d^(i - key) 2^-level
                         if (k0 < row0) {
                             // for groups of 8 keys up to the last of them, and the one within
@@ -851,12 +843,14 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                         }
                     }
                     if (again) break;
-                    // the exponent of the row's largest, of both halves (what is not a normal number counts as 0)
-                    uint8_t* mine = largest + (x & 1) * 256 + quarter * 32 + lane;
-                    int e = exponent_of(m);
-                    mine[side * 128] = (uint8_t)(e + 127);
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                    e = max(e, (int)mine[(side ^ 1) * 128] - 127);
+                    // the exponent of the row's largest, of all its threads (what is not a normal number counts as 0)
+                    uint8_t* row = largest + (x & 1) * (S::kSides * 128) + quarter * 32 + lane;
+                    int e = exponent_of(m) + 127;
+                    row[side * 128] = (uint8_t)e;
+                    asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(S::kSides * 32) : "memory");
+#pragma unroll
+                    for (int y = 0; y < S::kSides; ++y) e = max(e, (int)row[y * 128]);
+                    e -= 127;
                     // The level moves where the row's first scores that are not 0 are not of a middling size, and
                     // where later ones would leave fp16.
                     const bool move = e > -127 && (e >= 15 || (!set && e < -4));
@@ -867,9 +861,13 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     pending -= by;
                     again = true;
                 }
-                tc_st32(t_s + lanes + side * 64, pk);  // over the thread's own scores
+                // over the thread's own scores
+                if constexpr (kKeys == 64)
+                    tc_st32(own, pk);
+                else
+                    tc_st16(own, pk);
                 if (__any_sync(kFull, pending != 0.f)) {
-                    // (the accumulator holds nothing before a first tile without a state)
+                    // (the accumulator holds nothing before a first step without a state)
                     if (j == 0 && u.inter) {
                         ok = tc_warp_wait(bar(kBarInter), inters & 1, limit, failed);
                     } else if (j > 0) {
@@ -878,34 +876,44 @@ __global__ void __launch_bounds__(kOutThreads, 2)
                     if (!ok) break;
                     if (j > 0 || u.inter) {
                         tc_fence_after();
-                        rescale(exp2f(pending));
+                        const float f = exp2f(pending);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kMine; c0 += 32) {
+                            uint32_t o[32];
+                            tc_ld32(acc + c0, o);
+#pragma unroll
+                            for (int v = 0; v < 32; v += 2) mul2(o[v], o[v + 1], f, f);
+                            tc_st32(acc + c0, o);
+                        }
                     }
                     pending = 0.f;
                 }
-                if (cleaned(u.dirty, u.count, u.tiles, j)) {
+                const int v_stage = stages + S::kStepStages + (j == 0 && u.inter ? kStateStages : 0);
+                if (cleaned(u.dirty, u.count, u.half, j)) {
                     // V rows behind the block's last token belong to other sequences, and a NaN or
                     // infinity must not meet the zeros of tokens before it: both become 0 (the latter's column
                     // is set from its token on in the end)
                     if (!(ok = tc_warp_wait(bar(kBarV), cleans & 1, limit, failed))) break;
                     ++cleans;
 #pragma unroll 1
-                    for (int y = 0; y < step_tiles(u.half, u.tiles, j); ++y) {
-                        uint8_t* vt = ring + ((stages + v_stage(u, j) + y) % S::kSlots) * S::kStageBytes;
-                        const int k0 = (u.half - j) * 128 + y * 64;
-                        for (int v = t; v < S::kStageBytes / 16; v += kOutRowWarps * 32) {
-                            const int row = (v >> 3) & 63;
-                            uint4* at = reinterpret_cast<uint4*>(vt + (size_t)v * 16);
-                            const uint4 z = *at;
+                    for (int y = 0; y < S::kStepStages; ++y) {
+                        uint8_t* vt = ring + ((v_stage + y) % S::kSlots) * S::kStageBytes;
+                        const int k0 = (u.half - j) * 128 + y * S::kStageRows;
+                        for (int v = t; v < S::kStageBytes / 16; v += S::kRowWarps * 32) {
+                            const int row = (v >> 3) % S::kStageRows;
+                            uint4* cell = reinterpret_cast<uint4*>(vt + (size_t)v * 16);
+                            const uint4 z = *cell;
                             auto clean = [](uint32_t h) {
                                 if ((h & 0x7c00u) == 0x7c00u) h &= 0xffff0000u;
                                 if ((h & 0x7c000000u) == 0x7c000000u) h &= 0xffffu;
                                 return h;
                             };
-                            *at = k0 + row < u.count ? make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w)) : make_uint4(0u, 0u, 0u, 0u);
+                            *cell = k0 + row < u.count ? make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w)) : make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
+                stages = v_stage + S::kStepStages;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarP));
@@ -914,14 +922,14 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             if (!(ok = tc_warp_wait(bar(kBarPV), (x - 1) & 1, limit, failed))) break;
             tc_fence_after();
             const float f = p.scale * exp2f(level);
-            __half* out = p.out + ((size_t)(u.first + i) * H + u.head) * D + u.split * S::kCols + side * kMine;
+            __half* out = p.out + ((size_t)(u.first + i) * H + u.head) * D + side * kMine;
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
             for (int c0 = 0; c0 < kMine; c0 += 32) {
                 uint32_t o[32], y[16];
                 tc_ld32(acc + c0, o);
                 if (u.dirty) {
-                    const int* bad = c.first_bad + (size_t)u.index * D + u.split * S::kCols + side * kMine + c0;
+                    const int* bad = c.first_bad + (size_t)u.index * D + side * kMine + c0;
 #pragma unroll
                     for (int v = 0; v < 32; ++v)
                         if (i >= __ldg(bad + v)) o[v] = 0x7fffffffu;
@@ -937,7 +945,6 @@ __global__ void __launch_bounds__(kOutThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarRead));
             inters += u.inter;
-            stages += v_stage(u, u.half) + step_tiles(u.half, u.tiles, u.half);
         }
         if (!ok && lane == 0) fail();
     }
@@ -980,12 +987,19 @@ cudaError_t out(const LinearChunkParams& prm, const LinearMaps& maps, int num_sm
     });
     if (e != cudaSuccess) return e;
     // An odd number of CTAs, so that each takes first and second halves of blocks in turn.
-    const long long units = (long long)prm.blocks * 2 * prm.lin.num_heads * S::kSplits;
-    const long long room = 2ll * num_sms - 1;
-    return launch(linear_out_kernel<D>, dim3((unsigned)(units < room ? units : room)), kOutThreads, S::kSmem, stream, maps, prm);
+    const long long units = (long long)prm.blocks * 2 * prm.lin.num_heads;
+    const long long room = (long long)S::kCtas * num_sms - (S::kCtas * num_sms % 2 == 0);
+    return launch(linear_out_kernel<D>, dim3((unsigned)(units < room ? units : room)), S::kThreads, S::kSmem, stream, maps, prm);
 }
 
 }  // namespace
+
+void linear_out_boxes(int head_dim, int* rows, int* state_rows) {
+    *rows = head_dim == 256 ? OutShape<256>::kStageRows : head_dim == 128 ? OutShape<128>::kStageRows : OutShape<64>::kStageRows;
+    *state_rows = head_dim == 256   ? OutShape<256>::kStateRows
+                  : head_dim == 128 ? OutShape<128>::kStateRows
+                                    : OutShape<64>::kStateRows;
+}
 
 cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream) {
     switch (head_dim) {

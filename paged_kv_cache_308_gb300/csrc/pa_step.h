@@ -84,10 +84,12 @@ struct LinearChunkParams {
     int blocks;            // numbers of blocks, those of no block among them
     int wait_limit;
 };
-// 64 rows of a tile's columns of k, v and starts; 128 rows of q.
+// 64 rows of a tile's columns of k and v; of all columns 128 rows of q, and of k, v and starts as many as a
+// ring stage of the outputs' kernel has.
 struct LinearMaps {
-    CUtensorMap q, k, v, starts;
+    CUtensorMap k_group, v_group, q, k, v, starts;
 };
+void linear_out_boxes(int head_dim, int* rows, int* state_rows);
 cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
 cudaError_t launch_linear_scan(int head_dim, const LinearChunkParams& prm, cudaStream_t stream);
 cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, int num_sms,

@@ -289,7 +289,7 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     const LinearSpace sp = linear_space(a->num_seqs, a->num_tokens, K, D);
     if (!few) {
         // rows of the tensor maps and CTAs of a grid are 32-bit
-        if (sp.blocks * K * D >= (1ll << 31) || sp.blocks * 2 * a->num_heads * 2 >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+        if (sp.blocks * K * D >= (1ll << 31) || sp.blocks * 2 * a->num_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
         if (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
     }
     p.status = pa::device_status_ptr();
@@ -310,10 +310,14 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK) return PA_ERR_CUDA;
     pa::LinearMaps maps;
-    if ((rc = pa::make_rows_map(&maps.q, a->q, a->num_tokens, a->num_heads, D, 128, D)) ||
-        (rc = pa::make_rows_map(&maps.k, a->k, a->num_tokens, K, D, 64, tile)) ||
-        (rc = pa::make_rows_map(&maps.v, a->v, a->num_tokens, K, D, 64, tile)) ||
-        (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, 64, tile)))
+    int rows, state_rows;
+    pa::linear_out_boxes(D, &rows, &state_rows);
+    if ((rc = pa::make_rows_map(&maps.k_group, a->k, a->num_tokens, K, D, 64, tile)) ||
+        (rc = pa::make_rows_map(&maps.v_group, a->v, a->num_tokens, K, D, 64, tile)) ||
+        (rc = pa::make_rows_map(&maps.q, a->q, a->num_tokens, a->num_heads, D, 128, D)) ||
+        (rc = pa::make_rows_map(&maps.k, a->k, a->num_tokens, K, D, rows, D)) ||
+        (rc = pa::make_rows_map(&maps.v, a->v, a->num_tokens, K, D, rows, D)) ||
+        (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, state_rows, D)))
         return rc;
     if (pa::launch_linear_adds(D, c, maps, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
         pa::launch_linear_out(D, c, maps, num_sms, stream) != cudaSuccess)
