@@ -445,7 +445,7 @@ struct OutShape {
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = kStageRows * D * 2;
     static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 2 : 4;
-    static constexpr int kBars = 13 + 2 * kSlots;
+    static constexpr int kBars = 18 + 2 * kSlots;
     // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by threads
     static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * kSides * 128;
     static constexpr int kSmemNeed = kQBytes + kSlots * kStageBytes + kCtrl;
@@ -480,6 +480,8 @@ enum : int {
     kBarUnitFree = kBarUnit + 2,  // and read by the MMAs' warp and the rows', 2
     kBarDrain = kBarUnitFree + 2,
     kBarV,                        // V tiles that the rows clean have landed
+    kBarSwap,                     // the threads of a quarter of the rows meet, 4
+    kBarOut = kBarSwap + 4,       // the rows are done with the stages that the outputs went through
     kBarFull
 };
 
@@ -493,21 +495,6 @@ __device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, float x, float y)
 __device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
     asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
     return m;
-}
-
-// 32 outputs of a row: 32 bytes (a whole sector) a store where they are aligned so.
-__device__ __forceinline__ void store32(__half* to, const uint32_t (&y)[16], bool wide) {
-#pragma unroll
-    for (int v = 0; v < 16; v += 8) {
-        if (wide) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * v), "r"(y[v]), "r"(y[v + 1]),
-                         "r"(y[v + 2]), "r"(y[v + 3]), "r"(y[v + 4]), "r"(y[v + 5]), "r"(y[v + 6]), "r"(y[v + 7])
-                         : "memory");
-        } else {
-            *reinterpret_cast<uint4*>(to + 2 * v) = make_uint4(y[v], y[v + 1], y[v + 2], y[v + 3]);
-            *reinterpret_cast<uint4*>(to + 2 * v + 8) = make_uint4(y[v + 4], y[v + 5], y[v + 6], y[v + 7]);
-        }
-    }
 }
 
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
@@ -551,7 +538,8 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
     if (t == 0) {
         *failed = 0;
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bar(i), i == kBarP || i == kBarRead                      ? S::kRowWarps
+            mbar_init(bar(i), i == kBarP || i == kBarRead || i == kBarOut  ? S::kRowWarps
+                              : i >= kBarSwap && i < kBarOut               ? S::kSides
                               : i == kBarUnitFree || i == kBarUnitFree + 1 ? S::kRowWarps + 1
                                                                            : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -674,12 +662,15 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             auto wait = [&](int b, int parity) { return ok = ok && tc_wait(bar(b), parity & 1, limit, failed); };
             auto landed = [&] { return wait(kBarFull + slot, turn); };
             auto at = [&] { return (uint64_t)(slot * (S::kStageBytes >> 4)); };
-            auto release = [&] {
-                tc_commit(bar(kBarEmpty + slot));
+            auto next = [&] {
                 if (++slot == S::kSlots) {
                     slot = 0;
                     turn ^= 1;
                 }
+            };
+            auto release = [&] {
+                tc_commit(bar(kBarEmpty + slot));
+                next();
             };
             for (int done = 0;; ++done) {
                 const int s = done & 1;
@@ -753,7 +744,9 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                             tc_mma_ts(t_out, t_s + k / kPer * (128 / S::kSides) + k % kPer * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
                                       k > 0 ? 1u : add);
                         }
-                        release();
+                        // (the unit's last V goes to the rows, who put the outputs there)
+                        if (j < half) tc_commit(bar(kBarEmpty + slot));
+                        next();
                     }
                     if (!ok) break;
                     tc_commit(bar(kBarPV));
@@ -776,6 +769,14 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
         int x = 0, inters = 0;  // steps; units with a state
         int stages = 0;         // ring stages of earlier steps
         int cleans = 0;         // steps whose V was cleaned
+        int swaps = 0;          // meetings of the quarter's warps
+        // (by an mbarrier, whose waits are bounded: a warp that gave up elsewhere would leave others at a hardware
+        // barrier for good)
+        auto meet = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarSwap + quarter));
+            return ok = tc_warp_wait(bar(kBarSwap + quarter), swaps++ & 1, limit, failed);
+        };
         for (int done = 0;; ++done) {
             const int s = done & 1;
             if (!(ok = tc_warp_wait(bar(kBarUnit + s), (done >> 1) & 1, limit, failed))) break;
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                     uint8_t* row = largest + (x & 1) * (S::kSides * 128) + quarter * 32 + lane;
                     int e = exponent_of(m) + 127;
                     row[side * 128] = (uint8_t)e;
-                    asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(S::kSides * 32) : "memory");
+                    if (!meet()) break;
 #pragma unroll
                     for (int y = 0; y < S::kSides; ++y) e = max(e, (int)row[y * 128]);
                     e -= 127;
@@ -861,6 +862,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                     pending -= by;
                     again = true;
                 }
+                if (!ok) break;
                 // over the thread's own scores
                 if constexpr (kKeys == 64)
                     tc_st32(own, pk);
@@ -922,8 +924,16 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             if (!(ok = tc_warp_wait(bar(kBarPV), (x - 1) & 1, limit, failed))) break;
             tc_fence_after();
             const float f = p.scale * exp2f(level);
+            // Whole tiles go out through the memory of the unit's last V stages, which hold as many rows
+            // and columns: 16 bytes a thread by the 128-byte swizzle, then a copy of the warp's 32 rows by
+            // the copy engine.  (Stores of the threads' own rows, 32 rows a warp, kept the
+            // load-store unit busy for a third of the kernel's time.)  In a sequence's last tile,
+            // whose other rows are not its own, each thread stores its row.
+            const bool whole = row0 - quarter * 32 + 128 <= u.count;
+            const int last = (stages - S::kStepStages + quarter * 32 / S::kStageRows) % S::kSlots;
+            uint8_t* tile = ring + last * S::kStageBytes + side * kMine / 64 * (S::kStageRows * 128) +
+                            quarter * 32 % S::kStageRows * 128;
             __half* out = p.out + ((size_t)(u.first + i) * H + u.head) * D + side * kMine;
-            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
             for (int c0 = 0; c0 < kMine; c0 += 32) {
                 uint32_t o[32], y[16];
@@ -939,14 +949,47 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                     mul2(o[2 * v], o[2 * v + 1], f, f);
                     y[v] = half2_bits(__floats2half2_rn(__uint_as_float(o[2 * v]), __uint_as_float(o[2 * v + 1])));
                 }
-                if (i < u.count) store32(out + c0, y, wide);
+                const int unit0 = (side * kMine + c0) % 64 / 8;  // of the row's eight 16-byte units in the chunk
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint4 z = make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+                    if (whole)
+                        *reinterpret_cast<uint4*>(tile + lane * 128 + (((unit0 + v) ^ (lane & 7)) << 4)) = z;
+                    else if (i < u.count)
+                        *reinterpret_cast<uint4*>(out + c0 + 8 * v) = z;
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarRead));
+            if (whole) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                // (at head_dim 64 two warps share the rows' one chunk)
+                __syncwarp();
+                if (kMine == 32 && !meet()) break;
+                if (lane == 0 && (kMine == 64 || side == 0)) {
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
+                        "cp.async.bulk.commit_group;\n\t"
+                        "cp.async.bulk.wait_group.read 0;" ::"l"(&maps.out),
+                        "r"(0), "r"(u.head), "r"(u.first + row0), "r"(side * kMine / 64), "r"(smem_addr(tile))
+                        : "memory");
+                }
+                __syncwarp();
+            }
+            // the stages are free when every warp is done with them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarOut));
+            if (warp == 0) {
+                if (!(ok = tc_warp_wait(bar(kBarOut), done & 1, limit, failed))) break;
+                if (lane == 0)
+                    for (int y = 0; y < S::kStepStages; ++y)
+                        mbar_arrive(bar(kBarEmpty + (stages - S::kStepStages + y) % S::kSlots));
+            }
             inters += u.inter;
         }
         if (!ok && lane == 0) fail();
+        // (the warp's last copies out have read their memory; what they write is there when the grid ends)
     }
     tc_fence_before();
     __syncthreads();  // no copy or MMA is in flight

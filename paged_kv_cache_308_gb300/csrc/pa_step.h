@@ -85,9 +85,9 @@ struct LinearChunkParams {
     int wait_limit;
 };
 // 64 rows of a tile's columns of k and v; of all columns 128 rows of q, and of k, v and starts as many as a
-// ring stage of the outputs' kernel has.
+// ring stage of the outputs' kernel has; 32 rows of 64 columns of out.
 struct LinearMaps {
-    CUtensorMap k_group, v_group, q, k, v, starts;
+    CUtensorMap k_group, v_group, q, k, v, starts, out;
 };
 void linear_out_boxes(int head_dim, int* rows, int* state_rows);
 cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
