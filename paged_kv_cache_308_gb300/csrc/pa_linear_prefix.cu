@@ -481,7 +481,7 @@ enum : int {
     kBarDrain = kBarUnitFree + 2,
     kBarV,                        // V tiles that the rows clean have landed
     kBarSwap,                     // the threads of a quarter of the rows meet, 4
-    kBarOut = kBarSwap + 4,       // the rows are done with the stages that the outputs went through
+    kBarOut = kBarSwap + 4,       // the rows' outputs are in the unit's last V stages
     kBarFull
 };
 
@@ -566,44 +566,87 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
     if (warp == S::kRowWarps + 1) {
         int n = 0, slot = 0, turn = 0;  // stages; the next one's slot of the ring and its phase
         bool ok = true;
-        const unsigned total = (unsigned)c.blocks * K * G * 2;
         int done = 0, q_tiles = 0;  // units; Q tiles
-        // The next unit of the CTA, from number x on; what it takes from memory is asked for at once, and a unit
-        // ahead of when it is needed.
-        auto unit_at = [&](unsigned& x) {
-            OutUnit u;
-            u.count = 0;
-            for (; x < total; x += gridDim.x) {
-                unsigned y = x;
-                u.half = y % 2;
-                y /= 2;
-                const int h = y % G;
-                y /= G;
-                u.kvh = y % K;
-                u.head = u.kvh * G + h;
-                u.index = (int)y;  // (number * K + kvh)
-                const int4 info = __ldg(c.block_info + y / K);
-                u.dirty = 0;
-#pragma unroll
-                for (int i = 0; i < AddShape<D>::kTiles; ++i) u.dirty |= __ldg(c.any_bad + (size_t)y * AddShape<D>::kTiles + i);
-                u.exponent = __ldg(c.exponents + y);
-                u.l2 = fmaxf(__ldg(p.log_decay + u.kvh) * kLog2e, -1e6f);
-                u.first = info.x;
-                u.inter = info.z;
-                if (u.half * 128 >= info.y) continue;
-                u.count = info.y;
-                break;
-            }
-            return u;
-        };
-        unsigned x = blockIdx.x;
-        OutUnit coming = unit_at(x);
         if (tc_elect()) {
+            // The CTA's units are every gridDim.x-th, counted by the halves, the heads of a group, the kv heads and
+            // the blocks, each with a carry (divisions took this thread longer than its copies).
+            auto digits = [&](unsigned x, int& half, int& h, int& kvh, int& number) {
+                half = x % 2;
+                x /= 2;
+                h = x % G;
+                x /= G;
+                kvh = x % K;
+                number = x / K;
+            };
+            int half, h, kvh, number, d_half, d_h, d_kvh, d_number;
+            digits(blockIdx.x, half, h, kvh, number);
+            digits(gridDim.x, d_half, d_h, d_kvh, d_number);
+            // What a unit takes from memory is asked for a unit ahead of when it is needed.
+            int4 info;
+            int dirty, exponent;
+            float decay;
+            auto ask = [&] {
+                if (number >= c.blocks) return;
+                const size_t y = (size_t)number * K + kvh;
+                info = __ldg(c.block_info + number);
+                dirty = __ldg(c.any_bad + y * AddShape<D>::kTiles);
+                if (AddShape<D>::kTiles == 2) dirty |= __ldg(c.any_bad + y * 2 + 1);
+                exponent = __ldg(c.exponents + y);
+                decay = __ldg(p.log_decay + kvh);
+            };
+            auto advance = [&] {
+                half += d_half;
+                h += d_h + (half >> 1);
+                half &= 1;
+                const int c1 = h >= G;
+                h -= c1 ? G : 0;
+                kvh += d_kvh + c1;
+                const int c2 = kvh >= K;
+                kvh -= c2 ? K : 0;
+                number += d_number + c2;
+            };
+            ask();
+            // The last unit's outputs lie in its last V stages (from owed_stage on) until they are copied
+            // out; its stages are then free.
+            bool owed = false, owed_whole = false;
+            int owed_stage = 0, owed_head = 0, owed_row = 0, settled = 0;
+            auto settle = [&] {
+                owed = false;
+                if (!tc_wait(bar(kBarOut), (settled++) & 1, limit, failed)) return false;
+#pragma unroll
+                for (int y = 0; y < S::kStepStages; ++y) {
+                    const int from = (owed_stage + y) % S::kSlots;
+                    if (owed_whole)
+                        asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(&maps.out),
+                                     "r"(0), "r"(owed_head), "r"(owed_row + y * S::kStageRows), "r"(0),
+                                     "r"(smem_addr(ring) + from * S::kStageBytes)
+                                     : "memory");
+                }
+                asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+#pragma unroll
+                for (int y = 0; y < S::kStepStages; ++y) mbar_arrive(bar(kBarEmpty + (owed_stage + y) % S::kSlots));
+                return true;
+            };
             for (;;) {
-                const OutUnit u = coming;
-                if (u.count > 0) {
-                    x += gridDim.x;
-                    coming = unit_at(x);
+                while (number < c.blocks && half * 128 >= info.y) {  // no such half of a block
+                    advance();
+                    ask();
+                }
+                OutUnit u;
+                u.count = 0;
+                if (number < c.blocks) {
+                    u.first = info.x;
+                    u.count = info.y;
+                    u.index = number * K + kvh;
+                    u.half = half;
+                    u.kvh = kvh;
+                    u.head = kvh * G + h;
+                    u.inter = info.z;
+                    u.dirty = dirty;
+                    u.exponent = exponent;
+                    u.l2 = fmaxf(decay * kLog2e, -1e6f);
+                    advance();
+                    ask();
                 }
                 const int s = done & 1;
                 if (done >= 2 && !(ok = tc_wait(bar(kBarUnitFree + s), ((done - 2) >> 1) & 1, limit, failed))) break;
@@ -611,7 +654,11 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                 mbar_arrive(bar(kBarUnit + s));
                 if (u.count == 0) break;
                 auto stage = [&](const CUtensorMap* map, int y, int z, int bytes) {
-                    if (!ok || (n >= S::kSlots && !(ok = tc_wait(bar(kBarEmpty + slot), turn ^ 1, limit, failed)))) return;
+                    if (!ok) return;
+                    if (n >= S::kSlots) {
+                        if (owed && n - S::kSlots == owed_stage && !(ok = settle())) return;
+                        if (!(ok = tc_wait(bar(kBarEmpty + slot), turn ^ 1, limit, failed))) return;
+                    }
                     const uint32_t full = bar(kBarFull + slot);
                     mbar_arrive_expect_tx(full, bytes);
                     tc_tma_load_4d(smem_addr(ring) + slot * S::kStageBytes, map, 0, y, z, 0, full);
@@ -639,9 +686,16 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                             stage(&maps.starts, 0, u.index * D + d * S::kStateRows, S::kStateRows * D * 2);
                     step(&maps.v, j);
                 }
-                if (!ok) break;
+                // (a unit may have fewer stages than the ring has slots)
+                if (!ok || (owed && !(ok = settle()))) break;
+                owed = true;
+                owed_stage = n - S::kStepStages;
+                owed_whole = u.half * 128 + 128 <= u.count;
+                owed_head = u.head;
+                owed_row = u.first + u.half * 128;
                 ++done;
             }
+            if (ok && owed) ok = settle();
             if (!ok) fail();
             // every copy lands before the CTA's memory is given back
             if (q_tiles > 0) mbar_wait(bar(kBarQ), (q_tiles - 1) & 1, kDefaultWaitLimit);
@@ -925,11 +979,11 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             tc_fence_after();
             const float f = p.scale * exp2f(level);
             // Whole tiles go out through the memory of the unit's last V stages, which hold as many rows
-            // and columns: 16 bytes a thread by the 128-byte swizzle, then a copy of the warp's 32 rows by
-            // the copy engine.  (Stores of the threads' own rows, 32 rows a warp, kept the
-            // load-store unit busy for a third of the kernel's time.)  In a sequence's last tile,
-            // whose other rows are not its own, each thread stores its row.
-            const bool whole = row0 - quarter * 32 + 128 <= u.count;
+            // and columns: 16 bytes a thread by the 128-byte swizzle, and from there by the copy engine,
+            // which the copies' warp asks before it loads those stages again.  (Stores of the threads' own
+            // rows, 32 rows a warp, kept the load-store unit busy for a third of the kernel's time.)  In a
+            // sequence's last tile, whose other rows are not its own, each thread stores its row.
+            const bool whole = u.half * 128 + 128 <= u.count;
             const int last = (stages - S::kStepStages + quarter * 32 / S::kStageRows) % S::kSlots;
             uint8_t* tile = ring + last * S::kStageBytes + side * kMine / 64 * (S::kStageRows * 128) +
                             quarter * 32 % S::kStageRows * 128;
@@ -962,34 +1016,12 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarRead));
-            if (whole) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                // (at head_dim 64 two warps share the rows' one chunk)
-                __syncwarp();
-                if (kMine == 32 && !meet()) break;
-                if (lane == 0 && (kMine == 64 || side == 0)) {
-                    asm volatile(
-                        "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
-                        "cp.async.bulk.commit_group;\n\t"
-                        "cp.async.bulk.wait_group.read 0;" ::"l"(&maps.out),
-                        "r"(0), "r"(u.head), "r"(u.first + row0), "r"(side * kMine / 64), "r"(smem_addr(tile))
-                        : "memory");
-                }
-                __syncwarp();
-            }
-            // the stages are free when every warp is done with them
+            if (whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarOut));
-            if (warp == 0) {
-                if (!(ok = tc_warp_wait(bar(kBarOut), done & 1, limit, failed))) break;
-                if (lane == 0)
-                    for (int y = 0; y < S::kStepStages; ++y)
-                        mbar_arrive(bar(kBarEmpty + (stages - S::kStepStages + y) % S::kSlots));
-            }
+            if (lane == 0) mbar_arrive(bar(kBarOut));  // the copies' warp takes it from here
             inters += u.inter;
         }
         if (!ok && lane == 0) fail();
-        // (the warp's last copies out have read their memory; what they write is there when the grid ends)
     }
     tc_fence_before();
     __syncthreads();  // no copy or MMA is in flight

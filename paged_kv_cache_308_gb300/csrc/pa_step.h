@@ -85,7 +85,7 @@ struct LinearChunkParams {
     int wait_limit;
 };
 // 64 rows of a tile's columns of k and v; of all columns 128 rows of q, and of k, v and starts as many as a
-// ring stage of the outputs' kernel has; 32 rows of 64 columns of out.
+// ring stage of the outputs' kernel has, and of out.
 struct LinearMaps {
     CUtensorMap k_group, v_group, q, k, v, starts, out;
 };

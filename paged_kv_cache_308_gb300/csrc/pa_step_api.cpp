@@ -317,7 +317,7 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
         (rc = pa::make_rows_map(&maps.q, a->q, a->num_tokens, a->num_heads, D, 128, D)) ||
         (rc = pa::make_rows_map(&maps.k, a->k, a->num_tokens, K, D, rows, D)) ||
         (rc = pa::make_rows_map(&maps.v, a->v, a->num_tokens, K, D, rows, D)) ||
-        (rc = pa::make_rows_map(&maps.out, a->out, a->num_tokens, a->num_heads, D, 32, 64)) ||
+        (rc = pa::make_rows_map(&maps.out, a->out, a->num_tokens, a->num_heads, D, rows, D)) ||
         (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, state_rows, D)))
         return rc;
     if (pa::launch_linear_adds(D, c, maps, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
