@@ -856,8 +856,9 @@ int pa_linear_decode(const pa_linear_decode_args* args, pa_stream_t stream);
  * range set PA_DEV_BAD_SEQ_LEN and skip the sequence; where query_start_loc is out
  * of order, outputs and states of the whole batch are unspecified.  The workspace
  * needs no initialisation and holds pa_linear_prefix_workspace_size bytes for the
- * same sizes: 0 up to 8 tokens a sequence, else about 6 head_dim^2 num_kv_heads
- * bytes for each of num_seqs + num_tokens / 256 blocks of tokens. */
+ * same sizes: 0 up to 9, 14 or 24 tokens a sequence (head_dim 256, 128, 64), else about
+ * 6 head_dim^2 num_kv_heads bytes for each of num_seqs + num_tokens / 256 blocks of
+ * tokens. */
 typedef struct {
     void* out;
     const void* q;

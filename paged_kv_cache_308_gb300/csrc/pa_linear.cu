@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, G > 4 ? 3 : 4) linear_recurrent_kern
         }
         fresh = context == 0;
     }
-    if (first == last) return;
+    if (first == last || (prm.few > 0 && last - first > prm.few)) return;
     const float g = __ldg(prm.log_decay + kvh);
     if (!(g <= 0.f) && t == 0 && blockIdx.x == 0) atomicOr(prm.status, PA_DEV_BAD_DECAY);
     const Decay dec = decay_of(g);

@@ -36,7 +36,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // floor(log2 |x|) for normal x, -127 for less, 128 for infinities
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
-// A sequence's rows and slot; false where there is nothing to do for it.
+// A sequence's rows and slot; false where there is nothing to do for it here.
 struct Seq {
     int first, count, slot, context;
 };
@@ -51,7 +51,7 @@ __device__ __forceinline__ bool seq_of(const LinearParams& p, int b, Seq& s, uns
     if (s.slot >= p.num_slots) status |= PA_DEV_BAD_BLOCK_ID;
     if (s.first < 0 || last < s.first || last > p.num_tokens || s.count > p.max_query_len || s.context < 0)
         status |= PA_DEV_BAD_SEQ_LEN;
-    return status == 0 && s.count > 0;
+    return status == 0 && s.count > p.few;
 }
 
 // The block of a number: sequence, its place in it, its tokens.  By a whole warp: 32
@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
     const size_t index = (size_t)(s.first / kLinearBlock + b) * p.num_kv_heads + kvh;  // of the first block
     const float4* add = reinterpret_cast<const float4*>(c.adds + index * D * D + at);
     const size_t step = (size_t)p.num_kv_heads * D * D;
-    // four blocks ahead: what a round of the loop waits for has long been asked for
-    constexpr int kAhead = 4;
+    // Eight blocks ahead: what a round of the loop waits for has long been asked for (one prompt of 8192 tokens of 4
+    // x 256, the call: 130.5 us four ahead, 127.0 eight).
+    constexpr int kAhead = 8;
     float4 next[kAhead];
     float most_next[kAhead];
     auto fetch = [&](int n, float4& a, float& most) {

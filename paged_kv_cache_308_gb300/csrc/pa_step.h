@@ -61,6 +61,7 @@ struct LinearParams {
     const int32_t* query_start_loc;  // null: row b is sequence b's one token
     int num_slots, num_seqs, num_tokens, max_query_len;
     int num_heads, num_kv_heads, group;
+    int few;  // > 0: sequences of up to so many tokens go token by token, the others in chunks; 0: all go one way
     float scale;
     unsigned int* status;
 };

@@ -128,8 +128,12 @@ int check_linear_prefix(const pa_linear_prefix_args* a) {
 // sequences take a cluster of one block.
 constexpr int kAllocPlaceTokens = 4096, kAllocOneSeqs = 128;
 
-// Up to so many new tokens a sequence go token by token.
-constexpr int kLinearFewTokens = 8;
+// Up to so many new tokens a sequence go token by token, by head_dim: the calls' us there and in chunks, 1
+// sequence of 24/4 x 256 with 9 tokens 20.6 / 21.3 and 12 tokens 26.6 / 21.1, 64 of them with 9 tokens 139 / 174; of
+// 32/8 x 128 with 12 tokens 16.7 / 16.7, 64 of them with 16 tokens 76 / 100; of 12/12 x 64 with 16 tokens 9.8 / 14.8.
+// In a batch whose longest sequence is above it, those that are not have a launch of their own (about 1.5 us; in
+// chunks, a block's sums cost a token as much as 256).
+int few_tokens(int head_dim) { return head_dim == 256 ? 9 : head_dim == 128 ? 14 : 24; }
 
 // The chunked form's workspace: bytes, offsets (the blocks' sums are at 0).
 struct LinearSpace {
@@ -256,7 +260,7 @@ size_t pa_linear_prefix_workspace_size(int num_seqs, int num_tokens, int max_que
                                        int num_kv_heads, int head_dim) {
     if (num_seqs <= 0 || num_seqs > 65535 || num_tokens <= 0 || num_tokens > kMaxTokens || max_query_len <= 0 ||
         num_heads <= 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
-        (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_query_len <= kLinearFewTokens)
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_query_len <= few_tokens(head_dim))
         return 0;
     return linear_space(num_seqs, num_tokens, num_kv_heads, head_dim).bytes;
 }
@@ -285,7 +289,8 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     p.num_kv_heads = K;
     p.group = a->num_heads / K;
     p.scale = a->scale;
-    const bool few = a->max_query_len <= kLinearFewTokens;
+    const bool few = a->max_query_len <= few_tokens(D);
+    p.few = few || a->num_seqs == 1 ? 0 : few_tokens(D);
     const LinearSpace sp = linear_space(a->num_seqs, a->num_tokens, K, D);
     if (!few) {
         // rows of the tensor maps and CTAs of a grid are 32-bit
@@ -320,6 +325,7 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
         (rc = pa::make_rows_map(&maps.out, a->out, a->num_tokens, a->num_heads, D, rows, D)) ||
         (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, state_rows, D)))
         return rc;
+    if (p.few > 0 && pa::launch_linear_recurrent(D, p, stream) != cudaSuccess) return PA_ERR_CUDA;
     if (pa::launch_linear_adds(D, c, maps, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
         pa::launch_linear_out(D, c, maps, num_sms, stream) != cudaSuccess)
         return PA_ERR_CUDA;

@@ -122,6 +122,9 @@ def linear(q, k, v, s0, g, scale, chunked=True):
 def check(got, want, bound, what=""):
     off = (got.double() - want).abs()
     bad = ~(off <= bound)
+    if got.dtype == torch.float16:
+        # from 65520 on (the largest, 65504, and half of the step of 32 above it) a value rounds to infinity
+        bad &= ~(torch.isinf(got) & (got.double().sign() == want.sign()) & (want.abs() + bound >= 65520.0))
     if bool(bad.any()):
         i = int(torch.argmax(torch.where(bad, off / bound.clamp(min=1e-300), torch.zeros_like(off)).flatten()))
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside; at {i}: {float(got.flatten()[i])} for "
