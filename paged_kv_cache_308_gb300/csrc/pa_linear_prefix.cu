@@ -388,9 +388,17 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
     const size_t index = (size_t)(s.first / kLinearBlock + b) * p.num_kv_heads + kvh;  // of the first block
     const float4* add = reinterpret_cast<const float4*>(c.adds + index * D * D + at);
     const size_t step = (size_t)p.num_kv_heads * D * D;
-    // Eight blocks ahead: what a round of the loop waits for has long been asked for (one prompt of 8192 tokens of 4
-    // x 256, the call: 130.5 us four ahead, 127.0 eight).
-    constexpr int kAhead = 8;
+    // d^L S: next to 1 the factor less 1 is what 32 bits hold
+    float whole, rest;
+    auto set_decay = [&](int tokens) {
+        const float y = fmaxf(g, -1e4f) * (float)tokens;
+        whole = y > -0.5f ? 1.f : 0.f;
+        rest = y > -0.5f ? expm1f(y) : expf(y);
+    };
+    set_decay(kLinearBlock);
+    // four blocks ahead: what a round of the loop waits for has long been asked for (eight: 8 prompts of 8192 tokens of
+    // 8 x 128 43 -> 55 us, one of 4 x 256 20 either way)
+    constexpr int kAhead = 4;
     float4 next[kAhead];
     float most_next[kAhead];
     auto fetch = [&](int n, float4& a, float& most) {
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
         fetch(n + kAhead, slot, most_slot);
         const size_t i = index + (size_t)n * p.num_kv_heads;
         if (n > 0 || s.context > 0) {
-            const int e = bound > 0.f ? max(min(exponent_of(bound) - 8, 100), -100) : 0;
+            const int e = bound > 0.f ? max(min(exponent_of(bound) - 8, 119), -100) : 0;
             const float down = pow2(-e);
             uint2 h;
             h.x = half2_bits(__floats2half2_rn(x.x * down, x.y * down));
@@ -416,9 +424,7 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
             *reinterpret_cast<uint2*>(c.starts + i * D * D + at) = h;
             if (first) c.exponents[i] = e;
         }
-        // d^L S: next to 1 the factor less 1 is what 32 bits hold
-        const float y = fmaxf(g, -1e4f) * (float)min(kLinearBlock, s.count - n * kLinearBlock);
-        const float whole = y > -0.5f ? 1.f : 0.f, rest = y > -0.5f ? expm1f(y) : expf(y);
+        if (n == blocks - 1) set_decay(s.count - n * kLinearBlock);
         auto chain = [&](float v, float plus) { return fmaf(v, rest, v * whole) + plus; };
         x = make_float4(chain(x.x, a.x), chain(x.y, a.y), chain(x.z, a.z), chain(x.w, a.w));
         bound = (bound * (whole + rest) + most) * 1.0001f;

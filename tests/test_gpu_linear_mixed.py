@@ -186,3 +186,12 @@ def test_values_behind_the_last_token_are_not_read(n):
         S.check(c.out[:n], o, ob)
         S.check(c.states[slot], s, sb)
         assert bool((c.out[2 * n + 1:] == 7.0).all())
+
+
+@pytest.mark.parametrize("n", [1, 3, 24, 25, 130])
+def test_one_sequence_far_below_the_bound(n):
+    for dim in (64, 128, 256):
+        c = S.LinearCase([n], 4, 2, dim, seed=44 + n)
+        prefix(c, max_new=5000)
+        assert status() == 0
+        c.check(c.out, c.states)
