@@ -92,34 +92,42 @@ struct AddShape {
     static constexpr int kSlots = 3;
     static constexpr int kRing = kSlots * 2 * kHalf;
     // two CTAs an SM, whose TMEM allocations then always fit
-    static constexpr int kSmem = (kRing > 78 * 1024 ? kRing : 78 * 1024) + 2048 + 1024;
+    static constexpr int kSmem = (kRing > 78 * 1024 ? kRing : 78 * 1024) + 3072 + 1024;
     static constexpr int kTmem = 256;  // the sum, and 64 tokens of v in two halves, twice
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 constexpr int kAddThreads = 6 * 32;
 
-// A CTA has a tile of (128 columns of k) x (128 columns of v) of a block's sum, and
-// takes the block's tokens 64 at a time, the last ones first.  Warp 5 brings them; lane
-// (thread) c of warps 0-3 is a column of v, whose tokens it scales and writes to tensor
+// A tile of (128 columns of k) x (128 columns of v) of a block's sum.
+struct AddUnit {
+    int first, count;  // of the block; count 0: no more units
+    int number, kvh, tile;
+};
+
+// A grid of the CTAs that the SMs hold takes the tiles in turn, a block's tokens 64 at a time, the last ones
+// first.  Warp 5 finds the blocks and brings their tokens, running ahead into the next unit;
+// lane (thread) c of warps 0-3 is a column of v, whose tokens it scales and writes to tensor
 // memory as the MMA's A operand (two halves); warp 4 multiplies by k, the B operand, as TMA
 // laid it out.  The column's power of two is set by the first tokens that are not 0 (the
 // decay makes earlier ones smaller) with room above, and moves, with the column's sum so far,
-// where later ones would not fit.  CTAs past the blocks find the largest entries of the
-// sequences' first states.
+// where later ones would not fit.  The first CTAs find the largest entries of the sequences'
+// first states.
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 2)
     linear_adds_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {
     using S = AddShape<D>;
     const LinearParams& p = c.lin;
+    constexpr int kTiles2 = S::kTiles * S::kTiles;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    float* w = reinterpret_cast<float*>(ring + S::kRing);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(w + kLinearBlock);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 8);
+    float* weights = reinterpret_cast<float*>(ring + S::kRing);  // of the tokens, two units
+    AddUnit* units = reinterpret_cast<AddUnit*>(weights + 2 * kLinearBlock);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(units + 4);  // (two are used: 16-byte multiples)
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
     volatile int* failed = reinterpret_cast<volatile int*>(tslot + 1);
-    int* bad_sm = reinterpret_cast<int*>(tslot + 2);
-    float* red = reinterpret_cast<float*>(tslot + 3);
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, kvh = blockIdx.y, number = blockIdx.x;
+    float* red = reinterpret_cast<float*>(tslot + 2);   // of the warps, two units
+    int* bad_sm = reinterpret_cast<int*>(red + 8);      // as many
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, K = p.num_kv_heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -132,14 +140,15 @@ __global__ void __launch_bounds__(kAddThreads, 2)
         const float a = fabsf(x);
         return a <= 3.402823466e38f ? fmaxf(m, a) : m;
     };
-    if (number >= c.blocks) {
-        const int b = number - c.blocks;
+    const int state_ctas = p.num_seqs * K;
+    if ((int)blockIdx.x < state_ctas) {
+        const int b = blockIdx.x / K, kvh = blockIdx.x % K;
         Seq s;
         unsigned status;
-        if (blockIdx.z != 0 || !seq_of(p, b, s, status)) return;
+        if (!seq_of(p, b, s, status)) return;
         float m = 0.f;
         if (s.context > 0) {
-            const float4* st = reinterpret_cast<const float4*>(p.states + ((size_t)s.slot * p.num_kv_heads + kvh) * D * D);
+            const float4* st = reinterpret_cast<const float4*>(p.states + ((size_t)s.slot * K + kvh) * D * D);
 #pragma unroll 8
             for (int i = t; i < D * D / 4; i += kAddThreads) {
                 const float4 x = st[i];
@@ -151,26 +160,30 @@ __global__ void __launch_bounds__(kAddThreads, 2)
         __syncthreads();
         if (t == 0) {
             for (int i = 1; i < kAddThreads / 32; ++i) m = fmaxf(m, red[i]);
-            c.state_max[(size_t)b * p.num_kv_heads + kvh] = m;
+            c.state_max[(size_t)b * K + kvh] = m;
         }
         return;
     }
-    Block k;
-    const bool real = block_of(p, number, k);
-    if (t == 0 && kvh == 0 && blockIdx.z == 0)
-        c.block_info[number] = real ? make_int4(k.first, k.count, k.n > 0 || k.context > 0, 0) : make_int4(0, 0, 0, 0);
-    if (!real) return;
-    const int k_tile = blockIdx.z / S::kTiles, v_tile = blockIdx.z % S::kTiles;
-    const int groups = (k.count + S::kGroup - 1) / S::kGroup;
-    const uint32_t bar_full = smem_addr(bars), bar_v = bar_full + 8 * S::kSlots, bar_mma = bar_v + 16;
+    // barriers: a stage has landed, has been used; the operand of a group in buffer i is written, has been read;
+    // a unit is in its slot, has been taken from it; the column warps meet; they have read the sums
+    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * S::kSlots, bar_v = bar_empty + 8 * S::kSlots,
+                   bar_mma = bar_v + 16, bar_unit = bar_mma + 16, bar_free = bar_unit + 16, bar_meet = bar_free + 16,
+                   bar_read = bar_meet + 8;
+    static_assert(2 * S::kSlots + 2 + 2 + 2 + 2 + 1 + 1 <= 20, "barriers");
     if (t == 0) {
         *failed = 0;
-        *bad_sm = 0;
-        for (int i = 0; i < S::kSlots; ++i) mbar_init(bar_full + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar_v + 8 * i, 4);    // the operand of a group in buffer i is written
-            mbar_init(bar_mma + 8 * i, 1);  // and has been read
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_v + 8 * i, 4);
+            mbar_init(bar_mma + 8 * i, 1);
+            mbar_init(bar_unit + 8 * i, 1);
+            mbar_init(bar_free + 8 * i, 5);
+        }
+        mbar_init(bar_meet, 4);
+        mbar_init(bar_read, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -178,56 +191,99 @@ __global__ void __launch_bounds__(kAddThreads, 2)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const float g = fmaxf(__ldg(p.log_decay + kvh), -1e4f);  // (whose exp is 0, and 1 for no tokens)
-    for (int i = t; i < kLinearBlock; i += kAddThreads) w[i] = i < k.count ? expf(g * (float)(k.count - 1 - i)) : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot, t_sum = tmem, t_v = tmem + 128;
     const unsigned limit = c.wait_limit;
-    // group x holds the tokens from 64 * (groups - 1 - x) of the block on
-    auto tokens_at = [&](int x) { return (groups - 1 - x) * S::kGroup; };
     auto fail = [&] {
         *failed = 1;
         atomicOr(p.status, PA_DEV_TIMEOUT);
     };
+    // group x of a block holds its tokens from 64 * (groups - 1 - x) on
+    auto groups_of = [](int count) { return (count + S::kGroup - 1) / S::kGroup; };
 
     if (warp == 5) {
-        if (lane == 0) {
-            bool ok = true;
-            int x = 0;
-            for (; x < groups; ++x) {
-                const int s = x % S::kSlots;
-                if (x >= S::kSlots &&
-                    !(ok = tc_wait(bar_mma + 8 * ((x - S::kSlots) & 1), ((x - S::kSlots) >> 1) & 1, limit, failed)))
-                    break;
-                mbar_arrive_expect_tx(bar_full + 8 * s, 2 * S::kHalf);
-                const uint32_t dst = smem_addr(ring + s * 2 * S::kHalf);
-                tc_tma_load_4d(dst, &maps.k_group, 0, kvh, k.first + tokens_at(x), k_tile * (S::kTile / 64), bar_full + 8 * s);
-                tc_tma_load_4d(dst + S::kHalf, &maps.v_group, 0, kvh, k.first + tokens_at(x), v_tile * (S::kTile / 64), bar_full + 8 * s);
+        const unsigned total = (unsigned)c.blocks * K * kTiles2, ctas = gridDim.x - state_ctas;
+        int n = 0, done = 0, last = -1;  // stages; units; the block looked up last
+        bool ok = true, valid = false;
+        Block k;
+        for (unsigned x = blockIdx.x - state_ctas;; x += ctas) {
+            AddUnit u;
+            u.count = 0;
+            if (x < total) {
+                u.tile = x % kTiles2;
+                u.kvh = x / kTiles2 % K;
+                u.number = x / kTiles2 / K;
+                if (u.number != last) valid = block_of(p, u.number, k);
+                last = u.number;
+                if (lane == 0 && u.kvh == 0 && u.tile == 0)
+                    c.block_info[u.number] = valid ? make_int4(k.first, k.count, k.n > 0 || k.context > 0, 0) : make_int4(0, 0, 0, 0);
+                if (!valid) continue;
+                u.first = k.first;
+                u.count = k.count;
             }
+            const int s = done & 1;
+            if (done >= 2 && !(ok = tc_warp_wait(bar_free + 8 * s, ((done - 2) >> 1) & 1, limit, failed))) break;
+            if (lane == 0) {
+                units[s] = u;
+                mbar_arrive(bar_unit + 8 * s);
+            }
+            __syncwarp();
+            if (u.count == 0) break;
+            const int groups = groups_of(u.count), k_tile = u.tile / S::kTiles, v_tile = u.tile % S::kTiles;
+#pragma unroll 1
+            for (int y = 0; y < groups; ++y, ++n) {
+                const int slot = n % S::kSlots;
+                if (n >= S::kSlots && !(ok = tc_warp_wait(bar_empty + 8 * slot, (n / S::kSlots - 1) & 1, limit, failed))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar_full + 8 * slot, 2 * S::kHalf);
+                    const uint32_t dst = smem_addr(ring + slot * 2 * S::kHalf);
+                    const int at = u.first + (groups - 1 - y) * S::kGroup;
+                    tc_tma_load_4d(dst, &maps.k_group, 0, u.kvh, at, k_tile * (S::kTile / 64), bar_full + 8 * slot);
+                    tc_tma_load_4d(dst + S::kHalf, &maps.v_group, 0, u.kvh, at, v_tile * (S::kTile / 64), bar_full + 8 * slot);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            ++done;
+        }
+        if (lane == 0) {
             if (!ok) fail();
             // every copy lands before the CTA's memory is given back
-            for (int i = max(0, x - S::kSlots); i < x; ++i)
+            for (int i = max(0, n - S::kSlots); i < n; ++i)
                 mbar_wait(bar_full + 8 * (i % S::kSlots), (i / S::kSlots) & 1, kDefaultWaitLimit);
         }
         __syncwarp();
     } else if (warp == 4) {
-        if (lane == 0) {
+        if (tc_elect()) {
             constexpr uint32_t id = tc_idesc(128, S::kTile, 1);
             bool ok = true;
-            int x = 0;
-            for (; x < groups; ++x) {
-                // (the rows wait for the group's copies before they write the operand)
-                if (!(ok = tc_wait(bar_v + 8 * (x & 1), (x >> 1) & 1, limit, failed))) break;
-                tc_fence_after();
-                const uint64_t kd = tc_desc(smem_addr(ring + (x % S::kSlots) * 2 * S::kHalf), S::kGroup * 128, 1024);
-                const int steps = (min(k.count - tokens_at(x), S::kGroup) + 15) / 16;
-                for (int part = 1; part >= 0; --part)  // the small halves first
-                    for (int s = 0; s < steps; ++s)
-                        tc_mma_ts(t_sum, t_v + (x & 1) * 64 + part * 32 + s * 8, kd + (uint64_t)((s * 2048) >> 4), id,
-                                  x > 0 || part == 0 || s > 0);
-                tc_commit(bar_mma + 8 * (x & 1));
+            int x = 0;  // groups
+            for (int done = 0; ok; ++done) {
+                const int s = done & 1;
+                if (!(ok = tc_wait(bar_unit + 8 * s, (done >> 1) & 1, limit, failed))) break;
+                const int count = units[s].count;
+                mbar_arrive(bar_free + 8 * s);
+                if (count == 0) break;
+                const int groups = groups_of(count);
+                // the last unit's sums have been read
+                if (done > 0 && !(ok = tc_wait(bar_read, (done - 1) & 1, limit, failed))) break;
+#pragma unroll 1
+                for (int y = 0; y < groups; ++y, ++x) {
+                    // (the columns' threads wait for the group's copies before they write the operand)
+                    if (!(ok = tc_wait(bar_v + 8 * (x & 1), (x >> 1) & 1, limit, failed))) break;
+                    tc_fence_after();
+                    const int slot = x % S::kSlots;
+                    const uint64_t kd = tc_desc(smem_addr(ring + slot * 2 * S::kHalf), S::kGroup * 128, 1024);
+                    const int steps = (min(count - (groups - 1 - y) * S::kGroup, S::kGroup) + 15) / 16;
+                    for (int part = 1; part >= 0; --part)  // the small halves first
+                        for (int i = 0; i < steps; ++i)
+                            tc_mma_ts(t_sum, t_v + (x & 1) * 64 + part * 32 + i * 8, kd + (uint64_t)((i * 2048) >> 4), id,
+                                      y > 0 || part == 0 || i > 0);
+                    tc_commit(bar_empty + 8 * slot);
+                    tc_commit(bar_mma + 8 * (x & 1));
+                }
             }
             if (!ok) fail();
             // every MMA is done before the CTA's memory is given back
@@ -242,88 +298,110 @@ __global__ void __launch_bounds__(kAddThreads, 2)
         auto column = [&](const uint8_t* tile, int i) {
             return __half2float(*reinterpret_cast<const __half*>(tile + i * 128 + ((unit ^ (i & 7)) << 4) + in_unit * 2));
         };
-        int up = 0, first = kLinearBlock;
-        bool set = false, ok = true;
-        for (int x = 0; x < groups; ++x) {
-            const int at = tokens_at(x), count = min(k.count - at, S::kGroup);
-            uint8_t* ks = ring + (x % S::kSlots) * 2 * S::kHalf;
-            const uint8_t* vs = ks + S::kHalf + chunk * (S::kGroup * 128);
-            if (!(ok = tc_warp_wait(bar_full + 8 * (x % S::kSlots), (x / S::kSlots) & 1, limit, failed))) break;
-            // rows of other sequences behind the block's last token: nothing of them, whatever they hold
-            const int tail = (count + 15) / 16 * 16 - count;
-            for (int i = t; i < tail * (S::kTile / 8); i += 128) {
-                const int r = count + i / (S::kTile / 8), u = i % (S::kTile / 8);
-                *reinterpret_cast<uint4*>(ks + (u >> 3) * (S::kGroup * 128) + r * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (tail) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            float a[64];
-            float m = 0.f;
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                const float v = mine && i < count ? column(vs, i) : 0.f;
-                bad |= !(fabsf(v) <= 65504.f);
-                a[i] = v * w[at + i];
-                m = fmaxf(m, fabsf(a[i]));
-            }
-            if (bad) {  // the power of two is that of the others
-                m = 0.f;
-#pragma unroll
-                for (int i = 63; i >= 0; --i) {
-                    const bool there = mine && i < count;
-                    if (there && !(fabsf(column(vs, i)) <= 65504.f))
-                        first = at + i;
-                    else
-                        m = fmaxf(m, fabsf(a[i]));
-                }
-            }
-            const int e = exponent_of(m);
-            const bool move = m > 0.f && (!set || e + up > 14);
-            const int was = up;
-            if (move) up = min(8 - e, 100);
-            if (x >= 2) {  // the operand's buffer has been read
-                if (!(ok = tc_warp_wait(bar_mma + 8 * (x & 1), ((x - 2) >> 1) & 1, limit, failed))) break;
-                tc_fence_after();
-            }
-            if (x > 0 && __any_sync(kFull, move && set)) {
-                if (!(ok = tc_warp_wait(bar_mma + 8 * ((x - 1) & 1), ((x - 1) >> 1) & 1, limit, failed))) break;
-                tc_fence_after();
-                const float f = move && set ? pow2(up - was) : 1.f;
-#pragma unroll 1
-                for (int c0 = 0; c0 < S::kTile; c0 += 32) {
-                    uint32_t o[32];
-                    tc_ld32(t_sum + lanes + c0, o);
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-                    tc_st32(t_sum + lanes + c0, o);
-                }
-            }
-            set |= move;
-            const float raise = pow2(up);
-            uint32_t hi[32], lo[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float y0 = a[2 * i] * raise, y1 = a[2 * i + 1] * raise;
-                const __half2 h = __floats2half2_rn(y0, y1);
-                const float2 back = __half22float2(h);
-                hi[i] = half2_bits(h);
-                lo[i] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
-            }
-            tc_st32x2(t_v + lanes + (x & 1) * 64, hi, t_v + lanes + (x & 1) * 64 + 32, lo);
-            tc_fence_before();
+        bool ok = true;
+        int x = 0, meets = 0;  // groups; meetings of the columns' warps
+        auto meet = [&] {
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_v + 8 * (x & 1));
-        }
-        if (k_tile == 0 && mine) {
-            c.first_bad[((size_t)number * p.num_kv_heads + kvh) * D + v_tile * S::kTile + t] = first;
-            if (first < kLinearBlock) *bad_sm = 1;
-        }
-        if (ok) ok = tc_warp_wait(bar_mma + 8 * ((groups - 1) & 1), ((groups - 1) >> 1) & 1, limit, failed);
-        float m = 0.f;
-        if (ok) {
+            if (lane == 0) mbar_arrive(bar_meet);
+            return ok = tc_warp_wait(bar_meet, meets++ & 1, limit, failed);
+        };
+        for (int done = 0;; ++done) {
+            const int s = done & 1;
+            if (!(ok = tc_warp_wait(bar_unit + 8 * s, (done >> 1) & 1, limit, failed))) break;
+            const AddUnit u = units[s];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_free + 8 * s);
+            if (u.count == 0) break;
+            const int groups = groups_of(u.count), k_tile = u.tile / S::kTiles, v_tile = u.tile % S::kTiles;
+            float* w = weights + s * kLinearBlock;
+            const float g = fmaxf(__ldg(p.log_decay + u.kvh), -1e4f);  // (whose exp is 0, and 1 for no tokens)
+            for (int i = t; i < kLinearBlock; i += 128) w[i] = i < u.count ? expf(g * (float)(u.count - 1 - i)) : 0.f;
+            if (t == 0) bad_sm[s] = 0;
+            if (!meet()) break;  // (who writes these again has met the others, done with this unit, once more)
+            int up = 0, first = kLinearBlock;
+            bool set = false;
+#pragma unroll 1
+            for (int y = 0; y < groups; ++y, ++x) {
+                const int at = (groups - 1 - y) * S::kGroup, count = min(u.count - at, S::kGroup);
+                uint8_t* ks = ring + (x % S::kSlots) * 2 * S::kHalf;
+                const uint8_t* vs = ks + S::kHalf + chunk * (S::kGroup * 128);
+                if (!(ok = tc_warp_wait(bar_full + 8 * (x % S::kSlots), (x / S::kSlots) & 1, limit, failed))) break;
+                // rows of other sequences behind the block's last token: nothing of them, whatever they hold
+                const int tail = (count + 15) / 16 * 16 - count;
+                for (int i = t; i < tail * (S::kTile / 8); i += 128) {
+                    const int r = count + i / (S::kTile / 8), q = i % (S::kTile / 8);
+                    *reinterpret_cast<uint4*>(ks + (q >> 3) * (S::kGroup * 128) + r * 128 + (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (tail) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                float a[64];
+                float m = 0.f;
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    const float v = mine && i < count ? column(vs, i) : 0.f;
+                    bad |= !(fabsf(v) <= 65504.f);
+                    a[i] = v * w[at + i];
+                    m = fmaxf(m, fabsf(a[i]));
+                }
+                if (bad) {  // the power of two is that of the others
+                    m = 0.f;
+#pragma unroll
+                    for (int i = 63; i >= 0; --i) {
+                        const bool there = mine && i < count;
+                        if (there && !(fabsf(column(vs, i)) <= 65504.f))
+                            first = at + i;
+                        else
+                            m = fmaxf(m, fabsf(a[i]));
+                    }
+                }
+                const int e = exponent_of(m);
+                const bool move = m > 0.f && (!set || e + up > 14);
+                const int was = up;
+                if (move) up = min(8 - e, 100);
+                if (x >= 2) {  // the operand's buffer has been read
+                    if (!(ok = tc_warp_wait(bar_mma + 8 * (x & 1), ((x - 2) >> 1) & 1, limit, failed))) break;
+                    tc_fence_after();
+                }
+                if (y > 0 && __any_sync(kFull, move && set)) {
+                    if (!(ok = tc_warp_wait(bar_mma + 8 * ((x - 1) & 1), ((x - 1) >> 1) & 1, limit, failed))) break;
+                    tc_fence_after();
+                    const float f = move && set ? pow2(up - was) : 1.f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < S::kTile; c0 += 32) {
+                        uint32_t o[32];
+                        tc_ld32(t_sum + lanes + c0, o);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                        tc_st32(t_sum + lanes + c0, o);
+                    }
+                }
+                set |= move;
+                const float raise = pow2(up);
+                uint32_t hi[32], lo[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float y0 = a[2 * i] * raise, y1 = a[2 * i + 1] * raise;
+                    const __half2 h = __floats2half2_rn(y0, y1);
+                    const float2 back = __half22float2(h);
+                    hi[i] = half2_bits(h);
+                    lo[i] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
+                }
+                tc_st32x2(t_v + lanes + (x & 1) * 64, hi, t_v + lanes + (x & 1) * 64 + 32, lo);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_v + 8 * (x & 1));
+            }
+            if (!ok) break;
+            const size_t index = (size_t)u.number * K + u.kvh;
+            if (k_tile == 0 && mine) {
+                c.first_bad[index * D + v_tile * S::kTile + t] = first;
+                if (first < kLinearBlock) bad_sm[s] = 1;
+            }
+            if (!(ok = tc_warp_wait(bar_mma + 8 * ((x - 1) & 1), ((x - 1) >> 1) & 1, limit, failed))) break;
             tc_fence_after();
+            float m = 0.f;
             const float lower = pow2(-up);
-            float* dst = c.adds + (((size_t)number * p.num_kv_heads + kvh) * D + k_tile * S::kTile) * D + v_tile * S::kTile + t;
+            float* dst = c.adds + (index * D + k_tile * S::kTile) * D + v_tile * S::kTile + t;
 #pragma unroll 1
             for (int c0 = 0; c0 < S::kTile; c0 += 32) {
                 uint32_t o[32];
@@ -331,25 +409,28 @@ __global__ void __launch_bounds__(kAddThreads, 2)
                 if (mine) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float y = __uint_as_float(o[i]) * lower;
-                        m = finite_max(m, y);
-                        dst[(size_t)(c0 + i) * D] = y;
+                        const float z = __uint_as_float(o[i]) * lower;
+                        m = finite_max(m, z);
+                        dst[(size_t)(c0 + i) * D] = z;
                     }
                 }
             }
-        } else if (lane == 0) {
-            fail();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_read);
+            m = warp_max(m);
+            if (lane == 0) red[s * 4 + warp] = m;
+            if (!meet()) break;
+            if (t == 0) {
+                const float* r = red + s * 4;
+                c.add_max[index * kTiles2 + u.tile] = fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
+                if (k_tile == 0) c.any_bad[index * S::kTiles + v_tile] = bad_sm[s];
+            }
         }
-        m = warp_max(m);
-        if (lane == 0) red[warp] = m;
+        if (!ok && lane == 0) fail();
     }
     tc_fence_before();
-    __syncthreads();
-    if (t == 0) {
-        const size_t index = (size_t)number * p.num_kv_heads + kvh;
-        c.add_max[index * (S::kTiles * S::kTiles) + blockIdx.z] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        if (k_tile == 0) c.any_bad[index * S::kTiles + v_tile] = *bad_sm;
-    }
+    __syncthreads();  // no copy or MMA is in flight
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem));
 }
 
@@ -452,7 +533,7 @@ struct OutShape {
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = kStageRows * D * 2;
     static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 2 : 4;
-    static constexpr int kBars = 18 + 2 * kSlots;
+    static constexpr int kBars = 19 + 2 * kSlots;
     // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by threads
     static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * kSides * 128;
     static constexpr int kSmemNeed = kQBytes + kSlots * kStageBytes + kCtrl;
@@ -488,8 +569,9 @@ enum : int {
     kBarDrain = kBarUnitFree + 2,
     kBarV,                        // V tiles that the rows clean have landed
     kBarSwap,                     // the threads of a quarter of the rows meet, 4
-    kBarOut = kBarSwap + 4,       // the rows' outputs are in the unit's last V stages
-    kBarFull
+    kBarOut = kBarSwap + 4,       // a unit's outputs are in its last V stages, 2 (in turn: the unit after the next
+                                  // starts when this one's have gone)
+    kBarFull = kBarOut + 2
 };
 
 // Products of two numbers at a time (one instruction), and the larger magnitude of three.
@@ -545,7 +627,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
     if (t == 0) {
         *failed = 0;
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bar(i), i == kBarP || i == kBarRead || i == kBarOut  ? S::kRowWarps
+            mbar_init(bar(i), i == kBarP || i == kBarRead || i == kBarOut || i == kBarOut + 1 ? S::kRowWarps
                               : i >= kBarSwap && i < kBarOut               ? S::kSides
                               : i == kBarUnitFree || i == kBarUnitFree + 1 ? S::kRowWarps + 1
                                                                            : 1);
@@ -619,7 +701,8 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             int owed_stage = 0, owed_head = 0, owed_row = 0, settled = 0;
             auto settle = [&] {
                 owed = false;
-                if (!tc_wait(bar(kBarOut), (settled++) & 1, limit, failed)) return false;
+                if (!tc_wait(bar(kBarOut + (settled & 1)), (settled >> 1) & 1, limit, failed)) return false;
+                ++settled;
 #pragma unroll
                 for (int y = 0; y < S::kStepStages; ++y) {
                     const int from = (owed_stage + y) % S::kSlots;
@@ -1025,7 +1108,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             if (lane == 0) mbar_arrive(bar(kBarRead));
             if (whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarOut));  // the copies' warp takes it from here
+            if (lane == 0) mbar_arrive(bar(kBarOut + s));  // the copies' warp takes it from here
             inters += u.inter;
         }
         if (!ok && lane == 0) fail();
@@ -1049,15 +1132,16 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStr
 }
 
 template <int D>
-cudaError_t adds(const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream) {
+cudaError_t adds(const LinearChunkParams& prm, const LinearMaps& maps, int num_sms, cudaStream_t stream) {
     using S = AddShape<D>;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(linear_adds_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    return launch(linear_adds_kernel<D>, dim3(prm.blocks + prm.lin.num_seqs, prm.lin.num_kv_heads, S::kTiles * S::kTiles),
-                  kAddThreads, S::kSmem, stream, maps, prm);
+    const long long units = (long long)prm.blocks * prm.lin.num_kv_heads * S::kTiles * S::kTiles, room = 2ll * num_sms;
+    const unsigned grid = (unsigned)prm.lin.num_seqs * prm.lin.num_kv_heads + (unsigned)(units < room ? units : room);
+    return launch(linear_adds_kernel<D>, dim3(grid), kAddThreads, S::kSmem, stream, maps, prm);
 }
 
 template <int D>
@@ -1083,11 +1167,12 @@ void linear_out_boxes(int head_dim, int* rows, int* state_rows) {
                                     : OutShape<64>::kStateRows;
 }
 
-cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream) {
+cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, int num_sms,
+                               cudaStream_t stream) {
     switch (head_dim) {
-        case 64: return adds<64>(prm, maps, stream);
-        case 128: return adds<128>(prm, maps, stream);
-        case 256: return adds<256>(prm, maps, stream);
+        case 64: return adds<64>(prm, maps, num_sms, stream);
+        case 128: return adds<128>(prm, maps, num_sms, stream);
+        case 256: return adds<256>(prm, maps, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

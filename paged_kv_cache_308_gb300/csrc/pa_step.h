@@ -91,7 +91,8 @@ struct LinearMaps {
     CUtensorMap k_group, v_group, q, k, v, starts, out;
 };
 void linear_out_boxes(int head_dim, int* rows, int* state_rows);
-cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, cudaStream_t stream);
+cudaError_t launch_linear_adds(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, int num_sms,
+                               cudaStream_t stream);
 cudaError_t launch_linear_scan(int head_dim, const LinearChunkParams& prm, cudaStream_t stream);
 cudaError_t launch_linear_out(int head_dim, const LinearChunkParams& prm, const LinearMaps& maps, int num_sms,
                               cudaStream_t stream);

@@ -294,7 +294,7 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
     const LinearSpace sp = linear_space(a->num_seqs, a->num_tokens, K, D);
     if (!few) {
         // rows of the tensor maps and CTAs of a grid are 32-bit
-        if (sp.blocks * K * D >= (1ll << 31) || sp.blocks * 2 * a->num_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+        if (sp.blocks * K * D >= (1ll << 31) || sp.blocks * 4 * a->num_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
         if (!ws || ws_bytes < sp.bytes || !aligned(ws, kWsAlign)) return PA_ERR_WORKSPACE;
     }
     p.status = pa::device_status_ptr();
@@ -326,7 +326,7 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
         (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, state_rows, D)))
         return rc;
     if (p.few > 0 && pa::launch_linear_recurrent(D, p, stream) != cudaSuccess) return PA_ERR_CUDA;
-    if (pa::launch_linear_adds(D, c, maps, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
+    if (pa::launch_linear_adds(D, c, maps, num_sms, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
         pa::launch_linear_out(D, c, maps, num_sms, stream) != cudaSuccess)
         return PA_ERR_CUDA;
     return PA_OK;
