@@ -14,7 +14,9 @@ constexpr int kThreads = 256;
 
 template <int D>
 struct Slice {
-    static constexpr int kCols = D == 256 ? 32 : 64;      // of the state's columns (of V), of a block: 32 KB (16 at D = 64)
+    // of the state's columns (of V), of a block: 32 KB (16 at D = 64).  64 at D = 256 take 44.7 us for 64 sequences
+    // of 24/4 heads, 32 take 30.6; 32 at D = 128 take 51.4 for 256 sequences of 32/8 heads, 64 take 45.4
+    static constexpr int kCols = D == 256 ? 32 : 64;
     static constexpr int kLanes = kCols / 4;              // threads of a row
     static constexpr int kRows = kThreads / kLanes;       // rows at a time
     static constexpr int kPasses = D / kRows;
@@ -53,11 +55,23 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     return r;
 }
 
-// A block takes kCols columns of a (sequence, kv head)'s state through all of its
-// tokens; each thread holds kPasses rows, next to each other, of four columns.  A token's products with
-// q are summed over the block's rows by shuffles and in shared memory.
+// Blocks an SM that the registers are shared out for: the sums of more than four query heads spill at four blocks,
+// and take less of the time the smaller the state is (64 sequences of 24/4 x 256: 30.6 us with three, 31.7 with four;
+// 128 of 32/4 x 128: 16.1 / 20.7; 512 of 32/4 x 64: 19.2 / 16.8; with up to four heads, 256 of 32/8 x 128: 47.8 / 45.4).
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, G > 4 ? 3 : 4) linear_recurrent_kernel(const LinearParams prm) {
+constexpr int kBlocksPerSm = G > 4 && D > 64 ? 3 : 4;
+
+// For each token S <- d S + k v^T and out = scale q S.  A block takes kCols columns of a
+// (sequence, kv head)'s state through all of its tokens; each thread holds kPasses rows, next to
+// each other, of four columns, so that the state is read and written once however many tokens
+// there are.  A token's products with q are summed over the block's rows by shuffles and in
+// shared memory.  One token a sequence is bound by the state's traffic, 8 D^2 bytes a kv head:
+// 256 sequences of 32/8 x 128 (268 MB of states there and back) 46 us, 87 % of the measured
+// bandwidth; 64 of 24/4 x 256 (134 MB) 30.6 us, 66 %, where the blocks' waits for their states are not all covered (without the hint that
+// states are not read again 41 us); a single sequence 4.2 us, a launch and two trips to memory.
+// More tokens cost about 1.2 us each, the chain through shared memory.
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, G>) linear_recurrent_kernel(const LinearParams prm) {
     using S = Slice<D>;
     __shared__ __align__(16) float ks[D];
     __shared__ __align__(16) float qs[G][D];

@@ -7,7 +7,9 @@
 //     S_(n+1) = d^L S_n + A_n
 //     out_i   = scale (d^(i + 1) q_i S_n + sum_{j <= i} d^(i - j) (q_i . k_j) v_j)
 // in three launches: the sums A of all blocks at once, the chain of states
-// (elementwise along a sequence), and the outputs of all blocks at once.  Nothing
+// (elementwise along a sequence), and the outputs of all blocks at once.  The calls take
+// 54 us for 4 x 512 tokens of 24/4 x 256, 126 us for one sequence of 8192 of them, 119 us for
+// 16 of up to 4096 of 12/12 x 64, and 444 us for 8 x 8192 of 32/8 x 128.  Nothing
 // is sequential but the chain, so one long prompt fills the device as a batch does.
 // What that costs is the states' traffic, 12 D^2 bytes a block and kv head beside
 // the 4 (1 + G) * 256 * D of its tokens: blocks half as long would double it,
@@ -112,6 +114,10 @@ struct AddUnit {
 // decay makes earlier ones smaller) with room above, and moves, with the column's sum so far,
 // where later ones would not fit.  The first CTAs find the largest entries of the sequences'
 // first states.
+// 8 x 8192 tokens of 8 x 128: 74.5 us for 402 MB of tokens and sums, 80 % of the measured
+// bandwidth (a CTA a tile, without the run ahead: 86 us).  One sequence of 8192 of 4 x 256: 25.5 us,
+// 512 tiles for 304 CTAs, where the scaling of a column's 64 tokens (two halves each) bounds it;
+// two threads a column take 25.5 too, and 79.5 us for the 8 sequences: their warps wait for each other.
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 2)
     linear_adds_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {
@@ -441,7 +447,9 @@ constexpr int kScanThreads = 256;
 // A thread takes four entries of a (sequence, kv head)'s state through its blocks.
 // The state before each block goes to the outputs' kernel as halves of S 2^-e; e comes
 // from a bound on |S| that runs along (no more than a few bits above it), so that no
-// block has to look for the largest entry.
+// block has to look for the largest entry.  Bound by memory, 6 D^2 bytes a block and kv head:
+// 8 x 8192 tokens of 8 x 128 (201 MB) 41 us, 72 % of the measured bandwidth; where one
+// sequence has all blocks, by the trips along it (8192 of 4 x 256, 50 MB: 19.4 us).
 template <int D>
 __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearChunkParams c) {
     const LinearParams& p = c.lin;
@@ -596,9 +604,13 @@ __device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
 // row's power of two, and write the outputs.  Steps go from the row's own keys backwards,
 // where scores only shrink by the decay, so that the first one nearly always sets that
 // power.  What bounds it is the chain of hand-overs between the roles, each of which takes
-// longer than its products: hence steps of 128 keys (64 were 10 to 20 % slower), whole steps a
-// stage where they fit, and one elected thread for the copies and one for the MMAs (in a branch
+// longer than its products: hence steps of 128 keys, whole steps a stage where they fit (stages of
+// 64 keys at head_dim 128: the call on 8 x 8192 of 32/8 463 -> 520 us), and one elected thread for the copies and one for the MMAs (in a branch
 // of `lane == 0` the compiler does not know that it is one).
+// 8 x 8192 tokens of 32/8 x 128: 312 us for 1.41 GB, 66 % of the measured bandwidth, and 880
+// TFLOP/s of its tiles' products, 46 % of the measured rate; the hand-overs alone, without the row
+// warps' arithmetic, take half of that.  One sequence of 8192 of 24/4 x 256: 81 us (one CTA an SM,
+// whose hand-overs nothing else covers), and 5 to 27 us more with outputs stored by the row warps.
 template <int D>
 __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
     linear_out_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {

@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(256) kv_alloc_place_kernel(const KvAllocParams
 // finds in shared memory: of all sequences where they are few enough (`All`), so that
 // tokens can be placed next to the blocks' moves, else of its own share of them.  Its warps
 // then move the blocks of its share, a sequence a warp at a time.
+// What bounds it is the chain of trips to memory (lengths; sums; blocks given back; blocks
+// taken; slots), not its bytes, a few hundred KB at most: 2.8 us for one sequence, 6.8 for a step of 64
+// of which four end or shrink, 12.3 for 512 sequences' 130000 new tokens, 2 of them the second launch.
 template <bool All>
 __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(const KvAllocParams prm) {
     namespace cg = cooperative_groups;
@@ -237,7 +240,10 @@ struct alignas(16) Piece {
 // at a time.  What is rotated lies in the lane's own piece (pairs) or in that of
 // another lane of the row (halves); where half the rotated dims is not a whole
 // number of pieces, partners are read one by one.
-template <int D>
+// Bound by memory: 16384 tokens of 32/8 x 128 (436 MB) 80 us, 80 % of the measured
+// bandwidth, the slots in no order; 64 tokens of 24/4 x 256 3.2 us, of 32/8 x 128 2.5, a launch and the chain
+// position -> factors -> row.
+template <int D, int Ahead>
 __global__ void __launch_bounds__(kPutThreads) kv_put_kernel(const KvPutParams prm) {
     constexpr int kPieces = D / 8, kRows = 32 / kPieces;
     const int lane = threadIdx.x & 31, token = blockIdx.x * (kPutThreads / 32) + (threadIdx.x >> 5);
@@ -291,9 +297,8 @@ __global__ void __launch_bounds__(kPutThreads) kv_put_kernel(const KvPutParams p
     const int src_lane = (lane & ~(kPieces - 1)) + (d0 >= r ? piece : d0 < half_r ? piece + half_r / 8 : piece - half_r / 8);
     const int H = prm.num_heads, K = prm.num_kv_heads, all = H + K + (caching ? K : 0);
     const int first = blockIdx.y * prm.rows_per_warp, last = min(all, first + prm.rows_per_warp);
-    // the lane's next kAhead rows are on their way while it works on as many (in place: a row is read whole before
+    // the lane's next Ahead rows are on their way while it works on as many (in place: a row is read whole before
     // any of it is written)
-    constexpr int kAhead = 4;
     const int mine = lane / kPieces;
     auto source = [&](int row) {
         const bool is_q = row < H, is_v = row >= H + K;
@@ -301,22 +306,22 @@ __global__ void __launch_bounds__(kPutThreads) kv_put_kernel(const KvPutParams p
                : is_v ? prm.v + token * prm.v_stride + (size_t)(row - H - K) * D
                       : prm.k + token * prm.k_stride + (size_t)(row - H) * D;
     };
-    Piece x[kAhead], next[kAhead];
+    Piece x[Ahead], next[Ahead];
     auto fetch = [&](int base) {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < Ahead; ++a) {
             const int row = base + a * kRows + mine;
             next[a].raw() = make_uint4(0u, 0u, 0u, 0u);
             if (row < last) next[a].raw() = __ldcs(reinterpret_cast<const uint4*>(source(row) + d0));
         }
     };
     fetch(first);
-    for (int base = first; base < last; base += kRows * kAhead) {
+    for (int base = first; base < last; base += kRows * Ahead) {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) x[a] = next[a];
-        fetch(base + kRows * kAhead);
+        for (int a = 0; a < Ahead; ++a) x[a] = next[a];
+        fetch(base + kRows * Ahead);
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < Ahead; ++a) {
             const int row = base + a * kRows + mine;
             const bool real = row < last, is_q = row < H, is_v = row >= H + K;
             const int head = is_q ? row : is_v ? row - H - K : row - H;
@@ -402,8 +407,14 @@ cudaError_t launch_kv_alloc(const KvAllocParams& prm, int cluster, cudaStream_t 
                                          : launch_alloc<false>(prm, cluster, stream);
 }
 
+// Rows ahead of a lane: two where that is all of a warp's rows, or rows are so many at a time that four would
+// leave the last ones of a token's heads mostly empty (head_dim 64); else four, which cover more of the trips to
+// memory.  With two and four: 64 tokens of 32/8 x 128 2.5 / 3.0 us, 8192 of them 45.9 / 42.1; 64 of 12/12 x 64
+// 2.2 / 2.7, 4096 of them 11.3 / 12.3, 8192 of them 23.7 / 23.5; 8192 of 24/4 x 256 58.4 / 51.8 (eight: 57.7).
 template <int D>
 static cudaError_t launch_put(const KvPutParams& prm, dim3 grid, cudaStream_t stream) {
+    constexpr int kRows = 256 / D;  // at a time
+    const bool two = D == 64 || prm.rows_per_warp <= 2 * kRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kPutThreads);
@@ -411,7 +422,7 @@ static cudaError_t launch_put(const KvPutParams& prm, dim3 grid, cudaStream_t st
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_put_kernel<D>, prm);
+    return two ? cudaLaunchKernelEx(&cfg, kv_put_kernel<D, 2>, prm) : cudaLaunchKernelEx(&cfg, kv_put_kernel<D, D == 64 ? 2 : 4>, prm);
 }
 
 cudaError_t launch_kv_put(int head_dim, const KvPutParams& prm, dim3 grid, cudaStream_t stream) {

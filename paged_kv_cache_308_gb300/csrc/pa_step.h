@@ -28,7 +28,9 @@ struct KvAllocParams {
 };
 constexpr int kAllocThreads = 512;
 constexpr int kAllocMaxCluster = 8;
-constexpr int kAllocAllSeqs = 2048;  // up to so many are kept in each block's shared memory
+// Up to so many sequences (48 KB) are kept in each block's shared memory, which saves the second launch for their tokens:
+// a step of 64 sequences 6.8 us, with each block's own share kept 8.9; of 2048 15.8 / 17.5.
+constexpr int kAllocAllSeqs = 2048;
 cudaError_t launch_kv_alloc(const KvAllocParams& prm, int cluster, cudaStream_t stream);
 
 struct KvPutParams {

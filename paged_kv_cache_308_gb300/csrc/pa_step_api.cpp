@@ -124,9 +124,21 @@ int check_linear_prefix(const pa_linear_prefix_args* a) {
     return PA_OK;
 }
 
-// pa_kv_alloc: up to so many tokens are placed by the cluster that moves the blocks, and up to so many
-// sequences take a cluster of one block.
-constexpr int kAllocPlaceTokens = 4096, kAllocOneSeqs = 128;
+// pa_kv_alloc: up to so many sequences take a cluster of one block, more of them one of kAllocMaxCluster: a step of
+// one new token each, 32 sequences 5.2 us in one and 5.4 in eight, 64 of them 6.8 either way, 128 of them 7.5 / 7.0,
+// 512 of them 15.6 / 10.2.
+constexpr int kAllocOneSeqs = 64;
+// Up to so many new tokens for each block of the cluster are placed by it, more of them by a launch of their own:
+// 4 sequences of 512 new tokens 5.0 us placed here and 5.1 apart, 8 of them 7.9 / 5.2; in eight blocks 4096 tokens
+// 8.6 / 10.0, 16384 of them 10.9 / 10.3, 32768 of them 14.9 / 11.6.
+constexpr int kAllocPlaceTokens = 4 * pa::kAllocThreads;
+
+// pa_kv_put: a warp takes all heads of a token, or where there are few tokens a share of them, of at least kPutRows
+// and so that there are no more than kPutWarps warps an SM.  64 tokens of 24/4 x 256: 3.2 us with shares of 4 heads,
+// 4.1 with 8, 11.0 with all; 32/8 x 128 2.5, 3.1 and 9.5.  1024 tokens: 9.9 and 8.2 us with 16 warps an SM, 10.2 and
+// 9.4 with 32, 12.4 and 10.7 with one warp a token (of 12/12 x 64 5.3, 5.8 and 5.6).  A second warp for each of 4096
+// tokens gains 10 % there and loses 15 % at 12/12 x 64; at 8192 it gains nothing and loses up to 28 %.
+constexpr int kPutRows = 4, kPutWarps = 16;
 
 // Up to so many new tokens a sequence go token by token, by head_dim: the calls' us there and in chunks, 1
 // sequence of 24/4 x 256 with 9 tokens 20.6 / 21.3 and 12 tokens 26.6 / 21.1, 64 of them with 9 tokens 139 / 174; of
@@ -183,8 +195,8 @@ int pa_kv_alloc(const pa_kv_alloc_args* a, pa_stream_t stream) {
     p.cols = a->max_blocks_per_seq;
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
-    p.place = a->num_tokens <= kAllocPlaceTokens;
     const int cluster = a->num_seqs <= kAllocOneSeqs ? 1 : pa::kAllocMaxCluster;
+    p.place = a->num_tokens <= kAllocPlaceTokens * cluster;
     return pa::launch_kv_alloc(p, cluster, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
@@ -219,10 +231,9 @@ int pa_kv_put(const pa_kv_put_args* a, pa_stream_t stream) {
     p.status = pa::device_status_ptr();
     if (!p.status) return PA_ERR_CUDA;
     const int rows = a->num_heads + 2 * c.num_kv_heads, warps = pa::kPutThreads / 32;
-    // all heads of a token to a warp where there are many tokens, at least 8
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK) return PA_ERR_CUDA;
-    const long long splits = std::max(1ll, std::min((long long)rows / 8, 32ll * num_sms / a->num_tokens));
+    const long long splits = std::max(1ll, std::min((long long)rows / kPutRows, (long long)kPutWarps * num_sms / a->num_tokens));
     p.rows_per_warp = static_cast<int>(std::max((rows + splits - 1) / splits, (rows + 65534ll) / 65535));
     const dim3 grid((a->num_tokens + warps - 1) / warps, (rows + p.rows_per_warp - 1) / p.rows_per_warp);
     return pa::launch_kv_put(c.head_dim, p, grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
