@@ -55,11 +55,12 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     return r;
 }
 
-// Blocks an SM that the registers are shared out for: the sums of more than four query heads spill at four blocks,
-// and take less of the time the smaller the state is (64 sequences of 24/4 x 256: 30.6 us with three, 31.7 with four;
-// 128 of 32/4 x 128: 16.1 / 20.7; 512 of 32/4 x 64: 19.2 / 16.8; with up to four heads, 256 of 32/8 x 128: 47.8 / 45.4).
-template <int D, int G>
-constexpr int kBlocksPerSm = G > 4 && D > 64 ? 3 : 4;
+// Blocks an SM that the registers are shared out for: half a state a block at head_dim 64, a quarter and an eighth
+// above (512 sequences of 24/4 x 64: 16.0 us with four, 14.8 with five; 256 of 32/8 x 128: 46.8 / 50.8, and 48.8
+// with three).  More than four query heads are summed in two halves: six at once leave room for three blocks or spill
+// (128 sequences of 24/4 x 256 57.0 us, in halves 52.9; 256 of 64/8 x 128 61.4 / 58.2).
+template <int D>
+constexpr int kBlocksPerSm = D == 64 ? 5 : 4;
 
 // For each token S <- d S + k v^T and out = scale q S.  A block takes kCols columns of a
 // (sequence, kv head)'s state through all of its tokens; each thread holds kPasses rows, next to
@@ -67,12 +68,14 @@ constexpr int kBlocksPerSm = G > 4 && D > 64 ? 3 : 4;
 // there are.  A token's products with q are summed over the block's rows by shuffles and in
 // shared memory.  One token a sequence is bound by the state's traffic, 8 D^2 bytes a kv head:
 // 256 sequences of 32/8 x 128 (268 MB of states there and back) 46 us, 87 % of the measured
-// bandwidth; 64 of 24/4 x 256 (134 MB) 30.6 us, 66 %, where the blocks' waits for their states are not all covered (without the hint that
-// states are not read again 41 us); a single sequence 4.2 us, a launch and two trips to memory.
+// bandwidth; 64 of 24/4 x 256 (134 MB) 29 us, 68 %, where the products with six heads are not all
+// covered (23 us with one head; without the hint that states are not read again 41 us); a
+// single sequence 4.2 us, a launch and two trips to memory.
 // More tokens cost about 1.2 us each, the chain through shared memory.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, G>) linear_recurrent_kernel(const LinearParams prm) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<D>) linear_recurrent_kernel(const LinearParams prm) {
     using S = Slice<D>;
+    constexpr int kHeads = G > 4 ? G / 2 : G;  // whose sums are in registers at a time
     __shared__ __align__(16) float ks[D];
     __shared__ __align__(16) float qs[G][D];
     __shared__ __align__(16) float red[kThreads / 32][G][S::kCols];
@@ -119,9 +122,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, G>) linear_recurrent
         const float2 v23 = __half22float2(*reinterpret_cast<const __half2*>(&vr.y));
         const Two va = two(v01.x, v01.y), vb = two(v23.x, v23.y);
         __syncthreads();
-        Two sum[G][2];
-#pragma unroll
-        for (int h = 0; h < G; ++h) sum[h][0] = sum[h][1] = 0;
 #pragma unroll
         for (int i = 0; i < S::kPasses; i += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(ks + r0 + i);
@@ -132,33 +132,41 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, G>) linear_recurrent
                 x.x = fma2(two(kk, kk), va, fma2(x.x, rest, mul2(x.x, whole)));
                 x.y = fma2(two(kk, kk), vb, fma2(x.y, rest, mul2(x.y, whole)));
             }
+        }
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-                const float4 q4 = *reinterpret_cast<const float4*>(&qs[h][r0 + i]);
+        for (int h0 = 0; h0 < G; h0 += kHeads) {
+            Two sum[kHeads][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float qq = j == 0 ? q4.x : j == 1 ? q4.y : j == 2 ? q4.z : q4.w;
-                    sum[h][0] = fma2(two(qq, qq), s[i + j].x, sum[h][0]);
-                    sum[h][1] = fma2(two(qq, qq), s[i + j].y, sum[h][1]);
+            for (int h = 0; h < kHeads; ++h) sum[h][0] = sum[h][1] = 0;
+#pragma unroll
+            for (int i = 0; i < S::kPasses; i += 4) {
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(&qs[h0 + h][r0 + i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float qq = j == 0 ? q4.x : j == 1 ? q4.y : j == 2 ? q4.z : q4.w;
+                        sum[h][0] = fma2(two(qq, qq), s[i + j].x, sum[h][0]);
+                        sum[h][1] = fma2(two(qq, qq), s[i + j].y, sum[h][1]);
+                    }
                 }
             }
-        }
-        float4 acc[G];
+            // each lane of a column's four (at head_dim 256, else two) ends with a share of the columns
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float2 a = parts(sum[h][0]), b = parts(sum[h][1]);
-            acc[h] = make_float4(a.x, a.y, b.x, b.y);
-        }
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-#pragma unroll
-            for (int d = S::kLanes; d < 32; d *= 2) {
-                acc[h].x += __shfl_xor_sync(kFull, acc[h].x, d);
-                acc[h].y += __shfl_xor_sync(kFull, acc[h].y, d);
-                acc[h].z += __shfl_xor_sync(kFull, acc[h].z, d);
-                acc[h].w += __shfl_xor_sync(kFull, acc[h].w, d);
+            for (int h = 0; h < kHeads; ++h) {
+                const bool upper = lane & S::kLanes;
+                const float2 mine = parts(upper ? sum[h][1] : sum[h][0]), other = parts(upper ? sum[h][0] : sum[h][1]);
+                float2 o = make_float2(mine.x + __shfl_xor_sync(kFull, other.x, S::kLanes),
+                                       mine.y + __shfl_xor_sync(kFull, other.y, S::kLanes));
+                float* at = &red[warp][h0 + h][lane % S::kLanes * 4 + (upper ? 2 : 0)];
+                if (S::kLanes == 8) {
+                    const bool odd = lane & 16;
+                    const float x = (odd ? o.y : o.x) + __shfl_xor_sync(kFull, odd ? o.x : o.y, 16);
+                    at[odd] = x;
+                } else {
+                    *reinterpret_cast<float2*>(at) = o;
+                }
             }
-            if (lane < S::kLanes) *reinterpret_cast<float4*>(&red[warp][h][lane * 4]) = acc[h];
         }
         __syncthreads();
         for (int i = t; i < prm.group * S::kCols; i += kThreads) {
