@@ -736,8 +736,8 @@ int pa_kv_evict(const pa_kv_evict_args* args, pa_stream_t stream);
  * its context length and its slots are -1; those that need none are served.  A
  * sequence whose lengths are out of range (PA_DEV_BAD_SEQ_LEN: negative, context
  * above held, more blocks than a row has) keeps its row, with seq_lens 0, slots
- * -1 and positions unspecified; runs that end past num_tokens are cut there (PA_DEV_BAD_SEQ_LEN).  Where
- * free_count is outside [0, num_blocks], or more blocks come back than there
+ * -1 and positions unspecified; runs that end past num_tokens are cut there
+ * (PA_DEV_BAD_SEQ_LEN).  Where free_count is outside [0, num_blocks], or more blocks come back than there
  * are, no block moves (PA_DEV_NO_BLOCKS).  Each block belongs in one row only.
  * The outputs must not overlap each other or the inputs, but for new_free_count.
  * num_blocks * block_size < 2^31; lengths and num_tokens up to 2^30. */
@@ -781,7 +781,8 @@ int pa_kv_alloc(const pa_kv_alloc_args* args, pa_stream_t stream);
  * unspecified mix of both.  q, k and v may have other distances between tokens
  * than num_heads * head_dim elements (a row of a joint projection): q_stride,
  * k_stride and v_stride, multiples of 8, 0 for contiguous tokens (in place only
- * for these). */
+ * for these).  But for q_out on q and k_out on k no output may overlap another
+ * one or an input. */
 typedef struct {
     pa_kv_cache cache;           /* PA_KV_F16; scales not used */
     void* q_out;
@@ -823,7 +824,10 @@ int pa_kv_put(const pa_kv_put_args* args, pa_stream_t stream);
  * (calls that may overlap need a workspace each).  A decay that is positive or
  * NaN sets PA_DEV_BAD_DECAY; its head's outputs and states are then unspecified.
  * A NaN or infinity in a token's v reaches this token's outputs and later
- * ones of its sequence and kv head, in its own column of v only; no other. */
+ * ones of its sequence and kv head, in its own column of v only; no other.  One
+ * in k reaches them in all columns, where pa_linear_prefix may make NaN what
+ * would be an infinity token by token; one in q, this token's and head's.  Outputs
+ * and states must not overlap each other or the inputs. */
 typedef struct {
     float* states;               /* [num_slots][num_kv_heads][head_dim][head_dim], in place */
     int64_t num_slots;           /* below 2^31 */

@@ -934,7 +934,7 @@ def pa_linear_decode(out, q, k, v, states, slots, log_decay, scale, stream=None)
 
 
 def pa_linear_prefix_workspace_size(num_seqs, num_tokens, max_query_len, num_heads, num_kv_heads, head_dim) -> int:
-    """Bytes of pa_linear_prefix's workspace on the current device."""
+    """Bytes of pa_linear_prefix's workspace."""
     return lib.pa_linear_prefix_workspace_size(int(num_seqs), int(num_tokens), int(max_query_len), int(num_heads),
                                                int(num_kv_heads), int(head_dim))
 
@@ -958,9 +958,6 @@ def pa_linear_prefix(out, q, k, v, states, slots, log_decay, context_lens, query
                          _tensor("log_decay", log_decay, _F32, (hkv,), dev), _tensor("slots", slots, _I32, (B,), dev),
                          _tensor("context_lens", context_lens, _I32, (B,), dev),
                          _tensor("query_start_loc", query_start_loc, _I32, (B + 1,), dev), B, T, max_query_len, H, scale)
-    need = 0
-    if workspace is None:
-        with torch.cuda.device(dev):  # (the blocks go by the device's SMs)
-            need = lib.pa_linear_prefix_workspace_size(B, T, max_query_len, H, hkv, dim)
+    need = lib.pa_linear_prefix_workspace_size(B, T, max_query_len, H, hkv, dim) if workspace is None else 0
     ptr, nbytes, _hold = _workspace(workspace, need, dev, stream)
     _call("pa_linear_prefix", dev, stream, lib.pa_linear_prefix, args, ptr, nbytes)

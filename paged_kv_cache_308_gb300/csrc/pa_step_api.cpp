@@ -18,11 +18,12 @@ constexpr size_t kWsAlign = 256;
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool bad_ptr(const void* p, uintptr_t a) { return !p || !aligned(p, a); }
 
-// An array of words of four bytes that a call reads or writes.
+// An array of words of four bytes that a call reads or writes (n below 2^61, as all memory is).
 struct Words {
     const void* p;
     long long n;
 };
+Words halves(const void* p, long long n) { return {p, n / 2}; }
 bool overlap(const Words& a, const Words& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
     return a.p && b.p && a.n > 0 && b.n > 0 && (x < y ? y - x < 4ull * a.n : x - y < 4ull * b.n);
@@ -91,6 +92,17 @@ int check_put(const pa_kv_put_args* a) {
     // rows of another pitch than the outputs' cannot be rotated in place
     if ((a->q_out == a->q && stride[0] && stride[0] != row[0]) || (a->k_out == a->k && stride[1] && stride[1] != row[1]))
         return PA_ERR_INVALID_ARG;
+    const long long T = a->num_tokens, cached = c.num_blocks * row[1] * pa::kBlockSize;
+    auto span = [&](int i) { return (T - 1) * (stride[i] ? stride[i] : row[i]) + row[i]; };
+    const Words out[] = {halves(a->q_out, T * row[0]), halves(a->k_out, T * row[1]), halves(c.k_cache, cached),
+                         halves(c.v_cache, cached)};
+    const Words in[] = {halves(a->q, span(0)), halves(a->k, span(1)), halves(c.k_cache ? a->v : nullptr, span(2))};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return PA_ERR_INVALID_ARG;
+        for (int j = 0; j < 3; ++j)
+            if (!(i == j && i < 2 && out[i].p == in[j].p) && overlap(out[i], in[j])) return PA_ERR_INVALID_ARG;
+    }
     return PA_OK;
 }
 
@@ -104,10 +116,19 @@ int check_linear(const pa_linear_state& s, int num_heads, float scale) {
     return PA_OK;
 }
 
-bool bad_linear_pointers(const void* out, const void* q, const void* k, const void* v, const pa_linear_state& s,
-                         const void* log_decay, const void* slots) {
-    return bad_ptr(out, 16) || bad_ptr(q, 16) || bad_ptr(k, 16) || bad_ptr(v, 16) || bad_ptr(s.states, 16) ||
-           bad_ptr(log_decay, 4) || bad_ptr(slots, 4);
+template <typename Args>
+bool bad_linear_pointers(const Args& a, long long tokens) {
+    if (bad_ptr(a.out, 16) || bad_ptr(a.q, 16) || bad_ptr(a.k, 16) || bad_ptr(a.v, 16) || bad_ptr(a.state.states, 16) ||
+        bad_ptr(a.log_decay, 4) || bad_ptr(a.slots, 4))
+        return true;
+    const long long D = a.state.head_dim, K = a.state.num_kv_heads;
+    const Words out = halves(a.out, tokens * a.num_heads * D);
+    const Words states{a.state.states, std::min(a.state.num_slots * K * D * D, 1ll << 60)};
+    const Words in[] = {halves(a.q, tokens * a.num_heads * D), halves(a.k, tokens * K * D), halves(a.v, tokens * K * D),
+                        {a.log_decay, K}, {a.slots, a.num_seqs}};
+    for (const Words& x : in)
+        if (overlap(out, x) || overlap(states, x)) return true;
+    return overlap(out, states);
 }
 
 int check_linear_prefix(const pa_linear_prefix_args* a) {
@@ -118,8 +139,7 @@ int check_linear_prefix(const pa_linear_prefix_args* a) {
     if (a->num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
     if (a->num_tokens > 0 && a->max_query_len == 0) return PA_ERR_INVALID_ARG;
     if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
-    if (bad_linear_pointers(a->out, a->q, a->k, a->v, a->state, a->log_decay, a->slots) || bad_ptr(a->context_lens, 4) ||
-        bad_ptr(a->query_start_loc, 4))
+    if (bad_linear_pointers(*a, a->num_tokens) || bad_ptr(a->context_lens, 4) || bad_ptr(a->query_start_loc, 4))
         return PA_ERR_INVALID_ARG;
     return PA_OK;
 }
@@ -244,7 +264,7 @@ int pa_linear_decode(const pa_linear_decode_args* a, pa_stream_t stream) {
     if (!a || a->num_seqs < 0 || a->num_seqs > 65535) return PA_ERR_INVALID_ARG;
     int rc = check_linear(a->state, a->num_heads, a->scale);
     if (rc || a->num_seqs == 0) return rc;
-    if (bad_linear_pointers(a->out, a->q, a->k, a->v, a->state, a->log_decay, a->slots)) return PA_ERR_INVALID_ARG;
+    if (bad_linear_pointers(*a, a->num_seqs)) return PA_ERR_INVALID_ARG;
     pa::LinearParams p{};
     p.out = static_cast<__half*>(a->out);
     p.q = static_cast<const __half*>(a->q);

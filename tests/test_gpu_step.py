@@ -89,6 +89,46 @@ def test_alloc_batches(seqs, top, chunk, seed):
     Step(held, ctx, new, seed).run().check()
 
 
+# one and eight blocks of a cluster, tokens placed by it and by a launch of their own; blocks run out or not
+@pytest.mark.parametrize("short", [False, True])
+@pytest.mark.parametrize("seqs,top,chunk", [(64, 500, 60), (64, 500, 70), (65, 2000, 1), (100, 300, 200), (300, 300, 200),
+                                            (2048, 100, 4), (2049, 100, 4)])
+def test_alloc_batches_of_every_path(seqs, top, chunk, short):
+    rng = random.Random(seqs + chunk)
+    held = [rng.randint(0, top) for _ in range(seqs)]
+    new = [rng.randint(0, chunk) for _ in range(seqs)]
+    ctx = [0 if rng.random() < 0.1 else h for h in held]
+    taken = sum(max(0, S.blocks(c + q) - S.blocks(h)) for h, c, q in zip(held, ctx, new))
+    back = sum(max(0, S.blocks(h) - S.blocks(c + q)) for h, c, q in zip(held, ctx, new))
+    Step(held, ctx, new, seqs, extra=-back - taken // 3 if short else 8).run().check()
+
+
+@pytest.mark.parametrize("seqs", [6, 100])
+@pytest.mark.parametrize("more", [100, 20000])
+def test_alloc_bad_lengths_next_to_many_tokens(seqs, more):
+    held = [20] * (seqs - 1) + [0]
+    new = [1] * (seqs - 1) + [more]
+    for h, c, q in [(-1, 0, 1), (16, 17, 1), (20, 20, -3), (20, -5, 5), (20, -5, 9), (1 << 30, 1 << 30, 1)]:
+        a = Step(held, held, new)
+        tables = a.tables.clone()
+        a.held_t[2], a.args[0][2], a.args[1][2] = h, c, q
+        a.slots, a.positions = ints([-5] * (sum(new) + 30)), ints([-5] * (sum(new) + 30))
+        a.run()
+        assert status() == pb.PA_DEV_BAD_SEQ_LEN
+        lens, loc, slots = a.lens.tolist(), a.loc.tolist(), a.slots.tolist()
+        assert lens == [21, 21, 0] + [21] * (seqs - 4) + [more] and torch.equal(a.tables[2], tables[2])
+        assert [y - x for x, y in zip(loc, loc[1:])] == [1, 1, max(q, 0)] + [1] * (seqs - 4) + [more]
+        table = a.tables.tolist()
+        for b in range(seqs):
+            at = range(loc[b], loc[b + 1])
+            if b == 2:
+                assert all(slots[i] == -1 for i in at)
+                continue
+            first = lens[b] - len(at)
+            assert [slots[i] for i in at] == [table[b][p // 16] * 16 + p % 16 for p in range(first, lens[b])]
+        assert all(x == -1 for x in slots[loc[-1]:])
+
+
 @pytest.mark.parametrize("extra", [-1, -2, -5, -9, -1000])
 def test_alloc_runs_out(extra):
     # later sequences that need nothing are served, earlier ones too; one that does not fit takes nothing

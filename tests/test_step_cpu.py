@@ -20,8 +20,13 @@ def alloc_args(nb=100, B=4, T=10, cols=8, bs=16, **p):
     return pb.pa_kv_alloc_args(*at.values(), nb, B, T, cols, bs)
 
 
+def apart(*names):
+    """Addresses so far apart that no array of these tests reaches the next."""
+    return {n: FAKE + (i + 1) * (1 << 28) for i, n in enumerate(names)}
+
+
 def put_args(T=4, H=8, hkv=2, D=128, nb=10, bs=16, fmt=pb.PA_KV_F16, rot=128, top=100, pairs=0, strides=(0, 0, 0), **p):
-    at = dict(kc=FAKE, vc=FAKE, q_out=FAKE, k_out=FAKE, q=FAKE + 16, k=FAKE + 16, v=FAKE, slots=FAKE, pos=FAKE, cs=FAKE)
+    at = apart("kc", "vc", "q_out", "k_out", "q", "k", "v", "slots", "pos", "cs")
     at.update(p)
     cache = pb.pa_kv_cache(at["kc"], at["vc"], 0, 0, nb, hkv, D, bs, fmt)
     return pb.pa_kv_put_args(cache, at["q_out"], at["k_out"], at["q"], at["k"], at["v"], at["slots"], at["pos"], at["cs"],
@@ -33,13 +38,13 @@ def state(slots=5, hkv=4, D=128, states=FAKE):
 
 
 def ldecode_args(s=None, B=3, H=8, scale=0.1, **p):
-    at = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, g=FAKE, slots=FAKE)
+    at = apart("out", "q", "k", "v", "g", "slots")
     at.update(p)
     return pb.pa_linear_decode_args(at["out"], at["q"], at["k"], at["v"], s or state(), at["g"], at["slots"], B, H, scale)
 
 
 def lprefix_args(s=None, B=3, T=10, max_q=5, H=8, scale=0.1, **p):
-    at = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, g=FAKE, slots=FAKE, ctx=FAKE, loc=FAKE)
+    at = apart("out", "q", "k", "v", "g", "slots", "ctx", "loc")
     at.update(p)
     return pb.pa_linear_prefix_args(at["out"], at["q"], at["k"], at["v"], s or state(), at["g"], at["slots"], at["ctx"],
                                     at["loc"], B, T, max_q, H, scale)
@@ -80,7 +85,8 @@ def test_alloc_refusals(kw, code):
     (dict(strides=(-1024, 0, 0)), BAD), (dict(q=0), BAD), (dict(k=0), BAD), (dict(v=0), BAD), (dict(q_out=0), BAD),
     (dict(pos=0), BAD), (dict(slots=0), BAD), (dict(cs=0), BAD), (dict(cs=FAKE + 4), BAD), (dict(k_out=FAKE + 8), BAD),
     (dict(kc=0), BAD), (dict(vc=0), BAD), (dict(kc=FAKE + 8), BAD),
-    (dict(q=FAKE, strides=(2048, 0, 0)), BAD), (dict(k=FAKE, strides=(0, 2048, 0)), BAD)])
+    (dict(q=FAKE, q_out=FAKE, strides=(2048, 0, 0)), BAD),
+    (dict(k=FAKE, k_out=FAKE, strides=(0, 2048, 0)), BAD)])
 def test_put_refusals(kw, code):
     assert call("pa_kv_put", put_args(**kw)) == code
 
@@ -102,6 +108,50 @@ def test_linear_refusals(kw, code):
                                      (dict(loc=FAKE + 2), BAD), (dict(T=(1 << 30) + 1), UNSUP)])
 def test_linear_prefix_refusals(kw, code):
     assert call("pa_linear_prefix", lprefix_args(**kw)) == code
+
+
+Q, K, V, OUT = (apart("out", "q", "k", "v")[n] for n in ("q", "k", "v", "out"))
+
+
+@pytest.mark.parametrize("fn,make", [("pa_linear_decode", ldecode_args), ("pa_linear_prefix", lprefix_args)])
+def test_linear_arrays_that_overlap(fn, make):
+    T = 3 if fn == "pa_linear_decode" else 10
+    row = 128 * 2
+    for kw in (dict(out=Q), dict(out=Q + T * 8 * row - 16), dict(q=OUT + T * 8 * row - 16), dict(out=K), dict(v=OUT),
+               dict(s=state(states=OUT)), dict(s=state(states=K + 16)), dict(g=OUT), dict(slots=FAKE + 4),
+               dict(s=state(slots=(1 << 31) - 1, hkv=1, D=256), H=8)):
+        assert call(fn, make(**kw)) == BAD, kw
+    # arrays next to each other are not refused for it
+    if fn == "pa_linear_prefix":
+        assert call(fn, make(out=Q - T * 8 * row, max_q=20)) == pb.PA_ERR_WORKSPACE
+        assert call(fn, make(q=OUT + T * 8 * row, max_q=20)) == pb.PA_ERR_WORKSPACE
+
+
+def test_put_arrays_that_overlap():
+    at = apart("kc", "vc", "q_out", "k_out", "q", "k", "v", "slots", "pos", "cs")
+    q_row, k_row = 8 * 128 * 2, 2 * 128 * 2
+    for kw in (dict(q_out=at["q"] + q_row), dict(q_out=at["k"]), dict(k_out=at["v"]), dict(kc=at["k"]),
+               dict(vc=at["v"] + 16), dict(k_out=at["kc"] + 10 * 16 * k_row - 16), dict(q_out=at["k_out"] - 16),
+               dict(vc=at["kc"] + 16), dict(q_out=at["k"] + 4 * k_row - 16)):
+        assert call("pa_kv_put", put_args(**kw)) == BAD, kw
+    # a strided input reaches to its last token's row
+    assert call("pa_kv_put", put_args(strides=(4096, 0, 0), q_out=at["q"] + 3 * 8192 + q_row - 16)) == BAD
+
+
+# few new tokens a sequence go without a workspace: up to 9, 14 and 24 by head_dim
+@pytest.mark.parametrize("dim,few", [(256, 9), (128, 14), (64, 24)])
+def test_linear_prefix_workspace_size(dim, few):
+    size = lambda B=3, T=1000, top=500, H=8, hkv=4, D=dim: pb.pa_linear_prefix_workspace_size(B, T, top, H, hkv, D)
+    assert size(top=few) == 0 and size(top=few + 1) > 0 and size(top=1) == 0
+    blocks = 3 + 1000 // 256  # one more for each sequence than whole blocks of 256 tokens
+    states = blocks * 4 * dim * dim * 6
+    assert states <= size() <= states * 1.02 + 16384
+    assert size(T=1023) == size(T=1000) < size(T=1024) and size(B=4) > size() and size(hkv=8) > size()
+    assert size(top=few + 1) == size()  # the sizes' sum counts, not the longest
+    for bad in (dict(B=0), dict(B=-1), dict(B=65536), dict(T=0), dict(T=(1 << 30) + 1), dict(top=0), dict(H=0), dict(hkv=0),
+                dict(hkv=65536), dict(D=96)):
+        assert size(**bad) == 0, bad
+    assert size(B=65535, T=1 << 30, top=1 << 30, H=8, hkv=8) > 1 << 32
 
 
 def test_empty_calls_do_nothing():
