@@ -541,15 +541,16 @@ struct OutShape {
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = kStageRows * D * 2;
     static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 2 : 4;
-    static constexpr int kBars = 19 + 2 * kSlots;
+    static constexpr int kScores = D == 256 ? 2 : 1;  // steps whose scores or P are in tensor memory
+    static constexpr int kBars = 22 + 2 * kSlots;
     // barriers, TMEM address and flag, two units, the exponents of the rows' largest scores by threads
     static constexpr int kCtrl = kBars * 8 + 16 + 2 * 64 + 2 * kSides * 128;
     static constexpr int kSmemNeed = kQBytes + kSlots * kStageBytes + kCtrl;
     // (so much that no more CTAs fit, and their TMEM allocations always do)
     static constexpr int kSmem = kSmemNeed > 80 * 1024 ? kSmemNeed : 80 * 1024;
-    static constexpr int kTmem = D == 256 ? 512 : 256;    // D of the outputs, 128 scores
+    static constexpr int kTmem = D == 256 ? 512 : 256;    // D of the outputs, 128 for each step's scores
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "CTAs an SM");
-    static_assert(D + 128 <= kTmem && kCtas * kTmem <= 512, "tensor memory of an SM");
+    static_assert(D + 128 * kScores <= kTmem && kCtas * kTmem <= 512, "tensor memory of an SM");
 };
 
 // 128 tokens (a half of a block) of one query head.
@@ -569,10 +570,10 @@ enum : int {
     kBarQFree,                 // and its MMAs are done
     kBarInter,                 // the accumulator holds Q S
     kBarRead,                  // the rows have read the accumulator
-    kBarScores,                // a step's scores are there
-    kBarP,                     // P over them
-    kBarPV,                    // P V is done
-    kBarUnit,                  // a unit's slot is written, 2
+    kBarScores,                // a step's scores are there (in turn, where the next step's may come before they are used), 2
+    kBarP = kBarScores + 2,    // P over them, 2 (a warp may be a step ahead of another)
+    kBarPV = kBarP + 2,        // P V is done, 2 (so may the products be)
+    kBarUnit = kBarPV + 2,     // a unit's slot is written, 2
     kBarUnitFree = kBarUnit + 2,  // and read by the MMAs' warp and the rows', 2
     kBarDrain = kBarUnitFree + 2,
     kBarV,                        // V tiles that the rows clean have landed
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
     if (t == 0) {
         *failed = 0;
         for (int i = 0; i < S::kBars; ++i)
-            mbar_init(bar(i), i == kBarP || i == kBarRead || i == kBarOut || i == kBarOut + 1 ? S::kRowWarps
+            mbar_init(bar(i), i == kBarP || i == kBarP + 1 || i == kBarRead || i == kBarOut || i == kBarOut + 1 ? S::kRowWarps
                               : i >= kBarSwap && i < kBarOut               ? S::kSides
                               : i == kBarUnitFree || i == kBarUnitFree + 1 ? S::kRowWarps + 1
                                                                            : 1);
@@ -781,11 +782,12 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                 ++q_tiles;
 #pragma unroll 1
                 for (int j = 0; j <= u.half; ++j) {
-                    step(&maps.k, j);
+                    if (S::kScores == 1 || j == 0) step(&maps.k, j);
                     if (j == 0 && u.inter)
 #pragma unroll
                         for (int d = 0; d < kStateStages; ++d)
                             stage(&maps.starts, 0, u.index * D + d * S::kStateRows, S::kStateRows * D * 2);
+                    if (S::kScores == 2 && j < u.half) step(&maps.k, j + 1);
                     step(&maps.v, j);
                 }
                 // (a unit may have fewer stages than the ring has slots)
@@ -836,23 +838,29 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                 mbar_arrive(bar(kBarUnitFree + s));
                 if (count == 0) break;
                 if (!wait(kBarQ, done)) break;
-#pragma unroll 1
-                for (int j = 0; j <= half; ++j, ++x) {
-                    // scores over the P that P V has read
-                    if (x > 0 && !wait(kBarPV, x - 1)) break;
+                // The scores of step x + ahead, over the P of kScores steps before, whose P V was the last one issued
+                // or came before that one.
+                auto scores = [&](int ahead) {
+                    const int z = x + ahead, buffer = z % S::kScores;
+                    if (x > 0 && !wait(kBarPV + (x - 1) % S::kScores, (x - 1) / S::kScores)) return false;
 #pragma unroll
                     for (int y = 0; y < S::kStepStages; ++y) {
-                        if (!landed()) break;
+                        if (!landed()) return false;
                         tc_fence_after();
                         const uint64_t kd = kdesc + at();
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            tc_mma_ss(t_s + y * S::kStageRows, qdesc + (uint64_t)(((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4),
+                            tc_mma_ss(t_s + buffer * 128 + y * S::kStageRows,
+                                      qdesc + (uint64_t)(((i >> 2) * (128 * 128) + (i & 3) * 32) >> 4),
                                       kd + (uint64_t)(((i >> 2) * (S::kStageRows * 128) + (i & 3) * 32) >> 4), id_s, i > 0);
                         release();
                     }
-                    if (!ok) break;
-                    tc_commit(bar(kBarScores));
+                    tc_commit(bar(kBarScores + buffer));
+                    return true;
+                };
+#pragma unroll 1
+                for (int j = 0; j <= half; ++j, ++x) {
+                    if ((S::kScores == 1 || j == 0) && !scores(0)) break;
                     if (j == 0 && inter) {
                         // the accumulator's last outputs have been read
                         if (done >= 1 && !wait(kBarRead, done - 1)) break;
@@ -871,7 +879,8 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                         tc_commit(bar(kBarInter));
                         ++inters;
                     }
-                    if (j == half) tc_commit(bar(kBarQFree));
+                    if (S::kScores == 2 && j < half && !scores(1)) break;  // while the rows make P
+                    if (j == (S::kScores == 2 ? 0 : half)) tc_commit(bar(kBarQFree));
                     // (the rows cannot tell a ring slot's phases apart: they may be two behind)
                     if (cleaned(dirty, count, half, j)) {
                         if (!landed()) break;
@@ -882,7 +891,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                         mbar_arrive(bar(kBarV));
                     }
                     // (rows that have written P have read the last outputs too)
-                    if (!wait(kBarP, x)) break;
+                    if (!wait(kBarP + x % S::kScores, x / S::kScores)) break;
                     // Q S, whose operand comes from shared memory, is done before P V, whose comes from
                     // tensor memory, adds to it: nothing orders the two kinds in the tensor cores
                     if (j == 0 && inter && !wait(kBarInter, inters - 1)) break;
@@ -897,7 +906,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                             // each of a row's threads has its P over its own 128 / kSides scores
                             constexpr int kPer = 8 / S::kSides;
                             const int k = y * (S::kStageRows / 16) + i;
-                            tc_mma_ts(t_out, t_s + k / kPer * (128 / S::kSides) + k % kPer * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
+                            tc_mma_ts(t_out, t_s + x % S::kScores * 128 + k / kPer * (128 / S::kSides) + k % kPer * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
                                       k > 0 ? 1u : add);
                         }
                         // (the unit's last V goes to the rows, who put the outputs there)
@@ -905,7 +914,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                         next();
                     }
                     if (!ok) break;
-                    tc_commit(bar(kBarPV));
+                    tc_commit(bar(kBarPV + x % S::kScores));
                 }
                 if (!ok) break;
             }
@@ -920,7 +929,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
         const int quarter = warp & 3, side = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         constexpr int kMine = D / S::kSides, kKeys = 128 / S::kSides;
-        const uint32_t acc = t_out + lanes + side * kMine, own = t_s + lanes + side * kKeys;
+        const uint32_t acc = t_out + lanes + side * kMine, scores0 = t_s + lanes + side * kKeys;
         bool ok = true;
         int x = 0, inters = 0;  // steps; units with a state
         int stages = 0;         // ring stages of earlier steps
@@ -932,6 +941,9 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarSwap + quarter));
             return ok = tc_warp_wait(bar(kBarSwap + quarter), swaps++ & 1, limit, failed);
+        };
+        auto product = [&](int step) {  // a step's P V is done
+            return tc_warp_wait(bar(kBarPV + step % S::kScores), step / S::kScores & 1, limit, failed);
         };
         for (int done = 0;; ++done) {
             const int s = done & 1;
@@ -955,7 +967,8 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
 #pragma unroll 1
             for (int j = 0; j <= u.half; ++j, ++x) {
                 const int kc = (u.half - j) * 128 + side * kKeys;  // first key of the warp's share of the step
-                if (!(ok = tc_warp_wait(bar(kBarScores), x & 1, limit, failed))) break;
+                const uint32_t own = scores0 + x % S::kScores * 128;
+                if (!(ok = tc_warp_wait(bar(kBarScores + x % S::kScores), x / S::kScores & 1, limit, failed))) break;
                 tc_fence_after();
                 uint32_t pk[kKeys / 2];
                 // A second time where a row's level has to move: 64 scores a thread kept beside their P would not
@@ -1029,7 +1042,7 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                     if (j == 0 && u.inter) {
                         ok = tc_warp_wait(bar(kBarInter), inters & 1, limit, failed);
                     } else if (j > 0) {
-                        ok = tc_warp_wait(bar(kBarPV), (x - 1) & 1, limit, failed);
+                        ok = product(x - 1);
                     }
                     if (!ok) break;
                     if (j > 0 || u.inter) {
@@ -1046,7 +1059,9 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                     }
                     pending = 0.f;
                 }
-                const int v_stage = stages + S::kStepStages + (j == 0 && u.inter ? kStateStages : 0);
+                // (behind the step's keys and, where they come early, the next one's)
+                const int v_stage = stages + (S::kScores == 1 ? 1 : j > 0 ? 0 : u.half + 1) * S::kStepStages +
+                                    (j == 0 && u.inter ? kStateStages : 0);
                 if (cleaned(u.dirty, u.count, u.half, j)) {
                     // V rows behind the block's last token belong to other sequences, and a NaN or
                     // infinity must not meet the zeros of tokens before it: both become 0 (the latter's column
@@ -1074,10 +1089,10 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                 stages = v_stage + S::kStepStages;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarP));
+                if (lane == 0) mbar_arrive(bar(kBarP + x % S::kScores));
             }
             if (!ok) break;
-            if (!(ok = tc_warp_wait(bar(kBarPV), (x - 1) & 1, limit, failed))) break;
+            if (!(ok = product(x - 1))) break;
             tc_fence_after();
             const float f = p.scale * exp2f(level);
             // Whole tiles go out through the memory of the unit's last V stages, which hold as many rows
