@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D>) linear_recurrent_ke
     __shared__ __align__(16) float qs[G][D];
     __shared__ __align__(16) float red[kThreads / 32][G][S::kCols];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int kvh = blockIdx.y, b = blockIdx.z, c0 = blockIdx.x * S::kCols + (t % S::kLanes) * 4, r0 = t / S::kLanes * S::kPasses;
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int c0 = blockIdx.x * S::kCols + (t % S::kLanes) * 4, r0 = t / S::kLanes * S::kPasses;  // column, first row
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int slot = __ldg(prm.slots + b);

@@ -8,7 +8,7 @@
 //     out_i   = scale (d^(i + 1) q_i S_n + sum_{j <= i} d^(i - j) (q_i . k_j) v_j)
 // in three launches: the sums A of all blocks at once, the chain of states
 // (elementwise along a sequence), and the outputs of all blocks at once.  The calls take
-// 54 us for 4 x 512 tokens of 24/4 x 256, 126 us for one sequence of 8192 of them, 119 us for
+// 51 us for 4 x 512 tokens of 24/4 x 256, 120 us for one sequence of 8192 of them, 118 us for
 // 16 of up to 4096 of 12/12 x 64, and 444 us for 8 x 8192 of 32/8 x 128.  Nothing
 // is sequential but the chain, so one long prompt fills the device as a batch does.
 // What that costs is the states' traffic, 12 D^2 bytes a block and kv head beside
@@ -94,7 +94,7 @@ struct AddShape {
     static constexpr int kSlots = 3;
     static constexpr int kRing = kSlots * 2 * kHalf;
     // two CTAs an SM, whose TMEM allocations then always fit
-    static constexpr int kSmem = (kRing > 78 * 1024 ? kRing : 78 * 1024) + 3072 + 1024;
+    static constexpr int kSmem = (kRing > 78 * 1024 ? kRing : 78 * 1024) + 4 * 1024;
     static constexpr int kTmem = 256;  // the sum, and 64 tokens of v in two halves, twice
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
@@ -570,7 +570,8 @@ enum : int {
     kBarQFree,                 // and its MMAs are done
     kBarInter,                 // the accumulator holds Q S
     kBarRead,                  // the rows have read the accumulator
-    kBarScores,                // a step's scores are there (in turn, where the next step's may come before they are used), 2
+    kBarScores,                // a step's scores are there, 2 (in turn, where the next step's may come before they
+                               // are used)
     kBarP = kBarScores + 2,    // P over them, 2 (a warp may be a step ahead of another)
     kBarPV = kBarP + 2,        // P V is done, 2 (so may the products be)
     kBarUnit = kBarPV + 2,     // a unit's slot is written, 2
@@ -598,7 +599,8 @@ __device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
 // (one and two steps of 128 keys) neighbours in that order.  A unit's 128 rows are the
 // lanes of the accumulator.  The last warp finds the units and brings Q, then in ring stages a
-// step's keys, the state's rows (behind the first step's keys) and the step's values, in the
+// step's keys, the state's rows (behind the first step's keys; at head_dim 256 the second step's
+// follow them) and the step's values, in the
 // order in which the warp before it feeds them to the tensor cores: a step's scores; Q S_n;
 // P V.  Both run ahead into the next unit while the row warps, two or four threads a
 // row, turn a step's scores into P, in fp16 over the scores, keep the accumulator in the
@@ -606,11 +608,13 @@ __device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
 // where scores only shrink by the decay, so that the first one nearly always sets that
 // power.  What bounds it is the chain of hand-overs between the roles, each of which takes
 // longer than its products: hence steps of 128 keys, whole steps a stage where they fit (stages of
-// 64 keys at head_dim 128: the call on 8 x 8192 of 32/8 463 -> 520 us), and one elected thread for the copies and one for the MMAs (in a branch
-// of `lane == 0` the compiler does not know that it is one).
+// 64 keys at head_dim 128: the call on 8 x 8192 of 32/8 463 -> 520 us), and one elected thread for
+// the copies and one for the MMAs (in a branch of `lane == 0` the compiler does not know that it
+// is one).  At head_dim 256, where tensor memory has room for them, a unit's second scores are
+// multiplied while the rows work on the first (without: 81 us where it takes 76 below).
 // 8 x 8192 tokens of 32/8 x 128: 312 us for 1.41 GB, 66 % of the measured bandwidth, and 880
 // TFLOP/s of its tiles' products, 46 % of the measured rate; the hand-overs alone, without the row
-// warps' arithmetic, take half of that.  One sequence of 8192 of 24/4 x 256: 81 us (one CTA an SM,
+// warps' arithmetic, take half of that.  One sequence of 8192 of 24/4 x 256: 76 us (one CTA an SM,
 // whose hand-overs nothing else covers), and 5 to 27 us more with outputs stored by the row warps.
 template <int D>
 __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
@@ -906,7 +910,8 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                             // each of a row's threads has its P over its own 128 / kSides scores
                             constexpr int kPer = 8 / S::kSides;
                             const int k = y * (S::kStageRows / 16) + i;
-                            tc_mma_ts(t_out, t_s + x % S::kScores * 128 + k / kPer * (128 / S::kSides) + k % kPer * 8, vd + (uint64_t)((i * 2048) >> 4), id_o,
+                            tc_mma_ts(t_out, t_s + x % S::kScores * 128 + k / kPer * (128 / S::kSides) + k % kPer * 8,
+                                      vd + (uint64_t)((i * 2048) >> 4), id_o,
                                       k > 0 ? 1u : add);
                         }
                         // (the unit's last V goes to the rows, who put the outputs there)
@@ -1081,7 +1086,8 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
                                 if ((h & 0x7c000000u) == 0x7c000000u) h &= 0xffffu;
                                 return h;
                             };
-                            *cell = k0 + row < u.count ? make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w)) : make_uint4(0u, 0u, 0u, 0u);
+                            *cell = k0 + row < u.count ? make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w))
+                                                       : make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1182,7 +1188,8 @@ cudaError_t out(const LinearChunkParams& prm, const LinearMaps& maps, int num_sm
     // An odd number of CTAs, so that each takes first and second halves of blocks in turn.
     const long long units = (long long)prm.blocks * 2 * prm.lin.num_heads;
     const long long room = (long long)S::kCtas * num_sms - (S::kCtas * num_sms % 2 == 0);
-    return launch(linear_out_kernel<D>, dim3((unsigned)(units < room ? units : room)), S::kThreads, S::kSmem, stream, maps, prm);
+    const unsigned grid = (unsigned)(units < room ? units : room);
+    return launch(linear_out_kernel<D>, dim3(grid), S::kThreads, S::kSmem, stream, maps, prm);
 }
 
 }  // namespace

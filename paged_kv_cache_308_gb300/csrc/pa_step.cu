@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kPutThreads) kv_put_kernel(const KvPutParams p
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 u = __half22float2(x[a].h[e]), v = __half22float2(o.h[e]);
-                        y.h[e] = __floats2half2_rn(fmaf(u.x, c[2 * e], v.x * s[2 * e]), fmaf(u.y, c[2 * e + 1], v.y * s[2 * e + 1]));
+                        y.h[e] = __floats2half2_rn(fmaf(u.x, c[2 * e], v.x * s[2 * e]),
+                                                   fmaf(u.y, c[2 * e + 1], v.y * s[2 * e + 1]));
                         // (a dim past the rotated ones is copied: NaN payloads and signed zeros too)
                         if (d0 + 2 * e >= r) y.h[e] = x[a].h[e];
                     }
@@ -353,8 +354,10 @@ __global__ void __launch_bounds__(kPutThreads) kv_put_kernel(const KvPutParams p
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int d = d0 + e;
-                    if (d < r)
-                        ye[e] = __float2half_rn(fmaf(__half2float(xe[e]), c[e], __half2float(src[d < half_r ? d + half_r : d - half_r]) * s[e]));
+                    if (d < r) {
+                        const float partner = __half2float(src[d < half_r ? d + half_r : d - half_r]);
+                        ye[e] = __float2half_rn(fmaf(__half2float(xe[e]), c[e], partner * s[e]));
+                    }
                 }
             }
             __syncwarp();  // (in place: the row has been read)
@@ -422,7 +425,8 @@ static cudaError_t launch_put(const KvPutParams& prm, dim3 grid, cudaStream_t st
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return two ? cudaLaunchKernelEx(&cfg, kv_put_kernel<D, 2>, prm) : cudaLaunchKernelEx(&cfg, kv_put_kernel<D, D == 64 ? 2 : 4>, prm);
+    return two ? cudaLaunchKernelEx(&cfg, kv_put_kernel<D, 2>, prm)
+               : cudaLaunchKernelEx(&cfg, kv_put_kernel<D, D == 64 ? 2 : 4>, prm);
 }
 
 cudaError_t launch_kv_put(int head_dim, const KvPutParams& prm, dim3 grid, cudaStream_t stream) {

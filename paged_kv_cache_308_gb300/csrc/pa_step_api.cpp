@@ -80,7 +80,8 @@ int check_put(const pa_kv_put_args* a) {
         (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256))
         return PA_ERR_UNSUPPORTED;
     // slots are ints; heads a grid dimension
-    if (c.num_blocks >= (1ll << 31) / pa::kBlockSize || a->num_heads > 65535 || c.num_kv_heads > 16384 || a->num_tokens > kMaxTokens)
+    if (c.num_blocks >= (1ll << 31) / pa::kBlockSize || a->num_heads > 65535 || c.num_kv_heads > 16384 ||
+        a->num_tokens > kMaxTokens)
         return PA_ERR_UNSUPPORTED;
     if (a->num_tokens == 0) return PA_OK;
     if (bad_ptr(a->q, 16) || bad_ptr(a->k, 16) || bad_ptr(a->q_out, 16) || !aligned(a->k_out, 16) ||
@@ -253,7 +254,8 @@ int pa_kv_put(const pa_kv_put_args* a, pa_stream_t stream) {
     const int rows = a->num_heads + 2 * c.num_kv_heads, warps = pa::kPutThreads / 32;
     int num_sms = 0;
     if (pa::sm_count(&num_sms) != PA_OK) return PA_ERR_CUDA;
-    const long long splits = std::max(1ll, std::min((long long)rows / kPutRows, (long long)kPutWarps * num_sms / a->num_tokens));
+    const long long splits =
+        std::max(1ll, std::min((long long)rows / kPutRows, (long long)kPutWarps * num_sms / a->num_tokens));
     p.rows_per_warp = static_cast<int>(std::max((rows + splits - 1) / splits, (rows + 65534ll) / 65535));
     const dim3 grid((a->num_tokens + warps - 1) / warps, (rows + p.rows_per_warp - 1) / p.rows_per_warp);
     return pa::launch_kv_put(c.head_dim, p, grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
@@ -357,7 +359,8 @@ int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, 
         (rc = pa::make_rows_map(&maps.starts, c.starts, sp.blocks * K * D, 1, D, state_rows, D)))
         return rc;
     if (p.few > 0 && pa::launch_linear_recurrent(D, p, stream) != cudaSuccess) return PA_ERR_CUDA;
-    if (pa::launch_linear_adds(D, c, maps, num_sms, stream) != cudaSuccess || pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
+    if (pa::launch_linear_adds(D, c, maps, num_sms, stream) != cudaSuccess ||
+        pa::launch_linear_scan(D, c, stream) != cudaSuccess ||
         pa::launch_linear_out(D, c, maps, num_sms, stream) != cudaSuccess)
         return PA_ERR_CUDA;
     return PA_OK;

@@ -195,3 +195,20 @@ def test_one_sequence_far_below_the_bound(n):
         prefix(c, max_new=5000)
         assert status() == 0
         c.check(c.out, c.states)
+
+
+@pytest.mark.parametrize("heads,hkv,dim", [(24, 4, 256), (32, 8, 128), (12, 12, 64)])
+def test_blocks_of_one_token_in_their_second_half_repeat(heads, hkv, dim):
+    """Rows that do next to nothing in a block's first step run ahead of the products; the outputs stay the same."""
+    c = S.LinearCase([129, 385, 128, 131, 257] * 6, heads, hkv, dim, ctx=[0, 5, 0, 0, 9] * 6, seed=dim)
+    states = c.states.clone()
+    first = None
+    for _ in range(6):
+        c.states.copy_(states)
+        prefix(c)
+        assert status() == 0
+        if first is None:
+            c.check(c.out, c.states)
+            first = c.out.clone(), c.states.clone()
+        assert torch.equal(c.out, first[0])
+        assert torch.equal(c.states.nan_to_num(nan=-9.0), first[1].nan_to_num(nan=-9.0))
