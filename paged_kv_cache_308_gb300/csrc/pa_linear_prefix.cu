@@ -963,7 +963,10 @@ __global__ void __launch_bounds__(OutShape<D>::kThreads, OutShape<D>::kCtas)
             // simply go by it, and the accumulator is not touched.
             const float state = u.inter ? (float)u.exponent + u.l2 * (float)(i + 1) : 0.f;
             float level = u.inter ? fminf(fmaxf(state, -6.f), 60.f) : 0.f;
-            const float least = u.inter ? state - 60.f : -200.f;  // below which the state's part could overflow
+            // The level stays where nothing overflows: the state's part (from state - 60 on), and 2^-level itself, the
+            // factor of keys next to the row, whose scores may be 0 (and of an accumulator that holds nothing yet).  At
+            // -119 the smallest largest score, 2^-126, is still a normal number of fp16, 2^-7.
+            const float least = u.inter ? fmaxf(state - 60.f, -119.f) : -119.f;
             float pending = u.inter ? state - level : 0.f;        // by how much the accumulator is behind
             bool set = false;
             float within[8];  // decays inside a group of 8 keys

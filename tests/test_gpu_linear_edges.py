@@ -1,0 +1,67 @@
+"""Linear attention where decays, zeros and infinities leave little or nothing of a token: against the recurrence in
+float64."""
+import math
+
+import pytest
+import torch
+
+import step_helpers as S
+from paged_kv_cache_308_gb300 import binding as pb
+
+pytestmark = pytest.mark.gpu
+
+
+def status():
+    torch.cuda.synchronize()
+    return pb.pa_get_device_status()
+
+
+def prefix(c, max_new=None, **kw):
+    pb.pa_linear_prefix(c.out, c.q, c.k, c.v, c.states, c.slots, c.g, c.ctx_lens, c.loc, c.scale,
+                        max_query_len=max(c.new + [1]) if max_new is None else max_new, **kw)
+
+
+def check_out(c):
+    """Every sequence's outputs against their reference."""
+    loc = c.loc.tolist()
+    for b in range(len(c.new)):
+        rows, slot = slice(loc[b], loc[b + 1]), int(c.slots[b])
+        s0 = c.before[slot] if c.ctx[b] > 0 else torch.zeros_like(c.before[slot])
+        o, _, ob, _ = S.linear(c.q[rows], c.k[rows], c.v[rows], s0, c.g, c.scale)
+        got = c.out[rows]
+        # Half of fp16's last step beyond its largest value is 65520: what is within its bound of o and past that
+        # on either side rounds to the infinity of that side (o itself may have the other sign, where the bound of a
+        # difference of large products spans both).
+        rounded = (got == math.inf) & (o + ob >= 65520.0) | (got == -math.inf) & (o - ob <= -65520.0)
+        S.check(torch.where(rounded, 0.0, got), torch.where(rounded, 0.0, o), ob, f"sequence {b} out")
+
+
+# Keys that are 0 from some token on: the rows behind have scores of 0 next to them and a largest one that falls by
+# the decay down to 2^-126 and below, in a row's own 128 keys (g up to -0.7) and in those before (-0.5, -0.36).
+# A scale of 2^96 brings what is 2^-112 into fp16; what is below 2^-126, which 32 bits may drop, stays below half of
+# its smallest step.
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g", [-6.0, -3.0, -1.0, -0.7, -0.5, -0.36])
+@pytest.mark.parametrize("scale", [0.1, 2.0 ** 96])
+def test_zero_keys_behind_others(g, dim, scale):
+    new = [256, 250, 256, 250, 256, 130]
+    c = S.LinearCase(new, 4, 2, dim, ctx=[0, 0, 0, 3, 3, 3], g=[g, g / 2], seed=51, scale=scale)
+    loc = c.loc.tolist()
+    for b, kept in enumerate([1, 70, 140, 1, 70, 2]):
+        c.k[loc[b] + kept:loc[b + 1]] = 0
+    prefix(c)
+    assert status() == 0
+    check_out(c)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g", [-6.0, -1.0, -0.36])
+def test_runs_of_zero_keys_between_others(g, dim):
+    """Masked tokens, in runs that end and start anywhere, over several blocks."""
+    c = S.LinearCase([700, 300], 4, 2, dim, ctx=[0, 3], g=[g, -0.01], seed=52)
+    runs = [(0, 5), (9, 130), (140, 255), (258, 400), (401, 690), (700, 705), (710, 996)]
+    for lo, hi in runs:
+        c.k[lo:hi] = 0
+    prefix(c)
+    assert status() == 0
+    check_out(c)
