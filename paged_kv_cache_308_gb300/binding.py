@@ -837,7 +837,7 @@ def pa_kv_alloc(block_tables, free_blocks, free_count, context_lens, query_lens,
     free_count / new_free_count [1] (None: in place); held_lens (None: context_lens), context_lens,
     query_lens and the output seq_lens [num_seqs]; the outputs query_start_loc [num_seqs + 1], slot_map
     and positions [num_tokens] (-1 behind the last token)."""
-    dev = block_tables.get_device()
+    dev = _on_gpu("block_tables", block_tables)
     B, T, nb = context_lens.shape[0], slot_map.shape[0], free_blocks.shape[0]
     table, cols = _table("block_tables", block_tables, B, dev)
     count = _ints("free_count", free_count, 1, dev)
@@ -849,6 +849,14 @@ def pa_kv_alloc(block_tables, free_blocks, free_count, context_lens, query_lens,
                        _ints("slot_map", slot_map, T, dev), _ints("positions", positions, T, dev), nb, B, T, cols,
                        int(block_size))
     _call("pa_kv_alloc", dev, stream, lib.pa_kv_alloc, args)
+
+
+def _on_gpu(name, t):
+    """The device of a call's first tensor, which the others have to be on too."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return dev
 
 
 def _ints(name, t, n, dev):
@@ -878,7 +886,7 @@ def pa_kv_put(q_out, k_out, q, k, v, k_cache, v_cache, slot_map, positions, cos_
     head_dim] (inputs may be parts of a joint projection's rows); q_out and k_out may be q and k,
     k_out may be None.  cos_sin: float32 [max_positions, rotary_dim], cosines then sines.  k_cache and
     v_cache None: rotation only; v and slot_map are then not used and may be None."""
-    dev = q.get_device()
+    dev = _on_gpu("q", q)
     T, H, dim = q.shape
     hkv = k.shape[1]
     q_shape, k_shape = (T, H, dim), (T, hkv, dim)
@@ -921,7 +929,7 @@ def pa_linear_decode(out, q, k, v, states, slots, log_decay, scale, stream=None)
     q / out: float16 [num_seqs, num_heads, head_dim]; k / v: [num_seqs, num_kv_heads, head_dim];
     states: float32 [num_slots, num_kv_heads, head_dim, head_dim], in place; slots: int32 [num_seqs]
     (negative: none); log_decay: float32 [num_kv_heads], <= 0."""
-    dev = q.get_device()
+    dev = _on_gpu("q", q)
     state = _linear_state(states, dev)
     B, H = q.shape[0], q.shape[1]
     hkv, dim = state[2], state[3]
@@ -947,7 +955,7 @@ def pa_linear_prefix(out, q, k, v, states, slots, log_decay, context_lens, query
     states, slots and log_decay as for pa_linear_decode; context_lens: int32 [num_seqs], 0 where the
     sequence has no state yet; query_start_loc: int32 [num_seqs + 1].  `workspace`: a tensor of
     pa_linear_prefix_workspace_size bytes (None: one from the allocator)."""
-    dev = q.get_device()
+    dev = _on_gpu("q", q)
     state = _linear_state(states, dev)
     T, H, B = q.shape[0], q.shape[1], context_lens.shape[0]
     hkv, dim = state[2], state[3]
