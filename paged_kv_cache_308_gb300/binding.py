@@ -872,9 +872,12 @@ def _rows(name, t, shape, dev):
         _bad(name, t, torch.float16, shape, dev)
     if t.is_contiguous():
         return t.data_ptr(), 0
+    step = t.stride(0)
     if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
         _bad(name, t, torch.float16, shape, dev)
-    return t.data_ptr(), t.stride(0)
+    if step < shape[1] * shape[2]:  # (0, a row for all tokens, would read as contiguous)
+        raise ValueError(f"{name}'s tokens must not share memory, got strides {list(t.stride())}")
+    return t.data_ptr(), step
 
 
 def pa_kv_put(q_out, k_out, q, k, v, k_cache, v_cache, slot_map, positions, cos_sin, stream=None, *,

@@ -34,3 +34,34 @@ def test_cpu_tensors_are_refused(reached):
     with pytest.raises(ValueError, match="q must be"):
         pb.pa_linear_prefix(q, q, k, k, states, ints(1), g, ints(1), ints(2), 1.0, max_query_len=3)
     assert reached == []
+
+
+@pytest.fixture
+def as_on_gpu(monkeypatch):
+    """Every tensor says that it is on device 0."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+
+
+# one token's row for all of them; rows that overlap the next
+def spread(x, step, T=5):
+    return x.as_strided((T,) + x.shape[1:], (step,) + x.stride()[1:])
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+@pytest.mark.parametrize("step", [0, 8, 64])
+def test_put_refuses_tokens_that_share_memory(reached, as_on_gpu, which, step):
+    t = dict(q=rows(5, 4, 64), k=rows(5, 2, 64), v=rows(5, 2, 64))
+    t[which] = spread(t[which], step)
+    caches = rows(2, 2, 16, 64), rows(2, 2, 16, 64)
+    with pytest.raises(ValueError, match=which):
+        pb.pa_kv_put(rows(5, 4, 64), rows(5, 2, 64), t["q"], t["k"], t["v"], *caches, ints(5), ints(5), torch.zeros(8, 64))
+    assert reached == []
+
+
+def test_put_takes_rows_of_a_joint_projection_and_single_tokens(reached, as_on_gpu):
+    joint = rows(5, 8, 64)
+    caches = rows(2, 2, 16, 64), rows(2, 2, 16, 64)
+    for T, step in ((5, 512), (1, 0), (1, 8), (0, 512)):
+        q, k, v = (spread(joint[:, a:b], step, T) for a, b in ((0, 4), (4, 6), (6, 8)))
+        pb.pa_kv_put(rows(T, 4, 64), None, q, k, v, *caches, ints(T), ints(T), torch.zeros(8, 64))
+    assert reached == ["pa_kv_put"] * 4
