@@ -97,11 +97,13 @@ int check_put(const pa_kv_put_args* a) {
     auto span = [&](int i) { return (T - 1) * (stride[i] ? stride[i] : row[i]) + row[i]; };
     const Words out[] = {halves(a->q_out, T * row[0]), halves(a->k_out, T * row[1]), halves(c.k_cache, cached),
                          halves(c.v_cache, cached)};
-    const Words in[] = {halves(a->q, span(0)), halves(a->k, span(1)), halves(c.k_cache ? a->v : nullptr, span(2))};
+    const Words in[] = {halves(a->q, span(0)), halves(a->k, span(1)), halves(c.k_cache ? a->v : nullptr, span(2)),
+                        {c.k_cache ? a->slot_map : nullptr, T}, {a->positions, T},
+                        {a->cos_sin, (long long)a->max_positions * a->rotary_dim}};
     for (int i = 0; i < 4; ++i) {
         for (int j = 0; j < i; ++j)
             if (overlap(out[i], out[j])) return PA_ERR_INVALID_ARG;
-        for (int j = 0; j < 3; ++j)
+        for (int j = 0; j < 6; ++j)
             if (!(i == j && i < 2 && out[i].p == in[j].p) && overlap(out[i], in[j])) return PA_ERR_INVALID_ARG;
     }
     return PA_OK;

@@ -1,4 +1,6 @@
 """What the binding and the C interface of a serving step's calls refuse before anything reaches a GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -65,3 +67,27 @@ def test_put_takes_rows_of_a_joint_projection_and_single_tokens(reached, as_on_g
         q, k, v = (spread(joint[:, a:b], step, T) for a, b in ((0, 4), (4, 6), (6, 8)))
         pb.pa_kv_put(rows(T, 4, 64), None, q, k, v, *caches, ints(T), ints(T), torch.zeros(8, 64))
     assert reached == ["pa_kv_put"] * 4
+
+
+# ---- the C interface: outputs over arrays that a call reads
+
+FAKE = 0x100000  # aligned addresses that no call dereferences
+FAR = 1 << 28
+
+
+def put_code(strides=(0, 0, 0), **over):
+    at = {n: FAKE + (i + 1) * FAR for i, n in enumerate(["kc", "vc", "q_out", "k_out", "q", "k", "v", "slots", "pos", "cs"])}
+    at.update({n: at[x] + off for n, (x, off) in over.items()})
+    cache = pb.pa_kv_cache(at["kc"], at["vc"], 0, 0, 10, 2, 16 * 8, 16, pb.PA_KV_F16)
+    a = pb.pa_kv_put_args(cache, at["q_out"], at["k_out"], at["q"], at["k"], at["v"], at["slots"], at["pos"], at["cs"],
+                          *strides, 4, 8, 128, 100, 0)
+    return pb.lib.pa_kv_put(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("out,size", [("q_out", 4 * 8 * 256), ("k_out", 4 * 2 * 256), ("kc", 10 * 2 * 16 * 256), ("vc", 10 * 2 * 16 * 256)])
+@pytest.mark.parametrize("array", ["slots", "pos", "cs"])
+def test_put_outputs_over_slots_positions_and_factors(out, size, array):
+    assert put_code(**{array: (out, 0)}) == pb.PA_ERR_INVALID_ARG
+    assert put_code(**{array: (out, size - 16)}) == pb.PA_ERR_INVALID_ARG
+    if array == "cs":
+        assert put_code(**{out: (array, 100 * 128 * 4 - 16)}) == pb.PA_ERR_INVALID_ARG
