@@ -780,8 +780,8 @@ int pa_kv_alloc(const pa_kv_alloc_args* args, pa_stream_t stream);
  * written, the second treated as padding.  Two tokens with one slot leave an
  * unspecified mix of both.  q, k and v may have other distances between tokens
  * than num_heads * head_dim elements (a row of a joint projection): q_stride,
- * k_stride and v_stride, multiples of 8, 0 for contiguous tokens (in place only
- * for these).  But for q_out on q and k_out on k no output may overlap another
+ * k_stride and v_stride, multiples of 8 below 2^31, 0 for contiguous tokens (in
+ * place only for these).  But for q_out on q and k_out on k no output may overlap another
  * one or an input. */
 typedef struct {
     pa_kv_cache cache;           /* PA_KV_F16; scales not used */

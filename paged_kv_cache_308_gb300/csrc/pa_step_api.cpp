@@ -83,6 +83,8 @@ int check_put(const pa_kv_put_args* a) {
     if (c.num_blocks >= (1ll << 31) / pa::kBlockSize || a->num_heads > 65535 || c.num_kv_heads > 16384 ||
         a->num_tokens > kMaxTokens)
         return PA_ERR_UNSUPPORTED;
+    // (so that no array's extent passes 64 bits)
+    if (std::max({stride[0], stride[1], stride[2]}) >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     if (a->num_tokens == 0) return PA_OK;
     if (bad_ptr(a->q, 16) || bad_ptr(a->k, 16) || bad_ptr(a->q_out, 16) || !aligned(a->k_out, 16) ||
         bad_ptr(a->positions, 4) || (a->rotary_dim > 0 && bad_ptr(a->cos_sin, 16)))

@@ -91,3 +91,9 @@ def test_put_outputs_over_slots_positions_and_factors(out, size, array):
     assert put_code(**{array: (out, size - 16)}) == pb.PA_ERR_INVALID_ARG
     if array == "cs":
         assert put_code(**{out: (array, 100 * 128 * 4 - 16)}) == pb.PA_ERR_INVALID_ARG
+
+
+def test_put_strides_past_32_bits():
+    for i in range(3):
+        for far in (1 << 31, (1 << 62) + 8, (1 << 63) - 8):
+            assert put_code(strides=[far if j == i else 0 for j in range(3)]) == pb.PA_ERR_UNSUPPORTED
