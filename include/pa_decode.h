@@ -826,8 +826,8 @@ int pa_kv_put(const pa_kv_put_args* args, pa_stream_t stream);
  * A NaN or infinity in a token's v reaches this token's outputs and later
  * ones of its sequence and kv head, in its own column of v only; no other.  One
  * in k reaches them in all columns, where pa_linear_prefix may make NaN what
- * would be an infinity token by token; one in q, this token's and head's.  Outputs
- * and states must not overlap each other or the inputs. */
+ * would be an infinity token by token; one in q, this token's and head's.  Outputs,
+ * states and workspace must not overlap each other or the inputs. */
 typedef struct {
     float* states;               /* [num_slots][num_kv_heads][head_dim][head_dim], in place */
     int64_t num_slots;           /* below 2^31 */

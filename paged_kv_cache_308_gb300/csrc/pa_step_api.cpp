@@ -6,6 +6,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <iterator>
 
 #include "pa_kv.h"
 #include "pa_step.h"
@@ -121,8 +123,9 @@ int check_linear(const pa_linear_state& s, int num_heads, float scale) {
     return PA_OK;
 }
 
+// `read` is what else the call reads, `ws` its workspace.
 template <typename Args>
-bool bad_linear_pointers(const Args& a, long long tokens) {
+bool bad_linear_pointers(const Args& a, long long tokens, std::initializer_list<Words> read = {}, const Words& ws = {}) {
     if (bad_ptr(a.out, 16) || bad_ptr(a.q, 16) || bad_ptr(a.k, 16) || bad_ptr(a.v, 16) || bad_ptr(a.state.states, 16) ||
         bad_ptr(a.log_decay, 4) || bad_ptr(a.slots, 4))
         return true;
@@ -131,12 +134,12 @@ bool bad_linear_pointers(const Args& a, long long tokens) {
     const Words states{a.state.states, std::min(a.state.num_slots * K * D * D, 1ll << 60)};
     const Words in[] = {halves(a.q, tokens * a.num_heads * D), halves(a.k, tokens * K * D), halves(a.v, tokens * K * D),
                         {a.log_decay, K}, {a.slots, a.num_seqs}};
-    for (const Words& x : in)
-        if (overlap(out, x) || overlap(states, x)) return true;
-    return overlap(out, states);
+    auto written = [&](const Words& x) { return overlap(out, x) || overlap(states, x) || overlap(ws, x); };
+    return std::any_of(std::begin(in), std::end(in), written) || std::any_of(read.begin(), read.end(), written) ||
+           overlap(out, states) || overlap(ws, out) || overlap(ws, states);
 }
 
-int check_linear_prefix(const pa_linear_prefix_args* a) {
+int check_linear_prefix(const pa_linear_prefix_args* a, const void* ws) {
     if (!a) return PA_ERR_INVALID_ARG;
     if (a->num_seqs < 0 || a->num_seqs > 65535 || a->num_tokens < 0 || a->max_query_len < 0) return PA_ERR_INVALID_ARG;
     int rc = check_linear(a->state, a->num_heads, a->scale);
@@ -144,7 +147,12 @@ int check_linear_prefix(const pa_linear_prefix_args* a) {
     if (a->num_tokens > kMaxTokens) return PA_ERR_UNSUPPORTED;
     if (a->num_tokens > 0 && a->max_query_len == 0) return PA_ERR_INVALID_ARG;
     if (a->num_seqs == 0 || a->num_tokens == 0) return PA_OK;
-    if (bad_linear_pointers(*a, a->num_tokens) || bad_ptr(a->context_lens, 4) || bad_ptr(a->query_start_loc, 4))
+    const size_t need = pa_linear_prefix_workspace_size(a->num_seqs, a->num_tokens, a->max_query_len, a->num_heads,
+                                                        a->state.num_kv_heads, a->state.head_dim);
+    if (bad_ptr(a->context_lens, 4) || bad_ptr(a->query_start_loc, 4) ||
+        bad_linear_pointers(*a, a->num_tokens,
+                            {{a->context_lens, a->num_seqs}, {a->query_start_loc, a->num_seqs + 1ll}},
+                            {ws, (long long)(need / 4)}))
         return PA_ERR_INVALID_ARG;
     return PA_OK;
 }
@@ -303,7 +311,7 @@ size_t pa_linear_prefix_workspace_size(int num_seqs, int num_tokens, int max_que
 }
 
 int pa_linear_prefix(const pa_linear_prefix_args* a, void* ws, size_t ws_bytes, pa_stream_t stream_) {
-    int rc = check_linear_prefix(a);
+    int rc = check_linear_prefix(a, ws);
     if (rc || a->num_seqs == 0 || a->num_tokens == 0) return rc;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int D = a->state.head_dim, K = a->state.num_kv_heads;

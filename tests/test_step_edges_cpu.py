@@ -97,3 +97,36 @@ def test_put_strides_past_32_bits():
     for i in range(3):
         for far in (1 << 31, (1 << 62) + 8, (1 << 63) - 8):
             assert put_code(strides=[far if j == i else 0 for j in range(3)]) == pb.PA_ERR_UNSUPPORTED
+
+
+def linear_code(fn, hkv=4, max_q=5, **over):
+    at = {n: FAKE + (i + 1) * FAR for i, n in enumerate(["states", "out", "q", "k", "v", "g", "slots", "ctx", "loc", "ws"])}
+    at.update({n: at[x] + off for n, (x, off) in over.items()})
+    state = pb.pa_linear_state(at["states"], 5, hkv, 128)
+    if fn == "pa_linear_decode":
+        a = pb.pa_linear_decode_args(at["out"], at["q"], at["k"], at["v"], state, at["g"], at["slots"], 10, 8, 0.1)
+        return pb.lib.pa_linear_decode(ctypes.byref(a), None)
+    a = pb.pa_linear_prefix_args(at["out"], at["q"], at["k"], at["v"], state, at["g"], at["slots"], at["ctx"], at["loc"], 3, 10,
+                                 max_q, 8, 0.1)
+    return pb.lib.pa_linear_prefix(ctypes.byref(a), at["ws"], pb.lib.pa_linear_prefix_workspace_size(3, 10, max_q, 8, hkv, 128), None)
+
+
+LINEAR_SIZES = dict(out=10 * 8 * 256, states=5 * 4 * 128 * 128 * 4, q=10 * 8 * 256, k=10 * 4 * 256, v=10 * 4 * 256, g=16, slots=12,
+                    ctx=12, loc=16)
+
+
+@pytest.mark.parametrize("out", ["out", "states"])
+@pytest.mark.parametrize("array", ["ctx", "loc"])
+@pytest.mark.parametrize("max_q", [5, 20])
+def test_linear_outputs_over_lengths(out, array, max_q):
+    for off in (0, LINEAR_SIZES[out] - 4):
+        assert linear_code("pa_linear_prefix", max_q=max_q, **{array: (out, off)}) == pb.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("array", sorted(LINEAR_SIZES))
+def test_linear_workspace_over_other_arrays(array):
+    need = pb.lib.pa_linear_prefix_workspace_size(3, 10, 20, 8, 4, 128)
+    assert need % 256 == 0
+    assert linear_code("pa_linear_prefix", max_q=20, **{array: ("ws", 0)}) == pb.PA_ERR_INVALID_ARG
+    assert linear_code("pa_linear_prefix", max_q=20, **{array: ("ws", need - 256)}) == pb.PA_ERR_INVALID_ARG
+    assert linear_code("pa_linear_prefix", max_q=20, ws=(array, (LINEAR_SIZES[array] - 1) // 256 * 256)) == pb.PA_ERR_INVALID_ARG
