@@ -730,6 +730,8 @@ int pa_kv_evict(const pa_kv_evict_args* args, pa_stream_t stream);
  *   slot_map          [num_tokens]: block * block_size + place in the block, for
  *                     each new token in the order of query_start_loc
  *   positions         [num_tokens]: its position in its sequence
+ *   new_held_lens     [num_seqs]: the tokens whose blocks its row holds now, the
+ *                     next call's held_lens
  * with -1 in both for rows from query_start_loc[num_seqs] on (padding).
  * When blocks run out (PA_DEV_NO_BLOCKS) the sequences up to the last one that
  * can be served are: from there on one that needs blocks gets none, seq_lens is
@@ -737,9 +739,16 @@ int pa_kv_evict(const pa_kv_evict_args* args, pa_stream_t stream);
  * sequence whose lengths are out of range (PA_DEV_BAD_SEQ_LEN: negative, context
  * above held, more blocks than a row has) keeps its row, with seq_lens 0, slots
  * -1 and positions unspecified; runs that end past num_tokens are cut there
- * (PA_DEV_BAD_SEQ_LEN).  Where free_count is outside [0, num_blocks], or more blocks come back than there
- * are, no block moves (PA_DEV_NO_BLOCKS).  Each block belongs in one row only.
- * The outputs must not overlap each other or the inputs, but for new_free_count.
+ * (PA_DEV_BAD_SEQ_LEN).  Where free_count is outside [0, num_blocks], or more
+ * blocks come back than there are, no block moves (PA_DEV_NO_BLOCKS).
+ * new_held_lens is context + query where a sequence was served and its blocks
+ * moved, and its held_lens where not: a sequence that shrinks and grows in one
+ * step, is not served and has fewer seq_lens than it holds blocks for keeps them
+ * all, and gives them back only to a later call that gets these held_lens.  (A
+ * caller without new_held_lens keeps the old held_lens for those whose seq_lens
+ * is not context + query.)  Each block belongs in one row only.
+ * The outputs must not overlap each other or the inputs, but for new_free_count
+ * on free_count and new_held_lens on held_lens.
  * num_blocks * block_size < 2^31; lengths and num_tokens up to 2^30. */
 typedef struct {
     int32_t* block_tables;       /* [num_seqs][max_blocks_per_seq], in place */
@@ -758,6 +767,7 @@ typedef struct {
     int num_tokens;
     int max_blocks_per_seq;
     int block_size;
+    int32_t* new_held_lens;      /* [num_seqs]; may be held_lens; NULL: not written */
 } pa_kv_alloc_args;
 
 int pa_kv_alloc(const pa_kv_alloc_args* args, pa_stream_t stream);

@@ -157,7 +157,7 @@ class pa_kv_alloc_args(ctypes.Structure):
         ("query_lens", ctypes.c_void_p), ("query_start_loc", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
         ("slot_map", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
         ("num_seqs", ctypes.c_int), ("num_tokens", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int),
-        ("block_size", ctypes.c_int),
+        ("block_size", ctypes.c_int), ("new_held_lens", ctypes.c_void_p),
     ]
 
 
@@ -830,13 +830,16 @@ _ALLOC, _PUT, _LDECODE, _LPREFIX = (_packer(c) for c in (pa_kv_alloc_args, pa_kv
 
 def pa_kv_alloc(block_tables, free_blocks, free_count, context_lens, query_lens, query_start_loc, seq_lens, slot_map,
                 positions, stream=None, *, held_lens: Optional[torch.Tensor] = None,
-                new_free_count: Optional[torch.Tensor] = None, block_size: int = 16) -> None:
+                new_free_count: Optional[torch.Tensor] = None, new_held_lens: Optional[torch.Tensor] = None,
+                block_size: int = 16) -> None:
     """Hand out and take back cache blocks, and build slot map and positions (see include/pa_decode.h).
 
     All int32: block_tables [num_seqs, max_blocks_per_seq] and free_blocks [num_blocks] in place;
     free_count / new_free_count [1] (None: in place); held_lens (None: context_lens), context_lens,
     query_lens and the output seq_lens [num_seqs]; the outputs query_start_loc [num_seqs + 1], slot_map
-    and positions [num_tokens] (-1 behind the last token)."""
+    and positions [num_tokens] (-1 behind the last token); new_held_lens [num_seqs] (None: not written;
+    may be held_lens) the next call's held_lens, where a sequence that gets no blocks, or has bad lengths,
+    keeps those it holds."""
     dev = _on_gpu("block_tables", block_tables)
     B, T, nb = context_lens.shape[0], slot_map.shape[0], free_blocks.shape[0]
     table, cols = _table("block_tables", block_tables, B, dev)
@@ -847,7 +850,8 @@ def pa_kv_alloc(block_tables, free_blocks, free_count, context_lens, query_lens,
                        _ints("context_lens", context_lens, B, dev), _ints("query_lens", query_lens, B, dev),
                        _ints("query_start_loc", query_start_loc, B + 1, dev), _ints("seq_lens", seq_lens, B, dev),
                        _ints("slot_map", slot_map, T, dev), _ints("positions", positions, T, dev), nb, B, T, cols,
-                       int(block_size))
+                       int(block_size),
+                       0 if new_held_lens is None else _ints("new_held_lens", new_held_lens, B, dev))
     _call("pa_kv_alloc", dev, stream, lib.pa_kv_alloc, args)
 
 

@@ -57,7 +57,7 @@ __device__ __forceinline__ Seq seq_of(const KvAllocParams& prm, int b) {
     Seq s;
     s.context = __ldg(prm.context + b);
     s.query = __ldg(prm.query + b);
-    const int held = __ldg(prm.held + b);
+    const int held = prm.held[b];  // (which may become new_held)
     const long long room = min((long long)prm.cols * kBlockSize, 1ll << 30);
     s.bad = s.context < 0 || s.query < 0 || held < s.context || held > room || (long long)s.context + s.query > room;
     s.n0 = s.bad ? 0 : (held + kBlockSize - 1) / kBlockSize;
@@ -195,9 +195,16 @@ __global__ void __launch_bounds__(kAllocThreads) kv_alloc_kernel(const KvAllocPa
     if (status && rank == 0) atomicOr(prm.status, status);
     const int end = (int)min(total.query, (long long)prm.num_tokens);
     if (rank == 0 && t == 0) prm.loc[B] = end;
-    cluster.sync();  // every block has read the count
+    cluster.sync();  // every block has read the count and the lengths
 
     if (rank == 0 && t == 0) *prm.new_count = bad_pool ? count : (int)(top - (long long)taken_sm);
+    if (prm.new_held) {
+        for (int b = b0 + t; b < b1; b += kAllocThreads) {
+            const Seq s = seq_of(prm, b);
+            const bool moved = kept[b - k0].before >= 0 && (!bad_pool || s.n0 == s.n1);
+            prm.new_held[b] = moved ? s.context + s.query : prm.held[b];
+        }
+    }
     if (!bad_pool && total.back > 0) {
         for (int b = b0 + warp; b < b1; b += kWarps) {
             const int held = kept[b - k0].held;

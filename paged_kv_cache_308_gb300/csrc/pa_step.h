@@ -20,6 +20,7 @@ struct KvAllocParams {
     const int32_t* query;
     int32_t* loc;
     int32_t* lens;
+    int32_t* new_held;  // may be null, or held
     int32_t* slots;
     int32_t* positions;
     int num_blocks, num_seqs, num_tokens, cols;

@@ -41,7 +41,7 @@ int check_alloc(const pa_kv_alloc_args* a) {
     if (bad_ptr(a->free_count, 4) || bad_ptr(a->new_free_count, 4) || bad_ptr(a->query_start_loc, 4))
         return PA_ERR_INVALID_ARG;
     if (a->num_seqs > 0 && (bad_ptr(a->context_lens, 4) || bad_ptr(a->query_lens, 4) || bad_ptr(a->seq_lens, 4) ||
-                            !aligned(a->held_lens, 4)))
+                            !aligned(a->held_lens, 4) || !aligned(a->new_held_lens, 4)))
         return PA_ERR_INVALID_ARG;
     if (a->num_seqs > 0 && a->max_blocks_per_seq > 0 && bad_ptr(a->block_tables, 4)) return PA_ERR_INVALID_ARG;
     if (a->num_blocks > 0 && bad_ptr(a->free_blocks, 4)) return PA_ERR_INVALID_ARG;
@@ -52,15 +52,18 @@ int check_alloc(const pa_kv_alloc_args* a) {
                          {a->new_free_count, 1},
                          {a->query_start_loc, B + 1},
                          {a->seq_lens, B},
+                         {a->new_held_lens, B},
                          {a->slot_map, a->num_tokens},
                          {a->positions, a->num_tokens}};
     const Words in[] = {{a->free_count, 1}, {a->held_lens, B}, {a->context_lens, B}, {a->query_lens, B}};
     for (const Words& o : out) {
         for (const Words& x : out)
             if (&x != &o && overlap(o, x)) return PA_ERR_INVALID_ARG;
-        for (const Words& x : in)  // (the new count may take the old one's place)
-            if (!(o.p == a->new_free_count && x.p == o.p && x.p == a->free_count) && overlap(o, x))
-                return PA_ERR_INVALID_ARG;
+        for (const Words& x : in) {  // (the new count and the new held_lens may take the old ones' place)
+            const bool in_place = x.p == o.p && ((o.p == a->new_free_count && x.p == a->free_count) ||
+                                                 (o.p == a->new_held_lens && x.p == a->held_lens));
+            if (!in_place && overlap(o, x)) return PA_ERR_INVALID_ARG;
+        }
     }
     return PA_OK;
 }
@@ -220,6 +223,7 @@ int pa_kv_alloc(const pa_kv_alloc_args* a, pa_stream_t stream) {
     p.query = a->query_lens;
     p.loc = a->query_start_loc;
     p.lens = a->seq_lens;
+    p.new_held = a->new_held_lens;
     p.slots = a->slot_map;
     p.positions = a->positions;
     p.num_blocks = static_cast<int>(a->num_blocks);

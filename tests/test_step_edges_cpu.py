@@ -130,3 +130,24 @@ def test_linear_workspace_over_other_arrays(array):
     assert linear_code("pa_linear_prefix", max_q=20, **{array: ("ws", 0)}) == pb.PA_ERR_INVALID_ARG
     assert linear_code("pa_linear_prefix", max_q=20, **{array: ("ws", need - 256)}) == pb.PA_ERR_INVALID_ARG
     assert linear_code("pa_linear_prefix", max_q=20, ws=(array, (LINEAR_SIZES[array] - 1) // 256 * 256)) == pb.PA_ERR_INVALID_ARG
+
+
+def alloc_code(**over):
+    at = {n: FAKE + (i + 1) * FAR for i, n in enumerate(["bt", "free", "count", "new_count", "held", "ctx", "q", "loc", "lens",
+                                                         "slots", "pos", "new_held"])}
+    at.update({n: (at[x] if x else 0) + off for n, (x, off) in over.items()})
+    new_held = at.pop("new_held")
+    a = pb.pa_kv_alloc_args(*at.values(), 100, 4, 10, 8, 16, new_held)
+    return pb.lib.pa_kv_alloc(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("array,size", [("bt", 128), ("free", 400), ("count", 4), ("new_count", 4), ("ctx", 16), ("q", 16),
+                                        ("loc", 20), ("lens", 16), ("slots", 40), ("pos", 40), ("held", 16)])
+def test_new_held_lens_over_other_arrays(array, size):
+    if array != "held":
+        assert alloc_code(new_held=(array, 0)) == pb.PA_ERR_INVALID_ARG
+    assert alloc_code(new_held=(array, size - 4)) == pb.PA_ERR_INVALID_ARG
+    assert alloc_code(new_held=(array, -12)) == pb.PA_ERR_INVALID_ARG
+    assert alloc_code(new_held=("new_held", 2)) == pb.PA_ERR_INVALID_ARG
+    # without held_lens, the context lengths are no place for it either
+    assert alloc_code(held=(None, 0), new_held=("ctx", 0)) == pb.PA_ERR_INVALID_ARG
