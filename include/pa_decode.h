@@ -835,8 +835,10 @@ int pa_kv_put(const pa_kv_put_args* args, pa_stream_t stream);
  * NaN sets PA_DEV_BAD_DECAY; its head's outputs and states are then unspecified.
  * A NaN or infinity in a token's v reaches this token's outputs and later
  * ones of its sequence and kv head, in its own column of v only; no other.  One
- * in k reaches them in all columns, where pa_linear_prefix may make NaN what
- * would be an infinity token by token; one in q, this token's and head's.  Outputs,
+ * in k reaches them in all columns; one in q, this token's and head's.  An
+ * infinite entry of a state stays one (until its decay is 0 in 32 bits), and its
+ * column's outputs are not finite.  pa_linear_prefix may make NaN of an infinity
+ * of the outputs, and of a state that one in its own tokens reaches.  Outputs,
  * states and workspace must not overlap each other or the inputs. */
 typedef struct {
     float* states;               /* [num_slots][num_kv_heads][head_dim][head_dim], in place */

@@ -4,6 +4,7 @@
 #include "pa_decode.h"
 
 #include "pa_device.cuh"
+#include "pa_linear.cuh"
 #include "pa_step.h"
 
 namespace pa {
@@ -21,16 +22,6 @@ struct Slice {
     static constexpr int kRows = kThreads / kLanes;       // rows at a time
     static constexpr int kPasses = D / kRows;
 };
-
-// What a state is multiplied by for one token: S -> S * whole + S * rest, where
-// exp(g) - 1 in 32 bits has what exp(g) loses next to 1.
-struct Decay {
-    float whole, rest;
-};
-__device__ __forceinline__ Decay decay_of(float g) {
-    if (g > -0.5f) return {1.f, expm1f(g)};
-    return {0.f, expf(g)};
-}
 
 // Two 32-bit numbers a register pair, for the instructions that take two at a time.
 typedef unsigned long long Two;
@@ -130,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D>) linear_recurrent_ke
             for (int j = 0; j < 4; ++j) {
                 const float kk = j == 0 ? k4.x : j == 1 ? k4.y : j == 2 ? k4.z : k4.w;
                 ulonglong2& x = s[i + j];
-                x.x = fma2(two(kk, kk), va, fma2(x.x, rest, mul2(x.x, whole)));
-                x.y = fma2(two(kk, kk), vb, fma2(x.y, rest, mul2(x.y, whole)));
+                x.x = fma2(two(kk, kk), va, fma2(x.x, whole, mul2(x.x, rest)));
+                x.y = fma2(two(kk, kk), vb, fma2(x.y, whole, mul2(x.y, rest)));
             }
         }
 #pragma unroll

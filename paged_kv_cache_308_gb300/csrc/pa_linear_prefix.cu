@@ -25,6 +25,7 @@
 #include "pa_decode.h"
 
 #include "pa_device.cuh"
+#include "pa_linear.cuh"
 #include "pa_step.h"
 #include "pa_tcgen05.cuh"
 
@@ -477,14 +478,7 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
     const size_t index = (size_t)(s.first / kLinearBlock + b) * p.num_kv_heads + kvh;  // of the first block
     const float4* add = reinterpret_cast<const float4*>(c.adds + index * D * D + at);
     const size_t step = (size_t)p.num_kv_heads * D * D;
-    // d^L S: next to 1 the factor less 1 is what 32 bits hold
-    float whole, rest;
-    auto set_decay = [&](int tokens) {
-        const float y = fmaxf(g, -1e4f) * (float)tokens;
-        whole = y > -0.5f ? 1.f : 0.f;
-        rest = y > -0.5f ? expm1f(y) : expf(y);
-    };
-    set_decay(kLinearBlock);
+    Decay d = decay_of(fmaxf(g, -1e4f) * (float)kLinearBlock);  // d^L
     // four blocks ahead: what a round of the loop waits for has long been asked for (eight: 8 prompts of 8192 tokens of
     // 8 x 128 43 -> 55 us, one of 4 x 256 20 either way)
     constexpr int kAhead = 4;
@@ -513,10 +507,10 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearC
             *reinterpret_cast<uint2*>(c.starts + i * D * D + at) = h;
             if (first) c.exponents[i] = e;
         }
-        if (n == blocks - 1) set_decay(s.count - n * kLinearBlock);
-        auto chain = [&](float v, float plus) { return fmaf(v, rest, v * whole) + plus; };
+        if (n == blocks - 1) d = decay_of(fmaxf(g, -1e4f) * (float)(s.count - n * kLinearBlock));
+        auto chain = [&](float v, float plus) { return fmaf(v, d.whole, v * d.rest) + plus; };
         x = make_float4(chain(x.x, a.x), chain(x.y, a.y), chain(x.z, a.z), chain(x.w, a.w));
-        bound = (bound * (whole + rest) + most) * 1.0001f;
+        bound = (bound * (d.whole + d.rest) + most) * 1.0001f;
     };
     for (int n = 0; n < blocks; n += kAhead) {
 #pragma unroll

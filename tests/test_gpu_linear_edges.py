@@ -65,3 +65,60 @@ def test_runs_of_zero_keys_between_others(g, dim):
     prefix(c)
     assert status() == 0
     check_out(c)
+
+
+def linear_without(c, b, row, col):
+    """Reference of sequence b whose state, of kv head 1, has a 0 at (row, col)."""
+    loc, slot = c.loc.tolist(), int(c.slots[b])
+    s0 = c.before[slot].clone()
+    s0[1, row, col] = 0
+    rows = slice(loc[b], loc[b + 1])
+    return S.linear(c.q[rows], c.k[rows], c.v[rows], s0, c.g, c.scale, chunked=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g", [0.0, -1e-9, -1e-6, -0.3, -0.4999, -0.5, -0.7, -30.0, -100.0])
+@pytest.mark.parametrize("call,n", [("decode", 1), ("prefix", 1), ("prefix", 5)])
+def test_infinite_states_stay_infinite_token_by_token(call, n, g, dim):
+    c = S.LinearCase([n, n], 4, 2, dim, g=[-0.2, g], seed=53)
+    row, col = 5, dim - 2
+    for b, x in enumerate((math.inf, -math.inf)):
+        c.states[int(c.slots[b]), 1, row, col] = x
+    c.before = c.states.clone()
+    if call == "decode":
+        pb.pa_linear_decode(c.out[:2], c.q[:2], c.k[:2], c.v[:2], c.states, c.slots, c.g, c.scale)
+    else:
+        prefix(c)
+    assert status() == 0
+    for b, x in enumerate((math.inf, -math.inf)):
+        o, s, ob, sb = linear_without(c, b, row, col)
+        got, state = c.out[b * n:(b + 1) * n].clone(), c.states[int(c.slots[b])].clone()
+        assert float(state[1, row, col]) == x
+        want = torch.sign(c.q[b * n:(b + 1) * n, 2:, row].float()) * x
+        assert torch.equal(got[:, 2:, col].float(), want)
+        got[:, 2:, col], state[1, row, col] = 0, 0
+        o[:, 2:, col], s[1, row, col] = 0, 0
+        S.check(got, o, ob, "out")
+        S.check(state, s, sb, "state")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g", [0.0, -1e-9, -1e-6, -0.01, -0.2])
+def test_infinite_states_stay_infinite_in_chunks(g, dim):
+    c = S.LinearCase([300, 300], 4, 2, dim, g=[-0.2, g], seed=54)
+    row, col = 5, dim - 2
+    for b, x in enumerate((math.inf, -math.inf)):
+        c.states[int(c.slots[b]), 1, row, col] = x
+    c.before = c.states.clone()
+    prefix(c)
+    assert status() == 0
+    for b, x in enumerate((math.inf, -math.inf)):
+        _, s, _, sb = linear_without(c, b, row, col)
+        state = c.states[int(c.slots[b])].clone()
+        assert float(state[1, row, col]) == x
+        state[1, row, col] = s[1, row, col] = 0
+        S.check(state, s, sb, "state")
+        bad = ~torch.isfinite(c.out[b * 300:(b + 1) * 300])
+        assert bool(bad[:, 2:, col].all())
+        bad[:, 2:, col] = False
+        assert not bool(bad.any())
