@@ -39,6 +39,18 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // floor(log2 |x|) for normal x, -127 for less, 128 for infinities
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
+// Products of two numbers at a time (one instruction), and the larger magnitude of three.
+__device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\t"
+        "mov.b64 {%0, %1}, p;\n\t}"
+        : "+r"(a), "+r"(b)
+        : "f"(x), "f"(y));
+}
+__device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return m;
+}
+
 // A sequence's rows and slot; false where there is nothing to do for it here.
 struct Seq {
     int first, count, slot, context;
@@ -340,15 +352,42 @@ __global__ void __launch_bounds__(kAddThreads, 2)
                     *reinterpret_cast<uint4*>(ks + (q >> 3) * (S::kGroup * 128) + r * 128 + (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 if (tail) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                // Tokens whose keys (of this tile) are all 0 add nothing and have no say in the power of two: masked
+                // ones may follow others that the decay has made smaller than their v's last bit.  A lane looks at two
+                // tokens, 16 bytes of each where these are not 0.
+                auto key = [&](int r, int q) {
+                    const uint4 z = *reinterpret_cast<const uint4*>(ks + (q >> 3) * (S::kGroup * 128) + r * 128 +
+                                                                    (((q & 7) ^ (r & 7)) << 4));
+                    return ((z.x | z.y | z.z | z.w) & 0x7fff7fffu) != 0;
+                };
+                bool some[2] = {key(lane, 0), key(lane + 32, 0)};
                 float a[64];
                 float m = 0.f;
                 bool bad = false;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const float v = mine && i < count ? column(vs, i) : 0.f;
-                    bad |= !(fabsf(v) <= 65504.f);
-                    a[i] = v * w[at + i];
-                    m = fmaxf(m, fabsf(a[i]));
+                for (int i = 0; i < 64; i += 2) {
+#pragma unroll
+                    for (int j = i; j < i + 2; ++j) {
+                        const float v = mine && j < count ? column(vs, j) : 0.f;
+                        bad |= !(fabsf(v) <= 65504.f);
+                        a[j] = v * w[at + j];
+                    }
+                    m = max3(m, __float_as_uint(a[i]), __float_as_uint(a[i + 1]));
+                }
+                if (!__all_sync(kFull, some[0] && some[1])) {
+                    m = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                        for (int q = 1; q < S::kTile / 8 && !some[h]; ++q) some[h] = key(h * 32 + lane, q);
+                        const unsigned live = __ballot_sync(kFull, some[h]);
+#pragma unroll
+                        for (int i = h * 32; i < h * 32 + 32; ++i) {
+                            // (0 times a NaN or an infinity stays NaN)
+                            if (!(live >> (i & 31) & 1u) && fabsf(a[i]) <= 65504.f) a[i] = 0.f;
+                            m = fmaxf(m, fabsf(a[i]));
+                        }
+                    }
                 }
                 if (bad) {  // the power of two is that of the others
                     m = 0.f;
@@ -364,7 +403,7 @@ __global__ void __launch_bounds__(kAddThreads, 2)
                 const int e = exponent_of(m);
                 const bool move = m > 0.f && (!set || e + up > 14);
                 const int was = up;
-                if (move) up = min(8 - e, 100);
+                if (move) up = min(8 - e, 118);  // (moves down by 125 at most, from there to 65504)
                 if (x >= 2) {  // the operand's buffer has been read
                     if (!(ok = tc_warp_wait(bar_mma + 8 * (x & 1), ((x - 2) >> 1) & 1, limit, failed))) break;
                     tc_fence_after();
@@ -577,18 +616,6 @@ enum : int {
                                   // starts when this one's have gone)
     kBarFull = kBarOut + 2
 };
-
-// Products of two numbers at a time (one instruction), and the larger magnitude of three.
-__device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, float x, float y) {
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\t"
-        "mov.b64 {%0, %1}, p;\n\t}"
-        : "+r"(a), "+r"(b)
-        : "f"(x), "f"(y));
-}
-__device__ __forceinline__ float max3(float m, uint32_t a, uint32_t b) {
-    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
-    return m;
-}
 
 // A grid of the CTAs that the SMs hold takes the units in turn, the two halves of a block
 // (one and two steps of 128 keys) neighbours in that order.  A unit's 128 rows are the

@@ -122,3 +122,47 @@ def test_infinite_states_stay_infinite_in_chunks(g, dim):
         assert bool(bad[:, 2:, col].all())
         bad[:, 2:, col] = False
         assert not bool(bad.any())
+
+
+# What tokens leave in the state does not depend on v of later tokens whose keys are 0, however small it has become
+# by then (2^-133 for 256 tokens of -0.36).
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("g", [-6.0, -1.0, -0.36, -0.1])
+def test_states_behind_zero_keys(g, dim):
+    new = [256, 250, 40, 700, 130, 300]
+    c = S.LinearCase(new, 4, 2, dim, ctx=[0, 3, 0, 0, 3, 0], g=[g, g / 2], seed=55)
+    loc = c.loc.tolist()
+    for b, (lo, hi) in enumerate([(1, 256), (70, 250), (3, 40), (280, 700), (5, 66), (256, 300)]):
+        c.k[loc[b] + lo:loc[b] + hi] = 0
+        if dim == 256:  # a half of the keys only
+            c.k[loc[b] + lo - 1, 0, :128] = 0
+    c.k[loc[3] + 600, 1, dim - 1] = -0.0
+    prefix(c)
+    assert status() == 0
+    for b in range(len(new)):
+        rows, slot = slice(loc[b], loc[b + 1]), int(c.slots[b])
+        s0 = c.before[slot] if c.ctx[b] > 0 else torch.zeros_like(c.before[slot])
+        _, s, _, sb = S.linear(c.q[rows], c.k[rows], c.v[rows], s0, c.g, c.scale)
+        # Decayed values of v below 2^-110 become two halves after times 2^118, the largest factor that later
+        # values up to 65504 can take back in one step: half of the second half's last step, 2^-24, is then 2^-143
+        # for each |k|.  (Seen in states of 2^-130 only.)
+        sb = sb + 2.0 ** -143 * c.k[rows].double().abs().sum(dim=0)[:, :, None]
+        S.check(c.states[slot], s, sb, f"sequence {b} state")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_non_finite_values_of_zero_keys(bad, dim):
+    """0 times what is not a number is none: as for other keys, its column's state and later outputs."""
+    c = S.LinearCase([300], 4, 2, dim, seed=56)
+    c.k[20:200] = 0
+    c.v[100, 1, 3] = bad
+    prefix(c)
+    assert status() == 0
+    slot = int(c.slots[0])
+    assert bool(c.states[slot, 1, :, 3].isnan().all())
+    want = torch.zeros_like(c.out[:300], dtype=torch.bool)
+    want[100:, 2:, 3] = True
+    assert torch.equal(~torch.isfinite(c.out[:300]), want)
+    c.states[slot, 1, :, 3] = 0
+    assert bool(torch.isfinite(c.states[slot]).all())
