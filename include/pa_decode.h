@@ -870,7 +870,14 @@ int pa_linear_decode(const pa_linear_decode_args* args, pa_stream_t stream);
  * rows from query_start_loc[num_seqs] on are neither read nor written.
  * max_query_len is a host-side bound on a sequence's new tokens.  Lengths out of
  * range set PA_DEV_BAD_SEQ_LEN and skip the sequence; where query_start_loc is out
- * of order, outputs and states of the whole batch are unspecified.  The workspace
+ * of order, outputs and states of the whole batch are unspecified.
+ * Sequences of more tokens than a few (below) go in blocks of 256 tokens on the
+ * tensor cores.  Their outputs then come from scores and from states before each
+ * block that were rounded to fp16 once; entries of such a state below 2^-22 of its
+ * largest one are off by up to 2^-33 of that (token by token, by their own 2^-24).
+ * The states that are left take each product k v to 22 bits, or to 2^-33 of |k|
+ * times the column's largest decayed v.
+ * The workspace
  * needs no initialisation and holds pa_linear_prefix_workspace_size bytes for the
  * same sizes: 0 up to 9, 14 or 24 tokens a sequence (head_dim 256, 128, 64), else about
  * 6 head_dim^2 num_kv_heads bytes for each of num_seqs + num_tokens / 256 blocks of

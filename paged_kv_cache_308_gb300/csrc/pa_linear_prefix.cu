@@ -18,10 +18,15 @@
 // Precision.  The states are 32-bit values that a user keeps, so A's operand
 // d^(L-1-i) v_i goes to the tensor cores as two halves, its nearest and the nearest
 // of the rest (22 bits), times a power of two for each column of v that brings the
-// column's largest into fp16's upper range; k is exact.  The outputs are fp16:
-// their operands d^(i-j) (q_i . k_j) and S_n are rounded once, to fp16 as the outputs
-// themselves are, also after powers of two (of a row, of a state) that take
-// overflow and underflow out of it.
+// column's largest to 2^8 or above; k is exact.  Half of the second half's last step is
+// 2^-25: what is below 2^-11 of the column's largest is off by up to 2^-33 of that.
+// The outputs are fp16: their operands d^(i-j) (q_i . k_j) and S_n are rounded once, to
+// fp16 as the outputs themselves are, also after powers of two, of a row and of a
+// whole state, that keep them from overflow.  A row's own largest score, and a state's
+// largest entry (as its blocks' largest bound it), come to 2^8 or near: a state's entries
+// below 2^-22 of it are fp16's subnormals, off by up to 2^-33 of it, and columns of v as
+// much smaller than others have fewer bits in the outputs than token by token.  A power of
+// two for each column would need a pass over the accumulator.
 #include "pa_decode.h"
 
 #include "pa_device.cuh"

@@ -166,3 +166,42 @@ def test_non_finite_values_of_zero_keys(bad, dim):
     assert torch.equal(~torch.isfinite(c.out[:300]), want)
     c.states[slot, 1, :, 3] = 0
     assert bool(torch.isfinite(c.states[slot]).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ratio", [20, 24, 28, 30])
+def test_columns_far_below_the_states_largest(ratio, dim):
+    """Columns of v 2^-ratio of the others: their outputs are as exact as their own size, but for what the rounding of
+    the state before a block leaves, 2^-33 of the state's largest entry for each |q|."""
+    n, block = 700, 256
+    c = S.LinearCase([n], 2, 2, dim, ctx=[4], g=[-0.004, -0.05], seed=57)
+    col = torch.where(torch.arange(dim, device="cuda") % 2 == 0, 2.0 ** 10, 2.0 ** (10 - ratio))
+    c.v[:n] = (c.v[:n].float() * col).half()
+    slot = int(c.slots[0])
+    c.states[slot] *= col
+    c.before = c.states.clone()
+    prefix(c)
+    assert status() == 0
+    q, k, v, g = (x.double() for x in (c.q[:n], c.k[:n], c.v[:n], c.g))
+    for h in range(2):
+        # of the state's largest entry before each block: the kernel's bound sums up the largest entries of the blocks'
+        # sums, and rounds it up a little each time
+        state, most = c.before[slot, h].double(), float(c.before[slot, h].abs().max())
+        for lo in range(0, n, block):
+            rows = slice(lo, min(n, lo + block))
+            count = rows.stop - lo
+            t = torch.arange(count, device="cuda", dtype=torch.float64)
+            one = S.linear(c.q[rows, h:h + 1], c.k[rows, h:h + 1], c.v[rows, h:h + 1], state[None], c.g[h:h + 1], c.scale,
+                           chunked=False)
+            own = S.linear(c.q[rows, h:h + 1], c.k[rows, h:h + 1], c.v[rows, h:h + 1], torch.zeros_like(state)[None], c.g[h:h + 1],
+                           c.scale, chunked=False)
+            decay = torch.exp(g[h] * (t + 1))[:, None]
+            # one rounding of each score and of each entry of the state, half a step each
+            p = (q[rows, h] @ k[rows, h].T).abs() * torch.exp(g[h] * (t[:, None] - t).clamp(min=0)) * (t[:, None] >= t)
+            lost = S.H16 * (1 + 2.0 ** -10) * (p @ v[rows, h].abs() + q[rows, h].abs() @ state.abs() * decay)
+            # a row's scores below fp16's normals, of a largest that is brought to 2^-4 or more
+            lost += 2.0 ** -21 * p.amax(dim=1, keepdim=True) * v[rows, h].abs().sum(dim=0)
+            lost += 2.0 ** -33 * 1.01 * most * decay * q[rows, h].abs().sum(dim=1, keepdim=True)
+            S.check(c.out[rows, h], one[0][:, 0], one[2][:, 0] + c.scale * lost, f"head {h} block {lo}")
+            state = one[1][0]
+            most = most * float(torch.exp(g[h] * count)) + float(own[1].abs().max())
