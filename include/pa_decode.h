@@ -873,10 +873,12 @@ int pa_linear_decode(const pa_linear_decode_args* args, pa_stream_t stream);
  * of order, outputs and states of the whole batch are unspecified.
  * Sequences of more tokens than a few (below) go in blocks of 256 tokens on the
  * tensor cores.  Their outputs then come from scores and from states before each
- * block that were rounded to fp16 once; entries of such a state below 2^-22 of its
- * largest one are off by up to 2^-33 of that (token by token, by their own 2^-24).
- * The states that are left take each product k v to 22 bits, or to 2^-33 of |k|
- * times the column's largest decayed v.
+ * block that were rounded to fp16 once: a decayed score by half a step, or by up to
+ * 2^-21 of its row's largest one where it is below 2^-10 of that; an entry of a state
+ * by half a step, or by up to 2^-33 of the state's largest one where it is below
+ * 2^-22 of that (token by token, both are off by 2^-24 of themselves).  The states
+ * that are left take each product k v to 22 bits, or to 2^-33 of |k| times the
+ * column's largest decayed v (2^-37 of that v where k is below fp16's normals).
  * The workspace
  * needs no initialisation and holds pa_linear_prefix_workspace_size bytes for the
  * same sizes: 0 up to 9, 14 or 24 tokens a sequence (head_dim 256, 128, 64), else about

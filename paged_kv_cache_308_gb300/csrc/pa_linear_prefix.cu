@@ -22,11 +22,12 @@
 // 2^-25: what is below 2^-11 of the column's largest is off by up to 2^-33 of that.
 // The outputs are fp16: their operands d^(i-j) (q_i . k_j) and S_n are rounded once, to
 // fp16 as the outputs themselves are, also after powers of two, of a row and of a
-// whole state, that keep them from overflow.  A row's own largest score, and a state's
-// largest entry (as its blocks' largest bound it), come to 2^8 or near: a state's entries
-// below 2^-22 of it are fp16's subnormals, off by up to 2^-33 of it, and columns of v as
-// much smaller than others have fewer bits in the outputs than token by token.  A power of
-// two for each column would need a pass over the accumulator.
+// whole state, that keep them from overflow.  A row's largest score comes to 2^-4 or above
+// (where it is there already the accumulator need not be touched), a state's largest entry,
+// as its blocks' largest bound it, to 2^8: scores below 2^-10 of the first and entries below
+// 2^-22 of the second may be fp16's subnormals, off by up to 2^-21 and 2^-33 of it, and columns
+// of v as much smaller than others have fewer bits in the outputs than token by token.  A
+// power of two for each column would need a pass over the accumulator.
 #include "pa_decode.h"
 
 #include "pa_device.cuh"
