@@ -205,3 +205,33 @@ def test_columns_far_below_the_states_largest(ratio, dim):
             S.check(c.out[rows, h], one[0][:, 0], one[2][:, 0] + c.scale * lost, f"head {h} block {lo}")
             state = one[1][0]
             most = most * float(torch.exp(g[h] * count)) + float(own[1].abs().max())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("small", ["k", "v"])
+def test_states_of_subnormal_inputs(small, dim):
+    """Keys, or values, that are subnormal numbers of fp16, next to others that are not."""
+    c = S.LinearCase([300, 40], 4, 2, dim, ctx=[0, 0], g=[-1.0, -0.05], seed=58)
+    x = c.k if small == "k" else c.v
+    for lo, hi in ((100, 290), (305, 340)):
+        x[lo:hi] = (x[lo:hi].float() * 2.0 ** -20).half()
+    prefix(c)
+    assert status() == 0
+    loc = c.loc.tolist()
+    for b in range(2):
+        rows, slot = slice(loc[b], loc[b + 1]), int(c.slots[b])
+        o, s, ob, sb = S.linear(c.q[rows], c.k[rows], c.v[rows], torch.zeros_like(c.before[slot]), c.g, c.scale)
+        k, v = c.k[rows].double().abs(), c.v[rows].double().abs()
+        left = torch.exp(c.g.double() * torch.arange(c.new[b] - 1, -1, -1, device="cuda")[:, None])
+        most = (v * left[:, :, None]).amax(dim=0)[:, None]
+        # the header's bounds: each product, and of the column's largest decayed v 2^-33 of |k| or 2^-37
+        sb = sb + 2.0 ** -33 * most * k.sum(dim=0)[:, :, None] + 2.0 ** -37 * most
+        S.check(c.states[slot], s, sb, f"sequence {b} state")
+        # a row's scores to 2^-21 of its largest (256 keys at most)
+        q = c.q[rows].double()
+        for j in range(4):
+            p = (q[:, j] @ c.k[rows, j // 2].double().T).abs()
+            t = torch.arange(c.new[b], device="cuda", dtype=torch.float64)
+            p = p * torch.exp(c.g[j // 2].double() * (t[:, None] - t).clamp(min=0)) * (t[:, None] >= t)
+            ob[:, j] += c.scale * 2.0 ** -21 * p.amax(dim=1, keepdim=True) * v[:, j // 2].sum(dim=0)
+        S.check(c.out[rows], o, ob, f"sequence {b} out")
