@@ -25,8 +25,9 @@ __device__ __forceinline__ Decay decay_of(float y) {
         }
         return d;
     }
+    // (so little that next to no rounding sees it; down to the smallest number, below 2^-24 of exp(y) above 2^-125)
     const float whole = expf(y);
-    return {whole, whole > 0.f ? fmaxf(whole * 0x1p-30f, 0x1p-149f) : 0.f};
+    return {whole, whole > 0.f ? fmaxf(whole * 0x1p-64f, 0x1p-149f) : 0.f};
 }
 
 }  // namespace

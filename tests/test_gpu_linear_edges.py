@@ -235,3 +235,26 @@ def test_states_of_subnormal_inputs(small, dim):
             p = p * torch.exp(c.g[j // 2].double() * (t[:, None] - t).clamp(min=0)) * (t[:, None] >= t)
             ob[:, j] += c.scale * 2.0 ** -21 * p.amax(dim=1, keepdim=True) * v[:, j // 2].sum(dim=0)
         S.check(c.out[rows], o, ob, f"sequence {b} out")
+
+
+@pytest.mark.parametrize("g", [0.0, -0.5, -0.7, -3.0, -40.0, -80.0])
+def test_decays_are_one_rounding(g):
+    """Behind a key of 0 a state is its product with exp(g), which an entry of 1 shows, rounded once."""
+    c = S.LinearCase([1, 1], 4, 2, 128, g=[g, g], seed=59)
+    c.k[:2] = 0
+    c.states[c.slots.long(), :, 0, 0] = 1.0
+    c.before = c.states.clone()
+    pb.pa_linear_decode(c.out[:2], c.q[:2], c.k[:2], c.v[:2], c.states, c.slots, c.g, c.scale)
+    assert status() == 0
+    got, before = c.states[c.slots.long()], c.before[c.slots.long()]
+    factor = got[0, 0, 0, 0]
+    assert abs(float(factor) - math.exp(g)) <= 2.0 ** -22 * math.exp(g)
+    if g > -59:
+        assert torch.equal(got, before * factor)
+    else:
+        # 2^-64 of exp(-80), which keeps an infinite entry one, is less than the smallest number, 2^-149, that is added
+        # in its place, times the entry; that product and the sum are rounded, the sum by half a unit, and each by half
+        # of 2^-149 where it is subnormal
+        exact = before.double() * float(factor)
+        bound = before.double().abs() * 2.0 ** -149 + exact.abs() * 2.0 ** -24 + 2.0 ** -149
+        assert bool(((got.double() - exact).abs() <= bound).all())
