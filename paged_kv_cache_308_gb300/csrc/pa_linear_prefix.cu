@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kAddThreads, 2)
                                                                     (((q & 7) ^ (r & 7)) << 4));
                     return ((z.x | z.y | z.z | z.w) & 0x7fff7fffu) != 0;
                 };
-                bool some[2] = {key(lane, 0), key(lane + 32, 0)};
+                bool some[2] = {lane >= count || key(lane, 0), lane + 32 >= count || key(lane + 32, 0)};
                 float a[64];
                 float m = 0.f;
                 bool bad = false;
