@@ -786,8 +786,8 @@ int pa_kv_alloc(const pa_kv_alloc_args* args, pa_stream_t stream);
  * A negative slot is not written.  A negative position is a row of padding:
  * nothing of it is read or written.  Without a cache (k_cache and v_cache NULL)
  * v and slot_map are not used.  Slots beyond the pool set PA_DEV_BAD_BLOCK_ID
- * and positions from max_positions on PA_DEV_BAD_SEQ_LEN; the first are not
- * written, the second treated as padding.  Two tokens with one slot leave an
+ * and, with a rotation, positions from max_positions on PA_DEV_BAD_SEQ_LEN; the
+ * first are not written, the second treated as padding.  Two tokens with one slot leave an
  * unspecified mix of both.  q, k and v may have other distances between tokens
  * than num_heads * head_dim elements (a row of a joint projection): q_stride,
  * k_stride and v_stride, multiples of 8 below 2^31, 0 for contiguous tokens (in

@@ -8,8 +8,8 @@
 //     out_i   = scale (d^(i + 1) q_i S_n + sum_{j <= i} d^(i - j) (q_i . k_j) v_j)
 // in three launches: the sums A of all blocks at once, the chain of states
 // (elementwise along a sequence), and the outputs of all blocks at once.  The calls take
-// 51 us for 4 x 512 tokens of 24/4 x 256, 120 us for one sequence of 8192 of them, 118 us for
-// 16 of up to 4096 of 12/12 x 64, and 444 us for 8 x 8192 of 32/8 x 128.  Nothing
+// 52 us for 4 x 512 tokens of 24/4 x 256, 122 us for one sequence of 8192 of them, 121 us for
+// 16 of up to 4096 of 12/12 x 64, and 452 us for 8 x 8192 of 32/8 x 128.  Nothing
 // is sequential but the chain, so one long prompt fills the device as a batch does.
 // What that costs is the states' traffic, 12 D^2 bytes a block and kv head beside
 // the 4 (1 + G) * 256 * D of its tokens: blocks half as long would double it,
@@ -137,6 +137,7 @@ struct AddUnit {
 // bandwidth (a CTA a tile, without the run ahead: 86 us).  One sequence of 8192 of 4 x 256: 25.5 us,
 // 512 tiles for 304 CTAs, where the scaling of a column's 64 tokens (two halves each) bounds it;
 // two threads a column take 25.5 too, and 79.5 us for the 8 sequences: their warps wait for each other.
+// Looking for keys of 0 costs 2 of 53 us for 16 sequences of up to 4096 of 12 x 64, and less than 1 elsewhere.
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 2)
     linear_adds_kernel(const __grid_constant__ LinearMaps maps, const LinearChunkParams c) {

@@ -176,9 +176,12 @@ constexpr int kAllocPlaceTokens = 4 * pa::kAllocThreads;
 // tokens gains 10 % there and loses 15 % at 12/12 x 64; at 8192 it gains nothing and loses up to 28 %.
 constexpr int kPutRows = 4, kPutWarps = 16;
 
-// Up to so many new tokens a sequence go token by token, by head_dim: the calls' us there and in chunks, 1
-// sequence of 24/4 x 256 with 9 tokens 20.6 / 21.3 and 12 tokens 26.6 / 21.1, 64 of them with 9 tokens 139 / 174; of
-// 32/8 x 128 with 12 tokens 16.7 / 16.7, 64 of them with 16 tokens 76 / 100; of 12/12 x 64 with 16 tokens 9.8 / 14.8.
+// Up to so many new tokens a sequence go token by token, by head_dim: where one sequence, with the group that these
+// heads usually have, takes as long in chunks.  On the device, us there and in chunks: 1 sequence of 24/4 x 256 with 9
+// tokens 19.4 / 21.7 and with 12 25.2 / 21.5; of 32/8 x 128 with 14 tokens 17.7 / 17.8; of 12/12 x 64 with 24 tokens
+// 13.6 / 15.3.  Fewer heads a kv head and more sequences move it up, which the limit does not know: 1 sequence of
+// 16/16 x 128 breaks even at 26 tokens, of 8/8 x 256 at 34; 64 sequences of 24/4 x 256 at 14 (159 / 169), of 32/8 x 128
+// at 26 (with 16 66 / 98), of 12/12 x 64 at 42; 1 sequence of 8/1 x 64 already at 11 (with 24 29.8 / 14.2).
 // In a batch whose longest sequence is above it, those that are not have a launch of their own (about 1.5 us; in
 // chunks, a block's sums cost a token as much as 256).
 int few_tokens(int head_dim) { return head_dim == 256 ? 9 : head_dim == 128 ? 14 : 24; }
