@@ -498,7 +498,7 @@ constexpr int kScanThreads = 256;
 // 8 x 8192 tokens of 8 x 128 (201 MB) 41 us, 72 % of the measured bandwidth; where one
 // sequence has all blocks, by the trips along it (8192 of 4 x 256, 50 MB: 19.4 us).
 template <int D>
-__global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearChunkParams c) {
+__global__ void __launch_bounds__(kScanThreads, 4) linear_scan_kernel(const LinearChunkParams c) {
     const LinearParams& p = c.lin;
     constexpr int kTiles = AddShape<D>::kTiles * AddShape<D>::kTiles;
     asm volatile("griddepcontrol.wait;" ::: "memory");
