@@ -9,7 +9,7 @@
 // in three launches: the sums A of all blocks at once, the chain of states
 // (elementwise along a sequence), and the outputs of all blocks at once.  The calls take
 // 52 us for 4 x 512 tokens of 24/4 x 256, 122 us for one sequence of 8192 of them, 121 us for
-// 16 of up to 4096 of 12/12 x 64, and 452 us for 8 x 8192 of 32/8 x 128.  Nothing
+// 16 of up to 4096 of 12/12 x 64, and 448 us for 8 x 8192 of 32/8 x 128.  Nothing
 // is sequential but the chain, so one long prompt fills the device as a batch does.
 // What that costs is the states' traffic, 12 D^2 bytes a block and kv head beside
 // the 4 (1 + G) * 256 * D of its tokens: blocks half as long would double it,
@@ -495,8 +495,9 @@ constexpr int kScanThreads = 256;
 // The state before each block goes to the outputs' kernel as halves of S 2^-e; e comes
 // from a bound on |S| that runs along (no more than a few bits above it), so that no
 // block has to look for the largest entry.  Bound by memory, 6 D^2 bytes a block and kv head:
-// 8 x 8192 tokens of 8 x 128 (201 MB) 41 us, 72 % of the measured bandwidth; where one
-// sequence has all blocks, by the trips along it (8192 of 4 x 256, 50 MB: 19.4 us).
+// 8 x 8192 tokens of 8 x 128 (201 MB) 36 us, 82 % of the measured bandwidth (with 70 registers,
+// three blocks an SM, 41); where one sequence has all blocks, by the trips along it (8192 of
+// 4 x 256, 50 MB: 19.4 us).
 template <int D>
 __global__ void __launch_bounds__(kScanThreads, 4) linear_scan_kernel(const LinearChunkParams c) {
     const LinearParams& p = c.lin;
