@@ -744,9 +744,9 @@ int pa_kv_evict(const pa_kv_evict_args* args, pa_stream_t stream);
  * new_held_lens is context + query where a sequence was served and its blocks
  * moved, and its held_lens where not: a sequence that shrinks and grows in one
  * step, is not served and has fewer seq_lens than it holds blocks for keeps them
- * all, and gives them back only to a later call that gets these held_lens.  (A
- * caller without new_held_lens keeps the old held_lens for those whose seq_lens
- * is not context + query.)  Each block belongs in one row only.
+ * all, and gives them back only to a later call that gets these held_lens.
+ * seq_lens alone does not say what a row holds where a call may report an error.
+ * Each block belongs in one row only.
  * The outputs must not overlap each other or the inputs, but for new_free_count
  * on free_count and new_held_lens on held_lens.
  * num_blocks * block_size < 2^31; lengths and num_tokens up to 2^30. */
@@ -787,12 +787,12 @@ int pa_kv_alloc(const pa_kv_alloc_args* args, pa_stream_t stream);
  * nothing of it is read or written.  Without a cache (k_cache and v_cache NULL)
  * v and slot_map are not used.  Slots beyond the pool set PA_DEV_BAD_BLOCK_ID
  * and, with a rotation, positions from max_positions on PA_DEV_BAD_SEQ_LEN; the
- * first are not written, the second treated as padding.  Two tokens with one slot leave an
- * unspecified mix of both.  q, k and v may have other distances between tokens
- * than num_heads * head_dim elements (a row of a joint projection): q_stride,
- * k_stride and v_stride, multiples of 8 below 2^31, 0 for contiguous tokens (in
- * place only for these).  But for q_out on q and k_out on k no output may overlap another
- * one or an input. */
+ * first are not written, the second treated as padding.  Two tokens with one slot
+ * leave an unspecified mix of both.  q, k and v may have other distances between
+ * tokens than num_heads * head_dim elements (a row of a joint projection):
+ * q_stride, k_stride and v_stride, multiples of 8 below 2^31, 0 for contiguous
+ * tokens (in place only for these).  But for q_out on q and k_out on k no output
+ * may overlap another one or an input. */
 typedef struct {
     pa_kv_cache cache;           /* PA_KV_F16; scales not used */
     void* q_out;
