@@ -8,8 +8,8 @@ namespace {
 // What a state is multiplied by: S -> exp(y) S = S * whole + S * rest, the sum
 // rounded once (a fused sum over the product with rest).  Next to 1 the two hold
 // what exp(y) alone loses there: rest is what 1 + expm1(y) has below whole's last
-// place.  Both are positive unless exp(y) is 0 in 32 bits, so that an infinite
-// entry stays one instead of meeting itself with the other sign, or a 0.
+// place.  Both are positive unless exp(y) is 0 or the smallest number in 32 bits, so
+// that an infinite entry stays one instead of meeting itself with the other sign, or a 0.
 struct Decay {
     float whole, rest;
 };
@@ -25,9 +25,10 @@ __device__ __forceinline__ Decay decay_of(float y) {
         }
         return d;
     }
-    // (so little that next to no rounding sees it; down to the smallest number, below 2^-24 of exp(y) above 2^-125)
-    const float whole = expf(y);
-    return {whole, whole > 0.f ? fmaxf(whole * 0x1p-64f, 0x1p-149f) : 0.f};
+    // So little that next to no rounding sees it, down to the smallest number: that is no more than 2^-24 of exp(y)
+    // from 2^-125 on, and below whole is a multiple of it.
+    const float whole = expf(y), rest = whole > 0.f ? fmaxf(whole * 0x1p-64f, 0x1p-149f) : 0.f;
+    return {whole < 0x1p-125f ? whole - rest : whole, rest};
 }
 
 }  // namespace

@@ -258,3 +258,17 @@ def test_decays_are_one_rounding(g):
         exact = before.double() * float(factor)
         bound = before.double().abs() * 2.0 ** -149 + exact.abs() * 2.0 ** -24 + 2.0 ** -149
         assert bool(((got.double() - exact).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("g", [-88.0, -90.0, -97.0, -100.0])
+def test_decays_below_the_normal_numbers(g):
+    """exp(g) is then a number of units of 2^-149, off by half of one and as much of the function's own error."""
+    c = S.LinearCase([1, 1], 4, 2, 64, g=[g, g], seed=60)
+    c.k[:2] = 0
+    c.states[c.slots.long(), :, 0, 0] = 1.0
+    c.states[c.slots.long(), :, 0, 1] = 2.0 ** 20
+    pb.pa_linear_decode(c.out[:2], c.q[:2], c.k[:2], c.v[:2], c.states, c.slots, c.g, c.scale)
+    assert status() == 0
+    got = c.states[c.slots.long()].double() * 2.0 ** 149
+    for col, size in ((0, 1.0), (1, 2.0 ** 20)):
+        assert bool(((got[:, :, 0, col] - math.exp(g) * 2.0 ** 149 * size).abs() <= size).all())
